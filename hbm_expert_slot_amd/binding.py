@@ -25,13 +25,19 @@ SC_MFMA_MIN_ROWS_DOWN = 5
 SC_N_KERNELS = 5
 SC_N_EVENTS = 2 * SC_N_KERNELS
 SC_STATIC_SCRATCH_BYTES = 16777216
+SC_DTYPE_F32 = 0
+SC_DTYPE_BF16 = 1
+SC_DTYPE_F16 = 2
+SC_FP4_NV = 0
+SC_FP4_MX = 1
+SC_FP4_QUANT_WORKSPACE_BYTES = 4096
 
 EXPORTED = (
     "slotcache_query_sizes", "slotcache_init", "slotcache_backing", "slotcache_set_global_scales",
     "slotcache_preload", "moe_layer_decode", "moe_layer_decode_ev", "slotcache_stats",
     "slotcache_read_state", "slotcache_write_state", "slotcache_read_events",
     "slotcache_read_routing", "slotcache_read_kernel_spans", "slotcache_pin", "slotcache_last_error",
-    "slotcache_destroy", "moe_layer_decode_static",
+    "slotcache_destroy", "moe_layer_decode_static", "fp4_quantize", "fp4_dequantize", "fp4_linear",
 )
 
 
@@ -70,6 +76,12 @@ class sc_event(ctypes.Structure):
                 ("evicted", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class sc_fp4_matrix(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int32), ("rows", ctypes.c_int32), ("cols", ctypes.c_int32),
+                ("d_codes", ctypes.c_void_p), ("d_scales", ctypes.c_void_p),
+                ("d_global_scale", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -98,6 +110,9 @@ def lib():
             "slotcache_read_routing": [P, P, P, ctypes.POINTER(i32), ctypes.POINTER(i32)],
             "slotcache_read_kernel_spans": [P, ctypes.POINTER(ctypes.c_double)],
             "slotcache_pin": [P, i32, P, i32],
+            "fp4_quantize": [P, i32, i64, ctypes.POINTER(sc_fp4_matrix), i32, P, P],
+            "fp4_dequantize": [ctypes.POINTER(sc_fp4_matrix), P, i32, i64, P],
+            "fp4_linear": [ctypes.POINTER(sc_fp4_matrix), P, i32, i64, i32, P, P, i32, i64, P],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -199,6 +214,18 @@ def slotcache_read_kernel_spans(h):
     out = (ctypes.c_double * SC_N_KERNELS)()
     _check(lib().slotcache_read_kernel_spans(h, out))
     return list(out)
+
+
+def fp4_quantize(d_w, w_type, ldw, out, scale_given, d_workspace, stream):
+    _check(lib().fp4_quantize(d_w, w_type, ldw, out, scale_given, d_workspace, stream))
+
+
+def fp4_dequantize(w, d_w, w_type, ldw, stream):
+    _check(lib().fp4_dequantize(w, d_w, w_type, ldw, stream))
+
+
+def fp4_linear(w, d_x, x_type, ldx, M, d_bias, d_y, y_type, ldy, stream):
+    _check(lib().fp4_linear(w, d_x, x_type, ldx, M, d_bias, d_y, y_type, ldy, stream))
 
 
 def slotcache_last_error():

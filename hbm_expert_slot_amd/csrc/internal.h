@@ -28,6 +28,14 @@ enum Counter {
 // H_RESIDENT / H_STAGED: a staged prefill step's resident and staged unique experts.
 enum Hdr { H_UNIQUE = 0, H_MISS = 1, H_BYPASS = 2, H_ROWS = 3, H_RESIDENT = 4, H_STAGED = 5, H_WORDS = 64 };
 
+// Records the calling thread's error message and returns the status.
+sc_status fail(sc_status st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+sc_status hip_fail(hipError_t e, const char* what);
+
+// Longest row of a 4-bit matrix: a block's rows stay addressable by 32-bit offsets.
+constexpr int kMaxFp4Cols = 1 << 20;
+sc_status check_fp4_matrix(const sc_fp4_matrix* w);
+
 // Device view of one layer: its maps, clock, counters, event ring, slots,
 // the backing bank it reads and that bank's global-scale table.
 struct LayerDev {

@@ -24,9 +24,9 @@ using namespace sc;
 // once per device (static_scratch below).
 static __device__ __align__(256) uint8_t scratch[SC_STATIC_SCRATCH_BYTES];
 
-namespace {
+static thread_local std::string g_err;
 
-thread_local std::string g_err;
+namespace sc {
 
 sc_status fail(sc_status st, const char* fmt, ...) {
   char buf[512];
@@ -41,6 +41,10 @@ sc_status fail(sc_status st, const char* fmt, ...) {
 sc_status hip_fail(hipError_t e, const char* what) {
   return fail(SC_E_HIP, "%s: %s", what, hipGetErrorString(e));
 }
+
+}  // namespace sc
+
+namespace {
 
 constexpr size_t kAlign = 256;
 constexpr int64_t kMaxStateStep = (int64_t)1 << 40;

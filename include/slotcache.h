@@ -335,6 +335,64 @@ SC_API sc_status slotcache_read_events(sc_handle* h, int32_t layer, sc_event* h_
 SC_API sc_status slotcache_read_routing(sc_handle* h, int32_t* h_ids, float* h_w, int32_t* M_out,
                                  int32_t* bypass);
 
+/* ---- 4-bit weights -------------------------------------------------------- */
+
+/* Element types of dense tensors. */
+#define SC_DTYPE_F32 0
+#define SC_DTYPE_BF16 1
+#define SC_DTYPE_F16 2
+
+/* 4-bit weight formats: E2M1 codes, two per byte, the even element in the low
+ * nibble, with a scale per group of consecutive elements of a row.
+ *   SC_FP4_NV  one E4M3 scale per 16 elements and one fp32 scale of the matrix
+ *              (the format of the expert blobs)
+ *   SC_FP4_MX  one E8M0 scale (2^(byte - 127), 255 is NaN) per 32 elements */
+#define SC_FP4_NV 0
+#define SC_FP4_MX 1
+
+/* A matrix [rows][cols] held in 4 bits, in device memory.  cols is a multiple
+ * of the group; rows follow each other without padding. */
+typedef struct {
+  int32_t format;          /* SC_FP4_NV or SC_FP4_MX */
+  int32_t rows;            /* >= 0 */
+  int32_t cols;            /* <= 2^20; rows * cols <= 2^36 - 16 */
+  void* d_codes;           /* [rows][cols/2], 16-byte aligned */
+  void* d_scales;          /* [rows][cols/16] or [rows][cols/32], 2-byte aligned */
+  float* d_global_scale;   /* one float; NULL stands for 1 where it is only read */
+} sc_fp4_matrix;
+
+#define SC_FP4_QUANT_WORKSPACE_BYTES 4096
+
+/* Quantises d_w [rows][cols] (row stride ldw elements, type w_type) into `out`.
+ * NVFP4: the matrix scale is read from out->d_global_scale when scale_given is
+ * nonzero (positive and finite; matrices that share one, or a gate/up pair cut
+ * into shards), else it is max|w| / 2688 and written there (1 when that is 0).
+ * A group's scale is the E4M3 number nearest to max|group| / (6 scale), at most
+ * 448; a code is the E2M1 number nearest to w / (group scale * scale), at most
+ * 6.  MXFP4: the group scale is 2^(floor(log2 max|group|) - 2).  Nearest is of
+ * the exact quotient, ties to even.  A group whose scale rounds to 0 has codes
+ * 0.  Infinities and NaN do not count in the matrix scale; a group that holds
+ * one gets a NaN scale, so that it reads back as NaN.  d_workspace:
+ * SC_FP4_QUANT_WORKSPACE_BYTES of device memory when the scale is computed
+ * (NVFP4 without scale_given), else ignored.  Asynchronous on `stream`, whose
+ * device is current; can be captured.  rows == 0 does nothing. */
+SC_API sc_status fp4_quantize(const void* d_w, int32_t w_type, int64_t ldw, const sc_fp4_matrix* out,
+                              int32_t scale_given, void* d_workspace, void* stream);
+
+/* Writes the values `w` stands for to d_w (type w_type, row stride ldw): code *
+ * group scale * matrix scale, rounded to fp32 once and then to w_type. */
+SC_API sc_status fp4_dequantize(const sc_fp4_matrix* w, void* d_w, int32_t w_type, int64_t ldw, void* stream);
+
+/* y = x W^T + bias: x [M][w->cols] of bf16 or fp16 (row stride ldx elements), y
+ * [M][w->rows] (row stride ldy, type y_type), bias fp32 [w->rows] or NULL.
+ * Products of x with the codes are exact, a group's sum is scaled in fp32, and
+ * y is rounded once.  |x| has to stay below 2^121 for the group sums to be
+ * finite.  Any M >= 0; rows are independent of each other.  y must not overlap
+ * x or the weights.  Asynchronous on `stream`, whose device is current; no
+ * workspace, no allocation; can be captured. */
+SC_API sc_status fp4_linear(const sc_fp4_matrix* w, const void* d_x, int32_t x_type, int64_t ldx, int32_t M,
+                            const float* d_bias, void* d_y, int32_t y_type, int64_t ldy, void* stream);
+
 /* Message for the last non-OK status returned on this thread. */
 SC_API const char* slotcache_last_error(void);
 

@@ -1,0 +1,274 @@
+"""4-bit weights on the GPU: quantising and reading back (whole numbers equal the
+float64 oracle's), and products against float64."""
+import numpy as np
+import pytest
+
+from oracle import fp4
+
+from gpu_util import log, torch_cuda
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"bf16": "bfloat16", "fp16": "float16", "fp32": "float32"}
+
+
+def _ops():
+    from hbm_expert_slot_amd import ops
+    return ops
+
+
+def _np64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def _weights(torch, rows, cols, dtype, seed, scale=0.02):
+    rng = np.random.default_rng(seed)
+    w = rng.standard_normal((rows, cols)) * scale * np.exp(0.5 * rng.standard_normal((rows, 1)))
+    return torch.tensor(w, dtype=getattr(torch, TYPES[dtype])).cuda()
+
+
+def _check_quant(torch, w, q, fmt, given=None):
+    codes, sb, gs = fp4.quantize(_np64(w), fmt, given)
+    assert np.array_equal(q.scales.cpu().numpy(), sb)
+    assert np.array_equal(fp4.unpack(q.codes.cpu().numpy()), codes)
+    if fmt == "nvfp4":
+        assert np.float32(q.global_scale.item()) == gs
+    v = fp4.values(codes, sb, fmt, gs)
+    for dt in TYPES.values():
+        got = _ops().fp4_dequantize(q, getattr(torch, dt))
+        want = torch.tensor(v).float().to(getattr(torch, dt))
+        assert torch.equal(torch.nan_to_num(got.cpu(), nan=777.0), torch.nan_to_num(want, nan=777.0)), dt
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("fmt,rows,cols", [("nvfp4", 1, 16), ("nvfp4", 3, 48), ("nvfp4", 257, 1040),
+                                           ("nvfp4", 64, 6144), ("mxfp4", 1, 32), ("mxfp4", 5, 96),
+                                           ("mxfp4", 130, 2080)])
+def test_quantize(fmt, rows, cols, dtype):
+    torch = torch_cuda()
+    log("quantize", fmt, rows, cols, dtype)
+    w = _weights(torch, rows, cols, dtype, rows * 7 + cols)
+    _check_quant(torch, w, _ops().fp4_quantize(w, fmt), fmt)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("g", [2.0 ** -13, 0.00123, 2.0 ** -7])
+def test_quantize_with_a_given_scale(g, dtype):
+    """Powers of two make ties common; the large one saturates scales at 0, the small one at 448."""
+    torch = torch_cuda()
+    log("given scale", g, dtype)
+    w = _weights(torch, 96, 512, dtype, 5, scale=0.05)
+    w[0] = torch.round(w[0] * 512) / 512
+    w[1, :16] = torch.tensor([6, .25, .75, 1.25, 1.75, 2.5, 3.5, 5, -.25, -.75, -1.25, -1.75, -2.5, -3.5, -5, 0]) * g
+    w[2] *= 1e4
+    w[3] *= 1e-6
+    gs = torch.tensor([g], dtype=torch.float32).cuda()
+    _check_quant(torch, w, _ops().fp4_quantize(w, "nvfp4", global_scale=gs), "nvfp4", np.float32(g))
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_quantize_next_to_borders(fmt):
+    """fp32 weights one step beside a rounding border take the side they are on."""
+    torch = torch_cuda()
+    rng = np.random.default_rng(3)
+    base = np.float32(rng.uniform(0.5, 2, (64, 1)))
+    mid = np.array([.25, .75, 1.25, 1.75, 2.5, 3.5, 5.0], np.float32)
+    w = np.zeros((64, 64), np.float32)
+    w[:, 0::16] = 6 * base                      # every group's max: the scale is about base
+    for i in range(7):
+        b = (base * mid[i]).astype(np.float32)[:, 0]
+        w[:, 2 * i + 1] = np.nextafter(b, np.float32(0))
+        w[:, 2 * i + 2] = -np.nextafter(b, np.float32(9))
+        w[:, 16 + 2 * i + 1] = b
+    t = torch.tensor(w).cuda()
+    for g in ([np.float32(2.0 ** -9), np.float32(0.0017)] if fmt == "nvfp4" else [None]):
+        gs = None if g is None else torch.tensor([g]).cuda()
+        _check_quant(torch, t, _ops().fp4_quantize(t, fmt, global_scale=gs), fmt, g)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_quantize_edges(fmt):
+    """Zeros, infinities, NaN, denormals and the type's extremes; each spoils its own group only."""
+    torch = torch_cuda()
+    w = _weights(torch, 12, 64, "fp32", 9)
+    w[0] = 0
+    w[1, 5] = float("nan")
+    w[2, 40] = float("inf")
+    w[3, 63] = -float("inf")
+    w[4] = 1e-42
+    w[5, :32] = -0.0
+    _check_quant(torch, w, _ops().fp4_quantize(w, fmt), fmt)
+    z = torch.zeros(3, 64, device="cuda")
+    _check_quant(torch, z, _ops().fp4_quantize(z, fmt), fmt)
+    big = torch.full((2, 64), 3e38, device="cuda")
+    big[1] = 1.0
+    if fmt == "mxfp4":
+        _check_quant(torch, big, _ops().fp4_quantize(big, fmt), fmt)
+    else:
+        q = _ops().fp4_quantize(big, fmt)
+        codes, sb, gs = fp4.quantize(_np64(big), fmt)
+        assert np.array_equal(q.scales.cpu().numpy(), sb) and np.float32(q.global_scale.item()) == gs
+
+
+def test_quantize_strides_and_views():
+    torch = torch_cuda()
+    big = _weights(torch, 40, 300, "bf16", 11)
+    for off, cols in ((0, 288), (1, 288), (8, 96)):
+        w = big[3:33, off:off + cols]
+        _check_quant(torch, w, _ops().fp4_quantize(w, "nvfp4"), "nvfp4")
+    q = _ops().FP4Weight.empty(30, 96)
+    out = torch.full((30, 120), 7.0, device="cuda")
+    _ops().fp4_quantize(w, out=q)
+    _ops().fp4_dequantize(q, out=out[:, 3:99])
+    assert torch.equal(out[:, 3:99], _ops().fp4_dequantize(q)) and (out[:, :3] == 7).all() and (out[:, 99:] == 7).all()
+
+
+def test_no_rows():
+    torch = torch_cuda()
+    ops = _ops()
+    q = ops.fp4_quantize(torch.empty(0, 64, device="cuda", dtype=torch.bfloat16))
+    assert q.shape == (0, 64) and ops.fp4_dequantize(q).shape == (0, 64)
+    x = torch.ones(3, 64, device="cuda", dtype=torch.bfloat16)
+    assert ops.fp4_linear(x, q).shape == (3, 0)
+    w = ops.fp4_quantize(torch.ones(5, 64, device="cuda"))
+    assert ops.fp4_linear(x[:0], w).shape == (0, 5)
+
+
+# ---- products -------------------------------------------------------------------
+
+def _random_fp4(torch, rows, cols, fmt, seed):
+    rng = np.random.default_rng(seed)
+    codes = rng.integers(0, 16, (rows, cols)).astype(np.uint8)
+    g = fp4.GROUP[fmt]
+    if fmt == "nvfp4":
+        sb = rng.integers(0x20, 0x7F, (rows, cols // g)).astype(np.uint8)
+        gs = np.float32(rng.uniform(0.001, 0.002))
+    else:
+        sb = rng.integers(110, 130, (rows, cols // g)).astype(np.uint8)
+        gs = None
+    q = _ops().FP4Weight(torch.tensor(fp4.pack(codes)).cuda(), torch.tensor(sb).cuda(),
+                         None if gs is None else torch.tensor([gs]).cuda(), fmt)
+    return q, fp4.values(codes, sb, fmt, gs)
+
+
+def _bound(x, w, dtype, torch, terms):
+    """Rounding of `terms` fp32 additions against the sum of magnitudes (each adds half a step of a
+    partial sum no larger than that), and of the result to its type."""
+    mag = np.abs(x) @ np.abs(w).T
+    want = x @ w.T
+    return terms * 2.0 ** -24 * mag + torch.finfo(dtype).eps / 2 * np.abs(want) * 1.01 + 1e-37
+
+
+# one chain of fp32 additions: 16 or 32 products of a group, one addition per group of a lane,
+# the sums over lanes and wavefronts; the bias and the scale of the matrix add three roundings
+def _terms(K):
+    return 32 + 2 * (K // 512 + 1) + 12 + 3
+
+
+LINEAR = [
+    (1, 1, 16, "nvfp4"), (1, 5, 32, "mxfp4"), (1, 64, 512, "nvfp4"), (1, 130, 2064, "nvfp4"), (1, 77, 6144, "nvfp4"),
+    (2, 33, 48, "nvfp4"), (3, 40, 1056, "mxfp4"), (4, 130, 2064, "nvfp4"), (5, 19, 544, "mxfp4"),
+    (7, 65, 1040, "nvfp4"), (8, 256, 4096, "nvfp4"), (9, 31, 528, "nvfp4"), (13, 67, 2064, "nvfp4"),
+    (16, 128, 6144, "mxfp4"), (17, 96, 1040, "nvfp4"), (33, 100, 512, "nvfp4"), (64, 129, 800, "mxfp4"),
+    (100, 64, 16400, "nvfp4"), (1, 70, 17424, "nvfp4"),
+]
+
+
+@pytest.mark.parametrize("x_type", ["bf16", "fp16"])
+@pytest.mark.parametrize("M,N,K,fmt", LINEAR)
+def test_linear(M, N, K, fmt, x_type):
+    torch = torch_cuda()
+    ops = _ops()
+    log("linear", M, N, K, fmt, x_type)
+    q, w = _random_fp4(torch, N, K, fmt, M * 1000 + N)
+    rng = np.random.default_rng(K)
+    x = torch.tensor(rng.standard_normal((M, K)), dtype=getattr(torch, TYPES[x_type])).cuda()
+    bias = torch.tensor(rng.standard_normal(N), dtype=torch.float32).cuda()
+    x64, b64 = _np64(x), _np64(bias)
+    for out, b in ((torch.float32, bias), (x.dtype, None)):
+        y = _np64(ops.fp4_linear(x, q, bias=b, out_dtype=out))
+        want = x64 @ w.T + (0 if b is None else b64)
+        tol = _bound(x64, w, out, torch, _terms(K)) + (0 if b is None else 2.0 ** -22 * np.abs(b64))
+        assert (np.abs(y - want) <= tol).all(), (out, np.abs((y - want) / tol).max())
+
+
+@pytest.mark.parametrize("M", [1, 4, 13, 40])
+def test_linear_strides_and_rows_beside_the_output(M):
+    torch = torch_cuda()
+    ops = _ops()
+    q, _ = _random_fp4(torch, 37, 1040, "nvfp4", 3)
+    rng = np.random.default_rng(M)
+    big = torch.tensor(rng.standard_normal((M + 2, 1100)), dtype=torch.bfloat16).cuda()
+    for off in (0, 1, 8):
+        x = big[1:M + 1, off:off + 1040]
+        out = torch.full((M + 2, 64), 9.0, device="cuda")
+        ops.fp4_linear(x, q, out=out[1:M + 1, 5:42])
+        dense = ops.fp4_linear(x.contiguous(), q, out_dtype=torch.float32)
+        assert torch.equal(out[1:M + 1, 5:42], dense)
+        out[1:M + 1, 5:42] = 9.0
+        assert (out == 9.0).all()
+
+
+@pytest.mark.parametrize("M", [1, 3, 9, 40])
+@pytest.mark.parametrize("fmt,K", [("nvfp4", 1040), ("nvfp4", 1024), ("mxfp4", 1056)])
+def test_linear_nan_stays_where_it_is(M, fmt, K):
+    """A NaN scale reaches its output column only, a NaN or infinity in x its row only."""
+    torch = torch_cuda()
+    ops = _ops()
+    q, _ = _random_fp4(torch, 70, K, fmt, 8)
+    x = torch.randn(M, K, device="cuda").to(torch.bfloat16)
+    clean = ops.fp4_linear(x, q, out_dtype=torch.float32)
+    keep = q.scales.clone()
+    q.scales[33, q.scales.shape[1] - 1] = 0x7F if fmt == "nvfp4" else 0xFF
+    y = ops.fp4_linear(x, q, out_dtype=torch.float32)
+    assert torch.isnan(y[:, 33]).all()
+    y[:, 33] = clean[:, 33]
+    assert torch.equal(y, clean)
+    q.scales.copy_(keep)
+    for bad in (float("nan"), float("inf")):
+        xb = x.clone()
+        xb[M // 2, K - 1] = bad
+        y = ops.fp4_linear(xb, q, out_dtype=torch.float32)
+        assert not torch.isfinite(y[M // 2]).any()
+        y[M // 2] = clean[M // 2]
+        assert torch.equal(y, clean)
+
+
+def test_linear_on_another_stream_and_replayed():
+    torch = torch_cuda()
+    ops = _ops()
+    q, _ = _random_fp4(torch, 96, 2048, "nvfp4", 4)
+    x = torch.randn(4, 2048, device="cuda").to(torch.bfloat16)
+    want = ops.fp4_linear(x, q)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y = ops.fp4_linear(x, q, stream=side)
+    side.synchronize()
+    assert torch.equal(y, want)
+    out = torch.empty_like(want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ops.fp4_linear(x, q, out=out)
+    for i in range(4):
+        x.copy_(torch.randn(4, 2048, device="cuda").to(torch.bfloat16))
+        eager = ops.fp4_linear(x, q)
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager), i
+
+
+def test_quantize_replayed():
+    torch = torch_cuda()
+    ops = _ops()
+    w = _weights(torch, 64, 512, "bf16", 2)
+    q = ops.FP4Weight.empty(64, 512)
+    ops.fp4_quantize(w, out=q)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ops.fp4_quantize(w, out=q)
+    for i in range(3):
+        w.copy_(_weights(torch, 64, 512, "bf16", 20 + i))
+        g.replay()
+        torch.cuda.synchronize()
+        _check_quant(torch, w, q, "nvfp4")
