@@ -31,6 +31,9 @@ SC_DTYPE_F16 = 2
 SC_FP4_NV = 0
 SC_FP4_MX = 1
 SC_FP4_QUANT_WORKSPACE_BYTES = 4096
+SC_MOE_MAX_ROWS = 16
+SC_SCORE_SOFTMAX = 0
+SC_SCORE_SIGMOID = 1
 
 EXPORTED = (
     "slotcache_query_sizes", "slotcache_init", "slotcache_backing", "slotcache_set_global_scales",
@@ -38,6 +41,7 @@ EXPORTED = (
     "slotcache_read_state", "slotcache_write_state", "slotcache_read_events",
     "slotcache_read_routing", "slotcache_read_kernel_spans", "slotcache_pin", "slotcache_last_error",
     "slotcache_destroy", "moe_layer_decode_static", "fp4_quantize", "fp4_dequantize", "fp4_linear",
+    "moe_layer_workspace_bytes", "moe_layer_prepare", "moe_layer_forward",
 )
 
 
@@ -82,6 +86,17 @@ class sc_fp4_matrix(ctypes.Structure):
                 ("d_global_scale", ctypes.c_void_p)]
 
 
+class sc_moe_config(ctypes.Structure):
+    _fields_ = [("hidden", ctypes.c_int32), ("inter", ctypes.c_int32), ("n_experts", ctypes.c_int32),
+                ("top_k", ctypes.c_int32), ("shared_inter", ctypes.c_int32), ("max_rows", ctypes.c_int32),
+                ("score", ctypes.c_int32), ("routed_scale", ctypes.c_float)]
+
+
+class sc_moe_weights(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "d_router", "d_score_bias", "d_blobs", "d_global_scales", "d_shared_blob", "d_shared_scales")]
+
+
 _lib = None
 
 
@@ -112,6 +127,10 @@ def lib():
             "slotcache_pin": [P, i32, P, i32],
             "fp4_quantize": [P, i32, i64, ctypes.POINTER(sc_fp4_matrix), i32, P, P],
             "fp4_dequantize": [ctypes.POINTER(sc_fp4_matrix), P, i32, i64, P],
+            "moe_layer_workspace_bytes": [ctypes.POINTER(sc_moe_config), ctypes.POINTER(sz)],
+            "moe_layer_prepare": [ctypes.POINTER(sc_moe_config), P, P],
+            "moe_layer_forward": [ctypes.POINTER(sc_moe_config), ctypes.POINTER(sc_moe_weights), P, P, i64, i32, P,
+                                  i32, i64, P, P, P],
             "fp4_linear": [ctypes.POINTER(sc_fp4_matrix), P, i32, i64, i32, P, P, i32, i64, P],
         }
         for name, args in sig.items():
@@ -226,6 +245,20 @@ def fp4_dequantize(w, d_w, w_type, ldw, stream):
 
 def fp4_linear(w, d_x, x_type, ldx, M, d_bias, d_y, y_type, ldy, stream):
     _check(lib().fp4_linear(w, d_x, x_type, ldx, M, d_bias, d_y, y_type, ldy, stream))
+
+
+def moe_layer_workspace_bytes(cfg):
+    n = ctypes.c_size_t()
+    _check(lib().moe_layer_workspace_bytes(cfg, ctypes.byref(n)))
+    return n.value
+
+
+def moe_layer_prepare(cfg, d_workspace, stream):
+    _check(lib().moe_layer_prepare(cfg, d_workspace, stream))
+
+
+def moe_layer_forward(cfg, w, d_workspace, d_x, ldx, M, d_y, y_type, ldy, d_ids, d_weights, stream):
+    _check(lib().moe_layer_forward(cfg, w, d_workspace, d_x, ldx, M, d_y, y_type, ldy, d_ids, d_weights, stream))
 
 
 def slotcache_last_error():

@@ -91,10 +91,9 @@ __device__ __forceinline__ f32x2 lane_scales(uint32_t raw) {
 }
 
 // Sums over lanes that agree in lane % 4 (the sixteen tiles).  V values per
-// lane are halved while there are pairs to trade: after the two lane-swap
-// steps a lane holds the totals of values first..first + V/4 - 1 of its
-// quarter, first = (lane >> 5 & 1) * V/2 + (lane >> 4 & 1) * V/4.  Every lane
-// adds the same numbers in the same tree, whatever V is.
+// lane (a power of two) are halved while there are pairs to trade: after the
+// two lane-swap steps a lane holds the totals of kTileOut<V> values, from
+// tile_sum_first on.  Every total is added in the same tree, whatever V is.
 template <int O>
 __device__ __forceinline__ float swap_sum(float a, float b) {
   if constexpr (O == 32) {
@@ -109,23 +108,30 @@ template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
   return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xF, 0xF, false));
 }
-// V must be a multiple of four (pad with zeros).
+template <int V>
+constexpr int kTileOut = V >= 4 ? V / 4 : 1;
 template <int V>
 __device__ __forceinline__ void tile_sum(float (&v)[V]) {
-  static_assert(V % 4 == 0, "values are traded in fours");
+  static_assert((V & (V - 1)) == 0, "values are traded in pairs");
+  constexpr int H1 = V >= 2 ? V / 2 : 1, H2 = kTileOut<V>;
 #pragma unroll
-  for (int i = 0; i < V / 2; ++i) v[i] = swap_sum<32>(v[i], v[i + V / 2]);
+  for (int i = 0; i < H1; ++i) v[i] = swap_sum<32>(v[i], v[V >= 2 ? i + H1 : i]);
 #pragma unroll
-  for (int i = 0; i < V / 4; ++i) v[i] = swap_sum<16>(v[i], v[i + V / 4]);
+  for (int i = 0; i < H2; ++i) v[i] = swap_sum<16>(v[i], v[V >= 4 ? i + H2 : i]);
 #pragma unroll
-  for (int i = 0; i < V / 4; ++i) {
+  for (int i = 0; i < H2; ++i) {
     v[i] += dpp<0x128>(v[i]);   // rotated by 8 in the row of 16
     v[i] += dpp<0x124>(v[i]);   // and by 4
   }
 }
+// First value that a lane holds, and whether it is the lane that hands it on.
 template <int V>
 __device__ __forceinline__ int tile_sum_first(int lane) {
-  return ((lane >> 5) & 1) * (V / 2) + ((lane >> 4) & 1) * (V / 4);
+  return (V >= 2 ? ((lane >> 5) & 1) * (V / 2) : 0) + (V >= 4 ? ((lane >> 4) & 1) * (V / 4) : 0);
+}
+template <int V>
+__device__ __forceinline__ bool tile_sum_owner(int lane) {
+  return (lane & (V >= 4 ? 12 : V >= 2 ? 28 : 60)) == 0;
 }
 
 // ---- few rows against 4-bit weights ------------------------------------------
@@ -174,40 +180,60 @@ __device__ __forceinline__ void load_stage(Stage<FMT, ODD, Q>& st, Rsrc rc, Rsrc
 }
 
 // acc[j][r] += sum of the stage's products with operand row r.  xs: the lane's
-// operand rows in LDS, 32 elements at this step; row set a (rows 4a..4a+3)
-// lies at xs + a * set_bytes.  A lane of row l % 4 >= rows reads any valid
-// row: its results are not used.
-template <int FMT, bool ODD, int Q, int ROWS, bool HALF>
+// operand row in LDS (row l % 4 of row set 0), 32 elements at this step; row set
+// a (rows 4a..4a+3) lies at xs + a * set_bytes.  A lane of a row behind the last
+// reads any finite or unused memory: its results are not used.
+//
+// SPLIT: the operand is fp32, held as three bf16 parts that add up to it (24
+// bits).  With one row the parts stand as three rows of its set and their sums
+// are added; otherwise part p lies at xs + p * part_bytes and the matrix
+// instructions add all three into one sum.
+template <int FMT, bool ODD, int Q, int ROWS, bool HALF, bool SPLIT = false>
 __device__ __forceinline__ void use_stage(const Stage<FMT, ODD, Q>& st, const uint8_t* xs, int set_bytes,
-                                          float (&acc)[Q][ROWS]) {
-  constexpr int NA = (ROWS + 3) / 4;
+                                          float (&acc)[Q][ROWS], int part_bytes = 0) {
+  constexpr int NA = (ROWS + 3) / 4, NP = SPLIT && ROWS > 1 ? 3 : 1;
   f32x2 sc[Q];
 #pragma unroll
   for (int j = 0; j < Q; ++j) sc[j] = lane_scales<FMT>(st.s[j]);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    u32x4 x[NA][2];
-#pragma unroll
-    for (int a = 0; a < NA; ++a) {
-      x[a][0] = *reinterpret_cast<const u32x4*>(xs + a * set_bytes + h * 32);
-      x[a][1] = *reinterpret_cast<const u32x4*>(xs + a * set_bytes + h * 32 + 16);
-    }
+    u32x2 w[Q][4];
 #pragma unroll
     for (int j = 0; j < Q; ++j) {
       const uint32_t d0 = h == 0 ? st.q[j].x : st.q[j].z, d1 = h == 0 ? st.q[j].y : st.q[j].w;
-      const u32x2 w0 = widen4<HALF, 0>(d0), w1 = widen4<HALF, 2>(d0);
-      const u32x2 w2 = widen4<HALF, 0>(d1), w3 = widen4<HALF, 2>(d1);
+      w[j][0] = widen4<HALF, 0>(d0);
+      w[j][1] = widen4<HALF, 2>(d0);
+      w[j][2] = widen4<HALF, 0>(d1);
+      w[j][3] = widen4<HALF, 2>(d1);
+    }
 #pragma unroll
-      for (int a = 0; a < NA; ++a) {
-        f32x4 p = {0.0f, 0.0f, 0.0f, 0.0f};
-        p = mfma4<HALF>(u32x2{x[a][0].x, x[a][0].y}, w0, p);
-        p = mfma4<HALF>(u32x2{x[a][0].z, x[a][0].w}, w1, p);
-        p = mfma4<HALF>(u32x2{x[a][1].x, x[a][1].y}, w2, p);
-        p = mfma4<HALF>(u32x2{x[a][1].z, x[a][1].w}, w3, p);
+    for (int a = 0; a < NA; ++a) {
+      f32x4 p[Q];
+#pragma unroll
+      for (int j = 0; j < Q; ++j) p[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int t = 0; t < NP; ++t) {
+        const uint8_t* x = xs + a * set_bytes + t * part_bytes + h * 32;
+        const u32x4 x0 = *reinterpret_cast<const u32x4*>(x), x1 = *reinterpret_cast<const u32x4*>(x + 16);
+#pragma unroll
+        for (int j = 0; j < Q; ++j) p[j] = mfma4<HALF>(u32x2{x0.x, x0.y}, w[j][0], p[j]);
+#pragma unroll
+        for (int j = 0; j < Q; ++j) p[j] = mfma4<HALF>(u32x2{x0.z, x0.w}, w[j][1], p[j]);
+#pragma unroll
+        for (int j = 0; j < Q; ++j) p[j] = mfma4<HALF>(u32x2{x1.x, x1.y}, w[j][2], p[j]);
+#pragma unroll
+        for (int j = 0; j < Q; ++j) p[j] = mfma4<HALF>(u32x2{x1.z, x1.w}, w[j][3], p[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < Q; ++j) {
         const float s = h == 0 ? sc[j].x : sc[j].y;
+        if constexpr (SPLIT && ROWS == 1) {
+          acc[j][0] = fmaf(p[j][0] + (p[j][1] + p[j][2]), s, acc[j][0]);
+        } else {
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (a * 4 + r < ROWS) acc[j][a * 4 + r] = fmaf(p[r], s, acc[j][a * 4 + r]);
+          for (int r = 0; r < 4; ++r)
+            if (a * 4 + r < ROWS) acc[j][a * 4 + r] = fmaf(p[j][r], s, acc[j][a * 4 + r]);
+        }
       }
     }
   }

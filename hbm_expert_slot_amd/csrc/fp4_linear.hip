@@ -37,7 +37,7 @@ constexpr int kRowPad = 16;   // bytes between operand rows in LDS: four rows' r
 template <int FMT, bool ODD, bool HALF, int ROWS, int Q, int D>
 __global__ __launch_bounds__(256) void k_fp4_rows(LinearArgs a) {
   extern __shared__ __align__(16) uint8_t lds[];
-  constexpr int V = Q * ROWS < 4 ? 4 : Q * ROWS;
+  constexpr int V = Q * ROWS;
   constexpr int G = FMT == kNv ? 16 : 32;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wk = a.wk, kw = wave & (wk - 1), rw = wave / wk;
@@ -101,15 +101,15 @@ __global__ __launch_bounds__(256) void k_fp4_rows(LinearArgs a) {
 
   float v[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) v[i] = i < Q * ROWS ? acc[i / ROWS][i % ROWS] : 0.0f;
+  for (int i = 0; i < V; ++i) v[i] = acc[i / ROWS][i % ROWS];
   tile_sum<V>(v);
   // each wavefront's sums of its K share, then their total in wavefront order
   __syncthreads();
   float* red = reinterpret_cast<float*>(lds);
-  if ((lane & 12) == 0) {
+  if (tile_sum_owner<V>(lane)) {
     const int first = tile_sum_first<V>(lane);
 #pragma unroll
-    for (int i = 0; i < V / 4; ++i) red[(wave * V + first + i) * 4 + (lane & 3)] = v[i];
+    for (int i = 0; i < kTileOut<V>; ++i) red[(wave * V + first + i) * 4 + (lane & 3)] = v[i];
   }
   __syncthreads();
   const float gs = a.gs ? *a.gs : 1.0f;
@@ -137,7 +137,7 @@ hipError_t launch_rows(LinearArgs a, hipStream_t st) {
   const int block_rows = 4 * Q * (4 / a.wk);
   // rows behind the last are read by the lanes that stand for them, and not used
   size_t lds = (size_t)ROWS * (a.kc * 2 + kRowPad);
-  const size_t red = 4 * 4 * sizeof(float) * (Q * ROWS < 4 ? 4 : Q * ROWS);
+  const size_t red = 4 * 4 * sizeof(float) * (Q * ROWS);
   if (lds < red) lds = red;
   hipLaunchKernelGGL((k_fp4_rows<FMT, ODD, HALF, ROWS, Q, D>), dim3((unsigned)((a.N + block_rows - 1) / block_rows)),
                      dim3(256), lds, st, a);

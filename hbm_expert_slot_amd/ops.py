@@ -183,3 +183,104 @@ def fp4_linear(x, q, bias=None, out_dtype=None, out=None, stream=None):
         B.fp4_linear(q._ref, x.data_ptr(), _TYPE[x.dtype], _ld(x), M, None if bias is None else bias.data_ptr(),
                      out.data_ptr(), _TYPE[out.dtype], _ld(out), s)
     return out
+
+
+def blob_bytes(hidden, inter):
+    """Bytes of one expert's blob."""
+    return 27 * hidden * inter // 16
+
+
+def expert_matrices(blob, hidden, inter, global_scales):
+    """The two matrices of an expert blob (uint8 [blob_bytes]) as FP4Weight views: w13
+    [2 inter, hidden] (gate rows, then up rows) and w2 [hidden, inter], with
+    the entries of global_scales fp32 [2]."""
+    _need(blob.dim() == 1 and blob.dtype == torch.uint8 and blob.numel() == blob_bytes(hidden, inter)
+          and hidden % 64 == 0 and inter % 64 == 0, "blob does not hold an expert of %d x %d" % (hidden, inter))
+    a, b, c = inter * hidden, inter * hidden // 8, hidden * inter // 2
+    w13 = FP4Weight(blob[:a].view(2 * inter, hidden // 2), blob[a:a + b].view(2 * inter, hidden // 16),
+                    global_scales[0:1])
+    w2 = FP4Weight(blob[a + b:a + b + c].view(hidden, inter // 2), blob[a + b + c:].view(hidden, inter // 16),
+                   global_scales[1:2])
+    return w13, w2
+
+
+class MoELayer:
+    """A whole mixture-of-experts layer for up to `max_rows` (16) tokens a call.
+
+    router bf16 [E, hidden]; blobs uint8 [E, blob_bytes] and global_scales fp32
+    [E, 2] hold the routed experts (the layout of the slot cache, all resident
+    in HBM); shared_blob and shared_global_scales [2] the shared expert, if any
+    (its inner size follows from the blob's).  score "softmax" or "sigmoid" (with
+    score_bias fp32 [E] added for the choice only); routed_scale multiplies the
+    routed sum.  The tensors are referred to, not copied.
+
+    The layer owns a workspace: calls have to be ordered with each other (one
+    stream, or streams the caller orders); use one layer object per stream
+    otherwise."""
+
+    def __init__(self, hidden, inter, top_k, router, blobs, global_scales, shared_blob=None,
+                 shared_global_scales=None, score="softmax", score_bias=None, routed_scale=1.0, max_rows=16):
+        _need(score in ("softmax", "sigmoid"), "unknown score %r" % (score,))
+        _need(router.dim() == 2 and router.shape[1] == hidden, "router must be [experts, hidden]")
+        E, dev = router.shape[0], router.device
+
+        def dense(t, name, dtype, shape):
+            _need(t.dtype == dtype and tuple(t.shape) == shape and t.is_contiguous(),
+                  "%s must be a contiguous %s tensor of shape %s" % (name, dtype, shape))
+            _need(t.is_cuda and t.device == dev, "%s must be on the GPU, with the router" % name)
+
+        dense(router, "router", torch.bfloat16, (E, hidden))
+        dense(blobs, "blobs", torch.uint8, (E, blob_bytes(hidden, inter)))
+        dense(global_scales, "global_scales", torch.float32, (E, 2))
+        shared_inter = 0
+        if shared_blob is not None:
+            _need(shared_global_scales is not None, "the shared expert needs shared_global_scales")
+            shared_inter = shared_blob.numel() * 16 // (27 * hidden)
+            dense(shared_blob, "shared_blob", torch.uint8, (blob_bytes(hidden, shared_inter),))
+            dense(shared_global_scales, "shared_global_scales", torch.float32, (2,))
+            _need(shared_inter > 0, "shared_blob is empty")
+        if score_bias is not None:
+            _need(score == "sigmoid", "only the sigmoid score has a bias")
+            dense(score_bias, "score_bias", torch.float32, (E,))
+        self._cfg = B.sc_moe_config(hidden, inter, E, top_k, shared_inter, max_rows,
+                                    B.SC_SCORE_SIGMOID if score == "sigmoid" else B.SC_SCORE_SOFTMAX, routed_scale)
+        self._cref = ctypes.byref(self._cfg)
+        n = B.moe_layer_workspace_bytes(self._cref)
+
+        def ptr(t):
+            return None if t is None else t.data_ptr()
+
+        self._keep = (router, blobs, global_scales, shared_blob, shared_global_scales, score_bias)
+        self._w = B.sc_moe_weights(ptr(router), ptr(score_bias), ptr(blobs), ptr(global_scales), ptr(shared_blob),
+                                   ptr(shared_global_scales))
+        self._wref = ctypes.byref(self._w)
+        self.hidden, self.inter, self.n_experts, self.top_k = hidden, inter, E, top_k
+        self.shared_inter, self.max_rows, self.device = shared_inter, max_rows, dev
+        with _On(dev, None) as s:
+            self.workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+            B.moe_layer_prepare(self._cref, self.workspace.data_ptr(), s)
+            torch.cuda.current_stream(dev).synchronize()
+
+    def forward(self, x, out_dtype=torch.float32, out=None, ids=None, weights=None, stream=None):
+        """y [M, hidden] for x bf16 [M, hidden], M <= max_rows.  out_dtype float32 or bfloat16.  ids int32 and
+        weights float32 [M, top_k], if given, receive the picks and their weights in rank order."""
+        _matrix(x, "x", (torch.bfloat16,))
+        _check_ld(x, "x")
+        M, dev = x.shape[0], self.device
+        _need(x.shape[1] == self.hidden and x.device == dev, "x does not fit the layer")
+        _need(M <= self.max_rows, "at most %d rows" % self.max_rows)
+        for t, name, dt in ((ids, "ids", torch.int32), (weights, "weights", torch.float32)):
+            _need(t is None or (t.dtype == dt and tuple(t.shape) == (M, self.top_k) and t.is_contiguous()
+                                and t.device == dev), "%s must be a contiguous [M, top_k] %s tensor" % (name, dt))
+        with _On(dev, stream) as s:
+            if out is None:
+                _need(out_dtype in (torch.float32, torch.bfloat16), "unsupported type %s" % (out_dtype,))
+                out = torch.empty((M, self.hidden), dtype=out_dtype, device=dev)
+            else:
+                _matrix(out, "out", (torch.float32, torch.bfloat16))
+                _check_ld(out, "out")
+                _need(tuple(out.shape) == (M, self.hidden) and out.device == dev, "out does not fit")
+            B.moe_layer_forward(self._cref, self._wref, self.workspace.data_ptr(), x.data_ptr(), _ld(x), M,
+                                out.data_ptr(), _TYPE[out.dtype], _ld(out), None if ids is None else ids.data_ptr(),
+                                None if weights is None else weights.data_ptr(), s)
+        return out

@@ -393,6 +393,60 @@ SC_API sc_status fp4_dequantize(const sc_fp4_matrix* w, void* d_w, int32_t w_typ
 SC_API sc_status fp4_linear(const sc_fp4_matrix* w, const void* d_x, int32_t x_type, int64_t ldx, int32_t M,
                             const float* d_bias, void* d_y, int32_t y_type, int64_t ldy, void* stream);
 
+/* ---- a whole MoE layer for a few tokens --------------------------------------- */
+
+#define SC_MOE_MAX_ROWS 16
+
+/* How router logits become picks and weights.  Both pick the k largest (ties
+ * to the lower expert id, NaN lowest) and multiply the weights by routed_scale.
+ *   SC_SCORE_SOFTMAX  picks by logit; weights are the softmax over the k chosen
+ *                     logits (the rule of moe_layer_decode)
+ *   SC_SCORE_SIGMOID  picks by sigmoid(logit) + bias; weights are the chosen
+ *                     sigmoids divided by their sum (equal when that is 0) */
+#define SC_SCORE_SOFTMAX 0
+#define SC_SCORE_SIGMOID 1
+
+typedef struct {
+  int32_t hidden;          /* H: a multiple of 64 in [64, 32768] */
+  int32_t inter;           /* I: a multiple of 64 in [64, 32768] */
+  int32_t n_experts;       /* top_k <= E <= 1024 */
+  int32_t top_k;           /* 1 <= k <= 32 */
+  int32_t shared_inter;    /* inner size of the shared expert, 0 for none, else as I */
+  int32_t max_rows;        /* largest M of a call, 1 .. SC_MOE_MAX_ROWS */
+  int32_t score;           /* SC_SCORE_SOFTMAX or SC_SCORE_SIGMOID */
+  float routed_scale;      /* factor of the routed experts' sum */
+} sc_moe_config;
+
+typedef struct {
+  const void* d_router;            /* bf16 [E][H], 16-byte aligned */
+  const float* d_score_bias;       /* fp32 [E] or NULL; only SC_SCORE_SIGMOID uses it */
+  const void* d_blobs;             /* [E][B_e] expert blobs in HBM, 16-byte aligned: a full slot pool, or a copy */
+  const float* d_global_scales;    /* fp32 [E][2] (w13, w2) */
+  const void* d_shared_blob;       /* the shared expert as a blob of its own inner size, 16-byte aligned */
+  const float* d_shared_scales;    /* fp32 [2] */
+} sc_moe_weights;
+
+/* Bytes of device workspace that moe_layer_forward needs. */
+SC_API sc_status moe_layer_workspace_bytes(const sc_moe_config* cfg, size_t* bytes);
+
+/* Enqueues the clearing of a new workspace's control words (256-byte aligned).
+ * Once per workspace, before its first forward call; not needed between calls. */
+SC_API sc_status moe_layer_prepare(const sc_moe_config* cfg, void* d_workspace, void* stream);
+
+/* One layer for M rows of x (bf16 [M][H], row stride ldx): y [M][H] (fp32 or
+ * bf16, row stride ldy) = sum over the row's k picks of weight * D(silu(G x) *
+ * (U x)), plus the shared expert's output.  d_ids int32 [M][k] and d_weights
+ * fp32 [M][k] receive the picks in rank order (either may be NULL).  Products
+ * are exact, sums fp32, the order of every sum is fixed; y is rounded once.  A
+ * row's result does not depend on the other rows beyond rounding, and not at
+ * all when it holds a NaN.  M == 0 does nothing.  Asynchronous on `stream`,
+ * whose device is current; no allocation; can be captured.  Calls that share a
+ * workspace must be ordered (one stream, or streams that the caller orders);
+ * y must not overlap x. */
+SC_API sc_status moe_layer_forward(const sc_moe_config* cfg, const sc_moe_weights* w, void* d_workspace,
+                                   const uint16_t* d_x, int64_t ldx, int32_t M, void* d_y, int32_t y_type,
+                                   int64_t ldy, int32_t* d_ids, float* d_weights, void* stream);
+
 /* Message for the last non-OK status returned on this thread. */
 SC_API const char* slotcache_last_error(void);
 
