@@ -179,18 +179,18 @@ __device__ __forceinline__ void load_stage(Stage<FMT, ODD, Q>& st, Rsrc rc, Rsrc
   }
 }
 
-// acc[j][r] += sum of the stage's products with operand row r.  xs: the lane's
-// operand row in LDS (row l % 4 of row set 0), 32 elements at this step; row set
-// a (rows 4a..4a+3) lies at xs + a * set_bytes.  A lane of a row behind the last
-// reads any finite or unused memory: its results are not used.
+// acc[j][r] += sum of the stage's products with operand row r.  xs[a] + at: the
+// lane's operand row of set a (row 4a + l % 4) in LDS, 32 elements at this step.
+// A lane of a row behind the last reads any memory: its results are not used.
 //
 // SPLIT: the operand is fp32, held as three bf16 parts that add up to it (24
 // bits).  With one row the parts stand as three rows of its set and their sums
-// are added; otherwise part p lies at xs + p * part_bytes and the matrix
+// are added; otherwise part p lies at + p * part_bytes and the matrix
 // instructions add all three into one sum.
 template <int FMT, bool ODD, int Q, int ROWS, bool HALF, bool SPLIT = false>
-__device__ __forceinline__ void use_stage(const Stage<FMT, ODD, Q>& st, const uint8_t* xs, int set_bytes,
-                                          float (&acc)[Q][ROWS], int part_bytes = 0) {
+__device__ __forceinline__ void use_stage(const Stage<FMT, ODD, Q>& st,
+                                          const uint8_t* const (&xs)[(ROWS + 3) / 4], int at, float (&acc)[Q][ROWS],
+                                          int part_bytes = 0) {
   constexpr int NA = (ROWS + 3) / 4, NP = SPLIT && ROWS > 1 ? 3 : 1;
   f32x2 sc[Q];
 #pragma unroll
@@ -213,7 +213,7 @@ __device__ __forceinline__ void use_stage(const Stage<FMT, ODD, Q>& st, const ui
       for (int j = 0; j < Q; ++j) p[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int t = 0; t < NP; ++t) {
-        const uint8_t* x = xs + a * set_bytes + t * part_bytes + h * 32;
+        const uint8_t* x = xs[a] + at + t * part_bytes + h * 32;
         const u32x4 x0 = *reinterpret_cast<const u32x4*>(x), x1 = *reinterpret_cast<const u32x4*>(x + 16);
 #pragma unroll
         for (int j = 0; j < Q; ++j) p[j] = mfma4<HALF>(u32x2{x0.x, x0.y}, w[j][0], p[j]);

@@ -59,7 +59,9 @@ __global__ __launch_bounds__(256) void k_fp4_rows(LinearArgs a) {
     for (int r = 0; r < ROWS; ++r) acc[j][r] = 0.0f;
 
   const int r0 = lane & 3;
-  const uint8_t* xs = lds + (r0 < ROWS ? r0 : 0) * row_lds + klane * 2;
+  const uint8_t* xs[(ROWS + 3) / 4];
+#pragma unroll
+  for (int s = 0; s < (ROWS + 3) / 4; ++s) xs[s] = lds + (4 * s + r0 < ROWS ? 4 * s + r0 : 0) * row_lds + klane * 2;
   for (int kc = 0; kc < a.K; kc += a.kc) {
     const int kend = min(a.K, kc + a.kc);
     const int steps = (kend - kc + kStepK - 1) / kStepK;
@@ -87,12 +89,11 @@ __global__ __launch_bounds__(256) void k_fp4_rows(LinearArgs a) {
       *reinterpret_cast<u32x4*>(lds + r * row_lds + c * 2) = v;
     }
     __syncthreads();
-    const uint8_t* xk = xs + kw * kStepK * 2;
     for (int i = 0; i < n; i += D) {
 #pragma unroll
       for (int d = 0; d < D; ++d) {
         if (i + d < n) {
-          use_stage<FMT, ODD, Q, ROWS, HALF>(st[d], xk + (i + d) * wk * kStepK * 2, 4 * row_lds, acc);
+          use_stage<FMT, ODD, Q, ROWS, HALF>(st[d], xs, ((i + d) * wk + kw) * kStepK * 2, acc);
           load_stage<FMT, ODD, Q>(st[d], rc, rs, code0, scale0, 4 * cb, 4 * sb, k0 + (i + d + D) * wk * kStepK, kend);
         }
       }

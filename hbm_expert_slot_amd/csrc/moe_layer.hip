@@ -1,5 +1,21 @@
-// A whole mixture-of-experts layer for up to 16 tokens: router product, top-k,
-// gate/up, SiLU, down, weighted combine and the shared expert.
+// A whole mixture-of-experts layer for up to 16 tokens in one launch: router
+// product, top-k, gate/up, SiLU, down, weighted combine and the shared expert.
+//
+// Bound: HBM, by the bytes of the experts picked.  Between the products there
+// is nothing to compute, only data to hand over, so the layer is one kernel of
+// tasks that blocks take in order from a counter:
+//   router tiles | shared gate/up tiles | routed gate/up tiles | down tiles
+// A task waits only for tasks before it: a router tile for none, a routed
+// gate/up tile for the picks (made by the block that ends the last router
+// tile), a down tile for all h of its expert.  The first unfinished task is
+// always held by a running block and waits for finished ones only, so every
+// wait ends, whatever part of the grid is resident.  A down tile starts its
+// weight loads before it waits.
+//
+// What one block hands to another goes through stores and loads at agent scope
+// (each XCD has an L2 of its own): written through, waited for, then counted.
+// A release fence would write back every dirty line of the L2 instead, other
+// kernels' among them (measured: 12 of 21 us of the router product).
 #include "fp4_device.h"
 #include "internal.h"
 
@@ -16,9 +32,18 @@ constexpr int kPad = 16;           // bytes between operand rows in LDS: four ro
 constexpr int kUpRows = 32;        // rows of h per gate/up task
 constexpr int kDownRows = 64;      // output rows per down task
 
-// Control words.  They are zero between calls: each counter is set back by the
-// block that finds it complete.
-enum Ctl { C_ARRIVED = 0, C_UNIQ = 1, C_TILES = 64 };
+// Control words, zero between calls: the block that leaves last clears them.
+// C_ROUTED holds the number of unique experts + 1 once the picks are made; the
+// hot ones lie in cache lines of their own.
+enum Ctl { C_TICKET = 0, C_ARRIVED = 32, C_ROUTED = 64, C_EXITS = 96, C_ERROR = 97, C_HDONE = 128 };
+constexpr int kHdone = kMaxPk + 1;                 // gate/up tiles done, per unique expert, then the shared one
+constexpr int kTiles = 32768 / kDownRows;          // down tasks done, per tile
+constexpr int kCtlWords = C_HDONE + kHdone + kTiles;
+constexpr int C_TILES = C_HDONE + kHdone;
+
+// Polls of a wait before the call is given up (about a second): only a
+// workspace that was not prepared, or that two calls share, gets there.
+constexpr int kMaxPolls = 1 << 20;
 
 struct MoeArgs {
   const uint16_t* router;    // [E][H] bf16
@@ -33,16 +58,31 @@ struct MoeArgs {
   float* w_out;              // [M][k] or null
   int32_t* ctl;
   float* logits;             // [M][E]
-  int32_t* uniq_expert;      // [U]
-  int32_t* uniq_off;         // [U + 1]
-  int32_t* uniq_picks;       // [P]
+  uint64_t* uniq;            // [U] expert, first pick and pick count
+  uint32_t* uniq_picks;      // [P]
   float* pick_w;             // [P]
   float* h;                  // [P][I], then [M][Is] of the shared expert
   float* part;               // [P][H], then [M][H]
   int64_t ldx, ldy, blob;
-  int M, H, I, E, k, Is, score, out, vec, lds;
+  int M, H, I, E, k, Is, score, out, vec;
+  int lds;                   // bytes of LDS for operand rows
+  int dense;                 // x lies in LDS whole, token by token
+  int router_tiles;
   float scale;
 };
+
+// Hand-over between blocks.
+template <typename T>
+__device__ __forceinline__ void put(T* p, T v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename T>
+__device__ __forceinline__ T get(const T* p) {
+  return __hip_atomic_load(const_cast<T*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+constexpr int kAgent = 16;   // buffer load at agent scope (sc1)
+// The wavefront's stores have been performed.
+__device__ __forceinline__ void stores_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // ---- routing -------------------------------------------------------------------
 
@@ -94,7 +134,7 @@ __device__ __forceinline__ void router_tile(const MoeArgs& a, int tile, float* r
   __syncthreads();
   for (int i = threadIdx.x; i < V; i += kThreads) {
     const int m = i / EB, e = e0 + i % EB;
-    if (m < a.M && e < a.E) a.logits[m * a.E + e] = ((red[i] + red[V + i]) + red[2 * V + i]) + red[3 * V + i];
+    if (m < a.M && e < a.E) put(&a.logits[m * a.E + e], ((red[i] + red[V + i]) + red[2 * V + i]) + red[3 * V + i]);
   }
 }
 
@@ -120,6 +160,7 @@ struct RouteLds {
   uint32_t rows[kMaxExperts];     // rows that picked the expert, then its place among the unique experts
   int32_t off[kMaxExperts];       // first pick of the expert
   int16_t id[kMaxPk];
+  int32_t nu;
 };
 
 // One wavefront picks a row's experts: lane l looks after experts l * epl ..,
@@ -136,7 +177,7 @@ __device__ __forceinline__ void route_row(const MoeArgs& a, int m, RouteLds& s) 
     key[i] = INT32_MIN;
     val[i] = 0.0f;
     if (i < epl && e < a.E) {
-      float z = a.logits[m * a.E + e];
+      float z = get(&a.logits[m * a.E + e]);
       if (a.score == SC_SCORE_SIGMOID) {
         z = 1.0f / (1.0f + expf(-z));
         val[i] = z;
@@ -190,7 +231,7 @@ __device__ __forceinline__ void route_row(const MoeArgs& a, int m, RouteLds& s) 
   if (on) {
     const int p = m * a.k + lane;
     s.id[p] = (int16_t)my_id;
-    a.pick_w[p] = w;
+    put(&a.pick_w[p], w);
     if (a.ids_out) a.ids_out[p] = my_id;
     if (a.w_out) a.w_out[p] = w;
     atomicOr(&s.rows[my_id], 1u << m);
@@ -223,46 +264,51 @@ __device__ __forceinline__ void route_all(const MoeArgs& a, RouteLds& s) {
       }
       if (n > 0) {
         const int u = nu + __popcll(mask & ((1ull << lane) - 1));
-        a.uniq_expert[u] = e;
-        a.uniq_off[u] = np + incl - n;
+        put(&a.uniq[u], (uint64_t)(uint32_t)e << 32 | (uint32_t)(np + incl - n) << 8 | (uint32_t)n);
         s.off[e] = np + incl - n;
       }
       nu += __popcll(mask);
       np += __shfl(incl, 63);
     }
-    if (lane == 0) {
-      a.uniq_off[nu] = np;
-      a.ctl[C_UNIQ] = nu;
-    }
+    if (lane == 0) s.nu = nu;
   }
   __syncthreads();
   for (int p = threadIdx.x; p < a.M * a.k; p += kThreads) {
     const int e = s.id[p], m = p / a.k;
-    a.uniq_picks[s.off[e] + __popc(s.rows[e] & ((1u << m) - 1))] = p;
+    put(&a.uniq_picks[s.off[e] + __popc(s.rows[e] & ((1u << m) - 1))], (uint32_t)p);
   }
+  stores_done();
+  __syncthreads();
+  if (threadIdx.x == 0) put(&a.ctl[C_ROUTED], s.nu + 1);
 }
 
-// True in the block that arrives last; everything stored before is visible to it.
-__device__ __forceinline__ bool arrive_last(int32_t* counter, int total, int32_t* flag) {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
+// Counts the block in, once all that its threads put has been performed; true
+// in the block that completes `total`.
+__device__ __forceinline__ bool arrive(int32_t* counter, int total, int32_t* flag) {
+  stores_done();
   __syncthreads();
-  if (threadIdx.x == 0) {
-    const int n = __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    *flag = n == total - 1;
-    if (n == total - 1) __hip_atomic_store(counter, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  }
+  if (threadIdx.x == 0)
+    *flag = __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == total - 1;
   __syncthreads();
-  const bool last = *flag != 0;
-  if (last) __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-  return last;
+  return *flag != 0;
 }
-
-template <int EB, int MR>
-__global__ __launch_bounds__(kThreads) void k_moe_route(MoeArgs a) {
-  __shared__ RouteLds s;
-  __shared__ int32_t flag;
-  router_tile<EB, MR>(a, blockIdx.x, reinterpret_cast<float*>(&s));
-  if (arrive_last(a.ctl + C_ARRIVED, gridDim.x, &flag)) route_all(a, s);
+// Same without asking who was last.
+__device__ __forceinline__ void post(int32_t* counter) {
+  stores_done();
+  __syncthreads();
+  if (threadIdx.x == 0) __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// Waits until *p >= value (one thread); false when the call was given up.
+__device__ __forceinline__ bool wait_for(const MoeArgs& a, const int32_t* p, int value) {
+  for (int i = 0; get(p) < value; ++i) {
+    if (get(&a.ctl[C_ERROR])) return false;
+    if (i >= kMaxPolls) {
+      put(&a.ctl[C_ERROR], 1);
+      return false;
+    }
+    __builtin_amdgcn_s_sleep(1);
+  }
+  return true;
 }
 
 // ---- expert products ----------------------------------------------------------
@@ -271,16 +317,27 @@ __global__ __launch_bounds__(kThreads) void k_moe_route(MoeArgs a) {
 struct Work {
   const uint8_t* blob;
   float gs13, gs2;
-  int inter, n, first;     // first: offset in uniq_picks, or -1 for the shared expert
-  int off;                 // row of h and part: picks themselves, or P + row
+  int inter, n;            // n rows
+  int first;               // offset in the list of picks, or -1 for the shared expert
+  int u;                   // unique index; U for the shared expert
 };
 
-__device__ __forceinline__ Work work_of(const MoeArgs& a, int u, int U) {
+// The picks as a block keeps them.
+struct BlockLds {
+  uint64_t uniq[kMaxPk];
+  uint16_t pick[kMaxPk];
+  int32_t tick, flag, U;
+};
+
+__device__ __forceinline__ Work work_of(const MoeArgs& a, const BlockLds& b, int u, bool shared) {
   Work w;
-  if (u < U) {
-    const int e = __builtin_amdgcn_readfirstlane(a.uniq_expert[u]);
-    w.first = __builtin_amdgcn_readfirstlane(a.uniq_off[u]);
-    w.n = __builtin_amdgcn_readfirstlane(a.uniq_off[u + 1]) - w.first;
+  w.u = u;
+  if (!shared) {
+    const uint64_t d = b.uniq[u];
+    const int e = __builtin_amdgcn_readfirstlane((int)(d >> 32));
+    const int lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)d);
+    w.first = lo >> 8;
+    w.n = lo & 255;
     w.blob = a.blobs + e * a.blob;
     w.gs13 = a.gs[2 * e];
     w.gs2 = a.gs[2 * e + 1];
@@ -295,16 +352,17 @@ __device__ __forceinline__ Work work_of(const MoeArgs& a, int u, int U) {
   }
   return w;
 }
-__device__ __forceinline__ int pick_at(const MoeArgs& a, const Work& w, int c) {
-  return w.first < 0 ? a.M * a.k + c : a.uniq_picks[w.first + c];
+// The expert's c-th pick (P + row for the shared expert) and its token.
+__device__ __forceinline__ int pick_at(const MoeArgs& a, const BlockLds& b, const Work& w, int c) {
+  return w.first < 0 ? a.M * a.k + c : b.pick[w.first + c];
 }
-__device__ __forceinline__ int token_at(const MoeArgs& a, const Work& w, int c) {
-  return w.first < 0 ? c : a.uniq_picks[w.first + c] / a.k;
+__device__ __forceinline__ int token_at(const MoeArgs& a, const BlockLds& b, const Work& w, int c) {
+  return w.first < 0 ? c : (int)((uint32_t)b.pick[w.first + c] / (uint32_t)a.k);
 }
-// h rows: picks [P][I], then the shared expert's [M][Is]
-__device__ __forceinline__ float* h_row(const MoeArgs& a, const Work& w, int p) {
-  const int P = a.M * a.k;
-  return p < P ? a.h + (int64_t)p * a.I : a.h + (int64_t)P * a.I + (int64_t)(p - P) * a.Is;
+// First element of a pick's row of h: picks [P][I], then the shared expert's [M][Is]
+__device__ __forceinline__ uint32_t h_at(const MoeArgs& a, int p) {
+  const uint32_t P = a.M * a.k;
+  return (uint32_t)p < P ? (uint32_t)p * a.I : P * a.I + ((uint32_t)p - P) * a.Is;
 }
 
 __device__ __forceinline__ float silu(float g) {
@@ -318,172 +376,213 @@ __device__ __forceinline__ int lds_range(int lds, int rows, int parts, int K) {
   return fit < need ? fit : need;
 }
 
-// h rows [tile * 32, +32) of an expert: a wavefront takes two quads of gate
-// rows and the quads of up rows that belong to them.
-template <int ROWS>
-__device__ __forceinline__ void gateup_task(const MoeArgs& a, const Work& w, int tile, uint8_t* lds) {
-  constexpr int Q = 4, D = 2;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int H = a.H, row0 = tile * kUpRows + wave * 8;
-  const uint32_t cb = H / 2, sb = H / 16;
-  const int64_t codes = (int64_t)2 * w.inter * cb;
-  const uint32_t up = (uint32_t)w.inter;
-  // quads: gate rows row0, row0 + 4, then the up rows of both
-  const Rsrc rc = make_rsrc(w.blob, (uint32_t)codes), rs = make_rsrc(w.blob + codes, 2u * up * sb);
-  const uint32_t r = row0 + (lane & 3);
-  const int klane = (lane >> 2) * 32;
-  const int KC = lds_range(a.lds, ROWS, 1, H);
-  const int row_lds = KC * 2 + kPad, r0 = lane & 3;
-  const uint8_t* xs = lds + (r0 < ROWS ? r0 : 0) * row_lds + klane * 2;
-  float acc[Q][ROWS];
+// `n` rows of x from column kc to kend (rounded up to whole steps, zeros behind
+// the end) into LDS; row c is token tok(c).
+template <typename F>
+__device__ __forceinline__ void stage_x(const MoeArgs& a, uint8_t* lds, int row_lds, int n, int kc, int kend, F tok) {
+  const int per_row = (kend - kc + kStepK - 1) / kStepK * (kStepK / 8);
+  for (int i = threadIdx.x; i < n * per_row; i += kThreads) {
+    const int c = i / per_row, o = (i - c * per_row) * 8;
+    u32x4 v = {0, 0, 0, 0};
+    if (kc + o < kend) {
+      const uint16_t* p = a.x + tok(c) * a.ldx + kc + o;
+      if (a.vec) {
+        v = *reinterpret_cast<const u32x4*>(p);
+      } else {
 #pragma unroll
-  for (int j = 0; j < Q; ++j)
-#pragma unroll
-    for (int c = 0; c < ROWS; ++c) acc[j][c] = 0.0f;
+        for (int e = 0; e < 4; ++e) v[e] = p[2 * e] | (uint32_t)p[2 * e + 1] << 16;
+      }
+    }
+    *reinterpret_cast<u32x4*>(lds + c * row_lds + o * 2) = v;
+  }
+}
 
-  typedef Stage<kNv, false, 2> St;
-  for (int kc = 0; kc < H; kc += KC) {
-    const int kend = min(H, kc + KC), steps = (kend - kc + kStepK - 1) / kStepK;
-    St g[D], u[D];
-    auto load = [&](int d, int s) {
-      load_stage<kNv, false, 2>(g[d], rc, rs, r * cb, r * sb, 4 * cb, 4 * sb, kc + s * kStepK + klane, kend);
-      load_stage<kNv, false, 2>(u[d], rc, rs, (r + up) * cb, (r + up) * sb, 4 * cb, 4 * sb, kc + s * kStepK + klane, kend);
-    };
+// h rows [tile * 32, +32) of an expert: a wavefront takes HQ quads of gate rows
+// at a time and the quads of up rows that belong to them.  x_there: all of x
+// lies in LDS (dense) and needs no staging.
+template <int ROWS>
+__device__ __forceinline__ void gateup_task(const MoeArgs& a, const BlockLds& b, const Work& w, int tile, uint8_t* lds,
+                                            bool x_there) {
+  constexpr int HQ = ROWS <= 4 ? 2 : 1, D = 2, NA = (ROWS + 3) / 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int H = a.H;
+  const uint32_t cb = H / 2, sb = H / 16, up = (uint32_t)w.inter;
+  const Rsrc rc = make_rsrc(w.blob, 2u * up * cb), rs = make_rsrc(w.blob + (int64_t)2 * up * cb, 2u * up * sb);
+  const int klane = (lane >> 2) * 32, r0 = lane & 3;
+  const int KC = a.dense ? (H + kStepK - 1) / kStepK * kStepK : lds_range(a.lds, ROWS, 1, H);
+  const int row_lds = KC * 2 + kPad;
+  const uint8_t* xs[NA];
 #pragma unroll
-    for (int d = 0; d < D; ++d) load(d, d);
-    __syncthreads();
-    const int per_row = steps * (kStepK / 8);
-    for (int i = threadIdx.x; i < w.n * per_row; i += kThreads) {
-      const int c = i / per_row, o = (i - c * per_row) * 8;
-      u32x4 v = {0, 0, 0, 0};
-      if (kc + o < kend) {
-        const uint16_t* p = a.x + token_at(a, w, c) * a.ldx + kc + o;
-        if (a.vec) {
-          v = *reinterpret_cast<const u32x4*>(p);
-        } else {
+  for (int s = 0; s < NA; ++s) {
+    const int c = 4 * s + r0 < w.n ? 4 * s + r0 : 0;
+    xs[s] = lds + (a.dense ? token_at(a, b, w, c) : c) * row_lds + klane * 2;
+  }
+  for (int part = 0; part < kUpRows / 4 / kWaves; part += HQ) {
+    const int row0 = tile * kUpRows + (wave * (kUpRows / 4 / kWaves) + part) * 4;
+    const uint32_t r = row0 + r0;
+    float acc[2 * HQ][ROWS];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = p[2 * e] | (uint32_t)p[2 * e + 1] << 16;
-        }
+    for (int j = 0; j < 2 * HQ; ++j)
+#pragma unroll
+      for (int c = 0; c < ROWS; ++c) acc[j][c] = 0.0f;
+    for (int kc = 0; kc < H; kc += KC) {
+      const int kend = min(H, kc + KC), steps = (kend - kc + kStepK - 1) / kStepK;
+      Stage<kNv, false, HQ> g[D], u[D];
+      auto load = [&](int d, int s) {
+        const int k = kc + s * kStepK + klane;
+        load_stage<kNv, false, HQ>(g[d], rc, rs, r * cb, r * sb, 4 * cb, 4 * sb, k, kend);
+        load_stage<kNv, false, HQ>(u[d], rc, rs, (r + up) * cb, (r + up) * sb, 4 * cb, 4 * sb, k, kend);
+      };
+#pragma unroll
+      for (int d = 0; d < D; ++d) load(d, d);
+      if (!x_there) {
+        __syncthreads();
+        if (a.dense) stage_x(a, lds, row_lds, a.M, 0, H, [&](int c) { return c; });
+        else stage_x(a, lds, row_lds, w.n, kc, kend, [&](int c) { return token_at(a, b, w, c); });
+        __syncthreads();
       }
-      *reinterpret_cast<u32x4*>(lds + c * row_lds + o * 2) = v;
-    }
-    __syncthreads();
-    for (int s = 0; s < steps; s += D) {
+      for (int s = 0; s < steps; s += D) {
 #pragma unroll
-      for (int d = 0; d < D; ++d) {
-        if (s + d < steps) {
-          Stage<kNv, false, 4> st;
+        for (int d = 0; d < D; ++d) {
+          if (s + d < steps) {
+            Stage<kNv, false, 2 * HQ> st;
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            st.q[j] = g[d].q[j];
-            st.s[j] = g[d].s[j];
-            st.q[2 + j] = u[d].q[j];
-            st.s[2 + j] = u[d].s[j];
+            for (int j = 0; j < HQ; ++j) {
+              st.q[j] = g[d].q[j];
+              st.s[j] = g[d].s[j];
+              st.q[HQ + j] = u[d].q[j];
+              st.s[HQ + j] = u[d].s[j];
+            }
+            use_stage<kNv, false, 2 * HQ, ROWS, false>(st, xs, (s + d) * kStepK * 2, acc);
+            load(d, s + d + D);
           }
-          use_stage<kNv, false, 4, ROWS, false>(st, xs + (s + d) * kStepK * 2, 4 * row_lds, acc);
-          load(d, s + d + D);
         }
       }
     }
-  }
-  constexpr int V = 2 * ROWS;
-  float vg[V], vu[V];
+    x_there = x_there || a.dense;
+    constexpr int V = HQ * ROWS;
+    float vg[V], vu[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    vg[i] = acc[i / ROWS][i % ROWS];
-    vu[i] = acc[2 + i / ROWS][i % ROWS];
-  }
-  tile_sum<V>(vg);
-  tile_sum<V>(vu);
-  if (tile_sum_owner<V>(lane)) {
-    const int first = tile_sum_first<V>(lane);
+    for (int i = 0; i < V; ++i) {
+      vg[i] = acc[i / ROWS][i % ROWS];
+      vu[i] = acc[HQ + i / ROWS][i % ROWS];
+    }
+    tile_sum<V>(vg);
+    tile_sum<V>(vu);
+    if (tile_sum_owner<V>(lane)) {
+      const int first = tile_sum_first<V>(lane);
 #pragma unroll
-    for (int i = 0; i < kTileOut<V>; ++i) {
-      const int q = (first + i) / ROWS, c = (first + i) % ROWS;
-      if (c < w.n) h_row(a, w, pick_at(a, w, c))[row0 + 4 * q + (lane & 3)] = silu(vg[i] * w.gs13) * (vu[i] * w.gs13);
+      for (int i = 0; i < kTileOut<V>; ++i) {
+        const int q = (first + i) / ROWS, c = (first + i) % ROWS;
+        if (c < w.n)
+          put(&a.h[h_at(a, pick_at(a, b, w, c)) + row0 + 4 * q + r0], silu(vg[i] * w.gs13) * (vu[i] * w.gs13));
+      }
     }
   }
 }
 
 // Output rows [tile * 64, +64) of an expert's down product, per pick.  h is
 // used to its 24 bits, in three bf16 parts: rounded to one part it would put
-// 2^-9 of itself into y, more than all fp32 sums together.
+// 2^-9 of itself into y, more than all fp32 sums together.  False when the call
+// was given up.
 template <int ROWS>
-__device__ __forceinline__ void down_task(const MoeArgs& a, const Work& w, int tile, uint8_t* lds) {
-  constexpr int Q = 4, D = 2;
+__device__ __forceinline__ bool down_task(const MoeArgs& a, BlockLds& b, const Work& w, int tile, uint8_t* lds) {
+  constexpr int Q = ROWS <= 4 ? 4 : 2, D = 2, NA = (ROWS + 3) / 4;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int I = w.inter, row0 = tile * kDownRows + wave * 16;
+  const int I = w.inter;
   const uint32_t cb = I / 2, sb = I / 16;
-  const int64_t w13 = (int64_t)2 * I * (a.H / 2) + (int64_t)2 * I * (a.H / 16);
-  const int64_t codes = (int64_t)a.H * cb;
+  const int64_t w13 = (int64_t)2 * I * (a.H / 2) + (int64_t)2 * I * (a.H / 16), codes = (int64_t)a.H * cb;
   const Rsrc rc = make_rsrc(w.blob + w13, (uint32_t)codes), rs = make_rsrc(w.blob + w13 + codes, (uint32_t)a.H * sb);
-  const uint32_t r = row0 + (lane & 3);
-  const int klane = (lane >> 2) * 32;
+  const Rsrc rh = make_rsrc(a.h, (uint32_t)(a.M * (a.k * a.I + a.Is)) * 4);
+  const int klane = (lane >> 2) * 32, r0 = lane & 3;
   const int KC = lds_range(a.lds, ROWS, 3, I);
-  const int part_lds = KC * 2 + kPad, row_lds = 3 * part_lds, r0 = lane & 3;
-  // one row: its parts are the rows of the set
-  const uint8_t* xs = lds + (ROWS == 1 ? (r0 < 3 ? r0 : 0) * part_lds : (r0 < ROWS ? r0 : 0) * row_lds) + klane * 2;
-  float acc[Q][ROWS];
+  const int part_lds = KC * 2 + kPad, row_lds = 3 * part_lds;
+  const uint8_t* xs[NA];
 #pragma unroll
-  for (int j = 0; j < Q; ++j)
+  for (int s = 0; s < NA; ++s) {
+    // one row: its parts are the rows of the set
+    const int c = 4 * s + r0 < w.n ? 4 * s + r0 : 0;
+    xs[s] = lds + (ROWS == 1 ? (r0 < 3 ? r0 : 0) * part_lds : c * row_lds) + klane * 2;
+  }
+  bool waited = false;
+  for (int part = 0; part < kDownRows / 4 / kWaves; part += Q) {
+    const int row0 = tile * kDownRows + (wave * (kDownRows / 4 / kWaves) + part) * 4;
+    const uint32_t r = row0 + r0;
+    float acc[Q][ROWS];
 #pragma unroll
-    for (int c = 0; c < ROWS; ++c) acc[j][c] = 0.0f;
-  typedef Stage<kNv, false, Q> St;
-  for (int kc = 0; kc < I; kc += KC) {
-    const int kend = min(I, kc + KC), steps = (kend - kc + kStepK - 1) / kStepK;
-    St st[D];
+    for (int j = 0; j < Q; ++j)
 #pragma unroll
-    for (int d = 0; d < D; ++d)
-      load_stage<kNv, false, Q>(st[d], rc, rs, r * cb, r * sb, 4 * cb, 4 * sb, kc + d * kStepK + klane, kend);
-    __syncthreads();
-    const int per_row = steps * (kStepK / 4);
-    for (int i = threadIdx.x; i < w.n * per_row; i += kThreads) {
-      const int c = i / per_row, o = (i - c * per_row) * 4;
-      f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (kc + o < kend) v = *reinterpret_cast<const f32x4*>(h_row(a, w, pick_at(a, w, c)) + kc + o);
-      uint8_t* dst = lds + c * row_lds + o * 2;
-      uint16_t b[3][4];
+      for (int c = 0; c < ROWS; ++c) acc[j][c] = 0.0f;
+    for (int kc = 0; kc < I; kc += KC) {
+      const int kend = min(I, kc + KC), steps = (kend - kc + kStepK - 1) / kStepK;
+      Stage<kNv, false, Q> st[D];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const __bf16 p0 = (__bf16)v[e];
-        const float f0 = (float)p0, d1 = v[e] - f0;
-        const bool fin = fabsf(f0) < INFINITY;      // what is not finite stands in the first part alone
-        const __bf16 p1 = (__bf16)(fin ? d1 : 0.0f);
-        const __bf16 p2 = (__bf16)(fin ? d1 - (float)p1 : 0.0f);
-        b[0][e] = __builtin_bit_cast(uint16_t, p0);
-        b[1][e] = __builtin_bit_cast(uint16_t, p1);
-        b[2][e] = __builtin_bit_cast(uint16_t, p2);
+      for (int d = 0; d < D; ++d)
+        load_stage<kNv, false, Q>(st[d], rc, rs, r * cb, r * sb, 4 * cb, 4 * sb, kc + d * kStepK + klane, kend);
+      if (!waited) {
+        if (threadIdx.x == 0) b.flag = wait_for(a, &a.ctl[C_HDONE + w.u], I / kUpRows);
+        waited = true;
       }
+      if (part == 0 || KC < I) {
+        __syncthreads();
+        if (!b.flag) return false;
+        const int per_row = steps * (kStepK / 4);
+        for (int i = threadIdx.x; i < w.n * per_row; i += kThreads) {
+          const int c = i / per_row, o = (i - c * per_row) * 4;
+          const u32x4 t = __builtin_amdgcn_raw_buffer_load_b128(
+              rh, kc + o < kend ? (int)((h_at(a, pick_at(a, b, w, c)) + kc + o) * 4) : (int)kBeyond, 0, kAgent);
+          const f32x4 v = __builtin_bit_cast(f32x4, t);
+          uint16_t p[3][4];
 #pragma unroll
-      for (int t = 0; t < 3; ++t)
-        *reinterpret_cast<u32x2*>(dst + t * part_lds) =
-            u32x2{b[t][0] | (uint32_t)b[t][1] << 16, b[t][2] | (uint32_t)b[t][3] << 16};
-    }
-    __syncthreads();
-    for (int s = 0; s < steps; s += D) {
+          for (int e = 0; e < 4; ++e) {
+            const __bf16 p0 = (__bf16)v[e];
+            const float f0 = (float)p0, d1 = v[e] - f0;
+            const bool fin = fabsf(f0) < INFINITY;      // what is not finite stands in the first part alone
+            const __bf16 p1 = (__bf16)(fin ? d1 : 0.0f);
+            const __bf16 p2 = (__bf16)(fin ? d1 - (float)p1 : 0.0f);
+            p[0][e] = __builtin_bit_cast(uint16_t, p0);
+            p[1][e] = __builtin_bit_cast(uint16_t, p1);
+            p[2][e] = __builtin_bit_cast(uint16_t, p2);
+          }
 #pragma unroll
-      for (int d = 0; d < D; ++d) {
-        if (s + d < steps) {
-          use_stage<kNv, false, Q, ROWS, false, true>(st[d], xs + (s + d) * kStepK * 2, 4 * row_lds, acc, part_lds);
-          load_stage<kNv, false, Q>(st[d], rc, rs, r * cb, r * sb, 4 * cb, 4 * sb, kc + (s + d + D) * kStepK + klane,
-                                    kend);
+          for (int t3 = 0; t3 < 3; ++t3)
+            *reinterpret_cast<u32x2*>(lds + c * row_lds + t3 * part_lds + o * 2) =
+                u32x2{p[t3][0] | (uint32_t)p[t3][1] << 16, p[t3][2] | (uint32_t)p[t3][3] << 16};
+        }
+        __syncthreads();
+      }
+      for (int s = 0; s < steps; s += D) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+          if (s + d < steps) {
+            use_stage<kNv, false, Q, ROWS, false, true>(st[d], xs, (s + d) * kStepK * 2, acc, part_lds);
+            load_stage<kNv, false, Q>(st[d], rc, rs, r * cb, r * sb, 4 * cb, 4 * sb, kc + (s + d + D) * kStepK + klane,
+                                      kend);
+          }
         }
       }
     }
-  }
-  constexpr int V = Q * ROWS;
-  float v[V];
+    constexpr int V = Q * ROWS;
+    float v[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) v[i] = acc[i / ROWS][i % ROWS];
-  tile_sum<V>(v);
-  if (tile_sum_owner<V>(lane)) {
-    const int first = tile_sum_first<V>(lane);
+    for (int i = 0; i < V; ++i) v[i] = acc[i / ROWS][i % ROWS];
+    tile_sum<V>(v);
+    if (tile_sum_owner<V>(lane)) {
+      const int first = tile_sum_first<V>(lane);
 #pragma unroll
-    for (int i = 0; i < kTileOut<V>; ++i) {
-      const int q = (first + i) / ROWS, c = (first + i) % ROWS;
-      if (c < w.n) a.part[(int64_t)pick_at(a, w, c) * a.H + row0 + 4 * q + (lane & 3)] = v[i] * w.gs2;
+      for (int i = 0; i < kTileOut<V>; ++i) {
+        const int q = (first + i) / ROWS, c = (first + i) % ROWS;
+        if (c < w.n) put(&a.part[(int64_t)pick_at(a, b, w, c) * a.H + row0 + 4 * q + r0], v[i] * w.gs2);
+      }
     }
   }
+  return true;
+}
+
+__device__ __forceinline__ void store_y(const MoeArgs& a, int m, int r, float v) {
+  const int64_t o = m * a.ldy + r;
+  if (a.out == SC_DTYPE_F32) static_cast<float*>(a.y)[o] = v;
+  else static_cast<uint16_t*>(a.y)[o] = __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
 // y of 64 rows: the picks in rank order, then the shared expert.
@@ -492,59 +591,94 @@ __device__ __forceinline__ void combine_tile(const MoeArgs& a, int tile) {
   for (int i = threadIdx.x; i < a.M * kDownRows; i += kThreads) {
     const int m = i / kDownRows, r = tile * kDownRows + i % kDownRows;
     float s = 0.0f;
-    for (int j = 0; j < a.k; ++j) s = fmaf(a.pick_w[m * a.k + j], a.part[(int64_t)(m * a.k + j) * a.H + r], s);
-    if (a.shared) s += a.part[(int64_t)(P + m) * a.H + r];
-    const int64_t o = m * a.ldy + r;
-    if (a.out == SC_DTYPE_F32) static_cast<float*>(a.y)[o] = s;
-    else static_cast<uint16_t*>(a.y)[o] = __builtin_bit_cast(uint16_t, (__bf16)s);
+    for (int j = 0; j < a.k; ++j)
+      s = fmaf(get(&a.pick_w[m * a.k + j]), get(&a.part[(int64_t)(m * a.k + j) * a.H + r]), s);
+    if (a.shared) s += get(&a.part[(int64_t)(P + m) * a.H + r]);
+    store_y(a, m, r, s);
   }
 }
 
 template <int MAXR>
-__device__ __forceinline__ void run_gateup(const MoeArgs& a, const Work& w, int tile, uint8_t* lds) {
-  if (MAXR == 1 || w.n == 1) return gateup_task<1>(a, w, tile, lds);
-  if (w.n == 2) return gateup_task<2>(a, w, tile, lds);
-  if (MAXR == 4 || w.n <= 4) return gateup_task<4>(a, w, tile, lds);
-  if constexpr (MAXR > 4) {
-    if (w.n <= 8) return gateup_task<8>(a, w, tile, lds);
-    return gateup_task<16>(a, w, tile, lds);
-  }
+__device__ __forceinline__ void run_gateup(const MoeArgs& a, const BlockLds& b, const Work& w, int tile, uint8_t* lds,
+                                           bool x_there) {
+  if (MAXR == 1 || w.n == 1) return gateup_task<1>(a, b, w, tile, lds, x_there);
+  if (w.n == 2) return gateup_task<2>(a, b, w, tile, lds, x_there);
+  if (MAXR == 4 || w.n <= 4) return gateup_task<4>(a, b, w, tile, lds, x_there);
+  if constexpr (MAXR > 4) return gateup_task<16>(a, b, w, tile, lds, x_there);
 }
 template <int MAXR>
-__device__ __forceinline__ void run_down(const MoeArgs& a, const Work& w, int tile, uint8_t* lds) {
-  if (MAXR == 1 || w.n == 1) return down_task<1>(a, w, tile, lds);
-  if (w.n == 2) return down_task<2>(a, w, tile, lds);
-  if (MAXR == 4 || w.n <= 4) return down_task<4>(a, w, tile, lds);
-  if constexpr (MAXR > 4) {
-    if (w.n <= 8) return down_task<8>(a, w, tile, lds);
-    return down_task<16>(a, w, tile, lds);
-  }
+__device__ __forceinline__ bool run_down(const MoeArgs& a, BlockLds& b, const Work& w, int tile, uint8_t* lds) {
+  if (MAXR == 1 || w.n == 1) return down_task<1>(a, b, w, tile, lds);
+  if (w.n == 2) return down_task<2>(a, b, w, tile, lds);
+  if (MAXR == 4 || w.n <= 4) return down_task<4>(a, b, w, tile, lds);
+  if constexpr (MAXR > 4) return down_task<16>(a, b, w, tile, lds);
+  return true;
 }
 
 template <int MAXR>
-__global__ __launch_bounds__(kThreads) void k_moe_gateup(MoeArgs a) {
+__global__ __launch_bounds__(kThreads, MAXR <= 4 ? 3 : 2) void k_moe_layer(MoeArgs a) {
+  constexpr int EB = MAXR == 1 ? 1 : MAXR == 4 ? 2 : 4;   // experts per router tile
   extern __shared__ __align__(16) uint8_t lds[];
-  const int U = __builtin_amdgcn_readfirstlane(a.ctl[C_UNIQ]);
-  const int tiles = a.I / kUpRows, routed = U * tiles, total = routed + (a.shared ? a.Is / kUpRows : 0);
-  for (int t = blockIdx.x; t < total; t += gridDim.x) {
-    const int u = t < routed ? t / tiles : U, tile = t < routed ? t % tiles : t - routed;
-    run_gateup<MAXR>(a, work_of(a, u, U), tile, lds);
+  __shared__ BlockLds b;
+  const int R = a.router_tiles, S = a.shared ? a.Is / kUpRows : 0, tu = a.I / kUpRows, td = a.H / kDownRows;
+  const int ns = a.shared ? 1 : 0;
+  int U = -1, total = INT32_MAX;
+  bool x_there = false;
+  if (threadIdx.x == 0) b.tick = __hip_atomic_fetch_add(&a.ctl[C_TICKET], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  for (;;) {
     __syncthreads();
-  }
-}
-
-template <int MAXR>
-__global__ __launch_bounds__(kThreads) void k_moe_down(MoeArgs a) {
-  extern __shared__ __align__(16) uint8_t lds[];
-  __shared__ int32_t flag;
-  const int U = __builtin_amdgcn_readfirstlane(a.ctl[C_UNIQ]);
-  const int tiles = a.H / kDownRows, n = U + (a.shared ? 1 : 0);
-  for (int t = blockIdx.x; t < n * tiles; t += gridDim.x) {
-    const int u = t / tiles, tile = t % tiles;
-    run_down<MAXR>(a, work_of(a, u, U), tile, lds);
-    if (arrive_last(a.ctl + C_TILES + tile, n, &flag)) combine_tile(a, tile);
+    const int t = __builtin_amdgcn_readfirstlane(b.tick);
+    if (t >= total) break;
+    // the next ticket is on its way while the task runs
+    int next = 0;
+    if (threadIdx.x == 0) next = __hip_atomic_fetch_add(&a.ctl[C_TICKET], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (t < R) {
+      router_tile<EB, MAXR>(a, t, reinterpret_cast<float*>(lds));
+      if (arrive(&a.ctl[C_ARRIVED], R, &b.flag)) route_all(a, *reinterpret_cast<RouteLds*>(lds));
+    } else if (t < R + S) {
+      run_gateup<MAXR>(a, b, work_of(a, b, kMaxPk, true), t - R, lds, x_there);
+      x_there = a.dense;
+      post(&a.ctl[C_HDONE + kMaxPk]);
+    } else {
+      if (U < 0) {
+        if (threadIdx.x == 0) b.U = wait_for(a, &a.ctl[C_ROUTED], 1) ? get(&a.ctl[C_ROUTED]) - 1 : -1;
+        __syncthreads();
+        U = __builtin_amdgcn_readfirstlane(b.U);
+        if (U < 0 || U > a.M * a.k) break;
+        total = R + S + U * tu + (U + ns) * td;
+        for (int i = threadIdx.x; i < U; i += kThreads) b.uniq[i] = get(&a.uniq[i]);
+        for (int i = threadIdx.x; i < a.M * a.k; i += kThreads) b.pick[i] = (uint16_t)get(&a.uniq_picks[i]);
+        __syncthreads();
+        if (t >= total) break;
+      }
+      const int g = t - R - S;
+      if (g < U * tu) {
+        const int u = g / tu;
+        run_gateup<MAXR>(a, b, work_of(a, b, u, false), g - u * tu, lds, x_there);
+        x_there = a.dense;
+        post(&a.ctl[C_HDONE + u]);
+      } else {
+        // the shared expert's h is there first
+        const int d = g - U * tu, u = d / td, tile = d - u * td;
+        const bool sh = ns && u == 0;
+        if (!run_down<MAXR>(a, b, work_of(a, b, sh ? kMaxPk : u - ns, sh), tile, lds)) break;
+        if (arrive(&a.ctl[C_TILES + tile], U + ns, &b.flag)) combine_tile(a, tile);
+      }
+    }
     __syncthreads();
+    if (threadIdx.x == 0) b.tick = next;
   }
+  // the last block out clears the control words; a call that was given up has no result
+  __syncthreads();
+  if (threadIdx.x == 0)
+    b.flag = __hip_atomic_fetch_add(&a.ctl[C_EXITS], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+             (int)gridDim.x - 1;
+  __syncthreads();
+  if (!b.flag) return;
+  if (get(&a.ctl[C_ERROR]))
+    for (int i = threadIdx.x; i < a.M * a.H; i += kThreads) store_y(a, i / a.H, i % a.H, NAN);
+  __syncthreads();
+  for (int i = threadIdx.x; i < kCtlWords; i += kThreads) put(&a.ctl[i], 0);
 }
 
 __global__ void k_moe_clear(int32_t* ctl, int n) {
@@ -553,12 +687,11 @@ __global__ void k_moe_clear(int32_t* ctl, int n) {
 
 // ---- host ------------------------------------------------------------------------
 
-constexpr int kCtlWords = C_TILES + 1024;
 constexpr size_t kAlign = 256;
 size_t up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
 struct MoeWs {
-  size_t ctl, logits, uniq_expert, uniq_off, uniq_picks, pick_w, h, part, end;
+  size_t ctl, logits, uniq, uniq_picks, pick_w, h, part, end;
 };
 MoeWs moe_ws(const sc_moe_config* c) {
   MoeWs o;
@@ -566,8 +699,7 @@ MoeWs moe_ws(const sc_moe_config* c) {
   size_t p = 0;
   o.ctl = p; p = up(p + kCtlWords * 4);
   o.logits = p; p = up(p + M * c->n_experts * 4);
-  o.uniq_expert = p; p = up(p + P * 4);
-  o.uniq_off = p; p = up(p + (P + 1) * 4);
+  o.uniq = p; p = up(p + P * 8);
   o.uniq_picks = p; p = up(p + P * 4);
   o.pick_w = p; p = up(p + P * 4);
   o.h = p; p = up(p + (P * c->inter + M * c->shared_inter) * 4);
@@ -576,7 +708,6 @@ MoeWs moe_ws(const sc_moe_config* c) {
   return o;
 }
 
-constexpr int kMaxDim = 65536;
 sc_status check_moe(const sc_moe_config* c) {
   if (!c) return fail(SC_E_ARG, "config is NULL");
   if (c->hidden < 64 || c->hidden % 64 || c->hidden > 32768 || c->inter < 64 || c->inter % 64 || c->inter > 32768)
@@ -591,21 +722,24 @@ sc_status check_moe(const sc_moe_config* c) {
   return SC_OK;
 }
 
-hipError_t launch_moe(const MoeArgs& a, hipStream_t st) {
-  const int blocks = 1024;
-  if (a.M == 1) hipLaunchKernelGGL((k_moe_route<1, 1>), dim3(a.E), dim3(kThreads), 0, st, a);
-  else if (a.M <= 4) hipLaunchKernelGGL((k_moe_route<2, 4>), dim3((a.E + 1) / 2), dim3(kThreads), 0, st, a);
-  else hipLaunchKernelGGL((k_moe_route<4, 16>), dim3((a.E + 3) / 4), dim3(kThreads), 0, st, a);
-  if (a.M == 1) {
-    hipLaunchKernelGGL((k_moe_gateup<1>), dim3(blocks), dim3(kThreads), a.lds, st, a);
-    hipLaunchKernelGGL((k_moe_down<1>), dim3(blocks), dim3(kThreads), a.lds, st, a);
-  } else if (a.M <= 4) {
-    hipLaunchKernelGGL((k_moe_gateup<4>), dim3(blocks), dim3(kThreads), a.lds, st, a);
-    hipLaunchKernelGGL((k_moe_down<4>), dim3(blocks), dim3(kThreads), a.lds, st, a);
-  } else {
-    hipLaunchKernelGGL((k_moe_gateup<16>), dim3(blocks), dim3(kThreads), a.lds, st, a);
-    hipLaunchKernelGGL((k_moe_down<16>), dim3(blocks), dim3(kThreads), a.lds, st, a);
-  }
+template <int MAXR>
+hipError_t launch_moe(MoeArgs a, hipStream_t st) {
+  constexpr int EB = MAXR == 1 ? 1 : MAXR == 4 ? 2 : 4;
+  const int steps_h = (a.H + kStepK - 1) / kStepK, inter = a.I > a.Is ? a.I : a.Is;
+  const int steps_i = (inter + kStepK - 1) / kStepK;
+  a.router_tiles = (a.E + EB - 1) / EB;
+  // LDS: the rows of x whole if they fit, and h of one expert's rows; 64 KB let two blocks share a compute unit
+  const int dense = a.M * (steps_h * kStepK * 2 + kPad), hrows = (a.M <= 2 ? a.M : MAXR) * 3 * (steps_i * kStepK * 2 + kPad);
+  const int cap = 65536, least = (int)sizeof(RouteLds);
+  a.dense = dense <= cap;
+  a.lds = (a.dense ? dense : cap) > hrows ? (a.dense ? dense : cap) : hrows;
+  if (a.lds > cap) a.lds = cap;
+  if (a.lds < least) a.lds = (least + 15) / 16 * 16;
+  const long picks = (long)a.M * a.k < a.E ? (long)a.M * a.k : a.E;
+  const long tasks = a.router_tiles + (a.shared ? a.Is / kUpRows : 0) + picks * (a.I / kUpRows) +
+                     (picks + (a.shared ? 1 : 0)) * (a.H / kDownRows);
+  const unsigned blocks = tasks < 1024 ? (unsigned)tasks : 1024u;
+  hipLaunchKernelGGL((k_moe_layer<MAXR>), dim3(blocks), dim3(kThreads), a.lds, st, a);
   return hipGetLastError();
 }
 
@@ -669,9 +803,8 @@ sc_status moe_layer_forward(const sc_moe_config* c, const sc_moe_weights* w, voi
   a.w_out = d_weights;
   a.ctl = reinterpret_cast<int32_t*>(ws + o.ctl);
   a.logits = reinterpret_cast<float*>(ws + o.logits);
-  a.uniq_expert = reinterpret_cast<int32_t*>(ws + o.uniq_expert);
-  a.uniq_off = reinterpret_cast<int32_t*>(ws + o.uniq_off);
-  a.uniq_picks = reinterpret_cast<int32_t*>(ws + o.uniq_picks);
+  a.uniq = reinterpret_cast<uint64_t*>(ws + o.uniq);
+  a.uniq_picks = reinterpret_cast<uint32_t*>(ws + o.uniq_picks);
   a.pick_w = reinterpret_cast<float*>(ws + o.pick_w);
   a.h = reinterpret_cast<float*>(ws + o.h);
   a.part = reinterpret_cast<float*>(ws + o.part);
@@ -688,8 +821,8 @@ sc_status moe_layer_forward(const sc_moe_config* c, const sc_moe_weights* w, voi
   a.out = y_type;
   a.vec = (uintptr_t)d_x % 16 == 0 && ldx % 8 == 0;
   a.scale = c->routed_scale;
-  a.lds = 65536;
-  const hipError_t e = launch_moe(a, static_cast<hipStream_t>(stream));
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  const hipError_t e = M == 1 ? launch_moe<1>(a, st) : M <= 4 ? launch_moe<4>(a, st) : launch_moe<16>(a, st);
   return e == hipSuccess ? SC_OK : hip_fail(e, "moe_layer_forward launch");
 }
 
