@@ -23,26 +23,28 @@ typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
 // scale of the matrix), or with one E8M0 scale per 32.
 enum Format { kNv = 0, kMx = 1 };
 
-// A buffer descriptor over [p, p + bytes): a load whose offset lies beyond it
-// returns zeros and touches no memory, so tails need no branches.
+// A buffer descriptor over [p, p + bytes).  A load whose lane offset is kBeyond
+// returns zeros and touches no memory, so tails need no branches; every other
+// lane offset plus the uniform one stays within the bytes.
 typedef __amdgpu_buffer_rsrc_t Rsrc;
 __device__ __forceinline__ Rsrc make_rsrc(const void* p, uint32_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00027000);
 }
-constexpr uint32_t kBeyond = 0x80000000u;   // an offset that lies beyond every descriptor
+constexpr uint32_t kBeyond = 0x80000000u;   // lies beyond every descriptor
 constexpr int kStream = 2;                  // nontemporal: weights are read once per call
 
-__device__ __forceinline__ u32x4 load16(Rsrc r, uint32_t off) {
-  return __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, kStream);
+// lane: offset of the lane; at: uniform offset
+__device__ __forceinline__ u32x4 load16(Rsrc r, uint32_t lane, uint32_t at) {
+  return __builtin_amdgcn_raw_buffer_load_b128(r, (int)lane, (int)at, kStream);
 }
-__device__ __forceinline__ u32x2 load8(Rsrc r, uint32_t off) {
-  return __builtin_amdgcn_raw_buffer_load_b64(r, (int)off, 0, kStream);
+__device__ __forceinline__ u32x2 load8(Rsrc r, uint32_t lane, uint32_t at) {
+  return __builtin_amdgcn_raw_buffer_load_b64(r, (int)lane, (int)at, kStream);
 }
-__device__ __forceinline__ uint32_t load2(Rsrc r, uint32_t off) {
-  return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)off, 0, kStream);
+__device__ __forceinline__ uint32_t load2(Rsrc r, uint32_t lane, uint32_t at) {
+  return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)lane, (int)at, kStream);
 }
-__device__ __forceinline__ uint32_t load1(Rsrc r, uint32_t off) {
-  return (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(r, (int)off, 0, kStream);
+__device__ __forceinline__ uint32_t load1(Rsrc r, uint32_t lane, uint32_t at) {
+  return (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(r, (int)lane, (int)at, kStream);
 }
 
 // Four codes (bytes B and B+1 of d) as bf16 or fp16.  The conversions are
@@ -151,30 +153,51 @@ struct Stage {
   uint32_t s[Q];
 };
 
-// Byte offsets of a lane in a quad's rows.  codes: row * K/2, scales: row * K/G.
+// What a lane reads of a matrix: its own offsets (row l % 4 of a quad, element
+// 32 (l / 4) of a step) and the distances between a wavefront's quads.
+template <int FMT>
+struct Reader {
+  Rsrc rc, rs;
+  uint32_t code, scale;              // of the lane
+  uint32_t row_code, row_scale;      // bytes per row
+  int klane;
+};
+template <int FMT>
+__device__ __forceinline__ Reader<FMT> reader(const uint8_t* codes, const uint8_t* scales, uint32_t rows, int K) {
+  constexpr int G = FMT == kNv ? 16 : 32;
+  const int lane = threadIdx.x & 63;
+  Reader<FMT> r;
+  r.row_code = (uint32_t)K / 2;
+  r.row_scale = (uint32_t)K / G;
+  r.rc = make_rsrc(codes, rows * r.row_code);
+  r.rs = make_rsrc(scales, rows * r.row_scale);
+  r.klane = (lane >> 2) * 32;
+  r.code = (lane & 3) * r.row_code + r.klane / 2;
+  r.scale = (lane & 3) * r.row_scale + r.klane / G;
+  return r;
+}
+
+// Step at element k of quads row, row + apart, ...: `in` says that the lane's
+// row is there; lanes past kend read nothing (codes and scales are zero there).
 template <int FMT, bool ODD, int Q>
-__device__ __forceinline__ void load_stage(Stage<FMT, ODD, Q>& st, Rsrc rc, Rsrc rs, uint32_t code0, uint32_t scale0,
-                                           uint32_t code_quad, uint32_t scale_quad, int k, int K) {
-  // lanes past the end of the row read nothing: codes and scales are zero there
-  const bool in = k < K;
+__device__ __forceinline__ void load_stage(Stage<FMT, ODD, Q>& st, const Reader<FMT>& r, uint32_t row, uint32_t apart,
+                                           int k, int kend, const bool (&in)[Q]) {
+  constexpr int G = FMT == kNv ? 16 : 32;
 #pragma unroll
   for (int j = 0; j < Q; ++j) {
-    const uint32_t oc = code0 + j * code_quad + (uint32_t)k / 2;
+    const uint32_t ac = (row + j * apart) * r.row_code + k / 2, as = (row + j * apart) * r.row_scale + k / G;
+    const bool on = r.klane + k < kend && in[j];
+    const uint32_t lc = on ? r.code : kBeyond, ls = on ? r.scale : kBeyond;
     if constexpr (ODD) {
       // an odd number of groups per row: rows are 8-byte aligned, scale pairs
       // may lie at odd addresses, and the row may end between the two groups
-      const bool in2 = k + 16 < K;
-      const u32x2 lo = load8(rc, in ? oc : kBeyond), hi = load8(rc, in2 ? oc + 8 : kBeyond);
+      const bool on2 = r.klane + k + 16 < kend && in[j];
+      const u32x2 lo = load8(r.rc, lc, ac), hi = load8(r.rc, on2 ? r.code + 8 : kBeyond, ac);
       st.q[j] = u32x4{lo.x, lo.y, hi.x, hi.y};
-      const uint32_t os = scale0 + j * scale_quad + (uint32_t)k / 16;
-      st.s[j] = load1(rs, in ? os : kBeyond) | load1(rs, in2 ? os + 1 : kBeyond) << 8;
-      continue;
-    }
-    st.q[j] = load16(rc, in ? oc : kBeyond);
-    if constexpr (FMT == kMx) {
-      st.s[j] = load1(rs, in ? scale0 + j * scale_quad + (uint32_t)k / 32 : kBeyond);
+      st.s[j] = load1(r.rs, ls, as) | load1(r.rs, on2 ? r.scale + 1 : kBeyond, as) << 8;
     } else {
-      st.s[j] = load2(rs, in ? scale0 + j * scale_quad + (uint32_t)k / 16 : kBeyond);
+      st.q[j] = load16(r.rc, lc, ac);
+      st.s[j] = FMT == kMx ? load1(r.rs, ls, as) : load2(r.rs, ls, as);
     }
   }
 }
@@ -192,47 +215,55 @@ __device__ __forceinline__ void use_stage(const Stage<FMT, ODD, Q>& st,
                                           const uint8_t* const (&xs)[(ROWS + 3) / 4], int at, float (&acc)[Q][ROWS],
                                           int part_bytes = 0) {
   constexpr int NA = (ROWS + 3) / 4, NP = SPLIT && ROWS > 1 ? 3 : 1;
-  f32x2 sc[Q];
-#pragma unroll
-  for (int j = 0; j < Q; ++j) sc[j] = lane_scales<FMT>(st.s[j]);
+  constexpr int W = Q < 2 ? Q : 2;   // quads whose widened codes are live at a time
+  static_assert(Q % W == 0, "quads are taken in pairs");
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    u32x2 w[Q][4];
-#pragma unroll
-    for (int j = 0; j < Q; ++j) {
-      const uint32_t d0 = h == 0 ? st.q[j].x : st.q[j].z, d1 = h == 0 ? st.q[j].y : st.q[j].w;
-      w[j][0] = widen4<HALF, 0>(d0);
-      w[j][1] = widen4<HALF, 2>(d0);
-      w[j][2] = widen4<HALF, 0>(d1);
-      w[j][3] = widen4<HALF, 2>(d1);
-    }
 #pragma unroll
     for (int a = 0; a < NA; ++a) {
-      f32x4 p[Q];
-#pragma unroll
-      for (int j = 0; j < Q; ++j) p[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      u32x4 x[NP][2];
 #pragma unroll
       for (int t = 0; t < NP; ++t) {
-        const uint8_t* x = xs[a] + at + t * part_bytes + h * 32;
-        const u32x4 x0 = *reinterpret_cast<const u32x4*>(x), x1 = *reinterpret_cast<const u32x4*>(x + 16);
-#pragma unroll
-        for (int j = 0; j < Q; ++j) p[j] = mfma4<HALF>(u32x2{x0.x, x0.y}, w[j][0], p[j]);
-#pragma unroll
-        for (int j = 0; j < Q; ++j) p[j] = mfma4<HALF>(u32x2{x0.z, x0.w}, w[j][1], p[j]);
-#pragma unroll
-        for (int j = 0; j < Q; ++j) p[j] = mfma4<HALF>(u32x2{x1.x, x1.y}, w[j][2], p[j]);
-#pragma unroll
-        for (int j = 0; j < Q; ++j) p[j] = mfma4<HALF>(u32x2{x1.z, x1.w}, w[j][3], p[j]);
+        const uint8_t* px = xs[a] + at + t * part_bytes + h * 32;
+        x[t][0] = *reinterpret_cast<const u32x4*>(px);
+        x[t][1] = *reinterpret_cast<const u32x4*>(px + 16);
       }
 #pragma unroll
-      for (int j = 0; j < Q; ++j) {
-        const float s = h == 0 ? sc[j].x : sc[j].y;
-        if constexpr (SPLIT && ROWS == 1) {
-          acc[j][0] = fmaf(p[j][0] + (p[j][1] + p[j][2]), s, acc[j][0]);
-        } else {
+      for (int j0 = 0; j0 < Q; j0 += W) {
+        u32x2 w[W][4];
+        f32x4 p[W];
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (a * 4 + r < ROWS) acc[j][a * 4 + r] = fmaf(p[j][r], s, acc[j][a * 4 + r]);
+        for (int j = 0; j < W; ++j) {
+          const u32x4& q = st.q[j0 + j];
+          const uint32_t d0 = h == 0 ? q.x : q.z, d1 = h == 0 ? q.y : q.w;
+          w[j][0] = widen4<HALF, 0>(d0);
+          w[j][1] = widen4<HALF, 2>(d0);
+          w[j][2] = widen4<HALF, 0>(d1);
+          w[j][3] = widen4<HALF, 2>(d1);
+          p[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+#pragma unroll
+        for (int t = 0; t < NP; ++t) {
+#pragma unroll
+          for (int j = 0; j < W; ++j) p[j] = mfma4<HALF>(u32x2{x[t][0].x, x[t][0].y}, w[j][0], p[j]);
+#pragma unroll
+          for (int j = 0; j < W; ++j) p[j] = mfma4<HALF>(u32x2{x[t][0].z, x[t][0].w}, w[j][1], p[j]);
+#pragma unroll
+          for (int j = 0; j < W; ++j) p[j] = mfma4<HALF>(u32x2{x[t][1].x, x[t][1].y}, w[j][2], p[j]);
+#pragma unroll
+          for (int j = 0; j < W; ++j) p[j] = mfma4<HALF>(u32x2{x[t][1].z, x[t][1].w}, w[j][3], p[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          const f32x2 sc = lane_scales<FMT>(st.s[j0 + j]);
+          const float s = h == 0 ? sc.x : sc.y;
+          if constexpr (SPLIT && ROWS == 1) {
+            acc[j0 + j][0] = fmaf(p[j][0] + (p[j][1] + p[j][2]), s, acc[j0 + j][0]);
+          } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (a * 4 + r < ROWS) acc[j0 + j][a * 4 + r] = fmaf(p[j][r], s, acc[j0 + j][a * 4 + r]);
+          }
         }
       }
     }

@@ -46,11 +46,11 @@ __global__ __launch_bounds__(256) void k_fp4_rows(LinearArgs a) {
   const int nrows = min(a.N - row_base, block_rows);
   const int row0 = rw * 4 * Q;                            // of the wavefront, within the block
   const int row_lds = a.kc * 2 + kRowPad;
-  const uint32_t cb = (uint32_t)a.K / 2, sb = (uint32_t)a.K / G;
-  const Rsrc rc = make_rsrc(a.codes + (size_t)row_base * cb, (uint32_t)nrows * cb);
-  const Rsrc rs = make_rsrc(a.scales + (size_t)row_base * sb, (uint32_t)nrows * sb);
-  const uint32_t code0 = (uint32_t)(row0 + (lane & 3)) * cb, scale0 = (uint32_t)(row0 + (lane & 3)) * sb;
-  const int klane = (lane >> 2) * 32;
+  const Reader<FMT> rd = reader<FMT>(a.codes + (size_t)row_base * (a.K / 2), a.scales + (size_t)row_base * (a.K / G),
+                                     (uint32_t)nrows, a.K);
+  bool in[Q];
+#pragma unroll
+  for (int j = 0; j < Q; ++j) in[j] = row0 + 4 * j + (lane & 3) < nrows;
 
   float acc[Q][ROWS];
 #pragma unroll
@@ -61,16 +61,16 @@ __global__ __launch_bounds__(256) void k_fp4_rows(LinearArgs a) {
   const int r0 = lane & 3;
   const uint8_t* xs[(ROWS + 3) / 4];
 #pragma unroll
-  for (int s = 0; s < (ROWS + 3) / 4; ++s) xs[s] = lds + (4 * s + r0 < ROWS ? 4 * s + r0 : 0) * row_lds + klane * 2;
+  for (int s = 0; s < (ROWS + 3) / 4; ++s) xs[s] = lds + (4 * s + r0 < ROWS ? 4 * s + r0 : 0) * row_lds + rd.klane * 2;
   for (int kc = 0; kc < a.K; kc += a.kc) {
     const int kend = min(a.K, kc + a.kc);
     const int steps = (kend - kc + kStepK - 1) / kStepK;
     const int n = steps > kw ? (steps - kw + wk - 1) / wk : 0;
     Stage<FMT, ODD, Q> st[D];
-    const int k0 = kc + kw * kStepK + klane;
+    const int k0 = kc + kw * kStepK;
 #pragma unroll
     for (int d = 0; d < D; ++d)
-      load_stage<FMT, ODD, Q>(st[d], rc, rs, code0, scale0, 4 * cb, 4 * sb, k0 + d * wk * kStepK, kend);
+      load_stage<FMT, ODD, Q>(st[d], rd, row0, 4, k0 + d * wk * kStepK, kend, in);
     if (kc) __syncthreads();
     // the operand rows of this range, zero behind the last element
     const int per_row = steps * (kStepK / 8);
@@ -94,7 +94,7 @@ __global__ __launch_bounds__(256) void k_fp4_rows(LinearArgs a) {
       for (int d = 0; d < D; ++d) {
         if (i + d < n) {
           use_stage<FMT, ODD, Q, ROWS, HALF>(st[d], xs, ((i + d) * wk + kw) * kStepK * 2, acc);
-          load_stage<FMT, ODD, Q>(st[d], rc, rs, code0, scale0, 4 * cb, 4 * sb, k0 + (i + d + D) * wk * kStepK, kend);
+          load_stage<FMT, ODD, Q>(st[d], rd, row0, 4, k0 + (i + d + D) * wk * kStepK, kend, in);
         }
       }
     }

@@ -2,15 +2,20 @@
 // product, top-k, gate/up, SiLU, down, weighted combine and the shared expert.
 //
 // Bound: HBM, by the bytes of the experts picked.  Between the products there
-// is nothing to compute, only data to hand over, so the layer is one kernel of
-// tasks that blocks take in order from a counter:
+// is nothing to compute, only data to hand over, so the layer is one kernel
+// whose blocks go through four phases of tasks:
 //   router tiles | shared gate/up tiles | routed gate/up tiles | down tiles
-// A task waits only for tasks before it: a router tile for none, a routed
-// gate/up tile for the picks (made by the block that ends the last router
-// tile), a down tile for all h of its expert.  The first unfinished task is
-// always held by a running block and waits for finished ones only, so every
-// wait ends, whatever part of the grid is resident.  A down tile starts its
-// weight loads before it waits.
+// Blocks take a phase's tasks from counters and go on to the next phase when
+// none is left to take.  A task waits for tasks of earlier phases only: a
+// routed gate/up tile for the picks (made by the block that ends the last
+// router tile), a down tile for all h of its expert.  When a block waits, every
+// task of the earlier phases is held by a block that runs, so every wait ends,
+// whatever part of the grid is resident.  A down tile starts its weight loads
+// before it waits.
+//
+// The counters are in 16 parts: additions to one address take 11 ns each from
+// wherever they come (with a single counter a token's 3500 tickets took longer
+// than its weights).
 //
 // What one block hands to another goes through stores and loads at agent scope
 // (each XCD has an L2 of its own): written through, waited for, then counted.
@@ -29,21 +34,36 @@ constexpr int kWaves = kThreads / 64;
 constexpr int kMaxTokens = SC_MOE_MAX_ROWS;
 constexpr int kMaxPk = kMaxTokens * kMaxTopK;
 constexpr int kPad = 16;           // bytes between operand rows in LDS: four rows' reads fall into different banks
-constexpr int kUpRows = 32;        // rows of h per gate/up task
-constexpr int kDownRows = 64;      // output rows per down task
+constexpr int kUpRows = 16;        // rows of h per gate/up tile: a quad per wavefront
+constexpr int kDownRows = 32;      // output rows per down tile: two quads per wavefront
 
 // Control words, zero between calls: the block that leaves last clears them.
-// C_ROUTED holds the number of unique experts + 1 once the picks are made; the
-// hot ones lie in cache lines of their own.
-enum Ctl { C_TICKET = 0, C_ARRIVED = 32, C_ROUTED = 64, C_EXITS = 96, C_ERROR = 97, C_HDONE = 128 };
-constexpr int kHdone = kMaxPk + 1;                 // gate/up tiles done, per unique expert, then the shared one
-constexpr int kTiles = 32768 / kDownRows;          // down tasks done, per tile
-constexpr int kCtlWords = C_HDONE + kHdone + kTiles;
-constexpr int C_TILES = C_HDONE + kHdone;
+// Counters that many blocks add to, and flags that many blocks poll, lie in
+// cache lines of their own, apart from each other: an addition to a line that
+// eight L2 caches hold for their pollers is slow, and so is all that waits in
+// its channel (a token's layer took 138 us with counters polled in place, 60
+// with flags set once).
+constexpr int kShards = 16, kLine = 32;
+enum Phase { kRouter = 0, kPick, kShared, kRouted, kDown, kPhases };
+constexpr int kExperts = kMaxPk + 1;               // unique experts, then the shared one
+constexpr int kTiles = 32768 / kDownRows;
+constexpr int C_TICKETS = 0,                                    // [phase][shard]: tasks taken
+    C_ARRIVED = kPhases * kShards * kLine,                      // router tiles done
+    C_PICKED = C_ARRIVED + kLine,                               // pick tasks done
+    C_EXITS = C_PICKED + kLine,                                 // blocks that left
+    C_LOGITS = C_EXITS + kLine,                                 // flag: every logit is there
+    C_ROUTED = C_LOGITS + kLine,                                // flag: unique experts + 1
+    C_ERROR = C_ROUTED + kLine,                                 // flag: the call was given up
+    C_HDONE = C_ERROR + kLine,                                  // [expert]: gate/up tiles done
+    C_TILES = C_HDONE + (kExperts + kLine) / kLine * kLine,     // [tile]: experts' down tiles done
+    C_HREADY = C_TILES + kTiles,                                // [expert]: flag: all of h is there
+    kCtlWords = C_HREADY + kExperts * kLine;
 
 // Polls of a wait before the call is given up (about a second): only a
 // workspace that was not prepared, or that two calls share, gets there.
-constexpr int kMaxPolls = 1 << 20;
+constexpr int kMaxPolls = 1 << 21;
+
+constexpr int kRouterShares = 4;
 
 struct MoeArgs {
   const uint16_t* router;    // [E][H] bf16
@@ -57,17 +77,18 @@ struct MoeArgs {
   int32_t* ids_out;          // [M][k] or null
   float* w_out;              // [M][k] or null
   int32_t* ctl;
-  float* logits;             // [M][E]
-  uint64_t* uniq;            // [U] expert, first pick and pick count
+  float* logits;             // [KS][M][E] partial sums over shares of H
+  uint32_t* uniq;            // [U] expert, first pick and pick count (see pack_uniq)
   uint32_t* uniq_picks;      // [P]
   float* pick_w;             // [P]
+  uint32_t* pick_id;         // [P] (five rows and more)
   float* h;                  // [P][I], then [M][Is] of the shared expert
   float* part;               // [P][H], then [M][H]
   int64_t ldx, ldy, blob;
   int M, H, I, E, k, Is, score, out, vec;
   int lds;                   // bytes of LDS for operand rows
   int dense;                 // x lies in LDS whole, token by token
-  int router_tiles;
+  int router_tiles, ks;      // ks: shares of H in the router product
   float scale;
 };
 
@@ -86,6 +107,14 @@ __device__ __forceinline__ void stores_done() { asm volatile("s_waitcnt vmcnt(0)
 
 // ---- routing -------------------------------------------------------------------
 
+__device__ __forceinline__ u32x4 load_x8(const MoeArgs& a, const uint16_t* p) {
+  if (a.vec) return *reinterpret_cast<const u32x4*>(p);
+  u32x4 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = p[2 * i] | (uint32_t)p[2 * i + 1] << 16;
+  return v;
+}
+
 // Logits of EB experts for up to MR rows: each wavefront sums a share of H, the
 // shares are added in wavefront order.
 template <int EB, int MR>
@@ -96,29 +125,23 @@ __device__ __forceinline__ void router_tile(const MoeArgs& a, int tile, float* r
   float acc[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+#pragma unroll 3
   for (int c = (wave * 64 + lane) * 8; c < a.H; c += kThreads * 8) {
-    u32x4 w[EB];
+    u32x4 w[EB], x[MR];
 #pragma unroll
     for (int e = 0; e < EB; ++e)
       w[e] = *reinterpret_cast<const u32x4*>(a.router + (int64_t)min(e0 + e, a.E - 1) * a.H + c);
 #pragma unroll
-    for (int m = 0; m < MR; ++m) {
-      if (m >= a.M) break;
-      const uint16_t* p = a.x + m * a.ldx + c;
-      u32x4 x;
-      if (a.vec) {
-        x = *reinterpret_cast<const u32x4*>(p);
-      } else {
+    for (int m = 0; m < MR; ++m) x[m] = load_x8(a, a.x + min(m, a.M - 1) * a.ldx + c);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = p[2 * i] | (uint32_t)p[2 * i + 1] << 16;
-      }
+    for (int m = 0; m < MR; ++m)
 #pragma unroll
       for (int e = 0; e < EB; ++e)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          acc[m * EB + e] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, (uint32_t)w[e][i]),
-                                                            __builtin_bit_cast(bf16x2, (uint32_t)x[i]), acc[m * EB + e], false);
-    }
+          acc[m * EB + e] =
+              __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, (uint32_t)w[e][i]),
+                                              __builtin_bit_cast(bf16x2, (uint32_t)x[m][i]), acc[m * EB + e], false);
   }
   tile_sum<V>(acc);
 #pragma unroll
@@ -138,6 +161,32 @@ __device__ __forceinline__ void router_tile(const MoeArgs& a, int tile, float* r
   }
 }
 
+// From five rows on: 16 experts and one of `ks` shares of H on the 16x16x32
+// matrix instruction (rows of x times rows of the router; lane l holds row
+// l % 16 of both, elements 8 (l / 16) .. + 7 of 32).  Four shares, so that the
+// products of 256 experts are spread over 64 blocks.
+__device__ __forceinline__ void router_tile_mfma(const MoeArgs& a, int tile, float* red) {
+  typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int share = tile % a.ks, e0 = tile / a.ks * 16, stride = a.ks * kWaves * 32;
+  const uint16_t* pw = a.router + (int64_t)min(e0 + (lane & 15), a.E - 1) * a.H + (lane >> 4) * 8;
+  const uint16_t* px = a.x + min(lane & 15, a.M - 1) * a.ldx + (lane >> 4) * 8;
+  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int k = (share * kWaves + wave) * 32; k < a.H; k += stride) {
+    const u32x4 w = *reinterpret_cast<const u32x4*>(pw + k), x = load_x8(a, px + k);
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, w), acc, 0,
+                                                  0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) red[(wave * 4 + i) * 64 + lane] = acc[i];
+  __syncthreads();
+  const int i = threadIdx.x;
+  const float z = ((red[i] + red[256 + i]) + red[512 + i]) + red[768 + i];
+  const int m = (i >> 4 & 3) * 4 + (i >> 6), e = e0 + (i & 15);   // lane i % 64 of register i / 64
+  if (m < a.M && e < a.E) put(&a.logits[(share * a.M + m) * a.E + e], z);
+}
+
 // Keys that order as the scores do: NaN below -inf, -0 equal to +0.
 __device__ __forceinline__ int order_key(float z) {
   if (z != z) return INT32_MIN + 1;
@@ -145,141 +194,206 @@ __device__ __forceinline__ int order_key(float z) {
   return b >= 0 ? b : b ^ 0x7FFFFFFF;
 }
 
+// Reductions over the wavefront in registers: halves and 16-lane rows trade by
+// lane swaps, the rest through DPP.
+template <typename F>
+__device__ __forceinline__ uint32_t wave_reduce(uint32_t v, F f) {
+  auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  v = f(r[0], r[1]);
+  r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = f(r[0], r[1]);
+  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xF, 0xF, false));
+  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xF, 0xF, false));
+  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));
+  return f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));
+}
 __device__ __forceinline__ int wave_max_i(int v) {
-#pragma unroll
-  for (int o = 32; o; o >>= 1) v = max(v, __shfl_xor(v, o));
-  return v;
+  return (int)wave_reduce((uint32_t)v, [](uint32_t x, uint32_t y) { return (uint32_t)max((int)x, (int)y); });
 }
 __device__ __forceinline__ float wave_sum_f(float v) {
-#pragma unroll
-  for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+  return __uint_as_float(wave_reduce(__float_as_uint(v), [](uint32_t x, uint32_t y) {
+    return __float_as_uint(__uint_as_float(x) + __uint_as_float(y));
+  }));
 }
 
 struct RouteLds {
-  uint32_t rows[kMaxExperts];     // rows that picked the expert, then its place among the unique experts
+  uint32_t rows[kMaxExperts];     // rows that picked the expert
   int32_t off[kMaxExperts];       // first pick of the expert
+  int32_t wave[kWaves];
   int16_t id[kMaxPk];
-  int32_t nu;
+  float val[];                    // [wavefront][E]: scores without the bias
 };
+inline int route_lds(int E) { return (int)sizeof(RouteLds) + kWaves * E * (int)sizeof(float); }
 
-// One wavefront picks a row's experts: lane l looks after experts l * epl ..,
-// so the lowest lane with the largest key holds the lowest id.
-template <int EPL>
+// An expert (10 bits), its first pick in the list (9 bits) and its picks (5 bits).
+__device__ __forceinline__ uint32_t pack_uniq(int e, int first, int n) {
+  return (uint32_t)e << 14 | (uint32_t)first << 5 | (uint32_t)n;
+}
+
+// One wavefront picks a row's experts.  Lane l looks after experts l * epl ..
+// and keeps them sorted (up to eight; more are looked through each time), so
+// that a pick costs one reduction: the lowest lane with the largest key holds
+// the lowest id.
+template <int EPL, int KS>
 __device__ __forceinline__ void route_row(const MoeArgs& a, int m, RouteLds& s) {
+  constexpr bool SORT = EPL <= 8;
   const int lane = threadIdx.x & 63;
   const int epl = (a.E + 63) / 64;
-  int key[EPL];
-  float val[EPL];
+  float* sval = s.val + (threadIdx.x >> 6) * a.E;
+  const Rsrc rl = make_rsrc(a.logits, (uint32_t)(KS * a.M * a.E) * 4), rb = make_rsrc(a.score_bias, (uint32_t)a.E * 4);
+  float part[EPL][KS], bias[EPL];
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     const int e = lane * epl + i;
-    key[i] = INT32_MIN;
-    val[i] = 0.0f;
-    if (i < epl && e < a.E) {
-      float z = get(&a.logits[m * a.E + e]);
-      if (a.score == SC_SCORE_SIGMOID) {
-        z = 1.0f / (1.0f + expf(-z));
-        val[i] = z;
-        if (a.score_bias) z += a.score_bias[e];
-      } else {
-        val[i] = z;
+    const bool in = i < epl && e < a.E;
+#pragma unroll
+    for (int q = 0; q < KS; ++q)
+      part[i][q] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+          rl, in ? ((q * a.M + m) * a.E + e) * 4 : (int)kBeyond, 0, kAgent));
+    bias[i] = 0.0f;
+    if (a.score_bias) bias[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rb, in ? e * 4 : (int)kBeyond, 0, 0));
+  }
+  int key[EPL], id[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    float z = part[i][0];
+#pragma unroll
+    for (int q = 1; q < KS; ++q) z += part[i][q];
+    if (a.score == SC_SCORE_SIGMOID) z = 1.0f / (1.0f + expf(-z));
+    id[i] = lane * epl + i;
+    const bool in = i < epl && id[i] < a.E;
+    if (in) sval[id[i]] = z;
+    key[i] = in ? order_key(z + bias[i]) : INT32_MIN;
+  }
+  if constexpr (SORT) {
+#pragma unroll
+    for (int n = EPL - 1; n > 0; --n)
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const bool up = key[i + 1] > key[i];       // equal keys keep their order
+        const int k0 = key[i], i0 = id[i];
+        key[i] = up ? key[i + 1] : k0;
+        id[i] = up ? id[i + 1] : i0;
+        key[i + 1] = up ? k0 : key[i + 1];
+        id[i + 1] = up ? i0 : id[i + 1];
       }
-      key[i] = order_key(z);
-    }
   }
   int my_id = 0;
-  float my_val = 0.0f;
+#pragma unroll 1
   for (int j = 0; j < a.k; ++j) {
-    int best = key[0], at = 0;
-    float bv = val[0];
+    int best = key[0], at = id[0];
+    if constexpr (!SORT) {
 #pragma unroll
-    for (int i = 1; i < EPL; ++i) {
-      if (key[i] > best) {
-        best = key[i];
-        at = i;
-        bv = val[i];
+      for (int i = 1; i < EPL; ++i)
+        if (key[i] > best) {
+          best = key[i];
+          at = id[i];
+        }
+    }
+    const int src = __builtin_ctzll(__ballot(best == wave_max_i(best)));
+    const int e = __builtin_amdgcn_readlane(at, src);
+    if (lane == j) my_id = e;
+    if constexpr (SORT) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        key[i] = lane == src ? (i + 1 < EPL ? key[i + 1] : INT32_MIN) : key[i];
+        id[i] = lane == src && i + 1 < EPL ? id[i + 1] : id[i];
       }
-    }
-    const int top = wave_max_i(best);
-    const int src = __builtin_ctzll(__ballot(best == top));
-    const int id = __builtin_amdgcn_readlane(lane * epl + at, src);
-    const float v = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(bv), src));
-    if (lane == j) {
-      my_id = id;
-      my_val = v;
-    }
+    } else {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (lane == src && i == at) key[i] = INT32_MIN;
+      for (int i = 0; i < EPL; ++i)
+        if (id[i] == e) key[i] = INT32_MIN;
+    }
   }
   // weights; NaN counts as the lowest score, picks of +inf share the weight,
   // and picks that all have the lowest score share it too
   const bool on = lane < a.k;
-  float z = my_val != my_val ? -INFINITY : my_val, w;
+  const float my_val = on ? sval[my_id] : 0.0f;
+  const float z = my_val != my_val ? -INFINITY : my_val;
+  float w;
   if (a.score == SC_SCORE_SIGMOID) {
     w = on && z > 0.0f ? z : 0.0f;
   } else {
-    float zmax = on ? z : -INFINITY;
-#pragma unroll
-    for (int o = 32; o; o >>= 1) zmax = fmaxf(zmax, __shfl_xor(zmax, o));
+    const float zmax = __uint_as_float(wave_reduce(__float_as_uint(on ? z : -INFINITY), [](uint32_t x, uint32_t y) {
+      return __float_as_uint(fmaxf(__uint_as_float(x), __uint_as_float(y)));
+    }));
     w = !on ? 0.0f : zmax == INFINITY ? (z == INFINITY ? 1.0f : 0.0f) : zmax == -INFINITY ? 1.0f : expf(z - zmax);
   }
   const float sum = wave_sum_f(w);
-  w = sum > 0.0f ? w / sum : 1.0f / (float)a.k;
-  w *= a.scale;
+  w = (sum > 0.0f ? w / sum : 1.0f / (float)a.k) * a.scale;
   if (on) {
     const int p = m * a.k + lane;
-    s.id[p] = (int16_t)my_id;
     put(&a.pick_w[p], w);
     if (a.ids_out) a.ids_out[p] = my_id;
     if (a.w_out) a.w_out[p] = w;
-    atomicOr(&s.rows[my_id], 1u << m);
+    if (a.M == 1) {
+      // one row: its picks are the unique experts
+      put(&a.uniq[p], pack_uniq(my_id, p, 1));
+      put(&a.uniq_picks[p], (uint32_t)p);
+    } else if (KS == 1) {
+      s.id[p] = (int16_t)my_id;
+    } else {
+      put(&a.pick_id[p], (uint32_t)my_id);
+    }
   }
 }
 
-// Picks of all rows, and the picks grouped by expert (experts ascending, an
-// expert's rows ascending).
-__device__ __forceinline__ void route_all(const MoeArgs& a, RouteLds& s) {
+template <int KS>
+__device__ __forceinline__ void route_row(const MoeArgs& a, int m, RouteLds& s) {
+  if (a.E <= 256) route_row<4, KS>(a, m, s);
+  else if (a.E <= 512) route_row<8, KS>(a, m, s);
+  else route_row<16, KS>(a, m, s);
+}
+
+// The picks grouped by expert (experts ascending, an expert's rows ascending);
+// publishes them.  s.id holds all picks.
+__device__ __forceinline__ void group_picks(const MoeArgs& a, RouteLds& s) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int e = threadIdx.x; e < a.E; e += kThreads) s.rows[e] = 0;
-  __syncthreads();
-  for (int m = wave; m < a.M; m += kWaves) {
-    if (a.E <= 256) route_row<4>(a, m, s);
-    else if (a.E <= 512) route_row<8>(a, m, s);
-    else route_row<16>(a, m, s);
-  }
-  __syncthreads();
-  if (wave == 0) {
-    int nu = 0, np = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 64) {
-      const int e = e0 + lane;
-      const int n = e < a.E ? __popc(s.rows[e]) : 0;
-      const uint64_t mask = __ballot(n > 0);
-      int incl = n;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const int t = __shfl_up(incl, o);
-        if (lane >= o) incl += t;
-      }
-      if (n > 0) {
-        const int u = nu + __popcll(mask & ((1ull << lane) - 1));
-        put(&a.uniq[u], (uint64_t)(uint32_t)e << 32 | (uint32_t)(np + incl - n) << 8 | (uint32_t)n);
-        s.off[e] = np + incl - n;
-      }
-      nu += __popcll(mask);
-      np += __shfl(incl, 63);
+  int nu = a.k;
+  if (a.M > 1) {
+    for (int e = threadIdx.x; e < a.E; e += kThreads) s.rows[e] = 0;
+    __syncthreads();
+    for (int p = threadIdx.x; p < a.M * a.k; p += kThreads) atomicOr(&s.rows[s.id[p]], 1u << (p / a.k));
+    __syncthreads();
+    // a thread's experts in a row; unique experts and picks before them in one scan (high and low half)
+    const int per = (a.E + kThreads - 1) / kThreads, e0 = threadIdx.x * per;
+    int mine = 0;
+    for (int e = e0; e < min(e0 + per, a.E); ++e) {
+      const int n = __popc(s.rows[e]);
+      mine += n + (n > 0 ? 1 << 16 : 0);
     }
-    if (lane == 0) s.nu = nu;
-  }
-  __syncthreads();
-  for (int p = threadIdx.x; p < a.M * a.k; p += kThreads) {
-    const int e = s.id[p], m = p / a.k;
-    put(&a.uniq_picks[s.off[e] + __popc(s.rows[e] & ((1u << m) - 1))], (uint32_t)p);
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int t = __shfl_up(incl, o);
+      if (lane >= o) incl += t;
+    }
+    if (lane == 63) s.wave[wave] = incl;
+    __syncthreads();
+    int before = incl - mine, all = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      if (w < wave) before += s.wave[w];
+      all += s.wave[w];
+    }
+    nu = all >> 16;
+    for (int e = e0; e < min(e0 + per, a.E); ++e) {
+      const int n = __popc(s.rows[e]);
+      if (n > 0) {
+        put(&a.uniq[before >> 16], pack_uniq(e, before & 0xFFFF, n));
+        s.off[e] = before & 0xFFFF;
+        before += n + (1 << 16);
+      }
+    }
+    __syncthreads();
+    for (int p = threadIdx.x; p < a.M * a.k; p += kThreads) {
+      const int e = s.id[p], m = p / a.k;
+      put(&a.uniq_picks[s.off[e] + __popc(s.rows[e] & ((1u << m) - 1))], (uint32_t)p);
+    }
   }
   stores_done();
   __syncthreads();
-  if (threadIdx.x == 0) put(&a.ctl[C_ROUTED], s.nu + 1);
+  if (threadIdx.x == 0) put(&a.ctl[C_ROUTED], nu + 1);
 }
 
 // Counts the block in, once all that its threads put has been performed; true
@@ -292,23 +406,23 @@ __device__ __forceinline__ bool arrive(int32_t* counter, int total, int32_t* fla
   __syncthreads();
   return *flag != 0;
 }
-// Same without asking who was last.
-__device__ __forceinline__ void post(int32_t* counter) {
+// Counts `n` gate/up tiles of an expert in; who completes them sets its flag.
+__device__ __forceinline__ void post_h(const MoeArgs& a, int u, int n, int total) {
   stores_done();
   __syncthreads();
-  if (threadIdx.x == 0) __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (threadIdx.x == 0 && __hip_atomic_fetch_add(&a.ctl[C_HDONE + u], n, __ATOMIC_RELAXED,
+                                                 __HIP_MEMORY_SCOPE_AGENT) == total - n)
+    put(&a.ctl[C_HREADY + u * kLine], 1);
 }
-// Waits until *p >= value (one thread); false when the call was given up.
-__device__ __forceinline__ bool wait_for(const MoeArgs& a, const int32_t* p, int value) {
-  for (int i = 0; get(p) < value; ++i) {
-    if (get(&a.ctl[C_ERROR])) return false;
-    if (i >= kMaxPolls) {
-      put(&a.ctl[C_ERROR], 1);
-      return false;
-    }
-    __builtin_amdgcn_s_sleep(1);
+// Waits until a flag is set and returns it (one thread); 0 when the call was given up.
+__device__ __forceinline__ int wait_for(const MoeArgs& a, int flag) {
+  for (int i = 0;; ++i) {
+    const int v = get(&a.ctl[flag]);
+    if (v) return v;
+    if (i >= kMaxPolls) put(&a.ctl[C_ERROR], 1);
+    if ((i & 63) == 63 && get(&a.ctl[C_ERROR])) return 0;
+    __builtin_amdgcn_s_sleep(4);
   }
-  return true;
 }
 
 // ---- expert products ----------------------------------------------------------
@@ -324,7 +438,7 @@ struct Work {
 
 // The picks as a block keeps them.
 struct BlockLds {
-  uint64_t uniq[kMaxPk];
+  uint32_t uniq[kMaxPk];
   uint16_t pick[kMaxPk];
   int32_t tick, flag, U;
 };
@@ -333,11 +447,10 @@ __device__ __forceinline__ Work work_of(const MoeArgs& a, const BlockLds& b, int
   Work w;
   w.u = u;
   if (!shared) {
-    const uint64_t d = b.uniq[u];
-    const int e = __builtin_amdgcn_readfirstlane((int)(d >> 32));
-    const int lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)d);
-    w.first = lo >> 8;
-    w.n = lo & 255;
+    const uint32_t d = __builtin_amdgcn_readfirstlane(b.uniq[u]);
+    const int e = d >> 14;
+    w.first = d >> 5 & 511;
+    w.n = d & 31;
     w.blob = a.blobs + e * a.blob;
     w.gs13 = a.gs[2 * e];
     w.gs2 = a.gs[2 * e + 1];
@@ -377,124 +490,128 @@ __device__ __forceinline__ int lds_range(int lds, int rows, int parts, int K) {
 }
 
 // `n` rows of x from column kc to kend (rounded up to whole steps, zeros behind
-// the end) into LDS; row c is token tok(c).
+// the end) into LDS; row c is token tok(c).  Four loads in flight per thread.
 template <typename F>
 __device__ __forceinline__ void stage_x(const MoeArgs& a, uint8_t* lds, int row_lds, int n, int kc, int kend, F tok) {
-  const int per_row = (kend - kc + kStepK - 1) / kStepK * (kStepK / 8);
-  for (int i = threadIdx.x; i < n * per_row; i += kThreads) {
-    const int c = i / per_row, o = (i - c * per_row) * 8;
-    u32x4 v = {0, 0, 0, 0};
-    if (kc + o < kend) {
-      const uint16_t* p = a.x + tok(c) * a.ldx + kc + o;
-      if (a.vec) {
-        v = *reinterpret_cast<const u32x4*>(p);
-      } else {
+  const int per_row = (kend - kc + kStepK - 1) / kStepK * (kStepK / 8), total = n * per_row;
+  for (int i0 = threadIdx.x; i0 < total; i0 += 4 * kThreads) {
+    u32x4 v[4];
+    int at[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = p[2 * e] | (uint32_t)p[2 * e + 1] << 16;
-      }
+    for (int j = 0; j < 4; ++j) {
+      const int i = min(i0 + j * kThreads, total - 1);
+      const int c = (int)((uint32_t)i / (uint32_t)per_row), o = (i - c * per_row) * 8;
+      at[j] = c * row_lds + o * 2;
+      v[j] = load_x8(a, a.x + tok(c) * a.ldx + min(kc + o, kend - 8));
+      if (kc + o >= kend) v[j] = u32x4{0, 0, 0, 0};
     }
-    *reinterpret_cast<u32x4*>(lds + c * row_lds + o * 2) = v;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i0 + j * kThreads < total) *reinterpret_cast<u32x4*>(lds + at[j]) = v[j];
   }
 }
 
-// h rows [tile * 32, +32) of an expert: a wavefront takes HQ quads of gate rows
-// at a time and the quads of up rows that belong to them.  x_there: all of x
-// lies in LDS (dense) and needs no staging.
+// h rows of tiles [tile, end) of an expert, 16 each: a wavefront takes a quad of
+// gate rows and the quad of up rows that belongs to it.  x_there: all of x lies
+// in LDS (dense) and needs no staging.
 template <int ROWS>
-__device__ __forceinline__ void gateup_task(const MoeArgs& a, const BlockLds& b, const Work& w, int tile, uint8_t* lds,
-                                            bool x_there) {
-  constexpr int HQ = ROWS <= 4 ? 2 : 1, D = 2, NA = (ROWS + 3) / 4;
+__device__ __forceinline__ void gateup_task(const MoeArgs& a, const BlockLds& b, const Work& w, int tile, int end,
+                                            uint8_t* lds, bool x_there) {
+  constexpr int D = ROWS <= 4 ? 4 : 2, NA = (ROWS + 3) / 4;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int H = a.H;
-  const uint32_t cb = H / 2, sb = H / 16, up = (uint32_t)w.inter;
-  const Rsrc rc = make_rsrc(w.blob, 2u * up * cb), rs = make_rsrc(w.blob + (int64_t)2 * up * cb, 2u * up * sb);
-  const int klane = (lane >> 2) * 32, r0 = lane & 3;
+  const Reader<kNv> rd = reader<kNv>(w.blob, w.blob + (int64_t)w.inter * H, 2u * w.inter, H);
+  const int r0 = lane & 3;
   const int KC = a.dense ? (H + kStepK - 1) / kStepK * kStepK : lds_range(a.lds, ROWS, 1, H);
   const int row_lds = KC * 2 + kPad;
   const uint8_t* xs[NA];
 #pragma unroll
   for (int s = 0; s < NA; ++s) {
     const int c = 4 * s + r0 < w.n ? 4 * s + r0 : 0;
-    xs[s] = lds + (a.dense ? token_at(a, b, w, c) : c) * row_lds + klane * 2;
+    xs[s] = lds + (a.dense ? token_at(a, b, w, c) : c) * row_lds + rd.klane * 2;
   }
-  for (int part = 0; part < kUpRows / 4 / kWaves; part += HQ) {
-    const int row0 = tile * kUpRows + (wave * (kUpRows / 4 / kWaves) + part) * 4;
-    const uint32_t r = row0 + r0;
-    float acc[2 * HQ][ROWS];
+  // Steps are loaded D ahead, on into the next range of K or the next tile.
+  // quads: gate rows, then the up rows that belong to them
+  Stage<kNv, false, 2> st[D];
+  auto load = [&](int d, int part, int kc, int s) {
+    const bool in[2] = {part < end, part < end};
+    load_stage<kNv, false, 2>(st[d], rd, part * kUpRows + wave * 4, w.inter, kc + s * kStepK, min(H, kc + KC), in);
+  };
 #pragma unroll
-    for (int j = 0; j < 2 * HQ; ++j)
+  for (int d = 0; d < D; ++d) load(d, tile, 0, d);
+  for (int part = tile; part < end; ++part) {
+    const int row0 = part * kUpRows + wave * 4;
+    float acc[2][ROWS];
 #pragma unroll
-      for (int c = 0; c < ROWS; ++c) acc[j][c] = 0.0f;
+    for (int c = 0; c < ROWS; ++c) acc[0][c] = acc[1][c] = 0.0f;
     for (int kc = 0; kc < H; kc += KC) {
-      const int kend = min(H, kc + KC), steps = (kend - kc + kStepK - 1) / kStepK;
-      Stage<kNv, false, HQ> g[D], u[D];
-      auto load = [&](int d, int s) {
-        const int k = kc + s * kStepK + klane;
-        load_stage<kNv, false, HQ>(g[d], rc, rs, r * cb, r * sb, 4 * cb, 4 * sb, k, kend);
-        load_stage<kNv, false, HQ>(u[d], rc, rs, (r + up) * cb, (r + up) * sb, 4 * cb, 4 * sb, k, kend);
-      };
-#pragma unroll
-      for (int d = 0; d < D; ++d) load(d, d);
+      const int kend = min(H, kc + KC), steps = (kend - kc + kStepK - 1) / kStepK, padded = (steps + D - 1) / D * D;
+      const bool more = kc + KC < H;
+      const int part2 = more ? part : part + 1, kc2 = more ? kc + KC : 0;
       if (!x_there) {
         __syncthreads();
-        if (a.dense) stage_x(a, lds, row_lds, a.M, 0, H, [&](int c) { return c; });
-        else stage_x(a, lds, row_lds, w.n, kc, kend, [&](int c) { return token_at(a, b, w, c); });
+        stage_x(a, lds, row_lds, w.n, kc, kend, [&](int c) { return token_at(a, b, w, c); });
         __syncthreads();
+        x_there = KC >= H;
       }
       for (int s = 0; s < steps; s += D) {
+        const bool on = s + D < padded;
 #pragma unroll
         for (int d = 0; d < D; ++d) {
-          if (s + d < steps) {
-            Stage<kNv, false, 2 * HQ> st;
-#pragma unroll
-            for (int j = 0; j < HQ; ++j) {
-              st.q[j] = g[d].q[j];
-              st.s[j] = g[d].s[j];
-              st.q[HQ + j] = u[d].q[j];
-              st.s[HQ + j] = u[d].s[j];
-            }
-            use_stage<kNv, false, 2 * HQ, ROWS, false>(st, xs, (s + d) * kStepK * 2, acc);
-            load(d, s + d + D);
-          }
+          if (s + d < steps) use_stage<kNv, false, 2, ROWS, false>(st[d], xs, (s + d) * kStepK * 2, acc);
+          load(d, on ? part : part2, on ? kc : kc2, on ? s + d + D : d);
         }
       }
     }
-    x_there = x_there || a.dense;
-    constexpr int V = HQ * ROWS;
-    float vg[V], vu[V];
+    tile_sum<ROWS>(acc[0]);
+    tile_sum<ROWS>(acc[1]);
+    if (tile_sum_owner<ROWS>(lane)) {
+      const int first = tile_sum_first<ROWS>(lane);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      vg[i] = acc[i / ROWS][i % ROWS];
-      vu[i] = acc[HQ + i / ROWS][i % ROWS];
-    }
-    tile_sum<V>(vg);
-    tile_sum<V>(vu);
-    if (tile_sum_owner<V>(lane)) {
-      const int first = tile_sum_first<V>(lane);
-#pragma unroll
-      for (int i = 0; i < kTileOut<V>; ++i) {
-        const int q = (first + i) / ROWS, c = (first + i) % ROWS;
+      for (int i = 0; i < kTileOut<ROWS>; ++i) {
+        const int c = first + i;
         if (c < w.n)
-          put(&a.h[h_at(a, pick_at(a, b, w, c)) + row0 + 4 * q + r0], silu(vg[i] * w.gs13) * (vu[i] * w.gs13));
+          put(&a.h[h_at(a, pick_at(a, b, w, c)) + row0 + r0], silu(acc[0][i] * w.gs13) * (acc[1][i] * w.gs13));
       }
     }
   }
 }
 
-// Output rows [tile * 64, +64) of an expert's down product, per pick.  h is
+// Four fp32 values as three bf16 parts that add up to them.
+__device__ __forceinline__ void split3(f32x4 v, uint8_t* dst, int part_bytes) {
+  uint16_t p[3][4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const __bf16 p0 = (__bf16)v[e];
+    const float f0 = (float)p0, d1 = v[e] - f0;
+    const bool fin = fabsf(f0) < INFINITY;      // what is not finite stands in the first part alone
+    const __bf16 p1 = (__bf16)(fin ? d1 : 0.0f);
+    const __bf16 p2 = (__bf16)(fin ? d1 - (float)p1 : 0.0f);
+    p[0][e] = __builtin_bit_cast(uint16_t, p0);
+    p[1][e] = __builtin_bit_cast(uint16_t, p1);
+    p[2][e] = __builtin_bit_cast(uint16_t, p2);
+  }
+#pragma unroll
+  for (int t = 0; t < 3; ++t)
+    *reinterpret_cast<u32x2*>(dst + t * part_bytes) =
+        u32x2{p[t][0] | (uint32_t)p[t][1] << 16, p[t][2] | (uint32_t)p[t][3] << 16};
+}
+
+// Output rows of tiles [tile, end), 32 each, of an expert's down product, per
+// pick.  h is
 // used to its 24 bits, in three bf16 parts: rounded to one part it would put
 // 2^-9 of itself into y, more than all fp32 sums together.  False when the call
 // was given up.
 template <int ROWS>
-__device__ __forceinline__ bool down_task(const MoeArgs& a, BlockLds& b, const Work& w, int tile, uint8_t* lds) {
-  constexpr int Q = ROWS <= 4 ? 4 : 2, D = 2, NA = (ROWS + 3) / 4;
+__device__ __forceinline__ bool down_task(const MoeArgs& a, BlockLds& b, const Work& w, int tile, int end,
+                                          uint8_t* lds) {
+  constexpr int Q = 2, D = ROWS <= 4 ? 4 : 2, NA = (ROWS + 3) / 4;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int I = w.inter;
-  const uint32_t cb = I / 2, sb = I / 16;
-  const int64_t w13 = (int64_t)2 * I * (a.H / 2) + (int64_t)2 * I * (a.H / 16), codes = (int64_t)a.H * cb;
-  const Rsrc rc = make_rsrc(w.blob + w13, (uint32_t)codes), rs = make_rsrc(w.blob + w13 + codes, (uint32_t)a.H * sb);
+  const int64_t w13 = (int64_t)I * a.H + (int64_t)I * a.H / 8, codes = (int64_t)a.H * (I / 2);
+  const Reader<kNv> rd = reader<kNv>(w.blob + w13, w.blob + w13 + codes, a.H, I);
   const Rsrc rh = make_rsrc(a.h, (uint32_t)(a.M * (a.k * a.I + a.Is)) * 4);
-  const int klane = (lane >> 2) * 32, r0 = lane & 3;
+  const int r0 = lane & 3;
   const int KC = lds_range(a.lds, ROWS, 3, I);
   const int part_lds = KC * 2 + kPad, row_lds = 3 * part_lds;
   const uint8_t* xs[NA];
@@ -502,63 +619,57 @@ __device__ __forceinline__ bool down_task(const MoeArgs& a, BlockLds& b, const W
   for (int s = 0; s < NA; ++s) {
     // one row: its parts are the rows of the set
     const int c = 4 * s + r0 < w.n ? 4 * s + r0 : 0;
-    xs[s] = lds + (ROWS == 1 ? (r0 < 3 ? r0 : 0) * part_lds : c * row_lds) + klane * 2;
+    xs[s] = lds + (ROWS == 1 ? (r0 < 3 ? r0 : 0) * part_lds : c * row_lds) + rd.klane * 2;
   }
-  bool waited = false;
-  for (int part = 0; part < kDownRows / 4 / kWaves; part += Q) {
-    const int row0 = tile * kDownRows + (wave * (kDownRows / 4 / kWaves) + part) * 4;
-    const uint32_t r = row0 + r0;
+  Stage<kNv, false, Q> st[D];
+  auto load = [&](int d, int part, int kc, int s) {
+    const bool in[Q] = {part < end, part < end};
+    load_stage<kNv, false, Q>(st[d], rd, part * kDownRows + wave * 4 * Q, 4, kc + s * kStepK, min(I, kc + KC), in);
+  };
+#pragma unroll
+  for (int d = 0; d < D; ++d) load(d, tile, 0, d);
+  if (threadIdx.x == 0) b.flag = wait_for(a, C_HREADY + w.u * kLine);
+  bool h_there = false;
+  for (int part = tile; part < end; ++part) {
+    const int row0 = part * kDownRows + wave * 4 * Q;
     float acc[Q][ROWS];
 #pragma unroll
     for (int j = 0; j < Q; ++j)
 #pragma unroll
       for (int c = 0; c < ROWS; ++c) acc[j][c] = 0.0f;
     for (int kc = 0; kc < I; kc += KC) {
-      const int kend = min(I, kc + KC), steps = (kend - kc + kStepK - 1) / kStepK;
-      Stage<kNv, false, Q> st[D];
-#pragma unroll
-      for (int d = 0; d < D; ++d)
-        load_stage<kNv, false, Q>(st[d], rc, rs, r * cb, r * sb, 4 * cb, 4 * sb, kc + d * kStepK + klane, kend);
-      if (!waited) {
-        if (threadIdx.x == 0) b.flag = wait_for(a, &a.ctl[C_HDONE + w.u], I / kUpRows);
-        waited = true;
-      }
-      if (part == 0 || KC < I) {
+      const int kend = min(I, kc + KC), steps = (kend - kc + kStepK - 1) / kStepK, padded = (steps + D - 1) / D * D;
+      const bool more = kc + KC < I;
+      const int part2 = more ? part : part + 1, kc2 = more ? kc + KC : 0;
+      if (!h_there) {
         __syncthreads();
         if (!b.flag) return false;
-        const int per_row = steps * (kStepK / 4);
-        for (int i = threadIdx.x; i < w.n * per_row; i += kThreads) {
-          const int c = i / per_row, o = (i - c * per_row) * 4;
-          const u32x4 t = __builtin_amdgcn_raw_buffer_load_b128(
-              rh, kc + o < kend ? (int)((h_at(a, pick_at(a, b, w, c)) + kc + o) * 4) : (int)kBeyond, 0, kAgent);
-          const f32x4 v = __builtin_bit_cast(f32x4, t);
-          uint16_t p[3][4];
+        const int per_row = steps * (kStepK / 4), total = w.n * per_row;
+        for (int i0 = threadIdx.x; i0 < total; i0 += 2 * kThreads) {
+          u32x4 t[2];
+          int at[2];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const __bf16 p0 = (__bf16)v[e];
-            const float f0 = (float)p0, d1 = v[e] - f0;
-            const bool fin = fabsf(f0) < INFINITY;      // what is not finite stands in the first part alone
-            const __bf16 p1 = (__bf16)(fin ? d1 : 0.0f);
-            const __bf16 p2 = (__bf16)(fin ? d1 - (float)p1 : 0.0f);
-            p[0][e] = __builtin_bit_cast(uint16_t, p0);
-            p[1][e] = __builtin_bit_cast(uint16_t, p1);
-            p[2][e] = __builtin_bit_cast(uint16_t, p2);
+          for (int j = 0; j < 2; ++j) {
+            const int i = min(i0 + j * kThreads, total - 1);
+            const int c = (int)((uint32_t)i / (uint32_t)per_row), o = (i - c * per_row) * 4;
+            at[j] = c * row_lds + o * 2;
+            t[j] = __builtin_amdgcn_raw_buffer_load_b128(
+                rh, kc + o < kend ? (int)((h_at(a, pick_at(a, b, w, c)) + kc + o) * 4) : (int)kBeyond, 0, kAgent);
           }
 #pragma unroll
-          for (int t3 = 0; t3 < 3; ++t3)
-            *reinterpret_cast<u32x2*>(lds + c * row_lds + t3 * part_lds + o * 2) =
-                u32x2{p[t3][0] | (uint32_t)p[t3][1] << 16, p[t3][2] | (uint32_t)p[t3][3] << 16};
+          for (int j = 0; j < 2; ++j)
+            if (i0 + j * kThreads < total) split3(__builtin_bit_cast(f32x4, t[j]), lds + at[j], part_lds);
         }
         __syncthreads();
+        h_there = KC >= I;
       }
       for (int s = 0; s < steps; s += D) {
+        const bool on = s + D < padded;
 #pragma unroll
         for (int d = 0; d < D; ++d) {
-          if (s + d < steps) {
+          if (s + d < steps)
             use_stage<kNv, false, Q, ROWS, false, true>(st[d], xs, (s + d) * kStepK * 2, acc, part_lds);
-            load_stage<kNv, false, Q>(st[d], rc, rs, r * cb, r * sb, 4 * cb, 4 * sb, kc + (s + d + D) * kStepK + klane,
-                                      kend);
-          }
+          load(d, on ? part : part2, on ? kc : kc2, on ? s + d + D : d);
         }
       }
     }
@@ -585,89 +696,201 @@ __device__ __forceinline__ void store_y(const MoeArgs& a, int m, int r, float v)
   else static_cast<uint16_t*>(a.y)[o] = __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
-// y of 64 rows: the picks in rank order, then the shared expert.
+// y of a tile: the picks in rank order, then the shared expert; eight loads in flight.
 __device__ __forceinline__ void combine_tile(const MoeArgs& a, int tile) {
   const int P = a.M * a.k;
+  const Rsrc rp = make_rsrc(a.part, (uint32_t)(P + (a.shared ? a.M : 0)) * a.H * 4), rw = make_rsrc(a.pick_w, P * 4);
   for (int i = threadIdx.x; i < a.M * kDownRows; i += kThreads) {
-    const int m = i / kDownRows, r = tile * kDownRows + i % kDownRows;
+    const int m = i / kDownRows, r = tile * kDownRows + i % kDownRows, p0 = m * a.k;
+    const float sh = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+        rp, a.shared ? ((P + m) * a.H + r) * 4 : (int)kBeyond, 0, kAgent));
     float s = 0.0f;
-    for (int j = 0; j < a.k; ++j)
-      s = fmaf(get(&a.pick_w[m * a.k + j]), get(&a.part[(int64_t)(m * a.k + j) * a.H + r]), s);
-    if (a.shared) s += get(&a.part[(int64_t)(P + m) * a.H + r]);
+    for (int j0 = 0; j0 < a.k; j0 += 8) {
+      float v[8], w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const bool in = j0 + j < a.k;
+        v[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+            rp, in ? ((p0 + j0 + j) * a.H + r) * 4 : (int)kBeyond, 0, kAgent));
+        w[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rw, in ? (p0 + j0 + j) * 4 : (int)kBeyond, 0, kAgent));
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j0 + j < a.k) s = fmaf(w[j], v[j], s);
+    }
+    if (a.shared) s += sh;
     store_y(a, m, r, s);
   }
 }
 
 template <int MAXR>
-__device__ __forceinline__ void run_gateup(const MoeArgs& a, const BlockLds& b, const Work& w, int tile, uint8_t* lds,
-                                           bool x_there) {
-  if (MAXR == 1 || w.n == 1) return gateup_task<1>(a, b, w, tile, lds, x_there);
-  if (w.n == 2) return gateup_task<2>(a, b, w, tile, lds, x_there);
-  if (MAXR == 4 || w.n <= 4) return gateup_task<4>(a, b, w, tile, lds, x_there);
-  if constexpr (MAXR > 4) return gateup_task<16>(a, b, w, tile, lds, x_there);
+__device__ __forceinline__ void run_gateup(const MoeArgs& a, const BlockLds& b, const Work& w, int tile, int end,
+                                           uint8_t* lds, bool x_there) {
+  if (MAXR == 1 || w.n == 1) return gateup_task<1>(a, b, w, tile, end, lds, x_there);
+  if (w.n == 2) return gateup_task<2>(a, b, w, tile, end, lds, x_there);
+  if (MAXR == 4 || w.n <= 4) return gateup_task<4>(a, b, w, tile, end, lds, x_there);
+  if constexpr (MAXR > 4) return gateup_task<16>(a, b, w, tile, end, lds, x_there);
 }
 template <int MAXR>
-__device__ __forceinline__ bool run_down(const MoeArgs& a, BlockLds& b, const Work& w, int tile, uint8_t* lds) {
-  if (MAXR == 1 || w.n == 1) return down_task<1>(a, b, w, tile, lds);
-  if (w.n == 2) return down_task<2>(a, b, w, tile, lds);
-  if (MAXR == 4 || w.n <= 4) return down_task<4>(a, b, w, tile, lds);
-  if constexpr (MAXR > 4) return down_task<16>(a, b, w, tile, lds);
+__device__ __forceinline__ bool run_down(const MoeArgs& a, BlockLds& b, const Work& w, int tile, int end,
+                                         uint8_t* lds) {
+  if (MAXR == 1 || w.n == 1) return down_task<1>(a, b, w, tile, end, lds);
+  if (w.n == 2) return down_task<2>(a, b, w, tile, end, lds);
+  if (MAXR == 4 || w.n <= 4) return down_task<4>(a, b, w, tile, end, lds);
+  if constexpr (MAXR > 4) return down_task<16>(a, b, w, tile, end, lds);
   return true;
 }
 
-template <int MAXR>
-__global__ __launch_bounds__(kThreads, MAXR <= 4 ? 3 : 2) void k_moe_layer(MoeArgs a) {
-  constexpr int EB = MAXR == 1 ? 1 : MAXR == 4 ? 2 : 4;   // experts per router tile
-  extern __shared__ __align__(16) uint8_t lds[];
-  __shared__ BlockLds b;
-  const int R = a.router_tiles, S = a.shared ? a.Is / kUpRows : 0, tu = a.I / kUpRows, td = a.H / kDownRows;
-  const int ns = a.shared ? 1 : 0;
-  int U = -1, total = INT32_MAX;
-  bool x_there = false;
-  if (threadIdx.x == 0) b.tick = __hip_atomic_fetch_add(&a.ctl[C_TICKET], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  for (;;) {
+// A phase's tasks as one block takes them: task t is number t / 16 of part t % 16.
+// `ahead` (thread 0) is the next number of the block's own part, asked for while
+// the task before runs; when that part is used up, the others are looked through.
+struct Taker {
+  int32_t* c;
+  int n, home, ahead;
+  __device__ __forceinline__ int limit(int shard) const { return (n - shard + kShards - 1) / kShards; }
+  __device__ __forceinline__ void ask() {
+    if (threadIdx.x == 0) ahead = __hip_atomic_fetch_add(c + home * kLine, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  // the next task, or -1 when every task is taken; the block agrees on it through *tick
+  __device__ __forceinline__ int next(int32_t* tick) {
     __syncthreads();
-    const int t = __builtin_amdgcn_readfirstlane(b.tick);
-    if (t >= total) break;
-    // the next ticket is on its way while the task runs
-    int next = 0;
-    if (threadIdx.x == 0) next = __hip_atomic_fetch_add(&a.ctl[C_TICKET], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (t < R) {
-      router_tile<EB, MAXR>(a, t, reinterpret_cast<float*>(lds));
-      if (arrive(&a.ctl[C_ARRIVED], R, &b.flag)) route_all(a, *reinterpret_cast<RouteLds*>(lds));
-    } else if (t < R + S) {
-      run_gateup<MAXR>(a, b, work_of(a, b, kMaxPk, true), t - R, lds, x_there);
-      x_there = a.dense;
-      post(&a.ctl[C_HDONE + kMaxPk]);
-    } else {
-      if (U < 0) {
-        if (threadIdx.x == 0) b.U = wait_for(a, &a.ctl[C_ROUTED], 1) ? get(&a.ctl[C_ROUTED]) - 1 : -1;
-        __syncthreads();
-        U = __builtin_amdgcn_readfirstlane(b.U);
-        if (U < 0 || U > a.M * a.k) break;
-        total = R + S + U * tu + (U + ns) * td;
-        for (int i = threadIdx.x; i < U; i += kThreads) b.uniq[i] = get(&a.uniq[i]);
-        for (int i = threadIdx.x; i < a.M * a.k; i += kThreads) b.pick[i] = (uint16_t)get(&a.uniq_picks[i]);
-        __syncthreads();
-        if (t >= total) break;
+    if (threadIdx.x < 64) {
+      int t = __builtin_amdgcn_readfirstlane(ahead);
+      t = t < limit(home) ? t * kShards + home : -1;
+      const int lane = threadIdx.x;
+      while (t < 0) {
+        const bool left = lane < kShards && get(c + lane * kLine) < limit(lane);
+        const uint32_t m = (uint32_t)__ballot(left);
+        if (!m) break;
+        const uint32_t rot = (m >> home | m << (kShards - home)) & ((1u << kShards) - 1);
+        const int s = (home + __builtin_ctz(rot)) % kShards;
+        int k = 0;
+        if (lane == 0) k = __hip_atomic_fetch_add(c + s * kLine, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        k = __builtin_amdgcn_readfirstlane(k);
+        if (k < limit(s)) {
+          t = k * kShards + s;
+          home = s;
+        }
       }
-      const int g = t - R - S;
-      if (g < U * tu) {
-        const int u = g / tu;
-        run_gateup<MAXR>(a, b, work_of(a, b, u, false), g - u * tu, lds, x_there);
-        x_there = a.dense;
-        post(&a.ctl[C_HDONE + u]);
-      } else {
-        // the shared expert's h is there first
-        const int d = g - U * tu, u = d / td, tile = d - u * td;
-        const bool sh = ns && u == 0;
-        if (!run_down<MAXR>(a, b, work_of(a, b, sh ? kMaxPk : u - ns, sh), tile, lds)) break;
-        if (arrive(&a.ctl[C_TILES + tile], U + ns, &b.flag)) combine_tile(a, tile);
-      }
+      if (lane == 0) *tick = t;
     }
     __syncthreads();
-    if (threadIdx.x == 0) b.tick = next;
+    return __builtin_amdgcn_readfirstlane(*tick);
   }
+};
+__device__ __forceinline__ Taker taker(const MoeArgs& a, int phase, int n) {
+  Taker t{a.ctl + C_TICKETS + phase * kShards * kLine, n, (int)(blockIdx.x % kShards), 0};
+  t.ask();
+  return t;
+}
+// Tiles per task: few enough tasks that staging an expert's rows pays, enough that the blocks end together.
+__device__ __forceinline__ int tiles_per_task(int tiles) {
+  const int f = tiles / (6 * (int)gridDim.x);
+  return f < 1 ? 1 : f > 8 ? 8 : f;
+}
+
+template <int MAXR>
+__device__ __forceinline__ void run_phases(const MoeArgs& a, BlockLds& b, uint8_t* lds) {
+  constexpr int EB = MAXR == 1 ? 1 : 2;   // experts per router tile of up to four rows
+  const int tu = a.I / kUpRows, td = a.H / kDownRows, ns = a.shared ? 1 : 0;
+  const bool x_there = a.dense;
+  {
+    Taker k = taker(a, kRouter, a.router_tiles);
+    for (int t; (t = k.next(&b.tick)) >= 0;) {
+      k.ask();
+      RouteLds& s = *reinterpret_cast<RouteLds*>(lds);
+      if constexpr (MAXR > 4) router_tile_mfma(a, t, reinterpret_cast<float*>(lds));
+      else router_tile<EB, MAXR>(a, t, reinterpret_cast<float*>(lds));
+      if (arrive(&a.ctl[C_ARRIVED], a.router_tiles, &b.flag)) {
+        if constexpr (MAXR > 4) {
+          if (threadIdx.x == 0) put(&a.ctl[C_LOGITS], 1);
+        } else {
+          // up to four rows are picked here, a wavefront each
+          if ((int)(threadIdx.x >> 6) < a.M) route_row<1>(a, threadIdx.x >> 6, s);
+          __syncthreads();
+          group_picks(a, s);
+        }
+      }
+    }
+  }
+  if constexpr (MAXR > 4) {
+    // rows are picked by fours; the block that ends the last four groups all picks
+    RouteLds& s = *reinterpret_cast<RouteLds*>(lds);
+    const int n = (a.M + kWaves - 1) / kWaves;
+    Taker k = taker(a, kPick, n);
+    for (int t; (t = k.next(&b.tick)) >= 0;) {
+      k.ask();
+      if (threadIdx.x == 0) b.flag = wait_for(a, C_LOGITS);
+      __syncthreads();
+      if (!b.flag) return;
+      const int m = t * kWaves + (threadIdx.x >> 6);
+      if (m < a.M) route_row<kRouterShares>(a, m, s);
+      if (arrive(&a.ctl[C_PICKED], n, &b.flag)) {
+        for (int p = threadIdx.x; p < a.M * a.k; p += kThreads) s.id[p] = (int16_t)get(&a.pick_id[p]);
+        __syncthreads();
+        group_picks(a, s);
+      }
+    }
+  }
+  if (a.dense) {
+    stage_x(a, lds, (a.H + kStepK - 1) / kStepK * kStepK * 2 + kPad, a.M, 0, a.H, [](int c) { return c; });
+    __syncthreads();
+  }
+  if (ns) {
+    Taker k = taker(a, kShared, a.Is / kUpRows);
+    for (int t; (t = k.next(&b.tick)) >= 0;) {
+      k.ask();
+      run_gateup<MAXR>(a, b, work_of(a, b, kMaxPk, true), t, t + 1, lds, x_there);
+      post_h(a, kMaxPk, 1, a.Is / kUpRows);
+    }
+  }
+  Taker kr = taker(a, kRouted, 0);
+  if (threadIdx.x == 0) b.U = wait_for(a, C_ROUTED) - 1;
+  __syncthreads();
+  const int U = __builtin_amdgcn_readfirstlane(b.U);
+  if (U < 0 || U > a.M * a.k) return;
+  for (int i = threadIdx.x; i < U; i += kThreads) b.uniq[i] = get(&a.uniq[i]);
+  for (int i = threadIdx.x; i < a.M * a.k; i += kThreads) b.pick[i] = (uint16_t)get(&a.uniq_picks[i]);
+  {
+    const int f = tiles_per_task(U * tu), per = (tu + f - 1) / f;
+    kr.n = U * per;
+    for (int t; (t = kr.next(&b.tick)) >= 0;) {
+      kr.ask();
+      const int u = t / per, i0 = (t - u * per) * f, i1 = min(i0 + f, tu);
+      run_gateup<MAXR>(a, b, work_of(a, b, u, false), i0, i1, lds, x_there);
+      post_h(a, u, i1 - i0, tu);
+    }
+  }
+  {
+    // the shared expert's h is there first
+    const int f = tiles_per_task((U + ns) * td), per = (td + f - 1) / f;
+    Taker k = taker(a, kDown, (U + ns) * per);
+    for (int t; (t = k.next(&b.tick)) >= 0;) {
+      k.ask();
+      const int u = t / per, i0 = (t - u * per) * f, i1 = min(i0 + f, td);
+      const bool sh = ns && u == 0;
+      if (!run_down<MAXR>(a, b, work_of(a, b, sh ? kMaxPk : u - ns, sh), i0, i1, lds)) return;
+      stores_done();
+      __syncthreads();
+      // one lane per tile counts it; the block combines the tiles that it completed
+      if (threadIdx.x < 64) {
+        const int i = i0 + threadIdx.x;
+        const bool last = i < i1 && __hip_atomic_fetch_add(&a.ctl[C_TILES + i], 1, __ATOMIC_RELAXED,
+                                                           __HIP_MEMORY_SCOPE_AGENT) == U + ns - 1;
+        const uint64_t m = __ballot(last);
+        if (threadIdx.x == 0) b.flag = (int)m;
+      }
+      __syncthreads();
+      for (uint32_t m = (uint32_t)b.flag; m; m &= m - 1) combine_tile(a, i0 + __builtin_ctz(m));
+    }
+  }
+}
+
+template <int MAXR>
+__global__ __launch_bounds__(kThreads, MAXR == 1 ? 4 : 3) void k_moe_layer(MoeArgs a) {
+  extern __shared__ __align__(16) uint8_t lds[];
+  __shared__ BlockLds b;
+  run_phases<MAXR>(a, b, lds);
   // the last block out clears the control words; a call that was given up has no result
   __syncthreads();
   if (threadIdx.x == 0)
@@ -691,17 +914,18 @@ constexpr size_t kAlign = 256;
 size_t up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
 struct MoeWs {
-  size_t ctl, logits, uniq, uniq_picks, pick_w, h, part, end;
+  size_t ctl, logits, uniq, uniq_picks, pick_w, pick_id, h, part, end;
 };
 MoeWs moe_ws(const sc_moe_config* c) {
   MoeWs o;
   const size_t M = c->max_rows, P = M * c->top_k;
   size_t p = 0;
   o.ctl = p; p = up(p + kCtlWords * 4);
-  o.logits = p; p = up(p + M * c->n_experts * 4);
-  o.uniq = p; p = up(p + P * 8);
+  o.logits = p; p = up(p + (M > 4 ? kRouterShares : 1) * M * c->n_experts * 4);
+  o.uniq = p; p = up(p + P * 4);
   o.uniq_picks = p; p = up(p + P * 4);
   o.pick_w = p; p = up(p + P * 4);
+  o.pick_id = p; p = up(p + P * 4);
   o.h = p; p = up(p + (P * c->inter + M * c->shared_inter) * 4);
   o.part = p; p = up(p + (P + M) * c->hidden * 4);
   o.end = p;
@@ -724,13 +948,15 @@ sc_status check_moe(const sc_moe_config* c) {
 
 template <int MAXR>
 hipError_t launch_moe(MoeArgs a, hipStream_t st) {
-  constexpr int EB = MAXR == 1 ? 1 : MAXR == 4 ? 2 : 4;
   const int steps_h = (a.H + kStepK - 1) / kStepK, inter = a.I > a.Is ? a.I : a.Is;
   const int steps_i = (inter + kStepK - 1) / kStepK;
-  a.router_tiles = (a.E + EB - 1) / EB;
-  // LDS: the rows of x whole if they fit, and h of one expert's rows; 64 KB let two blocks share a compute unit
+  a.ks = MAXR == 16 ? kRouterShares : 1;
+  a.router_tiles = MAXR == 16 ? (a.E + 15) / 16 * a.ks : MAXR == 1 ? a.E : (a.E + 1) / 2;
+  // LDS: the rows of x whole if they fit, and h of one expert's rows; three blocks share a compute unit's 160 KB
   const int dense = a.M * (steps_h * kStepK * 2 + kPad), hrows = (a.M <= 2 ? a.M : MAXR) * 3 * (steps_i * kStepK * 2 + kPad);
-  const int cap = 65536, least = (int)sizeof(RouteLds);
+  constexpr int cap = 49920;
+  static_assert((cap / (MAXR * 3) - kPad) / 2 >= kStepK, "one step of the largest row count must fit");
+  const int least = route_lds(a.E);
   a.dense = dense <= cap;
   a.lds = (a.dense ? dense : cap) > hrows ? (a.dense ? dense : cap) : hrows;
   if (a.lds > cap) a.lds = cap;
@@ -803,9 +1029,10 @@ sc_status moe_layer_forward(const sc_moe_config* c, const sc_moe_weights* w, voi
   a.w_out = d_weights;
   a.ctl = reinterpret_cast<int32_t*>(ws + o.ctl);
   a.logits = reinterpret_cast<float*>(ws + o.logits);
-  a.uniq = reinterpret_cast<uint64_t*>(ws + o.uniq);
+  a.uniq = reinterpret_cast<uint32_t*>(ws + o.uniq);
   a.uniq_picks = reinterpret_cast<uint32_t*>(ws + o.uniq_picks);
   a.pick_w = reinterpret_cast<float*>(ws + o.pick_w);
+  a.pick_id = reinterpret_cast<uint32_t*>(ws + o.pick_id);
   a.h = reinterpret_cast<float*>(ws + o.h);
   a.part = reinterpret_cast<float*>(ws + o.part);
   a.ldx = ldx;
