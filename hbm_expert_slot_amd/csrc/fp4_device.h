@@ -23,6 +23,15 @@ typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
 // scale of the matrix), or with one E8M0 scale per 32.
 enum Format { kNv = 0, kMx = 1 };
 
+// The lane, hidden from the optimiser: what depends on it is computed where it
+// is used.  In a kernel of many phases it would else be moved out of the task
+// loops and spilled, and each reload waits for every load in flight.
+__device__ __forceinline__ int fresh_lane() {
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));
+  return lane;
+}
+
 // A buffer descriptor over [p, p + bytes).  A load whose lane offset is kBeyond
 // returns zeros and touches no memory, so tails need no branches; every other
 // lane offset plus the uniform one stays within the bytes.
@@ -165,7 +174,7 @@ struct Reader {
 template <int FMT>
 __device__ __forceinline__ Reader<FMT> reader(const uint8_t* codes, const uint8_t* scales, uint32_t rows, int K) {
   constexpr int G = FMT == kNv ? 16 : 32;
-  const int lane = threadIdx.x & 63;
+  const int lane = fresh_lane();
   Reader<FMT> r;
   r.row_code = (uint32_t)K / 2;
   r.row_scale = (uint32_t)K / G;

@@ -115,50 +115,33 @@ __device__ __forceinline__ u32x4 load_x8(const MoeArgs& a, const uint16_t* p) {
   return v;
 }
 
-// Logits of EB experts for up to MR rows: each wavefront sums a share of H, the
-// shares are added in wavefront order.
-template <int EB, int MR>
-__device__ __forceinline__ void router_tile(const MoeArgs& a, int tile, float* red) {
-  constexpr int V = EB * MR;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int e0 = tile * EB;
-  float acc[V];
+// Logits of four experts, one per wavefront, for up to MR rows.
+template <int MR>
+__device__ __forceinline__ void router_tile(const MoeArgs& a, int tile) {
+  const int lane = fresh_lane(), e = tile * kWaves + (threadIdx.x >> 6);
+  const uint16_t* pw = a.router + (int64_t)min(e, a.E - 1) * a.H;
+  float acc[MR];
 #pragma unroll
-  for (int i = 0; i < V; ++i) acc[i] = 0.0f;
-#pragma unroll 3
-  for (int c = (wave * 64 + lane) * 8; c < a.H; c += kThreads * 8) {
-    u32x4 w[EB], x[MR];
-#pragma unroll
-    for (int e = 0; e < EB; ++e)
-      w[e] = *reinterpret_cast<const u32x4*>(a.router + (int64_t)min(e0 + e, a.E - 1) * a.H + c);
+  for (int m = 0; m < MR; ++m) acc[m] = 0.0f;
+#pragma unroll 4
+  for (int c = lane * 8; c < a.H; c += 64 * 8) {
+    const u32x4 w = *reinterpret_cast<const u32x4*>(pw + c);
+    u32x4 x[MR];
 #pragma unroll
     for (int m = 0; m < MR; ++m) x[m] = load_x8(a, a.x + min(m, a.M - 1) * a.ldx + c);
 #pragma unroll
     for (int m = 0; m < MR; ++m)
 #pragma unroll
-      for (int e = 0; e < EB; ++e)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          acc[m * EB + e] =
-              __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, (uint32_t)w[e][i]),
-                                              __builtin_bit_cast(bf16x2, (uint32_t)x[m][i]), acc[m * EB + e], false);
+      for (int i = 0; i < 4; ++i)
+        acc[m] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, (uint32_t)w[i]),
+                                                 __builtin_bit_cast(bf16x2, (uint32_t)x[m][i]), acc[m], false);
   }
-  tile_sum<V>(acc);
-#pragma unroll
-  for (int i = 0; i < kTileOut<V>; ++i) {
-    acc[i] += dpp<0x4E>(acc[i]);
-    acc[i] += dpp<0xB1>(acc[i]);
-  }
-  if (tile_sum_owner<V>(lane) && (lane & 3) == 0) {
-    const int first = tile_sum_first<V>(lane);
-#pragma unroll
-    for (int i = 0; i < kTileOut<V>; ++i) red[wave * V + first + i] = acc[i];
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < V; i += kThreads) {
-    const int m = i / EB, e = e0 + i % EB;
-    if (m < a.M && e < a.E) put(&a.logits[m * a.E + e], ((red[i] + red[V + i]) + red[2 * V + i]) + red[3 * V + i]);
-  }
+  tile_sum<MR>(acc);
+  float z = acc[0];                    // MR <= 4: one value per lane
+  z += dpp<0x4E>(z);
+  z += dpp<0xB1>(z);
+  const int m = tile_sum_first<MR>(lane);
+  if (tile_sum_owner<MR>(lane) && (lane & 3) == 0 && m < a.M && e < a.E) put(&a.logits[m * a.E + e], z);
 }
 
 // From five rows on: 16 experts and one of `ks` shares of H on the 16x16x32
@@ -167,7 +150,7 @@ __device__ __forceinline__ void router_tile(const MoeArgs& a, int tile, float* r
 // products of 256 experts are spread over 64 blocks.
 __device__ __forceinline__ void router_tile_mfma(const MoeArgs& a, int tile, float* red) {
   typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = fresh_lane(), wave = threadIdx.x >> 6;
   const int share = tile % a.ks, e0 = tile / a.ks * 16, stride = a.ks * kWaves * 32;
   const uint16_t* pw = a.router + (int64_t)min(e0 + (lane & 15), a.E - 1) * a.H + (lane >> 4) * 8;
   const uint16_t* px = a.x + min(lane & 15, a.M - 1) * a.ldx + (lane >> 4) * 8;
@@ -237,10 +220,11 @@ __device__ __forceinline__ uint32_t pack_uniq(int e, int first, int n) {
 template <int EPL, int KS>
 __device__ __forceinline__ void route_row(const MoeArgs& a, int m, RouteLds& s) {
   constexpr bool SORT = EPL <= 8;
-  const int lane = threadIdx.x & 63;
+  const int lane = fresh_lane();
   const int epl = (a.E + 63) / 64;
   float* sval = s.val + (threadIdx.x >> 6) * a.E;
-  const Rsrc rl = make_rsrc(a.logits, (uint32_t)(KS * a.M * a.E) * 4), rb = make_rsrc(a.score_bias, (uint32_t)a.E * 4);
+  const Rsrc rl = make_rsrc(a.logits, (uint32_t)(KS * a.M * a.E) * 4);
+  const Rsrc rb = make_rsrc(a.score_bias, a.score_bias ? (uint32_t)a.E * 4 : 0);   // none: zeros
   float part[EPL][KS], bias[EPL];
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
@@ -250,8 +234,7 @@ __device__ __forceinline__ void route_row(const MoeArgs& a, int m, RouteLds& s) 
     for (int q = 0; q < KS; ++q)
       part[i][q] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
           rl, in ? ((q * a.M + m) * a.E + e) * 4 : (int)kBeyond, 0, kAgent));
-    bias[i] = 0.0f;
-    if (a.score_bias) bias[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rb, in ? e * 4 : (int)kBeyond, 0, 0));
+    bias[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rb, in ? e * 4 : (int)kBeyond, 0, 0));
   }
   int key[EPL], id[EPL];
 #pragma unroll
@@ -348,7 +331,7 @@ __device__ __forceinline__ void route_row(const MoeArgs& a, int m, RouteLds& s) 
 // The picks grouped by expert (experts ascending, an expert's rows ascending);
 // publishes them.  s.id holds all picks.
 __device__ __forceinline__ void group_picks(const MoeArgs& a, RouteLds& s) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = fresh_lane(), wave = threadIdx.x >> 6;
   int nu = a.k;
   if (a.M > 1) {
     for (int e = threadIdx.x; e < a.E; e += kThreads) s.rows[e] = 0;
@@ -431,7 +414,8 @@ __device__ __forceinline__ int wait_for(const MoeArgs& a, int flag) {
 struct Work {
   const uint8_t* blob;
   float gs13, gs2;
-  int inter, n;            // n rows
+  int inter;
+  int row, n;              // rows row .. row + n - 1 of the expert's
   int first;               // offset in the list of picks, or -1 for the shared expert
   int u;                   // unique index; U for the shared expert
 };
@@ -446,6 +430,7 @@ struct BlockLds {
 __device__ __forceinline__ Work work_of(const MoeArgs& a, const BlockLds& b, int u, bool shared) {
   Work w;
   w.u = u;
+  w.row = 0;
   if (!shared) {
     const uint32_t d = __builtin_amdgcn_readfirstlane(b.uniq[u]);
     const int e = d >> 14;
@@ -467,10 +452,10 @@ __device__ __forceinline__ Work work_of(const MoeArgs& a, const BlockLds& b, int
 }
 // The expert's c-th pick (P + row for the shared expert) and its token.
 __device__ __forceinline__ int pick_at(const MoeArgs& a, const BlockLds& b, const Work& w, int c) {
-  return w.first < 0 ? a.M * a.k + c : b.pick[w.first + c];
+  return w.first < 0 ? a.M * a.k + w.row + c : b.pick[w.first + w.row + c];
 }
 __device__ __forceinline__ int token_at(const MoeArgs& a, const BlockLds& b, const Work& w, int c) {
-  return w.first < 0 ? c : (int)((uint32_t)b.pick[w.first + c] / (uint32_t)a.k);
+  return w.first < 0 ? w.row + c : (int)((uint32_t)b.pick[w.first + w.row + c] / (uint32_t)a.k);
 }
 // First element of a pick's row of h: picks [P][I], then the shared expert's [M][Is]
 __device__ __forceinline__ uint32_t h_at(const MoeArgs& a, int p) {
@@ -517,8 +502,8 @@ __device__ __forceinline__ void stage_x(const MoeArgs& a, uint8_t* lds, int row_
 template <int ROWS>
 __device__ __forceinline__ void gateup_task(const MoeArgs& a, const BlockLds& b, const Work& w, int tile, int end,
                                             uint8_t* lds, bool x_there) {
-  constexpr int D = ROWS <= 4 ? 4 : 2, NA = (ROWS + 3) / 4;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  constexpr int D = 4, NA = (ROWS + 3) / 4;
+  const int lane = fresh_lane(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int H = a.H;
   const Reader<kNv> rd = reader<kNv>(w.blob, w.blob + (int64_t)w.inter * H, 2u * w.inter, H);
   const int r0 = lane & 3;
@@ -605,8 +590,8 @@ __device__ __forceinline__ void split3(f32x4 v, uint8_t* dst, int part_bytes) {
 template <int ROWS>
 __device__ __forceinline__ bool down_task(const MoeArgs& a, BlockLds& b, const Work& w, int tile, int end,
                                           uint8_t* lds) {
-  constexpr int Q = 2, D = ROWS <= 4 ? 4 : 2, NA = (ROWS + 3) / 4;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  constexpr int Q = 2, D = 4, NA = (ROWS + 3) / 4;
+  const int lane = fresh_lane(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int I = w.inter;
   const int64_t w13 = (int64_t)I * a.H + (int64_t)I * a.H / 8, codes = (int64_t)a.H * (I / 2);
   const Reader<kNv> rd = reader<kNv>(w.blob + w13, w.blob + w13 + codes, a.H, I);
@@ -723,21 +708,36 @@ __device__ __forceinline__ void combine_tile(const MoeArgs& a, int tile) {
   }
 }
 
+// More than eight rows (the shared expert's, or those of an expert that many
+// tokens picked) are computed eight at a time: sixteen at once need more
+// registers than three blocks per compute unit leave, and the second reading of
+// a tile comes from the caches.
 template <int MAXR>
-__device__ __forceinline__ void run_gateup(const MoeArgs& a, const BlockLds& b, const Work& w, int tile, int end,
-                                           uint8_t* lds, bool x_there) {
+__device__ __forceinline__ void run_gateup(const MoeArgs& a, const BlockLds& b, Work w, int tile, int end, uint8_t* lds,
+                                           bool x_there) {
   if (MAXR == 1 || w.n == 1) return gateup_task<1>(a, b, w, tile, end, lds, x_there);
   if (w.n == 2) return gateup_task<2>(a, b, w, tile, end, lds, x_there);
   if (MAXR == 4 || w.n <= 4) return gateup_task<4>(a, b, w, tile, end, lds, x_there);
-  if constexpr (MAXR > 4) return gateup_task<16>(a, b, w, tile, end, lds, x_there);
+  if constexpr (MAXR > 4) {
+    const int n = w.n;
+    for (w.row = 0; w.row < n; w.row += 8) {
+      w.n = min(8, n - w.row);
+      gateup_task<8>(a, b, w, tile, end, lds, x_there);
+    }
+  }
 }
 template <int MAXR>
-__device__ __forceinline__ bool run_down(const MoeArgs& a, BlockLds& b, const Work& w, int tile, int end,
-                                         uint8_t* lds) {
+__device__ __forceinline__ bool run_down(const MoeArgs& a, BlockLds& b, Work w, int tile, int end, uint8_t* lds) {
   if (MAXR == 1 || w.n == 1) return down_task<1>(a, b, w, tile, end, lds);
   if (w.n == 2) return down_task<2>(a, b, w, tile, end, lds);
   if (MAXR == 4 || w.n <= 4) return down_task<4>(a, b, w, tile, end, lds);
-  if constexpr (MAXR > 4) return down_task<16>(a, b, w, tile, end, lds);
+  if constexpr (MAXR > 4) {
+    const int n = w.n;
+    for (w.row = 0; w.row < n; w.row += 8) {
+      w.n = min(8, n - w.row);
+      if (!down_task<8>(a, b, w, tile, end, lds)) return false;
+    }
+  }
   return true;
 }
 
@@ -791,7 +791,6 @@ __device__ __forceinline__ int tiles_per_task(int tiles) {
 
 template <int MAXR>
 __device__ __forceinline__ void run_phases(const MoeArgs& a, BlockLds& b, uint8_t* lds) {
-  constexpr int EB = MAXR == 1 ? 1 : 2;   // experts per router tile of up to four rows
   const int tu = a.I / kUpRows, td = a.H / kDownRows, ns = a.shared ? 1 : 0;
   const bool x_there = a.dense;
   {
@@ -800,7 +799,7 @@ __device__ __forceinline__ void run_phases(const MoeArgs& a, BlockLds& b, uint8_
       k.ask();
       RouteLds& s = *reinterpret_cast<RouteLds*>(lds);
       if constexpr (MAXR > 4) router_tile_mfma(a, t, reinterpret_cast<float*>(lds));
-      else router_tile<EB, MAXR>(a, t, reinterpret_cast<float*>(lds));
+      else router_tile<MAXR>(a, t);
       if (arrive(&a.ctl[C_ARRIVED], a.router_tiles, &b.flag)) {
         if constexpr (MAXR > 4) {
           if (threadIdx.x == 0) put(&a.ctl[C_LOGITS], 1);
@@ -863,13 +862,14 @@ __device__ __forceinline__ void run_phases(const MoeArgs& a, BlockLds& b, uint8_
   }
   {
     // the shared expert's h is there first
-    const int f = tiles_per_task((U + ns) * td), per = (td + f - 1) / f;
-    Taker k = taker(a, kDown, (U + ns) * per);
+    const int f = tiles_per_task(U * td), per = (td + f - 1) / f, first = ns * td;
+    Taker k = taker(a, kDown, first + U * per);
     for (int t; (t = k.next(&b.tick)) >= 0;) {
       k.ask();
-      const int u = t / per, i0 = (t - u * per) * f, i1 = min(i0 + f, td);
-      const bool sh = ns && u == 0;
-      if (!run_down<MAXR>(a, b, work_of(a, b, sh ? kMaxPk : u - ns, sh), i0, i1, lds)) return;
+      const bool sh = t < first;
+      const int u = sh ? kMaxPk : (t - first) / per;
+      const int i0 = sh ? t : (t - first - u * per) * f, i1 = sh ? t + 1 : min(i0 + f, td);
+      if (!run_down<MAXR>(a, b, work_of(a, b, u, sh), i0, i1, lds)) return;
       stores_done();
       __syncthreads();
       // one lane per tile counts it; the block combines the tiles that it completed
@@ -951,11 +951,12 @@ hipError_t launch_moe(MoeArgs a, hipStream_t st) {
   const int steps_h = (a.H + kStepK - 1) / kStepK, inter = a.I > a.Is ? a.I : a.Is;
   const int steps_i = (inter + kStepK - 1) / kStepK;
   a.ks = MAXR == 16 ? kRouterShares : 1;
-  a.router_tiles = MAXR == 16 ? (a.E + 15) / 16 * a.ks : MAXR == 1 ? a.E : (a.E + 1) / 2;
+  a.router_tiles = MAXR == 16 ? (a.E + 15) / 16 * a.ks : (a.E + kWaves - 1) / kWaves;
   // LDS: the rows of x whole if they fit, and h of one expert's rows; three blocks share a compute unit's 160 KB
-  const int dense = a.M * (steps_h * kStepK * 2 + kPad), hrows = (a.M <= 2 ? a.M : MAXR) * 3 * (steps_i * kStepK * 2 + kPad);
+  constexpr int most = MAXR == 16 ? 8 : MAXR;   // rows of one expert at a time
+  const int dense = a.M * (steps_h * kStepK * 2 + kPad), hrows = (a.M <= 2 ? a.M : most) * 3 * (steps_i * kStepK * 2 + kPad);
   constexpr int cap = 49920;
-  static_assert((cap / (MAXR * 3) - kPad) / 2 >= kStepK, "one step of the largest row count must fit");
+  static_assert((cap / (most * 3) - kPad) / 2 >= kStepK, "one step of the largest row count must fit");
   const int least = route_lds(a.E);
   a.dense = dense <= cap;
   a.lds = (a.dense ? dense : cap) > hrows ? (a.dense ? dense : cap) : hrows;
