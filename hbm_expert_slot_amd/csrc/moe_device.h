@@ -1,0 +1,386 @@
+// What the kernels of the whole MoE layer share: their arguments, the hand-over
+// between blocks, and the routing.
+//
+// What one block hands to another goes through stores and loads at agent scope
+// (each XCD has an L2 of its own): written through, waited for, then counted or
+// flagged.  A release fence would write back every dirty line of the L2 instead,
+// other kernels' among them (measured: 12 of 21 us of a router product).
+// Logits and picks are their own flags: a word that is not there yet holds a
+// value that no result has, and whoever needs it polls the word itself.
+#pragma once
+
+#include "fp4_device.h"
+#include "internal.h"
+
+namespace sc {
+namespace moe {
+
+using namespace fp4;
+
+constexpr int kMaxTokens = SC_MOE_MAX_ROWS;
+constexpr int kPad = 16;           // bytes between operand rows in LDS: four rows' reads fall into different banks
+constexpr int kRouterShares = 4;   // shares of H in the router product of five rows and more
+constexpr int kShards = 16, kLine = 32;   // parts of a counter, and words per cache line
+
+// Polls of a wait before the call is given up (about a second): only a
+// workspace that was not prepared, or that two calls share, gets there.
+constexpr int kMaxPolls = 1 << 21;
+
+struct MoeArgs {
+  const uint16_t* router;    // [E][H] bf16
+  const float* score_bias;   // [E] or null
+  const uint8_t* blobs;      // [E][blob]
+  const float* gs;           // [E][2]
+  const uint8_t* shared;     // blob of the shared expert or null
+  const float* sgs;          // [2]
+  const uint16_t* x;         // [M][H]
+  void* y;                   // [M][H]
+  int32_t* ids_out;          // [M][k] or null
+  float* w_out;              // [M][k] or null
+  int32_t* ctl;              // control words, zero between calls
+  uint32_t* logits;          // [KS][M][E] partial sums over shares of H, kNoLogit between calls
+  uint64_t* picks;           // [P] expert + 1 and weight, 0 between calls
+  float* h;                  // [P][I], then [M][Is] of the shared expert
+  float* part;               // [P][H], then [M][H]
+  int64_t ldx, ldy, blob;
+  int M, H, I, E, k, Is, score, out, vec;
+  int lds;                   // bytes of LDS for operand rows
+  int dense;                 // x lies in LDS whole, token by token
+  int router_tiles, ks;      // ks: shares of H in the router product
+  int logit_words;           // of the workspace
+  float scale;
+};
+
+// Hand-over between blocks.
+template <typename T>
+__device__ __forceinline__ void put(T* p, T v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename T>
+__device__ __forceinline__ T get(const T* p) {
+  return __hip_atomic_load(const_cast<T*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ int add(int32_t* p, int v) {
+  return __hip_atomic_fetch_add(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+constexpr int kAgent = 16;   // buffer load at agent scope (sc1)
+// The wavefront's stores have been performed.
+__device__ __forceinline__ void stores_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// One poll of a wait that has lasted `i` polls: false when the call is given up.
+__device__ __forceinline__ bool poll_on(int32_t* error, int i) {
+  if (i >= kMaxPolls) put(error, 1);
+  if ((i & 63) == 63 && get(error)) return false;
+  __builtin_amdgcn_s_sleep(4);
+  return true;
+}
+
+// ---- routing -------------------------------------------------------------------
+
+constexpr uint32_t kNoLogit = 0xFFFFFFFFu;   // a NaN that no logit is: NaN logits are stored as 0x7FC00000
+__device__ __forceinline__ void put_logit(uint32_t* p, float z) {
+  put(p, z != z ? 0x7FC00000u : __float_as_uint(z));
+}
+
+__device__ __forceinline__ u32x4 load_x8(const MoeArgs& a, const uint16_t* p) {
+  if (a.vec) return *reinterpret_cast<const u32x4*>(p);
+  u32x4 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = p[2 * i] | (uint32_t)p[2 * i + 1] << 16;
+  return v;
+}
+
+constexpr int kTileWaves = 4;
+
+// Logits of four experts for up to MR (4) rows: each wavefront sums a quarter of
+// H, all its loads in flight together up to H = 6144, and the quarters are added
+// in wavefront order.
+template <int MR>
+__device__ __forceinline__ void router_tile(const MoeArgs& a, int tile, float* red) {
+  constexpr int EB = 4, V = EB * MR, N = 3;
+  const int lane = fresh_lane(), wave = threadIdx.x >> 6;
+  const int e0 = tile * EB;
+  float acc[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+  for (int c0 = (wave * 64 + lane) * 8; c0 < a.H; c0 += N * (64 * kTileWaves) * 8) {
+    u32x4 w[N][EB], x[N][MR];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int c = min(c0 + n * (64 * kTileWaves) * 8, a.H - 8);
+#pragma unroll
+      for (int m = 0; m < MR; ++m) x[n][m] = load_x8(a, a.x + min(m, a.M - 1) * a.ldx + c);
+#pragma unroll
+      for (int e = 0; e < EB; ++e)
+        w[n][e] = *reinterpret_cast<const u32x4*>(a.router + (int64_t)min(e0 + e, a.E - 1) * a.H + c);
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      if (c0 + n * (64 * kTileWaves) * 8 >= a.H) break;
+#pragma unroll
+      for (int m = 0; m < MR; ++m)
+#pragma unroll
+        for (int e = 0; e < EB; ++e)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            acc[m * EB + e] =
+                __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, (uint32_t)w[n][e][i]),
+                                                __builtin_bit_cast(bf16x2, (uint32_t)x[n][m][i]), acc[m * EB + e], false);
+    }
+  }
+  tile_sum<V>(acc);
+#pragma unroll
+  for (int i = 0; i < kTileOut<V>; ++i) {
+    acc[i] += dpp<0x4E>(acc[i]);
+    acc[i] += dpp<0xB1>(acc[i]);
+  }
+  if (tile_sum_owner<V>(lane) && (lane & 3) == 0) {
+    const int first = tile_sum_first<V>(lane);
+#pragma unroll
+    for (int i = 0; i < kTileOut<V>; ++i) red[wave * V + first + i] = acc[i];
+  }
+  __syncthreads();
+  const int i = threadIdx.x, m = i / EB, e = e0 + i % EB;
+  if (i < V && m < a.M && e < a.E)
+    put_logit(&a.logits[m * a.E + e], ((red[i] + red[V + i]) + red[2 * V + i]) + red[3 * V + i]);
+}
+
+// From five rows on: 16 experts and one of `ks` shares of H on the 16x16x32
+// matrix instruction (rows of x times rows of the router; lane l holds row
+// l % 16 of both, elements 8 (l / 16) .. + 7 of 32).  Four shares, so that the
+// products of 256 experts are spread over 64 blocks.
+__device__ __forceinline__ void router_tile_mfma(const MoeArgs& a, int tile, float* red) {
+  typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
+  constexpr int N = 12;
+  const int lane = fresh_lane(), wave = threadIdx.x >> 6;
+  const int share = tile % a.ks, e0 = tile / a.ks * 16, stride = a.ks * kTileWaves * 32;
+  const uint16_t* pw = a.router + (int64_t)min(e0 + (lane & 15), a.E - 1) * a.H + (lane >> 4) * 8;
+  const uint16_t* px = a.x + min(lane & 15, a.M - 1) * a.ldx + (lane >> 4) * 8;
+  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int k0 = (share * kTileWaves + wave) * 32; k0 < a.H; k0 += N * stride) {
+    u32x4 w[N], x[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int k = min(k0 + n * stride, a.H - 32);
+      w[n] = *reinterpret_cast<const u32x4*>(pw + k);
+      x[n] = load_x8(a, px + k);
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      if (k0 + n * stride >= a.H) break;
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[n]), __builtin_bit_cast(bf16x8, w[n]),
+                                                    acc, 0, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) red[(wave * 4 + i) * 64 + lane] = acc[i];
+  __syncthreads();
+  const int i = threadIdx.x;
+  const float z = ((red[i] + red[256 + i]) + red[512 + i]) + red[768 + i];
+  const int m = (i >> 4 & 3) * 4 + (i >> 6), e = e0 + (i & 15);   // lane i % 64 of register i / 64
+  if (m < a.M && e < a.E) put_logit(&a.logits[(share * a.M + m) * a.E + e], z);
+}
+
+// Keys that order as the scores do: NaN below -inf, -0 equal to +0.
+__device__ __forceinline__ int order_key(float z) {
+  if (z != z) return INT32_MIN + 1;
+  const int b = (int)__float_as_uint(z + 0.0f);
+  return b >= 0 ? b : b ^ 0x7FFFFFFF;
+}
+
+// Reductions over the wavefront in registers: halves and 16-lane rows trade by
+// lane swaps, the rest through DPP.
+template <typename F>
+__device__ __forceinline__ uint32_t wave_reduce(uint32_t v, F f) {
+  auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  v = f(r[0], r[1]);
+  r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = f(r[0], r[1]);
+  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xF, 0xF, false));
+  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xF, 0xF, false));
+  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));
+  return f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));
+}
+__device__ __forceinline__ int wave_max_i(int v) {
+  return (int)wave_reduce((uint32_t)v, [](uint32_t x, uint32_t y) { return (uint32_t)max((int)x, (int)y); });
+}
+__device__ __forceinline__ float wave_sum_f(float v) {
+  return __uint_as_float(wave_reduce(__float_as_uint(v), [](uint32_t x, uint32_t y) {
+    return __float_as_uint(__uint_as_float(x) + __uint_as_float(y));
+  }));
+}
+
+// One wavefront picks row m's experts and publishes them.  Lane l looks after
+// experts l * epl .. and keeps them sorted (up to eight; more are looked through
+// each time), so that a pick costs one reduction: the lowest lane with the
+// largest key holds the lowest id.  val: LDS, [E].  The logits are set back to
+// kNoLogit.  False when the call was given up.
+template <int EPL, int KS>
+__device__ __forceinline__ bool route_row(const MoeArgs& a, int32_t* error, int m, float* sval) {
+  constexpr bool SORT = EPL <= 8;
+  const int lane = fresh_lane();
+  const int epl = (a.E + 63) / 64;
+  const Rsrc rl = make_rsrc(a.logits, (uint32_t)(KS * a.M * a.E) * 4);
+  const Rsrc rb = make_rsrc(a.score_bias, a.score_bias ? (uint32_t)a.E * 4 : 0);   // none: zeros
+  float bias[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int e = lane * epl + i;
+    bias[i] = __uint_as_float(
+        __builtin_amdgcn_raw_buffer_load_b32(rb, i < epl && e < a.E ? e * 4 : (int)kBeyond, 0, 0));
+  }
+  constexpr int QB = EPL * KS <= 32 ? KS : 32 / EPL;   // shares loaded at a time
+  float sum[EPL];
+#pragma unroll
+  for (int q0 = 0; q0 < KS; q0 += QB) {
+    uint32_t part[EPL][QB];
+    for (int poll = 0;; ++poll) {
+      bool all = true;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const int e = lane * epl + i;
+#pragma unroll
+        for (int q = 0; q < QB; ++q)
+          part[i][q] = __builtin_amdgcn_raw_buffer_load_b32(
+              rl, i < epl && e < a.E ? (((q0 + q) * a.M + m) * a.E + e) * 4 : (int)kBeyond, 0, kAgent);
+      }
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+#pragma unroll
+        for (int q = 0; q < QB; ++q) all = all && part[i][q] != kNoLogit;
+      if (!__ballot(!all)) break;
+      if (!poll_on(error, poll)) return false;
+    }
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+#pragma unroll
+      for (int q = 0; q < QB; ++q)
+        sum[i] = q0 + q == 0 ? __uint_as_float(part[i][q]) : sum[i] + __uint_as_float(part[i][q]);
+  }
+  int key[EPL], id[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    float z = sum[i];
+    // a few ulps from the hardware's exponential and reciprocal, below the logit's own rounding
+    if (a.score == SC_SCORE_SIGMOID) z = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-z * 1.4426950408889634f));
+    id[i] = lane * epl + i;
+    const bool in = i < epl && id[i] < a.E;
+    if (in) {
+      sval[id[i]] = z;
+#pragma unroll
+      for (int q = 0; q < KS; ++q) put(&a.logits[(q * a.M + m) * a.E + id[i]], kNoLogit);
+    }
+    key[i] = in ? order_key(z + bias[i]) : INT32_MIN;
+  }
+  if constexpr (SORT) {
+#pragma unroll
+    for (int n = EPL - 1; n > 0; --n)
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const bool up = key[i + 1] > key[i];       // equal keys keep their order
+        const int k0 = key[i], i0 = id[i];
+        key[i] = up ? key[i + 1] : k0;
+        id[i] = up ? id[i + 1] : i0;
+        key[i + 1] = up ? k0 : key[i + 1];
+        id[i + 1] = up ? i0 : id[i + 1];
+      }
+  }
+  int my_id = 0;
+#pragma unroll 1
+  for (int j = 0; j < a.k; ++j) {
+    int best = key[0], at = id[0];
+    if constexpr (!SORT) {
+#pragma unroll
+      for (int i = 1; i < EPL; ++i)
+        if (key[i] > best) {
+          best = key[i];
+          at = id[i];
+        }
+    }
+    const int src = __builtin_ctzll(__ballot(best == wave_max_i(best)));
+    const int e = __builtin_amdgcn_readlane(at, src);
+    if (lane == j) my_id = e;
+    if constexpr (SORT) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        key[i] = lane == src ? (i + 1 < EPL ? key[i + 1] : INT32_MIN) : key[i];
+        id[i] = lane == src && i + 1 < EPL ? id[i + 1] : id[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (id[i] == e) key[i] = INT32_MIN;
+    }
+  }
+  // weights; NaN counts as the lowest score, picks of +inf share the weight,
+  // and picks that all have the lowest score share it too
+  const bool on = lane < a.k;
+  const float my_val = on ? sval[my_id] : 0.0f;
+  const float z = my_val != my_val ? -INFINITY : my_val;
+  float w;
+  if (a.score == SC_SCORE_SIGMOID) {
+    w = on && z > 0.0f ? z : 0.0f;
+  } else {
+    const float zmax = __uint_as_float(wave_reduce(__float_as_uint(on ? z : -INFINITY), [](uint32_t x, uint32_t y) {
+      return __float_as_uint(fmaxf(__uint_as_float(x), __uint_as_float(y)));
+    }));
+    w = !on ? 0.0f : zmax == INFINITY ? (z == INFINITY ? 1.0f : 0.0f) : zmax == -INFINITY ? 1.0f : expf(z - zmax);
+  }
+  const float total = wave_sum_f(w);
+  w = (total > 0.0f ? w / total : 1.0f / (float)a.k) * a.scale;
+  if (on) {
+    const int p = m * a.k + lane;
+    put(&a.picks[p], (uint64_t)(uint32_t)(my_id + 1) << 32 | __float_as_uint(w));
+    if (a.ids_out) a.ids_out[p] = my_id;
+    if (a.w_out) a.w_out[p] = w;
+  }
+  return true;
+}
+
+template <int KS>
+__device__ __forceinline__ bool route_row(const MoeArgs& a, int32_t* error, int m, float* sval) {
+  if (a.E <= 256) return route_row<4, KS>(a, error, m, sval);
+  if (a.E <= 512) return route_row<8, KS>(a, error, m, sval);
+  return route_row<16, KS>(a, error, m, sval);
+}
+
+// ---- expert products -------------------------------------------------------------
+
+__device__ __forceinline__ float silu(float g) {
+  return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-g * 1.4426950408889634f));
+}
+
+// Four fp32 values as three bf16 parts that add up to them.
+__device__ __forceinline__ void split3(f32x4 v, uint8_t* dst, int part_bytes) {
+  uint16_t p[3][4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const __bf16 p0 = (__bf16)v[e];
+    const float f0 = (float)p0, d1 = v[e] - f0;
+    const bool fin = fabsf(f0) < INFINITY;      // what is not finite stands in the first part alone
+    const __bf16 p1 = (__bf16)(fin ? d1 : 0.0f);
+    const __bf16 p2 = (__bf16)(fin ? d1 - (float)p1 : 0.0f);
+    p[0][e] = __builtin_bit_cast(uint16_t, p0);
+    p[1][e] = __builtin_bit_cast(uint16_t, p1);
+    p[2][e] = __builtin_bit_cast(uint16_t, p2);
+  }
+#pragma unroll
+  for (int t = 0; t < 3; ++t)
+    *reinterpret_cast<u32x2*>(dst + t * part_bytes) =
+        u32x2{p[t][0] | (uint32_t)p[t][1] << 16, p[t][2] | (uint32_t)p[t][3] << 16};
+}
+
+__device__ __forceinline__ void store_y(const MoeArgs& a, int m, int r, float v) {
+  const int64_t o = m * a.ldy + r;
+  if (a.out == SC_DTYPE_F32) static_cast<float*>(a.y)[o] = v;
+  else static_cast<uint16_t*>(a.y)[o] = __builtin_bit_cast(uint16_t, (__bf16)v);
+}
+
+// After a call that was given up: y is NaN, and what is handed over is cleared.
+__device__ __forceinline__ void abandon(const MoeArgs& a) {
+  for (int i = threadIdx.x; i < a.M * a.H; i += blockDim.x) store_y(a, i / a.H, i % a.H, NAN);
+  for (int i = threadIdx.x; i < a.logit_words; i += blockDim.x) put(&a.logits[i], kNoLogit);
+}
+
+}  // namespace moe
+}  // namespace sc

@@ -16,24 +16,17 @@
 // The counters are in 16 parts: additions to one address take 11 ns each from
 // wherever they come (with a single counter a token's 3500 tickets took longer
 // than its weights).
-//
-// What one block hands to another goes through stores and loads at agent scope
-// (each XCD has an L2 of its own): written through, waited for, then counted.
-// A release fence would write back every dirty line of the L2 instead, other
-// kernels' among them (measured: 12 of 21 us of the router product).
-#include "fp4_device.h"
-#include "internal.h"
+#include "moe_device.h"
 
 namespace sc {
 namespace {
 
-using namespace fp4;
+using namespace moe;
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kMaxTokens = SC_MOE_MAX_ROWS;
+static_assert(kWaves == kTileWaves, "a block does a router tile");
 constexpr int kMaxPk = kMaxTokens * kMaxTopK;
-constexpr int kPad = 16;           // bytes between operand rows in LDS: four rows' reads fall into different banks
 constexpr int kUpRows = 16;        // rows of h per gate/up tile: a quad per wavefront
 constexpr int kDownRows = 32;      // output rows per down tile: two quads per wavefront
 
@@ -41,371 +34,31 @@ constexpr int kDownRows = 32;      // output rows per down tile: two quads per w
 // Counters that many blocks add to, and flags that many blocks poll, lie in
 // cache lines of their own, apart from each other: an addition to a line that
 // eight L2 caches hold for their pollers is slow, and so is all that waits in
-// its channel (a token's layer took 138 us with counters polled in place, 60
+// its channel (a token's layer took 138 us with counters polled in place, 81
 // with flags set once).
-constexpr int kShards = 16, kLine = 32;
 enum Phase { kRouter = 0, kPick, kShared, kRouted, kDown, kPhases };
 constexpr int kExperts = kMaxPk + 1;               // unique experts, then the shared one
 constexpr int kTiles = 32768 / kDownRows;
 constexpr int C_TICKETS = 0,                                    // [phase][shard]: tasks taken
-    C_ARRIVED = kPhases * kShards * kLine,                      // router tiles done
-    C_PICKED = C_ARRIVED + kLine,                               // pick tasks done
-    C_EXITS = C_PICKED + kLine,                                 // blocks that left
-    C_LOGITS = C_EXITS + kLine,                                 // flag: every logit is there
-    C_ROUTED = C_LOGITS + kLine,                                // flag: unique experts + 1
-    C_ERROR = C_ROUTED + kLine,                                 // flag: the call was given up
+    C_EXITS = kPhases * kShards * kLine,                        // blocks that left
+    C_ERROR = C_EXITS + kLine,                                  // flag: the call was given up
     C_HDONE = C_ERROR + kLine,                                  // [expert]: gate/up tiles done
     C_TILES = C_HDONE + (kExperts + kLine) / kLine * kLine,     // [tile]: experts' down tiles done
     C_HREADY = C_TILES + kTiles,                                // [expert]: flag: all of h is there
-    kCtlWords = C_HREADY + kExperts * kLine;
+    kLayerWords = C_HREADY + kExperts * kLine;
 
-// Polls of a wait before the call is given up (about a second): only a
-// workspace that was not prepared, or that two calls share, gets there.
-constexpr int kMaxPolls = 1 << 21;
-
-constexpr int kRouterShares = 4;
-
-struct MoeArgs {
-  const uint16_t* router;    // [E][H] bf16
-  const float* score_bias;   // [E] or null
-  const uint8_t* blobs;      // [E][blob]
-  const float* gs;           // [E][2]
-  const uint8_t* shared;     // blob of the shared expert or null
-  const float* sgs;          // [2]
-  const uint16_t* x;         // [M][H]
-  void* y;                   // [M][H]
-  int32_t* ids_out;          // [M][k] or null
-  float* w_out;              // [M][k] or null
-  int32_t* ctl;
-  float* logits;             // [KS][M][E] partial sums over shares of H
-  uint32_t* uniq;            // [U] expert, first pick and pick count (see pack_uniq)
-  uint32_t* uniq_picks;      // [P]
-  float* pick_w;             // [P]
-  uint32_t* pick_id;         // [P] (five rows and more)
-  float* h;                  // [P][I], then [M][Is] of the shared expert
-  float* part;               // [P][H], then [M][H]
-  int64_t ldx, ldy, blob;
-  int M, H, I, E, k, Is, score, out, vec;
-  int lds;                   // bytes of LDS for operand rows
-  int dense;                 // x lies in LDS whole, token by token
-  int router_tiles, ks;      // ks: shares of H in the router product
-  float scale;
-};
-
-// Hand-over between blocks.
-template <typename T>
-__device__ __forceinline__ void put(T* p, T v) {
-  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-template <typename T>
-__device__ __forceinline__ T get(const T* p) {
-  return __hip_atomic_load(const_cast<T*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-constexpr int kAgent = 16;   // buffer load at agent scope (sc1)
-// The wavefront's stores have been performed.
-__device__ __forceinline__ void stores_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
-
-// ---- routing -------------------------------------------------------------------
-
-__device__ __forceinline__ u32x4 load_x8(const MoeArgs& a, const uint16_t* p) {
-  if (a.vec) return *reinterpret_cast<const u32x4*>(p);
-  u32x4 v;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = p[2 * i] | (uint32_t)p[2 * i + 1] << 16;
-  return v;
-}
-
-// Logits of four experts, one per wavefront, for up to MR rows.
-template <int MR>
-__device__ __forceinline__ void router_tile(const MoeArgs& a, int tile) {
-  const int lane = fresh_lane(), e = tile * kWaves + (threadIdx.x >> 6);
-  const uint16_t* pw = a.router + (int64_t)min(e, a.E - 1) * a.H;
-  float acc[MR];
-#pragma unroll
-  for (int m = 0; m < MR; ++m) acc[m] = 0.0f;
-#pragma unroll 4
-  for (int c = lane * 8; c < a.H; c += 64 * 8) {
-    const u32x4 w = *reinterpret_cast<const u32x4*>(pw + c);
-    u32x4 x[MR];
-#pragma unroll
-    for (int m = 0; m < MR; ++m) x[m] = load_x8(a, a.x + min(m, a.M - 1) * a.ldx + c);
-#pragma unroll
-    for (int m = 0; m < MR; ++m)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        acc[m] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, (uint32_t)w[i]),
-                                                 __builtin_bit_cast(bf16x2, (uint32_t)x[m][i]), acc[m], false);
-  }
-  tile_sum<MR>(acc);
-  float z = acc[0];                    // MR <= 4: one value per lane
-  z += dpp<0x4E>(z);
-  z += dpp<0xB1>(z);
-  const int m = tile_sum_first<MR>(lane);
-  if (tile_sum_owner<MR>(lane) && (lane & 3) == 0 && m < a.M && e < a.E) put(&a.logits[m * a.E + e], z);
-}
-
-// From five rows on: 16 experts and one of `ks` shares of H on the 16x16x32
-// matrix instruction (rows of x times rows of the router; lane l holds row
-// l % 16 of both, elements 8 (l / 16) .. + 7 of 32).  Four shares, so that the
-// products of 256 experts are spread over 64 blocks.
-__device__ __forceinline__ void router_tile_mfma(const MoeArgs& a, int tile, float* red) {
-  typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
-  const int lane = fresh_lane(), wave = threadIdx.x >> 6;
-  const int share = tile % a.ks, e0 = tile / a.ks * 16, stride = a.ks * kWaves * 32;
-  const uint16_t* pw = a.router + (int64_t)min(e0 + (lane & 15), a.E - 1) * a.H + (lane >> 4) * 8;
-  const uint16_t* px = a.x + min(lane & 15, a.M - 1) * a.ldx + (lane >> 4) * 8;
-  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-  for (int k = (share * kWaves + wave) * 32; k < a.H; k += stride) {
-    const u32x4 w = *reinterpret_cast<const u32x4*>(pw + k), x = load_x8(a, px + k);
-    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, w), acc, 0,
-                                                  0, 0);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) red[(wave * 4 + i) * 64 + lane] = acc[i];
-  __syncthreads();
-  const int i = threadIdx.x;
-  const float z = ((red[i] + red[256 + i]) + red[512 + i]) + red[768 + i];
-  const int m = (i >> 4 & 3) * 4 + (i >> 6), e = e0 + (i & 15);   // lane i % 64 of register i / 64
-  if (m < a.M && e < a.E) put(&a.logits[(share * a.M + m) * a.E + e], z);
-}
-
-// Keys that order as the scores do: NaN below -inf, -0 equal to +0.
-__device__ __forceinline__ int order_key(float z) {
-  if (z != z) return INT32_MIN + 1;
-  const int b = (int)__float_as_uint(z + 0.0f);
-  return b >= 0 ? b : b ^ 0x7FFFFFFF;
-}
-
-// Reductions over the wavefront in registers: halves and 16-lane rows trade by
-// lane swaps, the rest through DPP.
-template <typename F>
-__device__ __forceinline__ uint32_t wave_reduce(uint32_t v, F f) {
-  auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-  v = f(r[0], r[1]);
-  r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-  v = f(r[0], r[1]);
-  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xF, 0xF, false));
-  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xF, 0xF, false));
-  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));
-  return f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));
-}
-__device__ __forceinline__ int wave_max_i(int v) {
-  return (int)wave_reduce((uint32_t)v, [](uint32_t x, uint32_t y) { return (uint32_t)max((int)x, (int)y); });
-}
-__device__ __forceinline__ float wave_sum_f(float v) {
-  return __uint_as_float(wave_reduce(__float_as_uint(v), [](uint32_t x, uint32_t y) {
-    return __float_as_uint(__uint_as_float(x) + __uint_as_float(y));
-  }));
-}
-
-struct RouteLds {
-  uint32_t rows[kMaxExperts];     // rows that picked the expert
-  int32_t off[kMaxExperts];       // first pick of the expert
-  int32_t wave[kWaves];
-  int16_t id[kMaxPk];
-  float val[];                    // [wavefront][E]: scores without the bias
-};
-inline int route_lds(int E) { return (int)sizeof(RouteLds) + kWaves * E * (int)sizeof(float); }
-
-// An expert (10 bits), its first pick in the list (9 bits) and its picks (5 bits).
-__device__ __forceinline__ uint32_t pack_uniq(int e, int first, int n) {
-  return (uint32_t)e << 14 | (uint32_t)first << 5 | (uint32_t)n;
-}
-
-// One wavefront picks a row's experts.  Lane l looks after experts l * epl ..
-// and keeps them sorted (up to eight; more are looked through each time), so
-// that a pick costs one reduction: the lowest lane with the largest key holds
-// the lowest id.
-template <int EPL, int KS>
-__device__ __forceinline__ void route_row(const MoeArgs& a, int m, RouteLds& s) {
-  constexpr bool SORT = EPL <= 8;
-  const int lane = fresh_lane();
-  const int epl = (a.E + 63) / 64;
-  float* sval = s.val + (threadIdx.x >> 6) * a.E;
-  const Rsrc rl = make_rsrc(a.logits, (uint32_t)(KS * a.M * a.E) * 4);
-  const Rsrc rb = make_rsrc(a.score_bias, a.score_bias ? (uint32_t)a.E * 4 : 0);   // none: zeros
-  float part[EPL][KS], bias[EPL];
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = lane * epl + i;
-    const bool in = i < epl && e < a.E;
-#pragma unroll
-    for (int q = 0; q < KS; ++q)
-      part[i][q] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
-          rl, in ? ((q * a.M + m) * a.E + e) * 4 : (int)kBeyond, 0, kAgent));
-    bias[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rb, in ? e * 4 : (int)kBeyond, 0, 0));
-  }
-  int key[EPL], id[EPL];
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    float z = part[i][0];
-#pragma unroll
-    for (int q = 1; q < KS; ++q) z += part[i][q];
-    if (a.score == SC_SCORE_SIGMOID) z = 1.0f / (1.0f + expf(-z));
-    id[i] = lane * epl + i;
-    const bool in = i < epl && id[i] < a.E;
-    if (in) sval[id[i]] = z;
-    key[i] = in ? order_key(z + bias[i]) : INT32_MIN;
-  }
-  if constexpr (SORT) {
-#pragma unroll
-    for (int n = EPL - 1; n > 0; --n)
-#pragma unroll
-      for (int i = 0; i < n; ++i) {
-        const bool up = key[i + 1] > key[i];       // equal keys keep their order
-        const int k0 = key[i], i0 = id[i];
-        key[i] = up ? key[i + 1] : k0;
-        id[i] = up ? id[i + 1] : i0;
-        key[i + 1] = up ? k0 : key[i + 1];
-        id[i + 1] = up ? i0 : id[i + 1];
-      }
-  }
-  int my_id = 0;
-#pragma unroll 1
-  for (int j = 0; j < a.k; ++j) {
-    int best = key[0], at = id[0];
-    if constexpr (!SORT) {
-#pragma unroll
-      for (int i = 1; i < EPL; ++i)
-        if (key[i] > best) {
-          best = key[i];
-          at = id[i];
-        }
-    }
-    const int src = __builtin_ctzll(__ballot(best == wave_max_i(best)));
-    const int e = __builtin_amdgcn_readlane(at, src);
-    if (lane == j) my_id = e;
-    if constexpr (SORT) {
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        key[i] = lane == src ? (i + 1 < EPL ? key[i + 1] : INT32_MIN) : key[i];
-        id[i] = lane == src && i + 1 < EPL ? id[i + 1] : id[i];
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if (id[i] == e) key[i] = INT32_MIN;
-    }
-  }
-  // weights; NaN counts as the lowest score, picks of +inf share the weight,
-  // and picks that all have the lowest score share it too
-  const bool on = lane < a.k;
-  const float my_val = on ? sval[my_id] : 0.0f;
-  const float z = my_val != my_val ? -INFINITY : my_val;
-  float w;
-  if (a.score == SC_SCORE_SIGMOID) {
-    w = on && z > 0.0f ? z : 0.0f;
-  } else {
-    const float zmax = __uint_as_float(wave_reduce(__float_as_uint(on ? z : -INFINITY), [](uint32_t x, uint32_t y) {
-      return __float_as_uint(fmaxf(__uint_as_float(x), __uint_as_float(y)));
-    }));
-    w = !on ? 0.0f : zmax == INFINITY ? (z == INFINITY ? 1.0f : 0.0f) : zmax == -INFINITY ? 1.0f : expf(z - zmax);
-  }
-  const float sum = wave_sum_f(w);
-  w = (sum > 0.0f ? w / sum : 1.0f / (float)a.k) * a.scale;
-  if (on) {
-    const int p = m * a.k + lane;
-    put(&a.pick_w[p], w);
-    if (a.ids_out) a.ids_out[p] = my_id;
-    if (a.w_out) a.w_out[p] = w;
-    if (a.M == 1) {
-      // one row: its picks are the unique experts
-      put(&a.uniq[p], pack_uniq(my_id, p, 1));
-      put(&a.uniq_picks[p], (uint32_t)p);
-    } else if (KS == 1) {
-      s.id[p] = (int16_t)my_id;
-    } else {
-      put(&a.pick_id[p], (uint32_t)my_id);
-    }
-  }
-}
-
-template <int KS>
-__device__ __forceinline__ void route_row(const MoeArgs& a, int m, RouteLds& s) {
-  if (a.E <= 256) route_row<4, KS>(a, m, s);
-  else if (a.E <= 512) route_row<8, KS>(a, m, s);
-  else route_row<16, KS>(a, m, s);
-}
-
-// The picks grouped by expert (experts ascending, an expert's rows ascending);
-// publishes them.  s.id holds all picks.
-__device__ __forceinline__ void group_picks(const MoeArgs& a, RouteLds& s) {
-  const int lane = fresh_lane(), wave = threadIdx.x >> 6;
-  int nu = a.k;
-  if (a.M > 1) {
-    for (int e = threadIdx.x; e < a.E; e += kThreads) s.rows[e] = 0;
-    __syncthreads();
-    for (int p = threadIdx.x; p < a.M * a.k; p += kThreads) atomicOr(&s.rows[s.id[p]], 1u << (p / a.k));
-    __syncthreads();
-    // a thread's experts in a row; unique experts and picks before them in one scan (high and low half)
-    const int per = (a.E + kThreads - 1) / kThreads, e0 = threadIdx.x * per;
-    int mine = 0;
-    for (int e = e0; e < min(e0 + per, a.E); ++e) {
-      const int n = __popc(s.rows[e]);
-      mine += n + (n > 0 ? 1 << 16 : 0);
-    }
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int t = __shfl_up(incl, o);
-      if (lane >= o) incl += t;
-    }
-    if (lane == 63) s.wave[wave] = incl;
-    __syncthreads();
-    int before = incl - mine, all = 0;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      if (w < wave) before += s.wave[w];
-      all += s.wave[w];
-    }
-    nu = all >> 16;
-    for (int e = e0; e < min(e0 + per, a.E); ++e) {
-      const int n = __popc(s.rows[e]);
-      if (n > 0) {
-        put(&a.uniq[before >> 16], pack_uniq(e, before & 0xFFFF, n));
-        s.off[e] = before & 0xFFFF;
-        before += n + (1 << 16);
-      }
-    }
-    __syncthreads();
-    for (int p = threadIdx.x; p < a.M * a.k; p += kThreads) {
-      const int e = s.id[p], m = p / a.k;
-      put(&a.uniq_picks[s.off[e] + __popc(s.rows[e] & ((1u << m) - 1))], (uint32_t)p);
-    }
-  }
-  stores_done();
-  __syncthreads();
-  if (threadIdx.x == 0) put(&a.ctl[C_ROUTED], nu + 1);
-}
-
-// Counts the block in, once all that its threads put has been performed; true
-// in the block that completes `total`.
-__device__ __forceinline__ bool arrive(int32_t* counter, int total, int32_t* flag) {
-  stores_done();
-  __syncthreads();
-  if (threadIdx.x == 0)
-    *flag = __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == total - 1;
-  __syncthreads();
-  return *flag != 0;
-}
-// Counts `n` gate/up tiles of an expert in; who completes them sets its flag.
+// Counts `n` gate/up tiles of an expert in, once all that the block's threads put
+// has been performed; who completes them sets the expert's flag.
 __device__ __forceinline__ void post_h(const MoeArgs& a, int u, int n, int total) {
   stores_done();
   __syncthreads();
-  if (threadIdx.x == 0 && __hip_atomic_fetch_add(&a.ctl[C_HDONE + u], n, __ATOMIC_RELAXED,
-                                                 __HIP_MEMORY_SCOPE_AGENT) == total - n)
-    put(&a.ctl[C_HREADY + u * kLine], 1);
+  if (threadIdx.x == 0 && add(&a.ctl[C_HDONE + u], n) == total - n) put(&a.ctl[C_HREADY + u * kLine], 1);
 }
-// Waits until a flag is set and returns it (one thread); 0 when the call was given up.
-__device__ __forceinline__ int wait_for(const MoeArgs& a, int flag) {
-  for (int i = 0;; ++i) {
-    const int v = get(&a.ctl[flag]);
-    if (v) return v;
-    if (i >= kMaxPolls) put(&a.ctl[C_ERROR], 1);
-    if ((i & 63) == 63 && get(&a.ctl[C_ERROR])) return 0;
-    __builtin_amdgcn_s_sleep(4);
-  }
+// Waits until a flag is set (one thread); false when the call was given up.
+__device__ __forceinline__ bool wait_for(const MoeArgs& a, int flag) {
+  for (int i = 0; !get(&a.ctl[flag]); ++i)
+    if (!poll_on(&a.ctl[C_ERROR], i)) return false;
+  return true;
 }
 
 // ---- expert products ----------------------------------------------------------
@@ -420,14 +73,98 @@ struct Work {
   int u;                   // unique index; U for the shared expert
 };
 
-// The picks as a block keeps them.
+// The picks as a block keeps them, grouped by expert (experts ascending, an
+// expert's rows ascending).
+template <int MAXR>
 struct BlockLds {
-  uint32_t uniq[kMaxPk];
-  uint16_t pick[kMaxPk];
-  int32_t tick, flag, U;
+  static constexpr int kPk = MAXR * kMaxTopK;
+  uint32_t uniq[kPk];              // see pack_uniq
+  uint16_t pick[kPk];
+  uint32_t rows[MAXR == 4 ? kMaxExperts / 2 : 1];   // rows that picked each expert, 16 bits (in the operands' LDS
+                                                     // from five rows on)
+  int32_t wave[kWaves];
+  int32_t tick, flag;
 };
+// An expert (10 bits), its first pick in the list (9 bits) and its picks (5 bits).
+__device__ __forceinline__ uint32_t pack_uniq(int e, int first, int n) {
+  return (uint32_t)e << 14 | (uint32_t)first << 5 | (uint32_t)n;
+}
 
-__device__ __forceinline__ Work work_of(const MoeArgs& a, const BlockLds& b, int u, bool shared) {
+// Waits for every pick and groups them; each block does so for itself, which
+// saves two hand-overs.  The number of unique experts, or -1.
+template <int MAXR>
+__device__ __forceinline__ int group_picks(const MoeArgs& a, BlockLds<MAXR>& b, uint32_t* rows) {
+  constexpr int N = (BlockLds<MAXR>::kPk + kThreads - 1) / kThreads;
+  const int lane = fresh_lane(), wave = threadIdx.x >> 6, P = a.M * a.k;
+  if (threadIdx.x == 0) b.flag = 1;
+  for (int i = threadIdx.x; i < (a.E + 1) / 2; i += kThreads) rows[i] = 0;
+  __syncthreads();
+  int id[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const int p = threadIdx.x + j * kThreads;
+    id[j] = -1;
+    if (p >= P) continue;
+    uint64_t v;
+    for (int i = 0; !(v = get(&a.picks[p])); ++i)
+      if (!poll_on(&a.ctl[C_ERROR], i)) {
+        b.flag = 0;
+        break;
+      }
+    id[j] = (int)(v >> 32) - 1;
+    if (v) atomicOr(&rows[id[j] >> 1], 1u << (p / a.k + (id[j] & 1) * 16));
+  }
+  __syncthreads();
+  if (!b.flag) return -1;
+  // a thread's experts in a row; unique experts and picks before them in one scan (high and low half)
+  const int per = (a.E + kThreads - 1) / kThreads, e0 = threadIdx.x * per;
+  auto mask = [&](int e) { return rows[e >> 1] >> ((e & 1) * 16) & 0xFFFFu; };
+  int mine = 0;
+  for (int e = e0; e < min(e0 + per, a.E); ++e) {
+    const int n = __popc(mask(e));
+    mine += n + (n > 0 ? 1 << 16 : 0);
+  }
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int t = __shfl_up(incl, o);
+    if (lane >= o) incl += t;
+  }
+  if (lane == 63) b.wave[wave] = incl;
+  __syncthreads();
+  int before = incl - mine, all = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    if (w < wave) before += b.wave[w];
+    all += b.wave[w];
+  }
+  const int U = __builtin_amdgcn_readfirstlane(all >> 16);
+  for (int e = e0; e < min(e0 + per, a.E); ++e) {
+    const int n = __popc(mask(e));
+    if (n > 0) {
+      b.uniq[before >> 16] = pack_uniq(e, before & 0xFFFF, n);
+      before += n + (1 << 16);
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const int p = threadIdx.x + j * kThreads;
+    if (p >= P) continue;
+    int lo = 0, hi = U - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if ((int)(b.uniq[mid] >> 14) < id[j]) lo = mid + 1;
+      else hi = mid;
+    }
+    b.pick[(b.uniq[lo] >> 5 & 511) + __popc(mask(id[j]) & ((1u << (p / a.k)) - 1))] = (uint16_t)p;
+  }
+  __syncthreads();
+  return U;
+}
+
+template <int MAXR>
+__device__ __forceinline__ Work work_of(const MoeArgs& a, const BlockLds<MAXR>& b, int u, bool shared) {
   Work w;
   w.u = u;
   w.row = 0;
@@ -451,20 +188,18 @@ __device__ __forceinline__ Work work_of(const MoeArgs& a, const BlockLds& b, int
   return w;
 }
 // The expert's c-th pick (P + row for the shared expert) and its token.
-__device__ __forceinline__ int pick_at(const MoeArgs& a, const BlockLds& b, const Work& w, int c) {
+template <int MAXR>
+__device__ __forceinline__ int pick_at(const MoeArgs& a, const BlockLds<MAXR>& b, const Work& w, int c) {
   return w.first < 0 ? a.M * a.k + w.row + c : b.pick[w.first + w.row + c];
 }
-__device__ __forceinline__ int token_at(const MoeArgs& a, const BlockLds& b, const Work& w, int c) {
+template <int MAXR>
+__device__ __forceinline__ int token_at(const MoeArgs& a, const BlockLds<MAXR>& b, const Work& w, int c) {
   return w.first < 0 ? w.row + c : (int)((uint32_t)b.pick[w.first + w.row + c] / (uint32_t)a.k);
 }
 // First element of a pick's row of h: picks [P][I], then the shared expert's [M][Is]
 __device__ __forceinline__ uint32_t h_at(const MoeArgs& a, int p) {
   const uint32_t P = a.M * a.k;
   return (uint32_t)p < P ? (uint32_t)p * a.I : P * a.I + ((uint32_t)p - P) * a.Is;
-}
-
-__device__ __forceinline__ float silu(float g) {
-  return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-g * 1.4426950408889634f));
 }
 
 // K-elements of ROWS operand rows of `parts` bf16 parts that fit in LDS.
@@ -499,8 +234,8 @@ __device__ __forceinline__ void stage_x(const MoeArgs& a, uint8_t* lds, int row_
 // h rows of tiles [tile, end) of an expert, 16 each: a wavefront takes a quad of
 // gate rows and the quad of up rows that belongs to it.  x_there: all of x lies
 // in LDS (dense) and needs no staging.
-template <int ROWS>
-__device__ __forceinline__ void gateup_task(const MoeArgs& a, const BlockLds& b, const Work& w, int tile, int end,
+template <int ROWS, int MAXR>
+__device__ __forceinline__ void gateup_task(const MoeArgs& a, const BlockLds<MAXR>& b, const Work& w, int tile, int end,
                                             uint8_t* lds, bool x_there) {
   constexpr int D = 4, NA = (ROWS + 3) / 4;
   const int lane = fresh_lane(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -562,33 +297,13 @@ __device__ __forceinline__ void gateup_task(const MoeArgs& a, const BlockLds& b,
   }
 }
 
-// Four fp32 values as three bf16 parts that add up to them.
-__device__ __forceinline__ void split3(f32x4 v, uint8_t* dst, int part_bytes) {
-  uint16_t p[3][4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const __bf16 p0 = (__bf16)v[e];
-    const float f0 = (float)p0, d1 = v[e] - f0;
-    const bool fin = fabsf(f0) < INFINITY;      // what is not finite stands in the first part alone
-    const __bf16 p1 = (__bf16)(fin ? d1 : 0.0f);
-    const __bf16 p2 = (__bf16)(fin ? d1 - (float)p1 : 0.0f);
-    p[0][e] = __builtin_bit_cast(uint16_t, p0);
-    p[1][e] = __builtin_bit_cast(uint16_t, p1);
-    p[2][e] = __builtin_bit_cast(uint16_t, p2);
-  }
-#pragma unroll
-  for (int t = 0; t < 3; ++t)
-    *reinterpret_cast<u32x2*>(dst + t * part_bytes) =
-        u32x2{p[t][0] | (uint32_t)p[t][1] << 16, p[t][2] | (uint32_t)p[t][3] << 16};
-}
-
 // Output rows of tiles [tile, end), 32 each, of an expert's down product, per
 // pick.  h is
 // used to its 24 bits, in three bf16 parts: rounded to one part it would put
 // 2^-9 of itself into y, more than all fp32 sums together.  False when the call
 // was given up.
-template <int ROWS>
-__device__ __forceinline__ bool down_task(const MoeArgs& a, BlockLds& b, const Work& w, int tile, int end,
+template <int ROWS, int MAXR>
+__device__ __forceinline__ bool down_task(const MoeArgs& a, BlockLds<MAXR>& b, const Work& w, int tile, int end,
                                           uint8_t* lds) {
   constexpr int Q = 2, D = 4, NA = (ROWS + 3) / 4;
   const int lane = fresh_lane(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -675,16 +390,10 @@ __device__ __forceinline__ bool down_task(const MoeArgs& a, BlockLds& b, const W
   return true;
 }
 
-__device__ __forceinline__ void store_y(const MoeArgs& a, int m, int r, float v) {
-  const int64_t o = m * a.ldy + r;
-  if (a.out == SC_DTYPE_F32) static_cast<float*>(a.y)[o] = v;
-  else static_cast<uint16_t*>(a.y)[o] = __builtin_bit_cast(uint16_t, (__bf16)v);
-}
-
 // y of a tile: the picks in rank order, then the shared expert; eight loads in flight.
 __device__ __forceinline__ void combine_tile(const MoeArgs& a, int tile) {
   const int P = a.M * a.k;
-  const Rsrc rp = make_rsrc(a.part, (uint32_t)(P + (a.shared ? a.M : 0)) * a.H * 4), rw = make_rsrc(a.pick_w, P * 4);
+  const Rsrc rp = make_rsrc(a.part, (uint32_t)(P + (a.shared ? a.M : 0)) * a.H * 4), rw = make_rsrc(a.picks, P * 8);
   for (int i = threadIdx.x; i < a.M * kDownRows; i += kThreads) {
     const int m = i / kDownRows, r = tile * kDownRows + i % kDownRows, p0 = m * a.k;
     const float sh = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
@@ -697,7 +406,7 @@ __device__ __forceinline__ void combine_tile(const MoeArgs& a, int tile) {
         const bool in = j0 + j < a.k;
         v[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
             rp, in ? ((p0 + j0 + j) * a.H + r) * 4 : (int)kBeyond, 0, kAgent));
-        w[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rw, in ? (p0 + j0 + j) * 4 : (int)kBeyond, 0, kAgent));
+        w[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rw, in ? (p0 + j0 + j) * 8 : (int)kBeyond, 0, kAgent));
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j)
@@ -713,9 +422,9 @@ __device__ __forceinline__ void combine_tile(const MoeArgs& a, int tile) {
 // registers than three blocks per compute unit leave, and the second reading of
 // a tile comes from the caches.
 template <int MAXR>
-__device__ __forceinline__ void run_gateup(const MoeArgs& a, const BlockLds& b, Work w, int tile, int end, uint8_t* lds,
+__device__ __forceinline__ void run_gateup(const MoeArgs& a, const BlockLds<MAXR>& b, Work w, int tile, int end, uint8_t* lds,
                                            bool x_there) {
-  if (MAXR == 1 || w.n == 1) return gateup_task<1>(a, b, w, tile, end, lds, x_there);
+  if (w.n == 1) return gateup_task<1>(a, b, w, tile, end, lds, x_there);
   if (w.n == 2) return gateup_task<2>(a, b, w, tile, end, lds, x_there);
   if (MAXR == 4 || w.n <= 4) return gateup_task<4>(a, b, w, tile, end, lds, x_there);
   if constexpr (MAXR > 4) {
@@ -727,8 +436,8 @@ __device__ __forceinline__ void run_gateup(const MoeArgs& a, const BlockLds& b, 
   }
 }
 template <int MAXR>
-__device__ __forceinline__ bool run_down(const MoeArgs& a, BlockLds& b, Work w, int tile, int end, uint8_t* lds) {
-  if (MAXR == 1 || w.n == 1) return down_task<1>(a, b, w, tile, end, lds);
+__device__ __forceinline__ bool run_down(const MoeArgs& a, BlockLds<MAXR>& b, Work w, int tile, int end, uint8_t* lds) {
+  if (w.n == 1) return down_task<1>(a, b, w, tile, end, lds);
   if (w.n == 2) return down_task<2>(a, b, w, tile, end, lds);
   if (MAXR == 4 || w.n <= 4) return down_task<4>(a, b, w, tile, end, lds);
   if constexpr (MAXR > 4) {
@@ -749,7 +458,7 @@ struct Taker {
   int n, home, ahead;
   __device__ __forceinline__ int limit(int shard) const { return (n - shard + kShards - 1) / kShards; }
   __device__ __forceinline__ void ask() {
-    if (threadIdx.x == 0) ahead = __hip_atomic_fetch_add(c + home * kLine, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (threadIdx.x == 0) ahead = add(c + home * kLine, 1);
   }
   // the next task, or -1 when every task is taken; the block agrees on it through *tick
   __device__ __forceinline__ int next(int32_t* tick) {
@@ -765,7 +474,7 @@ struct Taker {
         const uint32_t rot = (m >> home | m << (kShards - home)) & ((1u << kShards) - 1);
         const int s = (home + __builtin_ctz(rot)) % kShards;
         int k = 0;
-        if (lane == 0) k = __hip_atomic_fetch_add(c + s * kLine, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (lane == 0) k = add(c + s * kLine, 1);
         k = __builtin_amdgcn_readfirstlane(k);
         if (k < limit(s)) {
           t = k * kShards + s;
@@ -790,45 +499,31 @@ __device__ __forceinline__ int tiles_per_task(int tiles) {
 }
 
 template <int MAXR>
-__device__ __forceinline__ void run_phases(const MoeArgs& a, BlockLds& b, uint8_t* lds) {
+__device__ __forceinline__ void run_phases(const MoeArgs& a, BlockLds<MAXR>& b, uint8_t* lds) {
   const int tu = a.I / kUpRows, td = a.H / kDownRows, ns = a.shared ? 1 : 0;
   const bool x_there = a.dense;
   {
     Taker k = taker(a, kRouter, a.router_tiles);
     for (int t; (t = k.next(&b.tick)) >= 0;) {
       k.ask();
-      RouteLds& s = *reinterpret_cast<RouteLds*>(lds);
       if constexpr (MAXR > 4) router_tile_mfma(a, t, reinterpret_cast<float*>(lds));
-      else router_tile<MAXR>(a, t);
-      if (arrive(&a.ctl[C_ARRIVED], a.router_tiles, &b.flag)) {
-        if constexpr (MAXR > 4) {
-          if (threadIdx.x == 0) put(&a.ctl[C_LOGITS], 1);
-        } else {
-          // up to four rows are picked here, a wavefront each
-          if ((int)(threadIdx.x >> 6) < a.M) route_row<1>(a, threadIdx.x >> 6, s);
-          __syncthreads();
-          group_picks(a, s);
-        }
-      }
+      else router_tile<MAXR>(a, t, reinterpret_cast<float*>(lds));
     }
   }
-  if constexpr (MAXR > 4) {
-    // rows are picked by fours; the block that ends the last four groups all picks
-    RouteLds& s = *reinterpret_cast<RouteLds*>(lds);
+  {
+    // a wavefront per row
     const int n = (a.M + kWaves - 1) / kWaves;
     Taker k = taker(a, kPick, n);
     for (int t; (t = k.next(&b.tick)) >= 0;) {
       k.ask();
-      if (threadIdx.x == 0) b.flag = wait_for(a, C_LOGITS);
+      const int wave = threadIdx.x >> 6, m = t * kWaves + wave;
+      b.flag = 1;
+      __syncthreads();
+      if (m < a.M && !route_row<MAXR == 16 ? kRouterShares : 1>(a, &a.ctl[C_ERROR], m,
+                                                                reinterpret_cast<float*>(lds) + wave * a.E))
+        b.flag = 0;
       __syncthreads();
       if (!b.flag) return;
-      const int m = t * kWaves + (threadIdx.x >> 6);
-      if (m < a.M) route_row<kRouterShares>(a, m, s);
-      if (arrive(&a.ctl[C_PICKED], n, &b.flag)) {
-        for (int p = threadIdx.x; p < a.M * a.k; p += kThreads) s.id[p] = (int16_t)get(&a.pick_id[p]);
-        __syncthreads();
-        group_picks(a, s);
-      }
     }
   }
   if (a.dense) {
@@ -844,12 +539,8 @@ __device__ __forceinline__ void run_phases(const MoeArgs& a, BlockLds& b, uint8_
     }
   }
   Taker kr = taker(a, kRouted, 0);
-  if (threadIdx.x == 0) b.U = wait_for(a, C_ROUTED) - 1;
-  __syncthreads();
-  const int U = __builtin_amdgcn_readfirstlane(b.U);
-  if (U < 0 || U > a.M * a.k) return;
-  for (int i = threadIdx.x; i < U; i += kThreads) b.uniq[i] = get(&a.uniq[i]);
-  for (int i = threadIdx.x; i < a.M * a.k; i += kThreads) b.pick[i] = (uint16_t)get(&a.uniq_picks[i]);
+  const int U = group_picks<MAXR>(a, b, MAXR == 4 ? b.rows : reinterpret_cast<uint32_t*>(lds));
+  if (U < 0) return;
   {
     const int f = tiles_per_task(U * tu), per = (tu + f - 1) / f;
     kr.n = U * per;
@@ -875,8 +566,7 @@ __device__ __forceinline__ void run_phases(const MoeArgs& a, BlockLds& b, uint8_
       // one lane per tile counts it; the block combines the tiles that it completed
       if (threadIdx.x < 64) {
         const int i = i0 + threadIdx.x;
-        const bool last = i < i1 && __hip_atomic_fetch_add(&a.ctl[C_TILES + i], 1, __ATOMIC_RELAXED,
-                                                           __HIP_MEMORY_SCOPE_AGENT) == U + ns - 1;
+        const bool last = i < i1 && add(&a.ctl[C_TILES + i], 1) == U + ns - 1;
         const uint64_t m = __ballot(last);
         if (threadIdx.x == 0) b.flag = (int)m;
       }
@@ -887,49 +577,68 @@ __device__ __forceinline__ void run_phases(const MoeArgs& a, BlockLds& b, uint8_
 }
 
 template <int MAXR>
-__global__ __launch_bounds__(kThreads, MAXR == 1 ? 4 : 3) void k_moe_layer(MoeArgs a) {
+__global__ __launch_bounds__(kThreads, 3) void k_moe_layer(MoeArgs a) {
   extern __shared__ __align__(16) uint8_t lds[];
-  __shared__ BlockLds b;
+  __shared__ BlockLds<MAXR> b;
   run_phases<MAXR>(a, b, lds);
   // the last block out clears the control words; a call that was given up has no result
+  stores_done();
   __syncthreads();
   if (threadIdx.x == 0)
-    b.flag = __hip_atomic_fetch_add(&a.ctl[C_EXITS], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-             (int)gridDim.x - 1;
+    b.flag = add(&a.ctl[C_EXITS], 1) == (int)gridDim.x - 1;
   __syncthreads();
   if (!b.flag) return;
-  if (get(&a.ctl[C_ERROR]))
-    for (int i = threadIdx.x; i < a.M * a.H; i += kThreads) store_y(a, i / a.H, i % a.H, NAN);
+  if (get(&a.ctl[C_ERROR])) abandon(a);
+  for (int i = threadIdx.x; i < a.M * a.k; i += kThreads) put(&a.picks[i], (uint64_t)0);
   __syncthreads();
-  for (int i = threadIdx.x; i < kCtlWords; i += kThreads) put(&a.ctl[i], 0);
+  for (int i = threadIdx.x; i < C_HREADY; i += kThreads) put(&a.ctl[i], 0);
+  for (int i = threadIdx.x; i < min(a.M * a.k, a.E); i += kThreads) put(&a.ctl[C_HREADY + i * kLine], 0);
+  if (threadIdx.x == 0) put(&a.ctl[C_HREADY + kMaxPk * kLine], 0);
 }
 
-__global__ void k_moe_clear(int32_t* ctl, int n) {
-  for (int i = threadIdx.x; i < n; i += blockDim.x) ctl[i] = 0;
+// A workspace as it is between calls.
+__global__ void k_moe_clear(MoeArgs a, int ctl_words, int picks) {
+  const int i0 = blockIdx.x * blockDim.x + threadIdx.x, n = gridDim.x * blockDim.x;
+  for (int i = i0; i < ctl_words; i += n) a.ctl[i] = 0;
+  for (int i = i0; i < picks; i += n) a.picks[i] = 0;
+  for (int i = i0; i < a.logit_words; i += n) a.logits[i] = kNoLogit;
 }
 
 // ---- host ------------------------------------------------------------------------
 
+constexpr int kCtlWords = kLayerWords;
 constexpr size_t kAlign = 256;
 size_t up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
 struct MoeWs {
-  size_t ctl, logits, uniq, uniq_picks, pick_w, pick_id, h, part, end;
+  size_t ctl, logits, picks, h, part, end;
+  int logit_words;
 };
 MoeWs moe_ws(const sc_moe_config* c) {
   MoeWs o;
   const size_t M = c->max_rows, P = M * c->top_k;
+  o.logit_words = (M > 4 ? kRouterShares : 1) * M * c->n_experts;
   size_t p = 0;
   o.ctl = p; p = up(p + kCtlWords * 4);
-  o.logits = p; p = up(p + (M > 4 ? kRouterShares : 1) * M * c->n_experts * 4);
-  o.uniq = p; p = up(p + P * 4);
-  o.uniq_picks = p; p = up(p + P * 4);
-  o.pick_w = p; p = up(p + P * 4);
-  o.pick_id = p; p = up(p + P * 4);
+  o.logits = p; p = up(p + (size_t)o.logit_words * 4);
+  o.picks = p; p = up(p + P * 8);
   o.h = p; p = up(p + (P * c->inter + M * c->shared_inter) * 4);
   o.part = p; p = up(p + (P + M) * c->hidden * 4);
   o.end = p;
   return o;
+}
+// The parts of a workspace.
+MoeArgs bind(const sc_moe_config* c, void* d_workspace) {
+  uint8_t* ws = static_cast<uint8_t*>(d_workspace);
+  const MoeWs o = moe_ws(c);
+  MoeArgs a{};
+  a.ctl = reinterpret_cast<int32_t*>(ws + o.ctl);
+  a.logits = reinterpret_cast<uint32_t*>(ws + o.logits);
+  a.picks = reinterpret_cast<uint64_t*>(ws + o.picks);
+  a.h = reinterpret_cast<float*>(ws + o.h);
+  a.part = reinterpret_cast<float*>(ws + o.part);
+  a.logit_words = o.logit_words;
+  return a;
 }
 
 sc_status check_moe(const sc_moe_config* c) {
@@ -951,14 +660,14 @@ hipError_t launch_moe(MoeArgs a, hipStream_t st) {
   const int steps_h = (a.H + kStepK - 1) / kStepK, inter = a.I > a.Is ? a.I : a.Is;
   const int steps_i = (inter + kStepK - 1) / kStepK;
   a.ks = MAXR == 16 ? kRouterShares : 1;
-  a.router_tiles = MAXR == 16 ? (a.E + 15) / 16 * a.ks : (a.E + kWaves - 1) / kWaves;
+  a.router_tiles = MAXR == 16 ? (a.E + 15) / 16 * a.ks : (a.E + 3) / 4;
   // LDS: the rows of x whole if they fit, and h of one expert's rows; three blocks share a compute unit's 160 KB
   constexpr int most = MAXR == 16 ? 8 : MAXR;   // rows of one expert at a time
   const int dense = a.M * (steps_h * kStepK * 2 + kPad), hrows = (a.M <= 2 ? a.M : most) * 3 * (steps_i * kStepK * 2 + kPad);
   constexpr int cap = 49920;
   static_assert((cap / (most * 3) - kPad) / 2 >= kStepK, "one step of the largest row count must fit");
-  const int least = route_lds(a.E);
-  a.dense = dense <= cap;
+  const int least = kWaves * a.E * 4 > 4096 ? kWaves * a.E * 4 : 4096;   // routing: scores; router tiles: sums
+  a.dense = MAXR == 4 && dense <= cap;
   a.lds = (a.dense ? dense : cap) > hrows ? (a.dense ? dense : cap) : hrows;
   if (a.lds > cap) a.lds = cap;
   if (a.lds < least) a.lds = (least + 15) / 16 * 16;
@@ -989,8 +698,8 @@ sc_status moe_layer_prepare(const sc_moe_config* cfg, void* d_workspace, void* s
   const sc_status s = check_moe(cfg);
   if (s != SC_OK) return s;
   if (!d_workspace || (uintptr_t)d_workspace % kAlign) return fail(SC_E_ARG, "the workspace must be 256-byte aligned");
-  hipLaunchKernelGGL(k_moe_clear, dim3(1), dim3(256), 0, static_cast<hipStream_t>(stream),
-                     reinterpret_cast<int32_t*>(static_cast<uint8_t*>(d_workspace) + moe_ws(cfg).ctl), kCtlWords);
+  hipLaunchKernelGGL(k_moe_clear, dim3(32), dim3(256), 0, static_cast<hipStream_t>(stream), bind(cfg, d_workspace),
+                     kCtlWords, cfg->max_rows * cfg->top_k);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? SC_OK : hip_fail(e, "moe_layer_prepare launch");
 }
@@ -1015,9 +724,7 @@ sc_status moe_layer_forward(const sc_moe_config* c, const sc_moe_weights* w, voi
       (uintptr_t)d_weights % 4)
     return fail(SC_E_ARG, "x, y, ids or weights are not aligned to their elements");
   if (ldx < c->hidden || ldy < c->hidden) return fail(SC_E_ARG, "row strides must cover the rows");
-  uint8_t* ws = static_cast<uint8_t*>(d_workspace);
-  const MoeWs o = moe_ws(c);
-  MoeArgs a{};
+  MoeArgs a = bind(c, d_workspace);
   a.router = static_cast<const uint16_t*>(w->d_router);
   a.score_bias = c->score == SC_SCORE_SIGMOID ? w->d_score_bias : nullptr;
   a.blobs = static_cast<const uint8_t*>(w->d_blobs);
@@ -1028,14 +735,6 @@ sc_status moe_layer_forward(const sc_moe_config* c, const sc_moe_weights* w, voi
   a.y = d_y;
   a.ids_out = d_ids;
   a.w_out = d_weights;
-  a.ctl = reinterpret_cast<int32_t*>(ws + o.ctl);
-  a.logits = reinterpret_cast<float*>(ws + o.logits);
-  a.uniq = reinterpret_cast<uint32_t*>(ws + o.uniq);
-  a.uniq_picks = reinterpret_cast<uint32_t*>(ws + o.uniq_picks);
-  a.pick_w = reinterpret_cast<float*>(ws + o.pick_w);
-  a.pick_id = reinterpret_cast<uint32_t*>(ws + o.pick_id);
-  a.h = reinterpret_cast<float*>(ws + o.h);
-  a.part = reinterpret_cast<float*>(ws + o.part);
   a.ldx = ldx;
   a.ldy = ldy;
   a.blob = make_shape(c->hidden, c->inter, c->n_experts, c->top_k).blob;
@@ -1050,7 +749,7 @@ sc_status moe_layer_forward(const sc_moe_config* c, const sc_moe_weights* w, voi
   a.vec = (uintptr_t)d_x % 16 == 0 && ldx % 8 == 0;
   a.scale = c->routed_scale;
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  const hipError_t e = M == 1 ? launch_moe<1>(a, st) : M <= 4 ? launch_moe<4>(a, st) : launch_moe<16>(a, st);
+  const hipError_t e = M <= 4 ? launch_moe<4>(a, st) : launch_moe<16>(a, st);
   return e == hipSuccess ? SC_OK : hip_fail(e, "moe_layer_forward launch");
 }
 
