@@ -214,9 +214,10 @@ __device__ __forceinline__ float wave_sum_f(float v) {
 // experts l * epl .. and keeps them sorted (up to eight; more are looked through
 // each time), so that a pick costs one reduction: the lowest lane with the
 // largest key holds the lowest id.  val: LDS, [E].  The logits are set back to
-// kNoLogit.  False when the call was given up.
+// kNoLogit.  After `patience` polls it returns kLate with nothing done.
+enum Routed { kDone = 0, kLate, kGivenUp };
 template <int EPL, int KS>
-__device__ __forceinline__ bool route_row(const MoeArgs& a, int32_t* error, int m, float* sval) {
+__device__ __forceinline__ Routed route_row(const MoeArgs& a, int32_t* error, int m, float* sval, int patience) {
   constexpr bool SORT = EPL <= 8;
   const int lane = fresh_lane();
   const int epl = (a.E + 63) / 64;
@@ -249,7 +250,8 @@ __device__ __forceinline__ bool route_row(const MoeArgs& a, int32_t* error, int 
 #pragma unroll
         for (int q = 0; q < QB; ++q) all = all && part[i][q] != kNoLogit;
       if (!__ballot(!all)) break;
-      if (!poll_on(error, poll)) return false;
+      if (poll >= patience) return kLate;
+      if (!poll_on(error, poll)) return kGivenUp;
     }
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
@@ -334,14 +336,15 @@ __device__ __forceinline__ bool route_row(const MoeArgs& a, int32_t* error, int 
     if (a.ids_out) a.ids_out[p] = my_id;
     if (a.w_out) a.w_out[p] = w;
   }
-  return true;
+  return kDone;
 }
 
 template <int KS>
-__device__ __forceinline__ bool route_row(const MoeArgs& a, int32_t* error, int m, float* sval) {
-  if (a.E <= 256) return route_row<4, KS>(a, error, m, sval);
-  if (a.E <= 512) return route_row<8, KS>(a, error, m, sval);
-  return route_row<16, KS>(a, error, m, sval);
+__device__ __forceinline__ Routed route_row(const MoeArgs& a, int32_t* error, int m, float* sval,
+                                            int patience = INT32_MAX) {
+  if (a.E <= 256) return route_row<4, KS>(a, error, m, sval, patience);
+  if (a.E <= 512) return route_row<8, KS>(a, error, m, sval, patience);
+  return route_row<16, KS>(a, error, m, sval, patience);
 }
 
 // ---- expert products -------------------------------------------------------------
@@ -376,11 +379,52 @@ __device__ __forceinline__ void store_y(const MoeArgs& a, int m, int r, float v)
   else static_cast<uint16_t*>(a.y)[o] = __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
+// A phase's tasks as one block takes them: task t is number t / 16 of part t % 16.
+// `ahead` (thread 0) is the next number of the block's own part, asked for while
+// the task before runs; when that part is used up, the others are looked through.
+struct Taker {
+  int32_t* c;
+  int n, home, ahead;
+  __device__ __forceinline__ int limit(int shard) const { return (n - shard + kShards - 1) / kShards; }
+  __device__ __forceinline__ void ask() {
+    if (threadIdx.x == 0) ahead = add(c + home * kLine, 1);
+  }
+  // the next task, or -1 when every task is taken; the block agrees on it through *tick
+  __device__ __forceinline__ int next(int32_t* tick) {
+    __syncthreads();
+    if (threadIdx.x < 64) {
+      int t = __builtin_amdgcn_readfirstlane(ahead);
+      t = t < limit(home) ? t * kShards + home : -1;
+      const int lane = threadIdx.x;
+      while (t < 0) {
+        const bool left = lane < kShards && get(c + lane * kLine) < limit(lane);
+        const uint32_t m = (uint32_t)__ballot(left);
+        if (!m) break;
+        const uint32_t rot = (m >> home | m << (kShards - home)) & ((1u << kShards) - 1);
+        const int s = (home + __builtin_ctz(rot)) % kShards;
+        int k = 0;
+        if (lane == 0) k = add(c + s * kLine, 1);
+        k = __builtin_amdgcn_readfirstlane(k);
+        if (k < limit(s)) {
+          t = k * kShards + s;
+          home = s;
+        }
+      }
+      if (lane == 0) *tick = t;
+    }
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(*tick);
+  }
+};
 // After a call that was given up: y is NaN, and what is handed over is cleared.
 __device__ __forceinline__ void abandon(const MoeArgs& a) {
   for (int i = threadIdx.x; i < a.M * a.H; i += blockDim.x) store_y(a, i / a.H, i % a.H, NAN);
   for (int i = threadIdx.x; i < a.logit_words; i += blockDim.x) put(&a.logits[i], kNoLogit);
 }
+
+// Control words of the one-row kernel (moe_one.hip).
+constexpr int kOneWords = (3 * kShards + 4) * kLine;
+hipError_t launch_moe_one(const MoeArgs& a, hipStream_t st);
 
 }  // namespace moe
 }  // namespace sc

@@ -1,5 +1,6 @@
-// A whole mixture-of-experts layer for up to 16 tokens in one launch: router
+// A whole mixture-of-experts layer for 2 to 16 tokens in one launch: router
 // product, top-k, gate/up, SiLU, down, weighted combine and the shared expert.
+// (One token: moe_one.hip.)
 //
 // Bound: HBM, by the bytes of the experts picked.  Between the products there
 // is nothing to compute, only data to hand over, so the layer is one kernel
@@ -45,7 +46,8 @@ constexpr int C_TICKETS = 0,                                    // [phase][shard
     C_HDONE = C_ERROR + kLine,                                  // [expert]: gate/up tiles done
     C_TILES = C_HDONE + (kExperts + kLine) / kLine * kLine,     // [tile]: experts' down tiles done
     C_HREADY = C_TILES + kTiles,                                // [expert]: flag: all of h is there
-    kLayerWords = C_HREADY + kExperts * kLine;
+    kLayerWords = C_HREADY + kExperts * kLine;                  // whole lines: the one-row kernel's words follow
+static_assert(kLayerWords % kLine == 0, "");
 
 // Counts `n` gate/up tiles of an expert in, once all that the block's threads put
 // has been performed; who completes them sets the expert's flag.
@@ -450,43 +452,6 @@ __device__ __forceinline__ bool run_down(const MoeArgs& a, BlockLds<MAXR>& b, Wo
   return true;
 }
 
-// A phase's tasks as one block takes them: task t is number t / 16 of part t % 16.
-// `ahead` (thread 0) is the next number of the block's own part, asked for while
-// the task before runs; when that part is used up, the others are looked through.
-struct Taker {
-  int32_t* c;
-  int n, home, ahead;
-  __device__ __forceinline__ int limit(int shard) const { return (n - shard + kShards - 1) / kShards; }
-  __device__ __forceinline__ void ask() {
-    if (threadIdx.x == 0) ahead = add(c + home * kLine, 1);
-  }
-  // the next task, or -1 when every task is taken; the block agrees on it through *tick
-  __device__ __forceinline__ int next(int32_t* tick) {
-    __syncthreads();
-    if (threadIdx.x < 64) {
-      int t = __builtin_amdgcn_readfirstlane(ahead);
-      t = t < limit(home) ? t * kShards + home : -1;
-      const int lane = threadIdx.x;
-      while (t < 0) {
-        const bool left = lane < kShards && get(c + lane * kLine) < limit(lane);
-        const uint32_t m = (uint32_t)__ballot(left);
-        if (!m) break;
-        const uint32_t rot = (m >> home | m << (kShards - home)) & ((1u << kShards) - 1);
-        const int s = (home + __builtin_ctz(rot)) % kShards;
-        int k = 0;
-        if (lane == 0) k = add(c + s * kLine, 1);
-        k = __builtin_amdgcn_readfirstlane(k);
-        if (k < limit(s)) {
-          t = k * kShards + s;
-          home = s;
-        }
-      }
-      if (lane == 0) *tick = t;
-    }
-    __syncthreads();
-    return __builtin_amdgcn_readfirstlane(*tick);
-  }
-};
 __device__ __forceinline__ Taker taker(const MoeArgs& a, int phase, int n) {
   Taker t{a.ctl + C_TICKETS + phase * kShards * kLine, n, (int)(blockIdx.x % kShards), 0};
   t.ask();
@@ -519,8 +484,8 @@ __device__ __forceinline__ void run_phases(const MoeArgs& a, BlockLds<MAXR>& b, 
       const int wave = threadIdx.x >> 6, m = t * kWaves + wave;
       b.flag = 1;
       __syncthreads();
-      if (m < a.M && !route_row<MAXR == 16 ? kRouterShares : 1>(a, &a.ctl[C_ERROR], m,
-                                                                reinterpret_cast<float*>(lds) + wave * a.E))
+      if (m < a.M && route_row<MAXR == 16 ? kRouterShares : 1>(a, &a.ctl[C_ERROR], m,
+                                                               reinterpret_cast<float*>(lds) + wave * a.E) != kDone)
         b.flag = 0;
       __syncthreads();
       if (!b.flag) return;
@@ -606,7 +571,7 @@ __global__ void k_moe_clear(MoeArgs a, int ctl_words, int picks) {
 
 // ---- host ------------------------------------------------------------------------
 
-constexpr int kCtlWords = kLayerWords;
+constexpr int kCtlWords = kLayerWords + kOneWords;
 constexpr size_t kAlign = 256;
 size_t up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
@@ -749,7 +714,8 @@ sc_status moe_layer_forward(const sc_moe_config* c, const sc_moe_weights* w, voi
   a.vec = (uintptr_t)d_x % 16 == 0 && ldx % 8 == 0;
   a.scale = c->routed_scale;
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  const hipError_t e = M <= 4 ? launch_moe<4>(a, st) : launch_moe<16>(a, st);
+  if (M == 1) a.ctl += kLayerWords;
+  const hipError_t e = M == 1 ? launch_moe_one(a, st) : M <= 4 ? launch_moe<4>(a, st) : launch_moe<16>(a, st);
   return e == hipSuccess ? SC_OK : hip_fail(e, "moe_layer_forward launch");
 }
 
