@@ -27,10 +27,12 @@ enum Format { kNv = 0, kMx = 1 };
 // is used.  In a kernel of many phases it would else be moved out of the task
 // loops and spilled, and each reload waits for every load in flight.
 __device__ __forceinline__ int fresh_lane() {
-  int lane = threadIdx.x & 63;
-  asm volatile("" : "+v"(lane));
+  int lane;
+  asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=&v"(lane));
   return lane;
 }
+__device__ __forceinline__ int wave_index() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+__device__ __forceinline__ int fresh_thread() { return wave_index() * 64 + fresh_lane(); }
 
 // A buffer descriptor over [p, p + bytes).  A load whose lane offset is kBeyond
 // returns zeros and touches no memory, so tails need no branches; every other
@@ -215,17 +217,19 @@ __device__ __forceinline__ void load_stage(Stage<FMT, ODD, Q>& st, const Reader<
 // lane's operand row of set a (row 4a + l % 4) in LDS, 32 elements at this step.
 // A lane of a row behind the last reads any memory: its results are not used.
 //
+// W quads are worked on at a time: their widened codes are live together, and
+// their chains of matrix instructions run side by side.
+//
 // SPLIT: the operand is fp32, held as three bf16 parts that add up to it (24
 // bits).  With one row the parts stand as three rows of its set and their sums
 // are added; otherwise part p lies at + p * part_bytes and the matrix
 // instructions add all three into one sum.
-template <int FMT, bool ODD, int Q, int ROWS, bool HALF, bool SPLIT = false>
+template <int FMT, bool ODD, int Q, int ROWS, bool HALF, bool SPLIT = false, int W = Q < 2 ? Q : 2>
 __device__ __forceinline__ void use_stage(const Stage<FMT, ODD, Q>& st,
                                           const uint8_t* const (&xs)[(ROWS + 3) / 4], int at, float (&acc)[Q][ROWS],
                                           int part_bytes = 0) {
   constexpr int NA = (ROWS + 3) / 4, NP = SPLIT && ROWS > 1 ? 3 : 1;
-  constexpr int W = Q < 2 ? Q : 2;   // quads whose widened codes are live at a time
-  static_assert(Q % W == 0, "quads are taken in pairs");
+  static_assert(Q % W == 0, "");
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
 #pragma unroll

@@ -423,7 +423,7 @@ __device__ __forceinline__ void abandon(const MoeArgs& a) {
 }
 
 // Control words of the one-row kernel (moe_one.hip).
-constexpr int kOneWords = (3 * kShards + 4) * kLine;
+constexpr int kOneWords = 1024 + (2 * kShards + 3) * kLine;
 hipError_t launch_moe_one(const MoeArgs& a, hipStream_t st);
 
 }  // namespace moe
