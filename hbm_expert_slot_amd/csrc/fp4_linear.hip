@@ -20,6 +20,7 @@ struct LinearArgs {
   int kc;                  // K-elements of the operand that LDS holds at a time
   int out;                 // sc_dtype of y
   int vec;                 // x rows can be read 16 bytes at a time
+  int mblocks;             // tiles of rows (k_fp4_tiles)
 };
 
 template <typename T>
@@ -154,11 +155,220 @@ hipError_t rows_by_count(const LinearArgs& a, hipStream_t st) {
   return launch_rows<FMT, ODD, HALF, 16>(a, st);
 }
 
+// ---- many rows -------------------------------------------------------------------
+//
+// Tiles of BM operand rows and 4 NT 16 weight rows on the 16x16x32 matrix
+// instruction: the four wavefronts share the operand through LDS and own
+// different weight rows, so a weight is widened once per block.  A lane reads 16
+// bytes of codes: 32 elements of row l % 16 at 32 (l / 16) of a 128-element chunk;
+// the order of K within a chunk is free as long as the operand is read in the
+// same order.  Widened weights carry their group scale, exactly: an E2M1 code
+// times an E4M3 scale has 6 significant bits, times a power of two 2.
+//   NVFP4, bf16: through fp32 products      (2 instructions per weight)
+//   NVFP4, fp16: packed fp16 products       (1)
+//   MXFP4: the scale goes into the conversion (1/2), always to bf16, whose
+//   exponent holds every E8M0 scale; fp16 operands are split into two bf16
+//   parts (11 = 8 + 3 significant bits), both multiplied.
+constexpr int kChunk = 128;
+
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
+typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
+
+template <bool F16>
+__device__ __forceinline__ f32x4 mfma16(u32x4 x, u32x4 w, f32x4 c) {
+  if constexpr (F16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, x), __builtin_bit_cast(f16x8, w), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, w), c, 0, 0,
+                                                   0);
+}
+
+// Two codes (byte B of d), times their scale s.
+template <int FMT, bool F16, int B>
+__device__ __forceinline__ uint32_t scaled2(uint32_t d, float s) {
+  if constexpr (FMT == kMx) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, B));
+  } else if constexpr (F16) {
+    const _Float16 h = (_Float16)s;
+    const f16x2 v = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(d, 1.0f, B));
+    return __builtin_bit_cast(uint32_t, v * f16x2{h, h});
+  } else {
+    const f32x2 v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d, 1.0f, B);
+    return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)(v.x * s), (__bf16)(v.y * s)});
+  }
+}
+template <int FMT, bool F16>
+__device__ __forceinline__ u32x4 scaled8(uint32_t d, float s) {
+  return u32x4{scaled2<FMT, F16, 0>(d, s), scaled2<FMT, F16, 1>(d, s), scaled2<FMT, F16, 2>(d, s),
+               scaled2<FMT, F16, 3>(d, s)};
+}
+
+template <int FMT, bool ODD, bool HALF, int BM, int NT>
+__global__ __launch_bounds__(256) void k_fp4_tiles(LinearArgs a) {
+  extern __shared__ __align__(16) uint8_t lds[];
+  constexpr bool F16 = HALF && FMT == kNv;                 // type of the products
+  constexpr int P = HALF && FMT == kMx ? 2 : 1;            // bf16 parts of the operand
+  constexpr int MT = BM / 16, BN = 4 * NT * 16, G = FMT == kNv ? 16 : 32;
+  constexpr int kRow = kChunk * 2 + 16, kPlane = BM * kRow;   // bytes; rows shifted by four banks each
+  constexpr int XL = BM * kChunk / 8 / 256;                // 16-byte pieces of the operand chunk per thread
+  const int lane = threadIdx.x & 63, wave = wave_index();
+  // blocks that share weight rows follow each other on one XCD (they are dealt out to eight in turn)
+  const int nb = gridDim.x / a.mblocks, id = blockIdx.x;
+  const int per = (nb + 7) / 8, xcd = id % 8, slot = id / 8;
+  int bn = xcd * per + slot / a.mblocks, bm = slot % a.mblocks;
+  if (nb % 8) {
+    bn = id / a.mblocks;
+    bm = id % a.mblocks;
+  }
+  const int n0 = bn * BN + wave * NT * 16, m0 = bm * BM;
+  const int rows = min(a.N - bn * BN, BN);
+  const uint32_t cb = (uint32_t)a.K / 2, sb = (uint32_t)a.K / G;
+  const Rsrc rc = make_rsrc(a.codes + (size_t)bn * BN * cb, (uint32_t)rows * cb);
+  const Rsrc rs = make_rsrc(a.scales + (size_t)bn * BN * sb, (uint32_t)rows * sb);
+  const int g = lane >> 4, r = lane & 15;
+
+  u32x4 q[NT];
+  uint32_t sc[NT];
+  auto load_w = [&](int kc) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int row = wave * NT * 16 + t * 16 + r, k = kc + 32 * g;
+      const bool in = row < rows && k < a.K;
+      const uint32_t oc = (uint32_t)row * cb + k / 2, os = (uint32_t)row * sb + k / G;
+      if constexpr (ODD) {
+        const bool in2 = in && k + 16 < a.K;
+        const u32x2 lo = load8(rc, in ? oc : kBeyond, 0), hi = load8(rc, in2 ? oc + 8 : kBeyond, 0);
+        q[t] = u32x4{lo.x, lo.y, hi.x, hi.y};
+        sc[t] = load1(rs, in ? os : kBeyond, 0) | load1(rs, in2 ? os + 1 : kBeyond, 0) << 8;
+      } else {
+        q[t] = load16(rc, in ? oc : kBeyond, 0);
+        sc[t] = FMT == kMx ? load1(rs, in ? os : kBeyond, 0) : load2(rs, in ? os : kBeyond, 0);
+      }
+    }
+  };
+  u32x4 xr[XL];
+  auto load_x = [&](int kc) {
+#pragma unroll
+    for (int i = 0; i < XL; ++i) {
+      const int e = threadIdx.x + i * 256, m = min(m0 + e / (kChunk / 8), a.M - 1), k = kc + e % (kChunk / 8) * 8;
+      xr[i] = u32x4{0, 0, 0, 0};
+      if (k < a.K) {
+        const uint16_t* p = a.x + (int64_t)m * a.ldx + k;
+        if (a.vec) {
+          xr[i] = *reinterpret_cast<const u32x4*>(p);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) xr[i][j] = p[2 * j] | (uint32_t)p[2 * j + 1] << 16;
+        }
+      }
+    }
+  };
+  auto put_x = [&](uint8_t* buf) {
+#pragma unroll
+    for (int i = 0; i < XL; ++i) {
+      const int e = threadIdx.x + i * 256;
+      uint8_t* p = buf + e / (kChunk / 8) * kRow + e % (kChunk / 8) * 16;
+      if constexpr (P == 1) {
+        *reinterpret_cast<u32x4*>(p) = xr[i];
+      } else {
+        u32x4 hi, lo;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const f16x2 v = __builtin_bit_cast(f16x2, (uint32_t)xr[i][j]);
+          const bf16x2 h = {(__bf16)(float)v.x, (__bf16)(float)v.y};
+          // what is not finite stands in the first part alone
+          const float d0 = (float)v.x - (float)h.x, d1 = (float)v.y - (float)h.y;
+          const bf16x2 l = {(__bf16)(d0 == d0 ? d0 : 0.0f), (__bf16)(d1 == d1 ? d1 : 0.0f)};
+          hi[j] = __builtin_bit_cast(uint32_t, h);
+          lo[j] = __builtin_bit_cast(uint32_t, l);
+        }
+        *reinterpret_cast<u32x4*>(p) = hi;
+        *reinterpret_cast<u32x4*>(p + kPlane) = lo;
+      }
+    }
+  };
+
+  f32x4 acc[MT][NT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[i][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  load_x(0);
+  load_w(0);
+  put_x(lds);
+  __syncthreads();
+  int buf = 0;
+  for (int kc = 0; kc < a.K; kc += kChunk) {
+    u32x4 cq[NT];
+    f32x2 cs[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      cq[t] = q[t];
+      cs[t] = lane_scales<FMT>(sc[t]);
+    }
+    const bool more = kc + kChunk < a.K;
+    if (more) {
+      load_x(kc + kChunk);
+      load_w(kc + kChunk);
+    }
+    const uint8_t* xb = lds + buf * (P * kPlane) + r * kRow + g * 64;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      u32x4 w[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) w[t] = scaled8<FMT, F16>(cq[t][j], j < 2 ? cs[t].x : cs[t].y);
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          const u32x4 x = *reinterpret_cast<const u32x4*>(xb + p * kPlane + i * 16 * kRow + j * 16);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) acc[i][t] = mfma16<F16>(x, w[t], acc[i][t]);
+        }
+    }
+    if (more) put_x(lds + (buf ^ 1) * (P * kPlane));
+    __syncthreads();
+    buf ^= 1;
+  }
+  const float gs = a.gs ? *a.gs : 1.0f;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int n = n0 + t * 16 + r;
+    if (n >= a.N) continue;
+    const float b = a.bias ? a.bias[n] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int m = m0 + i * 16 + g * 4 + e;
+        if (m < a.M) store_out(a.y, (int64_t)m * a.ldy + n, acc[i][t][e] * gs + b, a.out);
+      }
+  }
+}
+
+template <int FMT, bool ODD, bool HALF, int BM, int NT>
+hipError_t launch_tiles(LinearArgs a, hipStream_t st) {
+  constexpr int P = HALF && FMT == kMx ? 2 : 1;
+  a.mblocks = (a.M + BM - 1) / BM;
+  const long blocks = (long)a.mblocks * ((a.N + 64 * NT - 1) / (64 * NT));
+  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((k_fp4_tiles<FMT, ODD, HALF, BM, NT>), dim3((unsigned)blocks), dim3(256),
+                     2 * P * BM * (kChunk * 2 + 16), st, a);
+  return hipGetLastError();
+}
+
+template <int FMT, bool ODD, bool HALF>
+hipError_t by_count(const LinearArgs& a, hipStream_t st) {
+  if (a.M <= 16) return rows_by_count<FMT, ODD, HALF>(a, st);
+  if (a.M <= 32) return launch_tiles<FMT, ODD, HALF, 32, 1>(a, st);
+  return launch_tiles<FMT, ODD, HALF, 64, 2>(a, st);
+}
+
 template <bool HALF>
-hipError_t rows_by_format(const LinearArgs& a, int fmt, hipStream_t st) {
-  if (fmt == SC_FP4_MX) return rows_by_count<kMx, false, HALF>(a, st);
-  if (a.K / 16 % 2) return rows_by_count<kNv, true, HALF>(a, st);
-  return rows_by_count<kNv, false, HALF>(a, st);
+hipError_t by_format(const LinearArgs& a, int fmt, hipStream_t st) {
+  if (fmt == SC_FP4_MX) return by_count<kMx, false, HALF>(a, st);
+  if (a.K / 16 % 2) return by_count<kNv, true, HALF>(a, st);
+  return by_count<kNv, false, HALF>(a, st);
 }
 
 }  // namespace
@@ -190,15 +400,11 @@ extern "C" sc_status fp4_linear(const sc_fp4_matrix* w, const void* d_x, int32_t
   a.K = w->cols;
   a.out = y_type;
   a.vec = (uintptr_t)d_x % 16 == 0 && ldx % 8 == 0;
-  const size_t ysize = y_type == SC_DTYPE_F32 ? 4 : 2;
-  for (int64_t m = 0; m < M; m += 16) {
-    a.M = (int)(M - m < 16 ? M - m : 16);
-    a.x = static_cast<const uint16_t*>(d_x) + m * ldx;
-    a.y = static_cast<uint8_t*>(d_y) + (size_t)(m * ldy) * ysize;
-    const hipStream_t st = static_cast<hipStream_t>(stream);
-    const hipError_t e = x_type == SC_DTYPE_F16 ? rows_by_format<true>(a, w->format, st)
-                                                : rows_by_format<false>(a, w->format, st);
-    if (e != hipSuccess) return hip_fail(e, "fp4_linear launch");
-  }
+  a.M = M;
+  a.x = static_cast<const uint16_t*>(d_x);
+  a.y = d_y;
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  const hipError_t e = x_type == SC_DTYPE_F16 ? by_format<true>(a, w->format, st) : by_format<false>(a, w->format, st);
+  if (e != hipSuccess) return hip_fail(e, "fp4_linear launch");
   return SC_OK;
 }
