@@ -43,19 +43,24 @@ __device__ __forceinline__ Rsrc make_rsrc(const void* p, uint32_t bytes) {
 }
 constexpr uint32_t kBeyond = 0x80000000u;   // lies beyond every descriptor
 constexpr int kStream = 2;                  // nontemporal: weights are read once per call
+constexpr int kReuse = 0;                   // cached: several blocks read them
 
 // lane: offset of the lane; at: uniform offset
+template <int AUX = kStream>
 __device__ __forceinline__ u32x4 load16(Rsrc r, uint32_t lane, uint32_t at) {
-  return __builtin_amdgcn_raw_buffer_load_b128(r, (int)lane, (int)at, kStream);
+  return __builtin_amdgcn_raw_buffer_load_b128(r, (int)lane, (int)at, AUX);
 }
+template <int AUX = kStream>
 __device__ __forceinline__ u32x2 load8(Rsrc r, uint32_t lane, uint32_t at) {
-  return __builtin_amdgcn_raw_buffer_load_b64(r, (int)lane, (int)at, kStream);
+  return __builtin_amdgcn_raw_buffer_load_b64(r, (int)lane, (int)at, AUX);
 }
+template <int AUX = kStream>
 __device__ __forceinline__ uint32_t load2(Rsrc r, uint32_t lane, uint32_t at) {
-  return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)lane, (int)at, kStream);
+  return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)lane, (int)at, AUX);
 }
+template <int AUX = kStream>
 __device__ __forceinline__ uint32_t load1(Rsrc r, uint32_t lane, uint32_t at) {
-  return (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(r, (int)lane, (int)at, kStream);
+  return (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(r, (int)lane, (int)at, AUX);
 }
 
 // Four codes (bytes B and B+1 of d) as bf16 or fp16.  The conversions are

@@ -19,7 +19,6 @@ struct LinearArgs {
   int wk;                  // wavefronts of a block that share its rows along K (1, 2 or 4)
   int kc;                  // K-elements of the operand that LDS holds at a time
   int out;                 // sc_dtype of y
-  int vec;                 // x rows can be read 16 bytes at a time
   int mblocks;             // tiles of rows (k_fp4_tiles)
 };
 
@@ -31,6 +30,13 @@ __device__ __forceinline__ void store_out(void* y, int64_t i, float v, int out) 
   if (out == SC_DTYPE_F32) static_cast<float*>(y)[i] = v;
   else if (out == SC_DTYPE_BF16) static_cast<uint16_t*>(y)[i] = bits16<__bf16>(v);
   else static_cast<uint16_t*>(y)[i] = bits16<_Float16>(v);
+}
+
+// Eight elements of an operand row, which need not be aligned to more than themselves.
+__device__ __forceinline__ u32x4 load_x16(const uint16_t* p) {
+  u32x4 v;
+  __builtin_memcpy(&v, p, sizeof v);
+  return v;
 }
 
 constexpr int kRowPad = 16;   // bytes between operand rows in LDS: four rows' reads fall into different banks
@@ -78,15 +84,7 @@ __global__ __launch_bounds__(256) void k_fp4_rows(LinearArgs a) {
     for (int i = threadIdx.x; i < a.M * per_row; i += 256) {
       const int r = i / per_row, c = (i - r * per_row) * 8;
       u32x4 v = {0, 0, 0, 0};
-      if (kc + c < kend) {
-        const uint16_t* p = a.x + (int64_t)r * a.ldx + kc + c;
-        if (a.vec) {
-          v = *reinterpret_cast<const u32x4*>(p);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = p[2 * e] | (uint32_t)p[2 * e + 1] << 16;
-        }
-      }
+      if (kc + c < kend) v = load_x16(a.x + (int64_t)r * a.ldx + kc + c);
       *reinterpret_cast<u32x4*>(lds + r * row_lds + c * 2) = v;
     }
     __syncthreads();
@@ -150,16 +148,22 @@ template <int FMT, bool ODD, bool HALF>
 hipError_t rows_by_count(const LinearArgs& a, hipStream_t st) {
   if (a.M == 1) return launch_rows<FMT, ODD, HALF, 1>(a, st);
   if (a.M == 2) return launch_rows<FMT, ODD, HALF, 2>(a, st);
-  if (a.M <= 4) return launch_rows<FMT, ODD, HALF, 4>(a, st);
-  if (a.M <= 8) return launch_rows<FMT, ODD, HALF, 8>(a, st);
-  return launch_rows<FMT, ODD, HALF, 16>(a, st);
+  return launch_rows<FMT, ODD, HALF, 4>(a, st);
 }
 
 // ---- many rows -------------------------------------------------------------------
 //
-// Tiles of BM operand rows and 4 NT 16 weight rows on the 16x16x32 matrix
-// instruction: the four wavefronts share the operand through LDS and own
-// different weight rows, so a weight is widened once per block.  A lane reads 16
+// Tiles of BM operand rows and WN NT 16 weight rows on the 16x16x32 matrix
+// instruction.  A block has KS groups of WN wavefronts; a group takes every KS-th
+// 128-element chunk of K, and the groups' sums are added at the end, in group
+// order.  The wavefronts of a group share the operand's chunk through LDS and own
+// different weight rows, so a weight is widened once per block.  What bounds it up
+// to a few hundred rows is a wavefront's chain of chunks (load, wait, barrier,
+// multiply: half a microsecond each), not its arithmetic: the KS groups shorten the
+// chain and hide each other's waits (4096 x 12288, 16 rows, us: 47 with one group
+// per block, 32 with four, 15.6 with eight on tiles a quarter as wide), while a
+// second chunk under way in registers gained nothing.  From there on it is the
+// widening, done once per block of rows.  A lane reads 16
 // bytes of codes: 32 elements of row l % 16 at 32 (l / 16) of a 128-element chunk;
 // the order of K within a chunk is free as long as the operand is read in the
 // same order.  Widened weights carry their group scale, exactly: an E2M1 code
@@ -203,15 +207,16 @@ __device__ __forceinline__ u32x4 scaled8(uint32_t d, float s) {
                scaled2<FMT, F16, 3>(d, s)};
 }
 
-template <int FMT, bool ODD, bool HALF, int BM, int NT>
-__global__ __launch_bounds__(256) void k_fp4_tiles(LinearArgs a) {
-  extern __shared__ __align__(16) uint8_t lds[];
+template <int FMT, bool ODD, bool HALF, int BM, int NT, int WN, int KS>
+__global__ __launch_bounds__(64 * WN * KS) void k_fp4_tiles(LinearArgs a) {
+  extern __shared__ __align__(16) uint8_t lds_all[];
   constexpr bool F16 = HALF && FMT == kNv;                 // type of the products
   constexpr int P = HALF && FMT == kMx ? 2 : 1;            // bf16 parts of the operand
-  constexpr int MT = BM / 16, BN = 4 * NT * 16, G = FMT == kNv ? 16 : 32;
+  constexpr int MT = BM / 16, BN = WN * NT * 16, T = 64 * WN, G = FMT == kNv ? 16 : 32;
   constexpr int kRow = kChunk * 2 + 16, kPlane = BM * kRow;   // bytes; rows shifted by four banks each
-  constexpr int XL = BM * kChunk / 8 / 256;                // 16-byte pieces of the operand chunk per thread
-  const int lane = threadIdx.x & 63, wave = wave_index();
+  constexpr int XL = BM * kChunk / 8 / T;                // 16-byte pieces of the operand chunk per thread
+  const int lane = threadIdx.x & 63, wave = wave_index() % WN, kg = wave_index() / WN, tid = threadIdx.x % T;
+  uint8_t* lds = lds_all + kg * (2 * P * kPlane);
   // blocks that share weight rows follow each other on one XCD (they are dealt out to eight in turn)
   const int nb = gridDim.x / a.mblocks, id = blockIdx.x;
   const int per = (nb + 7) / 8, xcd = id % 8, slot = id / 8;
@@ -229,6 +234,7 @@ __global__ __launch_bounds__(256) void k_fp4_tiles(LinearArgs a) {
 
   u32x4 q[NT];
   uint32_t sc[NT];
+  // cached loads: the blocks of other rows read the same weights (256 rows: 50 us, 54 past the cache)
   auto load_w = [&](int kc) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -237,12 +243,12 @@ __global__ __launch_bounds__(256) void k_fp4_tiles(LinearArgs a) {
       const uint32_t oc = (uint32_t)row * cb + k / 2, os = (uint32_t)row * sb + k / G;
       if constexpr (ODD) {
         const bool in2 = in && k + 16 < a.K;
-        const u32x2 lo = load8(rc, in ? oc : kBeyond, 0), hi = load8(rc, in2 ? oc + 8 : kBeyond, 0);
+        const u32x2 lo = load8<kReuse>(rc, in ? oc : kBeyond, 0), hi = load8<kReuse>(rc, in2 ? oc + 8 : kBeyond, 0);
         q[t] = u32x4{lo.x, lo.y, hi.x, hi.y};
-        sc[t] = load1(rs, in ? os : kBeyond, 0) | load1(rs, in2 ? os + 1 : kBeyond, 0) << 8;
+        sc[t] = load1<kReuse>(rs, in ? os : kBeyond, 0) | load1<kReuse>(rs, in2 ? os + 1 : kBeyond, 0) << 8;
       } else {
-        q[t] = load16(rc, in ? oc : kBeyond, 0);
-        sc[t] = FMT == kMx ? load1(rs, in ? os : kBeyond, 0) : load2(rs, in ? os : kBeyond, 0);
+        q[t] = load16<kReuse>(rc, in ? oc : kBeyond, 0);
+        sc[t] = FMT == kMx ? load1<kReuse>(rs, in ? os : kBeyond, 0) : load2<kReuse>(rs, in ? os : kBeyond, 0);
       }
     }
   };
@@ -250,23 +256,15 @@ __global__ __launch_bounds__(256) void k_fp4_tiles(LinearArgs a) {
   auto load_x = [&](int kc) {
 #pragma unroll
     for (int i = 0; i < XL; ++i) {
-      const int e = threadIdx.x + i * 256, m = min(m0 + e / (kChunk / 8), a.M - 1), k = kc + e % (kChunk / 8) * 8;
+      const int e = tid + i * T, m = min(m0 + e / (kChunk / 8), a.M - 1), k = kc + e % (kChunk / 8) * 8;
       xr[i] = u32x4{0, 0, 0, 0};
-      if (k < a.K) {
-        const uint16_t* p = a.x + (int64_t)m * a.ldx + k;
-        if (a.vec) {
-          xr[i] = *reinterpret_cast<const u32x4*>(p);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) xr[i][j] = p[2 * j] | (uint32_t)p[2 * j + 1] << 16;
-        }
-      }
+      if (k < a.K) xr[i] = load_x16(a.x + (int64_t)m * a.ldx + k);
     }
   };
   auto put_x = [&](uint8_t* buf) {
 #pragma unroll
     for (int i = 0; i < XL; ++i) {
-      const int e = threadIdx.x + i * 256;
+      const int e = tid + i * T;
       uint8_t* p = buf + e / (kChunk / 8) * kRow + e % (kChunk / 8) * 16;
       if constexpr (P == 1) {
         *reinterpret_cast<u32x4*>(p) = xr[i];
@@ -293,12 +291,13 @@ __global__ __launch_bounds__(256) void k_fp4_tiles(LinearArgs a) {
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[i][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  load_x(0);
-  load_w(0);
+  // group kg takes every KS-th chunk; behind the last one it multiplies zeros
+  load_x(kg * kChunk);
+  load_w(kg * kChunk);
   put_x(lds);
   __syncthreads();
   int buf = 0;
-  for (int kc = 0; kc < a.K; kc += kChunk) {
+  for (int kc = kg * kChunk; kc - kg * kChunk < a.K; kc += KS * kChunk) {
     u32x4 cq[NT];
     f32x2 cs[NT];
 #pragma unroll
@@ -306,10 +305,10 @@ __global__ __launch_bounds__(256) void k_fp4_tiles(LinearArgs a) {
       cq[t] = q[t];
       cs[t] = lane_scales<FMT>(sc[t]);
     }
-    const bool more = kc + kChunk < a.K;
+    const bool more = kc - kg * kChunk + KS * kChunk < a.K;
     if (more) {
-      load_x(kc + kChunk);
-      load_w(kc + kChunk);
+      load_x(kc + KS * kChunk);
+      load_w(kc + KS * kChunk);
     }
     const uint8_t* xb = lds + buf * (P * kPlane) + r * kRow + g * 64;
 #pragma unroll
@@ -330,6 +329,25 @@ __global__ __launch_bounds__(256) void k_fp4_tiles(LinearArgs a) {
     __syncthreads();
     buf ^= 1;
   }
+  if constexpr (KS > 1) {
+    // the groups' sums in group order; the loop's last barrier has freed the chunks
+    static_assert((KS - 1) * MT * NT * 16 * T <= KS * 2 * P * kPlane, "the sums fit where the chunks were");
+    f32x4* part = reinterpret_cast<f32x4*>(lds_all);
+    if (kg) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) part[(((kg - 1) * MT + i) * NT + t) * T + tid] = acc[i][t];
+    }
+    __syncthreads();
+    if (kg) return;
+#pragma unroll
+    for (int o = 0; o < KS - 1; ++o)
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[i][t] += part[((o * MT + i) * NT + t) * T + tid];
+  }
   const float gs = a.gs ? *a.gs : 1.0f;
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -346,22 +364,37 @@ __global__ __launch_bounds__(256) void k_fp4_tiles(LinearArgs a) {
   }
 }
 
-template <int FMT, bool ODD, bool HALF, int BM, int NT>
+template <int FMT, bool ODD, bool HALF, int BM, int NT, int WN, int KS>
 hipError_t launch_tiles(LinearArgs a, hipStream_t st) {
   constexpr int P = HALF && FMT == kMx ? 2 : 1;
   a.mblocks = (a.M + BM - 1) / BM;
-  const long blocks = (long)a.mblocks * ((a.N + 64 * NT - 1) / (64 * NT));
+  const long blocks = (long)a.mblocks * ((a.N + 16 * NT * WN - 1) / (16 * NT * WN));
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((k_fp4_tiles<FMT, ODD, HALF, BM, NT>), dim3((unsigned)blocks), dim3(256),
-                     2 * P * BM * (kChunk * 2 + 16), st, a);
+  hipLaunchKernelGGL((k_fp4_tiles<FMT, ODD, HALF, BM, NT, WN, KS>), dim3((unsigned)blocks), dim3(64 * WN * KS),
+                     KS * 2 * P * BM * (kChunk * 2 + 16), st, a);
   return hipGetLastError();
 }
 
+// The smallest tiles that give each of the 256 compute units at most one block: a
+// compute unit's time is that of its blocks' longest chain of chunks, which more
+// units and more shares of K shorten, while larger tiles read and widen less.
+// Measured, us, bf16 NVFP4 4096 x 4096 (16x16 / 16x32 / 32x32 / 32x64 / 64x64 /
+// 64x128 / 128x128): 16 rows 7.5 / 9.2 / 10.5 / 14.5 / - / - / -, 64 rows
+// 15 / 13.7 / 11.3 / 15.0 / 20 / 31 / -, 256 rows - / - / - / 23.8 / 20.8 / 31 / -,
+// 1024 rows - / - / - / 92 / 62 / 54 / 70, 4096 rows - / - / - / 344 / 297 / 194 / 179.
 template <int FMT, bool ODD, bool HALF>
 hipError_t by_count(const LinearArgs& a, hipStream_t st) {
-  if (a.M <= 16) return rows_by_count<FMT, ODD, HALF>(a, st);
-  if (a.M <= 32) return launch_tiles<FMT, ODD, HALF, 32, 1>(a, st);
-  return launch_tiles<FMT, ODD, HALF, 64, 2>(a, st);
+  constexpr bool kTwo = HALF && FMT == kMx;        // operand in two parts: twice the LDS
+  const auto tiles = [&](int bm, int bn) { return (int64_t)((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
+  if (a.M <= 4) return rows_by_count<FMT, ODD, HALF>(a, st);
+  if (tiles(16, 16) <= 256) return launch_tiles<FMT, ODD, HALF, 16, 1, 1, 8>(a, st);
+  if (a.M <= 16 || tiles(16, 32) <= 256) return launch_tiles<FMT, ODD, HALF, 16, 1, 2, 8>(a, st);
+  if (tiles(32, 32) <= 256) return launch_tiles<FMT, ODD, HALF, 32, 1, 2, kTwo ? 4 : 8>(a, st);
+  if (a.M <= 32 || tiles(32, 64) <= 256) return launch_tiles<FMT, ODD, HALF, 32, 1, 4, 4>(a, st);
+  if (tiles(64, 64) <= 512) return launch_tiles<FMT, ODD, HALF, 64, 1, 4, 2>(a, st);
+  if constexpr (!kTwo)
+    if (tiles(64, 128) >= 2048) return launch_tiles<FMT, ODD, HALF, 128, 2, 4, 1>(a, st);
+  return launch_tiles<FMT, ODD, HALF, 64, 2, 4, 1>(a, st);
 }
 
 template <bool HALF>
@@ -399,7 +432,6 @@ extern "C" sc_status fp4_linear(const sc_fp4_matrix* w, const void* d_x, int32_t
   a.N = w->rows;
   a.K = w->cols;
   a.out = y_type;
-  a.vec = (uintptr_t)d_x % 16 == 0 && ldx % 8 == 0;
   a.M = M;
   a.x = static_cast<const uint16_t*>(d_x);
   a.y = d_y;

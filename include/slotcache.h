@@ -385,9 +385,11 @@ SC_API sc_status fp4_dequantize(const sc_fp4_matrix* w, void* d_w, int32_t w_typ
 
 /* y = x W^T + bias: x [M][w->cols] of bf16 or fp16 (row stride ldx elements), y
  * [M][w->rows] (row stride ldy, type y_type), bias fp32 [w->rows] or NULL.
- * Products of x with the codes are exact, a group's sum is scaled in fp32, and
- * y is rounded once.  |x| has to stay below 2^121 for the group sums to be
- * finite.  Any M >= 0; rows are independent of each other.  y must not overlap
+ * Products of x with the codes (up to 4 rows) or with the codes times their group
+ * scales (more rows) are exact, sums are fp32, and y is rounded once.  For the
+ * sums to be finite |x| has to stay below 2^121, and a code times its group scale
+ * below 2^128, as every matrix from fp4_quantize has it.  Any M >= 0; a NaN or
+ * infinity in a row of x or of W stays in its row or column of y.  y must not overlap
  * x or the weights.  Asynchronous on `stream`, whose device is current; no
  * workspace, no allocation; can be captured. */
 SC_API sc_status fp4_linear(const sc_fp4_matrix* w, const void* d_x, int32_t x_type, int64_t ldx, int32_t M,

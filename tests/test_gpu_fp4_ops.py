@@ -192,6 +192,50 @@ def test_linear(M, N, K, fmt, x_type):
         assert (np.abs(y - want) <= tol).all(), (out, np.abs((y - want) / tol).max())
 
 
+# each shape lies in another of the ranges that choose a tile size
+TILED = [(5, 4096, 144), (16, 4200, 1040), (20, 5000, 208), (64, 2050, 2064), (128, 2100, 1040), (30, 8300, 96),
+         (130, 4100, 272), (300, 6600, 144), (1100, 14500, 48)]
+
+
+@pytest.mark.parametrize("x_type", ["bf16", "fp16"])
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("M,N,K", TILED)
+def test_linear_tiles(M, N, K, fmt, x_type):
+    torch = torch_cuda()
+    ops = _ops()
+    if fmt == "mxfp4":
+        K = (K + 31) // 32 * 32
+    log("linear tiles", M, N, K, fmt, x_type)
+    q, w = _random_fp4(torch, N, K, fmt, M + N)
+    g = torch.Generator().manual_seed(K)
+    big = torch.randn(M + 1, K + 8, generator=g).to(getattr(torch, TYPES[x_type]))
+    x = big[1:, 3:3 + K]                         # rows that start at odd elements
+    y = ops.fp4_linear(big.cuda()[1:, 3:3 + K], q, out_dtype=torch.float32).double().cpu()
+    wt = torch.tensor(w).t()
+    want, mag = x.double() @ wt, x.double().abs() @ wt.abs()
+    # a matrix instruction adds 32 products to a sum, the groups of a block add 8; the scale of the matrix
+    tol = (32 + K / 32 + 8 + 1) * 2.0 ** -24 * mag + 1e-37
+    assert ((y - want).abs() <= tol).all(), ((y - want).abs() / tol).max()
+
+
+@pytest.mark.parametrize("M", [1, 4, 5, 40])
+def test_linear_mx_smallest_and_largest_scales(M):
+    """Weights down to 2^-128, below the smallest normal bf16 and fp32, and up to 6 * 2^125."""
+    torch = torch_cuda()
+    ops = _ops()
+    rng = np.random.default_rng(M)
+    N, K = 48, 256
+    codes = rng.integers(0, 16, (N, K)).astype(np.uint8)
+    for byte, size in ((0, 2.0 ** 100), (1, 2.0 ** 100), (252, 2.0 ** -60)):
+        sb = np.full((N, K // 32), byte, np.uint8)
+        q = ops.FP4Weight(torch.tensor(fp4.pack(codes)).cuda(), torch.tensor(sb).cuda(), None, "mxfp4")
+        x = torch.tensor(rng.standard_normal((M, K)) * size, dtype=torch.bfloat16).cuda()
+        w = fp4.values(codes, sb, "mxfp4", None)
+        y = _np64(ops.fp4_linear(x, q, out_dtype=torch.float32))
+        want, tol = _np64(x) @ w.T, _bound(_np64(x), w, torch.float32, torch, _terms(K))
+        assert (np.abs(y - want) <= tol).all(), byte
+
+
 @pytest.mark.parametrize("M", [1, 4, 13, 40])
 def test_linear_strides_and_rows_beside_the_output(M):
     torch = torch_cuda()
