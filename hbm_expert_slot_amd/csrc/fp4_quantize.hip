@@ -7,10 +7,15 @@
 // whole numbers and a neighbour would be off by half of its value, so a
 // quotient of rounded numbers next to a border is settled in fp64.
 //
-// Bound: HBM.  The max and the codes need one pass each; the second finds a
-// matrix of up to 256 MB in the memory-side cache.
+// The max and the codes need one pass each; the second finds a matrix of up to
+// 256 MB in the memory-side cache.  6144 x 4096 bf16: max 19 us (2.6 TB/s from
+// HBM, which more loads under way, wider blocks or fewer instructions leave as it
+// is), codes 21 us (vector instructions: 32 products, 16 conversions and an fp64
+// quotient per 16 elements), reading back 16.5 us (3.9 TB/s).
 #include "fp4_device.h"
 #include "internal.h"
+
+#include <type_traits>
 
 namespace sc {
 namespace {
@@ -18,6 +23,10 @@ namespace {
 using namespace fp4;
 
 constexpr int kThreads = 256;
+constexpr unsigned kGrid = 1280; // blocks of k_fp4_codes at most: what the card holds at a time (one group per thread: 32 us)
+constexpr unsigned kMaxBlocks = 512;
+static_assert(kMaxBlocks * 4 <= SC_FP4_QUANT_WORKSPACE_BYTES, "one maximum per block");
+constexpr int kMaxThreads = 512, kAhead = 4;   // k_fp4_max; pieces of a thread whose loads are under way together
 
 struct QuantArgs {
   const void* w;
@@ -30,46 +39,31 @@ struct QuantArgs {
   uint32_t n16;          // groups of 16 elements in the matrix
   uint32_t per_row;      // groups of 16 per row
   int K;
-  int vec;
 };
 
-// Sixteen elements of one row as fp32.
+// Sixteen elements of one row as they are in memory, which need not be aligned to
+// more than themselves, and as fp32.
 template <typename T>
-__device__ __forceinline__ void load_row16(const void* w, int64_t off, int vec, float (&v)[16]) {
-  if constexpr (sizeof(T) == 4) {
-    const float* p = static_cast<const float*>(w) + off;
-    if (vec) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const f32x4 t = *reinterpret_cast<const f32x4*>(p + 4 * i);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[4 * i + e] = t[e];
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = p[i];
-    }
-  } else {
-    typedef __attribute__((ext_vector_type(8))) T T8;
-    const T* p = static_cast<const T*>(w) + off;
-    if (vec) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const T8 t = *reinterpret_cast<const T8*>(p + 8 * i);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[8 * i + e] = (float)t[e];
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = (float)p[i];
-    }
+struct Raw16 {
+  u32x4 q[sizeof(T)];
+};
+template <typename T>
+__device__ __forceinline__ Raw16<T> load16_of(const QuantArgs& a, uint32_t i) {
+  int64_t off = (int64_t)i * 16;
+  if (a.ldw != a.K) {
+    const uint32_t row = i / a.per_row;
+    off = (int64_t)row * a.ldw + (i - row * a.per_row) * 16;
   }
+  Raw16<T> r;
+  __builtin_memcpy(&r, static_cast<const T*>(a.w) + off, sizeof r);
+  return r;
 }
-
-// |w| as bits, which order as the values do; infinities and NaN count as 0.
-__device__ __forceinline__ uint32_t finite_bits(float v) {
-  const uint32_t b = __float_as_uint(v) & 0x7FFFFFFFu;
-  return b < 0x7F800000u ? b : 0u;
+template <typename T>
+__device__ __forceinline__ void to_f32(const Raw16<T>& r, float (&v)[16]) {
+  typedef __attribute__((ext_vector_type(16 / sizeof(T)))) T TV;
+  constexpr int W = 16 / sizeof(T);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = (float)__builtin_bit_cast(TV, r.q[i / W])[i % W];
 }
 
 __device__ __forceinline__ uint32_t wave_max(uint32_t m) {
@@ -78,22 +72,61 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t m) {
   return m;
 }
 
+// Max of the magnitudes of 16 bytes as they order in memory's type, infinities and NaN too.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void k_fp4_max(QuantArgs a) {
-  uint32_t m = 0;
-  const uint32_t stride = gridDim.x * kThreads;
-  for (uint64_t i = blockIdx.x * kThreads + threadIdx.x; i < a.n16; i += stride) {
-    const uint32_t row = (uint32_t)i / a.per_row, c = (uint32_t)i - row * a.per_row;
-    float v[16];
-    load_row16<T>(a.w, (int64_t)row * a.ldw + c * 16, a.vec, v);
+__device__ __forceinline__ uint32_t top_bits(u32x4 q) {
+  if constexpr (sizeof(T) == 4) {
+    return max(max(q.x & 0x7FFFFFFFu, q.y & 0x7FFFFFFFu), max(q.z & 0x7FFFFFFFu, q.w & 0x7FFFFFFFu));
+  } else {
+    typedef __attribute__((ext_vector_type(2))) uint16_t u16x2;
+    u16x2 m = {0, 0};
 #pragma unroll
-    for (int e = 0; e < 16; ++e) m = max(m, finite_bits(v[e]));
+    for (int i = 0; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, q[i] & 0x7FFF7FFFu));
+    return max(m.x, m.y);
   }
-  __shared__ uint32_t part[kThreads / 64];
+}
+
+// Every wavefront reads 1 KB pieces, kAhead of them under way at a time.
+template <typename T>
+__global__ __launch_bounds__(kMaxThreads) void k_fp4_max(QuantArgs a) {
+  constexpr uint32_t kInf = sizeof(T) == 4 ? 0x7F800000u : std::is_same_v<T, __bf16> ? 0x7F80u : 0x7C00u;
+  constexpr int W = 16 / sizeof(T);          // elements of a piece
+  const uint64_t n = (uint64_t)a.n16 * sizeof(T), stride = (uint64_t)gridDim.x * kMaxThreads;
+  uint32_t m = 0;
+  for (uint64_t i = (uint64_t)blockIdx.x * kMaxThreads + threadIdx.x; i < n; i += kAhead * stride) {
+    u32x4 q[kAhead];          // behind the last piece: that one again
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const uint64_t j = min(i + u * stride, n - 1);
+      int64_t off = (int64_t)j * W;
+      if (a.ldw != a.K) off += (int64_t)((uint32_t)(j / sizeof(T)) / a.per_row) * (a.ldw - a.K);
+      __builtin_memcpy(&q[u], static_cast<const T*>(a.w) + off, 16);
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      uint32_t t = top_bits<T>(q[u]);
+      if (t < kInf) {
+        m = max(m, t);
+      } else {
+        const uint32_t mask = sizeof(T) == 4 ? 0x7FFFFFFFu : 0x7FFFu;
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          t = q[u][e * sizeof(T) / 4] >> (e * sizeof(T) % 4 * 8) & mask;
+          m = max(m, t < kInf ? t : 0u);
+        }
+      }
+    }
+  }
+  __shared__ uint32_t part[kMaxThreads / 64];
   m = wave_max(m);
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
   __syncthreads();
-  if (threadIdx.x == 0) a.partial[blockIdx.x] = max(max(part[0], part[1]), max(part[2], part[3]));
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int i = 1; i < kMaxThreads / 64; ++i) m = max(m, part[i]);
+    typedef std::conditional_t<sizeof(T) == 4, uint32_t, uint16_t> Bits;
+    a.partial[blockIdx.x] = __float_as_uint((float)__builtin_bit_cast(T, (Bits)m));
+  }
 }
 
 // E4M3 byte nearest to t >= 0 (exact quotient up to fp64 rounding, which cannot
@@ -124,24 +157,9 @@ __device__ __forceinline__ uint32_t e2m1_exact(float a, double d) {
 // One thread takes 16 elements: an NVFP4 group, or half of an MXFP4 group (the
 // halves trade their maxima with the neighbouring lane).
 template <typename T, int FMT>
-__global__ __launch_bounds__(kThreads) void k_fp4_codes(QuantArgs a) {
-  float gs = 1.0f;
-  if constexpr (FMT == kNv) {
-    if (a.partial) {
-      uint32_t m = 0;
-      for (int i = threadIdx.x & 63; i < a.nparts; i += 64) m = max(m, a.partial[i]);
-      gs = __uint_as_float(wave_max(m)) / 2688.0f;
-      if (!(gs > 0.0f)) gs = 1.0f;   // a matrix of zeros
-      if (blockIdx.x == 0 && threadIdx.x == 0) *a.gs = gs;
-    } else {
-      gs = *a.gs;
-    }
-  }
-  const uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (i >= a.n16) return;
-  const uint32_t row = (uint32_t)i / a.per_row, c = (uint32_t)i - row * a.per_row;
+__device__ __forceinline__ void codes_of(const QuantArgs& a, uint64_t i, const Raw16<T>& raw, float gs) {
   float v[16];
-  load_row16<T>(a.w, (int64_t)row * a.ldw + c * 16, a.vec, v);
+  to_f32(raw, v);
   uint32_t top = 0;
 #pragma unroll
   for (int e = 0; e < 16; ++e) top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
@@ -199,11 +217,37 @@ __global__ __launch_bounds__(kThreads) void k_fp4_codes(QuantArgs a) {
   else if ((i & 1) == 0) a.scales[i >> 1] = (uint8_t)sbyte;
 }
 
+// A thread goes on to the next group of its grid, whose load is under way while it
+// works on this one; a wavefront joins the per-block maxima once, not per group.
+template <typename T, int FMT>
+__global__ __launch_bounds__(kThreads) void k_fp4_codes(QuantArgs a) {
+  const uint64_t stride = (uint64_t)gridDim.x * kThreads;
+  uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
+  Raw16<T> raw = load16_of<T>(a, (uint32_t)min(i, (uint64_t)a.n16 - 1));
+  float gs = 1.0f;
+  if constexpr (FMT == kNv) {
+    if (a.partial) {
+      uint32_t m = 0;
+      for (int p = threadIdx.x & 63; p < a.nparts; p += 64) m = max(m, a.partial[p]);
+      gs = __uint_as_float(wave_max(m)) / 2688.0f;
+      if (!(gs > 0.0f)) gs = 1.0f;   // a matrix of zeros
+      if (blockIdx.x == 0 && threadIdx.x == 0) *a.gs = gs;
+    } else {
+      gs = *a.gs;
+    }
+  }
+  for (; i < a.n16; i += stride) {
+    const Raw16<T> next = load16_of<T>(a, (uint32_t)min(i + stride, (uint64_t)a.n16 - 1));
+    codes_of<T, FMT>(a, i, raw, gs);
+    raw = next;
+  }
+}
+
 // ---- reading back ------------------------------------------------------------
-// A thread writes 16 bytes: coalesced stores are what the time goes to.
+// A thread writes 16 bytes at a time, so that a wavefront's stores are one piece.
 template <int FMT, typename T>
 __global__ __launch_bounds__(kThreads) void k_fp4_values(const uint8_t* codes, const uint8_t* scales, const float* gsp,
-                                                         T* out, int64_t ld, uint64_t n, uint32_t per_row, int vec) {
+                                                         T* out, int64_t ld, uint64_t n, uint32_t K) {
   constexpr int W = 16 / sizeof(T), G = FMT == kNv ? 16 : 32;
   typedef __attribute__((ext_vector_type(W))) T TW;
   const uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
@@ -225,25 +269,24 @@ __global__ __launch_bounds__(kThreads) void k_fp4_values(const uint8_t* codes, c
     v[e] = t.x * s * gs;
     v[e + 1] = t.y * s * gs;
   }
-  const uint64_t row = i / per_row;
-  T* p = out + (int64_t)row * ld + (int64_t)(i - row * per_row) * W;
+  int64_t off = (int64_t)i * W;
+  if (ld != K) {
+    const uint32_t g16 = (uint32_t)(i * W / 16), row = g16 / (K / 16);     // fits: check_fp4_matrix
+    off += (int64_t)row * (ld - K);
+  }
   TW o;
 #pragma unroll
   for (int e = 0; e < W; ++e) o[e] = (T)v[e];
-  if (vec) {
-    *reinterpret_cast<TW*>(p) = o;
-  } else {
-#pragma unroll
-    for (int e = 0; e < W; ++e) p[e] = o[e];
-  }
+  __builtin_memcpy(out + off, &o, sizeof o);
 }
 
+unsigned blocks_of(uint64_t n) { return (unsigned)((n + kThreads - 1) / kThreads); }
 int type_size(int t) { return t == SC_DTYPE_F32 ? 4 : 2; }
 
 template <typename T>
 hipError_t run_quantize(const QuantArgs& a, int fmt, hipStream_t st) {
-  if (a.partial) hipLaunchKernelGGL((k_fp4_max<T>), dim3(a.nparts), dim3(kThreads), 0, st, a);
-  const unsigned grid = (a.n16 + kThreads - 1) / kThreads;
+  if (a.partial) hipLaunchKernelGGL((k_fp4_max<T>), dim3(a.nparts), dim3(kMaxThreads), 0, st, a);
+  const unsigned blocks = blocks_of(a.n16), grid = blocks < kGrid ? blocks : kGrid;
   if (fmt == SC_FP4_NV) hipLaunchKernelGGL((k_fp4_codes<T, kNv>), dim3(grid), dim3(kThreads), 0, st, a);
   else hipLaunchKernelGGL((k_fp4_codes<T, kMx>), dim3(grid), dim3(kThreads), 0, st, a);
   return hipGetLastError();
@@ -253,16 +296,15 @@ template <typename T>
 hipError_t run_values(const sc_fp4_matrix* m, void* out, int64_t ld, hipStream_t st) {
   constexpr int W = 16 / sizeof(T);
   const uint64_t n = (uint64_t)m->rows * m->cols / W;
-  const unsigned grid = (unsigned)((n + kThreads - 1) / kThreads);
-  const int vec = (uintptr_t)out % 16 == 0 && ld % W == 0;
+  const unsigned grid = blocks_of(n);
   const uint8_t* c = static_cast<const uint8_t*>(m->d_codes);
   const uint8_t* s = static_cast<const uint8_t*>(m->d_scales);
   if (m->format == SC_FP4_NV)
     hipLaunchKernelGGL((k_fp4_values<kNv, T>), dim3(grid), dim3(kThreads), 0, st, c, s, m->d_global_scale,
-                       static_cast<T*>(out), ld, n, (uint32_t)(m->cols / W), vec);
+                       static_cast<T*>(out), ld, n, (uint32_t)m->cols);
   else
     hipLaunchKernelGGL((k_fp4_values<kMx, T>), dim3(grid), dim3(kThreads), 0, st, c, s, m->d_global_scale,
-                       static_cast<T*>(out), ld, n, (uint32_t)(m->cols / W), vec);
+                       static_cast<T*>(out), ld, n, (uint32_t)m->cols);
   return hipGetLastError();
 }
 
@@ -312,11 +354,11 @@ sc_status fp4_quantize(const void* d_w, int32_t w_type, int64_t ldw, const sc_fp
   a.K = out->cols;
   a.per_row = (uint32_t)out->cols / 16;
   a.n16 = (uint32_t)out->rows * a.per_row;
-  a.vec = (uintptr_t)d_w % 16 == 0 && ldw * size % 16 == 0;
   if (nv && !scale_given) {
     a.partial = static_cast<uint32_t*>(d_workspace);
-    const uint32_t blocks = (a.n16 + kThreads - 1) / kThreads;
-    a.nparts = (int)(blocks < SC_FP4_QUANT_WORKSPACE_BYTES / 4 ? blocks : SC_FP4_QUANT_WORKSPACE_BYTES / 4);
+    // one block per 16 KB until the card is full
+    const uint64_t blocks = ((uint64_t)a.n16 * 16 * size + 16383) / 16384;
+    a.nparts = (int)(blocks < kMaxBlocks ? blocks : kMaxBlocks);
   }
   const hipStream_t st = static_cast<hipStream_t>(stream);
   const hipError_t e = w_type == SC_DTYPE_F32   ? run_quantize<float>(a, out->format, st)
