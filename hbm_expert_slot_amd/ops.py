@@ -15,6 +15,10 @@ _FORMAT = {"nvfp4": B.SC_FP4_NV, "mxfp4": B.SC_FP4_MX}
 GROUP = {"nvfp4": 16, "mxfp4": 32}
 
 
+# the handle alone: torch.cuda.current_stream also makes an object, which costs 1.8 us
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 class _On:
     """Makes `device`, and `stream` if one is given, current for the calls
     inside, and yields the raw stream: what a call allocates then belongs to
@@ -34,7 +38,7 @@ class _On:
             self.guard = torch.cuda.device(self.device)
         if self.guard is not None:
             self.guard.__enter__()
-        return torch.cuda.current_stream(self.device).cuda_stream
+        return _raw_stream(self.device.index)
 
     def __exit__(self, *exc):
         if self.guard is not None:
