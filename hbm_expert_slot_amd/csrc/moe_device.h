@@ -424,7 +424,8 @@ __device__ __forceinline__ void abandon(const MoeArgs& a) {
 
 // Control words of the one-row kernel (moe_one.hip).
 constexpr int kOneWords = 1024 + (2 * kShards + 3) * kLine;
-hipError_t launch_moe_one(const MoeArgs& a, hipStream_t st);
+// *fits: the device can hold the kernel's shares; if not, nothing is launched.
+hipError_t launch_moe_one(const MoeArgs& a, hipStream_t st, bool* fits);
 
 }  // namespace moe
 }  // namespace sc

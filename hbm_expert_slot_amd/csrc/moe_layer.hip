@@ -4,12 +4,12 @@
 //
 // Bound: HBM, by the bytes of the experts picked.  Between the products there
 // is nothing to compute, only data to hand over, so the layer is one kernel
-// whose blocks go through four phases of tasks:
-//   router tiles | shared gate/up tiles | routed gate/up tiles | down tiles
+// whose blocks go through five phases of tasks:
+//   router tiles | picks of a row | shared gate/up tiles | routed gate/up tiles | down tiles
 // Blocks take a phase's tasks from counters and go on to the next phase when
 // none is left to take.  A task waits for tasks of earlier phases only: a
-// routed gate/up tile for the picks (made by the block that ends the last
-// router tile), a down tile for all h of its expert.  When a block waits, every
+// row's picks for its logits, a routed gate/up tile for all picks (which every
+// block groups by expert for itself), a down tile for all h of its expert.  When a block waits, every
 // task of the earlier phases is held by a block that runs, so every wait ends,
 // whatever part of the grid is resident.  A down tile starts its weight loads
 // before it waits.
@@ -714,8 +714,14 @@ sc_status moe_layer_forward(const sc_moe_config* c, const sc_moe_weights* w, voi
   a.vec = (uintptr_t)d_x % 16 == 0 && ldx % 8 == 0;
   a.scale = c->routed_scale;
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  if (M == 1) a.ctl += kLayerWords;
-  const hipError_t e = M == 1 ? launch_moe_one(a, st) : M <= 4 ? launch_moe<4>(a, st) : launch_moe<16>(a, st);
+  hipError_t e;
+  bool done = false;
+  if (M == 1) {
+    MoeArgs one = a;
+    one.ctl += kLayerWords;
+    e = launch_moe_one(one, st, &done);
+  }
+  if (!done) e = M <= 4 ? launch_moe<4>(a, st) : launch_moe<16>(a, st);
   return e == hipSuccess ? SC_OK : hip_fail(e, "moe_layer_forward launch");
 }
 

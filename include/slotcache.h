@@ -444,7 +444,9 @@ SC_API sc_status moe_layer_prepare(const sc_moe_config* cfg, void* d_workspace, 
  * all when it holds a NaN.  M == 0 does nothing.  Asynchronous on `stream`,
  * whose device is current; no allocation; can be captured.  Calls that share a
  * workspace must be ordered (one stream, or streams that the caller orders);
- * y must not overlap x. */
+ * y must not overlap x.  Blocks wait for each other's results; a wait that lasts
+ * over a second (only calls that break that order can do this) gives the call up: y
+ * is NaN then, and moe_layer_prepare has to be called before the next use. */
 SC_API sc_status moe_layer_forward(const sc_moe_config* cfg, const sc_moe_weights* w, void* d_workspace,
                                    const uint16_t* d_x, int64_t ldx, int32_t M, void* d_y, int32_t y_type,
                                    int64_t ldy, int32_t* d_ids, float* d_weights, void* stream);

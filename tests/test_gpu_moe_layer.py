@@ -103,6 +103,91 @@ def test_layer(c):
     assert torch.equal(a, b)
 
 
+# one row: many picks, h longer than LDS holds at a time, ragged steps, shared and routed sizes far apart
+ONE = [
+    dict(M=1, H=256, I=2048, E=40, k=32), dict(M=1, H=192, I=1088, E=33, k=32, Is=64, score="sigmoid"),
+    dict(M=1, H=64, I=64, E=1024, k=32), dict(M=1, H=8256, I=64, E=6, k=2, Is=4160), dict(M=1, H=32768, I=64, E=2, k=2),
+    dict(M=1, H=64, I=32768, E=2, k=1), dict(M=1, H=64, I=64, E=2, k=1, Is=32768), dict(M=1, H=576, I=576, E=1000, k=1),
+    dict(M=1, H=4160, I=1600, E=10, k=9, Is=576, score="sigmoid", scale=0.5),
+]
+
+
+@pytest.mark.parametrize("c", ONE, ids=lambda c: "-".join("%s%s" % (k, v) for k, v in c.items()))
+def test_one_row(c):
+    torch = torch_cuda()
+    log("moe layer, one row", c)
+    case = Case(**c, max_rows=2)
+    want = case.want()
+    log("  rel L2 %.2e" % case.check(*case.run(), want=want))
+    case.check(*case.run(dtype=torch.bfloat16), want=want)
+    a = case.run()[0]
+    for _ in range(3):
+        assert torch.equal(case.run()[0], a)
+
+
+def test_one_row_beside_the_output_and_with_nan():
+    torch = torch_cuda()
+    case = Case(1, 576, 192, 20, 3, Is=64)
+    want, ids0, _ = case.run()
+    out = torch.full((3, 600), 9.0, device="cuda")
+    case.layer.forward(case.tx, out=out[1:2, 5:581])
+    assert torch.equal(out[1:2, 5:581], want)
+    out[1:2, 5:581] = 9.0
+    assert (out == 9.0).all()
+    for bad in (float("nan"), float("inf")):
+        x = case.tx.clone()
+        x[0, 3] = bad
+        y, ids, _ = case.run(x)
+        assert not torch.isfinite(y).any()
+        assert len(set(ids[0].tolist())) == 3 and int(ids.min()) >= 0 and int(ids.max()) < 20
+    y, ids, _ = case.run()
+    assert torch.equal(y, want) and torch.equal(ids, ids0)
+
+
+@pytest.mark.parametrize("M", [1, 2, 16])
+def test_replayed(M):
+    """Two graphs of one layer, replayed in turn with eager calls of other row counts between them."""
+    torch = torch_cuda()
+    case = Case(M, 512, 576, 40, 8, Is=192)
+    case.layer.forward(case.tx)
+    graphs, outs, xs = [], [], []
+    for i in range(2):
+        xs.append(torch.empty_like(case.tx))
+        outs.append(torch.empty(M, 512, device="cuda"))
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            case.layer.forward(xs[i], out=outs[i])
+    other = torch.randn(3, 512, device="cuda").to(torch.bfloat16)
+    for r in range(4):
+        for i in range(2):
+            xs[i].copy_(torch.randn(M, 512, device="cuda").to(torch.bfloat16))
+            eager = case.layer.forward(xs[i])
+            case.layer.forward(other[:1 + (r + i) % 3])
+            outs[i].zero_()
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert torch.equal(outs[i], case.layer.forward(xs[i])), (r, i)
+
+
+def test_layers_of_one_row_and_of_many_at_once():
+    """Layers with workspaces of their own on three streams: none waits for blocks that another keeps out."""
+    torch = torch_cuda()
+    cases = [Case(1, 2048, 1024, 16, 8, Is=512, seed=1), Case(1, 2048, 1024, 16, 8, Is=512, seed=2),
+             Case(16, 1024, 512, 16, 4, seed=3)]
+    want = [c.run()[0] for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = [[], [], []]
+    for _ in range(20):
+        for i, (c, s) in enumerate(zip(cases, streams)):
+            outs[i].append(c.layer.forward(c.tx, stream=s))
+    torch.cuda.synchronize()
+    for i in range(3):
+        for y in outs[i]:
+            assert torch.equal(y, want[i]), i
+
+
 def test_sizes_of_the_configurations():
     """One row and sixteen rows at the inner sizes of the GLM-shaped layer, few experts."""
     torch_cuda()
