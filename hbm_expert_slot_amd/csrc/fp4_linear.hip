@@ -379,9 +379,11 @@ hipError_t launch_tiles(LinearArgs a, hipStream_t st) {
 // compute unit's time is that of its blocks' longest chain of chunks, which more
 // units and more shares of K shorten, while larger tiles read and widen less.
 // Measured, us, bf16 NVFP4 4096 x 4096 (16x16 / 16x32 / 32x32 / 32x64 / 64x64 /
-// 64x128 / 128x128): 16 rows 7.5 / 9.2 / 10.5 / 14.5 / - / - / -, 64 rows
-// 15 / 13.7 / 11.3 / 15.0 / 20 / 31 / -, 256 rows - / - / - / 23.8 / 20.8 / 31 / -,
-// 1024 rows - / - / - / 92 / 62 / 54 / 70, 4096 rows - / - / - / 344 / 297 / 194 / 179.
+// 64x128): 16 rows 7.5 / 9.2 / 10.5 / 14.5 / - / -, 64 rows 15 / 13.7 / 11.3 /
+// 15.0 / 20 / 31, 256 rows - / - / - / 23.8 / 20.8 / 31, 1024 rows - / - / - / 92 /
+// 62 / 54.  Two blocks of 64x64 share a unit.  Tiles of 128x192, which widen least,
+// pay from two blocks per unit on (6144 x 6144, 1024 rows: 256 blocks, 114 against
+// 107 with 64x128; 2048 rows: 163 against 218).
 template <int FMT, bool ODD, bool HALF>
 hipError_t by_count(const LinearArgs& a, hipStream_t st) {
   constexpr bool kTwo = HALF && FMT == kMx;        // operand in two parts: twice the LDS
@@ -393,7 +395,7 @@ hipError_t by_count(const LinearArgs& a, hipStream_t st) {
   if (a.M <= 32 || tiles(32, 64) <= 256) return launch_tiles<FMT, ODD, HALF, 32, 1, 4, 4>(a, st);
   if (tiles(64, 64) <= 512) return launch_tiles<FMT, ODD, HALF, 64, 1, 4, 2>(a, st);
   if constexpr (!kTwo)
-    if (tiles(64, 128) >= 2048) return launch_tiles<FMT, ODD, HALF, 128, 2, 4, 1>(a, st);
+    if (tiles(128, 192) >= 512) return launch_tiles<FMT, ODD, HALF, 128, 3, 4, 1>(a, st);
   return launch_tiles<FMT, ODD, HALF, 64, 2, 4, 1>(a, st);
 }
 

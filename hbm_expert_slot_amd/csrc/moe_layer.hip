@@ -29,6 +29,7 @@ constexpr int kWaves = kThreads / 64;
 static_assert(kWaves == kTileWaves, "a block does a router tile");
 constexpr int kMaxPk = kMaxTokens * kMaxTopK;
 constexpr int kUpRows = 16;        // rows of h per gate/up tile: a quad per wavefront
+constexpr int kTaskRounds = 2, kTaskTail = 8;   // see Tasks
 constexpr int kDownRows = 32;      // output rows per down tile: two quads per wavefront
 
 // Control words, zero between calls: the block that leaves last clears them.
@@ -457,11 +458,35 @@ __device__ __forceinline__ Taker taker(const MoeArgs& a, int phase, int n) {
   t.ask();
   return t;
 }
-// Tiles per task: few enough tasks that staging an expert's rows pays, enough that the blocks end together.
-__device__ __forceinline__ int tiles_per_task(int tiles) {
-  const int f = tiles / (6 * (int)gridDim.x);
-  return f < 1 ? 1 : f > 8 ? 8 : f;
-}
+// The tasks of U experts of `tiles` tiles each.  Several tiles of an expert are a
+// task where there are many, since a task stages its rows first; the last experts'
+// tasks are single tiles, so that the blocks end together.  8 rows of 8 picks of
+// 4096 x 2048 among 288: 225 us with single tiles throughout, 190 like this; 16
+// rows of 6144 x 2048 among 256: 444 with three tiles throughout, 442 like this.
+struct Tasks {
+  int tiles, f, per, many;      // tiles of an expert; of a task; tasks of an expert; experts cut so
+  __device__ __forceinline__ Tasks(int U, int tiles_) : tiles(tiles_) {
+    const int most = U * tiles / (kTaskRounds * (int)gridDim.x);
+    f = most < 1 ? 1 : most > 4 ? 4 : most;
+    per = (tiles + f - 1) / f;
+    many = f == 1 ? 0 : U - U / kTaskTail;
+  }
+  __device__ __forceinline__ int count(int U) const { return many * per + (U - many) * tiles; }
+  // Task t: its expert, first tile and the one behind its last.
+  __device__ __forceinline__ void at(int t, int& u, int& i0, int& i1) const {
+    if (t < many * per) {
+      u = t / per;
+      i0 = (t - u * per) * f;
+      i1 = min(i0 + f, tiles);
+    } else {
+      t -= many * per;
+      u = t / tiles;
+      i0 = t - u * tiles;
+      i1 = i0 + 1;
+      u += many;
+    }
+  }
+};
 
 template <int MAXR>
 __device__ __forceinline__ void run_phases(const MoeArgs& a, BlockLds<MAXR>& b, uint8_t* lds) {
@@ -507,24 +532,26 @@ __device__ __forceinline__ void run_phases(const MoeArgs& a, BlockLds<MAXR>& b, 
   const int U = group_picks<MAXR>(a, b, MAXR == 4 ? b.rows : reinterpret_cast<uint32_t*>(lds));
   if (U < 0) return;
   {
-    const int f = tiles_per_task(U * tu), per = (tu + f - 1) / f;
-    kr.n = U * per;
+    const Tasks tasks(U, tu);
+    kr.n = tasks.count(U);
     for (int t; (t = kr.next(&b.tick)) >= 0;) {
       kr.ask();
-      const int u = t / per, i0 = (t - u * per) * f, i1 = min(i0 + f, tu);
+      int u, i0, i1;
+      tasks.at(t, u, i0, i1);
       run_gateup<MAXR>(a, b, work_of(a, b, u, false), i0, i1, lds, x_there);
       post_h(a, u, i1 - i0, tu);
     }
   }
   {
     // the shared expert's h is there first
-    const int f = tiles_per_task(U * td), per = (td + f - 1) / f, first = ns * td;
-    Taker k = taker(a, kDown, first + U * per);
+    const Tasks tasks(U, td);
+    const int first = ns * td;
+    Taker k = taker(a, kDown, first + tasks.count(U));
     for (int t; (t = k.next(&b.tick)) >= 0;) {
       k.ask();
       const bool sh = t < first;
-      const int u = sh ? kMaxPk : (t - first) / per;
-      const int i0 = sh ? t : (t - first - u * per) * f, i1 = sh ? t + 1 : min(i0 + f, td);
+      int u = kMaxPk, i0 = t, i1 = t + 1;
+      if (!sh) tasks.at(t - first, u, i0, i1);
       if (!run_down<MAXR>(a, b, work_of(a, b, u, sh), i0, i1, lds)) return;
       stores_done();
       __syncthreads();

@@ -125,6 +125,21 @@ def test_one_row(c):
         assert torch.equal(case.run()[0], a)
 
 
+# so many tiles that a task takes two or four of an expert's, and numbers that these do not divide
+MANY = [
+    dict(M=16, H=4160, I=64, E=40, k=8), dict(M=12, H=8256, I=64, E=40, k=8, Is=64), dict(M=16, H=64, I=2048, E=40, k=8),
+    dict(M=9, H=128, I=4160, E=36, k=6, Is=128, score="sigmoid"), dict(M=4, H=12352, I=64, E=30, k=6),
+]
+
+
+@pytest.mark.parametrize("c", MANY, ids=lambda c: "-".join("%s%s" % (k, v) for k, v in c.items()))
+def test_many_tiles(c):
+    torch_cuda()
+    log("moe layer, many tiles", c)
+    case = Case(**c)
+    log("  rel L2 %.2e" % case.check(*case.run()))
+
+
 def test_one_row_beside_the_output_and_with_nan():
     torch = torch_cuda()
     case = Case(1, 576, 192, 20, 3, Is=64)
