@@ -1,7 +1,8 @@
 """Operators on 4-bit weights over torch tensors.
 
 torch supplies device memory and streams; the work is done by the library's
-HIP kernels.  Calls are asynchronous on `stream` (the current stream of the
+HIP kernels.  The operators are for inference: nothing records a gradient.
+Calls are asynchronous on `stream` (the current stream of the
 tensors' device if None) and can be captured into a graph.
 """
 import ctypes
@@ -226,6 +227,7 @@ class MoELayer:
                  shared_global_scales=None, score="softmax", score_bias=None, routed_scale=1.0, max_rows=16):
         _need(score in ("softmax", "sigmoid"), "unknown score %r" % (score,))
         _need(router.dim() == 2 and router.shape[1] == hidden, "router must be [experts, hidden]")
+        _need(hidden > 0 and inter > 0, "hidden and inter must be positive")
         E, dev = router.shape[0], router.device
 
         def dense(t, name, dtype, shape):
