@@ -82,13 +82,26 @@ __device__ __forceinline__ u32x2 widen4(uint32_t d) {
 // l / 4: it holds row l % 4 of the operand and column l % 4 of the weights
 // (four consecutive K-elements each) and gets column l % 4 of the result, its
 // four rows in the four registers.  Products are exact, sums are fp32.
-template <bool HALF>
+//
+// KEEP: the operands live until the result is there, so that no result is written
+// over them; and the instructions stay in the order written, which needs fewer
+// registers (16 rows of the MoE layer: 168 to 158, and 442 to 422 us; without
+// "volatile" the compiler stretches their lives and spills).  A kernel whose sums
+// the compiler places in the accumulation registers has the first by itself.
+#ifdef FP4_SUMS_IN_VGPRS
+constexpr bool kKeepOperands = true;
+#else
+constexpr bool kKeepOperands = false;
+#endif
+template <bool HALF, bool KEEP>
 __device__ __forceinline__ f32x4 mfma4(u32x2 x, u32x2 w, f32x4 c) {
+  f32x4 d;
   if constexpr (HALF)
-    return __builtin_amdgcn_mfma_f32_4x4x4f16(__builtin_bit_cast(f16x4, x), __builtin_bit_cast(f16x4, w), c, 0, 0, 0);
+    d = __builtin_amdgcn_mfma_f32_4x4x4f16(__builtin_bit_cast(f16x4, x), __builtin_bit_cast(f16x4, w), c, 0, 0, 0);
   else
-    return __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(__builtin_bit_cast(s16x4, x), __builtin_bit_cast(s16x4, w), c, 0, 0,
-                                                  0);
+    d = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(__builtin_bit_cast(s16x4, x), __builtin_bit_cast(s16x4, w), c, 0, 0, 0);
+  if constexpr (KEEP) asm volatile("" : "+v"(d) : "v"(x), "v"(w));
+  return d;
 }
 
 // An E8M0 byte: 2^(b - 127); 255 is NaN.
@@ -229,7 +242,7 @@ __device__ __forceinline__ void load_stage(Stage<FMT, ODD, Q>& st, const Reader<
 // bits).  With one row the parts stand as three rows of its set and their sums
 // are added; otherwise part p lies at + p * part_bytes and the matrix
 // instructions add all three into one sum.
-template <int FMT, bool ODD, int Q, int ROWS, bool HALF, bool SPLIT = false, int W = Q < 2 ? Q : 2>
+template <int FMT, bool ODD, int Q, int ROWS, bool HALF, bool SPLIT = false, int W = Q < 2 ? Q : 2, bool KEEP = kKeepOperands>
 __device__ __forceinline__ void use_stage(const Stage<FMT, ODD, Q>& st,
                                           const uint8_t* const (&xs)[(ROWS + 3) / 4], int at, float (&acc)[Q][ROWS],
                                           int part_bytes = 0) {
@@ -263,13 +276,13 @@ __device__ __forceinline__ void use_stage(const Stage<FMT, ODD, Q>& st,
 #pragma unroll
         for (int t = 0; t < NP; ++t) {
 #pragma unroll
-          for (int j = 0; j < W; ++j) p[j] = mfma4<HALF>(u32x2{x[t][0].x, x[t][0].y}, w[j][0], p[j]);
+          for (int j = 0; j < W; ++j) p[j] = mfma4<HALF, KEEP>(u32x2{x[t][0].x, x[t][0].y}, w[j][0], p[j]);
 #pragma unroll
-          for (int j = 0; j < W; ++j) p[j] = mfma4<HALF>(u32x2{x[t][0].z, x[t][0].w}, w[j][1], p[j]);
+          for (int j = 0; j < W; ++j) p[j] = mfma4<HALF, KEEP>(u32x2{x[t][0].z, x[t][0].w}, w[j][1], p[j]);
 #pragma unroll
-          for (int j = 0; j < W; ++j) p[j] = mfma4<HALF>(u32x2{x[t][1].x, x[t][1].y}, w[j][2], p[j]);
+          for (int j = 0; j < W; ++j) p[j] = mfma4<HALF, KEEP>(u32x2{x[t][1].x, x[t][1].y}, w[j][2], p[j]);
 #pragma unroll
-          for (int j = 0; j < W; ++j) p[j] = mfma4<HALF>(u32x2{x[t][1].z, x[t][1].w}, w[j][3], p[j]);
+          for (int j = 0; j < W; ++j) p[j] = mfma4<HALF, KEEP>(u32x2{x[t][1].z, x[t][1].w}, w[j][3], p[j]);
         }
 #pragma unroll
         for (int j = 0; j < W; ++j) {

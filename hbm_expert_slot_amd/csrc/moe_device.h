@@ -9,6 +9,7 @@
 // value that no result has, and whoever needs it polls the word itself.
 #pragma once
 
+#define FP4_SUMS_IN_VGPRS    // three blocks of 256 or one of 768 threads per compute unit
 #include "fp4_device.h"
 #include "internal.h"
 

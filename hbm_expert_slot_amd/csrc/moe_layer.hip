@@ -461,8 +461,9 @@ __device__ __forceinline__ Taker taker(const MoeArgs& a, int phase, int n) {
 // The tasks of U experts of `tiles` tiles each.  Several tiles of an expert are a
 // task where there are many, since a task stages its rows first; the last experts'
 // tasks are single tiles, so that the blocks end together.  8 rows of 8 picks of
-// 4096 x 2048 among 288: 225 us with single tiles throughout, 190 like this; 16
-// rows of 6144 x 2048 among 256: 444 with three tiles throughout, 442 like this.
+// 4096 x 2048 among 288: 225 us with single tiles throughout, 190 like this (170
+// with what came later); 16 rows of 6144 x 2048 among 256: no difference to three
+// tiles throughout.
 struct Tasks {
   int tiles, f, per, many;      // tiles of an expert; of a task; tasks of an expert; experts cut so
   __device__ __forceinline__ Tasks(int U, int tiles_) : tiles(tiles_) {
