@@ -31,6 +31,7 @@ namespace {
 
 constexpr int kThreads = 768, kWaves = kThreads / 64;
 constexpr int kPatience = 4096;     // polls (about a millisecond) before a waiting block takes another share
+constexpr int kMaxLate = kMaxPolls / kPatience;      // such waits of a block after which the call is given up
 constexpr int kMaxShares = 1024;
 constexpr int kService = 4, kDownWaves = kWaves - kService;   // see above
 
@@ -477,7 +478,7 @@ __global__ __launch_bounds__(kThreads) void k_moe_one(MoeArgs a, Plan p) {
   int32_t* error = &a.ctl[O_ERROR];
   const int B = gridDim.x, wave = wave_index(), lane = fresh_lane();
 
-  int lost = 0;
+  int lost = 0, late = 0;
   if (threadIdx.x == 0) {
     s.n = 1;
     s.list[0] = (uint16_t)blockIdx.x;
@@ -535,6 +536,7 @@ __global__ __launch_bounds__(kThreads) void k_moe_one(MoeArgs a, Plan p) {
         ok = false;
         break;
       }
+      if (++late == kMaxLate && threadIdx.x == 0) put(error, 1);
       take_over(&s, lds, false);
     }
   }
@@ -606,6 +608,7 @@ __global__ __launch_bounds__(kThreads) void k_moe_one(MoeArgs a, Plan p) {
         }
       }
       if (r != kLate) break;
+      if (++late == kMaxLate && threadIdx.x == 0) put(error, 1);
       take_over(&s, lds, true);
     }
   }

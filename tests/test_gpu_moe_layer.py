@@ -159,6 +159,22 @@ def test_one_row_beside_the_output_and_with_nan():
     assert torch.equal(y, want) and torch.equal(ids, ids0)
 
 
+def test_one_row_gives_up_a_wait_that_does_not_end():
+    """A share marked as taken that nobody computes (as a call that shares its workspace could leave it): every block
+    leaves after its bounded wait, the result is NaN, and the workspace serves the next call."""
+    torch = torch_cuda()
+    case = Case(1, 576, 192, 20, 3, Is=64)
+    want = case.run()[0]
+    torch.cuda.synchronize()
+    claims = 5 * 16 * 32 + 2 * 32 + (513 + 32) // 32 * 32 + 1024 + 513 * 32     # words of the kernel for more rows
+    case.layer.workspace.view(torch.int32)[claims] = 1
+    log("a share that nobody computes")
+    y = case.layer.forward(case.tx)
+    torch.cuda.synchronize()
+    assert torch.isnan(y).all()
+    assert torch.equal(case.run()[0], want)
+
+
 @pytest.mark.parametrize("M", [1, 2, 16])
 def test_replayed(M):
     """Two graphs of one layer, replayed in turn with eager calls of other row counts between them."""
