@@ -183,10 +183,22 @@ __device__ __forceinline__ void router_tile_mfma(const MoeArgs& a, int tile, flo
 }
 
 // Keys that order as the scores do: NaN below -inf, -0 equal to +0.
-__device__ __forceinline__ int order_key(float z) {
-  if (z != z) return INT32_MIN + 1;
-  const int b = (int)__float_as_uint(z + 0.0f);
-  return b >= 0 ? b : b ^ 0x7FFFFFFF;
+__device__ __forceinline__ int64_t order_key(double z) {
+  if (z != z) return INT64_MIN + 1;
+  const int64_t b = __double_as_longlong(z + 0.0);
+  return b >= 0 ? b : b ^ INT64_MAX;
+}
+
+// What the picks are ordered by.  Sigmoids without a bias order as their logits do,
+// also where they are one fp32 number (from 17.3 on all are 1).  With one the sum is
+// formed in fp64 from the sigmoid's distance to 0 or 1, t / (1 + t) with t =
+// exp(-|z|), whose relative error of |z| 2^-23 and a few steps is the logit's own.
+__device__ __forceinline__ double pick_score(const MoeArgs& a, float z, float bias) {
+  if (!a.score_bias) return z;
+  const float y = fabsf(z) * -1.4426950408889634f, n = __builtin_rintf(fmaxf(y, -2000.0f));
+  const double t = ldexp((double)__builtin_amdgcn_exp2f(y - n), (int)n);
+  const double d = t * (double)__builtin_amdgcn_rcpf(1.0f + (float)t);
+  return (z > 0.0f ? 1.0 - d : z == z ? d : (double)z) + (double)bias;
 }
 
 // Reductions over the wavefront in registers: halves and 16-lane rows trade by
@@ -260,10 +272,12 @@ __device__ __forceinline__ Routed route_row(const MoeArgs& a, int32_t* error, in
       for (int q = 0; q < QB; ++q)
         sum[i] = q0 + q == 0 ? __uint_as_float(part[i][q]) : sum[i] + __uint_as_float(part[i][q]);
   }
-  int key[EPL], id[EPL];
+  int64_t key[EPL];
+  int id[EPL];
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     float z = sum[i];
+    const double by = pick_score(a, z, bias[i]);
     // a few ulps from the hardware's exponential and reciprocal, below the logit's own rounding
     if (a.score == SC_SCORE_SIGMOID) z = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-z * 1.4426950408889634f));
     id[i] = lane * epl + i;
@@ -273,7 +287,7 @@ __device__ __forceinline__ Routed route_row(const MoeArgs& a, int32_t* error, in
 #pragma unroll
       for (int q = 0; q < KS; ++q) put(&a.logits[(q * a.M + m) * a.E + id[i]], kNoLogit);
     }
-    key[i] = in ? order_key(z + bias[i]) : INT32_MIN;
+    key[i] = in ? order_key(by) : INT64_MIN;
   }
   if constexpr (SORT) {
 #pragma unroll
@@ -281,7 +295,8 @@ __device__ __forceinline__ Routed route_row(const MoeArgs& a, int32_t* error, in
 #pragma unroll
       for (int i = 0; i < n; ++i) {
         const bool up = key[i + 1] > key[i];       // equal keys keep their order
-        const int k0 = key[i], i0 = id[i];
+        const int64_t k0 = key[i];
+        const int i0 = id[i];
         key[i] = up ? key[i + 1] : k0;
         id[i] = up ? id[i + 1] : i0;
         key[i + 1] = up ? k0 : key[i + 1];
@@ -291,7 +306,8 @@ __device__ __forceinline__ Routed route_row(const MoeArgs& a, int32_t* error, in
   int my_id = 0;
 #pragma unroll 1
   for (int j = 0; j < a.k; ++j) {
-    int best = key[0], at = id[0];
+    int64_t best = key[0];
+    int at = id[0];
     if constexpr (!SORT) {
 #pragma unroll
       for (int i = 1; i < EPL; ++i)
@@ -300,19 +316,27 @@ __device__ __forceinline__ Routed route_row(const MoeArgs& a, int32_t* error, in
           at = id[i];
         }
     }
-    const int src = __builtin_ctzll(__ballot(best == wave_max_i(best)));
+    const int hi = (int)(best >> 32), first = wave_max_i(hi);
+    uint64_t top = __ballot(hi == first);
+    if (top & (top - 1)) {
+      // lanes that agree in the upper half; every lane takes part in the reduction
+      const bool in = top >> lane & 1;
+      const int lo = in ? (int)((uint32_t)best ^ 0x80000000u) : INT32_MIN, most = wave_max_i(lo);
+      top = __ballot(in && lo == most);
+    }
+    const int src = __builtin_ctzll(top);
     const int e = __builtin_amdgcn_readlane(at, src);
     if (lane == j) my_id = e;
     if constexpr (SORT) {
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
-        key[i] = lane == src ? (i + 1 < EPL ? key[i + 1] : INT32_MIN) : key[i];
+        key[i] = lane == src ? (i + 1 < EPL ? key[i + 1] : INT64_MIN) : key[i];
         id[i] = lane == src && i + 1 < EPL ? id[i + 1] : id[i];
       }
     } else {
 #pragma unroll
       for (int i = 0; i < EPL; ++i)
-        if (id[i] == e) key[i] = INT32_MIN;
+        if (id[i] == e) key[i] = INT64_MIN;
     }
   }
   // weights; NaN counts as the lowest score, picks of +inf share the weight,

@@ -403,8 +403,10 @@ SC_API sc_status fp4_linear(const sc_fp4_matrix* w, const void* d_x, int32_t x_t
  * to the lower expert id, NaN lowest) and multiply the weights by routed_scale.
  *   SC_SCORE_SOFTMAX  picks by logit; weights are the softmax over the k chosen
  *                     logits (the rule of moe_layer_decode)
- *   SC_SCORE_SIGMOID  picks by sigmoid(logit) + bias; weights are the chosen
- *                     sigmoids divided by their sum (equal when that is 0) */
+ *   SC_SCORE_SIGMOID  picks by sigmoid(logit) + bias (compared in fp64, so that
+ *                     scores near 1 stay apart; without a bias by the logit);
+ *                     weights are the chosen sigmoids divided by their sum
+ *                     (equal when that is 0) */
 #define SC_SCORE_SOFTMAX 0
 #define SC_SCORE_SIGMOID 1
 

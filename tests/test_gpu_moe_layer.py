@@ -360,3 +360,81 @@ def test_quantised_weights_through_the_layer():
             want += wt[m, j].double() * (ops.fp4_dequantize(q2).double() @ h)
         # w13's products and w2's: fp32 sums of at most 40 terms each, twice
         assert float((y[m].double() - want).norm() / want.norm()) < 1e-5
+
+
+# ---- sigmoid scores near their ends ------------------------------------------------
+
+def _scored(M, z, bias, k, scale=1.0):
+    """Picks and weights of a layer whose logits are exactly z [E] for every row (x is 1 in three places, where the
+    router holds three bf16 parts of z)."""
+    import torch
+    from hbm_expert_slot_amd.ops import MoELayer
+    E, H, I = len(z), 64, 64
+    rng = np.random.default_rng(E)
+    router = np.zeros((E, H), np.float32)
+    for i in range(3):
+        router[:, i] = decode_bf16(bf16_bits_from_f32((z - router.sum(1, dtype=np.float64)).astype(np.float32)))
+    assert np.array_equal(router.sum(1, dtype=np.float64), z)
+    x = torch.zeros(M, H, dtype=torch.bfloat16, device="cuda")
+    x[:, :3] = 1
+    cu = lambda v: None if v is None else torch.tensor(v).cuda()
+    layer = MoELayer(H, I, k, torch.tensor(router, dtype=torch.bfloat16).cuda(),
+                     cu(np.stack([_blob(rng, H, I) for _ in range(E)])),
+                     cu(np.full((E, 2), 1e-4, np.float32)), score="sigmoid", score_bias=cu(bias), routed_scale=scale)
+    ids = torch.full((M, k), -1, dtype=torch.int32, device="cuda")
+    w = torch.full((M, k), float("nan"), device="cuda")
+    layer.forward(x, ids=ids, weights=w)
+    return ids.cpu().numpy(), w.double().cpu().numpy()
+
+
+def _steps(E, base, seed):
+    """E different logits from base on, 2^-12 apart, in any order."""
+    return base + np.random.default_rng(seed).permutation(E) * 2.0 ** -12
+
+
+# the kernels for one row, for up to four and for more; experts per lane that are sorted, and that are not
+ROWS_AND_EXPERTS = [(1, 40), (3, 40), (7, 40), (1, 700), (6, 700)]
+
+
+@pytest.mark.parametrize("base", [10.0, 20.0, 100.0, -20.0, -100.0])
+@pytest.mark.parametrize("M,E", ROWS_AND_EXPERTS)
+def test_sigmoid_scores_that_fp32_cannot_tell_apart(M, E, base):
+    """Without a bias the order is that of the logits: near 1 sigmoids of different logits are one fp32 number."""
+    torch_cuda()
+    z = _steps(E, base, M)
+    ids, _ = _scored(M, z, None, 6)
+    assert (ids == np.argsort(-z)[:6]).all()
+
+
+@pytest.mark.parametrize("base", [0.0, 10.0, 20.0, -20.0])
+@pytest.mark.parametrize("M,E", ROWS_AND_EXPERTS)
+def test_sigmoid_scores_with_one_bias_for_all(M, E, base):
+    """The same bias for all leaves that order; at 20 the neighbours' sums differ by 5e-13."""
+    torch_cuda()
+    z = _steps(E, base, M + 1)
+    for b in (0.0, 0.25, -0.75):
+        ids, _ = _scored(M, z, np.full(E, b, np.float32), 6)
+        assert (ids == np.argsort(-z)[:6]).all(), b
+
+
+@pytest.mark.parametrize("M,E", ROWS_AND_EXPERTS)
+def test_sigmoid_scores_and_biases_that_nearly_balance(M, E):
+    """Sums apart by less than fp32 holds next to 1."""
+    torch_cuda()
+    rng = np.random.default_rng(M * E)
+    z = 10.0 + rng.integers(0, 4096, E) * 2.0 ** -12
+    bias = (rng.standard_normal(E) * 1e-6).astype(np.float32)
+    by = 1.0 / (1.0 + np.exp(-z)) + bias.astype(np.float64)
+    order = np.argsort(-by, kind="stable")
+    # sigmoid's distance to 1 is 4.5e-5 and known to 16 steps of fp32
+    assert (-np.diff(by[order[:7]])).min() > 4.5e-5 * 16 * 2.0 ** -24, "draw other inputs: scores too close"
+    ids, _ = _scored(M, z, bias, 6)
+    assert (ids == order[:6]).all()
+
+
+def test_sigmoid_ties_go_to_the_lower_expert():
+    torch_cuda()
+    for z in (0.0, 12.0, 90.0, -90.0):
+        for bias in (None, np.full(300, 0.5, np.float32)):
+            ids, w = _scored(2, np.full(300, z), bias, 5)
+            assert (ids == np.arange(5)).all() and np.abs(w - 0.2).max() < 1e-6
