@@ -226,7 +226,7 @@ __device__ __forceinline__ float wave_sum_f(float v) {
 // One wavefront picks row m's experts and publishes them.  Lane l looks after
 // experts l * epl .. and keeps them sorted (up to eight; more are looked through
 // each time), so that a pick costs one reduction: the lowest lane with the
-// largest key holds the lowest id.  val: LDS, [E].  The logits are set back to
+// largest key holds the lowest id.  sval: the logits, LDS, [E].  The logits are set back to
 // kNoLogit.  After `patience` polls it returns kLate with nothing done.
 enum Routed { kDone = 0, kLate, kGivenUp };
 template <int EPL, int KS>
@@ -276,10 +276,8 @@ __device__ __forceinline__ Routed route_row(const MoeArgs& a, int32_t* error, in
   int id[EPL];
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    float z = sum[i];
+    const float z = sum[i];
     const double by = pick_score(a, z, bias[i]);
-    // a few ulps from the hardware's exponential and reciprocal, below the logit's own rounding
-    if (a.score == SC_SCORE_SIGMOID) z = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-z * 1.4426950408889634f));
     id[i] = lane * epl + i;
     const bool in = i < epl && id[i] < a.E;
     if (in) {
@@ -344,13 +342,16 @@ __device__ __forceinline__ Routed route_row(const MoeArgs& a, int32_t* error, in
   const bool on = lane < a.k;
   const float my_val = on ? sval[my_id] : 0.0f;
   const float z = my_val != my_val ? -INFINITY : my_val;
+  const float zmax = __uint_as_float(wave_reduce(__float_as_uint(on ? z : -INFINITY), [](uint32_t x, uint32_t y) {
+    return __float_as_uint(fmaxf(__uint_as_float(x), __uint_as_float(y)));
+  }));
   float w;
   if (a.score == SC_SCORE_SIGMOID) {
-    w = on && z > 0.0f ? z : 0.0f;
+    // all times exp(-max) where that is negative: sigmoids below fp32's range keep their proportion
+    constexpr float kLog2e = 1.4426950408889634f;
+    const float q = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-fabsf(z) * kLog2e));
+    w = !on || z == -INFINITY ? 0.0f : z > 0.0f ? q : __builtin_amdgcn_exp2f((z - fminf(zmax, 0.0f)) * kLog2e) * q;
   } else {
-    const float zmax = __uint_as_float(wave_reduce(__float_as_uint(on ? z : -INFINITY), [](uint32_t x, uint32_t y) {
-      return __float_as_uint(fmaxf(__uint_as_float(x), __uint_as_float(y)));
-    }));
     w = !on ? 0.0f : zmax == INFINITY ? (z == INFINITY ? 1.0f : 0.0f) : zmax == -INFINITY ? 1.0f : expf(z - zmax);
   }
   const float total = wave_sum_f(w);

@@ -438,3 +438,18 @@ def test_sigmoid_ties_go_to_the_lower_expert():
         for bias in (None, np.full(300, 0.5, np.float32)):
             ids, w = _scored(2, np.full(300, z), bias, 5)
             assert (ids == np.arange(5)).all() and np.abs(w - 0.2).max() < 1e-6
+
+
+@pytest.mark.parametrize("M,E", ROWS_AND_EXPERTS)
+@pytest.mark.parametrize("base", [-20.0, -86.0, -88.0, -95.0, -120.0])
+def test_sigmoid_weights_far_below_zero(M, E, base):
+    """Sigmoids that are denormal in fp32, or below it, have weights in their own proportion."""
+    torch_cuda()
+    rng = np.random.default_rng(E)
+    z = base - rng.permutation(E) * 0.25
+    ids, w = _scored(M, z, None, 6, scale=2.0)
+    assert (ids == np.argsort(-z)[:6]).all()
+    top = np.sort(z)[::-1][:6]
+    v = np.exp(top - top.max()) / (1.0 + np.exp(top))
+    # exponentials of exact differences, a reciprocal, a sum of six and a division, a few steps each
+    assert np.abs(w - 2.0 * v / v.sum()).max() <= 2.0 * 16 * 2.0 ** -24
