@@ -292,20 +292,27 @@ hipError_t run_quantize(const QuantArgs& a, int fmt, hipStream_t st) {
   return hipGetLastError();
 }
 
+// Rows at a time: a launch has less than 2^32 threads, and runs only part of a larger grid without an error.
 template <typename T>
 hipError_t run_values(const sc_fp4_matrix* m, void* out, int64_t ld, hipStream_t st) {
   constexpr int W = 16 / sizeof(T);
-  const uint64_t n = (uint64_t)m->rows * m->cols / W;
-  const unsigned grid = blocks_of(n);
-  const uint8_t* c = static_cast<const uint8_t*>(m->d_codes);
-  const uint8_t* s = static_cast<const uint8_t*>(m->d_scales);
-  if (m->format == SC_FP4_NV)
-    hipLaunchKernelGGL((k_fp4_values<kNv, T>), dim3(grid), dim3(kThreads), 0, st, c, s, m->d_global_scale,
-                       static_cast<T*>(out), ld, n, (uint32_t)m->cols);
-  else
-    hipLaunchKernelGGL((k_fp4_values<kMx, T>), dim3(grid), dim3(kThreads), 0, st, c, s, m->d_global_scale,
-                       static_cast<T*>(out), ld, n, (uint32_t)m->cols);
-  return hipGetLastError();
+  const int64_t cols = m->cols, most = ((int64_t)1 << 31) * W / cols;
+  for (int64_t r = 0; r < m->rows; r += most) {
+    const uint64_t n = (uint64_t)(m->rows - r < most ? m->rows - r : most) * cols / W;
+    const unsigned grid = blocks_of(n);
+    const uint8_t* c = static_cast<const uint8_t*>(m->d_codes) + r * (cols / 2);
+    const uint8_t* s = static_cast<const uint8_t*>(m->d_scales) + r * (cols / (m->format == SC_FP4_NV ? 16 : 32));
+    T* o = static_cast<T*>(out) + r * ld;
+    if (m->format == SC_FP4_NV)
+      hipLaunchKernelGGL((k_fp4_values<kNv, T>), dim3(grid), dim3(kThreads), 0, st, c, s, m->d_global_scale, o, ld, n,
+                         (uint32_t)cols);
+    else
+      hipLaunchKernelGGL((k_fp4_values<kMx, T>), dim3(grid), dim3(kThreads), 0, st, c, s, m->d_global_scale, o, ld, n,
+                         (uint32_t)cols);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace

@@ -316,3 +316,32 @@ def test_quantize_replayed():
         g.replay()
         torch.cuda.synchronize()
         _check_quant(torch, w, q, "nvfp4")
+
+
+# ---- more threads than one launch has (2^32) ----------------------------------------
+
+def _rows_of(q, a, b):
+    return _ops().FP4Weight(q.codes[a:b], q.scales[a:b], q.global_scale, q.fmt)
+
+
+def _large_fp4(torch, rows, cols, fmt):
+    q = _ops().FP4Weight.empty(rows, cols, fmt)
+    for a in range(0, rows, 1 << 24):
+        q.codes[a:a + (1 << 24)].random_(0, 256)
+        q.scales[a:a + (1 << 24)].random_(0x28, 0x70)
+    return q
+
+
+def test_dequantize_a_matrix_of_more_than_2_to_34_elements():
+    """64 GiB of fp32 values."""
+    torch = torch_cuda()
+    rows, cols = (1 << 14) + 3, 1 << 20
+    log("dequantize", rows, cols)
+    q = _large_fp4(torch, rows, cols, "mxfp4")
+    out = torch.empty(rows, cols, device="cuda")
+    out[-4:] = float("nan")
+    out[:4] = float("nan")
+    _ops().fp4_dequantize(q, out=out)
+    for a in range(0, rows, 1024):
+        b = min(rows, a + 1024)
+        assert torch.equal(out[a:b], _ops().fp4_dequantize(_rows_of(q, a, b))), a
