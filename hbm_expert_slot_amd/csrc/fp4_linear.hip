@@ -377,7 +377,6 @@ hipError_t launch_tiles(LinearArgs a, hipStream_t st) {
   constexpr int P = HALF && FMT == kMx ? 2 : 1;
   a.mblocks = (int)(((int64_t)a.M + BM - 1) / BM);
   const long blocks = (long)a.mblocks * (((long)a.N + 16 * NT * WN - 1) / (16 * NT * WN));
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
   hipLaunchKernelGGL((k_fp4_tiles<FMT, ODD, HALF, BM, NT, WN, KS>), dim3((unsigned)blocks), dim3(64 * WN * KS),
                      KS * 2 * P * BM * (kChunk * 2 + 16), st, a);
   return hipGetLastError();
@@ -417,6 +416,30 @@ hipError_t by_format(const LinearArgs& a, int fmt, hipStream_t st) {
   return by_count<kNv, false, HALF>(a, st);
 }
 
+// A launch has less than 2^32 threads, and runs only part of a larger grid without an error.  Up to 32
+// rows take 32 threads per weight row at most, more of them 256 per 64 x 128 outputs (tiles with more
+// threads per output are taken for up to 512 blocks only); indexes of rows stay below 2^31 with a tile to spare.
+hipError_t in_pieces(const LinearArgs& all, bool half, int fmt, hipStream_t st) {
+  constexpr int kMostN = 1 << 25;
+  const int N0 = all.N < kMostN ? all.N : kMostN;
+  const int64_t most_m = 64 * ((((int64_t)1 << 24) - 1) / (((int64_t)N0 + 127) / 128));
+  const int row_codes = all.K / 2, row_scales = all.K / (fmt == SC_FP4_NV ? 16 : 32), size = all.out == SC_DTYPE_F32 ? 4 : 2;
+  for (int64_t n = 0; n < all.N; n += kMostN)
+    for (int64_t m = 0; m < all.M; m += most_m) {
+      LinearArgs a = all;
+      a.N = (int)(all.N - n < kMostN ? all.N - n : kMostN);
+      a.M = (int)(all.M - m < most_m ? all.M - m : most_m);
+      a.codes += n * row_codes;
+      a.scales += n * row_scales;
+      if (a.bias) a.bias += n;
+      a.x += m * a.ldx;
+      a.y = static_cast<uint8_t*>(a.y) + (m * a.ldy + n) * size;
+      const hipError_t e = half ? by_format<true>(a, fmt, st) : by_format<false>(a, fmt, st);
+      if (e != hipSuccess) return e;
+    }
+  return hipSuccess;
+}
+
 }  // namespace
 }  // namespace sc
 
@@ -449,7 +472,7 @@ extern "C" sc_status fp4_linear(const sc_fp4_matrix* w, const void* d_x, int32_t
   a.x = static_cast<const uint16_t*>(d_x);
   a.y = d_y;
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  const hipError_t e = x_type == SC_DTYPE_F16 ? by_format<true>(a, w->format, st) : by_format<false>(a, w->format, st);
+  const hipError_t e = in_pieces(a, x_type == SC_DTYPE_F16, w->format, st);
   if (e != hipSuccess) return hip_fail(e, "fp4_linear launch");
   return SC_OK;
 }

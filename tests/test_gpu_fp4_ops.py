@@ -345,3 +345,38 @@ def test_dequantize_a_matrix_of_more_than_2_to_34_elements():
     for a in range(0, rows, 1024):
         b = min(rows, a + 1024)
         assert torch.equal(out[a:b], _ops().fp4_dequantize(_rows_of(q, a, b))), a
+
+
+@pytest.mark.parametrize("M,N", [(1, (1 << 29) + 40), (5, (1 << 27) + 40)])
+def test_linear_with_very_many_weight_rows(M, N):
+    torch = torch_cuda()
+    log("linear", M, N)
+    q = _large_fp4(torch, N, 16, "nvfp4")
+    x = torch.randn(M, 16, device="cuda").to(torch.bfloat16)
+    bias = torch.randn(N, device="cuda")
+    out = torch.full((M, N), float("nan"), device="cuda")
+    _ops().fp4_linear(x, q, bias=bias, out=out)
+    for a in range(0, N, 1 << 24):
+        b = min(N, a + (1 << 24))
+        part = _ops().fp4_linear(x, _rows_of(q, a, b), bias=bias[a:b], out_dtype=torch.float32)
+        assert torch.equal(out[:, a:b], part), a
+
+
+def test_linear_with_very_many_operand_rows():
+    """2^30 rows and some: 64 GiB of x."""
+    torch = torch_cuda()
+    M, K = (1 << 30) + 70, 32
+    log("linear", M)
+    q = _large_fp4(torch, 2, K, "mxfp4")
+    x = torch.empty(M, K, dtype=torch.float16, device="cuda")
+    for a in range(0, M, 1 << 26):
+        x[a:a + (1 << 26)].normal_()
+    out = torch.full((M, 2), float("nan"), dtype=torch.float16, device="cuda")
+    _ops().fp4_linear(x, q, out=out)
+    for a in range(0, M, 1 << 26):
+        b = min(M, a + (1 << 26))
+        part = _ops().fp4_linear(x[a:b], q)
+        if b - a > 1000:
+            assert torch.equal(out[a:b], part), a
+        else:                                  # few rows: another order of the 32 products
+            assert torch.allclose(out[a:b].float(), part.float(), rtol=2e-3, atol=1e-3), a
