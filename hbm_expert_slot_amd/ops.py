@@ -67,14 +67,34 @@ def _check_ld(t, name):
     _need(t.shape[0] <= 1 or t.stride(0) >= t.shape[1], "%s has rows that overlap" % name)
 
 
-class FP4Weight:
+class _Fixed:
+    """Objects that hand addresses to the library: what those belong to cannot be
+    assigned again (assigning would leave the library with the old ones)."""
+
+    _fixed = frozenset()
+
+    def __setattr__(self, name, value):
+        if name in self._fixed and name in self.__dict__:
+            raise AttributeError("%s of a %s is fixed when it is made" % (name, type(self).__name__))
+        self.__dict__[name] = value
+
+    def __delattr__(self, name):
+        if name in self._fixed:
+            raise AttributeError("%s of a %s is fixed when it is made" % (name, type(self).__name__))
+        object.__delattr__(self, name)
+
+
+class FP4Weight(_Fixed):
     """A matrix [rows, cols] in 4 bits.
 
     codes uint8 [rows, cols/2] (two E2M1 codes per byte, the even element low),
     scales uint8 [rows, cols/16] (E4M3, "nvfp4") or [rows, cols/32] (E8M0,
     "mxfp4"), global_scale fp32 with one element ("nvfp4"; None stands for 1).
     The tensors are referred to, not copied: they may be views into an expert
-    blob."""
+    blob.  They can be written to, but not exchanged: the weight keeps the memory
+    it was made of, also where a tensor is given other storage later."""
+
+    _fixed = frozenset(("codes", "scales", "global_scale", "fmt", "rows", "cols", "device", "_memory", "_c", "_ref"))
 
     def __init__(self, codes, scales, global_scale=None, fmt="nvfp4"):
         _need(fmt in _FORMAT, "unknown format %r" % (fmt,))
@@ -91,6 +111,7 @@ class FP4Weight:
                   and global_scale.device == codes.device, "global_scale must be one float32 with the codes")
         self.codes, self.scales, self.global_scale, self.fmt = codes, scales, global_scale, fmt
         self.rows, self.cols, self.device = rows, cols, codes.device
+        self._memory = [t.untyped_storage() for t in (codes, scales, global_scale) if t is not None]
         self._c = B.sc_fp4_matrix(_FORMAT[fmt], rows, cols, codes.data_ptr(), scales.data_ptr(),
                                   None if global_scale is None else global_scale.data_ptr())
         self._ref = ctypes.byref(self._c)
@@ -209,7 +230,7 @@ def expert_matrices(blob, hidden, inter, global_scales):
     return w13, w2
 
 
-class MoELayer:
+class MoELayer(_Fixed):
     """A whole mixture-of-experts layer for up to `max_rows` (16) tokens a call.
 
     router bf16 [E, hidden]; blobs uint8 [E, blob_bytes] and global_scales fp32
@@ -217,11 +238,15 @@ class MoELayer:
     in HBM); shared_blob and shared_global_scales [2] the shared expert, if any
     (its inner size follows from the blob's).  score "softmax" or "sigmoid" (with
     score_bias fp32 [E] added for the choice only); routed_scale multiplies the
-    routed sum.  The tensors are referred to, not copied.
+    routed sum.  The tensors are referred to, not copied; they can be written to,
+    but the layer keeps the memory it was made of.
 
     The layer owns a workspace: calls have to be ordered with each other (one
     stream, or streams the caller orders); use one layer object per stream
     otherwise."""
+
+    _fixed = frozenset(("hidden", "inter", "n_experts", "top_k", "shared_inter", "max_rows", "device", "workspace",
+                        "_memory", "_cfg", "_cref", "_w", "_wref"))
 
     def __init__(self, hidden, inter, top_k, router, blobs, global_scales, shared_blob=None,
                  shared_global_scales=None, score="softmax", score_bias=None, routed_scale=1.0, max_rows=16):
@@ -256,7 +281,8 @@ class MoELayer:
         def ptr(t):
             return None if t is None else t.data_ptr()
 
-        self._keep = (router, blobs, global_scales, shared_blob, shared_global_scales, score_bias)
+        self._memory = [t.untyped_storage() for t in (router, blobs, global_scales, shared_blob, shared_global_scales,
+                                                      score_bias) if t is not None]
         self._w = B.sc_moe_weights(ptr(router), ptr(score_bias), ptr(blobs), ptr(global_scales), ptr(shared_blob),
                                    ptr(shared_global_scales))
         self._wref = ctypes.byref(self._w)

@@ -82,3 +82,37 @@ def test_python_refusals():
         ops.FP4Weight.empty(4, 32, "int4")
     with pytest.raises(ValueError, match="multiple"):
         ops.FP4Weight.empty(4, 40)
+
+
+def _made(cls, **attributes):
+    """An object with attributes as its constructor leaves them (the constructor needs a GPU)."""
+    q = cls.__new__(cls)
+    for name, value in attributes.items():
+        setattr(q, name, value)
+    return q
+
+
+def test_what_a_weight_was_made_of_cannot_be_exchanged():
+    """The library has the tensors' addresses: another tensor would be ignored, and the old one's memory freed."""
+    from hbm_expert_slot_amd import ops
+    made = dict(codes=1, scales=2, global_scale=None, fmt="nvfp4", rows=4, cols=16, device="cuda:0")
+    q = _made(ops.FP4Weight, **made)
+    for name, value in made.items():
+        with pytest.raises(AttributeError, match=name):
+            setattr(q, name, 5)
+        with pytest.raises(AttributeError, match=name):
+            delattr(q, name)
+        assert getattr(q, name) == value
+    q.name = "mine"
+    q.name = "other"
+    del q.name
+
+
+def test_what_a_layer_was_made_of_cannot_be_exchanged():
+    from hbm_expert_slot_amd import ops
+    made = dict(hidden=64, inter=64, n_experts=8, top_k=2, shared_inter=0, max_rows=16, device="cuda:0", workspace=3)
+    layer = _made(ops.MoELayer, **made)
+    for name, value in made.items():
+        with pytest.raises(AttributeError, match=name):
+            setattr(layer, name, 5)
+        assert getattr(layer, name) == value

@@ -318,6 +318,20 @@ def test_quantize_replayed():
         _check_quant(torch, w, q, "nvfp4")
 
 
+def test_a_weight_keeps_its_memory():
+    """Tensors whose storage is exchanged, or that are dropped, after the weight was made."""
+    torch = torch_cuda()
+    ops = _ops()
+    q, w = _random_fp4(torch, 96, 2048, "nvfp4", 6)
+    x = torch.randn(3, 2048, device="cuda").to(torch.bfloat16)
+    want, values = ops.fp4_linear(x, q), ops.fp4_dequantize(q)
+    for t in (q.codes, q.scales, q.global_scale):
+        t.data = torch.zeros_like(t)
+    filler = [torch.full((n,), 0x7F, dtype=torch.uint8, device="cuda") for n in (96 * 1024, 96 * 128, 4) for _ in range(4)]
+    assert torch.equal(ops.fp4_linear(x, q), want) and torch.equal(ops.fp4_dequantize(q), values)
+    del filler
+
+
 # ---- more threads than one launch has (2^32) ----------------------------------------
 
 def _rows_of(q, a, b):
