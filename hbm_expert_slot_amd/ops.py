@@ -3,7 +3,11 @@
 torch supplies device memory and streams; the work is done by the library's
 HIP kernels.  The operators are for inference: nothing records a gradient.
 Calls are asynchronous on `stream` (the current stream of the
-tensors' device if None) and can be captured into a graph.
+tensors' device if None) and can be captured into a graph.  What a call
+allocates belongs to its stream.  Tensors given to a call with `stream` may be
+dropped as soon as it returns: their memory is not used again before the
+stream is done with it.  A captured graph does not keep its tensors: that is
+the caller's part.
 """
 import ctypes
 
@@ -44,6 +48,13 @@ class _On:
     def __exit__(self, *exc):
         if self.guard is not None:
             self.guard.__exit__(*exc)
+
+
+def _record(stream, *tensors):
+    """The memory of the tensors is not given out again before what `stream` has been given is done."""
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
 
 
 def _need(cond, msg):
@@ -120,6 +131,10 @@ class FP4Weight(_Fixed):
     def shape(self):
         return (self.rows, self.cols)
 
+    def _record(self, stream):
+        for m in self._memory:
+            _record(stream, torch.empty(0, dtype=torch.uint8, device=self.device).set_(m))
+
     @staticmethod
     def empty(rows, cols, fmt="nvfp4", device="cuda"):
         _need(fmt in _FORMAT, "unknown format %r" % (fmt,))
@@ -166,6 +181,9 @@ def fp4_quantize(w, fmt="nvfp4", global_scale=None, out=None, stream=None):
             ws = torch.empty(B.SC_FP4_QUANT_WORKSPACE_BYTES, dtype=torch.uint8, device=dev)
         B.fp4_quantize(w.data_ptr(), _TYPE[w.dtype], _ld(w), out._ref, 0 if global_scale is None else 1,
                        None if ws is None else ws.data_ptr(), s)
+    if stream is not None:
+        _record(stream, w)
+        out._record(stream)
     return out
 
 
@@ -181,6 +199,9 @@ def fp4_dequantize(q, dtype=torch.float32, out=None, stream=None):
             _check_ld(out, "out")
             _need(tuple(out.shape) == q.shape and out.device == dev, "out does not fit")
         B.fp4_dequantize(q._ref, out.data_ptr(), _TYPE[out.dtype], _ld(out), s)
+    if stream is not None:
+        _record(stream, out)
+        q._record(stream)
     return out
 
 
@@ -208,6 +229,9 @@ def fp4_linear(x, q, bias=None, out_dtype=None, out=None, stream=None):
             _need(out_dtype is None or out.dtype == out_dtype, "out has type %s" % (out.dtype,))
         B.fp4_linear(q._ref, x.data_ptr(), _TYPE[x.dtype], _ld(x), M, None if bias is None else bias.data_ptr(),
                      out.data_ptr(), _TYPE[out.dtype], _ld(out), s)
+    if stream is not None:
+        _record(stream, x, bias, out)
+        q._record(stream)
     return out
 
 
@@ -243,10 +267,11 @@ class MoELayer(_Fixed):
 
     The layer owns a workspace: calls have to be ordered with each other (one
     stream, or streams the caller orders); use one layer object per stream
-    otherwise."""
+    otherwise.  A layer may be dropped while calls are under way, but not while a
+    captured graph is to be replayed."""
 
     _fixed = frozenset(("hidden", "inter", "n_experts", "top_k", "shared_inter", "max_rows", "device", "workspace",
-                        "_memory", "_cfg", "_cref", "_w", "_wref"))
+                        "_memory", "_streams", "_cfg", "_cref", "_w", "_wref"))
 
     def __init__(self, hidden, inter, top_k, router, blobs, global_scales, shared_blob=None,
                  shared_global_scales=None, score="softmax", score_bias=None, routed_scale=1.0, max_rows=16):
@@ -281,8 +306,9 @@ class MoELayer(_Fixed):
         def ptr(t):
             return None if t is None else t.data_ptr()
 
-        self._memory = [t.untyped_storage() for t in (router, blobs, global_scales, shared_blob, shared_global_scales,
-                                                      score_bias) if t is not None]
+        self._memory = [t.detach() for t in (router, blobs, global_scales, shared_blob, shared_global_scales, score_bias)
+                        if t is not None]
+        self._streams = set()        # that the memory is recorded on
         self._w = B.sc_moe_weights(ptr(router), ptr(score_bias), ptr(blobs), ptr(global_scales), ptr(shared_blob),
                                    ptr(shared_global_scales))
         self._wref = ctypes.byref(self._w)
@@ -290,6 +316,7 @@ class MoELayer(_Fixed):
         self.shared_inter, self.max_rows, self.device = shared_inter, max_rows, dev
         with _On(dev, None) as s:
             self.workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+            self._memory.append(self.workspace.detach())
             B.moe_layer_prepare(self._cref, self.workspace.data_ptr(), s)
             torch.cuda.current_stream(dev).synchronize()
 
@@ -315,4 +342,10 @@ class MoELayer(_Fixed):
             B.moe_layer_forward(self._cref, self._wref, self.workspace.data_ptr(), x.data_ptr(), _ld(x), M,
                                 out.data_ptr(), _TYPE[out.dtype], _ld(out), None if ids is None else ids.data_ptr(),
                                 None if weights is None else weights.data_ptr(), s)
+            if s not in self._streams:
+                # the layer may be dropped while the stream works on it
+                _record(torch.cuda.current_stream(dev), *self._memory)
+                self._streams.add(s)
+        if stream is not None:
+            _record(stream, x, out, ids, weights)
         return out

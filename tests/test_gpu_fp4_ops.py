@@ -332,6 +332,60 @@ def test_a_weight_keeps_its_memory():
     del filler
 
 
+def _busy(torch, stream, ms=40):
+    """Keeps a stream busy for about `ms` (a matrix product of 0.1 ms and more, many times)."""
+    a = torch.zeros(4096, 4096, dtype=torch.bfloat16, device="cuda")
+    torch.mm(a, a)
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        for _ in range(10 * ms):
+            torch.mm(a, a)
+    a.record_stream(stream)
+
+
+@pytest.mark.parametrize("op", ["quantize", "dequantize", "linear"])
+def test_tensors_dropped_while_another_stream_needs_them(op):
+    """Operands, weights and outputs of a call on a busy stream are not given out again until it is done."""
+    torch = torch_cuda()
+    ops = _ops()
+    side = torch.cuda.Stream()
+    q0, _ = _random_fp4(torch, 512, 1024, "nvfp4", 12)
+    x0 = torch.randn(512, 1024, device="cuda").to(torch.bfloat16)
+    bias0 = torch.randn(512, device="cuda")
+    want = {"quantize": lambda: ops.fp4_dequantize(ops.fp4_quantize(x0)), "dequantize": lambda: ops.fp4_dequantize(q0),
+            "linear": lambda: ops.fp4_linear(x0, q0, bias=bias0)}[op]()
+    torch.cuda.synchronize()
+    _busy(torch, side)
+    mine = [x0.clone(), bias0.clone(), q0.codes.clone(), q0.scales.clone(), q0.global_scale.clone()]
+    sizes = [t.numel() * t.element_size() for t in mine]
+    x, bias, q = mine[0], mine[1], ops.FP4Weight(*mine[2:])
+    side.wait_stream(torch.cuda.current_stream())
+    if op == "quantize":
+        kept = ops.fp4_quantize(x, stream=side)
+    elif op == "dequantize":
+        kept = ops.fp4_dequantize(q, stream=side)
+    else:
+        kept = ops.fp4_linear(x, q, bias=bias, stream=side)
+    used = {"quantize": mine[:1], "dequantize": mine[2:], "linear": mine}[op]
+    used = [t.data_ptr() for t in used]
+    del x, bias, q, mine
+    new = [torch.full((n,), 0x7F, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(4)]
+    assert not side.query(), "the stream was not busy long enough to tell"
+    assert not {t.data_ptr() for t in new} & set(used)
+    torch.cuda.synchronize()
+    assert torch.equal(ops.fp4_dequantize(kept) if op == "quantize" else kept, want)
+
+
+def test_no_rows_on_a_given_stream():
+    torch = torch_cuda()
+    ops = _ops()
+    side = torch.cuda.Stream()
+    q = ops.fp4_quantize(torch.empty(0, 64, device="cuda"), stream=side)
+    assert ops.fp4_dequantize(q, stream=side).shape == (0, 64)
+    assert ops.fp4_linear(torch.empty(2, 64, device="cuda", dtype=torch.bfloat16), q, stream=side).shape == (2, 0)
+    side.synchronize()
+
+
 # ---- more threads than one launch has (2^32) ----------------------------------------
 
 def _rows_of(q, a, b):

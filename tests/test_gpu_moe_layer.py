@@ -453,3 +453,34 @@ def test_sigmoid_weights_far_below_zero(M, E, base):
     v = np.exp(top - top.max()) / (1.0 + np.exp(top))
     # exponentials of exact differences, a reciprocal, a sum of six and a division, a few steps each
     assert np.abs(w - 2.0 * v / v.sum()).max() <= 2.0 * 16 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("given", [True, False])
+@pytest.mark.parametrize("M", [1, 5])
+def test_a_layer_dropped_while_another_stream_works_on_it(M, given):
+    """Its workspace and weights, and the call's operand, are not given out again until the stream is done."""
+    torch = torch_cuda()
+    case = Case(M, 512, 192, 24, 4, Is=128)
+    want = case.run()[0]
+    side = torch.cuda.Stream()
+    a = torch.zeros(4096, 4096, dtype=torch.bfloat16, device="cuda")
+    torch.mm(a, a)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(400):
+            torch.mm(a, a)
+    x = case.tx
+    mine = [v for v in case.args.values() if torch.is_tensor(v)] + [case.layer.workspace] + ([x] if given else [])
+    mine = [(t.data_ptr(), t.numel() * t.element_size()) for t in mine]
+    if given:
+        y = case.layer.forward(x, stream=side)
+        del x
+    else:
+        with torch.cuda.stream(side):
+            y = case.layer.forward(x)
+    del case
+    new = [torch.full((n,), 0x7F, dtype=torch.uint8, device="cuda") for _, n in mine for _ in range(4)]
+    assert not side.query(), "the stream was not busy long enough to tell"
+    assert not {t.data_ptr() for t in new} & {p for p, _ in mine}
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
