@@ -359,8 +359,8 @@ __device__ __forceinline__ Routed route_row(const MoeArgs& a, int32_t* error, in
   if (on) {
     const int p = m * a.k + lane;
     put(&a.picks[p], (uint64_t)(uint32_t)(my_id + 1) << 32 | __float_as_uint(w));
-    if (a.ids_out) a.ids_out[p] = my_id;
-    if (a.w_out) a.w_out[p] = w;
+    if (a.ids_out) put(&a.ids_out[p], my_id);
+    if (a.w_out) put(&a.w_out[p], w);
   }
   return kDone;
 }
@@ -399,10 +399,12 @@ __device__ __forceinline__ void split3(f32x4 v, uint8_t* dst, int part_bytes) {
         u32x2{p[t][0] | (uint32_t)p[t][1] << 16, p[t][2] | (uint32_t)p[t][3] << 16};
 }
 
+// Written through, like all that these kernels store: a line of y left in one XCD's L2 could reach memory
+// after the NaN that the block which leaves last, on another XCD, writes for a call that was given up.
 __device__ __forceinline__ void store_y(const MoeArgs& a, int m, int r, float v) {
   const int64_t o = m * a.ldy + r;
-  if (a.out == SC_DTYPE_F32) static_cast<float*>(a.y)[o] = v;
-  else static_cast<uint16_t*>(a.y)[o] = __builtin_bit_cast(uint16_t, (__bf16)v);
+  if (a.out == SC_DTYPE_F32) put(static_cast<float*>(a.y) + o, v);
+  else put(static_cast<uint16_t*>(a.y) + o, __builtin_bit_cast(uint16_t, (__bf16)v));
 }
 
 // A phase's tasks as one block takes them: task t is number t / 16 of part t % 16.
@@ -442,7 +444,8 @@ struct Taker {
     return __builtin_amdgcn_readfirstlane(*tick);
   }
 };
-// After a call that was given up: y is NaN, and what is handed over is cleared.
+// After a call that was given up, by the block that leaves last (the others' stores have been performed): y is
+// NaN, and what is handed over is cleared.
 __device__ __forceinline__ void abandon(const MoeArgs& a) {
   for (int i = threadIdx.x; i < a.M * a.H; i += blockDim.x) store_y(a, i / a.H, i % a.H, NAN);
   for (int i = threadIdx.x; i < a.logit_words; i += blockDim.x) put(&a.logits[i], kNoLogit);
