@@ -267,11 +267,13 @@ class MoELayer(_Fixed):
 
     The layer owns a workspace: calls have to be ordered with each other (one
     stream, or streams the caller orders); use one layer object per stream
-    otherwise.  A layer may be dropped while calls are under way, but not while a
+    otherwise.  A call that waits for over a second because another one runs on
+    the workspace gives up and returns NaN; prepare() makes the workspace ready
+    again once both are done.  A layer may be dropped while calls are under way, but not while a
     captured graph is to be replayed."""
 
     _fixed = frozenset(("hidden", "inter", "n_experts", "top_k", "shared_inter", "max_rows", "device", "workspace",
-                        "_memory", "_streams", "_cfg", "_cref", "_w", "_wref"))
+                        "_memory", "_streams", "_ws", "_cfg", "_cref", "_w", "_wref"))
 
     def __init__(self, hidden, inter, top_k, router, blobs, global_scales, shared_blob=None,
                  shared_global_scales=None, score="softmax", score_bias=None, routed_scale=1.0, max_rows=16):
@@ -317,8 +319,22 @@ class MoELayer(_Fixed):
         with _On(dev, None) as s:
             self.workspace = torch.empty(n, dtype=torch.uint8, device=dev)
             self._memory.append(self.workspace.detach())
-            B.moe_layer_prepare(self._cref, self.workspace.data_ptr(), s)
+            self._ws = self.workspace.data_ptr()
+            B.moe_layer_prepare(self._cref, self._ws, s)
             torch.cuda.current_stream(dev).synchronize()
+
+    def _used_on(self, s):
+        """The layer may be dropped while the current stream (raw: s) works on it."""
+        if s not in self._streams:
+            _record(torch.cuda.current_stream(self.device), *self._memory)
+            self._streams.add(s)
+
+    def prepare(self, stream=None):
+        """Clears the workspace's control words, as the constructor does: needed only after calls that ran on
+        the layer at once, when all of them are done."""
+        with _On(self.device, stream) as s:
+            B.moe_layer_prepare(self._cref, self._ws, s)
+            self._used_on(s)
 
     def forward(self, x, out_dtype=torch.float32, out=None, ids=None, weights=None, stream=None):
         """y [M, hidden] for x bf16 [M, hidden], M <= max_rows.  out_dtype float32 or bfloat16.  ids int32 and
@@ -339,13 +355,10 @@ class MoELayer(_Fixed):
                 _matrix(out, "out", (torch.float32, torch.bfloat16))
                 _check_ld(out, "out")
                 _need(tuple(out.shape) == (M, self.hidden) and out.device == dev, "out does not fit")
-            B.moe_layer_forward(self._cref, self._wref, self.workspace.data_ptr(), x.data_ptr(), _ld(x), M,
+            B.moe_layer_forward(self._cref, self._wref, self._ws, x.data_ptr(), _ld(x), M,
                                 out.data_ptr(), _TYPE[out.dtype], _ld(out), None if ids is None else ids.data_ptr(),
                                 None if weights is None else weights.data_ptr(), s)
-            if s not in self._streams:
-                # the layer may be dropped while the stream works on it
-                _record(torch.cuda.current_stream(dev), *self._memory)
-                self._streams.add(s)
+            self._used_on(s)
         if stream is not None:
             _record(stream, x, out, ids, weights)
         return out

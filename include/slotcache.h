@@ -433,8 +433,11 @@ typedef struct {
 /* Bytes of device workspace that moe_layer_forward needs. */
 SC_API sc_status moe_layer_workspace_bytes(const sc_moe_config* cfg, size_t* bytes);
 
-/* Enqueues the clearing of a new workspace's control words (256-byte aligned).
- * Once per workspace, before its first forward call; not needed between calls. */
+/* Enqueues the clearing of a workspace's control words (256-byte aligned), whose
+ * places follow from the configuration: once per workspace and configuration,
+ * max_rows included, before the first forward call with it; not needed between
+ * calls.  Also after forward calls that ran on one workspace without being
+ * ordered, once all of them are done. */
 SC_API sc_status moe_layer_prepare(const sc_moe_config* cfg, void* d_workspace, void* stream);
 
 /* One layer for M rows of x (bf16 [M][H], row stride ldx): y [M][H] (fp32 or
@@ -448,7 +451,8 @@ SC_API sc_status moe_layer_prepare(const sc_moe_config* cfg, void* d_workspace, 
  * workspace must be ordered (one stream, or streams that the caller orders);
  * y must not overlap x.  Blocks wait for each other's results; a wait that lasts
  * over a second (only calls that break that order can do this) gives the call up: y
- * is NaN then, and moe_layer_prepare has to be called before the next use. */
+ * is NaN then, d_ids and d_weights are undefined, and the control words are as
+ * after moe_layer_prepare unless the other call changed them since. */
 SC_API sc_status moe_layer_forward(const sc_moe_config* cfg, const sc_moe_weights* w, void* d_workspace,
                                    const uint16_t* d_x, int64_t ldx, int32_t M, void* d_y, int32_t y_type,
                                    int64_t ldy, int32_t* d_ids, float* d_weights, void* stream);

@@ -484,3 +484,14 @@ def test_a_layer_dropped_while_another_stream_works_on_it(M, given):
     assert not {t.data_ptr() for t in new} & {p for p, _ in mine}
     torch.cuda.synchronize()
     assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("M", [1, 3, 9])
+def test_prepare_makes_a_workspace_ready(M):
+    torch = torch_cuda()
+    case = Case(M, 320, 192, 20, 3, Is=64)
+    want = case.run()[0]
+    for fill in (0x00, 0x5A, 0xFF):
+        case.layer.workspace.fill_(fill)
+        case.layer.prepare()
+        assert torch.equal(case.run()[0], want)
