@@ -1,7 +1,8 @@
 """Operators on 4-bit weights over torch tensors.
 
 torch supplies device memory and streams; the work is done by the library's
-HIP kernels.  The operators are for inference: nothing records a gradient.
+HIP kernels.  The operators are for inference: their results have no gradient,
+and going backward through one raises NotImplementedError.
 Calls are asynchronous on `stream` (the current stream of the
 tensors' device if None) and can be captured into a graph.  What a call
 allocates belongs to its stream.  Tensors given to a call with `stream` may be
@@ -76,6 +77,23 @@ def _ld(t):
 
 def _check_ld(t, name):
     _need(t.shape[0] <= 1 or t.stride(0) >= t.shape[1], "%s has rows that overlap" % name)
+
+
+class _ForInference(torch.autograd.Function):
+    """call(), on behalf of inputs some of which require a gradient."""
+
+    @staticmethod
+    def forward(ctx, name, call, *inputs):
+        ctx.name = name
+        return call()
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise NotImplementedError("%s is for inference: it has no gradient" % ctx.name)
+
+
+def _wants_grad(*tensors):
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
 
 
 class _Fixed:
@@ -207,7 +225,10 @@ def fp4_dequantize(q, dtype=torch.float32, out=None, stream=None):
 
 def fp4_linear(x, q, bias=None, out_dtype=None, out=None, stream=None):
     """x [M, cols] (bfloat16 or float16) times the transpose of q [rows, cols],
-    plus bias fp32 [rows]; [M, rows] of out_dtype (default: x's type)."""
+    plus bias fp32 [rows]; [M, rows] of out_dtype (default: x's type), or in out,
+    which must not overlap x (and takes no part in a gradient)."""
+    if out is None and _wants_grad(x, bias):
+        return _ForInference.apply("fp4_linear", lambda: fp4_linear(x, q, bias, out_dtype, None, stream), x, bias)
     _matrix(x, "x", (torch.bfloat16, torch.float16))
     dev = x.device
     M = x.shape[0]
@@ -310,6 +331,7 @@ class MoELayer(_Fixed):
 
         self._memory = [t.detach() for t in (router, blobs, global_scales, shared_blob, shared_global_scales, score_bias)
                         if t is not None]
+        self._grads = (router, global_scales, shared_global_scales, score_bias)
         self._streams = set()        # that the memory is recorded on
         self._w = B.sc_moe_weights(ptr(router), ptr(score_bias), ptr(blobs), ptr(global_scales), ptr(shared_blob),
                                    ptr(shared_global_scales))
@@ -338,7 +360,11 @@ class MoELayer(_Fixed):
 
     def forward(self, x, out_dtype=torch.float32, out=None, ids=None, weights=None, stream=None):
         """y [M, hidden] for x bf16 [M, hidden], M <= max_rows.  out_dtype float32 or bfloat16.  ids int32 and
-        weights float32 [M, top_k], if given, receive the picks and their weights in rank order."""
+        weights float32 [M, top_k], if given, receive the picks and their weights in rank order.  out, if given,
+        must not overlap x (and takes no part in a gradient)."""
+        if out is None and _wants_grad(x, *self._grads):
+            return _ForInference.apply("MoELayer.forward",
+                                       lambda: self.forward(x, out_dtype, None, ids, weights, stream), x, *self._grads)
         _matrix(x, "x", (torch.bfloat16,))
         _check_ld(x, "x")
         M, dev = x.shape[0], self.device

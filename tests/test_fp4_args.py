@@ -116,3 +116,17 @@ def test_what_a_layer_was_made_of_cannot_be_exchanged():
         with pytest.raises(AttributeError, match=name):
             setattr(layer, name, 5)
         assert getattr(layer, name) == value
+
+
+def test_going_backward_through_an_operator_raises():
+    import torch
+
+    from hbm_expert_slot_amd import ops
+    x = torch.ones(3, requires_grad=True)
+    y = ops._ForInference.apply("fp4_linear", lambda: torch.zeros(2), x, None)
+    y.add_(1)
+    with pytest.raises(NotImplementedError, match="fp4_linear is for inference"):
+        (y.sum() + x.sum()).backward()
+    assert ops._wants_grad(None, x) and not ops._wants_grad(None, x.detach())
+    with torch.no_grad():
+        assert not ops._wants_grad(x)

@@ -386,6 +386,24 @@ def test_no_rows_on_a_given_stream():
     side.synchronize()
 
 
+def test_linear_has_no_gradient_and_says_so():
+    """Not a result that looks like one of constants: a layer in front of it would silently not be trained."""
+    torch = torch_cuda()
+    ops = _ops()
+    q, _ = _random_fp4(torch, 40, 256, "nvfp4", 2)
+    x, bias = torch.randn(3, 256, device="cuda").to(torch.bfloat16), torch.randn(40, device="cuda")
+    want = ops.fp4_linear(x, q, bias=bias, out_dtype=torch.float32)
+    for a, b in ((x.clone().requires_grad_(), bias), (x, bias.clone().requires_grad_())):
+        y = ops.fp4_linear(a, q, bias=b, out_dtype=torch.float32)
+        assert torch.equal(y, want) and y.requires_grad
+        with pytest.raises(NotImplementedError):
+            y.sum().backward()
+        with torch.no_grad():
+            assert not ops.fp4_linear(a, q, bias=b).requires_grad
+        assert torch.equal(ops.fp4_linear(a, q, bias=b, out=torch.empty_like(want)), want)
+    assert not want.requires_grad
+
+
 # ---- more threads than one launch has (2^32) ----------------------------------------
 
 def _rows_of(q, a, b):

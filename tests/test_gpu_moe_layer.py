@@ -495,3 +495,23 @@ def test_prepare_makes_a_workspace_ready(M):
         case.layer.workspace.fill_(fill)
         case.layer.prepare()
         assert torch.equal(case.run()[0], want)
+
+
+def test_a_layer_has_no_gradient_and_says_so():
+    torch = torch_cuda()
+    from hbm_expert_slot_amd.ops import MoELayer
+    case = Case(3, 320, 192, 20, 3, Is=64)
+    want, want_ids, _ = case.run()
+    assert not want.requires_grad
+    y, ids, _ = case.run(case.tx.clone().requires_grad_())
+    assert torch.equal(y, want) and torch.equal(ids, want_ids)
+    with pytest.raises(NotImplementedError):
+        y.sum().backward()
+    args = dict(case.args, router=torch.nn.Parameter(case.args["router"]))
+    layer = MoELayer(320, 192, 3, **args)
+    y = layer.forward(case.tx)
+    assert torch.equal(y, want)
+    with pytest.raises(NotImplementedError):
+        y.sum().backward()
+    with torch.no_grad():
+        assert not layer.forward(case.tx).requires_grad
