@@ -21,8 +21,12 @@ _FORMAT = {"nvfp4": B.SC_FP4_NV, "mxfp4": B.SC_FP4_MX}
 GROUP = {"nvfp4": 16, "mxfp4": 32}
 
 
-# the handle alone: torch.cuda.current_stream also makes an object, which costs 1.8 us
-_raw_stream = torch._C._cuda_getCurrentRawStream
+def _stream_handle(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# the handle alone, where torch has it: torch.cuda.current_stream also makes an object, which costs 1.8 us
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_handle)
 
 
 class _On:

@@ -130,3 +130,19 @@ def test_going_backward_through_an_operator_raises():
     assert ops._wants_grad(None, x) and not ops._wants_grad(None, x.detach())
     with torch.no_grad():
         assert not ops._wants_grad(x)
+
+
+def test_a_torch_without_the_raw_stream_call(monkeypatch):
+    import importlib.util
+
+    import torch
+
+    from hbm_expert_slot_amd import ops
+    if hasattr(torch._C, "_cuda_getCurrentRawStream"):
+        assert ops._raw_stream is torch._C._cuda_getCurrentRawStream
+        monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
+    spec = importlib.util.spec_from_file_location("hbm_expert_slot_amd.ops_again", ops.__file__)
+    again = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(again)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda index: type("Stream", (), {"cuda_stream": 77 + index})())
+    assert again._raw_stream(3) == 80
