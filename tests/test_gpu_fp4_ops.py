@@ -404,6 +404,44 @@ def test_linear_has_no_gradient_and_says_so():
     assert not want.requires_grad
 
 
+# nb blocks of weight rows, a multiple of eight, that each meet several blocks of operand rows; every tile size
+BLOCKS = [(20, 1024), (48, 2048), (128, 2048), (128, 4096), (256, 6144), (520, 6144), (1040, 12288)]
+
+
+@pytest.mark.parametrize("x_type,fmt", [("bf16", "nvfp4"), ("fp16", "mxfp4"), ("fp16", "nvfp4")])
+@pytest.mark.parametrize("M,N", BLOCKS)
+def test_linear_blocks_that_share_weight_rows(M, N, x_type, fmt):
+    """Every tile of the output is written, and by the rows it belongs to."""
+    torch = torch_cuda()
+    K = 144 if fmt == "nvfp4" else 160
+    log("linear blocks", M, N, K, fmt, x_type)
+    q, w = _random_fp4(torch, N, K, fmt, M + N)
+    x = torch.randn(M, K, generator=torch.Generator().manual_seed(K)).to(getattr(torch, TYPES[x_type]))
+    out = torch.full((M, N), float("nan"), device="cuda")
+    _ops().fp4_linear(x.cuda(), q, out=out)
+    wt = torch.tensor(w).t()
+    want, mag = x.double() @ wt, x.double().abs() @ wt.abs()
+    # as above: 32 products of an instruction, the chunks, eight groups, the scale of the matrix
+    tol = (32 + K / 32 + 8 + 1) * 2.0 ** -24 * mag + 1e-37
+    err = (out.double().cpu() - want).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
+
+
+# more groups than the threads of the grid, and more bytes than its blocks take at once; odd row counts
+@pytest.mark.parametrize("fmt,rows,cols,dtype", [("nvfp4", 1409, 4112, "bf16"), ("nvfp4", 2579, 2080, "fp32"),
+                                                 ("mxfp4", 2579, 2080, "fp32"), ("mxfp4", 1409, 4128, "fp16")])
+@pytest.mark.parametrize("strided", [False, True])
+def test_quantize_more_groups_than_threads(fmt, rows, cols, dtype, strided):
+    torch = torch_cuda()
+    log("quantize", fmt, rows, cols, dtype, strided)
+    big = _weights(torch, rows, cols + 24, dtype, rows)
+    w = big[:, 5:5 + cols] if strided else big[:, :cols].contiguous()
+    w[rows - 1, cols - 1] = 9.0                # the matrix's largest
+    w[rows - 2, cols - 40] = float("nan")
+    w[rows - 1, 3] = float("inf")
+    _check_quant(torch, w, _ops().fp4_quantize(w, fmt), fmt)
+
+
 # ---- more threads than one launch has (2^32) ----------------------------------------
 
 def _rows_of(q, a, b):
