@@ -82,3 +82,27 @@ def test_python_refusals():
         ops.MoELayer(128, 64, 2, r, b, g)
     with pytest.raises(ValueError, match="blob"):
         ops.expert_matrices(b[0, 1:], 64, 64, g[0])
+
+
+def test_places_of_the_control_words(tmp_path):
+    """The GPU test of a call that gives up marks a word of the one-row kernel, whose place it spells out: the sources
+    agree with it (on another word the mark would do something else)."""
+    import os
+    import shutil
+    import subprocess
+
+    from hbm_expert_slot_amd import build
+    cc = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
+    if not os.path.exists(cc):
+        pytest.skip("hipcc not available")
+    claims = 5 * 16 * 32 + 2 * 32 + (513 + 32) // 32 * 32 + 1024 + 513 * 32
+    with open(os.path.join(os.path.dirname(__file__), "test_gpu_moe_layer.py")) as f:
+        assert "5 * 16 * 32 + 2 * 32 + (513 + 32) // 32 * 32 + 1024 + 513 * 32" in f.read()
+    for name, claim in (("moe_layer", "sc::kLayerWords == %d" % claims),
+                        ("moe_layer", "offsetof(sc::MoeWs, ctl) == 0"), ("moe_one", "sc::moe::O_CLAIM == 0")):
+        src = tmp_path / "places.hip"
+        src.write_text('#include "%s.hip"\nstatic_assert(%s, "");\n' % (name, claim))
+        r = subprocess.run([cc] + build.FLAGS + ["-I" + os.path.join(build.HERE, "csrc"), "--cuda-device-only",
+                                                 "-fsyntax-only", str(src)],
+                           stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+        assert r.returncode == 0, (claim, r.stdout[-2000:])
