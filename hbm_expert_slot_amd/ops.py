@@ -97,7 +97,10 @@ class _ForInference(torch.autograd.Function):
 
 
 def _wants_grad(*tensors):
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            return torch.is_grad_enabled()
+    return False
 
 
 class _Fixed:
@@ -142,12 +145,14 @@ class FP4Weight(_Fixed):
             _need(fmt == "nvfp4", "only nvfp4 has a global scale")
             _need(global_scale.dtype == torch.float32 and global_scale.numel() == 1
                   and global_scale.device == codes.device, "global_scale must be one float32 with the codes")
-        self.codes, self.scales, self.global_scale, self.fmt = codes, scales, global_scale, fmt
-        self.rows, self.cols, self.device = rows, cols, codes.device
-        self._memory = [t.untyped_storage() for t in (codes, scales, global_scale) if t is not None]
-        self._c = B.sc_fp4_matrix(_FORMAT[fmt], rows, cols, codes.data_ptr(), scales.data_ptr(),
-                                  None if global_scale is None else global_scale.data_ptr())
-        self._ref = ctypes.byref(self._c)
+        memory = [codes.untyped_storage(), scales.untyped_storage()]
+        if global_scale is not None:
+            memory.append(global_scale.untyped_storage())
+        c = B.sc_fp4_matrix(_FORMAT[fmt], rows, cols, codes.data_ptr(), scales.data_ptr(),
+                            None if global_scale is None else global_scale.data_ptr())
+        # all at once, past the check of each name
+        self.__dict__.update(codes=codes, scales=scales, global_scale=global_scale, fmt=fmt, rows=rows, cols=cols,
+                             device=codes.device, _memory=memory, _c=c, _ref=ctypes.byref(c))
 
     @property
     def shape(self):
@@ -231,7 +236,7 @@ def fp4_linear(x, q, bias=None, out_dtype=None, out=None, stream=None):
     """x [M, cols] (bfloat16 or float16) times the transpose of q [rows, cols],
     plus bias fp32 [rows]; [M, rows] of out_dtype (default: x's type), or in out,
     which must not overlap x (and takes no part in a gradient)."""
-    if out is None and _wants_grad(x, bias):
+    if (x.requires_grad or bias is not None) and out is None and _wants_grad(x, bias):
         return _ForInference.apply("fp4_linear", lambda: fp4_linear(x, q, bias, out_dtype, None, stream), x, bias)
     _matrix(x, "x", (torch.bfloat16, torch.float16))
     dev = x.device
@@ -335,7 +340,7 @@ class MoELayer(_Fixed):
 
         self._memory = [t.detach() for t in (router, blobs, global_scales, shared_blob, shared_global_scales, score_bias)
                         if t is not None]
-        self._grads = (router, global_scales, shared_global_scales, score_bias)
+        self._grads = [t for t in (router, global_scales, shared_global_scales, score_bias) if t is not None]
         self._streams = set()        # that the memory is recorded on
         self._w = B.sc_moe_weights(ptr(router), ptr(score_bias), ptr(blobs), ptr(global_scales), ptr(shared_blob),
                                    ptr(shared_global_scales))
@@ -350,17 +355,17 @@ class MoELayer(_Fixed):
             torch.cuda.current_stream(dev).synchronize()
 
     def _used_on(self, s):
-        """The layer may be dropped while the current stream (raw: s) works on it."""
-        if s not in self._streams:
-            _record(torch.cuda.current_stream(self.device), *self._memory)
-            self._streams.add(s)
+        """The layer may be dropped while the current stream (raw: s, not in _streams yet) works on it."""
+        _record(torch.cuda.current_stream(self.device), *self._memory)
+        self._streams.add(s)
 
     def prepare(self, stream=None):
         """Clears the workspace's control words, as the constructor does: needed only after calls that ran on
         the layer at once, when all of them are done."""
         with _On(self.device, stream) as s:
             B.moe_layer_prepare(self._cref, self._ws, s)
-            self._used_on(s)
+            if s not in self._streams:
+                self._used_on(s)
 
     def forward(self, x, out_dtype=torch.float32, out=None, ids=None, weights=None, stream=None):
         """y [M, hidden] for x bf16 [M, hidden], M <= max_rows.  out_dtype float32 or bfloat16.  ids int32 and
@@ -388,7 +393,8 @@ class MoELayer(_Fixed):
             B.moe_layer_forward(self._cref, self._wref, self._ws, x.data_ptr(), _ld(x), M,
                                 out.data_ptr(), _TYPE[out.dtype], _ld(out), None if ids is None else ids.data_ptr(),
                                 None if weights is None else weights.data_ptr(), s)
-            self._used_on(s)
+            if s not in self._streams:
+                self._used_on(s)
         if stream is not None:
             _record(stream, x, out, ids, weights)
         return out
