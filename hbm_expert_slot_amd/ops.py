@@ -112,7 +112,7 @@ class _Fixed:
     def __setattr__(self, name, value):
         if name in self._fixed and name in self.__dict__:
             raise AttributeError("%s of a %s is fixed when it is made" % (name, type(self).__name__))
-        self.__dict__[name] = value
+        object.__setattr__(self, name, value)
 
     def __delattr__(self, name):
         if name in self._fixed:

@@ -146,3 +146,11 @@ def test_a_torch_without_the_raw_stream_call(monkeypatch):
     spec.loader.exec_module(again)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda index: type("Stream", (), {"cuda_stream": 77 + index})())
     assert again._raw_stream(3) == 80
+
+
+def test_a_weights_shape_is_no_attribute_to_set():
+    from hbm_expert_slot_amd import ops
+    q = _made(ops.FP4Weight, rows=4, cols=16)
+    with pytest.raises(AttributeError):
+        q.shape = (8, 16)
+    assert q.shape == (4, 16) and "shape" not in vars(q)
