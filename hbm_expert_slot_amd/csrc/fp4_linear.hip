@@ -393,7 +393,11 @@ hipError_t launch_tiles(LinearArgs a, hipStream_t st) {
 // 15.0 / 20 / 31, 256 rows - / - / - / 23.8 / 20.8 / 31, 1024 rows - / - / - / 92 /
 // 62 / 54.  Two blocks of 64x64 share a unit.  Tiles of 128x192, which widen least,
 // pay from two blocks per unit on (6144 x 6144, 1024 rows: 256 blocks, 114 against
-// 107 with 64x128; 2048 rows: 163 against 218).
+// 107 with 64x128; 2048 rows: 163 against 218).  The sweep was made for this format
+// and type only; the others take the same sizes.  6144 x 6144 with 16 / 64 / 256 /
+// 1024 / 2048 rows, caches cold: NVFP4 bf16 16.4 / 29.3 / 54.8 / 119 / 174, NVFP4
+// fp16 16.2 / 29.3 / 55.5 / 118 / 168, MXFP4 bf16 16.0 / 28.5 / 54.8 / 116 / 156, MXFP4
+// fp16, with twice the products, 18.0 / 33.3 / 117 / 229 / 398.
 template <int FMT, bool ODD, bool HALF>
 hipError_t by_count(const LinearArgs& a, hipStream_t st) {
   constexpr bool kTwo = HALF && FMT == kMx;        // operand in two parts: twice the LDS

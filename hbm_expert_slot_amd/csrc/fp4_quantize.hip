@@ -8,10 +8,10 @@
 // quotient of rounded numbers next to a border is settled in fp64.
 //
 // The max and the codes need one pass each; the second finds a matrix of up to
-// 256 MB in the memory-side cache.  6144 x 4096 bf16: max 19 us (2.6 TB/s from
-// HBM, which more loads under way, wider blocks or fewer instructions leave as it
-// is), codes 21 us (vector instructions: 32 products, 16 conversions and an fp64
-// quotient per 16 elements), reading back 16.5 us (3.9 TB/s).
+// 256 MB in the memory-side cache.  4096 x 6144 bf16: max 10.6 us (4.7 TB/s; 19 us
+// after 1 GiB of stores, which that cache then still has to write back), codes 25
+// us (vector instructions: 32 products, 16 conversions and an fp64 quotient per 16
+// elements), reading back to fp32 17.7 us (6.5 TB/s, into that cache).
 #include "fp4_device.h"
 #include "internal.h"
 

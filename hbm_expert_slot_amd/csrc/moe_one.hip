@@ -16,7 +16,9 @@
 //
 // Block b takes share b.  A wait that lasts looks for a share that no block has
 // claimed and does it too, so that it ends even if some blocks never start (two
-// such layers at once may each hold half of the machine).
+// such layers at once may each hold half of the machine).  A pair of calls at the
+// size above: 104 us on two streams (up to 169 seen), 107 on one; a call beside
+// 4096 x 4096 x 4096 products on another stream 149 us, alone 57.
 //
 // Loads return in order within a wavefront, so whoever polls or fetches h must
 // have no weights on their way: the first four wavefronts do that, the other
