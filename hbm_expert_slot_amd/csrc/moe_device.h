@@ -13,6 +13,9 @@
 #include "fp4_device.h"
 #include "internal.h"
 
+#include <limits>
+#include <type_traits>
+
 namespace sc {
 namespace moe {
 
@@ -183,6 +186,11 @@ __device__ __forceinline__ void router_tile_mfma(const MoeArgs& a, int tile, flo
 }
 
 // Keys that order as the scores do: NaN below -inf, -0 equal to +0.
+__device__ __forceinline__ int order_key(float z) {
+  if (z != z) return INT32_MIN + 1;
+  const int b = (int)__float_as_uint(z + 0.0f);
+  return b >= 0 ? b : b ^ 0x7FFFFFFF;
+}
 __device__ __forceinline__ int64_t order_key(double z) {
   if (z != z) return INT64_MIN + 1;
   const int64_t b = __double_as_longlong(z + 0.0);
@@ -193,12 +201,23 @@ __device__ __forceinline__ int64_t order_key(double z) {
 // also where they are one fp32 number (from 17.3 on all are 1).  With one the sum is
 // formed in fp64 from the sigmoid's distance to 0 or 1, t / (1 + t) with t =
 // exp(-|z|), whose relative error of |z| 2^-23 and a few steps is the logit's own.
-__device__ __forceinline__ double pick_score(const MoeArgs& a, float z, float bias) {
-  if (!a.score_bias) return z;
+// In the kernels of up to four rows its fp32 rounding settles nearly every pick, and
+// where two of those agree, exact_picks does: one row, 8 of 1000 experts of 1024 x 256,
+// 24.3 us, with a bias 25.1 (26.4 and 27.3 with 64-bit keys throughout).  The kernel of
+// more rows has 64-bit keys: the call would cost its products registers (16 rows, 4 of
+// 16 experts of 6144 x 2048: 135 us, 141 with the call).
+__device__ __forceinline__ double exact_score(float z, float bias) {
   const float y = fabsf(z) * -1.4426950408889634f, n = __builtin_rintf(fmaxf(y, -2000.0f));
   const double t = ldexp((double)__builtin_amdgcn_exp2f(y - n), (int)n);
   const double d = t * (double)__builtin_amdgcn_rcpf(1.0f + (float)t);
   return (z > 0.0f ? 1.0 - d : z == z ? d : (double)z) + (double)bias;
+}
+template <typename Key>
+__device__ __forceinline__ Key pick_key(const MoeArgs& a, float z, float bias) {
+  if constexpr (sizeof(Key) == 8) return order_key(a.score_bias ? exact_score(z, bias) : (double)z);
+  if (!a.score_bias) return order_key(z);
+  const float t = __builtin_amdgcn_exp2f(fabsf(z) * -1.4426950408889634f), d = t * __builtin_amdgcn_rcpf(1.0f + t);
+  return order_key((float)((double)bias + (z > 0.0f ? 1.0 - (double)d : (double)d)));
 }
 
 // Reductions over the wavefront in registers: halves and 16-lane rows trade by
@@ -223,15 +242,63 @@ __device__ __forceinline__ float wave_sum_f(float v) {
   }));
 }
 
-// One wavefront picks row m's experts and publishes them.  Lane l looks after
+// The lanes that have the largest key: by its upper half, then by the lower.  Every
+// lane takes part in both reductions.
+__device__ __forceinline__ uint64_t top_lanes(int64_t key) {
+  const int hi = (int)(key >> 32), most_hi = wave_max_i(hi);
+  const bool in = hi == most_hi;
+  const uint64_t top = __ballot(in);
+  if (!(top & (top - 1))) return top;
+  const int lo = in ? (int)((uint32_t)key ^ 0x80000000u) : INT32_MIN, most_lo = wave_max_i(lo);
+  return __ballot(in && lo == most_lo);
+}
+
+// The k experts of largest sigmoid and bias in fp64, one per lane; lane l looks
+// after experts l * epl .. of the logits in LDS.  Not inlined: it hardly ever runs,
+// and costs the kernels no registers.
+static __device__ __noinline__ int exact_picks(const float* logits, const float* bias, int E, int k) {
+  constexpr int EPL = kMaxExperts / 64;
+  const int lane = fresh_lane(), epl = (E + 63) / 64;
+  int64_t key[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int e = lane * epl + i;
+    const bool in = i < epl && e < E;
+    key[i] = in ? order_key(exact_score(logits[in ? e : 0], bias[in ? e : 0])) : INT64_MIN;
+  }
+  int my_id = 0;
+#pragma unroll 1
+  for (int j = 0; j < k; ++j) {
+    int64_t best = key[0];
+    int at = 0;
+#pragma unroll
+    for (int i = 1; i < EPL; ++i)
+      if (key[i] > best) {
+        best = key[i];
+        at = i;
+      }
+    const int src = __builtin_ctzll(top_lanes(best));
+    const int e = src * epl + __builtin_amdgcn_readlane(at, src);
+    if (lane == j) my_id = e;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (lane == src && i == at) key[i] = INT64_MIN;
+  }
+  return my_id;
+}
+
+// One wavefront picks row m's experts, lane j the j-th.  Lane l looks after
 // experts l * epl .. and keeps them sorted (up to eight; more are looked through
 // each time), so that a pick costs one reduction: the lowest lane with the
 // largest key holds the lowest id.  sval: the logits, LDS, [E].  The logits are set back to
 // kNoLogit.  After `patience` polls it returns kLate with nothing done.
 enum Routed { kDone = 0, kLate, kGivenUp };
 template <int EPL, int KS>
-__device__ __forceinline__ Routed route_row(const MoeArgs& a, int32_t* error, int m, float* sval, int patience) {
+__device__ __forceinline__ Routed pick_row(const MoeArgs& a, int32_t* error, int m, float* sval, int patience,
+                                           int& my_id, bool& tied) {
   constexpr bool SORT = EPL <= 8;
+  typedef std::conditional_t<KS == 1, int, int64_t> Key;
+  constexpr Key kNone = std::numeric_limits<Key>::min();
   const int lane = fresh_lane();
   const int epl = (a.E + 63) / 64;
   const Rsrc rl = make_rsrc(a.logits, (uint32_t)(KS * a.M * a.E) * 4);
@@ -272,12 +339,12 @@ __device__ __forceinline__ Routed route_row(const MoeArgs& a, int32_t* error, in
       for (int q = 0; q < QB; ++q)
         sum[i] = q0 + q == 0 ? __uint_as_float(part[i][q]) : sum[i] + __uint_as_float(part[i][q]);
   }
-  int64_t key[EPL];
+  Key key[EPL];
   int id[EPL];
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     const float z = sum[i];
-    const double by = pick_score(a, z, bias[i]);
+    const Key by = pick_key<Key>(a, z, bias[i]);
     id[i] = lane * epl + i;
     const bool in = i < epl && id[i] < a.E;
     if (in) {
@@ -285,7 +352,7 @@ __device__ __forceinline__ Routed route_row(const MoeArgs& a, int32_t* error, in
 #pragma unroll
       for (int q = 0; q < KS; ++q) put(&a.logits[(q * a.M + m) * a.E + id[i]], kNoLogit);
     }
-    key[i] = in ? order_key(by) : INT64_MIN;
+    key[i] = in ? by : kNone;
   }
   if constexpr (SORT) {
 #pragma unroll
@@ -293,7 +360,7 @@ __device__ __forceinline__ Routed route_row(const MoeArgs& a, int32_t* error, in
 #pragma unroll
       for (int i = 0; i < n; ++i) {
         const bool up = key[i + 1] > key[i];       // equal keys keep their order
-        const int64_t k0 = key[i];
+        const Key k0 = key[i];
         const int i0 = id[i];
         key[i] = up ? key[i + 1] : k0;
         id[i] = up ? id[i + 1] : i0;
@@ -301,10 +368,12 @@ __device__ __forceinline__ Routed route_row(const MoeArgs& a, int32_t* error, in
         id[i + 1] = up ? i0 : id[i + 1];
       }
   }
-  int my_id = 0;
+  Key last = kNone;
+  my_id = 0;
+  tied = false;
 #pragma unroll 1
   for (int j = 0; j < a.k; ++j) {
-    int64_t best = key[0];
+    Key best = key[0];
     int at = id[0];
     if constexpr (!SORT) {
 #pragma unroll
@@ -314,13 +383,14 @@ __device__ __forceinline__ Routed route_row(const MoeArgs& a, int32_t* error, in
           at = id[i];
         }
     }
-    const int hi = (int)(best >> 32), first = wave_max_i(hi);
-    uint64_t top = __ballot(hi == first);
-    if (top & (top - 1)) {
-      // lanes that agree in the upper half; every lane takes part in the reduction
-      const bool in = top >> lane & 1;
-      const int lo = in ? (int)((uint32_t)best ^ 0x80000000u) : INT32_MIN, most = wave_max_i(lo);
-      top = __ballot(in && lo == most);
+    uint64_t top;
+    if constexpr (KS == 1) {
+      const int most = wave_max_i(best);
+      tied = tied || most == last;
+      last = most;
+      top = __ballot(best == most);
+    } else {
+      top = top_lanes(best);
     }
     const int src = __builtin_ctzll(top);
     const int e = __builtin_amdgcn_readlane(at, src);
@@ -328,15 +398,38 @@ __device__ __forceinline__ Routed route_row(const MoeArgs& a, int32_t* error, in
     if constexpr (SORT) {
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
-        key[i] = lane == src ? (i + 1 < EPL ? key[i + 1] : INT64_MIN) : key[i];
+        key[i] = lane == src ? (i + 1 < EPL ? key[i + 1] : kNone) : key[i];
         id[i] = lane == src && i + 1 < EPL ? id[i + 1] : id[i];
       }
     } else {
 #pragma unroll
       for (int i = 0; i < EPL; ++i)
-        if (id[i] == e) key[i] = INT64_MIN;
+        if (id[i] == e) key[i] = kNone;
     }
   }
+  if constexpr (KS == 1) {
+    int rest = key[0];
+#pragma unroll
+    for (int i = 1; i < EPL; ++i) rest = max(rest, key[i]);
+    const int next = wave_max_i(rest);
+    tied = tied || next == last;
+  }
+  return kDone;
+}
+
+// One wavefront picks row m's experts and publishes them.
+template <int KS>
+__device__ __forceinline__ Routed route_row(const MoeArgs& a, int32_t* error, int m, float* sval,
+                                            int patience = INT32_MAX) {
+  int my_id;
+  bool tied;      // two of the 32-bit keys picked, or the last of them and the next
+  const Routed r = a.E <= 256   ? pick_row<4, KS>(a, error, m, sval, patience, my_id, tied)
+                   : a.E <= 512 ? pick_row<8, KS>(a, error, m, sval, patience, my_id, tied)
+                                : pick_row<16, KS>(a, error, m, sval, patience, my_id, tied);
+  if (r != kDone) return r;
+  // equal logits are a tie, equal fp32 sums need not be
+  if (KS == 1 && a.score_bias && __ballot(tied)) my_id = exact_picks(sval, a.score_bias, a.E, a.k);
+  const int lane = fresh_lane();
   // weights; NaN counts as the lowest score, picks of +inf share the weight,
   // and picks that all have the lowest score share it too
   const bool on = lane < a.k;
@@ -363,14 +456,6 @@ __device__ __forceinline__ Routed route_row(const MoeArgs& a, int32_t* error, in
     if (a.w_out) put(&a.w_out[p], w);
   }
   return kDone;
-}
-
-template <int KS>
-__device__ __forceinline__ Routed route_row(const MoeArgs& a, int32_t* error, int m, float* sval,
-                                            int patience = INT32_MAX) {
-  if (a.E <= 256) return route_row<4, KS>(a, error, m, sval, patience);
-  if (a.E <= 512) return route_row<8, KS>(a, error, m, sval, patience);
-  return route_row<16, KS>(a, error, m, sval, patience);
 }
 
 // ---- expert products -------------------------------------------------------------
