@@ -515,3 +515,54 @@ def test_a_layer_has_no_gradient_and_says_so():
         y.sum().backward()
     with torch.no_grad():
         assert not layer.forward(case.tx).requires_grad
+
+
+def test_captured_on_a_given_stream_and_dropped():
+    """The whole path on the stream that captures, first calls of a layer among them; tensors dropped while it
+    captures and after it."""
+    torch = torch_cuda()
+    from hbm_expert_slot_amd import ops
+    case = Case(2, 512, 192, 24, 4, Is=64)
+    w = torch.randn(256, 512, device="cuda")
+    side = torch.cuda.Stream()
+    x = case.tx.clone()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        q = ops.fp4_quantize(w, stream=side)
+        y = case.layer.forward(x, out_dtype=torch.bfloat16, stream=side)
+        z = ops.fp4_linear(y, q, out_dtype=torch.float32, stream=side)
+        values = ops.fp4_dequantize(q, stream=side)
+        del y
+    for i in range(4):
+        x.copy_(torch.randn(2, 512, device="cuda").to(torch.bfloat16))
+        eager_q = ops.fp4_quantize(w)
+        want = ops.fp4_linear(case.layer.forward(x, out_dtype=torch.bfloat16), eager_q, out_dtype=torch.float32)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(z, want) and torch.equal(values, ops.fp4_dequantize(eager_q)), i
+    del g, case, x, w, q, z, values
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    again = Case(2, 512, 192, 24, 4, Is=64)
+    again.check(*again.run())
+
+
+H_DONE = 5 * 16 * 32 + 2 * 32      # control word: gate/up tiles of the first expert that are done
+
+
+@pytest.mark.parametrize("M", [4, 9])
+def test_rows_give_up_a_wait_that_does_not_end(M):
+    """An expert whose h is never counted complete: every block leaves after its bounded wait, the result is NaN, and
+    the workspace serves the next call."""
+    torch = torch_cuda()
+    case = Case(M, 576, 192, 20, 3, Is=64)
+    want = case.run()[0]
+    torch.cuda.synchronize()
+    case.layer.workspace.view(torch.int32)[H_DONE] = -1000
+    log("an expert that is never complete", M)
+    y = case.layer.forward(case.tx)
+    torch.cuda.synchronize()
+    assert torch.isnan(y).all()
+    assert torch.equal(case.run()[0], want)

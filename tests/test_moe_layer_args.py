@@ -106,3 +106,21 @@ def test_places_of_the_control_words(tmp_path):
                                                  "-fsyntax-only", str(src)],
                            stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
         assert r.returncode == 0, (claim, r.stdout[-2000:])
+
+
+def test_place_of_the_count_that_a_test_marks(tmp_path):
+    import os
+    import shutil
+    import subprocess
+
+    from hbm_expert_slot_amd import build
+    from test_gpu_moe_layer import H_DONE
+    cc = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
+    if not os.path.exists(cc):
+        pytest.skip("hipcc not available")
+    src = tmp_path / "places.hip"
+    src.write_text('#include "moe_layer.hip"\nstatic_assert(sc::C_HDONE == %d && sc::C_HDONE < sc::C_TILES, "");\n' % H_DONE)
+    r = subprocess.run([cc] + build.FLAGS + ["-I" + os.path.join(build.HERE, "csrc"), "--cuda-device-only",
+                                             "-fsyntax-only", str(src)],
+                       stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    assert r.returncode == 0, r.stdout[-2000:]
