@@ -34,6 +34,15 @@ SC_FP4_QUANT_WORKSPACE_BYTES = 4096
 SC_MOE_MAX_ROWS = 16
 SC_SCORE_SOFTMAX = 0
 SC_SCORE_SIGMOID = 1
+SC_PROMPT_MAX_HEADS = 1024
+SC_PROMPT_MAX_SEQS = 65536
+SC_PROMPT_MAX_ROWS = 1 << 24
+SC_KV4_PAGE = 64
+SC_KV4_MAX_HEADS = 1024
+SC_KV4_MAX_SEQS = 65536
+SC_KV4_MAX_WIDTH = 1 << 24
+SC_KV4_MAX_ROWS = 16
+SC_KV4_MAX_GROUP = 64
 
 EXPORTED = (
     "slotcache_query_sizes", "slotcache_init", "slotcache_backing", "slotcache_set_global_scales",
@@ -41,7 +50,9 @@ EXPORTED = (
     "slotcache_read_state", "slotcache_write_state", "slotcache_read_events",
     "slotcache_read_routing", "slotcache_read_kernel_spans", "slotcache_pin", "slotcache_last_error",
     "slotcache_destroy", "moe_layer_decode_static", "fp4_quantize", "fp4_dequantize", "fp4_linear",
-    "moe_layer_workspace_bytes", "moe_layer_prepare", "moe_layer_forward",
+    "moe_layer_workspace_bytes", "moe_layer_prepare", "moe_layer_forward", "prompt_attention",
+    "kv4_page_bytes", "kv4_append", "kv4_read", "kv4_attention_workspace_bytes", "kv4_attention",
+    "kv4_evict_workspace_bytes", "kv4_evict",
 )
 
 
@@ -97,6 +108,34 @@ class sc_moe_weights(ctypes.Structure):
         "d_router", "d_score_bias", "d_blobs", "d_global_scales", "d_shared_blob", "d_shared_scales")]
 
 
+class sc_prompt(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "type", "head_dim", "q_heads", "kv_heads", "n_seqs", "rows", "keys")] + [("scale", ctypes.c_float)] + [
+        (n, ctypes.c_void_p) for n in ("d_q", "d_k", "d_v", "d_out", "d_lse", "d_starts", "d_key_starts")] + [
+        (n, ctypes.c_int64 * 2) for n in ("q_stride", "k_stride", "v_stride", "out_stride")]
+
+
+class sc_kv4_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("format", "head_dim", "kv_heads", "n_pages")] + [
+        (n, ctypes.c_void_p) for n in ("d_pages", "d_weights", "d_positions", "d_k_scale", "d_v_scale")]
+
+
+class sc_kv4_seqs(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("width", ctypes.c_int32), ("ld_table", ctypes.c_int64),
+                ("d_table", ctypes.c_void_p), ("d_lens", ctypes.c_void_p)]
+
+
+class sc_kv4_rows(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int32), ("d_k", ctypes.c_void_p), ("d_v", ctypes.c_void_p)] + [
+        (n, ctypes.c_int64) for n in ("k_token", "k_head", "v_token", "v_head")]
+
+
+class sc_kv4_query(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int32), ("rows", ctypes.c_int32), ("q_heads", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("d_q", ctypes.c_void_p), ("d_out", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64 * 3), ("out_stride", ctypes.c_int64 * 3)]
+
+
 _lib = None
 
 
@@ -131,6 +170,14 @@ def lib():
             "moe_layer_prepare": [ctypes.POINTER(sc_moe_config), P, P],
             "moe_layer_forward": [ctypes.POINTER(sc_moe_config), ctypes.POINTER(sc_moe_weights), P, P, i64, i32, P,
                                   i32, i64, P, P, P],
+            "prompt_attention": [P, P],
+            "kv4_page_bytes": [i32, i32, ctypes.POINTER(sz)],
+            "kv4_append": [P, P, P, i32, P, P, P],
+            "kv4_read": [P, P, P, i32, P, P],
+            "kv4_attention_workspace_bytes": [P, P, i32, i32, i32, ctypes.POINTER(sz)],
+            "kv4_attention": [P, P, P, i32, P, P],
+            "kv4_evict_workspace_bytes": [P, P, i32, ctypes.POINTER(sz)],
+            "kv4_evict": [P, P, i32, i32, i32, P, P, P],
             "fp4_linear": [ctypes.POINTER(sc_fp4_matrix), P, i32, i64, i32, P, P, i32, i64, P],
         }
         for name, args in sig.items():
@@ -259,6 +306,44 @@ def moe_layer_prepare(cfg, d_workspace, stream):
 
 def moe_layer_forward(cfg, w, d_workspace, d_x, ldx, M, d_y, y_type, ldy, d_ids, d_weights, stream):
     _check(lib().moe_layer_forward(cfg, w, d_workspace, d_x, ldx, M, d_y, y_type, ldy, d_ids, d_weights, stream))
+
+
+def prompt_attention(p, stream):
+    _check(lib().prompt_attention(p, stream))
+
+
+def kv4_page_bytes(fmt, head_dim):
+    n = ctypes.c_size_t()
+    _check(lib().kv4_page_bytes(fmt, head_dim, ctypes.byref(n)))
+    return n.value
+
+
+def kv4_append(cache, seqs, rows, tokens, d_starts, d_positions, stream):
+    _check(lib().kv4_append(cache, seqs, rows, tokens, d_starts, d_positions, stream))
+
+
+def kv4_read(cache, seqs, rows, tokens, d_starts, stream):
+    _check(lib().kv4_read(cache, seqs, rows, tokens, d_starts, stream))
+
+
+def kv4_attention_workspace_bytes(cache, seqs, rows, q_heads, accumulate):
+    n = ctypes.c_size_t()
+    _check(lib().kv4_attention_workspace_bytes(cache, seqs, rows, q_heads, accumulate, ctypes.byref(n)))
+    return n.value
+
+
+def kv4_attention(cache, seqs, query, accumulate, d_workspace, stream):
+    _check(lib().kv4_attention(cache, seqs, query, accumulate, d_workspace, stream))
+
+
+def kv4_evict_workspace_bytes(cache, seqs, keep):
+    n = ctypes.c_size_t()
+    _check(lib().kv4_evict_workspace_bytes(cache, seqs, keep, ctypes.byref(n)))
+    return n.value
+
+
+def kv4_evict(cache, seqs, keep, recent, sinks, d_new_lens, d_workspace, stream):
+    _check(lib().kv4_evict(cache, seqs, keep, recent, sinks, d_new_lens, d_workspace, stream))
 
 
 def slotcache_last_error():

@@ -12,7 +12,7 @@ from concurrent.futures import ThreadPoolExecutor
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SOURCES = ["route_remap.hip", "expert_gemv.hip", "fp4_quantize.hip", "fp4_linear.hip", "moe_layer.hip", "moe_one.hip",
-           "runtime.hip"]
+           "kv4_cache.hip", "kv4_attend.hip", "kv4_evict.hip", "prompt_attention.hip", "runtime.hip"]
 LIB = os.path.join(HERE, "libslotcache.so")
 ARCH = "gfx950"
 FLAGS = [

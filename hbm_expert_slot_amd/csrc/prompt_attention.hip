@@ -1,0 +1,320 @@
+// Attention over whole prompts: packed sequences of different lengths, causal,
+// query heads in groups that share a key head.
+//
+//   s_j = scale q . k_j,   o = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m)
+// over the keys j that a row sees: all up to its own, with rows at the end of
+// the keys when there are fewer rows than keys.  One pass over the keys keeps
+// the running maximum, the sum and o in fp32.
+//
+// Scores are formed transposed (keys times queries, 32x32x16 products): a lane
+// has one query's scores of the keys that it has to supply to the second product,
+// V^T times P^T, so P goes from the first product to the second in its registers.
+// V^T comes from the rows of V by LDS loads that transpose.
+#include "fp4_device.h"
+#include "internal.h"
+
+#include <type_traits>
+
+namespace sc {
+namespace prompt {
+namespace {
+
+using namespace fp4;
+
+constexpr int kWaves = 4, kThreads = 64 * kWaves;
+constexpr int kRows = 32 * kWaves;       // query rows of a block
+constexpr int kKeys = 64;                // keys of a tile
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+
+typedef __attribute__((ext_vector_type(16))) float f32x16;
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
+typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
+
+struct PromptArgs {
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  uint16_t* out;
+  float* lse;               // [rows][heads] or null
+  const int32_t* starts;    // [n + 1] rows
+  const int32_t* key_starts;
+  int64_t qs[2], ks[2], vs[2], os[2];     // strides: row, head
+  int32_t n, rows, keys, heads, group;
+  float scale;
+};
+
+template <bool HALF>
+__device__ __forceinline__ f32x16 product(u32x4 a, u32x4 b, f32x16 c) {
+  if constexpr (HALF)
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
+                                                   0);
+}
+template <bool HALF>
+__device__ __forceinline__ uint32_t pack(float a, float b) {
+  if constexpr (HALF) return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b});
+  else return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
+}
+__device__ __forceinline__ u32x4 load_row(const uint16_t* p) {
+  u32x4 v;
+  __builtin_memcpy(&v, p, 16);
+  return v;
+}
+template <bool HALF>
+__device__ __forceinline__ float widen(uint32_t v) {
+  if constexpr (HALF) return (float)__builtin_bit_cast(_Float16, (uint16_t)v);
+  else return __uint_as_float(v << 16);
+}
+// Eight elements, zeros for those that are not finite.
+template <bool HALF>
+__device__ __forceinline__ u32x4 finite8(u32x4 v) {
+  constexpr uint32_t kInf = HALF ? 0x7C00u : 0x7F80u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if ((v[i] & kInf) == kInf) v[i] &= 0xFFFF0000u;
+    if ((v[i] >> 16 & kInf) == kInf) v[i] &= 0xFFFFu;
+  }
+  return v;
+}
+// Four rows of 16 columns, 8 bytes of a row per lane: a lane gets its column.
+__device__ __forceinline__ u32x2 load_transposed(const uint8_t* p) {
+  typedef __attribute__((address_space(3))) s16x4 Lds;
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds*)(p)));
+}
+
+// A sequence's rows or keys; none where the starts make no sense.
+__device__ __forceinline__ int range_of(const int32_t* starts, int b, int all, int& first) {
+  first = starts[b];
+  const int end = starts[b + 1];
+  return first >= 0 && end >= first && end <= all ? end - first : 0;
+}
+__device__ __forceinline__ int tiles_of(const PromptArgs& a, int b) {
+  int first;
+  return b < a.n ? (range_of(a.starts, b, a.rows, first) + kRows - 1) / kRows : 0;
+}
+// The sequence of tile t of all, and t within it; a.n behind the last.
+__device__ __forceinline__ int sequence_at(const PromptArgs& a, int& t, int lane) {
+  int sum = 0;
+  for (int i = 0; i < a.n; i += 64) {
+    const int n = tiles_of(a, i + lane);
+    int upto = n;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int u = __shfl_up(upto, o);
+      if (lane >= o) upto += u;
+    }
+    upto += sum;
+    const uint64_t beyond = __ballot(upto > t);
+    if (beyond) {
+      const int l = __builtin_ctzll(beyond);
+      t -= __shfl(upto - n, l);
+      return i + l;
+    }
+    sum = __shfl(upto, 63);
+  }
+  return a.n;
+}
+
+template <int D, bool HALF>
+__global__ __launch_bounds__(kThreads) void k_prompt(PromptArgs a) {
+  constexpr int kRow = D * 2 + 16;                   // bytes of a row in LDS
+  constexpr int NO = D / 32, NK = D / 16;
+  constexpr float kShift = HALF ? 14.0f : 0.0f;
+  __shared__ __align__(16) uint8_t lds_k[kKeys * kRow], lds_v[kKeys * kRow];
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_index(), hi = lane >> 5, qc = lane & 31;
+  const int head = blockIdx.x % a.heads;
+  int tile = blockIdx.x / a.heads;
+  const int b = sequence_at(a, tile, lane);
+  if (b >= a.n) return;
+  int row0, key0;
+  const int rows = range_of(a.starts, b, a.rows, row0), keys = range_of(a.key_starts, b, a.keys, key0);
+  const int r0 = tile * kRows + wave * 32, row = r0 + qc;
+  const int ahead = keys - rows + 1;                 // keys that row 0 sees
+  const int mine = min(keys, ahead + min(row, rows - 1));
+  const int end = min(keys, ahead + min(tile * kRows + kRows, rows) - 1);
+  u32x4 q[NK];
+  const uint16_t* qp = a.q + (int64_t)(row0 + min(row, rows - 1)) * a.qs[0] + head * a.qs[1] + hi * 8;
+#pragma unroll
+  for (int i = 0; i < NK; ++i) q[i] = load_row(qp + 16 * i);
+  const uint16_t* kp = a.k + (int64_t)key0 * a.ks[0] + head / a.group * a.ks[1];
+  const uint16_t* vp = a.v + (int64_t)key0 * a.vs[0] + head / a.group * a.vs[1];
+  const float factor = a.scale * kLog2e;
+  const int seen_by_all = ahead + tile * kRows;      // keys that every row of the block sees
+  float m, l;
+  f32x16 o[NO];
+  bool careful = false;      // values that only some rows see are not finite: in a second pass
+again:
+  m = -INFINITY;
+  l = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NO; ++i)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[i][e] = 0.0f;
+
+  for (int j0 = 0; j0 < end; j0 += kKeys) {
+    __syncthreads();
+    constexpr int PR = D / 8;                        // pieces of a row
+#pragma unroll
+    for (int i = 0; i < kKeys * PR / kThreads; ++i) {
+      const int e = tid + i * kThreads, r = e / PR, c = e % PR, j = j0 + r;
+      u32x4 kv = {0, 0, 0, 0}, vv = {0, 0, 0, 0};    // nothing of other sequences
+      if (j < end) {
+        kv = load_row(kp + (int64_t)j * a.ks[0] + c * 8);
+        vv = load_row(vp + (int64_t)j * a.vs[0] + c * 8);
+        if (careful && j0 + kKeys > seen_by_all) vv = finite8<HALF>(vv);
+      }
+      *reinterpret_cast<u32x4*>(lds_k + r * kRow + c * 16) = kv;
+      *reinterpret_cast<u32x4*>(lds_v + r * kRow + c * 16) = vv;
+    }
+    __syncthreads();
+    f32x16 s[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[t][e] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NK; ++i) {
+        const u32x4 kw = *reinterpret_cast<const u32x4*>(lds_k + (t * 32 + qc) * kRow + i * 32 + hi * 16);
+        s[t] = product<HALF>(kw, q[i], s[t]);
+      }
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int j = j0 + t * 32 + e / 4 * 8 + hi * 4 + e % 4;
+        if (j >= mine) s[t][e] = -INFINITY;
+        top = fmaxf(top, s[t][e]);
+      }
+    top = fmaxf(top, __shfl_xor(top, 32));
+    // fp16 P counts from 2^14, so that what its range cuts off is below 2^-38 of the largest
+    const float mn = fmaxf(m, top * factor), mz = mn == -INFINITY ? 0.0f : mn, mu = mz - kShift;
+    if (__any(mn != m)) {
+      const float f = __builtin_amdgcn_exp2f(m - mz);
+      l *= f;
+#pragma unroll
+      for (int i = 0; i < NO; ++i) o[i] *= f;
+      m = mn;
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        s[t][e] = __builtin_amdgcn_exp2f(fmaf(s[t][e], factor, -mu));
+        l += s[t][e];
+      }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const f32x16& x = s[t / 2];
+      const int f = t % 2 * 8;
+      const u32x4 pw = {pack<HALF>(x[f], x[f + 1]), pack<HALF>(x[f + 2], x[f + 3]), pack<HALF>(x[f + 4], x[f + 5]),
+                        pack<HALF>(x[f + 6], x[f + 7])};
+#pragma unroll
+      for (int i = 0; i < NO; ++i) {
+        const uint8_t* p = lds_v + (t * 16 + hi * 4 + (lane & 15) / 4) * kRow + i * 64 + (lane >> 4 & 1) * 32 + lane % 4 * 8;
+        const u32x2 lo = load_transposed(p), hw = load_transposed(p + 8 * kRow);
+        o[i] = product<HALF>(u32x4{lo.x, lo.y, hw.x, hw.y}, pw, o[i]);
+      }
+    }
+    if (careful && j0 + kKeys > seen_by_all) {
+      for (int j = j0; j < min(j0 + kKeys, mine); ++j)
+#pragma unroll
+        for (int i = 0; i < NO; ++i)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float x = widen<HALF>(vp[(int64_t)j * a.vs[0] + i * 32 + e / 4 * 8 + hi * 4 + e % 4]);
+            if (!(fabsf(x) < INFINITY)) o[i][e] += x;
+          }
+    }
+  }
+  // 0 times a value that a row does not see is NaN where that is not finite
+  if (!careful) {
+    float z = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NO; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) z = fmaf(0.0f, o[i][e], z);
+    if (__syncthreads_or(z != z)) {
+      careful = true;
+      goto again;
+    }
+  }
+  l += __shfl_xor(l, 32);
+  if (row >= rows) return;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  uint16_t* op = a.out + (int64_t)(row0 + row) * a.os[0] + head * a.os[1] + hi * 4;
+#pragma unroll
+  for (int i = 0; i < NO; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      // dimensions 32 i + 8 e + 4 hi ..
+      const u32x2 w = {pack<HALF>(o[i][e * 4] * inv, o[i][e * 4 + 1] * inv),
+                       pack<HALF>(o[i][e * 4 + 2] * inv, o[i][e * 4 + 3] * inv)};
+      __builtin_memcpy(op + i * 32 + e * 8, &w, 8);
+    }
+  if (a.lse && hi == 0) a.lse[(int64_t)(row0 + row) * a.heads + head] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l) - kShift) * kLn2;
+}
+
+template <int D>
+hipError_t launch(const PromptArgs& a, bool half, hipStream_t st) {
+  const unsigned grid = (unsigned)((a.rows / kRows + a.n) * a.heads);
+  if (half) hipLaunchKernelGGL((k_prompt<D, true>), dim3(grid), dim3(kThreads), 0, st, a);
+  else hipLaunchKernelGGL((k_prompt<D, false>), dim3(grid), dim3(kThreads), 0, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace prompt
+}  // namespace sc
+
+using namespace sc;
+
+extern "C" sc_status prompt_attention(const sc_prompt* p, void* stream) {
+  if (!p) return fail(SC_E_ARG, "the description is NULL");
+  if (p->type != SC_DTYPE_BF16 && p->type != SC_DTYPE_F16) return fail(SC_E_ARG, "type must be bf16 or fp16");
+  if (p->head_dim != 64 && p->head_dim != 128 && p->head_dim != 256)
+    return fail(SC_E_ARG, "head_dim must be 64, 128 or 256");
+  if (p->kv_heads < 1 || p->q_heads < 1 || p->q_heads > SC_PROMPT_MAX_HEADS || p->q_heads % p->kv_heads)
+    return fail(SC_E_ARG, "q_heads must be a multiple of kv_heads and at most %d", SC_PROMPT_MAX_HEADS);
+  if (p->n_seqs < 0 || p->n_seqs > SC_PROMPT_MAX_SEQS || p->rows < 0 || p->rows > SC_PROMPT_MAX_ROWS || p->keys < 0)
+    return fail(SC_E_ARG, "n_seqs, rows or keys are out of range");
+  if (!(p->scale > 0.0f) || p->scale > 3e38f) return fail(SC_E_ARG, "scale must be positive and finite");
+  if (p->n_seqs == 0 || p->rows == 0) return SC_OK;
+  if (!p->d_q || !p->d_out || (p->keys > 0 && (!p->d_k || !p->d_v))) return fail(SC_E_ARG, "q, k, v or out is NULL");
+  if ((uintptr_t)p->d_q % 2 || (uintptr_t)p->d_k % 2 || (uintptr_t)p->d_v % 2 || (uintptr_t)p->d_out % 2 ||
+      (uintptr_t)p->d_lse % 4)
+    return fail(SC_E_ARG, "q, k, v, out or lse is not aligned to its elements");
+  if (!p->d_starts || !p->d_key_starts || (uintptr_t)p->d_starts % 4 || (uintptr_t)p->d_key_starts % 4)
+    return fail(SC_E_ARG, "starts are NULL or not 4-byte aligned");
+  prompt::PromptArgs a{};
+  a.q = static_cast<const uint16_t*>(p->d_q);
+  a.k = static_cast<const uint16_t*>(p->d_k);
+  a.v = static_cast<const uint16_t*>(p->d_v);
+  a.out = static_cast<uint16_t*>(p->d_out);
+  a.lse = p->d_lse;
+  a.starts = p->d_starts;
+  a.key_starts = p->d_key_starts;
+  for (int i = 0; i < 2; ++i) {
+    if (p->q_stride[i] < 0 || p->k_stride[i] < 0 || p->v_stride[i] < 0 || p->out_stride[i] < 0)
+      return fail(SC_E_ARG, "strides must be >= 0");
+    a.qs[i] = p->q_stride[i];
+    a.ks[i] = p->k_stride[i];
+    a.vs[i] = p->v_stride[i];
+    a.os[i] = p->out_stride[i];
+  }
+  a.n = p->n_seqs;
+  a.rows = p->rows;
+  a.keys = p->keys;
+  a.heads = p->q_heads;
+  a.group = p->q_heads / p->kv_heads;
+  a.scale = p->scale;
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  const bool half = p->type == SC_DTYPE_F16;
+  const hipError_t e = p->head_dim == 64    ? prompt::launch<64>(a, half, st)
+                       : p->head_dim == 128 ? prompt::launch<128>(a, half, st)
+                                            : prompt::launch<256>(a, half, st);
+  if (e != hipSuccess) return hip_fail(e, "prompt_attention launch");
+  return SC_OK;
+}

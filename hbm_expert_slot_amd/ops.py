@@ -398,3 +398,6 @@ class MoELayer(_Fixed):
         if stream is not None:
             _record(stream, x, out, ids, weights)
         return out
+
+
+from .attention import KV4Cache, prompt_attention  # noqa: E402  (they build on the helpers above)

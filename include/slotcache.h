@@ -457,6 +457,161 @@ SC_API sc_status moe_layer_forward(const sc_moe_config* cfg, const sc_moe_weight
                                    const uint16_t* d_x, int64_t ldx, int32_t M, void* d_y, int32_t y_type,
                                    int64_t ldy, int32_t* d_ids, float* d_weights, void* stream);
 
+/* ---- attention over prompts ------------------------------------------------- */
+
+#define SC_PROMPT_MAX_HEADS 1024
+#define SC_PROMPT_MAX_SEQS 65536
+#define SC_PROMPT_MAX_ROWS (1 << 24)
+
+/* Packed sequences: sequence b has the rows d_starts[b] .. d_starts[b+1]-1 of q
+ * and the keys d_key_starts[b] .. d_key_starts[b+1]-1 of k and v.  Element d of
+ * row t and head h of q is at t * q_stride[0] + h * q_stride[1] + d, and so for
+ * k, v and out (strides in elements). */
+typedef struct {
+  int32_t type;                   /* of q, k, v and out: SC_DTYPE_BF16 or SC_DTYPE_F16 */
+  int32_t head_dim;               /* 64, 128 or 256 */
+  int32_t q_heads, kv_heads;      /* q_heads is a multiple of kv_heads; head h reads key head h / (q_heads / kv_heads) */
+  int32_t n_seqs;                 /* <= SC_PROMPT_MAX_SEQS */
+  int32_t rows, keys;             /* of all sequences; rows <= SC_PROMPT_MAX_ROWS */
+  float scale;                    /* > 0 */
+  const void* d_q;
+  const void* d_k;
+  const void* d_v;
+  void* d_out;
+  float* d_lse;                   /* [rows][q_heads] or NULL */
+  const int32_t* d_starts;        /* [n_seqs + 1] */
+  const int32_t* d_key_starts;    /* [n_seqs + 1]; d_starts for whole prompts */
+  int64_t q_stride[2], k_stride[2], v_stride[2], out_stride[2];
+} sc_prompt;
+
+/* Causal attention of every row over its sequence's keys: with Lq rows and Lk
+ * keys row i sees the keys below Lk - Lq + i + 1.  out = softmax(scale q k^T) v
+ * of the keys seen, lse the natural logarithm of the sum of exponentials; a row
+ * that sees none gets 0 and -infinity.  Products are exact, sums and softmax
+ * statistics fp32, P is rounded to the type of v, out once.  Rows outside of the
+ * sequences are not written; a sequence whose starts are not in order or exceed
+ * rows or keys counts as empty.  out must not overlap q, k or v.  Asynchronous on
+ * `stream`, whose device is current; no workspace, no allocation; can be captured. */
+SC_API sc_status prompt_attention(const sc_prompt* p, void* stream);
+
+/* ---- a key/value cache in 4 bits ------------------------------------------------ */
+
+#define SC_KV4_PAGE 64               /* tokens of a page */
+#define SC_KV4_MAX_HEADS 1024
+#define SC_KV4_MAX_SEQS 65536
+#define SC_KV4_MAX_WIDTH (1 << 24)   /* pages of a sequence */
+#define SC_KV4_MAX_ROWS 16
+#define SC_KV4_MAX_GROUP 64
+
+/* One layer's cache: pages of 64 tokens, each with the codes and scales of all
+ * its heads' keys and values (the formats of 4-bit weights, groups along
+ * head_dim), kv4_page_bytes per page and head.  Where inside a page a token's
+ * codes lie follows the attention kernel's loads: pages are written by
+ * kv4_append and read back by kv4_read.
+ * Of a cache that evicts, every token has for each head its accumulated
+ * attention weight and its position in the sequence. */
+typedef struct {
+  int32_t format;            /* SC_FP4_NV or SC_FP4_MX */
+  int32_t head_dim;          /* 64, 128 or 256 */
+  int32_t kv_heads;          /* <= SC_KV4_MAX_HEADS */
+  int32_t n_pages;           /* > 0 */
+  void* d_pages;             /* [n_pages][kv_heads][kv4_page_bytes], 16-byte aligned */
+  float* d_weights;          /* [n_pages][kv_heads][64], 16-byte aligned, or NULL */
+  int32_t* d_positions;      /* [n_pages][kv_heads][64], 16-byte aligned; NULL with d_weights */
+  const float* d_k_scale;    /* NVFP4: one float > 0 that all keys' group scales are multiplied by; NULL stands for 1 */
+  const float* d_v_scale;    /* the same for values */
+} sc_kv4_cache;
+
+/* Sequences of a batch: place p of sequence b is token p % 64 of page
+ * d_table[b * ld_table + p / 64], for 0 <= p < d_lens[b].  d_lens counts the
+ * tokens that come with the call.  A length below 0 or above 64 * width and a
+ * page outside of the cache are found by the kernels: what each call says of it. */
+typedef struct {
+  int32_t n_seqs;            /* <= SC_KV4_MAX_SEQS */
+  int32_t width;             /* entries of a table row, <= SC_KV4_MAX_WIDTH */
+  int64_t ld_table;
+  const int32_t* d_table;
+  const int32_t* d_lens;     /* [n_seqs] */
+} sc_kv4_seqs;
+
+/* Keys and values of packed tokens: element d of token t and head h of k at t *
+ * k_token + h * k_head + d, and so for v. */
+typedef struct {
+  int32_t type;              /* SC_DTYPE_F32, SC_DTYPE_BF16 or SC_DTYPE_F16 */
+  void* d_k;
+  void* d_v;
+  int64_t k_token, k_head, v_token, v_head;
+} sc_kv4_rows;
+
+/* Bytes of one page of one head, keys and values. */
+SC_API sc_status kv4_page_bytes(int32_t format, int32_t head_dim, size_t* bytes);
+
+/* Quantises tokens into the cache: sequence b has the tokens d_starts[b] ..
+ * d_starts[b+1]-1 (NULL: tokens / n_seqs each), which are its last: the last one
+ * goes to place d_lens[b] - 1.  Codes and scales follow fp4_quantize with a given
+ * scale.  A cache with weights gets weight 0 and the position d_positions[token]
+ * (NULL: the place).  Tokens outside of the sequences, places that are not in the
+ * table and pages outside of the cache are not written.  No two tokens of a call
+ * may have one place of one page.  Asynchronous on `stream`, whose device is
+ * current; no workspace, no allocation; can be captured. */
+SC_API sc_status kv4_append(const sc_kv4_cache* cache, const sc_kv4_seqs* seqs, const sc_kv4_rows* rows, int32_t tokens,
+                            const int32_t* d_starts, const int32_t* d_positions, void* stream);
+
+/* Reads the last tokens of each sequence back, addressed as in kv4_append: code *
+ * group scale * scale, rounded to fp32 once and then to rows->type.  Tokens
+ * outside of the sequences are not written; places or pages that are not there
+ * read as NaN. */
+SC_API sc_status kv4_read(const sc_kv4_cache* cache, const sc_kv4_seqs* seqs, const sc_kv4_rows* rows, int32_t tokens,
+                          const int32_t* d_starts, void* stream);
+
+/* Queries of the last `rows` tokens of every sequence: element d of row r and
+ * head h of sequence b at b * q_stride[0] + r * q_stride[1] + h * q_stride[2] +
+ * d, and so for out. */
+typedef struct {
+  int32_t type;              /* of q and out: SC_DTYPE_BF16 or SC_DTYPE_F16 */
+  int32_t rows;              /* 1 .. SC_KV4_MAX_ROWS: a token and its drafts */
+  int32_t q_heads;           /* a multiple of kv_heads, up to SC_KV4_MAX_GROUP times */
+  float scale;               /* > 0 */
+  const void* d_q;
+  void* d_out;
+  int64_t q_stride[3], out_stride[3];
+} sc_kv4_query;
+
+/* Bytes of device workspace that kv4_attention needs. */
+SC_API sc_status kv4_attention_workspace_bytes(const sc_kv4_cache* cache, const sc_kv4_seqs* seqs, int32_t rows,
+                                               int32_t q_heads, int32_t accumulate, size_t* bytes);
+
+/* Attention over the cache: row r of sequence b sees the places below d_lens[b]
+ * - rows + r + 1 (its own token and those before it).  out = softmax(scale q
+ * k^T) v; a row that sees nothing gets 0.  With `accumulate` every token's weight
+ * grows by the sum of its probabilities over the rows and over the query heads of
+ * its head.  Products are exact; sums and softmax statistics are fp32 in a fixed
+ * order; P keeps 11 bits (NVFP4) or 16 (MXFP4).  Rows of a sequence whose length
+ * cannot be are NaN, and so are rows that see a page outside of the cache.
+ * d_workspace (256-byte aligned) holds nothing from one call to the next; calls
+ * that may run at once need one each.  out must not overlap q.  Asynchronous on
+ * `stream`, whose device is current; no allocation; can be captured. */
+SC_API sc_status kv4_attention(const sc_kv4_cache* cache, const sc_kv4_seqs* seqs, const sc_kv4_query* query,
+                               int32_t accumulate, void* d_workspace, void* stream);
+
+/* Bytes of device workspace that kv4_evict needs. */
+SC_API sc_status kv4_evict_workspace_bytes(const sc_kv4_cache* cache, const sc_kv4_seqs* seqs, int32_t keep,
+                                           size_t* bytes);
+
+/* Cuts every sequence of more than `keep` tokens down to `keep`: of each head the
+ * tokens at positions below `sinks` or among the last `recent` positions stay
+ * before all others, then those with the largest weights (NaN largest), equal
+ * ones by place.  recent + sinks <= keep.  Tokens that stay keep their places
+ * below `keep`; those behind move, in order, into the places that became free,
+ * with their weights and positions, so a sequence's tokens are not in order
+ * afterwards (attention does not depend on it; later calls to kv4_append should
+ * give positions).  d_new_lens[b] = min(d_lens[b], keep); a sequence with a
+ * length or page that cannot be stays as it is and keeps its length.  Sequences
+ * that are cut must not share pages.  d_lens is only read.  Asynchronous on
+ * `stream`, whose device is current; no allocation; can be captured. */
+SC_API sc_status kv4_evict(const sc_kv4_cache* cache, const sc_kv4_seqs* seqs, int32_t keep, int32_t recent,
+                           int32_t sinks, int32_t* d_new_lens, void* d_workspace, void* stream);
+
 /* Message for the last non-OK status returned on this thread. */
 SC_API const char* slotcache_last_error(void);
 

@@ -1,0 +1,181 @@
+"""Refusals of the attention operators and of the 4-bit key/value cache: wrong
+arguments return an error before anything is enqueued (no GPU needed)."""
+import ctypes
+
+import pytest
+
+from hbm_expert_slot_amd import binding as B
+
+P = 0x10000     # stands for a device pointer: never followed
+R = ctypes.byref
+
+
+def _fails(f, *args):
+    with pytest.raises(B.SlotCacheError) as e:
+        f(*args)
+    assert e.value.status == B.SC_E_ARG and str(e.value)
+
+
+def _cache(**kw):
+    d = dict(format=B.SC_FP4_NV, head_dim=128, kv_heads=8, n_pages=4, d_pages=P, d_weights=P, d_positions=P,
+             d_k_scale=None, d_v_scale=P)
+    d.update(kw)
+    return B.sc_kv4_cache(*[d[n] for n, _ in B.sc_kv4_cache._fields_])
+
+
+def _seqs(**kw):
+    d = dict(n_seqs=2, width=3, ld_table=3, d_table=P, d_lens=P)
+    d.update(kw)
+    return B.sc_kv4_seqs(*[d[n] for n, _ in B.sc_kv4_seqs._fields_])
+
+
+def _rows(**kw):
+    d = dict(type=B.SC_DTYPE_BF16, d_k=P, d_v=P, k_token=1024, k_head=128, v_token=1024, v_head=128)
+    d.update(kw)
+    return B.sc_kv4_rows(*[d[n] for n, _ in B.sc_kv4_rows._fields_])
+
+
+def _query(**kw):
+    d = dict(type=B.SC_DTYPE_BF16, rows=1, q_heads=16, scale=0.1, d_q=P, d_out=P, q_stride=(2048, 2048, 128),
+             out_stride=(2048, 2048, 128))
+    d.update(kw)
+    return B.sc_kv4_query(*[d[n] for n, _ in B.sc_kv4_query._fields_])
+
+
+BAD_CACHES = [dict(format=2), dict(head_dim=96), dict(head_dim=0), dict(kv_heads=0), dict(kv_heads=1025), dict(n_pages=0),
+              dict(d_pages=None), dict(d_pages=P + 8), dict(d_weights=None), dict(d_positions=None), dict(d_weights=P + 4),
+              dict(d_k_scale=P + 2), dict(format=B.SC_FP4_MX)]
+BAD_SEQS = [dict(n_seqs=-1), dict(n_seqs=65537), dict(width=0), dict(width=(1 << 24) + 1), dict(ld_table=2),
+            dict(d_table=None), dict(d_lens=None), dict(d_table=P + 2), dict(d_lens=P + 1)]
+
+
+def _every_call(c, s):
+    return [(B.kv4_append, c, s, R(_rows()), 2, None, None, None), (B.kv4_read, c, s, R(_rows()), 2, None, None),
+            (B.kv4_attention, c, s, R(_query()), 0, P, None), (B.kv4_attention_workspace_bytes, c, s, 1, 16, 0),
+            (B.kv4_evict, c, s, 10, 0, 0, P, P, None), (B.kv4_evict_workspace_bytes, c, s, 10)]
+
+
+@pytest.mark.parametrize("change", BAD_CACHES)
+def test_caches_that_are_refused(change):
+    for call in _every_call(R(_cache(**change)), R(_seqs())):
+        _fails(*call)
+
+
+@pytest.mark.parametrize("change", BAD_SEQS)
+def test_sequences_that_are_refused(change):
+    for call in _every_call(R(_cache()), R(_seqs(**change))):
+        _fails(*call)
+
+
+def test_null_structures():
+    for call in _every_call(None, R(_seqs())) + _every_call(R(_cache()), None):
+        _fails(*call)
+    c, s = R(_cache()), R(_seqs())
+    _fails(B.kv4_append, c, s, None, 2, None, None, None)
+    _fails(B.kv4_read, c, s, None, 2, None, None)
+    _fails(B.kv4_attention, c, s, None, 0, P, None)
+    _fails(B.prompt_attention, None, None)
+
+
+@pytest.mark.parametrize("change,tokens", [
+    (dict(type=3), 2), (dict(d_k=None), 2), (dict(d_v=None), 2), (dict(d_k=P + 1), 2), (dict(type=B.SC_DTYPE_F32, d_v=P + 2), 2),
+    (dict(k_token=-1), 2), (dict(v_head=-1), 2), (dict(), -1), (dict(), 3), (dict(), 2 ** 31 - 2),
+])
+def test_rows_that_are_refused(change, tokens):
+    c, s, r = R(_cache()), R(_seqs()), R(_rows(**change))
+    _fails(B.kv4_append, c, s, r, tokens, None, None, None)
+    _fails(B.kv4_read, c, s, r, tokens, None, None)
+
+
+def test_unaligned_starts_and_positions():
+    c, s, r = R(_cache()), R(_seqs()), R(_rows())
+    _fails(B.kv4_append, c, s, r, 2, P + 2, None, None)
+    _fails(B.kv4_append, c, s, r, 2, P, P + 1, None)
+    _fails(B.kv4_read, c, s, r, 2, P + 2, None)
+
+
+@pytest.mark.parametrize("change", [
+    dict(type=B.SC_DTYPE_F32), dict(rows=0), dict(rows=17), dict(q_heads=0), dict(q_heads=12), dict(q_heads=8 * 65),
+    dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(d_q=None), dict(d_out=None),
+    dict(d_q=P + 1), dict(q_stride=(-1, 0, 0)), dict(out_stride=(0, 0, -128)),
+])
+def test_queries_that_are_refused(change):
+    _fails(B.kv4_attention, R(_cache()), R(_seqs()), R(_query(**change)), 0, P, None)
+
+
+def test_attention_workspace_and_weights():
+    c, s, q = R(_cache()), R(_seqs()), R(_query())
+    _fails(B.kv4_attention, c, s, q, 0, None, None)
+    _fails(B.kv4_attention, c, s, q, 0, P + 16, None)
+    _fails(B.kv4_attention, R(_cache(d_weights=None, d_positions=None)), s, q, 1, P, None)
+    n = B.kv4_attention_workspace_bytes(c, s, 1, 16, 0)
+    assert B.kv4_attention_workspace_bytes(c, s, 1, 16, 1) > n > 0
+    _fails(B.kv4_attention, c, R(_seqs(n_seqs=65536)), R(_query(rows=16)), 0, P, None)     # 2^24 query rows
+
+
+@pytest.mark.parametrize("keep,recent,sinks", [(0, 0, 0), (-1, 0, 0), (4, 5, 0), (4, 3, 2), (4, -1, 0), (4, 0, -1),
+                                               (4, 2 ** 31 - 1, 2 ** 31 - 1)])
+def test_evictions_that_are_refused(keep, recent, sinks):
+    _fails(B.kv4_evict, R(_cache()), R(_seqs()), keep, recent, sinks, P, P, None)
+
+
+def test_eviction_needs_weights_and_memory():
+    c, s = R(_cache()), R(_seqs())
+    _fails(B.kv4_evict, R(_cache(d_weights=None, d_positions=None)), s, 4, 0, 0, P, P, None)
+    _fails(B.kv4_evict, c, s, 4, 0, 0, None, P, None)
+    _fails(B.kv4_evict, c, s, 4, 0, 0, P, None, None)
+    _fails(B.kv4_evict, c, s, 4, 0, 0, P + 2, P, None)
+    _fails(B.kv4_evict, c, s, 4, 0, 0, P, P + 2, None)
+    assert B.kv4_evict_workspace_bytes(c, s, 64) > B.kv4_evict_workspace_bytes(c, s, 1000) > 0
+
+
+def test_page_bytes():
+    assert B.kv4_page_bytes(B.SC_FP4_NV, 128) == 2 * 64 * (64 + 8)
+    assert B.kv4_page_bytes(B.SC_FP4_MX, 256) == 2 * 64 * (128 + 8)
+    _fails(B.kv4_page_bytes, 5, 128)
+    _fails(B.kv4_page_bytes, B.SC_FP4_NV, 80)
+
+
+def _prompt(**kw):
+    d = dict(type=B.SC_DTYPE_BF16, head_dim=128, q_heads=16, kv_heads=4, n_seqs=2, rows=100, keys=100, scale=0.1, d_q=P,
+             d_k=P, d_v=P, d_out=P, d_lse=None, d_starts=P, d_key_starts=P, q_stride=(2048, 128), k_stride=(512, 128),
+             v_stride=(512, 128), out_stride=(2048, 128))
+    d.update(kw)
+    return B.sc_prompt(*[d[n] for n, _ in B.sc_prompt._fields_])
+
+
+@pytest.mark.parametrize("change", [
+    dict(type=B.SC_DTYPE_F32), dict(head_dim=96), dict(q_heads=0), dict(kv_heads=0), dict(kv_heads=3), dict(q_heads=2048),
+    dict(n_seqs=-1), dict(n_seqs=65537), dict(rows=-1), dict(rows=(1 << 24) + 1), dict(keys=-1), dict(scale=0.0),
+    dict(scale=float("nan")), dict(scale=float("inf")), dict(d_q=None), dict(d_k=None), dict(d_v=None), dict(d_out=None),
+    dict(d_q=P + 1), dict(d_lse=P + 2), dict(d_starts=None), dict(d_key_starts=None), dict(d_starts=P + 2),
+    dict(q_stride=(-1, 0)), dict(k_stride=(0, -1)), dict(v_stride=(-1, 0)), dict(out_stride=(-1, 0)),
+])
+def test_prompts_that_are_refused(change):
+    _fails(B.prompt_attention, R(_prompt(**change)), None)
+
+
+def test_nothing_to_do_is_no_error():
+    B.prompt_attention(R(_prompt(rows=0)), None)
+    B.prompt_attention(R(_prompt(n_seqs=0)), None)
+    c, none = R(_cache()), R(_seqs(n_seqs=0))
+    B.kv4_append(c, none, R(_rows()), 0, None, None, None)
+    B.kv4_read(c, R(_seqs()), R(_rows()), 0, None, None)
+    B.kv4_attention(c, none, R(_query()), 0, P, None)
+    B.kv4_evict(c, none, 4, 0, 0, None, None, None)
+
+
+def test_the_python_layer_names_what_is_wrong():
+    torch = pytest.importorskip("torch")
+    from hbm_expert_slot_amd import ops
+    q = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="q must be on the GPU"):
+        ops.prompt_attention(q, q, q, torch.tensor([0, 4], dtype=torch.int32))
+    with pytest.raises(ValueError, match="q must be"):
+        ops.prompt_attention(q[0], q, q, torch.tensor([0, 4], dtype=torch.int32))
+    with pytest.raises(ValueError, match="q has type"):
+        ops.prompt_attention(q.float(), q, q, torch.tensor([0, 4], dtype=torch.int32))
+    for kw in (dict(fmt="fp4"), dict(head_dim=80), dict(n_pages=0), dict(kv_heads=0), dict(kv_heads=1025),
+               dict(fmt="mxfp4", k_scale=torch.ones(1))):
+        with pytest.raises(ValueError):
+            ops.KV4Cache(**dict(dict(n_pages=2, kv_heads=2, head_dim=64), **kw))

@@ -1,0 +1,758 @@
+"""Attention over prompts, the 4-bit key/value cache, attention over it and
+eviction from it, against float64."""
+import numpy as np
+import pytest
+
+from oracle import attention as oa
+
+from gpu_util import log, torch_cuda
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"bf16": "bfloat16", "fp16": "float16", "fp32": "float32"}
+EPS = {"bf16": 2.0 ** -8, "fp16": 2.0 ** -11, "fp32": 2.0 ** -24}      # half a step
+P_EPS = {"nvfp4": (2.0 ** -11, 2.0 ** -39), "mxfp4": (2.0 ** -16, 0.0)}      # of P: relative, of the largest
+TINY = {"bf16": 1e-37, "fp16": 2.0 ** -25, "fp32": 1e-37}
+
+
+def _ops():
+    from hbm_expert_slot_amd import ops
+    return ops
+
+
+def _np(t):
+    return t.detach().cpu().double().numpy()
+
+
+def _ints(torch, v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def _starts(torch, n):
+    return _ints(torch, np.concatenate(([0], np.cumsum(n))).tolist())
+
+
+def _randn(torch, seed, *shape):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return torch.randn(*shape, generator=g, device="cuda")
+
+
+def _close(got, want, bound, dtype, what):
+    got = _np(got)
+    assert np.array_equal(np.isnan(got), np.isnan(want)), (what, "NaN")
+    assert np.array_equal(np.isinf(got), np.isinf(want)), (what, "infinities")
+    ok = np.isfinite(want)
+    over = np.abs(got - want)[ok] - (bound[ok] * (1 + EPS[dtype]) + EPS[dtype] * np.abs(want[ok]) + TINY[dtype])
+    assert over.size == 0 or over.max() <= 0, (what, float(over.max()), int(over.argmax()))
+
+
+# ---- prompts ---------------------------------------------------------------
+
+def _check_prompt(torch, q, k, v, new, full, dtype, scale=None, lse=True):
+    ops = _ops()
+    starts, key_starts = _starts(torch, new), _starts(torch, full)
+    out, ls = ops.prompt_attention(q, k, v, starts, key_starts, scale=scale, return_lse=True)
+    assert out.dtype == q.dtype and out.shape == q.shape
+    qn, kn, vn = _np(q), _np(k), _np(v)
+    sc = 1.0 / np.sqrt(q.shape[2]) if scale is None else scale
+    q0 = k0 = 0
+    for i, (n, a) in enumerate(zip(new, full)):
+        o, l, _, eo, el, _ = oa.attend(qn[q0:q0 + n], kn[k0:k0 + a], vn[k0:k0 + a], sc, EPS[dtype], 2.0 ** -39 if dtype == "fp16" else 0.0)
+        _close(out[q0:q0 + n], o, eo, dtype, ("out", i, n, a))
+        _close(ls[q0:q0 + n], l, el, "fp32", ("lse", i, n, a))
+        q0, k0 = q0 + n, k0 + a
+    return out
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("d,hq,hkv", [(64, 4, 2), (128, 6, 2), (256, 3, 1), (128, 1, 1), (64, 8, 1)])
+def test_prompts_of_all_lengths(d, hq, hkv, dtype):
+    torch = torch_cuda()
+    log("prompts", d, hq, hkv, dtype)
+    new = [1, 2, 31, 32, 33, 0, 63, 64, 65, 127, 128, 129, 200]
+    T = sum(new)
+    dt = getattr(torch, TYPES[dtype])
+    q, k, v = (_randn(torch, 3 * d + i, T, h, d).to(dt) for i, h in enumerate((hq, hkv, hkv)))
+    _check_prompt(torch, 2 * q, k, v, new, new, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("new,full", [([1, 1], [300, 1]), ([5, 40, 0, 130], [700, 40, 9, 131]), ([64], [1000]),
+                                      ([10, 200], [3, 140])])
+def test_chunks_of_prompts(new, full, dtype):
+    """More keys than rows; and fewer, whose first rows see nothing."""
+    torch = torch_cuda()
+    log("chunks", new, full, dtype)
+    dt = getattr(torch, TYPES[dtype])
+    q = _randn(torch, 1, sum(new), 4, 128).to(dt)
+    k, v = (_randn(torch, 2 + i, sum(full), 2, 128).to(dt) for i in range(2))
+    _check_prompt(torch, q, k, v, new, full, dtype, scale=0.2)
+
+
+def test_prompt_of_a_few_thousand_tokens():
+    torch = torch_cuda()
+    log("long prompt")
+    q, k, v = (_randn(torch, i, 1500, 2, 128).to(torch.bfloat16) for i in range(3))
+    k[700:710] *= 8          # the maximum moves late
+    _check_prompt(torch, 3 * q, k, v, [1500], [1500], "bf16")
+
+
+def test_prompt_strides_and_alignment():
+    """Views of one projection at odd offsets, heads apart, and an output inside a larger tensor."""
+    torch = torch_cuda()
+    log("prompt strides")
+    new, hq, hkv, d = [70, 33, 129], 4, 2, 64
+    T = sum(new)
+    x = _randn(torch, 5, T, (hq + 2 * hkv) * d + 3).to(torch.bfloat16)
+    q = x[:, 1:1 + hq * d].unflatten(1, (hq, d))
+    k = x[:, 1 + hq * d:1 + (hq + hkv) * d].unflatten(1, (hkv, d))
+    v = x[:, 1 + (hq + hkv) * d:1 + (hq + 2 * hkv) * d].unflatten(1, (hkv, d))
+    want = _check_prompt(torch, q, k, v, new, new, "bf16")
+    big = torch.full((T + 2, hq + 1, d + 5), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = big[1:T + 1, 1:, 3:3 + d]
+    got = _ops().prompt_attention(q, k, v, _starts(torch, new), out=out)
+    assert got.data_ptr() == out.data_ptr() and torch.equal(out, want)
+    out.fill_(7.0)
+    assert bool((big == 7.0).all())
+    # heads before tokens
+    kt = k.transpose(0, 1).contiguous().transpose(0, 1)
+    vt = v.transpose(0, 1).contiguous().transpose(0, 1)
+    assert torch.equal(_ops().prompt_attention(q, kt, vt, _starts(torch, new)), want)
+    # one head for all by a stride of zero
+    one = _ops().prompt_attention(q, k[:, :1], v[:, :1], _starts(torch, new))
+    assert torch.equal(_ops().prompt_attention(q, k[:, :1].expand(-1, 4, -1), v[:, :1].expand(-1, 4, -1),
+                                               _starts(torch, new)), one)
+
+
+def test_prompt_rows_outside_of_the_sequences():
+    torch = torch_cuda()
+    log("rows behind the last sequence")
+    q, k, v = (_randn(torch, i, 300, 2, 64).to(torch.float16) for i in range(3))
+    out = torch.full_like(q, 9.0)
+    k[250:], v[250:] = float("nan"), float("inf")         # of no sequence
+    _ops().prompt_attention(q, k, v, _ints(torch, [10, 100, 250]), out=out)
+    assert bool((out[:10] == 9.0).all()) and bool((out[250:] == 9.0).all()) and bool(torch.isfinite(out).all())
+    want = _ops().prompt_attention(q[10:100].contiguous(), k[10:100].contiguous(), v[10:100].contiguous(),
+                                   _ints(torch, [0, 90]))
+    assert torch.equal(out[10:100], want)
+    # starts that make no sense: nothing is written for that sequence
+    for bad in ([0, 400], [50, 20], [-3, 20]):
+        out.fill_(9.0)
+        _ops().prompt_attention(q, k, v, _ints(torch, bad), out=out)
+        assert bool((out == 9.0).all()), bad
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("at", [0, 40, 90, 199])
+def test_prompt_values_that_are_not_finite(at, which, bad):
+    """Rows before the token do not see it; the others do."""
+    torch = torch_cuda()
+    log("not finite", at, which, bad)
+    q, k, v = (_randn(torch, i, 200, 2, 64).to(torch.bfloat16) for i in range(3))
+    sane = _ops().prompt_attention(q, k, v, _ints(torch, [0, 200]))
+    (k if which == "k" else v)[at, 0, 5] = bad
+    out = _ops().prompt_attention(q, k, v, _ints(torch, [0, 200]))
+    assert torch.equal(out[:at], sane[:at]) and torch.equal(out[:, 1], sane[:, 1])
+    if which == "v":
+        o = out[at:, 0]
+        assert not bool(torch.isfinite(o[:, 5]).any()) and torch.equal(torch.cat((o[:, :5], o[:, 6:]), 1),
+                                                                       torch.cat((sane[at:, 0, :5], sane[at:, 0, 6:]), 1))
+    elif bad != bad:
+        assert bool(torch.isnan(out[at:, 0]).all())
+
+
+# ---- the cache -------------------------------------------------------------
+
+class Filled:
+    """A cache with sequences of given lengths on pages in random order, among pages of NaN scales; the float64
+    values it holds by place."""
+
+    def __init__(self, torch, fmt, d, hkv, lens, dtype="bf16", track=False, scales=(None, None), seed=0, extra=0, size=1.0):
+        rng = np.random.default_rng(seed)
+        need = [(n + extra + 63) // 64 for n in lens]
+        pages = sum(need) + 3
+        self.torch, self.lens, self.hkv, self.d = torch, list(lens), hkv, d
+        gs = [None if s is None else torch.tensor([s], device="cuda") for s in scales]
+        self.cache = _ops().KV4Cache(pages, hkv, d, fmt, k_scale=gs[0], v_scale=gs[1], track=track)
+        self.cache.pages.fill_(255)
+        if track:
+            self.cache.weights.fill_(float("nan"))
+        order = rng.permutation(pages)
+        table = np.full((len(lens), max(max(need), 1) + 1), -1, np.int32)
+        i = 0
+        for b, n in enumerate(need):
+            table[b, :n] = order[i:i + n]
+            i += n
+        self.table, self.d_lens = _ints(torch, table.tolist()), _ints(torch, list(lens))
+        T = sum(lens)
+        dt = getattr(torch, TYPES[dtype])
+        k = (_randn(torch, seed + 1, T, hkv, d) * size).to(dt)
+        v = (_randn(torch, seed + 2, T, hkv, d) * size).to(dt)
+        self.fmt, self.scales = fmt, scales
+        self.k, self.v = self.held(k, 0), self.held(v, 1)
+        self.cache.append(k, v, self.table, self.d_lens, _starts(torch, lens))
+
+    def held(self, x, side):
+        g = self.scales[side]
+        return oa.quantized(_np(x), self.fmt, None if g is None else np.float32(g))
+
+    def of(self, b):
+        s = sum(self.lens[:b])
+        return self.k[s:s + self.lens[b]], self.v[s:s + self.lens[b]]
+
+    def check_read(self, dtypes=("bf16", "fp32")):
+        torch = self.torch
+        for dt in dtypes:
+            k, v = self.cache.read(self.table, self.d_lens, sum(self.lens), _starts(torch, self.lens),
+                                   dtype=getattr(torch, TYPES[dt]))
+            for got, want in ((k, self.k), (v, self.v)):
+                w = torch.tensor(want).float().to(getattr(torch, TYPES[dt]))
+                assert torch.equal(torch.nan_to_num(got.cpu(), nan=777.0), torch.nan_to_num(w, nan=777.0)), dt
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("d,hkv", [(64, 3), (128, 2), (256, 1)])
+def test_append_and_read(d, hkv, fmt, dtype):
+    torch = torch_cuda()
+    log("append", d, hkv, fmt, dtype)
+    Filled(torch, fmt, d, hkv, [1, 0, 5, 63, 64, 65, 200], dtype, seed=d).check_read(("bf16", "fp16", "fp32"))
+    if fmt == "nvfp4":
+        Filled(torch, fmt, d, hkv, [130, 7], dtype, scales=(0.037, 2.0 ** -9), seed=d + 1).check_read()
+        # scales that reach the ends of E4M3
+        Filled(torch, fmt, d, hkv, [130, 7], dtype, scales=(100.0, 1e-5), seed=d + 2).check_read(("fp32",))
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_append_what_is_not_finite(fmt):
+    torch = torch_cuda()
+    log("append nan", fmt)
+    c = Filled(torch, fmt, 128, 2, [70], "fp32")
+    x = _randn(torch, 9, 3, 2, 128)
+    x[0, 0, 5], x[1, 1, 100], x[2, 0, 127] = float("nan"), float("inf"), -float("inf")
+    c.cache.append(x, -x, c.table, c.d_lens)
+    k, v = c.cache.read(c.table, c.d_lens, 3, dtype=torch.float32)
+    g = 16 if fmt == "nvfp4" else 32
+    nan = torch.isnan(k)
+    assert torch.equal(nan, torch.isnan(v)) and int(nan.sum()) == 3 * g
+    assert bool(nan[0, 0, 5]) and bool(nan[1, 1, 100]) and bool(nan[2, 0, 127])
+
+
+def test_append_in_steps_gives_the_same_cache():
+    """Token by token with drafts that are overwritten, and all at once."""
+    torch = torch_cuda()
+    log("append in steps")
+    c = Filled(torch, "nvfp4", 128, 2, [140, 90], track=True)
+    n = [140, 90]
+    k, v = _randn(torch, 1, 230, 2, 128).to(torch.bfloat16), _randn(torch, 2, 230, 2, 128).to(torch.bfloat16)
+    whole = _ops().KV4Cache(c.cache.n_pages, 2, 128, track=True)
+    whole.append(k, v, c.table, c.d_lens, _starts(torch, n))
+    step = _ops().KV4Cache(c.cache.n_pages, 2, 128, track=True)
+    at = [0, 0]
+    rng = np.random.default_rng(3)
+    while at != n:
+        take = [min(int(rng.integers(0, 9)), n[b] - at[b]) for b in range(2)]
+        junk = [min(3, n[b] - at[b] - take[b]) for b in range(2)]
+        # drafts first, which the next step overwrites
+        for extra in (junk, [0, 0]):
+            cnt = [take[b] + extra[b] for b in range(2)]
+            rows = torch.cat([torch.arange(at[b], at[b] + cnt[b]) + (0 if b == 0 else 140) for b in range(2)]).cuda()
+            kk, vv = k[rows], v[rows]
+            if extra is junk:
+                kk, vv = kk * 3, vv - 1
+            step.append(kk, vv, c.table, _ints(torch, [at[b] + cnt[b] for b in range(2)]), _starts(torch, cnt))
+        at = [at[b] + take[b] for b in range(2)]
+    for p in range(2):
+        a = whole.read(c.table, c.d_lens, 230, _starts(torch, n))[p]
+        assert torch.equal(a, step.read(c.table, c.d_lens, 230, _starts(torch, n))[p])
+    for b in range(2):
+        for i in range(n[b]):
+            page = int(c.table[b, i // 64])
+            assert int(step.positions[page, 1, i % 64]) == i and float(step.weights[page, 0, i % 64]) == 0.0
+
+
+def test_append_strides_and_given_positions():
+    torch = torch_cuda()
+    log("append strides")
+    c = Filled(torch, "mxfp4", 64, 2, [100], track=True)
+    x = _randn(torch, 4, 5, 2 * 2 * 64 + 1).half()
+    k, v = x[:, 1:129].unflatten(1, (2, 64)), x[:, 129:].unflatten(1, (2, 64))
+    c.cache.append(k, v, c.table, c.d_lens, positions=_ints(torch, [7, 8, 9, 1000, 11]))
+    gk, gv = c.cache.read(c.table, c.d_lens, 5, dtype=torch.float32)
+    assert np.array_equal(_np(gk), oa.quantized(_np(k), "mxfp4")) and np.array_equal(_np(gv), oa.quantized(_np(v), "mxfp4"))
+    page = int(c.table[0, 1])
+    assert c.cache.positions[page, 1, 31:36].tolist() == [7, 8, 9, 1000, 11]
+
+
+def test_append_to_places_that_are_not_there():
+    """Nothing is written: places behind the table or before it, pages outside of the cache, tokens of no sequence."""
+    torch = torch_cuda()
+    log("append nowhere")
+    c = Filled(torch, "nvfp4", 64, 1, [64, 64], track=True)
+    before = [t.clone() for t in (c.cache.pages, c.cache.weights, c.cache.positions)]
+    k = _randn(torch, 1, 6, 1, 64)
+    bad = c.table.clone()
+    bad[:, 1] = _ints(torch, [-1, c.cache.n_pages])
+    c.cache.append(k, k, bad, _ints(torch, [67, 67]))                            # pages -1 and n_pages
+    c.cache.append(k, k, c.table[:, :1], _ints(torch, [67, 1000000]))            # behind the table
+    c.cache.append(k, k, c.table, _ints(torch, [-5, 0]))                         # before the first place
+    c.cache.append(k, k, c.table, _ints(torch, [3, 3]), _ints(torch, [9, 12, 15]))   # of no sequence
+    for a, b in zip(before, (c.cache.pages, c.cache.weights, c.cache.positions)):
+        assert torch.equal(torch.nan_to_num(a.float(), nan=7.0), torch.nan_to_num(b.float(), nan=7.0))
+    k2, v2 = c.cache.read(c.table[:, :1], _ints(torch, [66, 64]), 6, dtype=torch.float32)
+    nan = torch.isnan(k2).all(-1).flatten().tolist()
+    assert nan == [False, True, True, False, False, False] and torch.equal(torch.isnan(k2), torch.isnan(v2))
+
+
+# ---- attention over the cache ------------------------------------------------
+
+def _check_attend(torch, c, q, dtype, accumulate=False, scale=None, out=None):
+    got = c.cache.attend(q, c.table, c.d_lens, scale=scale, accumulate=accumulate, out=out)
+    qn = _np(q)
+    sc = 1.0 / np.sqrt(c.d) if scale is None else scale
+    sums = []
+    for b in range(len(c.lens)):
+        k, v = c.of(b)
+        o, _, w, eo, _, ew = oa.attend(qn[b], k, v, sc, *P_EPS[c.fmt])
+        _close(got[b], o, eo, dtype, ("out", b, c.lens[b]))
+        sums.append((w, ew))
+    return got, sums
+
+
+LENS = [1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 0, 700]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("d,hkv,group,rows", [(64, 2, 1, 1), (64, 1, 7, 3), (128, 2, 8, 1), (128, 2, 6, 4), (128, 1, 5, 16),
+                                              (256, 1, 4, 1), (256, 1, 9, 3), (128, 3, 1, 2)])
+def test_attend(d, hkv, group, rows, fmt, dtype):
+    torch = torch_cuda()
+    log("attend", d, hkv, group, rows, fmt, dtype)
+    c = Filled(torch, fmt, d, hkv, LENS, seed=d + rows)
+    q = (2 * _randn(torch, 7, len(LENS), rows, hkv * group, d)).to(getattr(torch, TYPES[dtype]))
+    _check_attend(torch, c, q, dtype)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_attend_one_long_sequence_and_short_ones(fmt):
+    """Parts of the list that hold a head's middle, its end and many whole heads."""
+    torch = torch_cuda()
+    log("attend long", fmt)
+    lens = [5, 9000, 1, 0, 64] + [3] * 70
+    c = Filled(torch, fmt, 64, 2, lens, seed=3)
+    q = _randn(torch, 8, len(lens), 2, 4, 64).to(torch.bfloat16)
+    _check_attend(torch, c, 3 * q, "bf16", scale=0.3)
+
+
+def test_attend_with_scales_of_all():
+    torch = torch_cuda()
+    log("attend scales")
+    c = Filled(torch, "nvfp4", 128, 2, [77, 300], scales=(0.013, 2.5), seed=4)
+    _check_attend(torch, c, _randn(torch, 1, 2, 1, 8, 128).to(torch.float16), "fp16")
+
+
+@pytest.mark.parametrize("size", [1e-30, 1e-10, 1e4, 1e20])
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_attend_queries_of_any_size(size, fmt):
+    torch = torch_cuda()
+    log("attend query size", size, fmt)
+    c = Filled(torch, fmt, 128, 1, [200], seed=5)
+    q = _randn(torch, 1, 1, 2, 2, 128)
+    q[:, :, :, 64:] *= 2.0 ** -20          # small elements beside large ones count
+    q = (q * size).to(torch.bfloat16)
+    _check_attend(torch, c, q, "bf16", scale=0.5 / size)
+
+
+def test_attend_mxfp4_of_any_size():
+    torch = torch_cuda()
+    log("attend mxfp4 sizes")
+    for size in (2.0 ** -60, 2.0 ** 50):
+        c = Filled(torch, "mxfp4", 64, 1, [150], dtype="fp32", size=size, seed=6)
+        q = _randn(torch, 1, 1, 1, 2, 64).to(torch.bfloat16)
+        _check_attend(torch, c, q, "bf16", scale=1.0 / size / 8)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_attend_scores_far_apart(fmt):
+    """One key takes everything, early or late, and scores around -1000."""
+    torch = torch_cuda()
+    log("attend far scores", fmt)
+    c = Filled(torch, fmt, 64, 1, [300, 300], seed=7)
+    q = 40 * _randn(torch, 1, 2, 1, 2, 64)
+    _check_attend(torch, c, q.to(torch.bfloat16), "bf16", scale=1.0)
+
+
+@pytest.mark.parametrize("fmt,dtype,d,hkv,group,rows", [("nvfp4", "bf16", 128, 2, 8, 1), ("mxfp4", "fp16", 128, 2, 8, 4),
+                                                        ("nvfp4", "bf16", 64, 3, 5, 2), ("mxfp4", "bf16", 256, 1, 3, 6),
+                                                        ("nvfp4", "fp16", 256, 1, 1, 1)])
+def test_attend_keeps_weights(fmt, dtype, d, hkv, group, rows):
+    torch = torch_cuda()
+    log("attend weights", fmt, dtype, d, hkv, group, rows)
+    c = Filled(torch, fmt, d, hkv, LENS, track=True, seed=11)
+    start = c.cache.weights.clone()
+    q = (2 * _randn(torch, 7, len(LENS), rows, hkv * group, d)).to(getattr(torch, TYPES[dtype]))
+    got, sums = _check_attend(torch, c, q, dtype, accumulate=True)
+    assert torch.equal(got, c.cache.attend(q, c.table, c.d_lens))
+    _check_attend(torch, c, q, dtype, accumulate=True)                     # and adds the same again
+    touched = torch.zeros_like(start, dtype=torch.bool)
+    for b, (w, ew) in enumerate(sums):
+        n = c.lens[b]
+        for p in range((n + 63) // 64):
+            m = min(64, n - 64 * p)
+            page = int(c.table[b, p])
+            touched[page, :, :m] = True
+            got_w = c.cache.weights[page, :, :m].t()
+            rows_w = slice(64 * p, 64 * p + m)
+            _close(got_w, 2 * w[rows_w], 2 * ew[rows_w] + 2.0 ** -23 * w[rows_w], "fp32", ("weights", b, p))
+    # tokens of no sequence keep what they had
+    assert torch.equal(torch.nan_to_num(c.cache.weights[~touched], nan=7.0), torch.nan_to_num(start[~touched], nan=7.0))
+
+
+def test_attend_lengths_and_pages_that_cannot_be():
+    torch = torch_cuda()
+    log("attend bad pages")
+    c = Filled(torch, "nvfp4", 64, 2, [100, 100, 100, 100], track=True)
+    q = _randn(torch, 1, 4, 2, 4, 64).to(torch.bfloat16)
+    good = c.cache.attend(q, c.table, c.d_lens)
+    bad = c.table.clone()
+    bad[1, 1], bad[3, 0] = c.cache.n_pages, -7
+    got = c.cache.attend(q, bad, c.d_lens, accumulate=True)
+    assert torch.equal(got[0], good[0]) and torch.equal(got[2], good[2])
+    assert bool(torch.isnan(got[1]).all()) and bool(torch.isnan(got[3]).all())
+    got = c.cache.attend(q, c.table, _ints(torch, [100, -1, 64 * c.table.shape[1] + 1, 100]))
+    assert torch.equal(got[0], good[0]) and torch.equal(got[3], good[3]) and bool(torch.isnan(got[1:3]).all())
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_attend_values_that_are_not_finite(which, fmt):
+    """A token whose group reads as NaN: rows before it are not touched, the others are."""
+    torch = torch_cuda()
+    log("attend nan", which, fmt)
+    for d in (64, 128, 256):
+        c = Filled(torch, fmt, d, 2, [130, 90])
+        q = _randn(torch, 1, 2, 4, 6, d).to(torch.bfloat16)
+        k, v = _randn(torch, 2, 8, 2, d), _randn(torch, 3, 8, 2, d)
+        c.cache.append(k, v, c.table, c.d_lens)
+        sane = c.cache.attend(q, c.table, c.d_lens)
+        (k if which == "k" else v)[2, 1, 35] = float("nan")           # row 2 of the first sequence, head 1
+        c.cache.append(k, v, c.table, c.d_lens)
+        out = c.cache.attend(q, c.table, c.d_lens)
+        assert torch.equal(out[1], sane[1]) and torch.equal(out[0, :2], sane[0, :2]) and torch.equal(out[0, :, :3], sane[0, :, :3])
+        nan = torch.isnan(out[0, 2:, 3:])
+        if which == "k":
+            assert bool(nan.all())
+        else:
+            g = 16 if fmt == "nvfp4" else 32
+            lo = 35 // g * g
+            assert bool(nan[..., lo:lo + g].all()) and int(nan.sum()) == nan.shape[0] * nan.shape[1] * g
+
+
+def test_attend_strides():
+    torch = torch_cuda()
+    log("attend strides")
+    c = Filled(torch, "nvfp4", 64, 2, [70, 5, 129])
+    big = _randn(torch, 1, 2, 3, 6 * 64 + 3).to(torch.bfloat16)
+    q = big[:, :, 2:2 + 4 * 64].unflatten(2, (4, 64)).transpose(0, 1)          # [3, 2, 4, 64]
+    want = c.cache.attend(q.contiguous(), c.table, c.d_lens)
+    assert torch.equal(c.cache.attend(q, c.table, c.d_lens), want)
+    pool = torch.full((3, 5, 2, 64 + 1), 3.0, dtype=torch.bfloat16, device="cuda")
+    out = pool[:, :4, :, 1:].transpose(1, 2)
+    c.cache.attend(q, c.table, c.d_lens, out=out)
+    assert torch.equal(out, want)
+    out.fill_(3.0)
+    assert bool((pool == 3.0).all())
+    wide = torch.full((3, 9), -1, dtype=torch.int32, device="cuda")
+    wide[:, 2:2 + c.table.shape[1]] = c.table
+    assert torch.equal(c.cache.attend(q, wide[:, 2:2 + c.table.shape[1]], c.d_lens), want)
+
+
+def test_attend_does_not_depend_on_the_pages_or_the_batch_beyond_rounding():
+    torch = torch_cuda()
+    log("attend repeat")
+    c = Filled(torch, "nvfp4", 128, 2, [1000, 3, 500])
+    q = _randn(torch, 1, 3, 1, 8, 128).to(torch.bfloat16)
+    a = c.cache.attend(q, c.table, c.d_lens)
+    for _ in range(5):
+        assert torch.equal(a, c.cache.attend(q, c.table, c.d_lens))
+
+
+# ---- eviction ----------------------------------------------------------------
+
+def _check_evict(torch, c, weights, positions, keep, recent, sinks):
+    """weights, positions: [tokens, hkv] by place of each sequence."""
+    s = 0
+    for b, n in enumerate(c.lens):
+        for p in range((n + 63) // 64):
+            m = min(64, n - 64 * p)
+            page = int(c.table[b, p])
+            c.cache.weights[page, :, :m] = torch.tensor(weights[s + 64 * p:s + 64 * p + m].T.copy(), device="cuda")
+            c.cache.positions[page, :, :m] = torch.tensor(positions[s + 64 * p:s + 64 * p + m].T.copy(), device="cuda")
+        s += n
+    new = c.cache.evict(c.table, c.d_lens, keep, recent=recent, sinks=sinks)
+    want = [min(n, keep) for n in c.lens]
+    assert new.tolist() == want
+    k, v = c.cache.read(c.table, new, sum(want), _starts(torch, want), dtype=torch.float32)
+    k, v = _np(k), _np(v)
+    s = o = 0
+    for b, n in enumerate(c.lens):
+        ck, cv = c.of(b)
+        for h in range(c.hkv):
+            src = oa.evict(weights[s:s + n, h], positions[s:s + n, h], keep, recent, sinks)
+            assert np.array_equal(k[o:o + want[b], h], ck[src, h]), (b, h)
+            assert np.array_equal(v[o:o + want[b], h], cv[src, h]), (b, h)
+            place = np.arange(want[b])
+            page = _np(c.table[b]).astype(int)[place // 64]
+            assert np.array_equal(_np(c.cache.positions)[page, h, place % 64], positions[s:s + n, h][src])
+            assert np.array_equal(np.nan_to_num(_np(c.cache.weights)[page, h, place % 64], nan=-5.0),
+                                  np.nan_to_num(weights[s:s + n, h][src].astype(np.float64), nan=-5.0))
+        s += n
+        o += want[b]
+    return new
+
+
+@pytest.mark.parametrize("fmt,d,hkv", [("nvfp4", 128, 2), ("mxfp4", 64, 3), ("mxfp4", 256, 1), ("nvfp4", 64, 1),
+                                       ("nvfp4", 256, 2), ("mxfp4", 128, 1)])
+@pytest.mark.parametrize("keep,recent,sinks", [(1, 0, 0), (1, 1, 0), (64, 10, 4), (100, 100, 0), (129, 0, 129), (700, 5, 5)])
+def test_evict(fmt, d, hkv, keep, recent, sinks):
+    torch = torch_cuda()
+    log("evict", fmt, d, hkv, keep, recent, sinks)
+    lens = [0, 1, 64, 65, 130, 500, 1100, 1024]
+    c = Filled(torch, fmt, d, hkv, lens, track=True, seed=keep)
+    rng = np.random.default_rng(keep)
+    T = sum(lens)
+    w = np.where(rng.random((T, hkv)) < 0.5, rng.integers(0, 4, (T, hkv)), rng.exponential(1.0, (T, hkv))).astype(np.float32)
+    at = np.concatenate([np.tile(np.arange(n)[:, None], (1, hkv)) for n in lens]).astype(np.int32)
+    for s, n in zip(np.concatenate(([0], np.cumsum(lens)[:-1])), lens):      # tokens of an earlier eviction: out of order
+        for h in range(hkv):
+            at[s:s + n, h] = rng.permutation(at[s:s + n, h]) * 3
+    _check_evict(torch, c, w, at, keep, recent, sinks)
+
+
+def test_evict_weights_of_all_kinds():
+    torch = torch_cuda()
+    log("evict kinds")
+    n = 600
+    c = Filled(torch, "nvfp4", 64, 1, [n], track=True)
+    rng = np.random.default_rng(2)
+    w = rng.choice(np.array([0.0, -0.0, 1e-45, 1e-38, 1.0, 1.0000001, np.inf, np.nan, 3e38, -1.0], np.float32), (n, 1))
+    at = np.arange(n, dtype=np.int32)[:, None]
+    for keep in (500, 300, 100, 20):
+        c = Filled(torch, "nvfp4", 64, 1, [n], track=True)
+        _check_evict(torch, c, w, at, keep, 3, 2)
+    c = Filled(torch, "nvfp4", 64, 1, [n], track=True)
+    _check_evict(torch, c, np.zeros((n, 1), np.float32), at, 250, 0, 0)      # all equal: the first places
+
+
+def test_evict_leaves_what_it_cannot_do():
+    torch = torch_cuda()
+    log("evict bad")
+    c = Filled(torch, "nvfp4", 64, 2, [200, 200, 200, 100], track=True)
+    c.cache.weights.uniform_()
+    bad = c.table.clone()
+    bad[1, 2] = c.cache.n_pages
+    lens = _ints(torch, [200, 200, 64 * bad.shape[1] + 1, 100])
+    keep_pages = torch.cat((c.table[1, :2], c.table[2, :4], c.table[3, :2])).long()
+    before = [t[keep_pages].clone() for t in (c.cache.pages, c.cache.weights, c.cache.positions)]
+    new = c.cache.evict(bad, lens, 100)
+    assert new.tolist() == [100, 200, 64 * bad.shape[1] + 1, 100] and lens.tolist()[0] == 200
+    for a, t in zip(before, (c.cache.pages, c.cache.weights, c.cache.positions)):
+        assert torch.equal(a, t[keep_pages])
+
+
+def test_evict_twice_and_go_on():
+    """Recent tokens are those of the last positions, wherever they are after an eviction."""
+    torch = torch_cuda()
+    log("evict twice")
+    c = Filled(torch, "mxfp4", 128, 2, [300], track=True)
+    w = np.random.default_rng(1).random((300, 2)).astype(np.float32)
+    at = np.tile(np.arange(300, dtype=np.int32)[:, None], (1, 2))
+    lens = _check_evict(torch, c, w, at, 100, 50, 4)
+    k = _randn(torch, 1, 20, 2, 128).to(torch.bfloat16)
+    c.cache.append(k, k, c.table, _ints(torch, [120]), positions=_ints(torch, list(range(300, 320))))
+    lens = c.cache.evict(c.table, _ints(torch, [120]), 72, recent=68, sinks=4)
+    assert lens.tolist() == [72]
+    for h in range(2):
+        got = sorted(int(c.cache.positions[int(c.table[0, i // 64]), h, i % 64]) for i in range(72))
+        assert got == list(range(4)) + list(range(252, 320))
+
+
+# ---- together ----------------------------------------------------------------
+
+def test_prompt_cache_steps_and_eviction_together():
+    """A prompt, its keys into the cache, steps with drafts that keep weights, eviction, more steps: as a program does."""
+    torch = torch_cuda()
+    log("together")
+    ops = _ops()
+    hq, hkv, d, new = 8, 2, 128, [150, 40]
+    T = sum(new)
+    starts = _starts(torch, new)
+    q, k, v = (_randn(torch, i, T, h, d).to(torch.bfloat16) for i, h in enumerate((hq, hkv, hkv)))
+    _check_prompt(torch, q, k, v, new, new, "bf16")
+    c = Filled(torch, "nvfp4", d, hkv, new, track=True, extra=200)
+    cache, table = c.cache, c.table
+    cache.append(k, v, table, _ints(torch, new), starts)
+    hk = [c.held(x, i) for i, x in enumerate((k, v))]
+    seqs = [[hk[0][:150], hk[1][:150]], [hk[0][150:], hk[1][150:]]]
+    sums = [np.zeros((n, hkv)) for n in new]
+    lens = _ints(torch, new)
+    pos = [150, 40]
+    for step in range(4):
+        R = 3
+        kn, vn = (_randn(torch, 100 + 2 * step + i, 2 * R, hkv, d).to(torch.bfloat16) for i in range(2))
+        qn = _randn(torch, 200 + step, 2, R, hq, d).to(torch.bfloat16)
+        lens = lens + R
+        at = _ints(torch, [p + i for p in pos for i in range(R)])
+        cache.append(kn, vn, table, lens, positions=at)
+        out = cache.attend(qn, table, lens, accumulate=True)
+        hn = [c.held(x, i) for i, x in enumerate((kn, vn))]
+        for b in range(2):
+            for i in range(2):
+                seqs[b][i] = np.concatenate((seqs[b][i], hn[i][b * R:b * R + R]))
+            o, _, w, eo, _, ew = oa.attend(_np(qn)[b], seqs[b][0], seqs[b][1], 1 / np.sqrt(d), *P_EPS["nvfp4"])
+            _close(out[b], o, eo, "bf16", ("step", step, b))
+            sums[b] = np.concatenate((sums[b], np.zeros((R, hkv)))) + w
+            pos[b] += R
+        if step == 1:
+            w_dev = cache.weights.clone()
+            lens = cache.evict(table, lens, 100, recent=16, sinks=2)
+            assert lens.tolist() == [100, 46]
+            n = 156
+            place = np.arange(n)
+            page = _np(table[0]).astype(int)[place // 64]
+            for h in range(hkv):
+                wd = _np(w_dev)[page, h, place % 64]
+                assert np.allclose(wd, sums[0][:, h], rtol=1e-4, atol=1e-6)
+                src = oa.evict(wd.astype(np.float32), place, 100, 16, 2)
+                for i in range(2):
+                    seqs[0][i][:100, h] = seqs[0][i][src, h]
+                sums[0][:100, h] = sums[0][src, h]
+            seqs[0] = [x[:100] for x in seqs[0]]
+            sums[0] = sums[0][:100]
+
+
+def test_calls_are_captured_and_replayed():
+    torch = torch_cuda()
+    log("graph")
+    c = Filled(torch, "nvfp4", 128, 2, [300, 70], track=True, extra=64)
+    q = _randn(torch, 1, 2, 2, 8, 128).to(torch.bfloat16)
+    k, v = (_randn(torch, 2 + i, 4, 2, 128).to(torch.bfloat16) for i in range(2))
+    pq, pk, pv = (_randn(torch, 5 + i, 200, h, 128).to(torch.bfloat16) for i, h in enumerate((8, 2, 2)))
+    starts = _ints(torch, [0, 77, 200])
+    lens = c.d_lens + 2
+
+    def step():
+        c.cache.append(k, v, c.table, lens)
+        o = c.cache.attend(q, c.table, lens, accumulate=True)
+        new = c.cache.evict(c.table, lens, 200, recent=10)
+        a, b = c.cache.read(c.table, new, 100)
+        return o, new, a, b, _ops().prompt_attention(pq, pk, pv, starts)
+
+    state = [t.clone() for t in (c.cache.pages, c.cache.weights, c.cache.positions)]
+
+    def reset():
+        for t, s in zip((c.cache.pages, c.cache.weights, c.cache.positions), state):
+            t.copy_(s)
+
+    step()
+    reset()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        res = step()
+    for i in range(4):
+        q.copy_(_randn(torch, 50 + i, 2, 2, 8, 128))
+        reset()
+        want = [t.clone() for t in step()]
+        w = c.cache.weights.clone()
+        reset()
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(res, want):
+            assert torch.equal(a, b), i
+        assert torch.equal(torch.nan_to_num(w, nan=7.0), torch.nan_to_num(c.cache.weights, nan=7.0))
+
+
+def test_calls_on_a_given_stream():
+    torch = torch_cuda()
+    log("streams")
+    c = Filled(torch, "mxfp4", 64, 2, [500, 90])
+    q = _randn(torch, 1, 2, 1, 8, 64).to(torch.bfloat16)
+    want = c.cache.attend(q, c.table, c.d_lens)
+    pq = _randn(torch, 2, 300, 2, 64).to(torch.bfloat16)
+    st = _ints(torch, [0, 300])
+    pwant = _ops().prompt_attention(pq, pq, pq, st)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    outs = []
+    for i in range(20):
+        for s in (s1, s2):
+            outs.append((c.cache.attend(q.clone() if s is None else q, c.table, c.d_lens, stream=s),
+                         _ops().prompt_attention(pq, pq, pq, st, stream=s)))
+    torch.cuda.synchronize()
+    for a, b in outs:
+        assert torch.equal(a, want) and torch.equal(b, pwant)
+
+
+def test_gradients_are_refused():
+    torch = torch_cuda()
+    log("gradients")
+    ops = _ops()
+    q = _randn(torch, 1, 5, 2, 64).to(torch.bfloat16).requires_grad_()
+    out = ops.prompt_attention(q, q.detach(), q.detach(), _ints(torch, [0, 5]))
+    with pytest.raises(NotImplementedError, match="prompt_attention"):
+        out.sum().backward()
+    c = Filled(torch, "nvfp4", 64, 1, [30])
+    qa = _randn(torch, 1, 1, 1, 2, 64).to(torch.bfloat16).requires_grad_()
+    with pytest.raises(NotImplementedError, match="attend"):
+        c.cache.attend(qa, c.table, c.d_lens).sum().backward()
+    with torch.no_grad():
+        c.cache.attend(qa, c.table, c.d_lens)
+
+
+def test_arguments_that_are_refused():
+    torch = torch_cuda()
+    log("refusals")
+    ops = _ops()
+    c = Filled(torch, "nvfp4", 64, 2, [30, 40])
+    cache, bf = c.cache, torch.bfloat16
+    q = torch.zeros(2, 1, 4, 64, dtype=bf, device="cuda")
+    k = torch.zeros(4, 2, 64, dtype=bf, device="cuda")
+    table, lens = c.table, c.d_lens
+    bad = [
+        lambda: cache.attend(q[:1], table, lens), lambda: cache.attend(q.float(), table, lens),
+        lambda: cache.attend(q[:, :, :3], table, lens), lambda: cache.attend(q[..., :32], table, lens),
+        lambda: cache.attend(q.transpose(2, 3), table, lens), lambda: cache.attend(q.cpu(), table, lens),
+        lambda: cache.attend(q.expand(2, 17, 4, 64), table, lens), lambda: cache.attend(q, table.long(), lens),
+        lambda: cache.attend(q, table.cpu(), lens), lambda: cache.attend(q, table, lens.long()),
+        lambda: cache.attend(q, table, lens[:1]), lambda: cache.attend(q, table, lens, scale=0.0),
+        lambda: cache.attend(q, table, lens, scale=float("nan")), lambda: cache.attend(q, table, lens, accumulate=True),
+        lambda: cache.attend(q, table, lens, out=q.new_empty(1, 1, 4, 64)),
+        lambda: cache.attend(q, table, lens, out=q.new_empty(1, 1, 4, 64).expand(2, 1, 4, 64)),
+        lambda: cache.attend(q, table[:, :0], lens), lambda: cache.attend(q, table[:1].expand(2, -1), lens),
+        lambda: cache.evict(table, lens, 10), lambda: cache.append(k[:3], k[:3], table, lens),
+        lambda: cache.append(k, k[:2], table, lens), lambda: cache.append(k, k.float(), table, lens),
+        lambda: cache.append(k[:, :1], k[:, :1], table, lens), lambda: cache.append(k.int(), k.int(), table, lens),
+        lambda: cache.append(k, k, table, lens, starts=lens), lambda: cache.append(k, k, table, lens, positions=lens),
+        lambda: cache.read(table, lens, 3), lambda: cache.read(table, lens, -2),
+        lambda: cache.read(table, lens, 2, dtype=torch.int32),
+        lambda: ops.prompt_attention(k, k, k, lens.long()), lambda: ops.prompt_attention(k, k[:3], k[:3], lens),
+        lambda: ops.prompt_attention(k, k, k.half(), lens), lambda: ops.prompt_attention(k[:, :1], k, k, lens),
+        lambda: ops.prompt_attention(k, k, k, lens, scale=-1.0), lambda: ops.prompt_attention(k, k, k, lens[:0]),
+        lambda: ops.prompt_attention(k, k, k, lens, key_starts=lens[:1]),
+        lambda: ops.prompt_attention(k, k, k, lens, out=k[:3]),
+        lambda: ops.prompt_attention(k, k, k, lens, out=k[:1].clone().expand(4, -1, -1)),
+    ]
+    for i, f in enumerate(bad):
+        with pytest.raises(ValueError):
+            f()
+            pytest.fail("call %d was taken" % i)
+    with pytest.raises(AttributeError):
+        cache.pages = cache.pages.clone()
+    t = ops.KV4Cache(2, 1, 64, track=True)
+    for kw in (dict(keep=0), dict(keep=4, recent=5), dict(keep=4, recent=3, sinks=2), dict(keep=4, recent=-1)):
+        with pytest.raises(ValueError):
+            t.evict(table, lens, **kw)
