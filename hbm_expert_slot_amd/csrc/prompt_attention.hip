@@ -116,23 +116,52 @@ __device__ __forceinline__ int sequence_at(const PromptArgs& a, int& t, int lane
   return a.n;
 }
 
-template <int D, bool HALF>
-__global__ __launch_bounds__(kThreads) void k_prompt(PromptArgs a) {
-  constexpr int kRow = D * 2 + 16;                   // bytes of a row in LDS
-  constexpr int NO = D / 32, NK = D / 16;
-  constexpr float kShift = HALF ? 14.0f : 0.0f;
-  __shared__ __align__(16) uint8_t lds_k[kKeys * kRow], lds_v[kKeys * kRow];
+// Tiles of keys and values lie in two LDS buffers; the next tile is fetched straight
+// into LDS during the products of this one.  Rows follow each other without padding,
+// as such loads need it; the 16-byte pieces of a row are exchanged so that neither
+// eight lanes that read a piece of eight rows of keys, nor sixteen that read two
+// pieces of four rows of values for a transposition, meet in a bank.
+//
+// m is the maximum that P counts from; it follows a row's scores only once they
+// exceed it by kSlack, so o is seldom multiplied again.
+template <int PR>
+__device__ __forceinline__ int key_piece(int row, int c) { return c ^ (row & 7); }
+template <int PR>
+__device__ __forceinline__ int value_piece(int row, int c) { return c ^ (row & 3) * 2; }
+
+// 16 bytes per lane from memory to LDS, one after the other from `to` on; waited for
+// by vmcnt.  (The builtin makes the compiler wait before every later LDS read.)
+__device__ __forceinline__ void load_to_lds(Rsrc from, uint32_t lane, uint32_t at, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(to), "v"(lane), "s"(from), "s"(at)
+               : "memory", "m0");
+}
+
+template <int D, bool HALF, bool DIRECT>
+__global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void k_prompt(PromptArgs a) {
+  constexpr int kRow = D * 2, kSide = kKeys * kRow;                // bytes in LDS
+  constexpr int NO = D / 32, NK = D / 16, PR = D / 8, NL = kKeys * PR / kThreads;   // pieces of a row, of a thread
+  constexpr int RL = kThreads / PR;                                // rows that the block loads at a time
+  // fp16 P counts from 2^14, so that what its range cuts off is below 2^-38 of the largest
+  constexpr float kShift = HALF ? 14.0f : 0.0f, kSlack = HALF ? 1.875f : 8.0f;
+  extern __shared__ __align__(16) uint8_t lds[];
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_index(), hi = lane >> 5, qc = lane & 31;
-  const int head = blockIdx.x % a.heads;
-  int tile = blockIdx.x / a.heads;
+  // blocks are dealt out to eight XCDs in turn: the heads of one, which share keys, to one of them
+  int head = blockIdx.x % a.heads, tile = blockIdx.x / a.heads;
+  if (a.heads % 8 == 0) {
+    const int per = a.heads / 8, xcd = blockIdx.x % 8, slot = blockIdx.x / 8;
+    head = xcd * per + slot % per;
+    tile = slot / per;
+  }
   const int b = sequence_at(a, tile, lane);
   if (b >= a.n) return;
   int row0, key0;
   const int rows = range_of(a.starts, b, a.rows, row0), keys = range_of(a.key_starts, b, a.keys, key0);
+  tile = (rows + kRows - 1) / kRows - 1 - tile;      // those with the most keys first
   const int r0 = tile * kRows + wave * 32, row = r0 + qc;
   const int ahead = keys - rows + 1;                 // keys that row 0 sees
   const int mine = min(keys, ahead + min(row, rows - 1));
-  const int end = min(keys, ahead + min(tile * kRows + kRows, rows) - 1);
+  const int end = min(keys, ahead + min(tile * kRows + kRows, rows) - 1);       // of the block
+  const int wave_end = r0 < rows ? min(keys, ahead + min(r0 + 32, rows) - 1) : 0, wave_all = ahead + r0;
   u32x4 q[NK];
   const uint16_t* qp = a.q + (int64_t)(row0 + min(row, rows - 1)) * a.qs[0] + head * a.qs[1] + hi * 8;
 #pragma unroll
@@ -144,6 +173,37 @@ __global__ __launch_bounds__(kThreads) void k_prompt(PromptArgs a) {
   float m, l;
   f32x16 o[NO];
   bool careful = false;      // values that only some rows see are not finite: in a second pass
+
+  const int lr = tid / PR, lc = tid % PR;            // the thread's row and piece
+  const uint32_t k_lane = (uint32_t)(lr * a.ks[0] * 2 + key_piece<PR>(lr, lc) * 16);
+  const uint32_t v_lane = (uint32_t)(lr * a.vs[0] * 2 + value_piece<PR>(lr, lc) * 16);
+  auto fetch = [&](int j0, int buf) {
+    uint8_t* to = lds + buf * 2 * kSide;
+    if (DIRECT && j0 + kKeys <= end && !careful) {
+      const Rsrc rk = make_rsrc(kp + (int64_t)j0 * a.ks[0], 0x7FFFFFFF), rv = make_rsrc(vp + (int64_t)j0 * a.vs[0], 0x7FFFFFFF);
+      const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)to) +
+                          wave * 1024;
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        load_to_lds(rk, k_lane, (uint32_t)(i * RL * a.ks[0] * 2), at + i * kThreads * 16);
+        load_to_lds(rv, v_lane, (uint32_t)(i * RL * a.vs[0] * 2), at + kSide + i * kThreads * 16);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        const int r = lr + i * RL, j = j0 + r;
+        u32x4 kr = {0, 0, 0, 0}, vr = {0, 0, 0, 0};      // nothing of other sequences
+        if (j < end) {
+          kr = load_row(kp + (int64_t)j * a.ks[0] + lc * 8);
+          vr = load_row(vp + (int64_t)j * a.vs[0] + lc * 8);
+        }
+        if (careful && j0 + kKeys > seen_by_all) vr = finite8<HALF>(vr);
+        *reinterpret_cast<u32x4*>(to + r * kRow + key_piece<PR>(r, lc) * 16) = kr;
+        *reinterpret_cast<u32x4*>(to + kSide + r * kRow + value_piece<PR>(r, lc) * 16) = vr;
+      }
+    }
+  };
+
 again:
   m = -INFINITY;
   l = 0.0f;
@@ -151,83 +211,82 @@ again:
   for (int i = 0; i < NO; ++i)
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[i][e] = 0.0f;
-
+  int buf = 0;
+  if (end > 0) fetch(0, 0);
+  __builtin_amdgcn_s_waitcnt(0x0F70);        // vmcnt(0): this wavefront's part of the tile is there
+  __syncthreads();
   for (int j0 = 0; j0 < end; j0 += kKeys) {
+    if (j0 + kKeys < end) fetch(j0 + kKeys, buf ^ 1);
+    const uint8_t* bk = lds + buf * 2 * kSide;
+    const uint8_t* bv = bk + kSide;
+    if (j0 < wave_end) {
+      f32x16 s[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[t][e] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NK; ++i) {
+          const u32x4 kw = *reinterpret_cast<const u32x4*>(bk + (t * 32 + qc) * kRow + key_piece<PR>(qc, 2 * i + hi) * 16);
+          s[t] = product<HALF>(kw, q[i], s[t]);
+        }
+      }
+      if (j0 + kKeys > wave_all) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (j0 + t * 32 + e / 4 * 8 + hi * 4 + e % 4 >= mine) s[t][e] = -INFINITY;
+      }
+      float top = s[0][0];
+#pragma unroll
+      for (int e = 1; e < 32; ++e) top = fmaxf(top, s[e / 16][e % 16]);
+      top = fmaxf(top, __shfl_xor(top, 32)) * factor;
+      if (__any(top > m + kSlack)) {
+        const float mn = top > m + kSlack ? top : m;       // of this row, whatever the others do
+        const float f = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.0f : mn));
+        l *= f;
+#pragma unroll
+        for (int i = 0; i < NO; ++i) o[i] *= f;
+        m = mn;
+      }
+      const float mu = (m == -INFINITY ? 0.0f : m) - kShift;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          s[t][e] = __builtin_amdgcn_exp2f(fmaf(s[t][e], factor, -mu));
+          l += s[t][e];
+        }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const f32x16& x = s[t / 2];
+        const int f = t % 2 * 8;
+        const u32x4 pw = {pack<HALF>(x[f], x[f + 1]), pack<HALF>(x[f + 2], x[f + 3]), pack<HALF>(x[f + 4], x[f + 5]),
+                          pack<HALF>(x[f + 6], x[f + 7])};
+#pragma unroll
+        for (int i = 0; i < NO; ++i) {
+          // rows 16 t + 4 hi .. + 3 and eight later, 16 dimensions of 32 i + 16 (lane / 16 % 2)
+          const int r = t * 16 + hi * 4 + (lane & 15) / 4, c = i * 4 + (lane >> 4 & 1) * 2 + (lane >> 1 & 1);
+          const uint8_t* p = bv + r * kRow + value_piece<PR>(r, c) * 16 + lane % 2 * 8;
+          const u32x2 lo = load_transposed(p), hw = load_transposed(p + 8 * kRow);
+          o[i] = product<HALF>(u32x4{lo.x, lo.y, hw.x, hw.y}, pw, o[i]);
+        }
+      }
+      if (careful && j0 + kKeys > seen_by_all) {
+        for (int j = j0; j < min(j0 + kKeys, mine); ++j)
+#pragma unroll
+          for (int i = 0; i < NO; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float x = widen<HALF>(vp[(int64_t)j * a.vs[0] + i * 32 + e / 4 * 8 + hi * 4 + e % 4]);
+              if (!(fabsf(x) < INFINITY)) o[i][e] += x;
+            }
+      }
+    }
+    buf ^= 1;
+    __builtin_amdgcn_s_waitcnt(0x0F70);      // vmcnt(0): this wavefront's part of the next tile is there
     __syncthreads();
-    constexpr int PR = D / 8;                        // pieces of a row
-#pragma unroll
-    for (int i = 0; i < kKeys * PR / kThreads; ++i) {
-      const int e = tid + i * kThreads, r = e / PR, c = e % PR, j = j0 + r;
-      u32x4 kv = {0, 0, 0, 0}, vv = {0, 0, 0, 0};    // nothing of other sequences
-      if (j < end) {
-        kv = load_row(kp + (int64_t)j * a.ks[0] + c * 8);
-        vv = load_row(vp + (int64_t)j * a.vs[0] + c * 8);
-        if (careful && j0 + kKeys > seen_by_all) vv = finite8<HALF>(vv);
-      }
-      *reinterpret_cast<u32x4*>(lds_k + r * kRow + c * 16) = kv;
-      *reinterpret_cast<u32x4*>(lds_v + r * kRow + c * 16) = vv;
-    }
-    __syncthreads();
-    f32x16 s[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) s[t][e] = 0.0f;
-#pragma unroll
-      for (int i = 0; i < NK; ++i) {
-        const u32x4 kw = *reinterpret_cast<const u32x4*>(lds_k + (t * 32 + qc) * kRow + i * 32 + hi * 16);
-        s[t] = product<HALF>(kw, q[i], s[t]);
-      }
-    }
-    float top = -INFINITY;
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int j = j0 + t * 32 + e / 4 * 8 + hi * 4 + e % 4;
-        if (j >= mine) s[t][e] = -INFINITY;
-        top = fmaxf(top, s[t][e]);
-      }
-    top = fmaxf(top, __shfl_xor(top, 32));
-    // fp16 P counts from 2^14, so that what its range cuts off is below 2^-38 of the largest
-    const float mn = fmaxf(m, top * factor), mz = mn == -INFINITY ? 0.0f : mn, mu = mz - kShift;
-    if (__any(mn != m)) {
-      const float f = __builtin_amdgcn_exp2f(m - mz);
-      l *= f;
-#pragma unroll
-      for (int i = 0; i < NO; ++i) o[i] *= f;
-      m = mn;
-    }
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        s[t][e] = __builtin_amdgcn_exp2f(fmaf(s[t][e], factor, -mu));
-        l += s[t][e];
-      }
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const f32x16& x = s[t / 2];
-      const int f = t % 2 * 8;
-      const u32x4 pw = {pack<HALF>(x[f], x[f + 1]), pack<HALF>(x[f + 2], x[f + 3]), pack<HALF>(x[f + 4], x[f + 5]),
-                        pack<HALF>(x[f + 6], x[f + 7])};
-#pragma unroll
-      for (int i = 0; i < NO; ++i) {
-        const uint8_t* p = lds_v + (t * 16 + hi * 4 + (lane & 15) / 4) * kRow + i * 64 + (lane >> 4 & 1) * 32 + lane % 4 * 8;
-        const u32x2 lo = load_transposed(p), hw = load_transposed(p + 8 * kRow);
-        o[i] = product<HALF>(u32x4{lo.x, lo.y, hw.x, hw.y}, pw, o[i]);
-      }
-    }
-    if (careful && j0 + kKeys > seen_by_all) {
-      for (int j = j0; j < min(j0 + kKeys, mine); ++j)
-#pragma unroll
-        for (int i = 0; i < NO; ++i)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float x = widen<HALF>(vp[(int64_t)j * a.vs[0] + i * 32 + e / 4 * 8 + hi * 4 + e % 4]);
-            if (!(fabsf(x) < INFINITY)) o[i][e] += x;
-          }
-    }
   }
   // 0 times a value that a row does not see is NaN where that is not finite
   if (!careful) {
@@ -257,12 +316,22 @@ again:
   if (a.lse && hi == 0) a.lse[(int64_t)(row0 + row) * a.heads + head] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l) - kShift) * kLn2;
 }
 
-template <int D>
-hipError_t launch(const PromptArgs& a, bool half, hipStream_t st) {
+template <int D, bool HALF, bool DIRECT>
+hipError_t launch(const PromptArgs& a, hipStream_t st) {
   const unsigned grid = (unsigned)((a.rows / kRows + a.n) * a.heads);
-  if (half) hipLaunchKernelGGL((k_prompt<D, true>), dim3(grid), dim3(kThreads), 0, st, a);
-  else hipLaunchKernelGGL((k_prompt<D, false>), dim3(grid), dim3(kThreads), 0, st, a);
+  constexpr int kLds = 4 * kKeys * D * 2;
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_prompt<D, HALF, DIRECT>),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((k_prompt<D, HALF, DIRECT>), dim3(grid), dim3(kThreads), kLds, st, a);
   return hipGetLastError();
+}
+// Loads to LDS take 16 aligned bytes; other keys and values go through registers.
+template <int D>
+hipError_t by_alignment(const PromptArgs& a, bool half, hipStream_t st) {
+  const bool direct = ((uintptr_t)a.k | (uintptr_t)a.v) % 16 == 0 && (a.ks[0] | a.ks[1] | a.vs[0] | a.vs[1]) % 8 == 0;
+  if (half) return direct ? launch<D, true, true>(a, st) : launch<D, true, false>(a, st);
+  return direct ? launch<D, false, true>(a, st) : launch<D, false, false>(a, st);
 }
 
 }  // namespace
@@ -299,6 +368,8 @@ extern "C" sc_status prompt_attention(const sc_prompt* p, void* stream) {
   for (int i = 0; i < 2; ++i) {
     if (p->q_stride[i] < 0 || p->k_stride[i] < 0 || p->v_stride[i] < 0 || p->out_stride[i] < 0)
       return fail(SC_E_ARG, "strides must be >= 0");
+    if (p->k_stride[0] > SC_PROMPT_MAX_STRIDE || p->v_stride[0] > SC_PROMPT_MAX_STRIDE)
+      return fail(SC_E_ARG, "keys and values must be at most %d elements apart", SC_PROMPT_MAX_STRIDE);
     a.qs[i] = p->q_stride[i];
     a.ks[i] = p->k_stride[i];
     a.vs[i] = p->v_stride[i];
@@ -312,9 +383,9 @@ extern "C" sc_status prompt_attention(const sc_prompt* p, void* stream) {
   a.scale = p->scale;
   const hipStream_t st = static_cast<hipStream_t>(stream);
   const bool half = p->type == SC_DTYPE_F16;
-  const hipError_t e = p->head_dim == 64    ? prompt::launch<64>(a, half, st)
-                       : p->head_dim == 128 ? prompt::launch<128>(a, half, st)
-                                            : prompt::launch<256>(a, half, st);
+  const hipError_t e = p->head_dim == 64    ? prompt::by_alignment<64>(a, half, st)
+                       : p->head_dim == 128 ? prompt::by_alignment<128>(a, half, st)
+                                            : prompt::by_alignment<256>(a, half, st);
   if (e != hipSuccess) return hip_fail(e, "prompt_attention launch");
   return SC_OK;
 }

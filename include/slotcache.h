@@ -462,6 +462,7 @@ SC_API sc_status moe_layer_forward(const sc_moe_config* cfg, const sc_moe_weight
 #define SC_PROMPT_MAX_HEADS 1024
 #define SC_PROMPT_MAX_SEQS 65536
 #define SC_PROMPT_MAX_ROWS (1 << 24)
+#define SC_PROMPT_MAX_STRIDE (1 << 23)   /* elements from a key or value to the next */
 
 /* Packed sequences: sequence b has the rows d_starts[b] .. d_starts[b+1]-1 of q
  * and the keys d_key_starts[b] .. d_key_starts[b+1]-1 of k and v.  Element d of
