@@ -23,7 +23,9 @@ using namespace fp4;
 
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kRows = 32 * kWaves;       // query rows of a block
-constexpr int kKeys = 64;                // keys of a tile
+// Keys of a tile.  With heads of 256 the sums alone take 128 registers.
+template <int D>
+constexpr int kKeysOf = D == 256 ? 32 : 64;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
 typedef __attribute__((ext_vector_type(16))) float f32x16;
@@ -77,10 +79,15 @@ __device__ __forceinline__ u32x4 finite8(u32x4 v) {
   }
   return v;
 }
+// LDS by its offsets: the products' operands are at a few lane offsets plus constants.
+template <typename T>
+__device__ __forceinline__ T lds_at(uint32_t at) {
+  return *(const __attribute__((address_space(3))) T*)at;
+}
 // Four rows of 16 columns, 8 bytes of a row per lane: a lane gets its column.
-__device__ __forceinline__ u32x2 load_transposed(const uint8_t* p) {
+__device__ __forceinline__ u32x2 load_transposed(uint32_t at) {
   typedef __attribute__((address_space(3))) s16x4 Lds;
-  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds*)(p)));
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds*)at));
 }
 
 // A sequence's rows or keys; none where the starts make no sense.
@@ -108,10 +115,10 @@ __device__ __forceinline__ int sequence_at(const PromptArgs& a, int& t, int lane
     const uint64_t beyond = __ballot(upto > t);
     if (beyond) {
       const int l = __builtin_ctzll(beyond);
-      t -= __shfl(upto - n, l);
+      t -= __builtin_amdgcn_readlane(upto - n, l);
       return i + l;
     }
-    sum = __shfl(upto, 63);
+    sum = __builtin_amdgcn_readlane(upto, 63);
   }
   return a.n;
 }
@@ -137,13 +144,13 @@ __device__ __forceinline__ void load_to_lds(Rsrc from, uint32_t lane, uint32_t a
 }
 
 template <int D, bool HALF, bool DIRECT>
-__global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void k_prompt(PromptArgs a) {
-  constexpr int kRow = D * 2, kSide = kKeys * kRow;                // bytes in LDS
+__global__ __launch_bounds__(kThreads, 2) void k_prompt(PromptArgs a) {
+  constexpr int kKeys = kKeysOf<D>, kRow = D * 2, kSide = kKeys * kRow;                // bytes in LDS
   constexpr int NO = D / 32, NK = D / 16, PR = D / 8, NL = kKeys * PR / kThreads;   // pieces of a row, of a thread
   constexpr int RL = kThreads / PR;                                // rows that the block loads at a time
   // fp16 P counts from 2^14, so that what its range cuts off is below 2^-38 of the largest
   constexpr float kShift = HALF ? 14.0f : 0.0f, kSlack = HALF ? 1.875f : 8.0f;
-  extern __shared__ __align__(16) uint8_t lds[];
+  extern __shared__ __align__(1024) uint8_t lds[];
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_index(), hi = lane >> 5, qc = lane & 31;
   // blocks are dealt out to eight XCDs in turn: the heads of one, which share keys, to one of them
   int head = blockIdx.x % a.heads, tile = blockIdx.x / a.heads;
@@ -177,12 +184,17 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void k_prompt(PromptArg
   const int lr = tid / PR, lc = tid % PR;            // the thread's row and piece
   const uint32_t k_lane = (uint32_t)(lr * a.ks[0] * 2 + key_piece<PR>(lr, lc) * 16);
   const uint32_t v_lane = (uint32_t)(lr * a.vs[0] * 2 + value_piece<PR>(lr, lc) * 16);
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+  // The lane's key row; its piece of product i differs from that of product 0 in bits 5 and 6.
+  const uint32_t k_at = lds0 + qc * kRow + key_piece<PR>(qc, hi) * 16;
+  // Rows 4 hi .. + 3 of the values, 16 dimensions of lane / 16 % 2; output tiles 1 and 3 of four differ in bit 6.
+  const int vr = hi * 4 + (lane & 15) / 4;
+  const uint32_t v_at = lds0 + kSide + vr * kRow + value_piece<PR>(vr, (lane >> 4 & 1) * 2 + (lane >> 1 & 1)) * 16 + lane % 2 * 8;
   auto fetch = [&](int j0, int buf) {
     uint8_t* to = lds + buf * 2 * kSide;
     if (DIRECT && j0 + kKeys <= end && !careful) {
       const Rsrc rk = make_rsrc(kp + (int64_t)j0 * a.ks[0], 0x7FFFFFFF), rv = make_rsrc(vp + (int64_t)j0 * a.vs[0], 0x7FFFFFFF);
-      const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)to) +
-                          wave * 1024;
+      const uint32_t at = lds0 + buf * 2 * kSide + wave * 1024;
 #pragma unroll
       for (int i = 0; i < NL; ++i) {
         load_to_lds(rk, k_lane, (uint32_t)(i * RL * a.ks[0] * 2), at + i * kThreads * 16);
@@ -217,30 +229,29 @@ again:
   __syncthreads();
   for (int j0 = 0; j0 < end; j0 += kKeys) {
     if (j0 + kKeys < end) fetch(j0 + kKeys, buf ^ 1);
-    const uint8_t* bk = lds + buf * 2 * kSide;
-    const uint8_t* bv = bk + kSide;
+    const uint32_t bk = k_at + buf * 2 * kSide, bv = v_at + buf * 2 * kSide;
     if (j0 < wave_end) {
-      f32x16 s[2];
+      f32x16 s[kKeys / 32];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
+      for (int t = 0; t < kKeys / 32; ++t) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) s[t][e] = 0.0f;
 #pragma unroll
         for (int i = 0; i < NK; ++i) {
-          const u32x4 kw = *reinterpret_cast<const u32x4*>(bk + (t * 32 + qc) * kRow + key_piece<PR>(qc, 2 * i + hi) * 16);
+          const u32x4 kw = lds_at<u32x4>((bk ^ i % 4 * 32) + i / 4 * 128 + t * 32 * kRow);
           s[t] = product<HALF>(kw, q[i], s[t]);
         }
       }
       if (j0 + kKeys > wave_all) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < kKeys / 32; ++t)
 #pragma unroll
           for (int e = 0; e < 16; ++e)
             if (j0 + t * 32 + e / 4 * 8 + hi * 4 + e % 4 >= mine) s[t][e] = -INFINITY;
       }
       float top = s[0][0];
 #pragma unroll
-      for (int e = 1; e < 32; ++e) top = fmaxf(top, s[e / 16][e % 16]);
+      for (int e = 1; e < kKeys / 2; ++e) top = fmaxf(top, s[e / 16][e % 16]);
       top = fmaxf(top, __shfl_xor(top, 32)) * factor;
       if (__any(top > m + kSlack)) {
         const float mn = top > m + kSlack ? top : m;       // of this row, whatever the others do
@@ -252,23 +263,22 @@ again:
       }
       const float mu = (m == -INFINITY ? 0.0f : m) - kShift;
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < kKeys / 32; ++t)
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           s[t][e] = __builtin_amdgcn_exp2f(fmaf(s[t][e], factor, -mu));
           l += s[t][e];
         }
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
+      for (int t = 0; t < kKeys / 16; ++t) {
         const f32x16& x = s[t / 2];
         const int f = t % 2 * 8;
         const u32x4 pw = {pack<HALF>(x[f], x[f + 1]), pack<HALF>(x[f + 2], x[f + 3]), pack<HALF>(x[f + 4], x[f + 5]),
                           pack<HALF>(x[f + 6], x[f + 7])};
 #pragma unroll
         for (int i = 0; i < NO; ++i) {
-          // rows 16 t + 4 hi .. + 3 and eight later, 16 dimensions of 32 i + 16 (lane / 16 % 2)
-          const int r = t * 16 + hi * 4 + (lane & 15) / 4, c = i * 4 + (lane >> 4 & 1) * 2 + (lane >> 1 & 1);
-          const uint8_t* p = bv + r * kRow + value_piece<PR>(r, c) * 16 + lane % 2 * 8;
+          // of rows 16 t + 4 hi .. + 3, and of those eight later
+          const uint32_t p = (bv ^ i % 2 * 64) + i / 2 * 128 + t * 16 * kRow;
           const u32x2 lo = load_transposed(p), hw = load_transposed(p + 8 * kRow);
           o[i] = product<HALF>(u32x4{lo.x, lo.y, hw.x, hw.y}, pw, o[i]);
         }
@@ -319,7 +329,7 @@ again:
 template <int D, bool HALF, bool DIRECT>
 hipError_t launch(const PromptArgs& a, hipStream_t st) {
   const unsigned grid = (unsigned)((a.rows / kRows + a.n) * a.heads);
-  constexpr int kLds = 4 * kKeys * D * 2;
+  constexpr int kLds = 4 * kKeysOf<D> * D * 2;
   const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_prompt<D, HALF, DIRECT>),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
   if (e != hipSuccess) return e;
