@@ -95,7 +95,10 @@ def prompt_attention(q, k, v, starts, key_starts=None, scale=None, out=None, ret
         p = B.sc_prompt(_TYPE[q.dtype], dim, heads, kv_heads, n, rows, keys, scale, q.data_ptr(), k.data_ptr(),
                         v.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(), starts.data_ptr(),
                         key_starts.data_ptr(), (qs[0], qs[1]), (ks[0], ks[1]), (vs[0], vs[1]), (os[0], os[1]))
-        B.prompt_attention(ctypes.byref(p), s)
+        ref = ctypes.byref(p)
+        need = B.prompt_attention_workspace_bytes(ref)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        B.prompt_attention(ref, None if ws is None else ws.data_ptr(), s)
     if stream is not None:
         _record(stream, q, k, v, starts, key_starts, out, lse)
     return (out, lse) if return_lse else out

@@ -37,6 +37,7 @@ SC_SCORE_SIGMOID = 1
 SC_PROMPT_MAX_HEADS = 1024
 SC_PROMPT_MAX_SEQS = 65536
 SC_PROMPT_MAX_ROWS = 1 << 24
+SC_PROMPT_MAX_STRIDE = 1 << 23
 SC_KV4_PAGE = 64
 SC_KV4_MAX_HEADS = 1024
 SC_KV4_MAX_SEQS = 65536
@@ -50,7 +51,8 @@ EXPORTED = (
     "slotcache_read_state", "slotcache_write_state", "slotcache_read_events",
     "slotcache_read_routing", "slotcache_read_kernel_spans", "slotcache_pin", "slotcache_last_error",
     "slotcache_destroy", "moe_layer_decode_static", "fp4_quantize", "fp4_dequantize", "fp4_linear",
-    "moe_layer_workspace_bytes", "moe_layer_prepare", "moe_layer_forward", "prompt_attention",
+    "moe_layer_workspace_bytes", "moe_layer_prepare", "moe_layer_forward",
+    "prompt_attention_workspace_bytes", "prompt_attention",
     "kv4_page_bytes", "kv4_append", "kv4_read", "kv4_attention_workspace_bytes", "kv4_attention",
     "kv4_evict_workspace_bytes", "kv4_evict",
 )
@@ -170,7 +172,8 @@ def lib():
             "moe_layer_prepare": [ctypes.POINTER(sc_moe_config), P, P],
             "moe_layer_forward": [ctypes.POINTER(sc_moe_config), ctypes.POINTER(sc_moe_weights), P, P, i64, i32, P,
                                   i32, i64, P, P, P],
-            "prompt_attention": [P, P],
+            "prompt_attention_workspace_bytes": [P, ctypes.POINTER(sz)],
+            "prompt_attention": [P, P, P],
             "kv4_page_bytes": [i32, i32, ctypes.POINTER(sz)],
             "kv4_append": [P, P, P, i32, P, P, P],
             "kv4_read": [P, P, P, i32, P, P],
@@ -308,8 +311,14 @@ def moe_layer_forward(cfg, w, d_workspace, d_x, ldx, M, d_y, y_type, ldy, d_ids,
     _check(lib().moe_layer_forward(cfg, w, d_workspace, d_x, ldx, M, d_y, y_type, ldy, d_ids, d_weights, stream))
 
 
-def prompt_attention(p, stream):
-    _check(lib().prompt_attention(p, stream))
+def prompt_attention_workspace_bytes(p):
+    n = ctypes.c_size_t()
+    _check(lib().prompt_attention_workspace_bytes(p, ctypes.byref(n)))
+    return n.value
+
+
+def prompt_attention(p, d_workspace, stream):
+    _check(lib().prompt_attention(p, d_workspace, stream))
 
 
 def kv4_page_bytes(fmt, head_dim):

@@ -575,16 +575,22 @@ __global__ __launch_bounds__(kThreads) void k_kv4_attend(AttendArgs a) {
 }
 
 // Joins the pieces of a head that several blocks worked on: one block per
-// sequence, head and column, one thread per dimension.  Also the sequences
-// without tokens (zeros), and those whose length cannot be (NaN).
+// sequence, head and column; groups of D / 4 threads take pieces in turn.  Also the
+// sequences without tokens (zeros), and those whose length cannot be (NaN).
 template <int D, int FMT, bool HALF, int NQ>
-__global__ __launch_bounds__(D) void k_kv4_join(AttendArgs a) {
-  const int lane = threadIdx.x & 63, d = threadIdx.x;
+__global__ __launch_bounds__(kThreads) void k_kv4_join(AttendArgs a) {
+  constexpr int T = D / 4, N = kThreads / T;       // threads of a group, groups
+  __shared__ float f_of[kBlocks];
+  __shared__ __align__(16) float red[N][D];
+  __shared__ float red_m[kWaves], red_l[kWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_index();
   const int col = blockIdx.x % a.cols, head = blockIdx.x / a.cols % a.pool.heads, b = blockIdx.x / a.cols / a.pool.heads;
   const int n = pages_of(a.seqs, b);
-  float v = 0.0f, lse = -INFINITY;
+  float lse = -INFINITY, inv = 0.0f;
+  f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
   if (n == 0) {
-    if (length_of(a.seqs, b) < 0) v = lse = NAN;
+    if (length_of(a.seqs, b) < 0) v.x = lse = inv = NAN;
+    if (tid < D) red[0][tid] = v.x;
   } else {
     const int per = a.pool.heads * a.chunks, chunk = col / (16 * NQ);
     int64_t pages;
@@ -592,24 +598,64 @@ __global__ __launch_bounds__(D) void k_kv4_join(AttendArgs a) {
     const int64_t start = before + (int64_t)(head * a.chunks + chunk) * n;
     const int w0 = part_of(units, start, a.nblocks), w1 = part_of(units, start + n - 1, a.nblocks);
     if (w0 == w1) return;
+    // the first part holds the piece that it ends with, the others those that they begin with
+    const auto place = [&](int w) -> int64_t {
+      return (int64_t)(2 * w + (w == w0 && cut(units, w, a.nblocks) < start)) * (16 * NQ) + col % (16 * NQ);
+    };
     float m = -INFINITY, l = 0.0f;
-    for (int w = w0; w <= w1; ++w) {
-      const int64_t u = cut(units, w, a.nblocks);
-      if (cut(units, w + 1, a.nblocks) == u) continue;
-      const int64_t at = (int64_t)(2 * w + (u < start)) * (16 * NQ) + col % (16 * NQ);
-      const float pm = a.part_ml[2 * at], pl = a.part_ml[2 * at + 1], x = a.part[at * D + d];
-      if (pl == 0.0f) continue;
-      const float mn = fmaxf(m, pm), mu = mn == -INFINITY ? 0.0f : mn;
-      const float f = __builtin_amdgcn_exp2f(m - mu), fp = __builtin_amdgcn_exp2f(pm - mu);
-      l = (l == 0.0f ? 0.0f : l * f) + pl * fp;
-      v = (m == -INFINITY && l == 0.0f ? 0.0f : v * f) + x * fp;
-      m = mn;
+    for (int w = w0 + tid; w <= w1; w += kThreads) {
+      const bool any = cut(units, w, a.nblocks) < cut(units, w + 1, a.nblocks);     // parts may be empty
+      const f32x2 ml = any ? *reinterpret_cast<const f32x2*>(a.part_ml + 2 * place(w)) : f32x2{-INFINITY, 0.0f};
+      m = fmaxf(m, ml.x);
     }
+#pragma unroll
+    for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+    if (lane == 0) red_m[wave] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) m = fmaxf(m, red_m[w]);
+    const float mu = m == -INFINITY ? 0.0f : m;
+    for (int w = w0 + tid; w <= w1; w += kThreads) {
+      const bool any = cut(units, w, a.nblocks) < cut(units, w + 1, a.nblocks);
+      const f32x2 ml = any ? *reinterpret_cast<const f32x2*>(a.part_ml + 2 * place(w)) : f32x2{-INFINITY, 0.0f};
+      const float f = ml.y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(ml.x - mu);
+      f_of[w - w0] = f;
+      if (ml.y != 0.0f) l += ml.y * f;
+    }
+#pragma unroll
+    for (int o = 32; o; o >>= 1) l += __shfl_xor(l, o);
+    if (lane == 0) red_l[wave] = l;
+    __syncthreads();
+    l = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) l += red_l[w];
+    constexpr int kAhead = 4;            // pieces of a group whose loads are under way together
+    const int first = w0 + tid / T;
+    for (int w = first; w <= w1; w += kAhead * N) {
+      f32x4 x[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        x[i] = *reinterpret_cast<const f32x4*>(a.part + place(min(w + i * N, w1)) * D + tid % T * 4);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const float f = w + i * N <= w1 ? f_of[w + i * N - w0] : 0.0f;
+        if (f != 0.0f) v += x[i] * f;        // what an empty part has is not looked at
+      }
+    }
+    *reinterpret_cast<f32x4*>(&red[tid / T][tid % T * 4]) = v;
     lse = lse2_of<FMT>(m, l);
-    v = l == 0.0f ? 0.0f : v * ((a.vs ? *a.vs : 1.0f) / l);
+    inv = l == 0.0f ? 0.0f : (a.vs ? *a.vs : 1.0f) / l;
+    __syncthreads();
+    if (tid < D) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int g = 0; g < N; ++g) sum += red[g][tid];
+      red[0][tid] = l == 0.0f ? 0.0f : sum * inv;
+    }
   }
-  a.out[b * a.os[0] + col / a.group * a.os[1] + (head * a.group + col % a.group) * a.os[2] + d] = narrow<HALF>(v);
-  if (a.lse && d == 0) a.lse[((int64_t)b * a.pool.heads + head) * a.cols + col] = lse;
+  if (tid < D)
+    a.out[b * a.os[0] + col / a.group * a.os[1] + (head * a.group + col % a.group) * a.os[2] + tid] = narrow<HALF>(red[0][tid]);
+  if (a.lse && tid == 0) a.lse[((int64_t)b * a.pool.heads + head) * a.cols + col] = lse;
 }
 
 // Adds the attention weights of all rows and query heads to the tokens' sums, from
@@ -698,7 +744,7 @@ template <int D, int FMT, bool HALF, int NQ>
 hipError_t launch(AttendArgs a, hipStream_t st) {
   hipLaunchKernelGGL((k_kv4_attend<D, FMT, HALF, NQ>), dim3(a.nblocks), dim3(kThreads), 0, st, a);
   const unsigned joins = (unsigned)a.seqs.n * a.pool.heads * a.cols;
-  hipLaunchKernelGGL((k_kv4_join<D, FMT, HALF, NQ>), dim3(joins), dim3(D), 0, st, a);
+  hipLaunchKernelGGL((k_kv4_join<D, FMT, HALF, NQ>), dim3(joins), dim3(kThreads), 0, st, a);
   if (a.lse) hipLaunchKernelGGL((k_kv4_weights<D, FMT, HALF>), dim3(a.nblocks), dim3(kThreads), 0, st, a);
   return hipGetLastError();
 }

@@ -473,7 +473,7 @@ typedef struct {
   int32_t head_dim;               /* 64, 128 or 256 */
   int32_t q_heads, kv_heads;      /* q_heads is a multiple of kv_heads; head h reads key head h / (q_heads / kv_heads) */
   int32_t n_seqs;                 /* <= SC_PROMPT_MAX_SEQS */
-  int32_t rows, keys;             /* of all sequences; rows <= SC_PROMPT_MAX_ROWS */
+  int32_t rows, keys;             /* of all sequences; (rows / 128 + n_seqs) * q_heads < 2^24 */
   float scale;                    /* > 0 */
   const void* d_q;
   const void* d_k;
@@ -485,15 +485,21 @@ typedef struct {
   int64_t q_stride[2], k_stride[2], v_stride[2], out_stride[2];
 } sc_prompt;
 
+/* Bytes of device workspace that prompt_attention needs: 0 but for few rows over
+ * many keys.  Reads the sizes only. */
+SC_API sc_status prompt_attention_workspace_bytes(const sc_prompt* p, size_t* bytes);
+
 /* Causal attention of every row over its sequence's keys: with Lq rows and Lk
  * keys row i sees the keys below Lk - Lq + i + 1.  out = softmax(scale q k^T) v
  * of the keys seen, lse the natural logarithm of the sum of exponentials; a row
  * that sees none gets 0 and -infinity.  Products are exact, sums and softmax
  * statistics fp32, P is rounded to the type of v, out once.  Rows outside of the
  * sequences are not written; a sequence whose starts are not in order or exceed
- * rows or keys counts as empty.  out must not overlap q, k or v.  Asynchronous on
- * `stream`, whose device is current; no workspace, no allocation; can be captured. */
-SC_API sc_status prompt_attention(const sc_prompt* p, void* stream);
+ * rows or keys counts as empty.  out must not overlap q, k or v.  d_workspace
+ * (16-byte aligned, NULL where it needs no bytes) holds nothing from one call to the
+ * next; calls that may run at once need one each.  Asynchronous on `stream`, whose
+ * device is current; no allocation; can be captured. */
+SC_API sc_status prompt_attention(const sc_prompt* p, void* d_workspace, void* stream);
 
 /* ---- a key/value cache in 4 bits ------------------------------------------------ */
 

@@ -74,7 +74,7 @@ def test_null_structures():
     _fails(B.kv4_append, c, s, None, 2, None, None, None)
     _fails(B.kv4_read, c, s, None, 2, None, None)
     _fails(B.kv4_attention, c, s, None, 0, P, None)
-    _fails(B.prompt_attention, None, None)
+    _fails(B.prompt_attention, None, None, None)
 
 
 @pytest.mark.parametrize("change,tokens", [
@@ -149,15 +149,26 @@ def _prompt(**kw):
     dict(n_seqs=-1), dict(n_seqs=65537), dict(rows=-1), dict(rows=(1 << 24) + 1), dict(keys=-1), dict(scale=0.0),
     dict(scale=float("nan")), dict(scale=float("inf")), dict(d_q=None), dict(d_k=None), dict(d_v=None), dict(d_out=None),
     dict(d_q=P + 1), dict(d_lse=P + 2), dict(d_starts=None), dict(d_key_starts=None), dict(d_starts=P + 2),
+    dict(rows=1 << 24, q_heads=1024, kv_heads=1), dict(k_stride=((1 << 23) + 1, 0)), dict(v_stride=((1 << 23) + 1, 0)),
     dict(q_stride=(-1, 0)), dict(k_stride=(0, -1)), dict(v_stride=(-1, 0)), dict(out_stride=(-1, 0)),
 ])
 def test_prompts_that_are_refused(change):
-    _fails(B.prompt_attention, R(_prompt(**change)), None)
+    _fails(B.prompt_attention, R(_prompt(**change)), None, None)
+
+
+def test_prompt_workspace():
+    assert B.prompt_attention_workspace_bytes(R(_prompt())) == 0
+    few = _prompt(rows=100, keys=20000)
+    assert B.prompt_attention_workspace_bytes(R(few)) > 0
+    _fails(B.prompt_attention, R(few), None, None)
+    _fails(B.prompt_attention, R(few), P + 8, None)
+    _fails(B.prompt_attention_workspace_bytes, None)
+    _fails(B.prompt_attention_workspace_bytes, R(_prompt(head_dim=80)))
 
 
 def test_nothing_to_do_is_no_error():
-    B.prompt_attention(R(_prompt(rows=0)), None)
-    B.prompt_attention(R(_prompt(n_seqs=0)), None)
+    B.prompt_attention(R(_prompt(rows=0)), None, None)
+    B.prompt_attention(R(_prompt(n_seqs=0)), None, None)
     c, none = R(_cache()), R(_seqs(n_seqs=0))
     B.kv4_append(c, none, R(_rows()), 0, None, None, None)
     B.kv4_read(c, R(_seqs()), R(_rows()), 0, None, None)

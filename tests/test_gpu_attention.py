@@ -90,6 +90,19 @@ def test_chunks_of_prompts(new, full, dtype):
     _check_prompt(torch, q, k, v, new, full, dtype, scale=0.2)
 
 
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("fp16", 64), ("bf16", 256)])
+def test_few_rows_over_many_keys(dtype, d):
+    """Keys in parts, some of which are behind what a row sees, or of sequences that have no key for a part."""
+    torch = torch_cuda()
+    log("few rows, many keys", dtype, d)
+    dt = getattr(torch, TYPES[dtype])
+    for new, full in (([7, 130, 1], [9000, 131, 8000]), ([3, 0, 2], [16500, 10, 1]), ([40], [5000])):
+        q = _randn(torch, 1, sum(new), 2, d).to(dt)
+        k, v = (_randn(torch, 2 + i, sum(full) + 3, 1, d).to(dt)[3:] for i in range(2))
+        assert sum(full) // len(full) >= 4096
+        _check_prompt(torch, 2 * q, k, v, new, full, dtype)
+
+
 def test_prompt_of_a_few_thousand_tokens():
     torch = torch_cuda()
     log("long prompt")
