@@ -52,7 +52,7 @@ struct AttendArgs {
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
 typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
 
-// The result takes no register of an operand: they live until it is there.
+// The operands live until the result is there, so that it takes no register of theirs.
 template <bool F16>
 __device__ __forceinline__ f32x4 product(u32x4 a, u32x4 b, f32x4 c) {
   f32x4 d;
@@ -81,22 +81,24 @@ __device__ __forceinline__ f16x2 scales2(uint32_t d) {
   return __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)d, 1.0f, W));
 }
 
-// What a lane holds of a page: see Layout.
+// What a lane holds of a step, half a page of 32 tokens: see Layout.
+constexpr int kStep = 32;
 template <int D, int FMT>
-struct PageKeys {
+struct Keys {
   typedef Layout<D, FMT> L;
   static constexpr int W = L::C * L::LaneDims / 8;     // words per tile of 16 tokens
-  uint32_t q[4][W];
-  uint32_t s[L::SP];
+  uint32_t q[2][W];
+  uint32_t s[(L::SP + 1) / 2];                         // scales of both tiles
 };
 template <int D, int FMT>
-struct PageValues {
+struct Values {
   typedef Layout<D, FMT> L;
   static constexpr int W = L::C * L::VDims / 2;        // words per 16 tokens
-  uint32_t q[4][W];
-  u32x4 s[L::C];
+  uint32_t q[2][W];
+  u32x2 s[L::C];
 };
 
+// Pages are read once a call (twice with weights): past the caches.
 template <int N>
 __device__ __forceinline__ void load_words(uint32_t* d, const uint8_t* p) {
   typedef __attribute__((ext_vector_type(N))) uint32_t V;
@@ -110,41 +112,43 @@ __device__ __forceinline__ void load_words<1>(uint32_t* d, const uint8_t* p) {
 }
 
 template <int D, int FMT>
-__device__ __forceinline__ void load_keys(PageKeys<D, FMT>& p, const uint8_t* side, int lane) {
+__device__ __forceinline__ void load_keys(Keys<D, FMT>& p, const uint8_t* side, int half, int lane) {
   typedef Layout<D, FMT> L;
   const int r = lane & 15, g = lane >> 4;
   constexpr int B = L::LaneDims / 2;
 #pragma unroll
-  for (int t = 0; t < 4; ++t)
+  for (int t = 0; t < 2; ++t)
 #pragma unroll
     for (int c = 0; c < L::C; ++c)
-      load_words<B / 4>(&p.q[t][c * (B / 4)], side + (t * 16 + r) * (D / 2) + c * 64 + g * B);
-  load_words<L::SP>(p.s, side + L::kCodes + (r * L::SL + (L::SL == 4 ? g : g >> 1)) * 4 * L::SP);
+      load_words<B / 4>(&p.q[t][c * (B / 4)], side + half * (16 * D) + (t * 16 + r) * (D / 2) + c * 64 + g * B);
+  const uint8_t* s = side + L::kCodes + half * 2 * L::SP + (r * L::SL + (L::SL == 4 ? g : g >> 1)) * 4 * L::SP;
+  if constexpr (L::SP == 1) p.s[0] = __builtin_nontemporal_load(reinterpret_cast<const uint16_t*>(s));
+  else load_words<L::SP / 2>(p.s, s);
 }
 template <int D, int FMT>
-__device__ __forceinline__ void load_values(PageValues<D, FMT>& p, const uint8_t* side, int lane) {
+__device__ __forceinline__ void load_values(Values<D, FMT>& p, const uint8_t* side, int half, int lane) {
   typedef Layout<D, FMT> L;
   const int n = lane & 15, g = lane >> 4;
   constexpr int B = L::VDims / 2;        // bytes of a token
 #pragma unroll
-  for (int t = 0; t < 4; ++t)
+  for (int t = 0; t < 2; ++t)
 #pragma unroll
     for (int c = 0; c < L::C; ++c)
-      load_words<B>(&p.q[t][c * B], side + (((t * 4 + g) * L::C + c) * 16 + n) * 4 * B);
+      load_words<B>(&p.q[t][c * B], side + half * (16 * D) + (((t * 4 + g) * L::C + c) * 16 + n) * 4 * B);
 #pragma unroll
   for (int c = 0; c < L::C; ++c) {
     const int s = c * (128 / L::G) + n * L::VDims / L::G;
-    p.s[c] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(side + L::kCodes + (g * L::NS + s) * 16));
+    p.s[c] = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(side + L::kCodes + (g * L::NS + s) * 16 + half * 8));
   }
 }
 
 // Operand words of tile T of the keys: words of chunk c, eight dimensions each.
 template <int D, int FMT>
-__device__ __forceinline__ void widen_keys(const PageKeys<D, FMT>& p, int t, u32x4 (&out)[PageKeys<D, FMT>::W]) {
+__device__ __forceinline__ void widen_keys(const Keys<D, FMT>& p, int t, u32x4 (&out)[Keys<D, FMT>::W]) {
   typedef Layout<D, FMT> L;
   constexpr int WC = L::LaneDims / 8, E = L::SP / L::C;     // words, scales of a chunk
 #pragma unroll
-  for (int w = 0; w < PageKeys<D, FMT>::W; ++w) {
+  for (int w = 0; w < Keys<D, FMT>::W; ++w) {
     const int c = w / WC, e = c * E + (w % WC) * E / WC;    // the word's scale
     const int at = t * L::SP + e;                           // its byte
     const uint32_t q = p.q[t][w];
@@ -205,20 +209,23 @@ __device__ __forceinline__ uint32_t rest16(float a, float b, uint32_t hi) {
   return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)(x == x ? x : 0.0f), (__bf16)(y == y ? y : 0.0f)});
 }
 
+// Over the four lanes of a column.
 __device__ __forceinline__ float max_over_g(float v) {
-  v = fmaxf(v, __shfl_xor(v, 16));
-  return fmaxf(v, __shfl_xor(v, 32));
+  const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 __device__ __forceinline__ float sum_over_g(float v) {
-  v += __shfl_xor(v, 16);
-  return v + __shfl_xor(v, 32);
+  v = swap_sum<32>(v, v);
+  return swap_sum<16>(v, v);
 }
 
 // The columns of one tile: column l % 16 of lane l, and its share of the dimensions.
 template <int D, int FMT, bool HALF>
 struct Queries {
   typedef Layout<D, FMT> L;
-  static constexpr int W = PageKeys<D, FMT>::W, P = FMT == kMx && HALF ? 2 : 1;
+  static constexpr int W = Keys<D, FMT>::W, P = FMT == kMx && HALF ? 2 : 1;
   u32x4 x[W][P];
   float factor;     // of the products, to get scores in base 2
   int row;          // of the column; beyond the last: it sees what the last does
@@ -292,19 +299,17 @@ __device__ __forceinline__ int64_t wave_scan(int64_t v, int lane) {
   }
   return v;
 }
+__device__ __forceinline__ int64_t of_lane(int64_t v, int l) {
+  const uint32_t lo = __builtin_amdgcn_readlane((int)v, l), hi = __builtin_amdgcn_readlane((int)(v >> 32), l);
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
 // Pages of the sequences before b, and of all.
 __device__ __forceinline__ int64_t pages_before(const Seqs& s, int b, int64_t& total, int lane) {
   int64_t before = 0, sum = 0;
   for (int i = 0; i < s.n; i += 64) {
-    const int64_t n = pages_of(s, i + lane);
-    int64_t x = n, y = i + lane < b ? n : 0;
-#pragma unroll
-    for (int o = 32; o; o >>= 1) {
-      x += __shfl_xor(x, o);
-      y += __shfl_xor(y, o);
-    }
-    sum += x;
-    before += y;
+    const int64_t upto = wave_scan(pages_of(s, i + lane), lane);
+    if (b >= i && b < i + 64) before = sum + (b > i ? of_lane(upto, b - i - 1) : 0);
+    sum += of_lane(upto, 63);
   }
   total = sum;
   return before;
@@ -319,10 +324,10 @@ __device__ __forceinline__ int sequence_at(const Seqs& s, int64_t u, int per, in
     const uint64_t beyond = __ballot(upto > u);
     if (beyond) {
       const int l = __builtin_ctzll(beyond);
-      before = __shfl(upto - n, l);
+      before = of_lane(upto - n, l);
       return i + l;
     }
-    sum = __shfl(upto, 63);
+    sum = of_lane(upto, 63);
   }
   before = sum;
   return s.n;
@@ -342,12 +347,17 @@ __device__ __forceinline__ float lse2_of(float m, float l) {
   return l == 0.0f ? -INFINITY : m + __builtin_amdgcn_logf(l) - (FMT == kNv ? 14.0f : 0.0f);
 }
 
+// The wavefronts of a block take its steps in turn.  A step's keys are fetched while
+// the step before is in its softmax and second product, its values during its own
+// first product: into the registers that the step before has just left.
 template <int D, int FMT, bool HALF, int NQ>
-__global__ __launch_bounds__(kThreads) void k_kv4_attend(AttendArgs a) {
+__global__ __launch_bounds__(kThreads, 2) void k_kv4_attend(AttendArgs a) {
   typedef Layout<D, FMT> L;
   constexpr bool F16 = FMT == kNv;
-  constexpr int W = PageKeys<D, FMT>::W, VD = L::VDims, NO = L::C * VD;     // output tiles
-  constexpr int PP = FMT == kMx ? 2 : 1;
+  constexpr int W = Keys<D, FMT>::W, VD = L::VDims, NO = L::C * VD;     // output tiles
+  constexpr int QP = Queries<D, FMT, HALF>::P, PP = FMT == kMx ? 2 : 1;
+  // m is the maximum that P counts from; it follows the scores once they exceed it by kSlack
+  constexpr float kShift = F16 ? 14.0f : 0.0f, kSlack = F16 ? 1.875f : 8.0f;
   constexpr int kRow = D + 4;
   __shared__ __align__(16) float red[kWaves][16][kRow];
   __shared__ float red_m[kWaves][16], red_l[kWaves][16];
@@ -363,12 +373,21 @@ __global__ __launch_bounds__(kThreads) void k_kv4_attend(AttendArgs a) {
     const int n = pages_of(a.seqs, b), len = length_of(a.seqs, b);
     const int hc = (int)((u - before) / n), head = hc / a.chunks, chunk = hc % a.chunks;
     const int p0 = (int)((u - before) % n), p1 = (int)(u1 - u < n - p0 ? p0 + (u1 - u) : n);
+    const int t0 = 2 * p0 + wave, t1 = min(2 * p1, (len + kStep - 1) / kStep);        // steps
     Queries<D, FMT, HALF> q[NQ];
     float m[NQ], l[NQ];
     f32x4 o[NQ][NO];
+    Keys<D, FMT> keys;
+    Values<D, FMT> vals;
+    const int seen_by_all = len - a.rows + 1;      // places that every row sees
+    const auto head_at = [&](int page) { return a.pool.pages + ((int64_t)max(page, 0) * a.pool.heads + head) * L::kHead; };
+    int page = t0 < t1 ? page_at(a.pool, a.seqs, b, t0 >> 1) : 0;
+    if (t0 < t1) {
+      load_keys(keys, head_at(page), t0 & 1, lane);
+      load_values(vals, head_at(page) + L::kSide, t0 & 1, lane);
+    }
 #pragma unroll
     for (int i = 0; i < NQ; ++i) load_queries(q[i], a, b, head, (chunk * NQ + i) * 16, lane);
-    const int seen_by_all = len - a.rows + 1;      // places that every row sees
     bool careful = false;      // values that only some rows see are not finite: in a second pass
   again:
 #pragma unroll
@@ -378,130 +397,119 @@ __global__ __launch_bounds__(kThreads) void k_kv4_attend(AttendArgs a) {
 #pragma unroll
       for (int j = 0; j < NO; ++j) o[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    for (int p = p0 + wave; p < p1; p += kWaves) {
-      const int page = page_at(a.pool, a.seqs, b, p);
-      const uint8_t* at = a.pool.pages + ((int64_t)max(page, 0) * a.pool.heads + head) * L::kHead;
-      PageKeys<D, FMT> keys;
-      PageValues<D, FMT> vals;
-      load_keys(keys, at, lane);
-      load_values(vals, at + L::kSide, lane);
-      f32x4 s[NQ][4];
+    for (int t = t0; t < t1; t += kWaves) {
+      f32x4 s[NQ][2];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
+      for (int x = 0; x < 2; ++x) {
         u32x4 kw[W];
-        widen_keys(keys, t, kw);
+        widen_keys(keys, x, kw);
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
-          f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+          s[i][x] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int w = 0; w < W; ++w)
 #pragma unroll
-            for (int x = 0; x < Queries<D, FMT, HALF>::P; ++x) acc = product<F16>(kw[w], q[i].x[w][x], acc);
-          s[i][t] = acc;
+            for (int y = 0; y < QP; ++y)
+              s[i][x] = product<F16>(kw[w], q[i].x[w][y], s[i][x]);
         }
       }
+      const int tn = t + kWaves < t1 ? t + kWaves : t;
+      const int next = page_at(a.pool, a.seqs, b, tn >> 1);
+      load_keys(keys, head_at(next), tn & 1, lane);
       if (page < 0) {
 #pragma unroll
-        for (int i = 0; i < NQ; ++i)
-#pragma unroll
-          for (int t = 0; t < 4; ++t) s[i][t] = f32x4{NAN, NAN, NAN, NAN};
+        for (int i = 0; i < NQ; ++i) s[i][0] = s[i][1] = f32x4{NAN, NAN, NAN, NAN};
       }
-      if ((p + 1) * kPage > seen_by_all) {
-        const int base = p * kPage + 4 * g;
+      if ((t + 1) * kStep > seen_by_all) {
+        const int base = t * kStep + 4 * g;
 #pragma unroll
         for (int i = 0; i < NQ; ++i)
 #pragma unroll
-          for (int t = 0; t < 4; ++t)
+          for (int x = 0; x < 2; ++x)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (base + t * 16 + e >= seen_by_all + q[i].row) s[i][t][e] = -INFINITY;
+              if (base + x * 16 + e >= seen_by_all + q[i].row) s[i][x][e] = -INFINITY;
         // scales behind the last token may be anything: zeros
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const int left = min(max(len - (base + t * 16), 0), 4);
+        for (int x = 0; x < 2; ++x) {
+          const int left = min(max(len - (base + x * 16), 0), 4);
           const uint32_t keep = left >= 4 ? 0xFFFFFFFFu : (1u << (8 * left)) - 1;
 #pragma unroll
           for (int c = 0; c < L::C; ++c) {
-            vals.s[c][t] &= keep;
-            if (careful) vals.s[c][t] = without_nan<FMT>(vals.s[c][t]);
+            vals.s[c][x] &= keep;
+            if (careful) vals.s[c][x] = without_nan<FMT>(vals.s[c][x]);
           }
         }
       }
-      u32x4 pw[NQ][2][PP];
+      u32x4 pw[NQ][PP];
 #pragma unroll
       for (int i = 0; i < NQ; ++i) {
-        float top = -INFINITY;
+        float top = s[i][0][0];
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) top = fmaxf(top, s[i][t][e]);
-        const float mn = fmaxf(m[i], max_over_g(top) * q[i].factor);
-        const float mu = (mn == -INFINITY ? 0.0f : mn) - (F16 ? 14.0f : 0.0f);
-        if (__any(mn != m[i])) {
-          // P of the pages before counts from the old maximum
+        for (int e = 1; e < 8; ++e) top = fmaxf(top, s[i][e / 4][e % 4]);
+        top = max_over_g(top) * q[i].factor;
+        if (__any(top > m[i] + kSlack)) {
+          const float mn = top > m[i] + kSlack ? top : m[i];       // of this column, whatever the others do
           const float f = __builtin_amdgcn_exp2f(m[i] - (mn == -INFINITY ? 0.0f : mn));
           l[i] *= f;
 #pragma unroll
           for (int j = 0; j < NO; ++j) o[i][j] *= f;
           m[i] = mn;
         }
+        const float mu = (m[i] == -INFINITY ? 0.0f : m[i]) - kShift;
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            s[i][t][e] = __builtin_amdgcn_exp2f(fmaf(s[i][t][e], q[i].factor, -mu));
-            l[i] += s[i][t][e];
-          }
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int x = 0; x < 2; ++x)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const f32x4& x = s[i][2 * h + e / 2];
-            pw[i][h][0][e] = pack16(x[e % 2 * 2], x[e % 2 * 2 + 1], F16);
-            if constexpr (PP == 2) pw[i][h][1][e] = rest16(x[e % 2 * 2], x[e % 2 * 2 + 1], pw[i][h][0][e]);
+            s[i][x][e] = __builtin_amdgcn_exp2f(fmaf(s[i][x][e], q[i].factor, -mu));
+            l[i] += s[i][x][e];
           }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const f32x4& x = s[i][e / 2];
+          pw[i][0][e] = pack16(x[e % 2 * 2], x[e % 2 * 2 + 1], F16);
+          if constexpr (PP == 2) pw[i][1][e] = rest16(x[e % 2 * 2], x[e % 2 * 2 + 1], pw[i][0][e]);
+        }
       }
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int c = 0; c < L::C; ++c) {
+        uint32_t vw[4][VD];        // pairs of tokens
 #pragma unroll
-        for (int c = 0; c < L::C; ++c) {
-          uint32_t vw[4][VD];        // pairs of tokens
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t* qd = vals.q[2 * h + k / 2] + c * (VD / 2);
-            const uint32_t sd = vals.s[c][2 * h + k / 2];
-            if constexpr (VD == 8) {
-              pair_tokens<FMT, VD>(qd[k % 2 * 2], qd[k % 2 * 2 + 1], sd, k % 2, vw[k]);
-            } else {
-              pair_tokens<FMT, VD>(qd[k % 2] & 0xFFFF, qd[k % 2] >> 16, sd, k % 2, vw[k]);
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < VD; ++j) {
-            const u32x4 x = {vw[0][j], vw[1][j], vw[2][j], vw[3][j]};
-#pragma unroll
-            for (int i = 0; i < NQ; ++i)
-#pragma unroll
-              for (int y = 0; y < PP; ++y) o[i][c * VD + j] = product<F16>(x, pw[i][h][y], o[i][c * VD + j]);
-          }
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t* qd = vals.q[k / 2] + c * (VD / 2);
+          const uint32_t sd = vals.s[c][k / 2];
+          if constexpr (VD == 8) pair_tokens<FMT, VD>(qd[k % 2 * 2], qd[k % 2 * 2 + 1], sd, k % 2, vw[k]);
+          else pair_tokens<FMT, VD>(qd[k % 2] & 0xFFFF, qd[k % 2] >> 16, sd, k % 2, vw[k]);
         }
-      if (careful && (p + 1) * kPage > seen_by_all) {
-        for (int t = 0; t < kPage && p * kPage + t < len; ++t)
+#pragma unroll
+        for (int j = 0; j < VD; ++j) {
+          const u32x4 x = {vw[0][j], vw[1][j], vw[2][j], vw[3][j]};
+#pragma unroll
+          for (int i = 0; i < NQ; ++i)
+#pragma unroll
+            for (int y = 0; y < PP; ++y) o[i][c * VD + j] = product<F16>(x, pw[i][y], o[i][c * VD + j]);
+        }
+      }
+      if (careful && (t + 1) * kStep > seen_by_all) {
+        const uint8_t* at = head_at(page) + L::kSide;
+        for (int j = t * kStep; j < min((t + 1) * kStep, len); ++j)
 #pragma unroll
           for (int k = 0; k < 4 * L::C; ++k) {
             const int c = k / 4, e = k % 4, sg = c * (128 / L::G) + (4 * g + e) * VD / L::G;
-            if (!nan_scale<FMT>(at[L::kSide + L::value_scale(t, sg)])) continue;
+            if (!nan_scale<FMT>(at[L::value_scale(j % kPage, sg)])) continue;
 #pragma unroll
             for (int i = 0; i < NQ; ++i)
-              if (p * kPage + t < seen_by_all + q[i].row) {
+              if (j < seen_by_all + q[i].row) {
 #pragma unroll
-                for (int j = 0; j < VD; ++j) o[i][c * VD + j][e] = NAN;
+                for (int x = 0; x < VD; ++x) o[i][c * VD + x][e] = NAN;
               }
           }
       }
+      page = next;
+      load_values(vals, head_at(next) + L::kSide, tn & 1, lane);
     }
     // 0 times a value that a row does not see is NaN where that is not finite
-    if (!careful && p1 * kPage > seen_by_all && a.rows > 1) {
+    if (!careful && a.rows > 1 && t0 < t1 && t1 * kStep > seen_by_all) {
       float z = 0.0f;
 #pragma unroll
       for (int i = 0; i < NQ; ++i)
@@ -511,6 +519,9 @@ __global__ __launch_bounds__(kThreads) void k_kv4_attend(AttendArgs a) {
           for (int e = 0; e < 4; ++e) z = fmaf(0.0f, o[i][j][e], z);
       if (__any(z != z)) {
         careful = true;
+        page = page_at(a.pool, a.seqs, b, t0 >> 1);
+        load_keys(keys, head_at(page), t0 & 1, lane);
+        load_values(vals, head_at(page) + L::kSide, t0 & 1, lane);
         goto again;
       }
     }
@@ -660,76 +671,88 @@ __global__ __launch_bounds__(kThreads) void k_kv4_join(AttendArgs a) {
 
 // Adds the attention weights of all rows and query heads to the tokens' sums, from
 // the keys again and the sums of exponentials that are known now: reading 4-bit
-// keys twice costs less than writing and reading the scores.  A wavefront has a
-// page to itself, so the order of every sum is fixed.
-template <int D, int FMT, bool HALF>
-__global__ __launch_bounds__(kThreads) void k_kv4_weights(AttendArgs a) {
+// keys twice costs less than writing and reading the scores.  A step belongs to one
+// wavefront, so the order of every sum is fixed.
+template <int D, int FMT, bool HALF, int NQ>
+__global__ __launch_bounds__(kThreads, 2) void k_kv4_weights(AttendArgs a) {
   typedef Layout<D, FMT> L;
   constexpr bool F16 = FMT == kNv;
-  constexpr int W = PageKeys<D, FMT>::W;
+  constexpr int W = Keys<D, FMT>::W, QP = Queries<D, FMT, HALF>::P;
   const int lane = threadIdx.x & 63, g = lane >> 4, part = blockIdx.x * kWaves + wave_index();
   int64_t pages;
   pages_before(a.seqs, 0, pages, lane);
-  const int64_t units = pages * a.pool.heads;
+  const int64_t units = pages * a.pool.heads * 2;          // steps
   const int64_t u0 = cut(units, part, a.nblocks * kWaves), u1 = cut(units, part + 1, a.nblocks * kWaves);
   for (int64_t u = u0; u < u1;) {
     int64_t before;
-    const int b = sequence_at(a.seqs, u, a.pool.heads, before, lane);
-    const int n = pages_of(a.seqs, b), len = length_of(a.seqs, b), head = (int)((u - before) / n);
-    const int p0 = (int)((u - before) % n), p1 = (int)(u1 - u < n - p0 ? p0 + (u1 - u) : n);
+    const int b = sequence_at(a.seqs, u, a.pool.heads * 2, before, lane);
+    const int n = 2 * pages_of(a.seqs, b), len = length_of(a.seqs, b), head = (int)((u - before) / n);
+    const int t0 = (int)((u - before) % n), t1 = (int)(u1 - u < n - t0 ? t0 + (u1 - u) : n);
     const float* lse = a.lse + ((int64_t)b * a.pool.heads + head) * a.cols;
     const int seen_by_all = len - a.rows + 1;
-    for (int p = p0; p < p1; ++p) {
-      const int page = page_at(a.pool, a.seqs, b, p);
-      if (page < 0) continue;
+    Queries<D, FMT, HALF> q[NQ];
+    float from[NQ];
+    const auto columns = [&](int chunk) {
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        const int first = (chunk * NQ + i) * 16, col = first + (lane & 15);
+        load_queries(q[i], a, b, head, first, lane);
+        const float ls = col < a.cols ? lse[col] : -INFINITY;
+        if (ls == -INFINITY) q[i].row = -(1 << 30);       // no such column, or one that sees nothing
+        from[i] = ls == -INFINITY ? 0.0f : ls;
+      }
+    };
+    if (a.chunks == 1) columns(0);
+    for (int t = t0; t < t1; ++t) {
+      const int page = page_at(a.pool, a.seqs, b, t >> 1);
+      if (page < 0 || t * kStep >= len) continue;
       const int64_t unit = (int64_t)page * a.pool.heads + head;
-      PageKeys<D, FMT> keys;
-      load_keys(keys, a.pool.pages + unit * L::kHead, lane);
-      f32x4 sum[4];
+      Keys<D, FMT> keys;
+      load_keys(keys, a.pool.pages + unit * L::kHead, t & 1, lane);
+      // the lane's place of the step, and what it has so far
+      const int at = (lane >> 2 & 1) * 16 + 4 * g + (lane & 3);
+      float* w = a.pool.weights + unit * kPage + (t & 1) * kStep + at;
+      const float old = *w;
+      float sum[2][4] = {};
+      for (int chunk = 0; chunk < a.chunks; ++chunk) {
+        if (a.chunks > 1) columns(chunk);
 #pragma unroll
-      for (int t = 0; t < 4; ++t) sum[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      for (int first = 0; first < a.cols; first += 16) {
-        Queries<D, FMT, HALF> q;
-        load_queries(q, a, b, head, first, lane);
-        const int col = first + (lane & 15);
-        const float ls = col < a.cols ? lse[col] : 0.0f, from = ls == -INFINITY ? 0.0f : ls;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
+        for (int x = 0; x < 2; ++x) {
           u32x4 kw[W];
-          widen_keys(keys, t, kw);
-          f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+          widen_keys(keys, x, kw);
 #pragma unroll
-          for (int w = 0; w < W; ++w)
+          for (int i = 0; i < NQ; ++i) {
+            f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int x = 0; x < Queries<D, FMT, HALF>::P; ++x) acc = product<F16>(kw[w], q.x[w][x], acc);
+            for (int k = 0; k < W; ++k)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int place = p * kPage + t * 16 + 4 * g + e;
-            if (col < a.cols && place < seen_by_all + q.row) sum[t][e] += __builtin_amdgcn_exp2f(fmaf(acc[e], q.factor, -from));
+              for (int y = 0; y < QP; ++y) s = product<F16>(kw[k], q[i].x[k][y], s);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float p = __builtin_amdgcn_exp2f(fmaf(s[e], q[i].factor, -from[i]));
+              sum[x][e] += t * kStep + x * 16 + 4 * g + e < seen_by_all + q[i].row ? p : 0.0f;
+            }
           }
         }
       }
+      // over the sixteen columns, halving the eight values while there are pairs: lane n ends with value n % 8
+      const int n3 = lane & 7;
+      float h4[4], h2[2], h1;
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-#pragma unroll
-          for (int o = 8; o; o >>= 1) sum[t][e] += __shfl_xor(sum[t][e], o);
-        }
-      if ((lane & 15) == 0) {
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          f32x4* w = reinterpret_cast<f32x4*>(a.pool.weights + unit * kPage + t * 16 + 4 * g);
-          f32x4 v = *w;
-          const int place = p * kPage + t * 16 + 4 * g;
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (place + e < len) v[e] += sum[t][e];
-          *w = v;
-        }
+      for (int e = 0; e < 4; ++e) {
+        const float keep = n3 & 4 ? sum[1][e] : sum[0][e], give = n3 & 4 ? sum[0][e] : sum[1][e];
+        h4[e] = keep + __shfl_xor(give, 4);
       }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float keep = n3 & 2 ? h4[2 + e] : h4[e], give = n3 & 2 ? h4[e] : h4[2 + e];
+        h2[e] = keep + __shfl_xor(give, 2);
+      }
+      h1 = (n3 & 1 ? h2[1] : h2[0]) + __shfl_xor(n3 & 1 ? h2[0] : h2[1], 1);
+      h1 += __shfl_xor(h1, 8);
+      if ((lane & 8) == 0 && t * kStep + at < len) *w = old + h1;
     }
-    u += p1 - p0;
+    u += t1 - t0;
   }
 }
 
@@ -745,7 +768,7 @@ hipError_t launch(AttendArgs a, hipStream_t st) {
   hipLaunchKernelGGL((k_kv4_attend<D, FMT, HALF, NQ>), dim3(a.nblocks), dim3(kThreads), 0, st, a);
   const unsigned joins = (unsigned)a.seqs.n * a.pool.heads * a.cols;
   hipLaunchKernelGGL((k_kv4_join<D, FMT, HALF, NQ>), dim3(joins), dim3(kThreads), 0, st, a);
-  if (a.lse) hipLaunchKernelGGL((k_kv4_weights<D, FMT, HALF>), dim3(a.nblocks), dim3(kThreads), 0, st, a);
+  if (a.lse) hipLaunchKernelGGL((k_kv4_weights<D, FMT, HALF, NQ>), dim3(a.nblocks), dim3(kThreads), 0, st, a);
   return hipGetLastError();
 }
 

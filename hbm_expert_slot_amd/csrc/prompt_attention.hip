@@ -48,13 +48,16 @@ struct PromptArgs {
   float* part_ml;           // [rows][heads][parts][2]
 };
 
+// The operands live until the result is there, so that it takes no register of theirs.
 template <bool HALF>
 __device__ __forceinline__ f32x16 product(u32x4 a, u32x4 b, f32x16 c) {
+  f32x16 d;
   if constexpr (HALF)
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    d = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
   else
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
-                                                   0);
+    d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  asm("" : "+v"(d) : "v"(a), "v"(b));
+  return d;
 }
 template <bool HALF>
 __device__ __forceinline__ uint32_t pack(float a, float b) {
