@@ -12,6 +12,8 @@ namespace {
 
 constexpr int kThreads = 256;
 
+constexpr int kMaxTokens = 64;   // of a block
+
 struct RowArgs {
   Pool pool;
   Seqs seqs;
@@ -21,14 +23,17 @@ struct RowArgs {
   void* rows[2];             // keys, values
   int64_t token[2], head[2]; // strides
   int32_t tokens;
+  int32_t block_tokens;
+  uint32_t per_magic;        // x / (2 heads) is the upper half of x times this
 };
 
-// Sequence and place of a token of the packed rows; place -1: it belongs to none.
+// Sequence and place of a token of the packed rows; place -1: it is not there, -2:
+// it belongs to no sequence.
 __device__ __forceinline__ int place_of(const RowArgs& a, int t, int& b) {
   int end;
   if (a.starts) {
     int lo = 0, hi = a.seqs.n;           // starts[lo] <= t < starts[hi]
-    if (t < a.starts[0] || t >= a.starts[hi]) return -1;
+    if (t < a.starts[0] || t >= a.starts[hi]) return -2;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (a.starts[mid] <= t) lo = mid;
@@ -45,124 +50,152 @@ __device__ __forceinline__ int place_of(const RowArgs& a, int t, int& b) {
   return p >= 0 && p < (int64_t)a.seqs.width * kPage ? (int)p : -1;
 }
 
-// A thread takes 16 elements of one row; the groups of a row, then heads, then
-// sides, then tokens follow each other.
-struct Piece {
-  int s16, head, side, token;
+// Where the tokens of a block lie: found once for all of their rows.
+struct Places {
+  int page[kMaxTokens], place[kMaxTokens];
 };
-template <int D>
-__device__ __forceinline__ Piece piece_of(const RowArgs& a, uint64_t i) {
-  constexpr int N = D / 16;
-  Piece p;
-  p.s16 = (int)(i % N);
-  const uint64_t row = i / N;
-  p.head = (int)(row % (uint32_t)a.pool.heads);
-  const uint64_t r2 = row / (uint32_t)a.pool.heads;
-  p.side = (int)(r2 & 1);
-  p.token = (int)(r2 >> 1);
-  return p;
+__device__ __forceinline__ int find_places(const RowArgs& a, Places& p, int t0) {
+  const int n = min(a.block_tokens, a.tokens - t0);
+  if ((int)threadIdx.x < n) {
+    int b;
+    const int place = place_of(a, t0 + threadIdx.x, b);
+    p.place[threadIdx.x] = place;
+    p.page[threadIdx.x] = place < 0 ? -1 : page_at(a.pool, a.seqs, b, place / kPage);
+  }
+  __syncthreads();
+  return n;
 }
 
+// Row r of a block's tokens: keys of all heads, then values, token after token.
+struct Row {
+  int token, side, head;
+};
+__device__ __forceinline__ Row row_of(const RowArgs& a, int r) {
+  Row w;
+  w.token = (int)__umulhi((uint32_t)r, a.per_magic);
+  const int in = r - w.token * 2 * a.pool.heads;
+  w.side = in >= a.pool.heads;
+  w.head = in - (w.side ? a.pool.heads : 0);
+  return w;
+}
+
+// A thread takes 16 elements of a row at a time; the next ones are on their way
+// while it works on these.
 template <typename T, int D, int FMT>
 __global__ __launch_bounds__(kThreads) void k_kv4_append(RowArgs a) {
   typedef Layout<D, FMT> L;
-  const uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
-  const uint64_t n = (uint64_t)a.tokens * 2 * a.pool.heads * (D / 16);
-  if (i >= n) return;
-  const Piece p = piece_of<D>(a, i);
-  int b;
-  const int place = place_of(a, p.token, b);
-  const int page = place < 0 ? -1 : page_at(a.pool, a.seqs, b, place / kPage);
-  const T* src = static_cast<const T*>(a.rows[p.side]) + p.token * a.token[p.side] + p.head * a.head[p.side] + p.s16 * 16;
-  T raw[16];
-  __builtin_memcpy(raw, src, sizeof raw);
-  float v[16];
+  constexpr int N = D / 16, R = kThreads / N;      // threads of a row, rows at a time
+  struct Raw {
+    T v[16];
+  };
+  __shared__ Places places;
+  const int t0 = blockIdx.x * a.block_tokens, s16 = threadIdx.x % N;
+  const int rows = find_places(a, places, t0) * 2 * a.pool.heads;
+  const auto load = [&](int r) {
+    const Row w = row_of(a, min(r, rows - 1));
+    Raw x;
+    __builtin_memcpy(&x, static_cast<const T*>(a.rows[w.side]) + (t0 + w.token) * a.token[w.side] + w.head * a.head[w.side] +
+                             s16 * 16, sizeof x);
+    return x;
+  };
+  int r = threadIdx.x / N;
+  Raw raw = load(r);
+  for (; r < rows; r += R) {
+    const Raw next = load(r + R);
+    float v[16];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) v[e] = (float)raw[e];
-  uint32_t sbyte;
-  u32x2 codes;
-  round16<FMT>(v, FMT == kNv && a.gs[p.side] ? *a.gs[p.side] : 1.0f, sbyte, codes);
-  if (page < 0) return;
-  const int t = place % kPage;
-  const int64_t unit = (int64_t)page * a.pool.heads + p.head;
-  uint8_t* at = a.pool.pages + unit * L::kHead + p.side * L::kSide;
-  const int sg = FMT == kNv ? p.s16 : p.s16 / 2;
-  if (FMT == kNv || (p.s16 & 1) == 0) at[p.side ? L::value_scale(t, sg) : L::key_scale(t, sg)] = (uint8_t)sbyte;
-  if (p.side == 0) {
-    *reinterpret_cast<u32x2*>(at + L::key_codes(t, p.s16 * 16)) = codes;
-    if (p.s16 == 0 && a.pool.weights) {
-      a.pool.weights[unit * kPage + t] = 0.0f;
-      a.pool.positions[unit * kPage + t] = a.given ? a.given[p.token] : place;
+    for (int e = 0; e < 16; ++e) v[e] = (float)raw.v[e];
+    raw = next;
+    const Row w = row_of(a, r);
+    uint32_t sbyte;
+    u32x2 codes;
+    round16<FMT>(v, FMT == kNv && a.gs[w.side] ? *a.gs[w.side] : 1.0f, sbyte, codes);
+    const int page = places.page[w.token], place = places.place[w.token];
+    if (page < 0) continue;
+    const int t = place % kPage;
+    const int64_t unit = (int64_t)page * a.pool.heads + w.head;
+    uint8_t* at = a.pool.pages + unit * L::kHead + w.side * L::kSide;
+    const int sg = FMT == kNv ? s16 : s16 / 2;
+    if (FMT == kNv || (s16 & 1) == 0) at[w.side ? L::value_scale(t, sg) : L::key_scale(t, sg)] = (uint8_t)sbyte;
+    if (w.side == 0) {
+      *reinterpret_cast<u32x2*>(at + L::key_codes(t, s16 * 16)) = codes;
+      if (s16 == 0 && a.pool.weights) {
+        a.pool.weights[unit * kPage + t] = 0.0f;
+        a.pool.positions[unit * kPage + t] = a.given ? a.given[t0 + w.token] : place;
+      }
+    } else if constexpr (D >= 128) {
+      const int c = s16 / 8, ln = s16 % 8 * 2;
+      *reinterpret_cast<uint32_t*>(at + L::value_codes(t, c, ln)) = codes.x;
+      *reinterpret_cast<uint32_t*>(at + L::value_codes(t, c, ln + 1)) = codes.y;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint16_t*>(at + L::value_codes(t, 0, s16 * 4 + j)) = (uint16_t)(codes[j / 2] >> (j % 2 * 16));
     }
-  } else if constexpr (D >= 128) {
-    const int c = p.s16 / 8, ln = p.s16 % 8 * 2;
-    *reinterpret_cast<uint32_t*>(at + L::value_codes(t, c, ln)) = codes.x;
-    *reinterpret_cast<uint32_t*>(at + L::value_codes(t, c, ln + 1)) = codes.y;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<uint16_t*>(at + L::value_codes(t, 0, p.s16 * 4 + j)) = (uint16_t)(codes[j / 2] >> (j % 2 * 16));
   }
 }
 
+// A thread writes 16 bytes of a row at a time, so that a wavefront's stores are one piece.
 template <typename T, int D, int FMT>
 __global__ __launch_bounds__(kThreads) void k_kv4_read(RowArgs a) {
   typedef Layout<D, FMT> L;
-  const uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
-  const uint64_t n = (uint64_t)a.tokens * 2 * a.pool.heads * (D / 16);
-  if (i >= n) return;
-  const Piece p = piece_of<D>(a, i);
-  int b;
-  if (a.starts && (p.token < a.starts[0] || p.token >= a.starts[a.seqs.n])) return;
-  const int place = place_of(a, p.token, b);
-  const int page = place < 0 ? -1 : page_at(a.pool, a.seqs, b, place / kPage);
-  T out[16];
-  if (page < 0) {
+  constexpr int E = 16 / sizeof(T), N = D / E, R = kThreads / N;
+  __shared__ Places places;
+  const int t0 = blockIdx.x * a.block_tokens, p = threadIdx.x % N, dim = p * E;
+  const int rows = find_places(a, places, t0) * 2 * a.pool.heads;
+#pragma unroll 2
+  for (int r = threadIdx.x / N; r < rows; r += R) {
+    const Row w = row_of(a, r);
+    const int page = places.page[w.token], place = places.place[w.token];
+    if (place == -2) continue;
+    typedef __attribute__((ext_vector_type(E))) T V;
+    V out;
+    if (page < 0) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) out[e] = (T)__builtin_nanf("");
-  } else {
-    const int t = place % kPage;
-    const uint8_t* at = a.pool.pages + ((int64_t)page * a.pool.heads + p.head) * L::kHead + p.side * L::kSide;
-    const int sg = FMT == kNv ? p.s16 : p.s16 / 2;
-    const uint32_t sb = at[p.side ? L::value_scale(t, sg) : L::key_scale(t, sg)];
-    u32x2 codes;
-    if (p.side == 0) {
-      codes = *reinterpret_cast<const u32x2*>(at + L::key_codes(t, p.s16 * 16));
-    } else if constexpr (D >= 128) {
-      const int c = p.s16 / 8, ln = p.s16 % 8 * 2;
-      codes.x = *reinterpret_cast<const uint32_t*>(at + L::value_codes(t, c, ln));
-      codes.y = *reinterpret_cast<const uint32_t*>(at + L::value_codes(t, c, ln + 1));
+      for (int e = 0; e < E; ++e) out[e] = (T)__builtin_nanf("");
     } else {
-      uint32_t h[4];
+      const int t = place % kPage, sg = dim / L::G;
+      const uint8_t* at = a.pool.pages + ((int64_t)page * a.pool.heads + w.head) * L::kHead + w.side * L::kSide;
+      const uint32_t sb = at[w.side ? L::value_scale(t, sg) : L::key_scale(t, sg)];
+      const auto two = [&](uint32_t off) { return (uint32_t)*reinterpret_cast<const uint16_t*>(at + off); };
+      uint32_t codes;
+      if constexpr (E == 4) {
+        codes = two(w.side == 0 ? L::key_codes(t, dim) : L::value_codes(t, dim / 128, dim % 128 / L::VDims) + dim % L::VDims / 2);
+      } else if constexpr (D >= 128) {
+        codes = *reinterpret_cast<const uint32_t*>(at + (w.side == 0 ? L::key_codes(t, dim) : L::value_codes(t, dim / 128, dim % 128 / 8)));
+      } else {
+        codes = w.side == 0 ? *reinterpret_cast<const uint32_t*>(at + L::key_codes(t, dim))
+                            : two(L::value_codes(t, 0, 2 * p)) | two(L::value_codes(t, 0, 2 * p + 1)) << 16;
+      }
+      const float s = FMT == kNv ? __builtin_amdgcn_cvt_pk_f32_fp8((int)sb, false)[0] : e8m0(sb);
+      const float gs = FMT == kNv && a.gs[w.side] ? *a.gs[w.side] : 1.0f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) h[j] = *reinterpret_cast<const uint16_t*>(at + L::value_codes(t, 0, p.s16 * 4 + j));
-      codes = u32x2{h[0] | h[1] << 16, h[2] | h[3] << 16};
+      for (int e = 0; e < E; e += 2) {
+        const f32x2 x = e == 0   ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 0)
+                        : e == 2 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 1)
+                        : e == 4 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 2)
+                                 : __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 3);
+        // code times group scale is exact; one rounding by the scale of all
+        out[e] = (T)(x.x * s * gs);
+        out[e + 1] = (T)(x.y * s * gs);
+      }
     }
-    const float s = FMT == kNv ? __builtin_amdgcn_cvt_pk_f32_fp8((int)sb, false)[0] : e8m0(sb);
-    const float gs = FMT == kNv && a.gs[p.side] ? *a.gs[p.side] : 1.0f;
-#pragma unroll
-    for (int e = 0; e < 16; e += 2) {
-      const uint32_t d = codes[e / 8];
-      const f32x2 w = e % 8 == 0   ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d, 1.0f, 0)
-                      : e % 8 == 2 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d, 1.0f, 1)
-                      : e % 8 == 4 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d, 1.0f, 2)
-                                   : __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d, 1.0f, 3);
-      // code times group scale is exact; one rounding by the scale of all
-      out[e] = (T)(w.x * s * gs);
-      out[e + 1] = (T)(w.y * s * gs);
-    }
+    T* dst = static_cast<T*>(a.rows[w.side]) + (t0 + w.token) * a.token[w.side] + w.head * a.head[w.side] + dim;
+    __builtin_memcpy(dst, &out, sizeof out);
   }
-  T* dst = static_cast<T*>(a.rows[p.side]) + p.token * a.token[p.side] + p.head * a.head[p.side] + p.s16 * 16;
-  __builtin_memcpy(dst, out, sizeof out);
 }
 
 int type_size(int t) { return t == SC_DTYPE_F32 ? 4 : 2; }
 
-// Tokens at a time: a launch of 2^32 threads or more would run only in part.
 template <bool WRITE, typename T>
 hipError_t run(RowArgs a, int dim, int fmt, hipStream_t st) {
-  const uint64_t n = (uint64_t)a.tokens * 2 * a.pool.heads * (dim / 16);
-  const unsigned grid = (unsigned)((n + kThreads - 1) / kThreads);
+  // a block has work for four rounds of its threads, unless that leaves compute units idle
+  const int per = 2 * a.pool.heads, threads = WRITE ? dim / 16 : dim * (int)sizeof(T) / 16;
+  const int full = (4 * kThreads / threads + per - 1) / per, even = (a.tokens + 511) / 512;
+  const int n = full < even ? full : even;
+  a.block_tokens = n < kMaxTokens ? n : kMaxTokens;
+  a.per_magic = (uint32_t)((1ull << 32) / per + 1);      // exact: rows of a block times heads are below 2^32
+  const unsigned grid = (unsigned)((a.tokens + a.block_tokens - 1) / a.block_tokens);
   return by_layout(dim, fmt, [&](auto d, auto f) {
     if constexpr (WRITE) hipLaunchKernelGGL((k_kv4_append<T, d(), f()>), dim3(grid), dim3(kThreads), 0, st, a);
     else hipLaunchKernelGGL((k_kv4_read<T, d(), f()>), dim3(grid), dim3(kThreads), 0, st, a);
@@ -184,8 +217,7 @@ sc_status rows(const sc_kv4_cache* cache, const sc_kv4_seqs* seqs, const sc_kv4_
   if (tokens == 0 || seqs->n_seqs == 0) return SC_OK;
   if (!starts && tokens % seqs->n_seqs)
     return fail(SC_E_ARG, "%d tokens cannot be dealt out evenly to %d sequences", tokens, seqs->n_seqs);
-  if ((uint64_t)tokens * 2 * cache->kv_heads * (cache->head_dim / 16) > 0xFFFFFF00ull)
-    return fail(SC_E_ARG, "too many tokens for one call");
+  if (tokens >= 1 << 24) return fail(SC_E_ARG, "too many tokens for one call");     // a launch has less than 2^32 threads
   const int size = type_size(r->type);
   if (!r->d_k || !r->d_v || (uintptr_t)r->d_k % size || (uintptr_t)r->d_v % size)
     return fail(SC_E_ARG, "k or v is NULL or not aligned to its elements");

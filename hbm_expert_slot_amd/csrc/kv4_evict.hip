@@ -7,6 +7,8 @@
 // move, into the places that became free: sources and targets never overlap.
 #include "kv4_device.h"
 
+#include <type_traits>
+
 namespace sc {
 namespace kv4 {
 namespace {
@@ -31,27 +33,26 @@ __device__ __forceinline__ uint32_t order_of(float w) {
   return b >> 31 ? ~b : b | 0x80000000u;
 }
 
-// One block per sequence and head: the keep-th largest key by four rounds of
-// counting bytes, then the places that become free and the tokens that move there.
+// One block per sequence and head: the keep-th largest key by three rounds of
+// counting 11, 11 and 10 bits, then the places that become free and the tokens that
+// move there.  A wavefront has consecutive places, 64 at a time, so that places are
+// ranked by ballots within it and one sum over the wavefronts.  Up to kHeld rounds
+// of places the keys stay in registers; more are formed again in every pass.
+constexpr int kHeld = 32, kBins = 2048;
+
 __global__ __launch_bounds__(kSelectThreads) void k_kv4_select(EvictArgs a) {
-  __shared__ uint32_t hist[256];
-  __shared__ int s_top, s_bad;
-  __shared__ uint32_t s_key, s_need;
-  __shared__ int s_wave[kSelectWaves], s_equal, s_free, s_move;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  __shared__ uint32_t hist[2][kBins];      // of even and odd wavefronts
+  __shared__ int s_bad, s_top[kSelectWaves];
+  __shared__ uint32_t s_key, s_need, s_sum[kSelectWaves];
+  __shared__ int s_count[3][kSelectWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_index();
   const int b = blockIdx.x / a.pool.heads, head = blockIdx.x % a.pool.heads;
-  const int n = length_of(a.seqs, b);
-  const auto unit_of = [&](int place) -> int64_t {
-    return ((int64_t)page_at(a.pool, a.seqs, b, place / kPage) * a.pool.heads + head) * kPage + place % kPage;
-  };
-  if (tid == 0) {
-    s_top = INT32_MIN;
-    s_bad = 0;
-  }
+  const int n = length_of(a.seqs, b), np = (n + kPage - 1) / kPage;
+  if (tid == 0) s_bad = 0;
   __syncthreads();
   if (n > a.keep) {
     // a page that is none: the sequence stays as it is
-    for (int i = tid; i < (n + kPage - 1) / kPage; i += kSelectThreads)
+    for (int i = tid; i < np; i += kSelectThreads)
       if (page_at(a.pool, a.seqs, b, i) < 0) s_bad = 1;
   }
   __syncthreads();
@@ -61,97 +62,190 @@ __global__ __launch_bounds__(kSelectThreads) void k_kv4_select(EvictArgs a) {
     if (tid == 0) a.count[blockIdx.x] = 0;
     return;
   }
+  const int rounds = (np + kSelectWaves - 1) / kSelectWaves, first = wave * rounds;      // pages of a wavefront
+  const int mine = min(rounds, np - first);
+  const bool held = rounds <= kHeld;
+  const auto at_of = [&](int i) -> int64_t {
+    return ((int64_t)a.seqs.table[b * a.seqs.ld + first + i] * a.pool.heads + head) * kPage + lane;
+  };
+  const auto in = [&](int i) { return (first + i) * kPage + lane < n; };
+  uint32_t key[kHeld];
+  int pos[kHeld];
   int top = INT32_MIN;
-  for (int i = tid; i < n; i += kSelectThreads) top = max(top, a.pool.positions[unit_of(i)]);
-  atomicMax(&s_top, top);
+  if (held) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (i < mine && in(i)) {
+        pos[i] = a.pool.positions[at_of(i)];
+        key[i] = __float_as_uint(a.pool.weights[at_of(i)]);
+      }
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (i < mine && in(i)) top = max(top, pos[i]);
+  } else {
+    for (int i = 0; i < mine; ++i)
+      if (in(i)) top = max(top, a.pool.positions[at_of(i)]);
+  }
+#pragma unroll
+  for (int o = 32; o; o >>= 1) top = max(top, __shfl_xor(top, o));
+  if (lane == 0) s_top[wave] = top;
   __syncthreads();
-  const int64_t last = (int64_t)s_top - a.recent;
-  const auto key_of = [&](int place) -> uint32_t {
-    const int64_t u = unit_of(place);
-    const int p = a.pool.positions[u];
-    return p < a.sinks || p > last ? 0xFFFFFFFFu : order_of(a.pool.weights[u]);
+#pragma unroll
+  for (int w = 0; w < kSelectWaves; ++w) top = max(top, s_top[w]);
+  const int64_t last = (int64_t)top - a.recent;
+  const auto key_from = [&](int p, float w) { return p < a.sinks || p > last ? 0xFFFFFFFFu : order_of(w); };
+  if (held) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (i < mine && in(i)) key[i] = key_from(pos[i], __uint_as_float(key[i]));
+  }
+  // f(i, key) for the wavefront's rounds of places; a place behind the last has no key
+  const auto each = [&](auto&& f) {
+    if (held) {
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i)
+        if (i < mine) f(i, in(i), key[i]);
+    } else {
+      for (int i = 0; i < mine; ++i) {
+        const bool is = in(i);
+        f(i, is, is ? key_from(a.pool.positions[at_of(i)], a.pool.weights[at_of(i)]) : 0u);
+      }
+    }
   };
   uint32_t prefix = 0, need = (uint32_t)a.keep;       // of the tokens whose key begins with prefix
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) hist[tid] = 0;
+  constexpr int kShift[3] = {21, 10, 0};
+#pragma unroll
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = kShift[pass], bits = pass == 2 ? 10 : 11;
+    for (int i = tid; i < 2 * kBins; i += kSelectThreads) hist[0][i] = 0;
     __syncthreads();
-    for (int i = tid; i < n; i += kSelectThreads) {
-      const uint32_t k = key_of(i);
-      if (shift == 24 || k >> (shift + 8) == prefix) atomicAdd(&hist[k >> shift & 255], 1u);
+    each([&](int, bool is, uint32_t k) {
+      if (is && (pass == 0 || k >> (shift + bits) == prefix)) atomicAdd(&hist[wave & 1][k >> shift & (kBins - 1) & ((1u << bits) - 1)], 1u);
+    });
+    __syncthreads();
+    // the largest bin that the tokens from the top down to it reach `need` in: a thread has two bins, descending
+    const int d = kBins - 1 - 2 * tid;
+    const uint32_t c0 = hist[0][d] + hist[1][d], c1 = hist[0][d - 1] + hist[1][d - 1];
+    uint32_t upto = c0 + c1;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const uint32_t u = __shfl_up(upto, o);
+      if (lane >= o) upto += u;
     }
+    if (lane == 63) s_sum[wave] = upto;
     __syncthreads();
-    if (tid == 0) {
-      uint32_t above = 0;
-      int d = 255;
-      for (; d > 0 && above + hist[d] < need; --d) above += hist[d];
-      s_key = prefix << 8 | (uint32_t)d;
-      s_need = need - above;
+    for (int w = 0; w < wave; ++w) upto += s_sum[w];
+    const uint32_t above = upto - c0 - c1;
+    if (above < need && upto >= need) {
+      const bool second = above + c0 < need;
+      s_key = prefix << bits | (uint32_t)(second ? d - 1 : d);
+      s_need = need - above - (second ? c0 : 0);
     }
     __syncthreads();
     prefix = s_key;
     need = s_need;
     __syncthreads();
   }
-  // prefix is the keep-th largest key, need the number of its tokens that stay
-  if (tid == 0) s_equal = s_free = s_move = 0;
-  int32_t* from = a.from + (int64_t)blockIdx.x * a.most;
-  int32_t* to = a.to + (int64_t)blockIdx.x * a.most;
-  const auto before = [&](bool mine, int& running) -> int {     // of the places before mine, in order
-    const uint64_t m = __ballot(mine);
+  // prefix is the keep-th largest key, need the number of its tokens that stay: the first ones
+  const auto before = [&](int which, int count) {       // counts of the wavefronts before this one
+    if (lane == 0) s_count[which][wave] = count;
     __syncthreads();
-    if (lane == 0) s_wave[wave] = __popcll(m);
-    __syncthreads();
-    int sum = running + __popcll(m & ((1ull << lane) - 1)), all = 0;
-    for (int w = 0; w < kSelectWaves; ++w) {
-      if (w < wave) sum += s_wave[w];
-      all += s_wave[w];
-    }
-    running += all;
+    int sum = 0;
+    for (int w = 0; w < wave; ++w) sum += s_count[which][w];
     return sum;
   };
-  int equal = 0, nfree = 0, nmove = 0;
-  for (int i0 = 0; i0 < n; i0 += kSelectThreads) {
-    const int i = i0 + tid;
-    const uint32_t k = i < n ? key_of(i) : 0u;
-    const bool same = i < n && k == prefix;
-    const int rank = before(same, equal);
-    const bool stays = i < n && (k > prefix || (same && rank < (int)need));
-    const int f = before(i < a.keep && !stays, nfree);
-    const int v = before(i >= a.keep && stays, nmove);
-    if (i < a.keep && !stays && f < a.most) to[f] = i;
-    if (i >= a.keep && stays && v < a.most) from[v] = i;
-  }
-  if (tid == 0) a.count[blockIdx.x] = min(nmove, a.most);
+  const uint64_t below = (1ull << lane) - 1;
+  int equal = 0;
+  each([&](int, bool is, uint32_t k) { equal += __popcll(__ballot(is && k == prefix)); });
+  equal = before(0, equal);
+  const auto places = [&](auto&& f) {                   // f(i, is, stays)
+    int e = equal;
+    each([&](int i, bool is, uint32_t k) {
+      const uint64_t same = __ballot(is && k == prefix);
+      f(i, is, is && (k > prefix || (k == prefix && e + __popcll(same & below) < (int)need)));
+      e += __popcll(same);
+    });
+  };
+  int nfree = 0, nmove = 0;
+  places([&](int i, bool is, bool stays) {
+    const bool front = (first + i) * kPage + lane < a.keep;
+    nfree += __popcll(__ballot(is && front && !stays));
+    nmove += __popcll(__ballot(is && !front && stays));
+  });
+  const int all = nmove;
+  nfree = before(1, nfree);
+  nmove = before(2, nmove);
+  if (wave == kSelectWaves - 1 && lane == 0) a.count[blockIdx.x] = min(nmove + all, a.most);
+  int32_t* from = a.from + (int64_t)blockIdx.x * a.most;
+  int32_t* to = a.to + (int64_t)blockIdx.x * a.most;
+  places([&](int i, bool is, bool stays) {
+    const int place = (first + i) * kPage + lane;
+    const bool front = place < a.keep, f = is && front && !stays, m = is && !front && stays;
+    const uint64_t fs = __ballot(f), ms = __ballot(m);
+    const int fi = nfree + __popcll(fs & below), mi = nmove + __popcll(ms & below);
+    if (f && fi < a.most) to[fi] = place;
+    if (m && mi < a.most) from[mi] = place;
+    nfree += __popcll(fs);
+    nmove += __popcll(ms);
+  });
 }
 
-// A wavefront moves one token at a time: its pieces of codes, scales, weight and position.
+// Sixteen lanes move a token: its pieces of codes, scales, weight and position.  A
+// block has 64 consecutive moves, whose tokens share lines on both sides.
+constexpr int kMoves = 64;
 template <int D, int FMT>
 __global__ __launch_bounds__(256) void k_kv4_move(EvictArgs a) {
   typedef Layout<D, FMT> L;
-  const int which = blockIdx.x, lane = threadIdx.x & 63;
+  constexpr int B = D / 32, U = kMoves / 16;       // bytes of keys and of values per lane; moves of a lane
+  typedef std::conditional_t<B == 2, uint16_t, std::conditional_t<B == 4, uint32_t, u32x2>> Key;
+  typedef std::conditional_t<L::VDims == 8, uint32_t, uint16_t> Value;
+  const int which = blockIdx.x, j = threadIdx.x & 15;
   const int b = which / a.pool.heads, head = which % a.pool.heads, n = a.count[which];
-  for (int i = blockIdx.y * 4 + (threadIdx.x >> 6); i < n; i += gridDim.y * 4) {
-    const int pf = a.from[(int64_t)which * a.most + i], pt = a.to[(int64_t)which * a.most + i];
-    const int64_t uf = (int64_t)page_at(a.pool, a.seqs, b, pf / kPage) * a.pool.heads + head;
-    const int64_t ut = (int64_t)page_at(a.pool, a.seqs, b, pt / kPage) * a.pool.heads + head;
-    const int f = pf % kPage, t = pt % kPage;
-    const uint8_t* src = a.pool.pages + uf * L::kHead;
-    uint8_t* dst = a.pool.pages + ut * L::kHead;
-    constexpr int B = L::VDims / 2;
-    for (int j = lane; j < D / 8; j += 64)
-      *reinterpret_cast<uint32_t*>(dst + L::key_codes(t, 8 * j)) = *reinterpret_cast<const uint32_t*>(src + L::key_codes(f, 8 * j));
-    for (int j = lane; j < 16 * L::C; j += 64) {
-      const uint8_t* s = src + L::kSide + L::value_codes(f, j / 16, j % 16);
-      uint8_t* d = dst + L::kSide + L::value_codes(t, j / 16, j % 16);
-      if constexpr (B == 4) *reinterpret_cast<uint32_t*>(d) = *reinterpret_cast<const uint32_t*>(s);
-      else *reinterpret_cast<uint16_t*>(d) = *reinterpret_cast<const uint16_t*>(s);
+  for (int i0 = blockIdx.y * kMoves; i0 < n; i0 += gridDim.y * kMoves) {
+    int f[U], t[U];
+    int64_t uf[U], ut[U];
+    Key kc[U];
+    Value vc[U][L::C];
+    uint8_t ks[U], vs[U];
+    uint32_t mark[U];
+#pragma unroll
+    for (int x = 0; x < U; ++x) {
+      const int64_t i = (int64_t)which * a.most + min(i0 + x * 16 + (int)(threadIdx.x >> 4), n - 1);
+      f[x] = a.from[i];
+      t[x] = a.to[i];
     }
-    for (int j = lane; j < L::NS; j += 64) {
-      dst[L::key_scale(t, j)] = src[L::key_scale(f, j)];
-      dst[L::kSide + L::value_scale(t, j)] = src[L::kSide + L::value_scale(f, j)];
+#pragma unroll
+    for (int x = 0; x < U; ++x) {
+      uf[x] = (int64_t)a.seqs.table[b * a.seqs.ld + f[x] / kPage] * a.pool.heads + head;
+      ut[x] = (int64_t)a.seqs.table[b * a.seqs.ld + t[x] / kPage] * a.pool.heads + head;
+      f[x] %= kPage;
+      t[x] %= kPage;
     }
-    if (lane == 0) a.pool.weights[ut * kPage + t] = a.pool.weights[uf * kPage + f];
-    if (lane == 1) a.pool.positions[ut * kPage + t] = a.pool.positions[uf * kPage + f];
+#pragma unroll
+    for (int x = 0; x < U; ++x) {
+      const uint8_t* s = a.pool.pages + uf[x] * L::kHead;
+      kc[x] = *reinterpret_cast<const Key*>(s + f[x] * (D / 2) + j * B);
+#pragma unroll
+      for (int c = 0; c < L::C; ++c) vc[x][c] = *reinterpret_cast<const Value*>(s + L::kSide + L::value_codes(f[x], c, j));
+      if (j < L::NS) {
+        ks[x] = s[L::key_scale(f[x], j)];
+        vs[x] = s[L::kSide + L::value_scale(f[x], j)];
+      }
+      if (j < 2) mark[x] = (j ? (const uint32_t*)a.pool.positions : (const uint32_t*)a.pool.weights)[uf[x] * kPage + f[x]];
+    }
+#pragma unroll
+    for (int x = 0; x < U; ++x) {
+      if (i0 + x * 16 + (int)(threadIdx.x >> 4) >= n) continue;
+      uint8_t* d = a.pool.pages + ut[x] * L::kHead;
+      *reinterpret_cast<Key*>(d + t[x] * (D / 2) + j * B) = kc[x];
+#pragma unroll
+      for (int c = 0; c < L::C; ++c) *reinterpret_cast<Value*>(d + L::kSide + L::value_codes(t[x], c, j)) = vc[x][c];
+      if (j < L::NS) {
+        d[L::key_scale(t[x], j)] = ks[x];
+        d[L::kSide + L::value_scale(t[x], j)] = vs[x];
+      }
+      if (j < 2) (j ? (uint32_t*)a.pool.positions : (uint32_t*)a.pool.weights)[ut[x] * kPage + t[x]] = mark[x];
+    }
   }
 }
 
@@ -214,7 +308,7 @@ sc_status kv4_evict(const sc_kv4_cache* cache, const sc_kv4_seqs* seqs, int32_t 
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && a.most > 0)
     e = by_layout(cache->head_dim, cache->format, [&](auto d, auto f) {
-      const int blocks = (a.most + 3) / 4;
+      const int blocks = (a.most + kMoves - 1) / kMoves;
       hipLaunchKernelGGL((k_kv4_move<d(), f()>), dim3(units, blocks < 64 ? blocks : 64), dim3(256), 0, st, a);
       return hipGetLastError();
     });

@@ -560,6 +560,18 @@ def test_evict_weights_of_all_kinds():
     _check_evict(torch, c, np.zeros((n, 1), np.float32), at, 250, 0, 0)      # all equal: the first places
 
 
+def test_evict_long_sequences():
+    """Around the most places whose keys are held in registers (32768), and far more."""
+    torch = torch_cuda()
+    log("evict long")
+    for n, keep in ((32768, 20000), (32769, 400), (70001, 35000)):
+        c = Filled(torch, "mxfp4", 64, 1, [n, 130], track=True, seed=n)
+        rng = np.random.default_rng(n)
+        w = np.floor(rng.exponential(30.0, (n + 130, 1))).astype(np.float32) / 8
+        at = np.concatenate((np.arange(n), np.arange(130))).astype(np.int32)[:, None]
+        _check_evict(torch, c, w, at, keep, keep // 10, 3)
+
+
 def test_evict_leaves_what_it_cannot_do():
     torch = torch_cuda()
     log("evict bad")
