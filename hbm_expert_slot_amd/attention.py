@@ -15,20 +15,25 @@ from .ops import _FORMAT, _TYPE, _Fixed, _ForInference, _need, _On, _record, _wa
 PAGE = B.SC_KV4_PAGE
 HEAD_DIMS = (64, 128, 256)
 _NARROW = (torch.bfloat16, torch.float16)
+_INT = torch.int32
 
 
-def _rows3(t, name, dtypes, dev=None):
+# What is wrong is only put into words once something is: a call spends less time on its checks.
+
+def _rows3(t, name, dtypes, dev):
     """[tokens, heads, head_dim] with the last dimension contiguous."""
-    _need(t.dim() == 3, "%s must be [tokens, heads, head_dim]" % name)
-    _need(t.dtype in dtypes, "%s has type %s" % (name, t.dtype))
-    _need(t.is_cuda and (dev is None or t.device == dev), "%s must be on the GPU%s" % (name, "" if dev is None else ", on %s" % dev))
-    _need(t.shape[2] in HEAD_DIMS, "%s: head_dim must be one of %s" % (name, HEAD_DIMS))
-    _need(t.stride(2) == 1, "%s must be contiguous along head_dim" % name)
+    if not (t.dim() == 3 and t.dtype in dtypes and t.device == dev and t.is_cuda and t.stride(2) == 1
+            and t.shape[2] in HEAD_DIMS):
+        _need(t.dim() == 3, "%s must be [tokens, heads, head_dim]" % name)
+        _need(t.dtype in dtypes, "%s has type %s" % (name, t.dtype))
+        _need(t.is_cuda and t.device == dev, "%s must be on the GPU, with the others" % name)
+        _need(t.shape[2] in HEAD_DIMS, "%s: head_dim must be one of %s" % (name, HEAD_DIMS))
+        _need(False, "%s must be contiguous along head_dim" % name)
 
 
-def _ints(t, name, shape, dev):
-    _need(t.dtype == torch.int32 and tuple(t.shape) == shape and t.device == dev and t.is_contiguous(),
-          "%s must be a contiguous int32 tensor of shape %s on %s" % (name, shape, dev))
+def _ints(t, name, n, dev):
+    if not (t.dtype == _INT and t.dim() == 1 and t.shape[0] == n and t.device == dev and (n < 2 or t.stride(0) == 1)):
+        raise ValueError("%s must be a contiguous int32 vector of %d on %s" % (name, n, dev))
 
 
 def _scale_of(scale, dim):
@@ -65,23 +70,24 @@ def prompt_attention(q, k, v, starts, key_starts=None, scale=None, out=None, ret
     if out is None and _wants_grad(q, k, v):
         return _ForInference.apply("prompt_attention", lambda: prompt_attention(
             q, k, v, starts, key_starts, scale, None, return_lse, stream), q, k, v)
-    _rows3(q, "q", _NARROW)
     dev = q.device
-    for t, name in ((k, "k"), (v, "v")):
-        _rows3(t, name, (q.dtype,), dev)
+    _rows3(q, "q", _NARROW, dev)
+    _rows3(k, "k", (q.dtype,), dev)
+    _rows3(v, "v", (q.dtype,), dev)
     rows, heads, dim = q.shape
-    keys, kv_heads = k.shape[0], k.shape[1]
-    _need(k.shape[2] == dim and k.shape == v.shape, "q %s, k %s and v %s do not fit" % (
-        tuple(q.shape), tuple(k.shape), tuple(v.shape)))
+    keys, kv_heads, kdim = k.shape
+    if not (kdim == dim and k.shape == v.shape):
+        raise ValueError("q %s, k %s and v %s do not fit" % (tuple(q.shape), tuple(k.shape), tuple(v.shape)))
     _need(kv_heads > 0 and heads > 0 and heads % kv_heads == 0, "heads must be a multiple of kv_heads")
     _need(starts.dim() == 1 and starts.shape[0] >= 1, "starts must be [sequences + 1]")
     n = starts.shape[0] - 1
-    _ints(starts, "starts", (n + 1,), dev)
+    _ints(starts, "starts", n + 1, dev)
     if key_starts is None:
-        _need(keys == rows, "%d rows and %d keys: key_starts are needed" % (rows, keys))
+        if keys != rows:
+            raise ValueError("%d rows and %d keys: key_starts are needed" % (rows, keys))
         key_starts = starts
     else:
-        _ints(key_starts, "key_starts", (n + 1,), dev)
+        _ints(key_starts, "key_starts", n + 1, dev)
     scale = _scale_of(scale, dim)
     with _On(dev, stream) as s:
         if out is None:
@@ -92,13 +98,14 @@ def prompt_attention(q, k, v, starts, key_starts=None, scale=None, out=None, ret
             _writable(out, "out")
         lse = torch.empty((rows, heads), dtype=torch.float32, device=dev) if return_lse else None
         qs, ks, vs, os = q.stride(), k.stride(), v.stride(), out.stride()
-        p = B.sc_prompt(_TYPE[q.dtype], dim, heads, kv_heads, n, rows, keys, scale, q.data_ptr(), k.data_ptr(),
-                        v.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(), starts.data_ptr(),
-                        key_starts.data_ptr(), (qs[0], qs[1]), (ks[0], ks[1]), (vs[0], vs[1]), (os[0], os[1]))
-        ref = ctypes.byref(p)
-        need = B.prompt_attention_workspace_bytes(ref)
-        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-        B.prompt_attention(ref, None if ws is None else ws.data_ptr(), s)
+        p = B.PROMPT.pack(_TYPE[q.dtype], dim, heads, kv_heads, n, rows, keys, scale, q.data_ptr(), k.data_ptr(),
+                          v.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(), starts.data_ptr(),
+                          key_starts.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os[0], os[1])
+        ws = None
+        if keys >= 2 * B.SC_PROMPT_PART_KEYS * n:
+            need = B.prompt_attention_workspace_bytes(p)
+            ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        B.prompt_attention(p, None if ws is None else ws.data_ptr(), s)
     if stream is not None:
         _record(stream, q, k, v, starts, key_starts, out, lse)
     return (out, lse) if return_lse else out
@@ -120,7 +127,7 @@ class KV4Cache(_Fixed):
     under way, but not while a captured graph is to be replayed."""
 
     _fixed = frozenset(("fmt", "head_dim", "kv_heads", "n_pages", "device", "pages", "weights", "positions", "k_scale",
-                        "v_scale", "_memory", "_streams", "_c", "_ref"))
+                        "v_scale", "_memory", "_streams", "_sizes", "_c", "_ref"))
 
     def __init__(self, n_pages, kv_heads, head_dim, fmt="nvfp4", k_scale=None, v_scale=None, track=False, device="cuda"):
         _need(fmt in _FORMAT, "unknown format %r" % (fmt,))
@@ -148,7 +155,8 @@ class KV4Cache(_Fixed):
                            ptr(k_scale), ptr(v_scale))
         self.__dict__.update(fmt=fmt, head_dim=head_dim, kv_heads=kv_heads, n_pages=n_pages, device=dev, pages=pages,
                              weights=weights, positions=positions, k_scale=k_scale, v_scale=v_scale, _memory=memory,
-                             _streams={torch.cuda.current_stream(dev).cuda_stream}, _c=c, _ref=ctypes.byref(c))
+                             _streams={torch.cuda.current_stream(dev).cuda_stream}, _sizes={}, _c=c,
+                             _ref=ctypes.byref(c))
 
     def _used_on(self, s):
         """The cache may be dropped while the current stream (raw: s, not in _streams yet) works on it."""
@@ -157,30 +165,38 @@ class KV4Cache(_Fixed):
 
     def _seqs(self, table, lens):
         dev = self.device
-        _need(table.dim() == 2 and table.dtype == torch.int32 and table.device == dev and table.shape[1] >= 1
-              and (table.shape[1] == 1 or table.stride(1) == 1),
-              "table must be an int32 tensor [sequences, pages] on %s, contiguous along its rows" % dev)
+        if not (table.dim() == 2 and table.dtype == _INT and table.device == dev and table.shape[1] >= 1
+                and (table.shape[1] == 1 or table.stride(1) == 1)):
+            raise ValueError("table must be an int32 tensor [sequences, pages] on %s, contiguous along its rows" % dev)
         n, width = table.shape
-        _ints(lens, "lens", (n,), dev)
+        _ints(lens, "lens", n, dev)
         ld = table.stride(0) if n > 1 else width
         _need(ld >= width, "table has rows that overlap")
-        return B.sc_kv4_seqs(n, width, ld, table.data_ptr(), lens.data_ptr())
+        return B.KV4_SEQS.pack(n, width, ld, table.data_ptr(), lens.data_ptr())
 
     def _rows(self, k, v, types):
         dev = self.device
-        for t, name in ((k, "k"), (v, "v")):
-            _rows3(t, name, types, dev)
-            _need(t.shape[1] == self.kv_heads and t.shape[2] == self.head_dim, "%s does not fit the cache" % name)
-        _need(k.shape == v.shape and k.dtype == v.dtype, "k and v differ")
+        _rows3(k, "k", types, dev)
+        _rows3(v, "v", types, dev)
+        shape = k.shape
+        if not (shape[1] == self.kv_heads and shape[2] == self.head_dim and v.shape == shape and v.dtype == k.dtype):
+            raise ValueError("k %s %s and v %s %s do not fit the cache or each other" % (
+                tuple(shape), k.dtype, tuple(v.shape), v.dtype))
         ks, vs = k.stride(), v.stride()
-        return B.sc_kv4_rows(_TYPE[k.dtype], k.data_ptr(), v.data_ptr(), ks[0], ks[1], vs[0], vs[1])
+        return B.KV4_ROWS.pack(_TYPE[k.dtype], k.data_ptr(), v.data_ptr(), ks[0], ks[1], vs[0], vs[1])
 
     def _deal(self, tokens, n, starts):
         if starts is not None:
-            _ints(starts, "starts", (n + 1,), self.device)
+            _ints(starts, "starts", n + 1, self.device)
             return starts.data_ptr()
-        _need(n > 0 and tokens % n == 0 or tokens == 0, "%d tokens cannot be dealt out to %d sequences" % (tokens, n))
+        if tokens and (n == 0 or tokens % n):
+            raise ValueError("%d tokens cannot be dealt out to %d sequences" % (tokens, n))
         return None
+
+    def _four(self, t, name, dtypes):
+        if not (t.dim() == 4 and t.dtype in dtypes and t.device == self.device and t.stride(3) == 1):
+            raise ValueError("%s must be [sequences, rows, heads, head_dim] of %s on %s, contiguous along head_dim"
+                             % (name, dtypes, self.device))
 
     def append(self, k, v, table, lens, starts=None, positions=None, stream=None):
         """Quantise tokens into the cache: k and v [tokens, kv_heads, head_dim] (float32, bfloat16 or
@@ -194,10 +210,9 @@ class KV4Cache(_Fixed):
         ps = self._deal(tokens, lens.shape[0], starts)
         if positions is not None:
             _need(self.positions is not None, "the cache keeps no positions")
-            _ints(positions, "positions", (tokens,), self.device)
+            _ints(positions, "positions", tokens, self.device)
         with _On(self.device, stream) as s:
-            B.kv4_append(self._ref, ctypes.byref(seqs), ctypes.byref(rows), tokens, ps,
-                         None if positions is None else positions.data_ptr(), s)
+            B.kv4_append(self._ref, seqs, rows, tokens, ps, None if positions is None else positions.data_ptr(), s)
             if s not in self._streams:
                 self._used_on(s)
         if stream is not None:
@@ -212,10 +227,11 @@ class KV4Cache(_Fixed):
         _need(tokens >= 0, "tokens must be >= 0")
         ps = self._deal(tokens, lens.shape[0], starts)
         with _On(self.device, stream) as s:
-            k = torch.empty((tokens, self.kv_heads, self.head_dim), dtype=dtype, device=self.device)
-            v = torch.empty_like(k)
-            rows = self._rows(k, v, _TYPE)
-            B.kv4_read(self._ref, ctypes.byref(seqs), ctypes.byref(rows), tokens, ps, s)
+            heads, dim = self.kv_heads, self.head_dim
+            k = torch.empty((tokens, heads, dim), dtype=dtype, device=self.device)
+            v = torch.empty((tokens, heads, dim), dtype=dtype, device=self.device)
+            rows = B.KV4_ROWS.pack(_TYPE[dtype], k.data_ptr(), v.data_ptr(), heads * dim, dim, heads * dim, dim)
+            B.kv4_read(self._ref, seqs, rows, tokens, ps, s)
             if s not in self._streams:
                 self._used_on(s)
         if stream is not None:
@@ -234,33 +250,35 @@ class KV4Cache(_Fixed):
                 q, table, lens, scale, accumulate, None, stream), q)
         seqs = self._seqs(table, lens)
         dev = self.device
-
-        def four(t, name, dtypes):
-            _need(t.dim() == 4 and t.dtype in dtypes and t.device == dev,
-                  "%s must be [sequences, rows, heads, head_dim] of %s on %s" % (name, dtypes, dev))
-            _need(t.stride(3) == 1, "%s must be contiguous along head_dim" % name)
-
-        four(q, "q", _NARROW)
+        self._four(q, "q", _NARROW)
         n, rows, heads, dim = q.shape
-        _need(n == lens.shape[0] and dim == self.head_dim, "q %s does not fit the cache or the table" % (tuple(q.shape),))
-        _need(1 <= rows <= B.SC_KV4_MAX_ROWS, "rows must be in [1, %d]" % B.SC_KV4_MAX_ROWS)
-        _need(heads > 0 and heads % self.kv_heads == 0 and heads // self.kv_heads <= B.SC_KV4_MAX_GROUP,
-              "heads must be a multiple of kv_heads, up to %d times" % B.SC_KV4_MAX_GROUP)
+        if not (n == lens.shape[0] and dim == self.head_dim):
+            raise ValueError("q %s does not fit the cache or the table" % (tuple(q.shape),))
+        if not (1 <= rows <= B.SC_KV4_MAX_ROWS and 0 < heads <= B.SC_KV4_MAX_GROUP * self.kv_heads
+                and heads % self.kv_heads == 0):
+            raise ValueError("rows must be in [1, %d], heads a multiple of kv_heads, up to %d times"
+                             % (B.SC_KV4_MAX_ROWS, B.SC_KV4_MAX_GROUP))
         _need(not accumulate or self.weights is not None, "the cache keeps no weights")
         scale = _scale_of(scale, dim)
+        # the workspace follows from the sizes
+        key = (n, table.shape[1], rows, heads, bool(accumulate))
+        need = self._sizes.get(key)
+        if need is None:
+            if len(self._sizes) > 1000:
+                self._sizes.clear()
+            need = self._sizes[key] = B.kv4_attention_workspace_bytes(self._ref, seqs, rows, heads, accumulate)
         with _On(dev, stream) as s:
             if out is None:
                 out = torch.empty((n, rows, heads, dim), dtype=q.dtype, device=dev)
             else:
-                four(out, "out", (q.dtype,))
+                self._four(out, "out", (q.dtype,))
                 _need(out.shape == q.shape, "out does not fit q")
                 _writable(out, "out")
-            sref = ctypes.byref(seqs)
-            ws = torch.empty(B.kv4_attention_workspace_bytes(self._ref, sref, rows, heads, accumulate), dtype=torch.uint8,
-                             device=dev)
-            x = B.sc_kv4_query(_TYPE[q.dtype], rows, heads, scale, q.data_ptr(), out.data_ptr(), q.stride()[:3],
-                               out.stride()[:3])
-            B.kv4_attention(self._ref, sref, ctypes.byref(x), accumulate, ws.data_ptr(), s)
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+            qs, os = q.stride(), out.stride()
+            x = B.KV4_QUERY.pack(_TYPE[q.dtype], rows, heads, scale, q.data_ptr(), out.data_ptr(), qs[0], qs[1], qs[2],
+                                 os[0], os[1], os[2])
+            B.kv4_attention(self._ref, seqs, x, accumulate, ws.data_ptr(), s)
             if s not in self._streams:
                 self._used_on(s)
         if stream is not None:
@@ -282,9 +300,8 @@ class KV4Cache(_Fixed):
         _need(keep < 2 ** 31, "keep is too large")
         with _On(self.device, stream) as s:
             new = torch.empty_like(lens)
-            sref = ctypes.byref(seqs)
-            ws = torch.empty(B.kv4_evict_workspace_bytes(self._ref, sref, keep), dtype=torch.uint8, device=self.device)
-            B.kv4_evict(self._ref, sref, keep, recent, sinks, new.data_ptr(), ws.data_ptr(), s)
+            ws = torch.empty(B.kv4_evict_workspace_bytes(self._ref, seqs, keep), dtype=torch.uint8, device=self.device)
+            B.kv4_evict(self._ref, seqs, keep, recent, sinks, new.data_ptr(), ws.data_ptr(), s)
             if s not in self._streams:
                 self._used_on(s)
         if stream is not None:

@@ -6,6 +6,7 @@ import of a call fails loudly -- there is no fallback implementation.
 """
 import ctypes
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libslotcache.so")
@@ -38,6 +39,7 @@ SC_PROMPT_MAX_HEADS = 1024
 SC_PROMPT_MAX_SEQS = 65536
 SC_PROMPT_MAX_ROWS = 1 << 24
 SC_PROMPT_MAX_STRIDE = 1 << 23
+SC_PROMPT_PART_KEYS = 2048
 SC_KV4_PAGE = 64
 SC_KV4_MAX_HEADS = 1024
 SC_KV4_MAX_SEQS = 65536
@@ -137,6 +139,12 @@ class sc_kv4_query(ctypes.Structure):
                 ("scale", ctypes.c_float), ("d_q", ctypes.c_void_p), ("d_out", ctypes.c_void_p),
                 ("q_stride", ctypes.c_int64 * 3), ("out_stride", ctypes.c_int64 * 3)]
 
+
+# The same structures as bytes, which cost a call less than ctypes objects.
+PROMPT = struct.Struct("@7if7N8q")
+KV4_SEQS = struct.Struct("@2iq2N")
+KV4_ROWS = struct.Struct("@i4x2N4q")
+KV4_QUERY = struct.Struct("@3if2N6q")
 
 _lib = None
 

@@ -13,6 +13,7 @@
 #include "fp4_device.h"
 #include "internal.h"
 
+#include <atomic>
 #include <type_traits>
 
 namespace sc {
@@ -403,9 +404,17 @@ template <int D, bool HALF, bool DIRECT, bool PARTS>
 hipError_t launch(const PromptArgs& a, hipStream_t st) {
   const unsigned grid = (unsigned)((a.rows / kRows + a.n) * a.heads);
   constexpr int kLds = 4 * kKeysOf<D> * D * 2;
-  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_prompt<D, HALF, DIRECT, PARTS>),
-                                     hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+  // once per device: more LDS than a block has by default
+  static std::atomic<uint64_t> allowed{0};
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return e;
+  if (dev >= 64 || !(allowed.load(std::memory_order_relaxed) >> dev & 1)) {
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_prompt<D, HALF, DIRECT, PARTS>),
+                            hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+    if (e != hipSuccess) return e;
+    if (dev < 64) allowed.fetch_or(1ull << dev, std::memory_order_relaxed);
+  }
   hipLaunchKernelGGL((k_prompt<D, HALF, DIRECT, PARTS>), dim3(grid, a.parts), dim3(kThreads), kLds, st, a);
   e = hipGetLastError();
   if (!PARTS || e != hipSuccess) return e;
@@ -440,7 +449,7 @@ sc_status check(const sc_prompt* p) {
 // 16380 keys: 160 blocks 339 us, in 3 parts 157 us.
 int parts_of(const sc_prompt* p) {
   const int64_t blocks = ((int64_t)p->rows / kRows + p->n_seqs) * p->q_heads, by_units = 512 / blocks;
-  const int64_t by_keys = p->keys / p->n_seqs / 2048, n = by_units < by_keys ? by_units : by_keys;
+  const int64_t by_keys = p->keys / p->n_seqs / SC_PROMPT_PART_KEYS, n = by_units < by_keys ? by_units : by_keys;
   return n < 2 ? 1 : n < 8 ? (int)n : 8;
 }
 size_t part_bytes(const sc_prompt* p, int parts) { return (size_t)p->rows * p->q_heads * parts * p->head_dim * 4; }

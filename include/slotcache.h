@@ -464,6 +464,8 @@ SC_API sc_status moe_layer_forward(const sc_moe_config* cfg, const sc_moe_weight
 #define SC_PROMPT_MAX_ROWS (1 << 24)
 #define SC_PROMPT_MAX_STRIDE (1 << 23)   /* elements from a key or value to the next */
 
+#define SC_PROMPT_PART_KEYS 2048
+
 /* Packed sequences: sequence b has the rows d_starts[b] .. d_starts[b+1]-1 of q
  * and the keys d_key_starts[b] .. d_key_starts[b+1]-1 of k and v.  Element d of
  * row t and head h of q is at t * q_stride[0] + h * q_stride[1] + d, and so for
@@ -486,7 +488,7 @@ typedef struct {
 } sc_prompt;
 
 /* Bytes of device workspace that prompt_attention needs: 0 but for few rows over
- * many keys.  Reads the sizes only. */
+ * many keys (2 * SC_PROMPT_PART_KEYS per sequence and more).  Reads the sizes only. */
 SC_API sc_status prompt_attention_workspace_bytes(const sc_prompt* p, size_t* bytes);
 
 /* Causal attention of every row over its sequence's keys: with Lq rows and Lk

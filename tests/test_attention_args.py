@@ -190,3 +190,17 @@ def test_the_python_layer_names_what_is_wrong():
                dict(fmt="mxfp4", k_scale=torch.ones(1))):
         with pytest.raises(ValueError):
             ops.KV4Cache(**dict(dict(n_pages=2, kv_heads=2, head_dim=64), **kw))
+
+
+def test_structures_as_bytes():
+    """The packed forms have the layout of the structures."""
+    import ctypes as ct
+    for packer, cls, flat in ((B.PROMPT, B.sc_prompt, 23), (B.KV4_SEQS, B.sc_kv4_seqs, 5), (B.KV4_ROWS, B.sc_kv4_rows, 7),
+                              (B.KV4_QUERY, B.sc_kv4_query, 12)):
+        assert packer.size == ct.sizeof(cls)
+        got = cls.from_buffer_copy(packer.pack(*range(1, flat + 1)))
+        vals = []
+        for name, _ in cls._fields_:
+            v = getattr(got, name)
+            vals += list(v) if isinstance(v, ct.Array) else [v]
+        assert vals == list(range(1, flat + 1))
