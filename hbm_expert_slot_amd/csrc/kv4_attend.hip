@@ -29,7 +29,8 @@ namespace kv4 {
 namespace {
 
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
-constexpr int kBlocks = 512;             // parts of the list: two per compute unit
+constexpr int kMaxParts = 768;           // of the list: up to three blocks per compute unit
+constexpr int kDirectPages = 8;          // up to which a head's pages are one block's
 constexpr float kLog2e = 1.44269504088896340736f;
 
 struct AttendArgs {
@@ -46,7 +47,8 @@ struct AttendArgs {
   float* part;              // [2 * blocks][16 * NQ][D]: sums of pieces
   float* part_ml;           // [2 * blocks][16 * NQ][2]
   float* lse;               // [sequence][head][cols], base 2; null unless weights are kept
-  int32_t nblocks;
+  int32_t nblocks, weight_blocks;
+  bool direct;              // a block has all of one head, with no list
 };
 
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
@@ -75,6 +77,8 @@ __device__ __forceinline__ uint32_t widen_bf16(uint32_t d, float s) {
 __device__ __forceinline__ uint32_t times(uint32_t a, f16x2 s) {
   return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, a) * s);
 }
+// The conversions take their scale's exponent field as E8M0: 0 is 2^-127, 255 NaN.
+__device__ __forceinline__ float e8m0_field(uint32_t d, int byte) { return __uint_as_float((d >> (8 * byte) & 0xFF) << 23); }
 // Two E4M3 scales (half W of d) as fp16, exactly.
 template <int W>
 __device__ __forceinline__ f16x2 scales2(uint32_t d) {
@@ -159,7 +163,7 @@ __device__ __forceinline__ void widen_keys(const Keys<D, FMT>& p, int t, u32x4 (
       out[w] = u32x4{times(widen_f16<0>(q), s), times(widen_f16<1>(q), s), times(widen_f16<2>(q), s),
                      times(widen_f16<3>(q), s)};
     } else {
-      const float s = e8m0((p.s[at / 4] >> (at % 4 * 8)) & 0xFF);
+      const float s = e8m0_field(p.s[at / 4], at % 4);
       out[w] = u32x4{widen_bf16<0>(q, s), widen_bf16<1>(q, s), widen_bf16<2>(q, s), widen_bf16<3>(q, s)};
     }
   }
@@ -184,7 +188,7 @@ __device__ __forceinline__ void pair_tokens(uint32_t a, uint32_t b, uint32_t sab
       out[7] = times(widen_f16<3>(odd), s);
     }
   } else {
-    const float sa = e8m0(sab >> (16 * half) & 0xFF), sb = e8m0(sab >> (16 * half + 8) & 0xFF);
+    const float sa = e8m0_field(sab, 2 * half), sb = e8m0_field(sab, 2 * half + 1);
     const auto two = [&](uint32_t x, uint32_t y, int i) {
       out[i] = __builtin_amdgcn_perm(y, x, 0x05040100u);
       out[i + 1] = __builtin_amdgcn_perm(y, x, 0x07060302u);
@@ -202,11 +206,10 @@ __device__ __forceinline__ uint32_t pack16(float a, float b, bool f16) {
   if (f16) return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b});
   return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
 }
-// What bf16 leaves of two numbers; nothing of one that is not finite.
+// What bf16 leaves of two numbers (NaN of one that is not finite).
 __device__ __forceinline__ uint32_t rest16(float a, float b, uint32_t hi) {
-  const bf16x2 h = __builtin_bit_cast(bf16x2, hi);
-  const float x = a - (float)h.x, y = b - (float)h.y;
-  return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)(x == x ? x : 0.0f), (__bf16)(y == y ? y : 0.0f)});
+  const float x = a - __uint_as_float(hi << 16), y = b - __uint_as_float(hi & 0xFFFF0000u);
+  return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)x, (__bf16)y});
 }
 
 // Over the four lanes of a column.
@@ -230,30 +233,34 @@ struct Queries {
   float factor;     // of the products, to get scores in base 2
   int row;          // of the column; beyond the last: it sees what the last does
 };
+// As they are in memory, and then as operands.
 template <int D, int FMT, bool HALF>
-__device__ __forceinline__ void load_queries(Queries<D, FMT, HALF>& q, const AttendArgs& a, int b, int head, int first,
-                                             int lane) {
+__device__ __forceinline__ void fetch_queries(Queries<D, FMT, HALF>& q, const AttendArgs& a, int b, int head, int first,
+                                              int lane) {
   typedef Layout<D, FMT> L;
-  typedef Queries<D, FMT, HALF> Q;
-  const int col = first + (lane & 15), g = lane >> 4;
-  const bool in = col < a.cols;
-  const int c1 = in ? col : a.cols - 1;
-  q.row = c1 / a.group;
-  const uint16_t* p = a.q + b * a.qs[0] + q.row * a.qs[1] + ((int64_t)head * a.group + c1 % a.group) * a.qs[2];
   constexpr int WC = L::LaneDims / 8;
+  const int col = min(first + (lane & 15), a.cols - 1), g = lane >> 4;
+  q.row = col / a.group;
+  const uint16_t* p = a.q + b * a.qs[0] + q.row * a.qs[1] + ((int64_t)head * a.group + col % a.group) * a.qs[2];
+#pragma unroll
+  for (int w = 0; w < Queries<D, FMT, HALF>::W; ++w)
+    __builtin_memcpy(&q.x[w][0], p + w / WC * 128 + g * L::LaneDims + w % WC * 8, 16);
+}
+template <int D, int FMT, bool HALF>
+__device__ __forceinline__ void widen_queries(Queries<D, FMT, HALF>& q, const AttendArgs& a, int first, int lane) {
+  typedef Queries<D, FMT, HALF> Q;
+  const bool in = first + (lane & 15) < a.cols;
   float v[Q::W][8];
   float top = 0.0f;
 #pragma unroll
-  for (int w = 0; w < Q::W; ++w) {
-    uint16_t raw[8];
-    __builtin_memcpy(raw, p + w / WC * 128 + g * L::LaneDims + w % WC * 8, 16);
+  for (int w = 0; w < Q::W; ++w)
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      v[w][e] = HALF ? (float)__builtin_bit_cast(_Float16, raw[e]) : __uint_as_float((uint32_t)raw[e] << 16);
+      const uint32_t raw = q.x[w][0][e / 2] >> (e % 2 * 16) & 0xFFFF;
+      v[w][e] = HALF ? (float)__builtin_bit_cast(_Float16, (uint16_t)raw) : __uint_as_float(raw << 16);
       if (!in) v[w][e] = 0.0f;
       top = fmaxf(top, fabsf(v[w][e]));
     }
-  }
   float up = 1.0f;
   q.factor = a.scale * kLog2e * (a.ks ? *a.ks : 1.0f);
   if constexpr (FMT == kNv) {
@@ -270,7 +277,7 @@ __device__ __forceinline__ void load_queries(Queries<D, FMT, HALF>& q, const Att
     for (int e = 0; e < 4; ++e) {
       const float x = v[w][2 * e] * up, y = v[w][2 * e + 1] * up;
       q.x[w][0][e] = pack16(x, y, FMT == kNv);
-      if constexpr (Q::P == 2) q.x[w][1][e] = rest16(x, y, q.x[w][0][e]);
+      if constexpr (Q::P == 2) q.x[w][1][e] = rest16(x, y, q.x[w][0][e]);      // NaN: its scores are NaN or infinite anyway
     }
 }
 
@@ -291,50 +298,96 @@ __device__ __forceinline__ int pages_of(const Seqs& s, int b) {
   const int n = b < s.n ? length_of(s, b) : 0;
   return n > 0 ? (n + kPage - 1) / kPage : 0;
 }
-__device__ __forceinline__ int64_t wave_scan(int64_t v, int lane) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int64_t u = __shfl_up(v, o);
-    if (lane >= o) v += u;
-  }
-  return v;
-}
 __device__ __forceinline__ int64_t of_lane(int64_t v, int l) {
   const uint32_t lo = __builtin_amdgcn_readlane((int)v, l), hi = __builtin_amdgcn_readlane((int)(v >> 32), l);
   return (int64_t)((uint64_t)hi << 32 | lo);
 }
-// Pages of the sequences before b, and of all.
-__device__ __forceinline__ int64_t pages_before(const Seqs& s, int b, int64_t& total, int lane) {
-  int64_t before = 0, sum = 0;
-  for (int i = 0; i < s.n; i += 64) {
-    const int64_t upto = wave_scan(pages_of(s, i + lane), lane);
-    if (b >= i && b < i + 64) before = sum + (b > i ? of_lane(upto, b - i - 1) : 0);
-    sum += of_lane(upto, 63);
-  }
-  total = sum;
-  return before;
+// Sums over the lanes up to each; the totals of 64 sequences fit 32 bits.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_add(int v) {
+  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
 }
-// The sequence that unit u of the list lies in, and the units before it; `per`
-// units of the list per page of a sequence.
-__device__ __forceinline__ int sequence_at(const Seqs& s, int64_t u, int per, int64_t& before, int lane) {
-  int64_t sum = 0;
-  for (int i = 0; i < s.n; i += 64) {
-    const int64_t n = (int64_t)pages_of(s, i + lane) * per;
-    const int64_t upto = sum + wave_scan(n, lane);
-    const uint64_t beyond = __ballot(upto > u);
-    if (beyond) {
-      const int l = __builtin_ctzll(beyond);
-      before = of_lane(upto - n, l);
-      return i + l;
+__device__ __forceinline__ int wave_scan(int v) {
+  v = dpp_add<0x111, 0xF>(v);      // from 1, 2, 4 and 8 lanes before in the row of 16
+  v = dpp_add<0x112, 0xF>(v);
+  v = dpp_add<0x114, 0xF>(v);
+  v = dpp_add<0x118, 0xF>(v);
+  v = dpp_add<0x142, 0xA>(v);      // a row's last lane to the next row, the second row's to both behind
+  return dpp_add<0x143, 0xC>(v);
+}
+struct List {
+  const Seqs& s;
+  int lane, own, upto;             // of the first 64 sequences: pages, and pages up to each
+  int64_t total;
+  __device__ __forceinline__ List(const Seqs& seqs, int l) : s(seqs), lane(l) {
+    own = pages_of(s, lane);
+    upto = wave_scan(own);
+    total = __builtin_amdgcn_readlane(upto, 63);
+    for (int i = 64; i < s.n; i += 64) total += __builtin_amdgcn_readlane(wave_scan(pages_of(s, i + lane)), 63);
+  }
+  // Pages of the sequences before b.
+  __device__ __forceinline__ int64_t before(int b) const {
+    int64_t sum = 0;
+    for (int i = 0; i <= b; i += 64) {
+      const int x = i ? wave_scan(pages_of(s, i + lane)) : upto;
+      if (b >= i + 64) sum += __builtin_amdgcn_readlane(x, 63);
+      else if (b > i) sum += __builtin_amdgcn_readlane(x, b - i - 1);
     }
-    sum = of_lane(upto, 63);
+    return sum;
   }
-  before = sum;
-  return s.n;
+  // The sequence that unit u lies in, its pages, and the units before it; `per` units per page of a sequence.
+  __device__ __forceinline__ int at(int64_t u, int per, int& pages, int64_t& units_before) const {
+    int64_t sum = 0;
+    for (int i = 0; i < s.n; i += 64) {
+      const int n = i ? pages_of(s, i + lane) : own;
+      const int64_t x = sum + (i ? wave_scan(n) : upto);
+      const uint64_t beyond = __ballot(x * per > u);
+      if (beyond) {
+        const int l = __builtin_ctzll(beyond);
+        pages = __builtin_amdgcn_readlane(n, l);
+        units_before = (of_lane(x, l) - pages) * per;
+        return i + l;
+      }
+      sum = of_lane(x, 63);
+    }
+    pages = 0;
+    units_before = sum * per;
+    return s.n;
+  }
+};
+// A sequence's pages, the entries of 64 at a time in a wavefront's lanes.
+struct Table {
+  const Pool& pool;
+  const Seqs& s;
+  int b, lane, first, entry;
+  __device__ __forceinline__ Table(const Pool& p, const Seqs& seqs, int l) : pool(p), s(seqs), lane(l) {}
+  __device__ __forceinline__ void open(int seq, int at) {
+    b = seq;
+    first = at;
+    entry = page_at(pool, s, b, at + lane);
+  }
+  __device__ __forceinline__ int page(int index) {
+    if (index < first || index >= first + 64) {
+      first = index;
+      entry = page_at(pool, s, b, index + lane);
+    }
+    return __builtin_amdgcn_readlane(entry, index - first);
+  }
+};
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {      // of numbers >= 0; most fit 32 bits
+  return (a | b) >> 32 == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : (int64_t)((uint64_t)a / (uint64_t)b);
 }
-__device__ __forceinline__ int64_t cut(int64_t units, int part, int parts) { return units * part / parts; }
-// The part that holds unit u.
-__device__ __forceinline__ int part_of(int64_t units, int64_t u, int parts) { return (int)(((u + 1) * parts - 1) / units); }
+// The list in equal parts.  The longer ones are spread evenly, so heads of one
+// length whose number divides that of the parts begin with one.
+struct Cuts {
+  int64_t units, each;
+  uint32_t rest;
+  int parts;
+  __device__ __forceinline__ Cuts(int64_t n, int p) : units(n), each(quotient(n, p)), rest((uint32_t)(n - each * p)), parts(p) {}
+  __device__ __forceinline__ int64_t start(int part) const { return each * part + rest * (uint32_t)part / (uint32_t)parts; }
+  // the part that holds unit u
+  __device__ __forceinline__ int holds(int64_t u) const { return (int)quotient((u + 1) * parts - 1, units); }
+};
 
 template <bool HALF>
 __device__ __forceinline__ uint16_t narrow(float v) {
@@ -351,7 +404,7 @@ __device__ __forceinline__ float lse2_of(float m, float l) {
 // the step before is in its softmax and second product, its values during its own
 // first product: into the registers that the step before has just left.
 template <int D, int FMT, bool HALF, int NQ>
-__global__ __launch_bounds__(kThreads, 2) void k_kv4_attend(AttendArgs a) {
+__global__ __launch_bounds__(kThreads, NQ == 1 && D <= 128 ? 3 : 2) void k_kv4_attend(AttendArgs a) {
   typedef Layout<D, FMT> L;
   constexpr bool F16 = FMT == kNv;
   constexpr int W = Keys<D, FMT>::W, VD = L::VDims, NO = L::C * VD;     // output tiles
@@ -363,31 +416,66 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv4_attend(AttendArgs a) {
   __shared__ float red_m[kWaves][16], red_l[kWaves][16];
   const int lane = threadIdx.x & 63, wave = wave_index(), g = lane >> 4;
   const int per = a.pool.heads * a.chunks;
-  int64_t pages;
-  pages_before(a.seqs, 0, pages, lane);
-  const int64_t units = pages * per;
-  const int64_t u0 = cut(units, blockIdx.x, a.nblocks), u1 = cut(units, blockIdx.x + 1, a.nblocks);
-  for (int64_t u = u0; u < u1;) {
-    int64_t before;
-    const int b = sequence_at(a.seqs, u, per, before, lane);
-    const int n = pages_of(a.seqs, b), len = length_of(a.seqs, b);
-    const int hc = (int)((u - before) / n), head = hc / a.chunks, chunk = hc % a.chunks;
-    const int p0 = (int)((u - before) % n), p1 = (int)(u1 - u < n - p0 ? p0 + (u1 - u) : n);
-    const int t0 = 2 * p0 + wave, t1 = min(2 * p1, (len + kStep - 1) / kStep);        // steps
-    Queries<D, FMT, HALF> q[NQ];
-    float m[NQ], l[NQ];
-    f32x4 o[NQ][NO];
-    Keys<D, FMT> keys;
-    Values<D, FMT> vals;
-    const int seen_by_all = len - a.rows + 1;      // places that every row sees
-    const auto head_at = [&](int page) { return a.pool.pages + ((int64_t)max(page, 0) * a.pool.heads + head) * L::kHead; };
-    int page = t0 < t1 ? page_at(a.pool, a.seqs, b, t0 >> 1) : 0;
+  const List list(a.seqs, lane);
+  const int64_t units = list.total * per;
+  const Cuts cuts(units, a.nblocks);
+  const int64_t u0 = a.direct ? blockIdx.x : cuts.start(blockIdx.x);
+  const int64_t u1 = a.direct ? u0 + 1 : cuts.start(blockIdx.x + 1);
+  if (u0 >= u1) return;
+  Queries<D, FMT, HALF> q[NQ];
+  Keys<D, FMT> keys;
+  Values<D, FMT> vals;
+  int b, n, head, chunk, p0, p1, len;      // the piece: pages p0 .. p1 of the n of a head and chunk
+  int t0, t1, page;                        // the wavefront's steps, the page of the next
+  Table table(a.pool, a.seqs, lane);
+  const auto head_at = [&](int pg) { return a.pool.pages + ((int64_t)max(pg, 0) * a.pool.heads + head) * L::kHead; };
+  // finds the piece at unit u and sends for what it begins with
+  const auto begin = [&](int64_t u) {
+    int hc;
+    if (a.direct) {
+      b = blockIdx.x / per;
+      hc = blockIdx.x % per;
+      n = p1 = pages_of(a.seqs, b);
+      p0 = 0;
+    } else {
+      int64_t before;
+      b = list.at(u, per, n, before);
+      hc = (int)quotient(u - before, n);
+      p0 = (int)(u - before - (int64_t)hc * n);
+      p1 = (int)(u1 - u < n - p0 ? p0 + (u1 - u) : n);
+    }
+    head = hc / a.chunks;
+    chunk = hc % a.chunks;
+    len = length_of(a.seqs, b);
+    t0 = 2 * p0 + wave;
+    t1 = min(2 * p1, (len + kStep - 1) / kStep);
+    page = -1;
     if (t0 < t1) {
+      table.open(b, t0 >> 1);
+      page = table.page(t0 >> 1);
       load_keys(keys, head_at(page), t0 & 1, lane);
       load_values(vals, head_at(page) + L::kSide, t0 & 1, lane);
     }
 #pragma unroll
-    for (int i = 0; i < NQ; ++i) load_queries(q[i], a, b, head, (chunk * NQ + i) * 16, lane);
+    for (int i = 0; i < NQ; ++i) fetch_queries(q[i], a, b, head, (chunk * NQ + i) * 16, lane);
+  };
+  begin(u0);
+  if (n == 0) {      // only without a list: no tokens, or a length that cannot be
+    const int cols = min(a.cols - chunk * NQ * 16, NQ * 16);
+    for (int i = threadIdx.x; i < cols * D; i += kThreads) {
+      const int at = chunk * NQ * 16 + i / D;
+      a.out[b * a.os[0] + at / a.group * a.os[1] + (head * a.group + at % a.group) * a.os[2] + i % D] =
+          narrow<HALF>(len < 0 ? NAN : 0.0f);
+      if (a.lse && i % D == 0) a.lse[((int64_t)b * a.pool.heads + head) * a.cols + at] = len < 0 ? NAN : -INFINITY;
+    }
+    return;
+  }
+  for (int64_t u = u0; u < u1;) {
+    const int seen_by_all = len - a.rows + 1;      // places that every row sees
+    float m[NQ], l[NQ];
+    f32x4 o[NQ][NO];
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) widen_queries(q[i], a, (chunk * NQ + i) * 16, lane);
     bool careful = false;      // values that only some rows see are not finite: in a second pass
   again:
 #pragma unroll
@@ -414,7 +502,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv4_attend(AttendArgs a) {
         }
       }
       const int tn = t + kWaves < t1 ? t + kWaves : t;
-      const int next = page_at(a.pool, a.seqs, b, tn >> 1);
+      const int next = table.page(tn >> 1);
       load_keys(keys, head_at(next), tn & 1, lane);
       if (page < 0) {
 #pragma unroll
@@ -519,15 +607,17 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv4_attend(AttendArgs a) {
           for (int e = 0; e < 4; ++e) z = fmaf(0.0f, o[i][j][e], z);
       if (__any(z != z)) {
         careful = true;
-        page = page_at(a.pool, a.seqs, b, t0 >> 1);
+        page = table.page(t0 >> 1);
         load_keys(keys, head_at(page), t0 & 1, lane);
         load_values(vals, head_at(page) + L::kSide, t0 & 1, lane);
         goto again;
       }
     }
-    // the wavefronts' sums, tile by tile
+    // what the next piece begins with is on its way while this one's sums are joined, tile by tile
     const bool whole = p1 - p0 == n;
-    const int slot = 2 * blockIdx.x + (u != u0);
+    const int slot = 2 * blockIdx.x + (u != u0), b1 = b, head1 = head, chunk1 = chunk;
+    u += a.direct ? 1 : p1 - p0;
+    if (u < u1) begin(u);
     const float vscale = a.vs ? *a.vs : 1.0f;
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
@@ -543,13 +633,17 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv4_attend(AttendArgs a) {
       for (int w = 0; w < kWaves; ++w) mx = fmaxf(mx, red_m[w][lane & 15]);
       const float f = m[i] == -INFINITY && l[i] == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(m[i] - (mx == -INFINITY ? 0.0f : mx));
 #pragma unroll
-      for (int j = 0; j < NO; ++j)
+      for (int c = 0; c < L::C; ++c)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          // row 4 g + e of output tile (c, j): dimension VD of that lane
-          red[wave][lane & 15][j / VD * 128 + (4 * g + e) * VD + j % VD] = o[i][j][e] * f;
+#pragma unroll
+          for (int j = 0; j < VD; j += 4)
+            // row 4 g + e of the tiles (c, ..): the dimensions of lane 4 g + e
+            *reinterpret_cast<f32x4*>(&red[wave][lane & 15][c * 128 + (4 * g + e) * VD + j]) =
+                f32x4{o[i][c * VD + j][e], o[i][c * VD + j + 1][e], o[i][c * VD + j + 2][e], o[i][c * VD + j + 3][e]} * f;
       __syncthreads();
-      const int col = threadIdx.x >> 4, k = threadIdx.x & 15;
+      constexpr int N = D / 16;          // dimensions of a thread
+      const int col = threadIdx.x >> 4, d = (threadIdx.x & 15) * N;
       float mt = -INFINITY, lt = 0.0f;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) mt = fmaxf(mt, red_m[w][col]);
@@ -557,31 +651,31 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv4_attend(AttendArgs a) {
       for (int w = 0; w < kWaves; ++w)
         if (red_l[w][col] != 0.0f)
           lt += red_l[w][col] * __builtin_amdgcn_exp2f(red_m[w][col] - (mt == -INFINITY ? 0.0f : mt));
-      const int at = (chunk * NQ + i) * 16 + col;
+      const int at = (chunk1 * NQ + i) * 16 + col;
       if (at < a.cols) {
-        const int row = at / a.group, hq = head * a.group + at % a.group;
-        const float inv = lt == 0.0f ? 0.0f : vscale / lt;
+        const int row = at / a.group, hq = head1 * a.group + at % a.group;
+        f32x4 v[N / 4];
 #pragma unroll
-        for (int d = k; d < D; d += 16) {
-          float v = 0.0f;
+        for (int x = 0; x < N / 4; ++x) {
+          v[x] = *reinterpret_cast<const f32x4*>(&red[0][col][d + 4 * x]);
 #pragma unroll
-          for (int w = 0; w < kWaves; ++w) v += red[w][col][d];
-          if (whole)
-            a.out[b * a.os[0] + row * a.os[1] + hq * a.os[2] + d] = narrow<HALF>(lt == 0.0f ? 0.0f : v * inv);
-          else
-            a.part[((int64_t)slot * (16 * NQ) + i * 16 + col) * D + d] = v;
+          for (int w = 1; w < kWaves; ++w) v[x] += *reinterpret_cast<const f32x4*>(&red[w][col][d + 4 * x]);
         }
-        if (k == 0) {
-          if (!whole) {
-            a.part_ml[((int64_t)slot * (16 * NQ) + i * 16 + col) * 2] = mt;
-            a.part_ml[((int64_t)slot * (16 * NQ) + i * 16 + col) * 2 + 1] = lt;
-          } else if (a.lse) {
-            a.lse[((int64_t)b * a.pool.heads + head) * a.cols + at] = lse2_of<FMT>(mt, lt);
-          }
+        if (whole) {
+          const float inv = lt == 0.0f ? 0.0f : vscale / lt;
+          uint32_t y[N / 2];
+#pragma unroll
+          for (int x = 0; x < N / 2; ++x) y[x] = pack16(v[x / 2][x % 2 * 2] * inv, v[x / 2][x % 2 * 2 + 1] * inv, HALF);
+          __builtin_memcpy(a.out + b1 * a.os[0] + row * a.os[1] + hq * a.os[2] + d, y, sizeof y);
+          if (a.lse && d == 0) a.lse[((int64_t)b1 * a.pool.heads + head1) * a.cols + at] = lse2_of<FMT>(mt, lt);
+        } else {
+          const int64_t p = (int64_t)slot * (16 * NQ) + i * 16 + col;
+#pragma unroll
+          for (int x = 0; x < N / 4; ++x) *reinterpret_cast<f32x4*>(a.part + p * D + d + 4 * x) = v[x];
+          if (d == 0) *reinterpret_cast<f32x2*>(a.part_ml + p * 2) = f32x2{mt, lt};
         }
       }
     }
-    u += p1 - p0;
   }
 }
 
@@ -591,7 +685,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv4_attend(AttendArgs a) {
 template <int D, int FMT, bool HALF, int NQ>
 __global__ __launch_bounds__(kThreads) void k_kv4_join(AttendArgs a) {
   constexpr int T = D / 4, N = kThreads / T;       // threads of a group, groups
-  __shared__ float f_of[kBlocks];
+  __shared__ float f_of[kMaxParts];
   __shared__ __align__(16) float red[N][D];
   __shared__ float red_m[kWaves], red_l[kWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_index();
@@ -604,18 +698,18 @@ __global__ __launch_bounds__(kThreads) void k_kv4_join(AttendArgs a) {
     if (tid < D) red[0][tid] = v.x;
   } else {
     const int per = a.pool.heads * a.chunks, chunk = col / (16 * NQ);
-    int64_t pages;
-    const int64_t before = pages_before(a.seqs, b, pages, lane) * per, units = pages * per;
-    const int64_t start = before + (int64_t)(head * a.chunks + chunk) * n;
-    const int w0 = part_of(units, start, a.nblocks), w1 = part_of(units, start + n - 1, a.nblocks);
+    const List list(a.seqs, lane);
+    const int64_t units = list.total * per, start = list.before(b) * per + (int64_t)(head * a.chunks + chunk) * n;
+    const Cuts cuts(units, a.nblocks);
+    const int w0 = cuts.holds(start), w1 = cuts.holds(start + n - 1);
     if (w0 == w1) return;
     // the first part holds the piece that it ends with, the others those that they begin with
     const auto place = [&](int w) -> int64_t {
-      return (int64_t)(2 * w + (w == w0 && cut(units, w, a.nblocks) < start)) * (16 * NQ) + col % (16 * NQ);
+      return (int64_t)(2 * w + (w == w0 && cuts.start(w) < start)) * (16 * NQ) + col % (16 * NQ);
     };
     float m = -INFINITY, l = 0.0f;
     for (int w = w0 + tid; w <= w1; w += kThreads) {
-      const bool any = cut(units, w, a.nblocks) < cut(units, w + 1, a.nblocks);     // parts may be empty
+      const bool any = cuts.start(w) < cuts.start(w + 1);     // parts may be empty
       const f32x2 ml = any ? *reinterpret_cast<const f32x2*>(a.part_ml + 2 * place(w)) : f32x2{-INFINITY, 0.0f};
       m = fmaxf(m, ml.x);
     }
@@ -627,7 +721,7 @@ __global__ __launch_bounds__(kThreads) void k_kv4_join(AttendArgs a) {
     for (int w = 0; w < kWaves; ++w) m = fmaxf(m, red_m[w]);
     const float mu = m == -INFINITY ? 0.0f : m;
     for (int w = w0 + tid; w <= w1; w += kThreads) {
-      const bool any = cut(units, w, a.nblocks) < cut(units, w + 1, a.nblocks);
+      const bool any = cuts.start(w) < cuts.start(w + 1);
       const f32x2 ml = any ? *reinterpret_cast<const f32x2*>(a.part_ml + 2 * place(w)) : f32x2{-INFINITY, 0.0f};
       const float f = ml.y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(ml.x - mu);
       f_of[w - w0] = f;
@@ -679,15 +773,18 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv4_weights(AttendArgs a) {
   constexpr bool F16 = FMT == kNv;
   constexpr int W = Keys<D, FMT>::W, QP = Queries<D, FMT, HALF>::P;
   const int lane = threadIdx.x & 63, g = lane >> 4, part = blockIdx.x * kWaves + wave_index();
-  int64_t pages;
-  pages_before(a.seqs, 0, pages, lane);
-  const int64_t units = pages * a.pool.heads * 2;          // steps
-  const int64_t u0 = cut(units, part, a.nblocks * kWaves), u1 = cut(units, part + 1, a.nblocks * kWaves);
+  const List list(a.seqs, lane);
+  const int64_t units = list.total * a.pool.heads * 2;          // steps
+  const Cuts cuts(units, gridDim.x * kWaves);
+  const int64_t u0 = cuts.start(part), u1 = cuts.start(part + 1);
   for (int64_t u = u0; u < u1;) {
     int64_t before;
-    const int b = sequence_at(a.seqs, u, a.pool.heads * 2, before, lane);
-    const int n = 2 * pages_of(a.seqs, b), len = length_of(a.seqs, b), head = (int)((u - before) / n);
-    const int t0 = (int)((u - before) % n), t1 = (int)(u1 - u < n - t0 ? t0 + (u1 - u) : n);
+    int pages;
+    const int b = list.at(u, a.pool.heads * 2, pages, before), n = 2 * pages, len = length_of(a.seqs, b);
+    const int head = (int)quotient(u - before, n);
+    const int t0 = (int)(u - before - (int64_t)head * n), t1 = (int)(u1 - u < n - t0 ? t0 + (u1 - u) : n);
+    Table table(a.pool, a.seqs, lane);
+    table.open(b, t0 >> 1);
     const float* lse = a.lse + ((int64_t)b * a.pool.heads + head) * a.cols;
     const int seen_by_all = len - a.rows + 1;
     Queries<D, FMT, HALF> q[NQ];
@@ -696,23 +793,34 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv4_weights(AttendArgs a) {
 #pragma unroll
       for (int i = 0; i < NQ; ++i) {
         const int first = (chunk * NQ + i) * 16, col = first + (lane & 15);
-        load_queries(q[i], a, b, head, first, lane);
+        fetch_queries(q[i], a, b, head, first, lane);
+        widen_queries(q[i], a, first, lane);
         const float ls = col < a.cols ? lse[col] : -INFINITY;
         if (ls == -INFINITY) q[i].row = -(1 << 30);       // no such column, or one that sees nothing
         from[i] = ls == -INFINITY ? 0.0f : ls;
       }
     };
     if (a.chunks == 1) columns(0);
-    for (int t = t0; t < t1; ++t) {
-      const int page = page_at(a.pool, a.seqs, b, t >> 1);
-      if (page < 0 || t * kStep >= len) continue;
-      const int64_t unit = (int64_t)page * a.pool.heads + head;
-      Keys<D, FMT> keys;
-      load_keys(keys, a.pool.pages + unit * L::kHead, t & 1, lane);
-      // the lane's place of the step, and what it has so far
-      const int at = (lane >> 2 & 1) * 16 + 4 * g + (lane & 3);
+    // the lane's place of a step
+    const int at = (lane >> 2 & 1) * 16 + 4 * g + (lane & 3);
+    const auto unit_of = [&](int t) { return (int64_t)max(table.page(t >> 1), 0) * a.pool.heads + head; };
+    const int te = min(t1, (len + kStep - 1) / kStep);
+    Keys<D, FMT> keys, ahead;
+    float old = 0.0f, old_ahead;
+    int64_t unit = 0;
+    if (t0 < te) {
+      unit = unit_of(t0);
+      load_keys(keys, a.pool.pages + unit * L::kHead, t0 & 1, lane);
+      old = a.pool.weights[unit * kPage + (t0 & 1) * kStep + at];
+    }
+    for (int t = t0; t < te; ++t) {
+      const bool is = table.page(t >> 1) >= 0;
       float* w = a.pool.weights + unit * kPage + (t & 1) * kStep + at;
-      const float old = *w;
+      // the next step's on their way
+      const int tn = min(t + 1, te - 1);
+      unit = unit_of(tn);
+      load_keys(ahead, a.pool.pages + unit * L::kHead, tn & 1, lane);
+      old_ahead = a.pool.weights[unit * kPage + (tn & 1) * kStep + at];
       float sum[2][4] = {};
       for (int chunk = 0; chunk < a.chunks; ++chunk) {
         if (a.chunks > 1) columns(chunk);
@@ -750,7 +858,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv4_weights(AttendArgs a) {
       }
       h1 = (n3 & 1 ? h2[1] : h2[0]) + __shfl_xor(n3 & 1 ? h2[0] : h2[1], 1);
       h1 += __shfl_xor(h1, 8);
-      if ((lane & 8) == 0 && t * kStep + at < len) *w = old + h1;
+      if (is && (lane & 8) == 0 && t * kStep + at < len) *w = old + h1;
+      keys = ahead;
+      old = old_ahead;
     }
     u += t1 - t0;
   }
@@ -761,14 +871,14 @@ int tiles_of(int cols, int dim) {
   return cols <= 16 || dim == 256 ? 1 : 2;
 }
 
-int blocks_for(int64_t most_units) { return (int)(most_units < kBlocks ? most_units : kBlocks); }
-
 template <int D, int FMT, bool HALF, int NQ>
 hipError_t launch(AttendArgs a, hipStream_t st) {
   hipLaunchKernelGGL((k_kv4_attend<D, FMT, HALF, NQ>), dim3(a.nblocks), dim3(kThreads), 0, st, a);
-  const unsigned joins = (unsigned)a.seqs.n * a.pool.heads * a.cols;
-  hipLaunchKernelGGL((k_kv4_join<D, FMT, HALF, NQ>), dim3(joins), dim3(kThreads), 0, st, a);
-  if (a.lse) hipLaunchKernelGGL((k_kv4_weights<D, FMT, HALF, NQ>), dim3(a.nblocks), dim3(kThreads), 0, st, a);
+  if (!a.direct) {
+    const unsigned joins = (unsigned)a.seqs.n * a.pool.heads * a.cols;
+    hipLaunchKernelGGL((k_kv4_join<D, FMT, HALF, NQ>), dim3(joins), dim3(kThreads), 0, st, a);
+  }
+  if (a.lse) hipLaunchKernelGGL((k_kv4_weights<D, FMT, HALF, NQ>), dim3(a.weight_blocks), dim3(kThreads), 0, st, a);
   return hipGetLastError();
 }
 
@@ -784,7 +894,8 @@ sc_status check_attention(const sc_kv4_cache* cache, const sc_kv4_seqs* seqs, in
 }
 
 struct Work {
-  int nq, chunks, blocks;
+  int nq, chunks, blocks, weight_blocks;
+  bool direct;
   size_t part, ml, lse, total;
 };
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
@@ -793,11 +904,16 @@ Work work_of(const sc_kv4_cache* cache, const sc_kv4_seqs* seqs, int32_t rows, i
   const int cols = rows * (q_heads / cache->kv_heads);
   w.nq = tiles_of(cols, cache->head_dim);
   w.chunks = (cols + 16 * w.nq - 1) / (16 * w.nq);
-  w.blocks = blocks_for((int64_t)seqs->n_seqs * cache->kv_heads * w.chunks * seqs->width);
+  const int64_t heads = (int64_t)seqs->n_seqs * cache->kv_heads * w.chunks, pages = heads * seqs->width;
+  const int most = w.nq == 1 && cache->head_dim <= 128 ? 768 : 512;        // blocks that run at a time
+  w.direct = seqs->width <= kDirectPages;
+  w.blocks = (int)(w.direct ? heads : pages < most ? pages : most);
+  w.weight_blocks = (int)(pages < 512 ? pages : 512);
+  const int slots = w.direct ? 0 : 2 * w.blocks;
   w.part = 0;
-  w.ml = round256((size_t)2 * w.blocks * 16 * w.nq * cache->head_dim * 4);
-  w.lse = w.ml + round256((size_t)2 * w.blocks * 16 * w.nq * 8);
-  w.total = w.lse + (weights ? round256((size_t)seqs->n_seqs * cache->kv_heads * cols * 4) : 0);
+  w.ml = round256((size_t)slots * 16 * w.nq * cache->head_dim * 4);
+  w.lse = w.ml + round256((size_t)slots * 16 * w.nq * 8);
+  w.total = 256 + w.lse + (weights ? round256((size_t)seqs->n_seqs * cache->kv_heads * cols * 4) : 0);
   return w;
 }
 
@@ -855,6 +971,8 @@ sc_status kv4_attention(const sc_kv4_cache* cache, const sc_kv4_seqs* seqs, cons
   a.part_ml = reinterpret_cast<float*>(ws + w.ml);
   a.lse = accumulate ? reinterpret_cast<float*>(ws + w.lse) : nullptr;
   a.nblocks = w.blocks;
+  a.weight_blocks = w.weight_blocks;
+  a.direct = w.direct;
   const hipStream_t st = static_cast<hipStream_t>(stream);
   const bool half = x->type == SC_DTYPE_F16;
   const hipError_t e = by_layout(cache->head_dim, cache->format, [&](auto d, auto f) {
