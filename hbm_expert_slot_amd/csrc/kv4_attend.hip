@@ -412,8 +412,8 @@ __global__ __launch_bounds__(kThreads, NQ == 1 && D <= 128 ? 3 : 2) void k_kv4_a
   // m is the maximum that P counts from; it follows the scores once they exceed it by kSlack
   constexpr float kShift = F16 ? 14.0f : 0.0f, kSlack = F16 ? 1.875f : 8.0f;
   constexpr int kRow = D + 4;
-  __shared__ __align__(16) float red[kWaves][16][kRow];
-  __shared__ float red_m[kWaves][16], red_l[kWaves][16];
+  __shared__ __align__(16) float red[NQ][kWaves][16][kRow];
+  __shared__ f32x2 red_ml[NQ][kWaves][16];
   const int lane = threadIdx.x & 63, wave = wave_index(), g = lane >> 4;
   const int per = a.pool.heads * a.chunks;
   const List list(a.seqs, lane);
@@ -613,25 +613,17 @@ __global__ __launch_bounds__(kThreads, NQ == 1 && D <= 128 ? 3 : 2) void k_kv4_a
         goto again;
       }
     }
-    // what the next piece begins with is on its way while this one's sums are joined, tile by tile
+    // what the next piece begins with is on its way while this one's sums are joined
     const bool whole = p1 - p0 == n;
     const int slot = 2 * blockIdx.x + (u != u0), b1 = b, head1 = head, chunk1 = chunk;
     u += a.direct ? 1 : p1 - p0;
     if (u < u1) begin(u);
     const float vscale = a.vs ? *a.vs : 1.0f;
+    __syncthreads();           // the sums of the piece before have been read
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
       l[i] = sum_over_g(l[i]);
-      __syncthreads();
-      if (g == 0) {
-        red_m[wave][lane] = m[i];
-        red_l[wave][lane] = l[i];
-      }
-      __syncthreads();
-      float mx = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) mx = fmaxf(mx, red_m[w][lane & 15]);
-      const float f = m[i] == -INFINITY && l[i] == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(m[i] - (mx == -INFINITY ? 0.0f : mx));
+      if (g == 0) red_ml[i][wave][lane] = f32x2{m[i], l[i]};
 #pragma unroll
       for (int c = 0; c < L::C; ++c)
 #pragma unroll
@@ -639,41 +631,44 @@ __global__ __launch_bounds__(kThreads, NQ == 1 && D <= 128 ? 3 : 2) void k_kv4_a
 #pragma unroll
           for (int j = 0; j < VD; j += 4)
             // row 4 g + e of the tiles (c, ..): the dimensions of lane 4 g + e
-            *reinterpret_cast<f32x4*>(&red[wave][lane & 15][c * 128 + (4 * g + e) * VD + j]) =
-                f32x4{o[i][c * VD + j][e], o[i][c * VD + j + 1][e], o[i][c * VD + j + 2][e], o[i][c * VD + j + 3][e]} * f;
-      __syncthreads();
+            *reinterpret_cast<f32x4*>(&red[i][wave][lane & 15][c * 128 + (4 * g + e) * VD + j]) =
+                f32x4{o[i][c * VD + j][e], o[i][c * VD + j + 1][e], o[i][c * VD + j + 2][e], o[i][c * VD + j + 3][e]};
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
       constexpr int N = D / 16;          // dimensions of a thread
-      const int col = threadIdx.x >> 4, d = (threadIdx.x & 15) * N;
+      const int col = threadIdx.x >> 4, d = (threadIdx.x & 15) * N, at = (chunk1 * NQ + i) * 16 + col;
+      if (at >= a.cols) continue;
+      f32x2 ml[kWaves];
       float mt = -INFINITY, lt = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) mt = fmaxf(mt, red_m[w][col]);
+      for (int w = 0; w < kWaves; ++w) {
+        ml[w] = red_ml[i][w][col];
+        mt = fmaxf(mt, ml[w].x);
+      }
+      f32x4 v[N / 4] = {};
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w)
-        if (red_l[w][col] != 0.0f)
-          lt += red_l[w][col] * __builtin_amdgcn_exp2f(red_m[w][col] - (mt == -INFINITY ? 0.0f : mt));
-      const int at = (chunk1 * NQ + i) * 16 + col;
-      if (at < a.cols) {
+      for (int w = 0; w < kWaves; ++w) {
+        if (ml[w].y == 0.0f) continue;
+        const float f = __builtin_amdgcn_exp2f(ml[w].x - (mt == -INFINITY ? 0.0f : mt));
+        lt += ml[w].y * f;
+#pragma unroll
+        for (int x = 0; x < N / 4; ++x) v[x] += *reinterpret_cast<const f32x4*>(&red[i][w][col][d + 4 * x]) * f;
+      }
+      if (whole) {
         const int row = at / a.group, hq = head1 * a.group + at % a.group;
-        f32x4 v[N / 4];
+        const float inv = lt == 0.0f ? 0.0f : vscale / lt;
+        uint32_t y[N / 2];
 #pragma unroll
-        for (int x = 0; x < N / 4; ++x) {
-          v[x] = *reinterpret_cast<const f32x4*>(&red[0][col][d + 4 * x]);
+        for (int x = 0; x < N / 2; ++x) y[x] = pack16(v[x / 2][x % 2 * 2] * inv, v[x / 2][x % 2 * 2 + 1] * inv, HALF);
+        __builtin_memcpy(a.out + b1 * a.os[0] + row * a.os[1] + hq * a.os[2] + d, y, sizeof y);
+        if (a.lse && d == 0) a.lse[((int64_t)b1 * a.pool.heads + head1) * a.cols + at] = lse2_of<FMT>(mt, lt);
+      } else {
+        const int64_t p = (int64_t)slot * (16 * NQ) + i * 16 + col;
 #pragma unroll
-          for (int w = 1; w < kWaves; ++w) v[x] += *reinterpret_cast<const f32x4*>(&red[w][col][d + 4 * x]);
-        }
-        if (whole) {
-          const float inv = lt == 0.0f ? 0.0f : vscale / lt;
-          uint32_t y[N / 2];
-#pragma unroll
-          for (int x = 0; x < N / 2; ++x) y[x] = pack16(v[x / 2][x % 2 * 2] * inv, v[x / 2][x % 2 * 2 + 1] * inv, HALF);
-          __builtin_memcpy(a.out + b1 * a.os[0] + row * a.os[1] + hq * a.os[2] + d, y, sizeof y);
-          if (a.lse && d == 0) a.lse[((int64_t)b1 * a.pool.heads + head1) * a.cols + at] = lse2_of<FMT>(mt, lt);
-        } else {
-          const int64_t p = (int64_t)slot * (16 * NQ) + i * 16 + col;
-#pragma unroll
-          for (int x = 0; x < N / 4; ++x) *reinterpret_cast<f32x4*>(a.part + p * D + d + 4 * x) = v[x];
-          if (d == 0) *reinterpret_cast<f32x2*>(a.part_ml + p * 2) = f32x2{mt, lt};
-        }
+        for (int x = 0; x < N / 4; ++x) *reinterpret_cast<f32x4*>(a.part + p * D + d + 4 * x) = v[x];
+        if (d == 0) *reinterpret_cast<f32x2*>(a.part_ml + p * 2) = f32x2{mt, lt};
       }
     }
   }

@@ -24,7 +24,8 @@ struct RowArgs {
   int64_t token[2], head[2]; // strides
   int32_t tokens;
   int32_t block_tokens;
-  uint32_t per_magic;        // x / (2 heads) is the upper half of x times this
+  int32_t per;               // threads that a token's rows take
+  bool write;
 };
 
 // Sequence and place of a token of the packed rows; place -1: it is not there, -2:
@@ -50,137 +51,153 @@ __device__ __forceinline__ int place_of(const RowArgs& a, int t, int& b) {
   return p >= 0 && p < (int64_t)a.seqs.width * kPage ? (int)p : -1;
 }
 
-// Where the tokens of a block lie: found once for all of their rows.
+// Where the tokens of a block lie, found once for all of their rows: offset of the
+// page (-1: none, -2: the token belongs to no sequence), and the places of a token's
+// codes and scales in a head's keys and values.
 struct Places {
-  int page[kMaxTokens], place[kMaxTokens];
+  int64_t page[kMaxTokens];
+  uint32_t codes[2][kMaxTokens], scales[2][kMaxTokens];
 };
+template <int D, int FMT>
 __device__ __forceinline__ int find_places(const RowArgs& a, Places& p, int t0) {
-  const int n = min(a.block_tokens, a.tokens - t0);
-  if ((int)threadIdx.x < n) {
+  typedef Layout<D, FMT> L;
+  const int n = min(a.block_tokens, a.tokens - t0), i = threadIdx.x;
+  if (i < n) {
     int b;
-    const int place = place_of(a, t0 + threadIdx.x, b);
-    p.place[threadIdx.x] = place;
-    p.page[threadIdx.x] = place < 0 ? -1 : page_at(a.pool, a.seqs, b, place / kPage);
+    const int place = place_of(a, t0 + i, b), t = place & (kPage - 1);
+    const int page = place < 0 ? place : page_at(a.pool, a.seqs, b, place / kPage);
+    p.page[i] = page < 0 ? page : (int64_t)page * a.pool.heads;
+    p.codes[0][i] = L::key_codes(t, 0);
+    p.codes[1][i] = L::value_codes(t, 0, 0);
+    p.scales[0][i] = L::key_scale(t, 0);
+    p.scales[1][i] = L::value_scale(t, 0);
+    if (blockIdx.y == 0 && page >= 0 && a.pool.weights && a.write) {
+      const int at = a.given ? a.given[t0 + i] : place;
+      for (int h = 0; h < a.pool.heads; ++h) {
+        const int64_t m = (p.page[i] + h) * kPage + t;
+        a.pool.weights[m] = 0.0f;
+        a.pool.positions[m] = at;
+      }
+    }
   }
   __syncthreads();
   return n;
 }
 
-// Row r of a block's tokens: keys of all heads, then values, token after token.
-struct Row {
-  int token, side, head;
+// A thread has one piece of a token's rows (keys of all heads, then values) and goes
+// through the block's tokens with it; small rows leave threads for several tokens at
+// a time.
+struct Work {
+  int piece, side, head, first, last;      // tokens of the block
 };
-__device__ __forceinline__ Row row_of(const RowArgs& a, int r) {
-  Row w;
-  w.token = (int)__umulhi((uint32_t)r, a.per_magic);
-  const int in = r - w.token * 2 * a.pool.heads;
-  w.side = in >= a.pool.heads;
-  w.head = in - (w.side ? a.pool.heads : 0);
+template <int N>
+__device__ __forceinline__ Work work_of(const RowArgs& a, int n) {
+  Work w;
+  const int at_once = max(1, kThreads / a.per), each = (n + at_once - 1) / at_once;
+  const int mine = a.per >= kThreads ? 0 : threadIdx.x / a.per;
+  const int i = a.per >= kThreads ? blockIdx.y * kThreads + threadIdx.x : threadIdx.x - mine * a.per;
+  w.piece = i % N;
+  const int row = i / N;
+  w.side = row >= a.pool.heads;
+  w.head = row - (w.side ? a.pool.heads : 0);
+  w.first = mine * each;
+  w.last = i < a.per && mine < at_once ? min(n, w.first + each) : 0;
   return w;
 }
 
-// A thread takes 16 elements of a row at a time; the next ones are on their way
+// A thread takes 16 elements of a token at a time; the next ones are on their way
 // while it works on these.
 template <typename T, int D, int FMT>
 __global__ __launch_bounds__(kThreads) void k_kv4_append(RowArgs a) {
   typedef Layout<D, FMT> L;
-  constexpr int N = D / 16, R = kThreads / N;      // threads of a row, rows at a time
+  constexpr int N = D / 16;
   struct Raw {
     T v[16];
   };
   __shared__ Places places;
-  const int t0 = blockIdx.x * a.block_tokens, s16 = threadIdx.x % N;
-  const int rows = find_places(a, places, t0) * 2 * a.pool.heads;
-  const auto load = [&](int r) {
-    const Row w = row_of(a, min(r, rows - 1));
-    Raw x;
-    __builtin_memcpy(&x, static_cast<const T*>(a.rows[w.side]) + (t0 + w.token) * a.token[w.side] + w.head * a.head[w.side] +
-                             s16 * 16, sizeof x);
-    return x;
-  };
-  int r = threadIdx.x / N;
-  Raw raw = load(r);
-  for (; r < rows; r += R) {
-    const Raw next = load(r + R);
+  const int t0 = blockIdx.x * a.block_tokens, n = find_places<D, FMT>(a, places, t0);
+  const Work w = work_of<N>(a, n);
+  const int s16 = w.piece, sg = FMT == kNv ? s16 : s16 / 2;
+  const int64_t step = a.token[w.side];
+  const T* src = static_cast<const T*>(a.rows[w.side]) + (t0 + w.first) * step + w.head * a.head[w.side] + s16 * 16;
+  const float gs = FMT == kNv && a.gs[w.side] ? *a.gs[w.side] : 1.0f;
+  // of token 0 of a page
+  uint8_t* at0 = a.pool.pages + w.head * (int64_t)L::kHead + w.side * L::kSide;
+  const uint32_t code = w.side ? L::value_codes(0, D >= 128 ? s16 / 8 : 0, D >= 128 ? s16 % 8 * 2 : s16 * 4) : s16 * 8;
+  const uint32_t scale = w.side ? L::value_scale(0, sg) - L::value_scale(0, 0) : L::key_scale(0, sg) - L::key_scale(0, 0);
+  Raw raw = {};
+  if (w.first < w.last) __builtin_memcpy(&raw, src, sizeof raw);
+  for (int i = w.first; i < w.last; ++i) {
     float v[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) v[e] = (float)raw.v[e];
-    raw = next;
-    const Row w = row_of(a, r);
+    src += step;
+    if (i + 1 < w.last) __builtin_memcpy(&raw, src, sizeof raw);
     uint32_t sbyte;
     u32x2 codes;
-    round16<FMT>(v, FMT == kNv && a.gs[w.side] ? *a.gs[w.side] : 1.0f, sbyte, codes);
-    const int page = places.page[w.token], place = places.place[w.token];
+    round16<FMT>(v, gs, sbyte, codes);
+    const int64_t page = places.page[i];
     if (page < 0) continue;
-    const int t = place % kPage;
-    const int64_t unit = (int64_t)page * a.pool.heads + w.head;
-    uint8_t* at = a.pool.pages + unit * L::kHead + w.side * L::kSide;
-    const int sg = FMT == kNv ? s16 : s16 / 2;
-    if (FMT == kNv || (s16 & 1) == 0) at[w.side ? L::value_scale(t, sg) : L::key_scale(t, sg)] = (uint8_t)sbyte;
+    uint8_t* at = at0 + page * L::kHead;
+    if (FMT == kNv || (s16 & 1) == 0) at[scale + places.scales[w.side][i]] = (uint8_t)sbyte;
+    at += code + places.codes[w.side][i];
     if (w.side == 0) {
-      *reinterpret_cast<u32x2*>(at + L::key_codes(t, s16 * 16)) = codes;
-      if (s16 == 0 && a.pool.weights) {
-        a.pool.weights[unit * kPage + t] = 0.0f;
-        a.pool.positions[unit * kPage + t] = a.given ? a.given[t0 + w.token] : place;
-      }
+      *reinterpret_cast<u32x2*>(at) = codes;
     } else if constexpr (D >= 128) {
-      const int c = s16 / 8, ln = s16 % 8 * 2;
-      *reinterpret_cast<uint32_t*>(at + L::value_codes(t, c, ln)) = codes.x;
-      *reinterpret_cast<uint32_t*>(at + L::value_codes(t, c, ln + 1)) = codes.y;
+      *reinterpret_cast<uint32_t*>(at) = codes.x;
+      *reinterpret_cast<uint32_t*>(at + 16) = codes.y;
     } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<uint16_t*>(at + L::value_codes(t, 0, s16 * 4 + j)) = (uint16_t)(codes[j / 2] >> (j % 2 * 16));
+      for (int j = 0; j < 4; ++j) *reinterpret_cast<uint16_t*>(at + j * 8) = (uint16_t)(codes[j / 2] >> (j % 2 * 16));
     }
   }
 }
 
-// A thread writes 16 bytes of a row at a time, so that a wavefront's stores are one piece.
+// A thread writes 16 bytes of a token at a time, so that a wavefront's stores are one piece.
 template <typename T, int D, int FMT>
 __global__ __launch_bounds__(kThreads) void k_kv4_read(RowArgs a) {
   typedef Layout<D, FMT> L;
-  constexpr int E = 16 / sizeof(T), N = D / E, R = kThreads / N;
+  constexpr int E = 16 / sizeof(T), N = D / E;
   __shared__ Places places;
-  const int t0 = blockIdx.x * a.block_tokens, p = threadIdx.x % N, dim = p * E;
-  const int rows = find_places(a, places, t0) * 2 * a.pool.heads;
-#pragma unroll 2
-  for (int r = threadIdx.x / N; r < rows; r += R) {
-    const Row w = row_of(a, r);
-    const int page = places.page[w.token], place = places.place[w.token];
-    if (place == -2) continue;
+  const int t0 = blockIdx.x * a.block_tokens, n = find_places<D, FMT>(a, places, t0);
+  const Work w = work_of<N>(a, n);
+  const int dim = w.piece * E, sg = dim / L::G;
+  const int64_t step = a.token[w.side];
+  T* dst = static_cast<T*>(a.rows[w.side]) + (t0 + w.first) * step + w.head * a.head[w.side] + dim;
+  const float gs = FMT == kNv && a.gs[w.side] ? *a.gs[w.side] : 1.0f;
+  const uint8_t* at0 = a.pool.pages + w.head * (int64_t)L::kHead + w.side * L::kSide;
+  const uint32_t code = w.side ? L::value_codes(0, D >= 128 ? dim / 128 : 0, dim % (16 * L::VDims) / L::VDims) + dim % L::VDims / 2
+                               : dim / 2;
+  const uint32_t scale = w.side ? L::value_scale(0, sg) - L::value_scale(0, 0) : L::key_scale(0, sg) - L::key_scale(0, 0);
+#pragma unroll 4
+  for (int i = w.first; i < w.last; ++i, dst += step) {
+    const int64_t page = places.page[i];
+    if (page == -2) continue;
     typedef __attribute__((ext_vector_type(E))) T V;
     V out;
-    if (page < 0) {
-#pragma unroll
-      for (int e = 0; e < E; ++e) out[e] = (T)__builtin_nanf("");
-    } else {
-      const int t = place % kPage, sg = dim / L::G;
-      const uint8_t* at = a.pool.pages + ((int64_t)page * a.pool.heads + w.head) * L::kHead + w.side * L::kSide;
-      const uint32_t sb = at[w.side ? L::value_scale(t, sg) : L::key_scale(t, sg)];
-      const auto two = [&](uint32_t off) { return (uint32_t)*reinterpret_cast<const uint16_t*>(at + off); };
-      uint32_t codes;
-      if constexpr (E == 4) {
-        codes = two(w.side == 0 ? L::key_codes(t, dim) : L::value_codes(t, dim / 128, dim % 128 / L::VDims) + dim % L::VDims / 2);
-      } else if constexpr (D >= 128) {
-        codes = *reinterpret_cast<const uint32_t*>(at + (w.side == 0 ? L::key_codes(t, dim) : L::value_codes(t, dim / 128, dim % 128 / 8)));
-      } else {
-        codes = w.side == 0 ? *reinterpret_cast<const uint32_t*>(at + L::key_codes(t, dim))
-                            : two(L::value_codes(t, 0, 2 * p)) | two(L::value_codes(t, 0, 2 * p + 1)) << 16;
-      }
-      const float s = FMT == kNv ? __builtin_amdgcn_cvt_pk_f32_fp8((int)sb, false)[0] : e8m0(sb);
-      const float gs = FMT == kNv && a.gs[w.side] ? *a.gs[w.side] : 1.0f;
-#pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        const f32x2 x = e == 0   ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 0)
-                        : e == 2 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 1)
-                        : e == 4 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 2)
-                                 : __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 3);
-        // code times group scale is exact; one rounding by the scale of all
-        out[e] = (T)(x.x * s * gs);
-        out[e + 1] = (T)(x.y * s * gs);
-      }
+    const uint8_t* at = at0 + max(page, (int64_t)0) * L::kHead;
+    const uint32_t sb = at[scale + places.scales[w.side][i]];
+    at += code + places.codes[w.side][i];
+    uint32_t codes;
+    if constexpr (E == 4) {
+      codes = *reinterpret_cast<const uint16_t*>(at);
+    } else if constexpr (D >= 128) {
+      codes = *reinterpret_cast<const uint32_t*>(at);
+    } else {           // values: eight dimensions are of two lanes
+      codes = *reinterpret_cast<const uint16_t*>(at) | (uint32_t)*reinterpret_cast<const uint16_t*>(at + (w.side ? 8 : 2)) << 16;
     }
-    T* dst = static_cast<T*>(a.rows[w.side]) + (t0 + w.token) * a.token[w.side] + w.head * a.head[w.side] + dim;
+    float s = FMT == kNv ? __builtin_amdgcn_cvt_pk_f32_fp8((int)sb, false)[0] : e8m0(sb);
+    if (page < 0) s = NAN;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      const f32x2 x = e == 0   ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 0)
+                      : e == 2 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 1)
+                      : e == 4 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 2)
+                               : __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 3);
+      // code times group scale is exact; one rounding by the scale of all
+      out[e] = (T)(x.x * s * gs);
+      out[e + 1] = (T)(x.y * s * gs);
+    }
     __builtin_memcpy(dst, &out, sizeof out);
   }
 }
@@ -189,16 +206,17 @@ int type_size(int t) { return t == SC_DTYPE_F32 ? 4 : 2; }
 
 template <bool WRITE, typename T>
 hipError_t run(RowArgs a, int dim, int fmt, hipStream_t st) {
-  // a block has work for four rounds of its threads, unless that leaves compute units idle
-  const int per = 2 * a.pool.heads, threads = WRITE ? dim / 16 : dim * (int)sizeof(T) / 16;
-  const int full = (4 * kThreads / threads + per - 1) / per, even = (a.tokens + 511) / 512;
-  const int n = full < even ? full : even;
-  a.block_tokens = n < kMaxTokens ? n : kMaxTokens;
-  a.per_magic = (uint32_t)((1ull << 32) / per + 1);      // exact: rows of a block times heads are below 2^32
+  a.write = WRITE;
+  a.per = 2 * a.pool.heads * (WRITE ? dim / 16 : dim * (int)sizeof(T) / 16);
+  const int groups = (a.per + kThreads - 1) / kThreads, at_once = a.per < kThreads ? kThreads / a.per : 1;
+  // eight tokens for each thread, fewer where that leaves compute units idle
+  const int64_t even = ((int64_t)a.tokens * groups + 1023) / 1024, full = 8 * at_once;
+  const int64_t n = full < even ? full : even;
+  a.block_tokens = (int)(n < 1 ? 1 : n < kMaxTokens ? n : kMaxTokens);
   const unsigned grid = (unsigned)((a.tokens + a.block_tokens - 1) / a.block_tokens);
   return by_layout(dim, fmt, [&](auto d, auto f) {
-    if constexpr (WRITE) hipLaunchKernelGGL((k_kv4_append<T, d(), f()>), dim3(grid), dim3(kThreads), 0, st, a);
-    else hipLaunchKernelGGL((k_kv4_read<T, d(), f()>), dim3(grid), dim3(kThreads), 0, st, a);
+    if constexpr (WRITE) hipLaunchKernelGGL((k_kv4_append<T, d(), f()>), dim3(grid, groups), dim3(kThreads), 0, st, a);
+    else hipLaunchKernelGGL((k_kv4_read<T, d(), f()>), dim3(grid, groups), dim3(kThreads), 0, st, a);
     return hipGetLastError();
   });
 }
@@ -217,7 +235,9 @@ sc_status rows(const sc_kv4_cache* cache, const sc_kv4_seqs* seqs, const sc_kv4_
   if (tokens == 0 || seqs->n_seqs == 0) return SC_OK;
   if (!starts && tokens % seqs->n_seqs)
     return fail(SC_E_ARG, "%d tokens cannot be dealt out evenly to %d sequences", tokens, seqs->n_seqs);
-  if (tokens >= 1 << 24) return fail(SC_E_ARG, "too many tokens for one call");     // a launch has less than 2^32 threads
+  // a launch has less than 2^32 threads
+  if (((int64_t)tokens + 1) * (2 * cache->kv_heads * (cache->head_dim / 4) + 255) >= (int64_t)1 << 32)
+    return fail(SC_E_ARG, "too many tokens for one call");
   const int size = type_size(r->type);
   if (!r->d_k || !r->d_v || (uintptr_t)r->d_k % size || (uintptr_t)r->d_v % size)
     return fail(SC_E_ARG, "k or v is NULL or not aligned to its elements");

@@ -65,8 +65,14 @@ __global__ __launch_bounds__(kSelectThreads) void k_kv4_select(EvictArgs a) {
   const int rounds = (np + kSelectWaves - 1) / kSelectWaves, first = wave * rounds;      // pages of a wavefront
   const int mine = min(rounds, np - first);
   const bool held = rounds <= kHeld;
+  // the table's entries of the wavefront's pages are in its lanes, 64 at a time
+  int entries = 0, group = -1;
   const auto at_of = [&](int i) -> int64_t {
-    return ((int64_t)a.seqs.table[b * a.seqs.ld + first + i] * a.pool.heads + head) * kPage + lane;
+    if (i >> 6 != group) {
+      group = i >> 6;
+      entries = page_at(a.pool, a.seqs, b, first + (i & ~63) + lane);
+    }
+    return ((int64_t)__builtin_amdgcn_readlane(entries, i & 63) * a.pool.heads + head) * kPage + lane;
   };
   const auto in = [&](int i) { return (first + i) * kPage + lane < n; };
   uint32_t key[kHeld];
@@ -155,23 +161,30 @@ __global__ __launch_bounds__(kSelectThreads) void k_kv4_select(EvictArgs a) {
     return sum;
   };
   const uint64_t below = (1ull << lane) - 1;
-  int equal = 0;
-  each([&](int, bool is, uint32_t k) { equal += __popcll(__ballot(is && k == prefix)); });
-  equal = before(0, equal);
+  // larger keys and equal ones, in front of place `keep` and behind
+  int more[2] = {0, 0}, same[2] = {0, 0}, front = 0;
+  each([&](int i, bool is, uint32_t k) {
+    const uint64_t g = __ballot(is && k > prefix), e = __ballot(is && k == prefix);
+    const int left = a.keep - (first + i) * kPage;           // places in front
+    const uint64_t f = left >= 64 ? ~0ull : left > 0 ? (1ull << left) - 1 : 0;
+    more[0] += __popcll(g & f);
+    more[1] += __popcll(g & ~f);
+    same[0] += __popcll(e & f);
+    same[1] += __popcll(e & ~f);
+    front += __popcll(__ballot(is) & f);
+  });
+  const int equal = before(0, same[0] + same[1]);
   const auto places = [&](auto&& f) {                   // f(i, is, stays)
     int e = equal;
     each([&](int i, bool is, uint32_t k) {
-      const uint64_t same = __ballot(is && k == prefix);
-      f(i, is, is && (k > prefix || (k == prefix && e + __popcll(same & below) < (int)need)));
-      e += __popcll(same);
+      const uint64_t m = __ballot(is && k == prefix);
+      f(i, is, is && (k > prefix || (k == prefix && e + __popcll(m & below) < (int)need)));
+      e += __popcll(m);
     });
   };
-  int nfree = 0, nmove = 0;
-  places([&](int i, bool is, bool stays) {
-    const bool front = (first + i) * kPage + lane < a.keep;
-    nfree += __popcll(__ballot(is && front && !stays));
-    nmove += __popcll(__ballot(is && !front && stays));
-  });
+  // equal ones stay as long as there is need: front ones first
+  const int stay = max(0, min((int)need - equal, same[0] + same[1])), stay_front = min(stay, same[0]);
+  int nfree = front - more[0] - stay_front, nmove = more[1] + stay - stay_front;
   const int all = nmove;
   nfree = before(1, nfree);
   nmove = before(2, nmove);
