@@ -138,7 +138,7 @@ __device__ __forceinline__ void codes_of(const QuantArgs& a, uint64_t i, const R
   to_f32(raw, v);
   uint32_t sbyte;
   u32x2 codes;
-  round16<FMT>(v, gs, sbyte, codes);
+  round16<FMT, sizeof(T) == 2>(v, gs, sbyte, codes);
   *reinterpret_cast<u32x2*>(a.codes + i * 8) = codes;
   if constexpr (FMT == kNv) a.scales[i] = (uint8_t)sbyte;
   else if ((i & 1) == 0) a.scales[i >> 1] = (uint8_t)sbyte;

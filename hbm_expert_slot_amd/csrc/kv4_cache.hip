@@ -29,19 +29,19 @@ struct RowArgs {
 };
 
 // Sequence and place of a token of the packed rows; place -1: it is not there, -2:
-// it belongs to no sequence.
-__device__ __forceinline__ int place_of(const RowArgs& a, int t, int& b) {
+// it belongs to no sequence.  starts: a.starts, or a copy of them.
+__device__ __forceinline__ int place_of(const RowArgs& a, const int32_t* starts, int t, int& b) {
   int end;
   if (a.starts) {
     int lo = 0, hi = a.seqs.n;           // starts[lo] <= t < starts[hi]
-    if (t < a.starts[0] || t >= a.starts[hi]) return -2;
+    if (t < starts[0] || t >= starts[hi]) return -2;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (a.starts[mid] <= t) lo = mid;
+      if (starts[mid] <= t) lo = mid;
       else hi = mid;
     }
     b = lo;
-    end = a.starts[lo + 1];
+    end = starts[lo + 1];
   } else {
     const int each = a.tokens / a.seqs.n;
     b = t / each;
@@ -57,14 +57,21 @@ __device__ __forceinline__ int place_of(const RowArgs& a, int t, int& b) {
 struct Places {
   int64_t page[kMaxTokens];
   uint32_t codes[2][kMaxTokens], scales[2][kMaxTokens];
+  int32_t starts[kThreads];
 };
 template <int D, int FMT>
 __device__ __forceinline__ int find_places(const RowArgs& a, Places& p, int t0) {
   typedef Layout<D, FMT> L;
   const int n = min(a.block_tokens, a.tokens - t0), i = threadIdx.x;
+  // a search in LDS waits for memory once, not at every step
+  const bool copied = a.starts && a.seqs.n < kThreads;
+  if (copied) {
+    if (i <= a.seqs.n) p.starts[i] = a.starts[i];
+    __syncthreads();
+  }
   if (i < n) {
     int b;
-    const int place = place_of(a, t0 + i, b), t = place & (kPage - 1);
+    const int place = copied ? place_of(a, p.starts, t0 + i, b) : place_of(a, a.starts, t0 + i, b), t = place & (kPage - 1);
     const int page = place < 0 ? place : page_at(a.pool, a.seqs, b, place / kPage);
     p.page[i] = page < 0 ? page : (int64_t)page * a.pool.heads;
     p.codes[0][i] = L::key_codes(t, 0);
@@ -125,30 +132,43 @@ __global__ __launch_bounds__(kThreads) void k_kv4_append(RowArgs a) {
   uint8_t* at0 = a.pool.pages + w.head * (int64_t)L::kHead + w.side * L::kSide;
   const uint32_t code = w.side ? L::value_codes(0, D >= 128 ? s16 / 8 : 0, D >= 128 ? s16 % 8 * 2 : s16 * 4) : s16 * 8;
   const uint32_t scale = w.side ? L::value_scale(0, sg) - L::value_scale(0, 0) : L::key_scale(0, sg) - L::key_scale(0, 0);
-  Raw raw = {};
-  if (w.first < w.last) __builtin_memcpy(&raw, src, sizeof raw);
-  for (int i = w.first; i < w.last; ++i) {
-    float v[16];
+  constexpr int U = sizeof(T) == 4 ? 1 : 2;      // tokens whose loads are under way together
+  Raw raw[U];
+  const auto load = [&](int i0) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] = (float)raw.v[e];
-    src += step;
-    if (i + 1 < w.last) __builtin_memcpy(&raw, src, sizeof raw);
-    uint32_t sbyte;
-    u32x2 codes;
-    round16<FMT>(v, gs, sbyte, codes);
-    const int64_t page = places.page[i];
-    if (page < 0) continue;
-    uint8_t* at = at0 + page * L::kHead;
-    if (FMT == kNv || (s16 & 1) == 0) at[scale + places.scales[w.side][i]] = (uint8_t)sbyte;
-    at += code + places.codes[w.side][i];
-    if (w.side == 0) {
-      *reinterpret_cast<u32x2*>(at) = codes;
-    } else if constexpr (D >= 128) {
-      *reinterpret_cast<uint32_t*>(at) = codes.x;
-      *reinterpret_cast<uint32_t*>(at + 16) = codes.y;
-    } else {
+    for (int u = 0; u < U; ++u)
+      if (i0 + u < w.last) __builtin_memcpy(&raw[u], src + (i0 + u - w.first) * step, sizeof(Raw));
+  };
+  load(w.first);
+  for (int i0 = w.first; i0 < w.last; i0 += U) {
+    Raw now[U];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) *reinterpret_cast<uint16_t*>(at + j * 8) = (uint16_t)(codes[j / 2] >> (j % 2 * 16));
+    for (int u = 0; u < U; ++u) now[u] = raw[u];
+    load(i0 + U);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u;
+      if (i >= w.last) break;
+      float v[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] = (float)now[u].v[e];
+      uint32_t sbyte;
+      u32x2 codes;
+      round16<FMT, sizeof(T) == 2>(v, gs, sbyte, codes);
+      const int64_t page = places.page[i];
+      if (page < 0) continue;
+      uint8_t* at = at0 + page * L::kHead;
+      if (FMT == kNv || (s16 & 1) == 0) at[scale + places.scales[w.side][i]] = (uint8_t)sbyte;
+      at += code + places.codes[w.side][i];
+      if (w.side == 0) {
+        *reinterpret_cast<u32x2*>(at) = codes;
+      } else if constexpr (D >= 128) {
+        *reinterpret_cast<uint32_t*>(at) = codes.x;
+        *reinterpret_cast<uint32_t*>(at + 16) = codes.y;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) *reinterpret_cast<uint16_t*>(at + j * 8) = (uint16_t)(codes[j / 2] >> (j % 2 * 16));
+      }
     }
   }
 }
@@ -169,36 +189,44 @@ __global__ __launch_bounds__(kThreads) void k_kv4_read(RowArgs a) {
   const uint32_t code = w.side ? L::value_codes(0, D >= 128 ? dim / 128 : 0, dim % (16 * L::VDims) / L::VDims) + dim % L::VDims / 2
                                : dim / 2;
   const uint32_t scale = w.side ? L::value_scale(0, sg) - L::value_scale(0, 0) : L::key_scale(0, sg) - L::key_scale(0, 0);
-#pragma unroll 4
-  for (int i = w.first; i < w.last; ++i, dst += step) {
-    const int64_t page = places.page[i];
-    if (page == -2) continue;
-    typedef __attribute__((ext_vector_type(E))) T V;
-    V out;
-    const uint8_t* at = at0 + max(page, (int64_t)0) * L::kHead;
-    const uint32_t sb = at[scale + places.scales[w.side][i]];
-    at += code + places.codes[w.side][i];
-    uint32_t codes;
-    if constexpr (E == 4) {
-      codes = *reinterpret_cast<const uint16_t*>(at);
-    } else if constexpr (D >= 128) {
-      codes = *reinterpret_cast<const uint32_t*>(at);
-    } else {           // values: eight dimensions are of two lanes
-      codes = *reinterpret_cast<const uint16_t*>(at) | (uint32_t)*reinterpret_cast<const uint16_t*>(at + (w.side ? 8 : 2)) << 16;
-    }
-    float s = FMT == kNv ? __builtin_amdgcn_cvt_pk_f32_fp8((int)sb, false)[0] : e8m0(sb);
-    if (page < 0) s = NAN;
+  constexpr int U = 4;               // tokens whose loads are under way together
+  typedef __attribute__((ext_vector_type(E))) T V;
+  for (int i0 = w.first; i0 < w.last; i0 += U) {
+    int64_t page[U];
+    uint32_t codes[U], sb[U];
 #pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      const f32x2 x = e == 0   ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 0)
-                      : e == 2 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 1)
-                      : e == 4 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 2)
-                               : __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 3);
-      // code times group scale is exact; one rounding by the scale of all
-      out[e] = (T)(x.x * s * gs);
-      out[e + 1] = (T)(x.y * s * gs);
+    for (int u = 0; u < U; ++u) {
+      const int i = min(i0 + u, w.last - 1);
+      page[u] = places.page[i];
+      const uint8_t* at = at0 + max(page[u], (int64_t)0) * L::kHead;
+      sb[u] = at[scale + places.scales[w.side][i]];
+      at += code + places.codes[w.side][i];
+      if constexpr (E == 4) {
+        codes[u] = *reinterpret_cast<const uint16_t*>(at);
+      } else if constexpr (D >= 128) {
+        codes[u] = *reinterpret_cast<const uint32_t*>(at);
+      } else {           // values: eight dimensions are of two lanes
+        codes[u] = *reinterpret_cast<const uint16_t*>(at) |
+                   (uint32_t)*reinterpret_cast<const uint16_t*>(at + (w.side ? 8 : 2)) << 16;
+      }
     }
-    __builtin_memcpy(dst, &out, sizeof out);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float s = FMT == kNv ? __builtin_amdgcn_cvt_pk_f32_fp8((int)sb[u], false)[0] : e8m0(sb[u]);
+      if (page[u] < 0) s = NAN;
+      V out;
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        const f32x2 x = e == 0   ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes[u], 1.0f, 0)
+                        : e == 2 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes[u], 1.0f, 1)
+                        : e == 4 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes[u], 1.0f, 2)
+                                 : __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes[u], 1.0f, 3);
+        // code times group scale is exact; one rounding by the scale of all
+        out[e] = (T)(x.x * s * gs);
+        out[e + 1] = (T)(x.y * s * gs);
+      }
+      if (i0 + u < w.last && page[u] != -2) __builtin_memcpy(dst + (i0 + u - w.first) * step, &out, sizeof out);
+    }
   }
 }
 

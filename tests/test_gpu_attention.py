@@ -238,6 +238,44 @@ def test_append_and_read(d, hkv, fmt, dtype):
         Filled(torch, fmt, d, hkv, [130, 7], dtype, scales=(100.0, 1e-5), seed=d + 2).check_read(("fp32",))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_append_on_and_beside_borders(dtype):
+    """Every bf16 (fp16) number of a few binades against largest elements whose scale is or is not rounded: quotients
+    that are borders, and those a step beside; then scales far from 1, subnormal and largest numbers."""
+    torch = torch_cuda()
+    log("append borders", dtype)
+    dt = getattr(torch, TYPES[dtype])
+    bits = {"bf16": 7, "fp16": 10, "fp32": 10}[dtype]
+    m = np.arange(1 << bits) / (1 << bits) + 1.0
+    x = np.concatenate([m * 2.0 ** e for e in range(-4, 3)])
+    x = np.concatenate((x, -x))
+    tops = [6.0, 6.5, 7.0, 5.5, 4.25, 6.75, 15.75, 3.0 * (1 + 2.0 ** -bits), 448.0 * 6]
+    for scales in ((None, None), (0.5, 4.0), (0.037, 1.5)):
+        rows = []
+        for t in tops:
+            y = x[: len(x) // 60 * 60].reshape(-1, 60)
+            y = np.concatenate((y[:, :15], np.full((len(y), 1), t), y[:, 15:30], np.full((len(y), 1), -t), y[:, 30:45],
+                                np.full((len(y), 1), t), y[:, 45:], np.full((len(y), 1), t)), 1)
+            rows.append(y)
+        y = np.concatenate(rows)
+        if dtype == "fp32":                      # a step of fp32 beside the borders
+            y = np.concatenate((y, np.nextafter(y.astype(np.float32), np.float32(0)), np.nextafter(y.astype(np.float32), np.float32(1e9))))
+        for size in (1.0, 2.0 ** -12):
+            k = torch.tensor(y * size, dtype=torch.float64).to(dt).cuda().view(-1, 1, 64)
+            c = Filled(torch, "nvfp4", 64, 1, [k.shape[0]], dtype, scales=scales)
+            c.cache.append(k, k, c.table, c.d_lens)
+            c.k, c.v = c.held(k, 0), c.held(k, 1)
+            c.check_read(("fp32",))
+    y = np.concatenate(rows)
+    for size in (2.0 ** -14, 2.0 ** -24, 2.0 ** 4):
+        k = torch.tensor(y * size, dtype=torch.float64).to(dt).cuda().view(-1, 1, 64)
+        for fmt in ("nvfp4", "mxfp4"):
+            c = Filled(torch, fmt, 64, 1, [k.shape[0]], dtype)
+            c.cache.append(k, k, c.table, c.d_lens)
+            c.k, c.v = c.held(k, 0), c.held(k, 1)
+            c.check_read(("fp32",))
+
+
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
 def test_append_what_is_not_finite(fmt):
     torch = torch_cuda()
