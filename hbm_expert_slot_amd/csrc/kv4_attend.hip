@@ -302,19 +302,6 @@ __device__ __forceinline__ int64_t of_lane(int64_t v, int l) {
   const uint32_t lo = __builtin_amdgcn_readlane((int)v, l), hi = __builtin_amdgcn_readlane((int)(v >> 32), l);
   return (int64_t)((uint64_t)hi << 32 | lo);
 }
-// Sums over the lanes up to each; the totals of 64 sequences fit 32 bits.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ int dpp_add(int v) {
-  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
-}
-__device__ __forceinline__ int wave_scan(int v) {
-  v = dpp_add<0x111, 0xF>(v);      // from 1, 2, 4 and 8 lanes before in the row of 16
-  v = dpp_add<0x112, 0xF>(v);
-  v = dpp_add<0x114, 0xF>(v);
-  v = dpp_add<0x118, 0xF>(v);
-  v = dpp_add<0x142, 0xA>(v);      // a row's last lane to the next row, the second row's to both behind
-  return dpp_add<0x143, 0xC>(v);
-}
 struct List {
   const Seqs& s;
   int lane, own, upto;             // of the first 64 sequences: pages, and pages up to each

@@ -191,41 +191,49 @@ __global__ __launch_bounds__(kThreads) void k_kv4_read(RowArgs a) {
   const uint32_t scale = w.side ? L::value_scale(0, sg) - L::value_scale(0, 0) : L::key_scale(0, sg) - L::key_scale(0, 0);
   constexpr int U = 4;               // tokens whose loads are under way together
   typedef __attribute__((ext_vector_type(E))) T V;
-  for (int i0 = w.first; i0 < w.last; i0 += U) {
-    int64_t page[U];
+  struct Batch {
     uint32_t codes[U], sb[U];
+  };
+  const auto load = [&](Batch& x, int i0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = min(i0 + u, w.last - 1);
-      page[u] = places.page[i];
-      const uint8_t* at = at0 + max(page[u], (int64_t)0) * L::kHead;
-      sb[u] = at[scale + places.scales[w.side][i]];
+      const uint8_t* at = at0 + max(places.page[i], (int64_t)0) * L::kHead;
+      x.sb[u] = at[scale + places.scales[w.side][i]];
       at += code + places.codes[w.side][i];
       if constexpr (E == 4) {
-        codes[u] = *reinterpret_cast<const uint16_t*>(at);
+        x.codes[u] = *reinterpret_cast<const uint16_t*>(at);
       } else if constexpr (D >= 128) {
-        codes[u] = *reinterpret_cast<const uint32_t*>(at);
+        x.codes[u] = *reinterpret_cast<const uint32_t*>(at);
       } else {           // values: eight dimensions are of two lanes
-        codes[u] = *reinterpret_cast<const uint16_t*>(at) |
-                   (uint32_t)*reinterpret_cast<const uint16_t*>(at + (w.side ? 8 : 2)) << 16;
+        x.codes[u] = *reinterpret_cast<const uint16_t*>(at) |
+                     (uint32_t)*reinterpret_cast<const uint16_t*>(at + (w.side ? 8 : 2)) << 16;
       }
     }
+  };
+  if (w.first >= w.last) return;
+  Batch next;
+  load(next, w.first);
+  for (int i0 = w.first; i0 < w.last; i0 += U) {
+    const Batch x = next;
+    load(next, i0 + U);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      float s = FMT == kNv ? __builtin_amdgcn_cvt_pk_f32_fp8((int)sb[u], false)[0] : e8m0(sb[u]);
-      if (page[u] < 0) s = NAN;
+      const int64_t page = places.page[min(i0 + u, w.last - 1)];
+      float s = FMT == kNv ? __builtin_amdgcn_cvt_pk_f32_fp8((int)x.sb[u], false)[0] : e8m0(x.sb[u]);
+      if (page < 0) s = NAN;
       V out;
 #pragma unroll
       for (int e = 0; e < E; e += 2) {
-        const f32x2 x = e == 0   ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes[u], 1.0f, 0)
-                        : e == 2 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes[u], 1.0f, 1)
-                        : e == 4 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes[u], 1.0f, 2)
-                                 : __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes[u], 1.0f, 3);
+        const f32x2 y = e == 0   ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(x.codes[u], 1.0f, 0)
+                        : e == 2 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(x.codes[u], 1.0f, 1)
+                        : e == 4 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(x.codes[u], 1.0f, 2)
+                                 : __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(x.codes[u], 1.0f, 3);
         // code times group scale is exact; one rounding by the scale of all
-        out[e] = (T)(x.x * s * gs);
-        out[e + 1] = (T)(x.y * s * gs);
+        out[e] = (T)(y.x * s * gs);
+        out[e + 1] = (T)(y.y * s * gs);
       }
-      if (i0 + u < w.last && page[u] != -2) __builtin_memcpy(dst + (i0 + u - w.first) * step, &out, sizeof out);
+      if (i0 + u < w.last && page != -2) __builtin_memcpy(dst + (i0 + u - w.first) * step, &out, sizeof out);
     }
   }
 }
@@ -237,8 +245,8 @@ hipError_t run(RowArgs a, int dim, int fmt, hipStream_t st) {
   a.write = WRITE;
   a.per = 2 * a.pool.heads * (WRITE ? dim / 16 : dim * (int)sizeof(T) / 16);
   const int groups = (a.per + kThreads - 1) / kThreads, at_once = a.per < kThreads ? kThreads / a.per : 1;
-  // eight tokens for each thread, fewer where that leaves compute units idle
-  const int64_t even = ((int64_t)a.tokens * groups + 1023) / 1024, full = 8 * at_once;
+  // twelve tokens for each thread, fewer where that leaves compute units idle
+  const int64_t even = ((int64_t)a.tokens * groups + 1023) / 1024, full = 12 * at_once;
   const int64_t n = full < even ? full : even;
   a.block_tokens = (int)(n < 1 ? 1 : n < kMaxTokens ? n : kMaxTokens);
   const unsigned grid = (unsigned)((a.tokens + a.block_tokens - 1) / a.block_tokens);

@@ -41,38 +41,33 @@ __device__ __forceinline__ uint32_t order_of(float w) {
 constexpr int kHeld = 32, kBins = 2048;
 
 __global__ __launch_bounds__(kSelectThreads) void k_kv4_select(EvictArgs a) {
-  __shared__ uint32_t hist[2][kBins];      // of even and odd wavefronts
-  __shared__ int s_bad, s_top[kSelectWaves];
-  __shared__ uint32_t s_key, s_need, s_sum[kSelectWaves];
-  __shared__ int s_count[3][kSelectWaves];
+  __shared__ uint32_t hist[3][2][kBins];      // of each pass, of even and odd wavefronts
+  __shared__ int s_top[kSelectWaves], s_bad[kSelectWaves];
+  __shared__ uint32_t s_key[3], s_need[3];
+  __shared__ int s_count[6][kSelectWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_index();
   const int b = blockIdx.x / a.pool.heads, head = blockIdx.x % a.pool.heads;
   const int n = length_of(a.seqs, b), np = (n + kPage - 1) / kPage;
-  if (tid == 0) s_bad = 0;
-  __syncthreads();
-  if (n > a.keep) {
-    // a page that is none: the sequence stays as it is
-    for (int i = tid; i < np; i += kSelectThreads)
-      if (page_at(a.pool, a.seqs, b, i) < 0) s_bad = 1;
-  }
-  __syncthreads();
-  const bool leave = n <= a.keep || s_bad;
-  if (head == 0 && tid == 0) a.new_lens[b] = leave ? a.seqs.lens[b] : a.keep;
-  if (leave) {
-    if (tid == 0) a.count[blockIdx.x] = 0;
-    return;
-  }
+  const auto leave = [&]() {
+    if (tid != 0) return;
+    a.count[blockIdx.x] = 0;
+    if (head == 0) a.new_lens[b] = a.seqs.lens[b];
+  };
+  if (n <= a.keep) return leave();
   const int rounds = (np + kSelectWaves - 1) / kSelectWaves, first = wave * rounds;      // pages of a wavefront
   const int mine = min(rounds, np - first);
   const bool held = rounds <= kHeld;
   // the table's entries of the wavefront's pages are in its lanes, 64 at a time
   int entries = 0, group = -1;
+  bool bad = false;                           // a page that is none: the sequence stays as it is
   const auto at_of = [&](int i) -> int64_t {
     if (i >> 6 != group) {
       group = i >> 6;
-      entries = page_at(a.pool, a.seqs, b, first + (i & ~63) + lane);
+      const int p = (i & ~63) + lane;
+      entries = p < mine ? page_at(a.pool, a.seqs, b, first + p) : 0;
+      bad |= __any(entries < 0);
     }
-    return ((int64_t)__builtin_amdgcn_readlane(entries, i & 63) * a.pool.heads + head) * kPage + lane;
+    return ((int64_t)max(__builtin_amdgcn_readlane(entries, i & 63), 0) * a.pool.heads + head) * kPage + lane;
   };
   const auto in = [&](int i) { return (first + i) * kPage + lane < n; };
   uint32_t key[kHeld];
@@ -85,20 +80,33 @@ __global__ __launch_bounds__(kSelectThreads) void k_kv4_select(EvictArgs a) {
         pos[i] = a.pool.positions[at_of(i)];
         key[i] = __float_as_uint(a.pool.weights[at_of(i)]);
       }
+  }
+  for (int i = tid; i < 3 * 2 * kBins; i += kSelectThreads) hist[0][0][i] = 0;
+  if (held) {
 #pragma unroll
     for (int i = 0; i < kHeld; ++i)
       if (i < mine && in(i)) top = max(top, pos[i]);
   } else {
-    for (int i = 0; i < mine; ++i)
-      if (in(i)) top = max(top, a.pool.positions[at_of(i)]);
+    for (int i = 0; i < mine; ++i) {
+      const int64_t at = at_of(i);
+      if (in(i)) top = max(top, a.pool.positions[at]);
+    }
   }
 #pragma unroll
   for (int o = 32; o; o >>= 1) top = max(top, __shfl_xor(top, o));
-  if (lane == 0) s_top[wave] = top;
+  if (lane == 0) {
+    s_top[wave] = top;
+    s_bad[wave] = bad;
+  }
   __syncthreads();
+  // what each wavefront has, in its first sixteen lanes
+  const auto of_waves = [&](const int* s, int otherwise) { return lane < kSelectWaves ? s[lane] : otherwise; };
+  if (__any(of_waves(s_bad, 0) != 0)) return leave();
+  if (head == 0 && tid == 0) a.new_lens[b] = a.keep;
+  top = of_waves(s_top, INT32_MIN);
 #pragma unroll
-  for (int w = 0; w < kSelectWaves; ++w) top = max(top, s_top[w]);
-  const int64_t last = (int64_t)top - a.recent;
+  for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor(top, o));
+  const int64_t last = (int64_t)__builtin_amdgcn_readfirstlane(top) - a.recent;
   const auto key_from = [&](int p, float w) { return p < a.sinks || p > last ? 0xFFFFFFFFu : order_of(w); };
   if (held) {
 #pragma unroll
@@ -113,53 +121,43 @@ __global__ __launch_bounds__(kSelectThreads) void k_kv4_select(EvictArgs a) {
         if (i < mine) f(i, in(i), key[i]);
     } else {
       for (int i = 0; i < mine; ++i) {
+        const int64_t at = at_of(i);
         const bool is = in(i);
-        f(i, is, is ? key_from(a.pool.positions[at_of(i)], a.pool.weights[at_of(i)]) : 0u);
+        f(i, is, is ? key_from(a.pool.positions[at], a.pool.weights[at]) : 0u);
       }
     }
+  };
+  // counts of the wavefronts before this one
+  const auto before = [&](int which, int count) {
+    if (lane == 0) s_count[which][wave] = count;
+    __syncthreads();
+    const int upto = wave_scan(of_waves(s_count[which], 0));
+    return wave ? __builtin_amdgcn_readlane(upto, wave - 1) : 0;
   };
   uint32_t prefix = 0, need = (uint32_t)a.keep;       // of the tokens whose key begins with prefix
   constexpr int kShift[3] = {21, 10, 0};
 #pragma unroll
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = kShift[pass], bits = pass == 2 ? 10 : 11;
-    for (int i = tid; i < 2 * kBins; i += kSelectThreads) hist[0][i] = 0;
-    __syncthreads();
     each([&](int, bool is, uint32_t k) {
-      if (is && (pass == 0 || k >> (shift + bits) == prefix)) atomicAdd(&hist[wave & 1][k >> shift & (kBins - 1) & ((1u << bits) - 1)], 1u);
+      if (is && (pass == 0 || k >> (shift + bits) == prefix)) atomicAdd(&hist[pass][wave & 1][k >> shift & ((1u << bits) - 1)], 1u);
     });
     __syncthreads();
     // the largest bin that the tokens from the top down to it reach `need` in: a thread has two bins, descending
     const int d = kBins - 1 - 2 * tid;
-    const uint32_t c0 = hist[0][d] + hist[1][d], c1 = hist[0][d - 1] + hist[1][d - 1];
-    uint32_t upto = c0 + c1;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const uint32_t u = __shfl_up(upto, o);
-      if (lane >= o) upto += u;
-    }
-    if (lane == 63) s_sum[wave] = upto;
-    __syncthreads();
-    for (int w = 0; w < wave; ++w) upto += s_sum[w];
-    const uint32_t above = upto - c0 - c1;
+    const uint32_t c0 = hist[pass][0][d] + hist[pass][1][d], c1 = hist[pass][0][d - 1] + hist[pass][1][d - 1];
+    const int own = wave_scan((int)(c0 + c1));
+    const uint32_t upto = (uint32_t)(own + before(pass, __builtin_amdgcn_readlane(own, 63))), above = upto - c0 - c1;
     if (above < need && upto >= need) {
       const bool second = above + c0 < need;
-      s_key = prefix << bits | (uint32_t)(second ? d - 1 : d);
-      s_need = need - above - (second ? c0 : 0);
+      s_key[pass] = prefix << bits | (uint32_t)(second ? d - 1 : d);
+      s_need[pass] = need - above - (second ? c0 : 0);
     }
     __syncthreads();
-    prefix = s_key;
-    need = s_need;
-    __syncthreads();
+    prefix = s_key[pass];
+    need = s_need[pass];
   }
   // prefix is the keep-th largest key, need the number of its tokens that stay: the first ones
-  const auto before = [&](int which, int count) {       // counts of the wavefronts before this one
-    if (lane == 0) s_count[which][wave] = count;
-    __syncthreads();
-    int sum = 0;
-    for (int w = 0; w < wave; ++w) sum += s_count[which][w];
-    return sum;
-  };
   const uint64_t below = (1ull << lane) - 1;
   // larger keys and equal ones, in front of place `keep` and behind
   int more[2] = {0, 0}, same[2] = {0, 0}, front = 0;
@@ -173,7 +171,7 @@ __global__ __launch_bounds__(kSelectThreads) void k_kv4_select(EvictArgs a) {
     same[1] += __popcll(e & ~f);
     front += __popcll(__ballot(is) & f);
   });
-  const int equal = before(0, same[0] + same[1]);
+  const int equal = before(3, same[0] + same[1]);
   const auto places = [&](auto&& f) {                   // f(i, is, stays)
     int e = equal;
     each([&](int i, bool is, uint32_t k) {
@@ -186,8 +184,8 @@ __global__ __launch_bounds__(kSelectThreads) void k_kv4_select(EvictArgs a) {
   const int stay = max(0, min((int)need - equal, same[0] + same[1])), stay_front = min(stay, same[0]);
   int nfree = front - more[0] - stay_front, nmove = more[1] + stay - stay_front;
   const int all = nmove;
-  nfree = before(1, nfree);
-  nmove = before(2, nmove);
+  nfree = before(4, nfree);
+  nmove = before(5, nmove);
   if (wave == kSelectWaves - 1 && lane == 0) a.count[blockIdx.x] = min(nmove + all, a.most);
   int32_t* from = a.from + (int64_t)blockIdx.x * a.most;
   int32_t* to = a.to + (int64_t)blockIdx.x * a.most;
