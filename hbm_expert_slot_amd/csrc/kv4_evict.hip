@@ -41,7 +41,8 @@ __device__ __forceinline__ uint32_t order_of(float w) {
 constexpr int kHeld = 32, kBins = 2048;
 
 __global__ __launch_bounds__(kSelectThreads) void k_kv4_select(EvictArgs a) {
-  __shared__ uint32_t hist[3][2][kBins];      // of each pass, of even and odd wavefronts
+  // of each pass; four counters of a bin side by side, for lanes that meet in it
+  __shared__ __align__(16) uint32_t hist[3][kBins][4];
   __shared__ int s_top[kSelectWaves], s_bad[kSelectWaves];
   __shared__ uint32_t s_key[3], s_need[3];
   __shared__ int s_count[6][kSelectWaves];
@@ -81,7 +82,7 @@ __global__ __launch_bounds__(kSelectThreads) void k_kv4_select(EvictArgs a) {
         key[i] = __float_as_uint(a.pool.weights[at_of(i)]);
       }
   }
-  for (int i = tid; i < 3 * 2 * kBins; i += kSelectThreads) hist[0][0][i] = 0;
+  for (int i = tid; i < 3 * kBins; i += kSelectThreads) *reinterpret_cast<u32x4*>(hist[0][i]) = u32x4{0, 0, 0, 0};
   if (held) {
 #pragma unroll
     for (int i = 0; i < kHeld; ++i)
@@ -140,12 +141,13 @@ __global__ __launch_bounds__(kSelectThreads) void k_kv4_select(EvictArgs a) {
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = kShift[pass], bits = pass == 2 ? 10 : 11;
     each([&](int, bool is, uint32_t k) {
-      if (is && (pass == 0 || k >> (shift + bits) == prefix)) atomicAdd(&hist[pass][wave & 1][k >> shift & ((1u << bits) - 1)], 1u);
+      if (is && (pass == 0 || k >> (shift + bits) == prefix)) atomicAdd(&hist[pass][k >> shift & ((1u << bits) - 1)][lane & 3], 1u);
     });
     __syncthreads();
     // the largest bin that the tokens from the top down to it reach `need` in: a thread has two bins, descending
     const int d = kBins - 1 - 2 * tid;
-    const uint32_t c0 = hist[pass][0][d] + hist[pass][1][d], c1 = hist[pass][0][d - 1] + hist[pass][1][d - 1];
+    const u32x4 h0 = *reinterpret_cast<const u32x4*>(hist[pass][d]), h1 = *reinterpret_cast<const u32x4*>(hist[pass][d - 1]);
+    const uint32_t c0 = h0.x + h0.y + h0.z + h0.w, c1 = h1.x + h1.y + h1.z + h1.w;
     const int own = wave_scan((int)(c0 + c1));
     const uint32_t upto = (uint32_t)(own + before(pass, __builtin_amdgcn_readlane(own, 63))), above = upto - c0 - c1;
     if (above < need && upto >= need) {
