@@ -97,37 +97,53 @@ __device__ __forceinline__ u32x2 load_transposed(uint32_t at) {
   return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds*)at));
 }
 
-// A sequence's rows or keys; none where the starts make no sense.
-__device__ __forceinline__ int range_of(const int32_t* starts, int b, int all, int& first) {
-  first = starts[b];
-  const int end = starts[b + 1];
-  return first >= 0 && end >= first && end <= all ? end - first : 0;
+// A sequence's rows and keys; none where the starts make no sense.
+struct Sequence {
+  int row0, rows, key0, keys;
+};
+__device__ __forceinline__ Sequence sequence(const PromptArgs& a, int b) {
+  Sequence s = {0, 0, 0, 0};
+  if (b < a.n) {
+    s.row0 = a.starts[b];
+    s.rows = a.starts[b + 1];
+    s.key0 = a.key_starts[b];
+    s.keys = a.key_starts[b + 1];
+    s.rows = s.row0 >= 0 && s.rows >= s.row0 && s.rows <= a.rows ? s.rows - s.row0 : 0;
+    s.keys = s.key0 >= 0 && s.keys >= s.key0 && s.keys <= a.keys ? s.keys - s.key0 : 0;
+  }
+  return s;
 }
-__device__ __forceinline__ int tiles_of(const PromptArgs& a, int b) {
-  int first;
-  return b < a.n ? (range_of(a.starts, b, a.rows, first) + kRows - 1) / kRows : 0;
+// Sums over the lanes up to each.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_add(int v) {
+  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
 }
-// The sequence of tile t of all, and t within it; a.n behind the last.
-__device__ __forceinline__ int sequence_at(const PromptArgs& a, int& t, int lane) {
+__device__ __forceinline__ int wave_scan(int v) {
+  v = dpp_add<0x111, 0xF>(v);      // from 1, 2, 4 and 8 lanes before in the row of 16
+  v = dpp_add<0x112, 0xF>(v);
+  v = dpp_add<0x114, 0xF>(v);
+  v = dpp_add<0x118, 0xF>(v);
+  v = dpp_add<0x142, 0xA>(v);      // a row's last lane to the next row, the second row's to both behind
+  return dpp_add<0x143, 0xC>(v);
+}
+// The sequence of tile t of all, and t within it; false behind the last.  The lanes
+// hold 64 sequences at a time, so the one that is found needs no further load.
+__device__ __forceinline__ bool sequence_at(const PromptArgs& a, int& t, int lane, Sequence& s) {
   int sum = 0;
   for (int i = 0; i < a.n; i += 64) {
-    const int n = tiles_of(a, i + lane);
-    int upto = n;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int u = __shfl_up(upto, o);
-      if (lane >= o) upto += u;
-    }
-    upto += sum;
+    const Sequence x = sequence(a, i + lane);
+    const int n = (x.rows + kRows - 1) / kRows, upto = sum + wave_scan(n);
     const uint64_t beyond = __ballot(upto > t);
     if (beyond) {
       const int l = __builtin_ctzll(beyond);
       t -= __builtin_amdgcn_readlane(upto - n, l);
-      return i + l;
+      s = {__builtin_amdgcn_readlane(x.row0, l), __builtin_amdgcn_readlane(x.rows, l),
+           __builtin_amdgcn_readlane(x.key0, l), __builtin_amdgcn_readlane(x.keys, l)};
+      return true;
     }
     sum = __builtin_amdgcn_readlane(upto, 63);
   }
-  return a.n;
+  return false;
 }
 
 // The tile and head of a block.  Blocks are dealt out to eight XCDs in turn: heads
@@ -174,10 +190,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt(PromptArgs a) {
   const int part = PARTS ? blockIdx.y : 0;
   int head, tile;
   block_of(a, head, tile);
-  const int b = sequence_at(a, tile, lane);
-  if (b >= a.n) return;
-  int row0, key0;
-  const int rows = range_of(a.starts, b, a.rows, row0), keys = range_of(a.key_starts, b, a.keys, key0);
+  Sequence seq;
+  if (!sequence_at(a, tile, lane, seq)) return;
+  const int row0 = seq.row0, rows = seq.rows, key0 = seq.key0, keys = seq.keys;
   tile = (rows + kRows - 1) / kRows - 1 - tile;      // those with the most keys first
   const int r0 = tile * kRows + wave * 32, row = r0 + qc;
   const int ahead = keys - rows + 1;                 // keys that row 0 sees
@@ -366,10 +381,9 @@ __global__ __launch_bounds__(kThreads) void k_prompt_join(PromptArgs a) {
   const int lane = threadIdx.x & 63;
   int head, tile;
   block_of(a, head, tile);
-  const int b = sequence_at(a, tile, lane);
-  if (b >= a.n) return;
-  int row0;
-  const int rows = range_of(a.starts, b, a.rows, row0);
+  Sequence seq;
+  if (!sequence_at(a, tile, lane, seq)) return;
+  const int row0 = seq.row0, rows = seq.rows;
   for (int i = wave_index(); i < kJoinRows; i += kWaves) {
     const int row = tile * kRows + blockIdx.y * kJoinRows + i;
     if (row >= rows) return;
