@@ -464,12 +464,18 @@ sc_status check(const sc_prompt* p) {
 }
 
 // The keys are cut into parts where blocks of whole rows would leave compute units
-// idle (two blocks fit on each of 256) and every part still has two thousand keys:
+// idle (two blocks fit on each of 256), at once or because the rows with the most
+// keys take longer than an even share, and every part still has two thousand keys:
 // the parts' sums are written and read again.  1107 rows of 16 heads of 256 over
-// 16380 keys: 160 blocks 339 us, in 3 parts 157 us.
+// 13527 keys: 144 blocks 339 us, in 3 parts 155.  Longest block of 2.0 even shares: 4
+// heads of 128, 16384 rows, 375 us, in 2 parts 337; 8 heads of 256, 8192 rows, 411 and
+// 334.  Of 1.6: 16 heads of 128, 5000 rows, 126 us and 157.
 int parts_of(const sc_prompt* p) {
-  const int64_t blocks = ((int64_t)p->rows / kRows + p->n_seqs) * p->q_heads, by_units = 512 / blocks;
-  const int64_t by_keys = p->keys / p->n_seqs / SC_PROMPT_PART_KEYS, n = by_units < by_keys ? by_units : by_keys;
+  const int64_t blocks = ((int64_t)p->rows / kRows + p->n_seqs) * p->q_heads, by_keys = p->keys / p->n_seqs / SC_PROMPT_PART_KEYS;
+  // a block's keys on average, and of the last rows
+  const double most = (double)p->keys / p->n_seqs, mean = most - 0.5 * p->rows / p->n_seqs;
+  const bool uneven = 512.0 * kRows * most > 1.8 * p->q_heads * p->rows * mean;
+  const int64_t by_units = 512 / blocks > 1 ? 512 / blocks : uneven ? 2 : 1, n = by_units < by_keys ? by_units : by_keys;
   return n < 2 ? 1 : n < 8 ? (int)n : 8;
 }
 size_t part_bytes(const sc_prompt* p, int parts) { return (size_t)p->rows * p->q_heads * parts * p->head_dim * 4; }
