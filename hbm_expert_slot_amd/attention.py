@@ -98,9 +98,13 @@ def prompt_attention(q, k, v, starts, key_starts=None, scale=None, out=None, ret
             _writable(out, "out")
         lse = torch.empty((rows, heads), dtype=torch.float32, device=dev) if return_lse else None
         qs, ks, vs, os = q.stride(), k.stride(), v.stride(), out.stride()
+        # a single key has no next one, whatever stride it has
+        kt, vt = (ks[0], vs[0]) if keys > 1 else (0, 0)
+        if kt > B.SC_PROMPT_MAX_STRIDE or vt > B.SC_PROMPT_MAX_STRIDE:
+            raise ValueError("keys and values must be at most %d elements apart" % B.SC_PROMPT_MAX_STRIDE)
         p = B.PROMPT.pack(_TYPE[q.dtype], dim, heads, kv_heads, n, rows, keys, scale, q.data_ptr(), k.data_ptr(),
                           v.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(), starts.data_ptr(),
-                          key_starts.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os[0], os[1])
+                          key_starts.data_ptr(), qs[0], qs[1], kt, ks[1], vt, vs[1], os[0], os[1])
         ws = None
         if keys >= 2 * B.SC_PROMPT_PART_KEYS * n:
             need = B.prompt_attention_workspace_bytes(p)
@@ -242,7 +246,8 @@ class KV4Cache(_Fixed):
         """Attention of each sequence's last tokens over the cache: q [n, rows, heads, head_dim] (bfloat16 or
         float16; rows up to 16: a token and its drafts; heads a multiple of kv_heads; any strides but along
         head_dim).  Row r sees the places below lens - rows + r + 1; a row that sees none gets 0.  With accumulate
-        every token's weight grows by its probabilities, summed over the rows and the heads that share its keys.
+        every token's weight grows by its probabilities, summed over the rows and the heads that share its keys;
+        sequences of such a call must not share pages.
         Sequences with a length that cannot be give NaN, as do rows that see a page the cache does not have.  out,
         if given, must not overlap q (and takes no part in a gradient)."""
         if out is None and _wants_grad(q):

@@ -559,8 +559,8 @@ SC_API sc_status kv4_page_bytes(int32_t format, int32_t head_dim, size_t* bytes)
  * d_starts[b+1]-1 (NULL: tokens / n_seqs each), which are its last: the last one
  * goes to place d_lens[b] - 1.  Codes and scales follow fp4_quantize with a given
  * scale.  A cache with weights gets weight 0 and the position d_positions[token]
- * (NULL: the place).  tokens * kv_heads * head_dim < 2^32.  Tokens outside of the sequences, places that are not in the
- * table and pages outside of the cache are not written.  No two tokens of a call
+ * (NULL: the place).  tokens * kv_heads * head_dim < 2^32.  Tokens outside of the
+ * sequences, places that are not in the table and pages outside of the cache are not written.  No two tokens of a call
  * may have one place of one page.  Asynchronous on `stream`, whose device is
  * current; no workspace, no allocation; can be captured. */
 SC_API sc_status kv4_append(const sc_kv4_cache* cache, const sc_kv4_seqs* seqs, const sc_kv4_rows* rows, int32_t tokens,
@@ -594,7 +594,7 @@ SC_API sc_status kv4_attention_workspace_bytes(const sc_kv4_cache* cache, const 
  * - rows + r + 1 (its own token and those before it).  out = softmax(scale q
  * k^T) v; a row that sees nothing gets 0.  With `accumulate` every token's weight
  * grows by the sum of its probabilities over the rows and over the query heads of
- * its head.  Products are exact; sums and softmax statistics are fp32 in a fixed
+ * its head; sequences of such a call must not share pages.  Products are exact; sums and softmax statistics are fp32 in a fixed
  * order; P keeps 11 bits (NVFP4) or 16 (MXFP4).  Rows of a sequence whose length
  * cannot be are NaN, and so are rows that see a page outside of the cache.
  * d_workspace (256-byte aligned) holds nothing from one call to the next; calls

@@ -43,7 +43,7 @@ def _close(got, want, bound, dtype, what):
     assert np.array_equal(np.isnan(got), np.isnan(want)), (what, "NaN")
     assert np.array_equal(np.isinf(got), np.isinf(want)), (what, "infinities")
     ok = np.isfinite(want)
-    over = np.abs(got - want)[ok] - (bound[ok] * (1 + EPS[dtype]) + EPS[dtype] * np.abs(want[ok]) + TINY[dtype])
+    over = np.abs(got[ok] - want[ok]) - (bound[ok] * (1 + EPS[dtype]) + EPS[dtype] * np.abs(want[ok]) + TINY[dtype])
     assert over.size == 0 or over.max() <= 0, (what, float(over.max()), int(over.argmax()))
 
 
@@ -529,6 +529,91 @@ def test_attend_does_not_depend_on_the_pages_or_the_batch_beyond_rounding():
     a = c.cache.attend(q, c.table, c.d_lens)
     for _ in range(5):
         assert torch.equal(a, c.cache.attend(q, c.table, c.d_lens))
+
+
+def test_attend_with_very_many_columns():
+    """Sixteen rows of 64 query heads on one key head: chunks of columns, with the weights of all of them."""
+    torch = torch_cuda()
+    log("attend columns")
+    for fmt, d in (("nvfp4", 64), ("mxfp4", 256)):
+        c = Filled(torch, fmt, d, 1, [200, 70, 9], track=True)
+        q = _randn(torch, 5, 3, 16, 64, d).to(torch.bfloat16)
+        _, sums = _check_attend(torch, c, q, "bf16", accumulate=True)
+        for b, (w, ew) in enumerate(sums):
+            page = int(c.table[b, 0])
+            m = min(64, c.lens[b])
+            _close(c.cache.weights[page, 0, :m], w[:m, 0], ew[:m, 0] + 2.0 ** -22 * w[:m, 0], "fp32", ("weights", b))
+
+
+@pytest.mark.parametrize("n", [64, 65, 300])
+def test_many_sequences(n):
+    """More sequences than a wavefront has lanes, and than a block has threads."""
+    torch = torch_cuda()
+    log("many sequences", n)
+    rng = np.random.default_rng(n)
+    lens = [int(x) for x in rng.integers(0, 90, n)]
+    lens[n // 2] = 1500
+    c = Filled(torch, "nvfp4", 64, 1, lens, track=True, seed=n)
+    c.check_read(("bf16",))
+    q = _randn(torch, 5, n, 1, 3, 64).to(torch.bfloat16)
+    _check_attend(torch, c, q, "bf16", accumulate=True)
+    assert c.cache.evict(c.table, c.d_lens, 80, recent=3).tolist() == [min(x, 80) for x in lens]
+    T = sum(lens)
+    q, k, v = (_randn(torch, i, T, h, 64).to(torch.float16) for i, h in enumerate((2, 1, 1)))
+    _check_prompt(torch, q, k, v, lens, lens, "fp16")
+
+
+def test_a_cache_of_more_than_4_gib():
+    """Pages behind 2^32 bytes, and positions and weights of them."""
+    torch = torch_cuda()
+    log("large cache")
+    pages, lens = 62000, [100, 70]
+    cache = _ops().KV4Cache(pages, 8, 128, track=True)
+    assert cache.pages.numel() > 2 ** 32
+    table = _ints(torch, [[pages - 1, 3], [pages - 2, 30000]])
+    k, v = (_randn(torch, i, 170, 8, 128).to(torch.bfloat16) for i in range(2))
+    d_lens, starts = _ints(torch, lens), _starts(torch, lens)
+    cache.append(k, v, table, d_lens, starts)
+    small = _ops().KV4Cache(4, 8, 128, track=True)
+    table2 = _ints(torch, [[0, 1], [2, 3]])
+    small.append(k, v, table2, d_lens, starts)
+    q = _randn(torch, 7, 2, 2, 16, 128).to(torch.bfloat16)
+
+    def same():
+        for a, b in zip(cache.read(table, d_lens, 170, starts), small.read(table2, d_lens, 170, starts)):
+            assert torch.equal(a, b)
+        for a, b in ((cache.weights, small.weights), (cache.positions, small.positions)):
+            assert torch.equal(a[table.long()], b[table2.long()])
+
+    same()
+    assert torch.equal(cache.attend(q, table, d_lens, accumulate=True), small.attend(q, table2, d_lens, accumulate=True))
+    same()
+    assert torch.equal(cache.evict(table, d_lens, 60, recent=5), small.evict(table2, d_lens, 60, recent=5))
+    same()
+
+
+def test_attend_and_prompts_at_once_on_two_streams():
+    """Calls that only read the cache may run at once; each has its own workspace."""
+    torch = torch_cuda()
+    log("at once")
+    c = Filled(torch, "nvfp4", 128, 2, [3000, 2000])
+    q = [_randn(torch, i, 2, 2, 8, 128).to(torch.bfloat16) for i in range(2)]
+    want = [c.cache.attend(x, c.table, c.d_lens) for x in q]
+    pq = [_randn(torch, 9 + i, 40, 2, 128).to(torch.bfloat16) for i in range(2)]
+    pk = _randn(torch, 11, 9000, 1, 128).to(torch.bfloat16)
+    st, ks = _ints(torch, [0, 40]), _ints(torch, [0, 9000])
+    pwant = [_ops().prompt_attention(x, pk, pk, st, ks) for x in pq]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = []
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                outs.append((c.cache.attend(q[i], c.table, c.d_lens), want[i]))
+                outs.append((_ops().prompt_attention(pq[i], pk, pk, st, ks), pwant[i]))
+    torch.cuda.synchronize()
+    for got, w in outs:
+        assert torch.equal(got, w)
 
 
 # ---- eviction ----------------------------------------------------------------
