@@ -826,20 +826,15 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv4_weights(AttendArgs a) {
         }
       }
       // over the sixteen columns, halving the eight values while there are pairs: lane n ends with value n % 8
+      // (with lane n ^ 7, then n ^ 2, n ^ 1 and n ^ 8)
       const int n3 = lane & 7;
       float h4[4], h2[2], h1;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float keep = n3 & 4 ? sum[1][e] : sum[0][e], give = n3 & 4 ? sum[0][e] : sum[1][e];
-        h4[e] = keep + __shfl_xor(give, 4);
-      }
+      for (int e = 0; e < 4; ++e) h4[e] = (n3 & 4 ? sum[1][e] : sum[0][e]) + dpp<0x141>(n3 & 4 ? sum[0][e] : sum[1][e]);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float keep = n3 & 2 ? h4[2 + e] : h4[e], give = n3 & 2 ? h4[e] : h4[2 + e];
-        h2[e] = keep + __shfl_xor(give, 2);
-      }
-      h1 = (n3 & 1 ? h2[1] : h2[0]) + __shfl_xor(n3 & 1 ? h2[0] : h2[1], 1);
-      h1 += __shfl_xor(h1, 8);
+      for (int e = 0; e < 2; ++e) h2[e] = (n3 & 2 ? h4[2 + e] : h4[e]) + dpp<0x4E>(n3 & 2 ? h4[e] : h4[2 + e]);
+      h1 = (n3 & 1 ? h2[1] : h2[0]) + dpp<0xB1>(n3 & 1 ? h2[0] : h2[1]);
+      h1 += dpp<0x128>(h1);
       if (is && (lane & 8) == 0 && t * kStep + at < len) *w = old + h1;
       keys = ahead;
       old = old_ahead;
