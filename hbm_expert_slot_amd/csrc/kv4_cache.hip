@@ -190,7 +190,7 @@ __global__ __launch_bounds__(kThreads) void k_kv4_read(RowArgs a) {
                                : dim / 2;
   const uint32_t scale = w.side ? L::value_scale(0, sg) - L::value_scale(0, 0) : L::key_scale(0, sg) - L::key_scale(0, 0);
   constexpr int U = 4;               // tokens whose loads are under way together
-  typedef __attribute__((ext_vector_type(E))) T V;
+  typedef __attribute__((ext_vector_type(E), aligned(sizeof(T)))) T V;
   struct Batch {
     uint32_t codes[U], sb[U];
   };
@@ -233,7 +233,8 @@ __global__ __launch_bounds__(kThreads) void k_kv4_read(RowArgs a) {
         out[e] = (T)(y.x * s * gs);
         out[e + 1] = (T)(y.y * s * gs);
       }
-      if (i0 + u < w.last && page != -2) __builtin_memcpy(dst + (i0 + u - w.first) * step, &out, sizeof out);
+      // past the caches: what is read back is many times what was read
+      if (i0 + u < w.last && page != -2) __builtin_nontemporal_store(out, reinterpret_cast<V*>(dst + (i0 + u - w.first) * step));
     }
   }
 }
