@@ -3,6 +3,11 @@
 // Codes and scales follow the rule of fp4_quantize with a given scale: a group's
 // scale is the nearest to max / (6 scale) (NVFP4) or 2^(floor(log2 max) - 2)
 // (MXFP4), a code the nearest to the exact quotient.
+//
+// What bounds them: HBM, and for writing the vector instructions of the rounding
+// (about 100 for 16 elements).  17417 tokens of 8 heads of 128: fp16 to MXFP4 29 us (90
+// MB, 3.1 TB/s), back to fp32 in 24 us with the values written past the caches (29
+// through them).
 #include "fp4_round.h"
 #include "kv4_device.h"
 

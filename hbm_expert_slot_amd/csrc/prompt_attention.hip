@@ -9,7 +9,18 @@
 // Scores are formed transposed (keys times queries, 32x32x16 products): a lane
 // has one query's scores of the keys that it has to supply to the second product,
 // V^T times P^T, so P goes from the first product to the second in its registers.
-// V^T comes from the rows of V by LDS loads that transpose.
+// V^T comes from the rows of V by LDS loads that transpose.  P is rounded to the
+// type of v for that product, as its other operand is.
+//
+// A block has 128 rows, 32 per wavefront, and two blocks share a compute unit, so
+// that one wavefront of a SIMD can be in its softmax while the other multiplies.
+// What bounds it: the matrix units, at the clock that their power allows.  16384
+// rows of 32 heads of 128, fp16: 2.13 to 2.23 ms, 0.99 to 1.03 PFLOP/s (an 8192^3
+// bf16 library product on the same card reaches 1.22); matrix units busy in 52% of
+// the cycles at a mean clock of 1.85 GHz.  9708 packed rows of 8 sequences, 48 heads:
+// 263 us, 0.83 PFLOP/s; the rest is starting 3840 blocks and tiles on the diagonal.
+// The first kernel here (one buffer through registers, no late maxima, masks
+// everywhere) took 7.03 ms and 783 us.
 #include "fp4_device.h"
 #include "internal.h"
 
@@ -45,8 +56,8 @@ struct PromptArgs {
   int32_t n, rows, keys, heads, group;
   float scale;
   int32_t parts;            // that the keys of a block's rows are cut into
-  float* part;              // [rows][heads][parts][D] sums of the parts, with parts > 1
-  float* part_ml;           // [rows][heads][parts][2]
+  float* part;              // [blocks][parts][wavefronts][32 D] sums of the parts, with parts > 1
+  float* part_ml;           // [blocks][parts][wavefronts][32][2]
 };
 
 // The operands live until the result is there, so that it takes no register of theirs.
@@ -95,6 +106,32 @@ __device__ __forceinline__ T lds_at(uint32_t at) {
 __device__ __forceinline__ u32x2 load_transposed(uint32_t at) {
   typedef __attribute__((address_space(3))) s16x4 Lds;
   return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds*)at));
+}
+
+// A wavefront's 32 rows of sums, times the lane's inv, to rows of out: lanes exchange
+// pieces in LDS so that a store covers whole rows (9708 packed rows of 48 heads of 128,
+// 3840 blocks: 263 us; with 8 bytes per lane straight from the registers 281).
+template <int NI, bool HALF>
+__device__ __forceinline__ void write_rows(uint32_t lds, const f32x16 (&o)[NI], float inv, int lane, int rows, uint16_t* out,
+                                           int64_t stride) {
+  constexpr int CH = NI * 4, RI = 64 / CH;          // 16-byte pieces of a row, rows of a store
+  const int hi = lane >> 5, qc = lane & 31;
+  const auto piece = [](int row, int c) { return c ^ (CH >= 16 ? row & 15 : row >> 1 & 7); };
+  typedef __attribute__((address_space(3))) u32x2 Lds;
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      // dimensions 32 i + 8 e + 4 hi ..
+      *(Lds*)(lds + qc * (CH * 16) + piece(qc, i * 4 + e) * 16 + hi * 8) =
+          u32x2{pack<HALF>(o[i][e * 4] * inv, o[i][e * 4 + 1] * inv), pack<HALF>(o[i][e * 4 + 2] * inv, o[i][e * 4 + 3] * inv)};
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+  for (int it = 0; it < 32 / RI; ++it) {
+    const int row = it * RI + lane / CH, c = lane % CH;
+    const u32x4 v = lds_at<u32x4>(lds + row * (CH * 16) + piece(row, c) * 16);
+    if (row < rows) __builtin_memcpy(out + row * stride + c * 8, &v, 16);
+  }
 }
 
 // A sequence's rows and keys; none where the starts make no sense.
@@ -352,72 +389,60 @@ again:
     }
   }
   l += __shfl_xor(l, 32);
-  if (row >= rows) return;
+  if (r0 >= rows) return;
   if constexpr (PARTS) {
-    const int64_t at = ((int64_t)(row0 + row) * a.heads + head) * a.parts + part;
+    // as the lanes hold them: whole kilobytes a store, and the join's lanes read the same
+    const int64_t at = ((int64_t)blockIdx.x * a.parts + part) * kWaves + wave;
+    float* to = a.part + at * (32 * D) + lane * 4;
 #pragma unroll
     for (int i = 0; i < NO; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        *reinterpret_cast<f32x4*>(a.part + at * D + i * 32 + e * 8 + hi * 4) =
-            f32x4{o[i][e * 4], o[i][e * 4 + 1], o[i][e * 4 + 2], o[i][e * 4 + 3]};
-    if (hi == 0) *reinterpret_cast<f32x2*>(a.part_ml + at * 2) = f32x2{m - kShift, l};
+        *reinterpret_cast<f32x4*>(to + (i * 4 + e) * 256) = f32x4{o[i][e * 4], o[i][e * 4 + 1], o[i][e * 4 + 2], o[i][e * 4 + 3]};
+    if (hi == 0) *reinterpret_cast<f32x2*>(a.part_ml + (at * 32 + qc) * 2) = f32x2{m - kShift, l};
     return;
   }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  uint16_t* op = a.out + (int64_t)(row0 + row) * a.os[0] + head * a.os[1] + hi * 4;
-#pragma unroll
-  for (int i = 0; i < NO; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      // dimensions 32 i + 8 e + 4 hi ..
-      const u32x2 w = {pack<HALF>(o[i][e * 4] * inv, o[i][e * 4 + 1] * inv),
-                       pack<HALF>(o[i][e * 4 + 2] * inv, o[i][e * 4 + 3] * inv)};
-      __builtin_memcpy(op + i * 32 + e * 8, &w, 8);
-    }
-  if (a.lse && hi == 0) a.lse[(int64_t)(row0 + row) * a.heads + head] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l) - kShift) * kLn2;
+  write_rows<NO, HALF>(lds0 + wave * (32 * kRow), o, l == 0.0f ? 0.0f : 1.0f / l, lane, rows - r0,
+                       a.out + (int64_t)(row0 + r0) * a.os[0] + head * a.os[1], a.os[0]);
+  if (a.lse && hi == 0 && row < rows)
+    a.lse[(int64_t)(row0 + row) * a.heads + head] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l) - kShift) * kLn2;
 }
 
-// Joins the parts of a row and head: a wavefront at a time, D / 64 dimensions per lane.
-constexpr int kJoinRows = 16;            // of a block
+// Joins the parts of a wavefront's 32 rows, two tiles of 32 dimensions at a time.
 template <int D, bool HALF>
 __global__ __launch_bounds__(kThreads) void k_prompt_join(PromptArgs a) {
-  constexpr int N = D / 64;
-  typedef __attribute__((ext_vector_type(N))) float V;
-  const int lane = threadIdx.x & 63;
+  __shared__ __align__(1024) uint8_t lds[kWaves * 32 * 128];
+  const int lane = threadIdx.x & 63, wave = wave_index(), qc = lane & 31;
   int head, tile;
   block_of(a, head, tile);
   Sequence seq;
   if (!sequence_at(a, tile, lane, seq)) return;
-  const int row0 = seq.row0, rows = seq.rows;
-  for (int i = wave_index(); i < kJoinRows; i += kWaves) {
-    const int row = tile * kRows + blockIdx.y * kJoinRows + i;
-    if (row >= rows) return;
-    const int64_t at = ((int64_t)(row0 + row) * a.heads + head) * a.parts;
-    float m = -INFINITY, l = 0.0f;
-    V v = {};
-    for (int p = 0; p < a.parts; ++p) {
-      const f32x2 ml = *reinterpret_cast<const f32x2*>(a.part_ml + (at + p) * 2);
-      const V x = *reinterpret_cast<const V*>(a.part + (at + p) * D + lane * N);
-      if (ml.y == 0.0f) continue;
-      const float mn = fmaxf(m, ml.x), mu = mn == -INFINITY ? 0.0f : mn;
-      const float f = l == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(m - mu), fp = __builtin_amdgcn_exp2f(ml.x - mu);
-      l = l * f + ml.y * fp;
-      v = v * f + x * fp;
-      m = mn;
-    }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    uint16_t* op = a.out + (int64_t)(row0 + row) * a.os[0] + head * a.os[1] + lane * N;
-    if constexpr (N == 1) {
-      op[0] = (uint16_t)pack<HALF>(v[0] * inv, 0.0f);
-    } else {
-      uint32_t w[N / 2];
+  tile = (seq.rows + kRows - 1) / kRows - 1 - tile;      // as the blocks have them
+  const int r0 = tile * kRows + wave * 32;
+  if (r0 >= seq.rows) return;
+  float m = -INFINITY, l = 0.0f;
+  f32x16 o[2] = {};
+  for (int p = 0; p < a.parts; ++p) {
+    const int64_t at = ((int64_t)blockIdx.x * a.parts + p) * kWaves + wave;
+    const f32x2 ml = *reinterpret_cast<const f32x2*>(a.part_ml + (at * 32 + qc) * 2);
+    const float* from = a.part + at * (32 * D) + blockIdx.y * (8 * 256) + lane * 4;
+    f32x4 x[8];
 #pragma unroll
-      for (int e = 0; e < N / 2; ++e) w[e] = pack<HALF>(v[2 * e] * inv, v[2 * e + 1] * inv);
-      __builtin_memcpy(op, w, sizeof w);
-    }
-    if (a.lse && lane == 0) a.lse[(int64_t)(row0 + row) * a.heads + head] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    for (int i = 0; i < 8; ++i) x[i] = *reinterpret_cast<const f32x4*>(from + i * 256);
+    // a part that the row sees nothing of has sums of 0
+    const float mn = ml.y == 0.0f ? m : fmaxf(m, ml.x), mu = mn == -INFINITY ? 0.0f : mn;
+    const float f = l == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(m - mu), fp = ml.y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(ml.x - mu);
+    l = l * f + ml.y * fp;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i / 16][i % 16] = o[i / 16][i % 16] * f + x[i / 4][i % 4] * fp;
+    m = mn;
   }
+  const int dim = blockIdx.y * 64;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+  write_rows<2, HALF>(lds0 + wave * (32 * 128), o, l == 0.0f ? 0.0f : 1.0f / l, lane, seq.rows - r0,
+                      a.out + (int64_t)(seq.row0 + r0) * a.os[0] + head * a.os[1] + dim, a.os[0]);
+  if (a.lse && dim == 0 && lane < 32 && r0 + qc < seq.rows)
+    a.lse[(int64_t)(seq.row0 + r0 + qc) * a.heads + head] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 template <int D, bool HALF, bool DIRECT, bool PARTS>
@@ -438,7 +463,7 @@ hipError_t launch(const PromptArgs& a, hipStream_t st) {
   hipLaunchKernelGGL((k_prompt<D, HALF, DIRECT, PARTS>), dim3(grid, a.parts), dim3(kThreads), kLds, st, a);
   e = hipGetLastError();
   if (!PARTS || e != hipSuccess) return e;
-  hipLaunchKernelGGL((k_prompt_join<D, HALF>), dim3(grid, kRows / kJoinRows), dim3(kThreads), 0, st, a);
+  hipLaunchKernelGGL((k_prompt_join<D, HALF>), dim3(grid, D / 64), dim3(kThreads), 0, st, a);
   return hipGetLastError();
 }
 // Loads to LDS take 16 aligned bytes; other keys and values go through registers.
@@ -478,7 +503,10 @@ int parts_of(const sc_prompt* p) {
   const int64_t by_units = 512 / blocks > 1 ? 512 / blocks : uneven ? 2 : 1, n = by_units < by_keys ? by_units : by_keys;
   return n < 2 ? 1 : n < 8 ? (int)n : 8;
 }
-size_t part_bytes(const sc_prompt* p, int parts) { return (size_t)p->rows * p->q_heads * parts * p->head_dim * 4; }
+size_t part_rows(const sc_prompt* p, int parts) {
+  return ((size_t)p->rows / kRows + p->n_seqs) * p->q_heads * parts * kRows;
+}
+size_t part_bytes(const sc_prompt* p, int parts) { return part_rows(p, parts) * p->head_dim * 4; }
 
 }  // namespace
 }  // namespace prompt
@@ -495,7 +523,7 @@ sc_status prompt_attention_workspace_bytes(const sc_prompt* p, size_t* bytes) {
   *bytes = 0;
   if (p->n_seqs == 0 || p->rows == 0) return SC_OK;
   const int parts = prompt::parts_of(p);
-  if (parts > 1) *bytes = prompt::part_bytes(p, parts) + (size_t)p->rows * p->q_heads * parts * 8;
+  if (parts > 1) *bytes = prompt::part_bytes(p, parts) + prompt::part_rows(p, parts) * 8;
   return SC_OK;
 }
 
