@@ -9,9 +9,9 @@
 //
 // The max and the codes need one pass each; the second finds a matrix of up to
 // 256 MB in the memory-side cache.  4096 x 6144 bf16: max 10.6 us (4.7 TB/s; 19 us
-// after 1 GiB of stores, which that cache then still has to write back), codes 25
-// us (vector instructions: 32 products, 16 conversions and an fp64 quotient per 16
-// elements), reading back to fp32 17.7 us (6.5 TB/s, into that cache).
+// after 1 GiB of stores, which that cache then still has to write back), codes 24
+// us (vector instructions: 32 products and 16 conversions per 16 elements; with every
+// group scale's quotient in fp64 25 us), reading back to fp32 17.7 us (6.5 TB/s, into that cache).
 #include "fp4_device.h"
 #include "fp4_round.h"
 #include "internal.h"

@@ -8,8 +8,8 @@
 // only what has to move is moved.
 //
 // 122835 tokens of 8 sequences and 8 heads of 128, NVFP4, cut down to 12000 each: the
-// choice 39 us (64 blocks, one per sequence and head: bound by its passes over 32
-// tokens per lane and their counters in LDS), the moves 50 us (24300 tokens of each head;
+// choice 38 us (64 blocks, one per sequence and head: bound by its passes over 32
+// tokens per lane and their counters in LDS), the moves 43 us (24300 tokens of each head;
 // bound by the scattered pieces of a token, 30 MB read and 42 MB written in all).
 #include "kv4_device.h"
 
@@ -211,7 +211,7 @@ __global__ __launch_bounds__(kSelectThreads) void k_kv4_select(EvictArgs a) {
 
 // Sixteen lanes move a token: its pieces of codes, scales, weight and position.  A
 // block has 64 consecutive moves, whose tokens share lines on both sides (a wavefront
-// per token: 224 us where this takes 50; 32 or 128 moves per block: no difference).
+// per token: 224 us where this takes 43; 32 or 128 moves per block: no difference).
 constexpr int kMoves = 64;
 template <int D, int FMT>
 __global__ __launch_bounds__(256) void k_kv4_move(EvictArgs a) {

@@ -1,4 +1,4 @@
-"""Operators on 4-bit weights over torch tensors.
+"""Operators on 4-bit weights, and attention, over torch tensors.
 
 torch supplies device memory and streams; the work is done by the library's
 HIP kernels.  The operators are for inference: their results have no gradient,
