@@ -383,7 +383,17 @@ again:
     for (int i = 0; i < NO; ++i)
 #pragma unroll
       for (int e = 0; e < 16; ++e) z = fmaf(0.0f, o[i][e], z);
-    if (__syncthreads_or(z != z)) {
+    // one of the wavefronts', over LDS that the tiles have left (nothing else is in LDS, so that loads to it
+    // stay below 64 KB)
+    typedef __attribute__((address_space(3))) uint32_t Lds;
+    const bool bad = __any(z != z);
+    if (lane == 0) *(Lds*)(lds0 + wave * 4) = bad;
+    __syncthreads();
+    uint32_t any = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) any |= lds_at<uint32_t>(lds0 + w * 4);
+    __syncthreads();
+    if (__builtin_amdgcn_readfirstlane(any)) {
       careful = true;
       goto again;
     }

@@ -55,3 +55,12 @@ def test_loads_to_lds_are_waited_for(tmp_path):
         elif line.startswith("s_barrier"):
             assert not waiting, line
     assert loads > 50
+
+
+def test_kernels_that_load_to_lds_have_no_other_lds(tmp_path):
+    """The address that such a load takes has 16 bits, and the tiles have all of them."""
+    text = _assembly("prompt_attention", tmp_path)
+    kernels = re.findall(r"\.amdhsa_kernel (\S*k_promptI\S*).*?\.amdhsa_group_segment_fixed_size (\d+)", text, flags=re.S)
+    assert len(kernels) > 10
+    for name, size in kernels:
+        assert size == "0", name
