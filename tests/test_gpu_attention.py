@@ -904,3 +904,78 @@ def test_arguments_that_are_refused():
     for kw in (dict(keep=0), dict(keep=4, recent=5), dict(keep=4, recent=3, sinks=2), dict(keep=4, recent=-1)):
         with pytest.raises(ValueError):
             t.evict(table, lens, **kw)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("at", [3, 8990])
+def test_few_rows_over_many_keys_that_are_not_finite(at, d):
+    """A value of the first part, which all rows see, and one of the last, which some do not."""
+    torch = torch_cuda()
+    log("parts, not finite", at, d)
+    q, k, v = (_randn(torch, i, n, 1, d).to(torch.bfloat16) for i, n in enumerate((20, 9000, 9000)))
+    starts, keys = _ints(torch, [0, 20]), _ints(torch, [0, 9000])
+    sane = _ops().prompt_attention(q, k, v, starts, keys)
+    v[at, 0, 7] = float("inf")
+    out = _ops().prompt_attention(q, k, v, starts, keys)
+    blind = max(0, at - 8980)                   # rows before the token
+    assert torch.equal(out[:blind], sane[:blind]) and not bool(torch.isfinite(out[blind:, 0, 7]).any())
+    out[blind:, 0, 7] = sane[blind:, 0, 7]
+    assert torch.equal(out, sane)
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_prompt_values_that_are_not_finite_at_many_places(d):
+    """In both LDS buffers, at their ends too, with both ways into LDS."""
+    torch = torch_cuda()
+    log("not finite, many", d)
+    n = 300
+    x = _randn(torch, 1, n, 3 * d + 1).to(torch.float16)
+    for shift in (0, 1):                        # 16-byte aligned rows, and others
+        big = torch.zeros(n, 3 * d + 8, dtype=torch.float16, device="cuda")
+        big[:, shift:shift + 3 * d] = x[:, :3 * d]
+        q, k, v = (big[:, shift + i * d:shift + (i + 1) * d].unsqueeze(1) for i in range(3))
+        sane = _ops().prompt_attention(q, k, v, _ints(torch, [0, n])).clone()
+        for at in (0, 31, 32, 63, 64, 127, 128, 255, 256, 299):
+            keep = v[at, 0, at % d].clone()
+            v[at, 0, at % d] = float("nan")
+            out = _ops().prompt_attention(q, k, v, _ints(torch, [0, n]))
+            v[at, 0, at % d] = keep
+            assert torch.equal(out[:at], sane[:at]) and bool(torch.isnan(out[at:, 0, at % d]).all()), at
+            out[at:, 0, at % d] = sane[at:, 0, at % d]
+            assert torch.equal(out, sane), at
+
+
+def test_attend_rows_before_a_page_that_cannot_be():
+    """Of two rows only the second sees the token on a page that the cache does not have."""
+    torch = torch_cuda()
+    log("attend, bad page of the last row")
+    c = Filled(torch, "nvfp4", 64, 1, [65])
+    q = _randn(torch, 1, 1, 2, 4, 64).to(torch.bfloat16)
+    good = c.cache.attend(q, c.table, c.d_lens)
+    for bad in (-1, c.cache.n_pages, 2 ** 31 - 1):
+        table = c.table.clone()
+        table[0, 1] = bad
+        got = c.cache.attend(q, table, c.d_lens)
+        assert torch.equal(got[0, 0], good[0, 0]) and bool(torch.isnan(got[0, 1]).all())
+
+
+def test_no_sequences_and_no_tokens():
+    torch = torch_cuda()
+    log("nothing")
+    ops = _ops()
+    c = ops.KV4Cache(3, 2, 64, track=True)
+    table, lens = torch.zeros(0, 2, dtype=torch.int32, device="cuda"), torch.zeros(0, dtype=torch.int32, device="cuda")
+    q = torch.zeros(0, 1, 4, 64, dtype=torch.bfloat16, device="cuda")
+    k = torch.zeros(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    assert c.attend(q, table, lens, accumulate=True).shape == (0, 1, 4, 64)
+    c.append(k, k, table, lens)
+    assert c.read(table, lens, 0)[0].shape == (0, 2, 64) and c.evict(table, lens, 5).shape == (0,)
+    one = _ints(torch, [[0, 1]])
+    c.append(k, k, one, _ints(torch, [0]))
+    out = c.attend(torch.ones(1, 2, 4, 64, dtype=torch.bfloat16, device="cuda"), one, _ints(torch, [0]), accumulate=True)
+    assert not bool(out.any()) and c.evict(one, _ints(torch, [0]), 5).tolist() == [0]
+    zero = _ints(torch, [0])
+    assert ops.prompt_attention(k, k, k, zero).shape == (0, 2, 64)
+    rows = torch.ones(4, 2, 64, dtype=torch.bfloat16, device="cuda")
+    out, lse = ops.prompt_attention(rows, k, k, _ints(torch, [0, 4]), _ints(torch, [0, 0]), return_lse=True)
+    assert not bool(out.any()) and bool((lse == -float("inf")).all())
