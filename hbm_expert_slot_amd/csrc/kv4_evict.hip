@@ -310,6 +310,9 @@ sc_status kv4_evict(const sc_kv4_cache* cache, const sc_kv4_seqs* seqs, int32_t 
     return fail(SC_E_ARG, "recent and sinks must be >= 0 and together at most keep");
   if (seqs->n_seqs == 0) return SC_OK;
   if (!d_new_lens || (uintptr_t)d_new_lens % 4) return fail(SC_E_ARG, "new lengths are NULL or not 4-byte aligned");
+  // every head reads the lengths, one of them writes the new ones
+  const uintptr_t old = (uintptr_t)seqs->d_lens, now = (uintptr_t)d_new_lens, bytes = 4 * (uintptr_t)seqs->n_seqs;
+  if (now < old + bytes && old < now + bytes) return fail(SC_E_ARG, "new lengths must not overlap the lengths");
   if (!d_workspace || (uintptr_t)d_workspace % 4) return fail(SC_E_ARG, "workspace is NULL or not 4-byte aligned");
   EvictArgs a{};
   a.pool = pool_of(cache);

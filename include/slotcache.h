@@ -594,10 +594,10 @@ SC_API sc_status kv4_attention_workspace_bytes(const sc_kv4_cache* cache, const 
  * - rows + r + 1 (its own token and those before it).  out = softmax(scale q
  * k^T) v; a row that sees nothing gets 0.  With `accumulate` every token's weight
  * grows by the sum of its probabilities over the rows and over the query heads of
- * its head; sequences of such a call must not share pages.  Products are exact; sums and softmax statistics are fp32 in a fixed
- * order; P keeps 11 bits (NVFP4) or 16 (MXFP4).  Rows of a sequence whose length
- * cannot be are NaN, and so are rows that see a page outside of the cache (and
- * the weights that those add to).
+ * its head; sequences of such a call must not share pages.  Products are exact;
+ * sums and softmax statistics are fp32 in a fixed order; P keeps 11 bits (NVFP4)
+ * or 16 (MXFP4).  Rows of a sequence whose length cannot be are NaN, and so are
+ * rows that see a page outside of the cache (and the weights that those add to).
  * d_workspace (256-byte aligned) holds nothing from one call to the next; calls
  * that may run at once need one each.  out must not overlap q.  Asynchronous on
  * `stream`, whose device is current; no allocation; can be captured. */
@@ -617,8 +617,9 @@ SC_API sc_status kv4_evict_workspace_bytes(const sc_kv4_cache* cache, const sc_k
  * afterwards (attention does not depend on it; later calls to kv4_append should
  * give positions).  d_new_lens[b] = min(d_lens[b], keep); a sequence with a
  * length or page that cannot be stays as it is and keeps its length.  Sequences
- * that are cut must not share pages.  d_lens is only read.  Asynchronous on
- * `stream`, whose device is current; no allocation; can be captured. */
+ * that are cut must not share pages.  d_new_lens [n_seqs] must not overlap d_lens.
+ * Asynchronous on `stream`, whose device is current; no allocation; can be
+ * captured. */
 SC_API sc_status kv4_evict(const sc_kv4_cache* cache, const sc_kv4_seqs* seqs, int32_t keep, int32_t recent,
                            int32_t sinks, int32_t* d_new_lens, void* d_workspace, void* stream);
 

@@ -204,3 +204,11 @@ def test_structures_as_bytes():
             v = getattr(got, name)
             vals += list(v) if isinstance(v, ct.Array) else [v]
         assert vals == list(range(1, flat + 1))
+
+
+def test_new_lengths_over_the_lengths_are_refused():
+    """Blocks of other heads may read a length when its new one is written."""
+    c, s = R(_cache()), R(_seqs(d_lens=P, n_seqs=4))
+    for new in (P, P + 4, P + 12, P - 12):
+        _fails(B.kv4_evict, c, s, 4, 0, 0, new, P + 4096, None)
+        assert "overlap" in B.slotcache_last_error()
