@@ -18,7 +18,7 @@
 // rows of 32 heads of 128, fp16: 2.13 to 2.23 ms, 0.99 to 1.03 PFLOP/s (an 8192^3
 // bf16 library product on the same card reaches 1.22); matrix units busy in 52% of
 // the cycles at a mean clock of 1.85 GHz.  9708 packed rows of 8 sequences, 48 heads:
-// 263 us, 0.83 PFLOP/s; the rest is starting 3840 blocks and tiles on the diagonal.
+// 263 to 276 us, 0.79 to 0.83 PFLOP/s; the rest is starting 3840 blocks and tiles on the diagonal.
 // The first kernel here (one buffer through registers, no late maxima, masks
 // everywhere) took 7.03 ms and 783 us.
 #include "fp4_device.h"
