@@ -503,13 +503,21 @@ sc_status check(const sc_prompt* p) {
 // keys take longer than an even share, and every part still has two thousand keys:
 // the parts' sums are written and read again.  1107 rows of 16 heads of 256 over
 // 13527 keys: 144 blocks 339 us, in 3 parts 155.  Longest block of 2.0 even shares: 4
-// heads of 128, 16384 rows, 375 us, in 2 parts 337; 8 heads of 256, 8192 rows, 411 and
-// 334.  Of 1.6: 16 heads of 128, 5000 rows, 126 us and 157.
+// heads of 128, 16384 rows, 347 us, in 2 parts 311; 8 heads of 256, 8192 rows, 402 and
+// 303.  Of 1.6: 16 heads of 128, 5000 rows, 126 us and 157.
+//
+// Rows that see no key are no work: rows beyond the keys do not count in the shares.
+// Shares are of rows, so sequences of a few rows look uneven however many they are: 16
+// rows of 64 sequences over 2500 to 30000 keys, 32 heads, 2304 blocks, take 1347 us, in 2
+// parts 1221 (all over 6000 keys: 535 and 585); 8056 blocks 6538 and 6596.  kMostBlocks
+// ends that, and the sums' memory with it: 2 kMostBlocks blocks have at most 676 MB.
+constexpr int64_t kMostBlocks = 5 * 512;
 int parts_of(const sc_prompt* p) {
   const int64_t blocks = ((int64_t)p->rows / kRows + p->n_seqs) * p->q_heads, by_keys = p->keys / p->n_seqs / SC_PROMPT_PART_KEYS;
   // a block's keys on average, and of the last rows
-  const double most = (double)p->keys / p->n_seqs, mean = most - 0.5 * p->rows / p->n_seqs;
-  const bool uneven = 512.0 * kRows * most > 1.8 * p->q_heads * p->rows * mean;
+  const int seeing = p->rows < p->keys ? p->rows : p->keys;
+  const double most = (double)p->keys / p->n_seqs, mean = most - 0.5 * seeing / p->n_seqs;
+  const bool uneven = blocks <= kMostBlocks && 512.0 * kRows * most > 1.8 * p->q_heads * seeing * mean;
   const int64_t by_units = 512 / blocks > 1 ? 512 / blocks : uneven ? 2 : 1, n = by_units < by_keys ? by_units : by_keys;
   return n < 2 ? 1 : n < 8 ? (int)n : 8;
 }

@@ -487,8 +487,9 @@ typedef struct {
   int64_t q_stride[2], k_stride[2], v_stride[2], out_stride[2];
 } sc_prompt;
 
-/* Bytes of device workspace that prompt_attention needs: 0 but for few rows over
- * many keys (2 * SC_PROMPT_PART_KEYS per sequence and more).  Reads the sizes only. */
+/* Bytes of device workspace that prompt_attention needs: 0 but where few blocks of
+ * rows, or blocks of uneven lengths, have many keys (2 * SC_PROMPT_PART_KEYS per
+ * sequence and more), and at most 5120 * 128 * (4 * head_dim + 8).  Reads the sizes only. */
 SC_API sc_status prompt_attention_workspace_bytes(const sc_prompt* p, size_t* bytes);
 
 /* Causal attention of every row over its sequence's keys: with Lq rows and Lk

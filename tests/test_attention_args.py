@@ -212,3 +212,31 @@ def test_new_lengths_over_the_lengths_are_refused():
     for new in (P, P + 4, P + 12, P - 12):
         _fails(B.kv4_evict, c, s, 4, 0, 0, new, P + 4096, None)
         assert "overlap" in B.slotcache_last_error()
+
+
+def _workspace(**kw):
+    return B.prompt_attention_workspace_bytes(R(_prompt(**kw)))
+
+
+@pytest.mark.parametrize("rows,keys,heads,n", [(65536, 16384, 32, 1), (200000, 8192, 32, 1), (1 << 20, 8192, 8, 1),
+                                               (1 << 24, 8192, 127, 1), (1 << 24, 1 << 23, 64, 3), (16385, 16384, 16, 1)])
+def test_rows_that_see_nothing_need_no_workspace(rows, keys, heads, n):
+    """More rows than keys: the first ones are no work that could be uneven."""
+    assert _workspace(rows=rows, keys=keys, q_heads=heads, kv_heads=1, n_seqs=n) == 0
+
+
+def test_prompt_workspace_is_bounded():
+    for d in (64, 128, 256):
+        most = 0
+        for heads in (1, 2, 4, 7, 8, 16, 32, 64, 128):
+            for n in (1, 3, 16, 64, 300, 1000, 4000):
+                for rows in (1, 16, 127, 1000, 4096, 16384, 70000):
+                    for keys in (0, 4095, 4096, 10000, 100000):
+                        sizes = dict(rows=rows * n, keys=keys * n, q_heads=heads, kv_heads=1, n_seqs=n, head_dim=d)
+                        if rows * n <= 1 << 24 and (rows * n // 128 + n) * heads < 1 << 24:
+                            most = max(most, _workspace(**sizes))
+        assert 0 < most <= 5120 * 128 * (4 * d + 8)
+    # parts that were measured as a gain
+    assert _workspace(rows=16384, keys=16384, q_heads=4, kv_heads=4, n_seqs=1) == 2 * 129 * 4 * 128 * (512 + 8)
+    assert _workspace(rows=16 * 64, keys=8000 * 64, q_heads=32, kv_heads=8, n_seqs=64) > 0
+    assert _workspace(rows=1107, keys=13527, q_heads=16, kv_heads=2, n_seqs=2, head_dim=256) > 0

@@ -979,3 +979,24 @@ def test_no_sequences_and_no_tokens():
     rows = torch.ones(4, 2, 64, dtype=torch.bfloat16, device="cuda")
     out, lse = ops.prompt_attention(rows, k, k, _ints(torch, [0, 4]), _ints(torch, [0, 0]), return_lse=True)
     assert not bool(out.any()) and bool((lse == -float("inf")).all())
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("fp16", 128), ("bf16", 256)])
+@pytest.mark.parametrize("rows,keys", [(4200, 4200), (9000, 4200)])
+def test_long_prompts_in_two_parts(rows, keys, dtype, d):
+    """Eight heads of 4200 rows and more have over 256 blocks, the last of which take twice the average: their keys
+    are cut.  With fewer keys than rows the first ones see nothing."""
+    torch = torch_cuda()
+    log("prompt in two parts", rows, keys, dtype, d)
+    dt = getattr(torch, TYPES[dtype])
+    q = (2 * _randn(torch, 1, rows, 8, d)).to(dt)
+    k, v = (_randn(torch, 2 + i, keys, 1, d).to(dt) for i in range(2))
+    out, lse = _ops().prompt_attention(q, k, v, _ints(torch, [0, rows]), _ints(torch, [0, keys]), return_lse=True)
+    qn, kn, vn, blind = _np(q), _np(k), _np(v), rows - keys
+    assert not bool(out[:blind].any()) and bool((lse[:blind] == -float("inf")).all())
+    for i in (0, 1, 127, 128, 2047, 2048, 2111, 2112, 4031, 4095, 4096, 4198, 4199):
+        r = blind + i
+        o, l, _, eo, el, _ = oa.attend(qn[r:r + 1], kn[:i + 1], vn[:i + 1], 1.0 / np.sqrt(d), EPS[dtype],
+                                       2.0 ** -39 if dtype == "fp16" else 0.0)
+        _close(out[r:r + 1], o, eo, dtype, ("out", i))
+        _close(lse[r:r + 1], l, el, "fp32", ("lse", i))
