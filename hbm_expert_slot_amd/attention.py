@@ -248,8 +248,9 @@ class KV4Cache(_Fixed):
         head_dim).  Row r sees the places below lens - rows + r + 1; a row that sees none gets 0.  With accumulate
         every token's weight grows by its probabilities, summed over the rows and the heads that share its keys;
         sequences of such a call must not share pages.
-        Sequences with a length that cannot be give NaN, as do rows that see a page the cache does not have.  out,
-        if given, must not overlap q (and takes no part in a gradient)."""
+        Sequences with a length that cannot be give NaN, as do rows that see a page the cache does not have, and all
+        that see anything where k_scale is NaN, infinite or negative.  out, if given, must not overlap q (and takes
+        no part in a gradient)."""
         if out is None and _wants_grad(q):
             return _ForInference.apply("KV4Cache.attend", lambda: self.attend(
                 q, table, lens, scale, accumulate, None, stream), q)

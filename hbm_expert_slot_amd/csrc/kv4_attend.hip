@@ -273,13 +273,17 @@ __device__ __forceinline__ void widen_queries(Queries<D, FMT, HALF>& q, const At
       top = fmaxf(top, fabsf(v[w][e]));
     }
   float up = 1.0f;
-  q.factor = a.scale * kLog2e * (a.ks ? *a.ks : 1.0f);
+  q.factor = a.scale * kLog2e;
   if constexpr (FMT == kNv) {
+    const float ks = a.ks ? *a.ks : 1.0f;
+    const bool sane = ks >= 0.0f && ks < INFINITY;
+    q.factor *= sane ? ks : 1.0f;
     top = max_over_g(top);
     int e = (int)(__float_as_uint(top) >> 23) - 127;
     e = top > 0.0f && e < 128 ? max(e, -100) : 13;
     up = __uint_as_float((uint32_t)(127 + 13 - e) << 23);
     q.factor *= __uint_as_float((uint32_t)(127 + e - 13) << 23);
+    if (!sane) up = NAN;        // a scale that cannot be: NaN scores, but where the mask replaces them
   }
   q.factor = fmaxf(q.factor, 1e-37f);       // masked scores are -inf times this
 #pragma unroll

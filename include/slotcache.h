@@ -598,7 +598,8 @@ SC_API sc_status kv4_attention_workspace_bytes(const sc_kv4_cache* cache, const 
  * its head; sequences of such a call must not share pages.  Products are exact;
  * sums and softmax statistics are fp32 in a fixed order; P keeps 11 bits (NVFP4)
  * or 16 (MXFP4).  Rows of a sequence whose length cannot be are NaN, and so are
- * rows that see a page outside of the cache (and the weights that those add to).
+ * rows that see a page outside of the cache, or anything where the keys' scale is
+ * NaN, infinite or negative (and the weights that those add to).
  * d_workspace (256-byte aligned) holds nothing from one call to the next; calls
  * that may run at once need one each.  out must not overlap q.  Asynchronous on
  * `stream`, whose device is current; no allocation; can be captured. */

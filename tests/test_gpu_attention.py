@@ -1000,3 +1000,32 @@ def test_long_prompts_in_two_parts(rows, keys, dtype, d):
                                        2.0 ** -39 if dtype == "fp16" else 0.0)
         _close(out[r:r + 1], o, eo, dtype, ("out", i))
         _close(lse[r:r + 1], l, el, "fp32", ("lse", i))
+
+
+@pytest.mark.parametrize("bad", [float("nan"), -1.0, float("inf"), -float("inf")])
+@pytest.mark.parametrize("d,group,rows", [(64, 3, 2), (128, 8, 4), (256, 1, 1)])
+def test_attend_with_a_scale_of_keys_that_cannot_be(d, group, rows, bad):
+    """Every row that sees a key is NaN, and so are the weights of all that is seen; with a list of pages (the table
+    has over eight) and without."""
+    torch = torch_cuda()
+    log("attend, bad scale of keys", d, group, rows, bad)
+    for lens in ([0, 1, 70, 700], [3, 130]):
+        c = Filled(torch, "nvfp4", d, 2, lens, scales=(1.0, 2.0), track=True)
+        c.cache.k_scale.fill_(bad)
+        start = c.cache.weights.clone()
+        q = _randn(torch, 1, len(lens), rows, 2 * group, d).to(torch.bfloat16)
+        out = c.cache.attend(q, c.table, c.d_lens)
+        assert torch.equal(torch.nan_to_num(out, nan=3.0), torch.nan_to_num(c.cache.attend(
+            q, c.table, c.d_lens, accumulate=True), nan=3.0))
+        for b, n in enumerate(lens):
+            for r in range(rows):
+                if n - rows + r + 1 > 0:
+                    assert bool(torch.isnan(out[b, r]).all()), (b, r)
+                else:
+                    assert not bool(out[b, r].any()), (b, r)
+            for p in range((n + 63) // 64):
+                m = min(64, n - 64 * p)
+                page = int(c.table[b, p])
+                assert bool(torch.isnan(c.cache.weights[page, :, :m]).all()), (b, p)
+                assert torch.equal(torch.nan_to_num(c.cache.weights[page, :, m:], nan=7.0),
+                                   torch.nan_to_num(start[page, :, m:], nan=7.0))
