@@ -207,7 +207,7 @@ class KV4Cache(_Fixed):
         float16).  starts int32 [n + 1] packs the sequences' new tokens (None: tokens / n each); they are each
         sequence's last, so the last one goes to place lens - 1.  positions int32 [tokens] are kept for eviction
         (default: the places).  Places the table does not have and pages the cache does not have are not written;
-        two tokens must not have one place."""
+        two tokens must not have one place.  tokens * kv_heads * head_dim is below 2^32, here and in read."""
         seqs = self._seqs(table, lens)
         rows = self._rows(k, v, _TYPE)
         tokens = k.shape[0]

@@ -277,8 +277,9 @@ sc_status rows(const sc_kv4_cache* cache, const sc_kv4_seqs* seqs, const sc_kv4_
   if (tokens == 0 || seqs->n_seqs == 0) return SC_OK;
   if (!starts && tokens % seqs->n_seqs)
     return fail(SC_E_ARG, "%d tokens cannot be dealt out evenly to %d sequences", tokens, seqs->n_seqs);
-  // a launch has less than 2^32 threads
-  if (((int64_t)tokens + 1) * (2 * cache->kv_heads * (cache->head_dim / 4) + 255) >= (int64_t)1 << 32)
+  // a launch has less than 2^32 threads: with less than 2^32 elements per side never over 0.26 of that, as a thread
+  // has at least 8 elements of a token and a block 12 tokens (but for about 1024 blocks, where there are fewer)
+  if ((int64_t)tokens * cache->kv_heads * cache->head_dim >= (int64_t)1 << 32)
     return fail(SC_E_ARG, "too many tokens for one call");
   const int size = type_size(r->type);
   if (!r->d_k || !r->d_v || (uintptr_t)r->d_k % size || (uintptr_t)r->d_v % size)

@@ -560,9 +560,10 @@ SC_API sc_status kv4_page_bytes(int32_t format, int32_t head_dim, size_t* bytes)
  * d_starts[b+1]-1 (NULL: tokens / n_seqs each), which are its last: the last one
  * goes to place d_lens[b] - 1.  Codes and scales follow fp4_quantize with a given
  * scale.  A cache with weights gets weight 0 and the position d_positions[token]
- * (NULL: the place).  tokens * kv_heads * head_dim < 2^32.  Tokens outside of the
- * sequences, places that are not in the table and pages outside of the cache are not written.  No two tokens of a call
- * may have one place of one page.  Asynchronous on `stream`, whose device is
+ * (NULL: the place).  tokens * kv_heads * head_dim < 2^32, here and in kv4_read.
+ * Tokens outside of the sequences, places that are not in the table and pages
+ * outside of the cache are not written.  No two tokens of a call may have one place
+ * of one page.  Asynchronous on `stream`, whose device is
  * current; no workspace, no allocation; can be captured. */
 SC_API sc_status kv4_append(const sc_kv4_cache* cache, const sc_kv4_seqs* seqs, const sc_kv4_rows* rows, int32_t tokens,
                             const int32_t* d_starts, const int32_t* d_positions, void* stream);

@@ -240,3 +240,15 @@ def test_prompt_workspace_is_bounded():
     assert _workspace(rows=16384, keys=16384, q_heads=4, kv_heads=4, n_seqs=1) == 2 * 129 * 4 * 128 * (512 + 8)
     assert _workspace(rows=16 * 64, keys=8000 * 64, q_heads=32, kv_heads=8, n_seqs=64) > 0
     assert _workspace(rows=1107, keys=13527, q_heads=16, kv_heads=2, n_seqs=2, head_dim=256) > 0
+
+
+@pytest.mark.parametrize("heads,dim", [(1, 64), (1, 256), (3, 128), (8, 128), (1024, 256)])
+def test_the_most_tokens_of_a_call(heads, dim):
+    """tokens * kv_heads * head_dim < 2^32, and no less.  Keys that are NULL are what is wrong with a call that is
+    not too large."""
+    c, s, r = R(_cache(kv_heads=heads, head_dim=dim)), R(_seqs(n_seqs=1)), R(_rows(d_k=None))
+    most = (2 ** 32 - 1) // (heads * dim)
+    for tokens, what in ((most, "NULL"), (most + 1, "too many tokens")):
+        for f, args in ((B.kv4_append, (P, None, None)), (B.kv4_read, (P, None))):
+            with pytest.raises(B.SlotCacheError, match=what):
+                f(c, s, r, tokens, *args)

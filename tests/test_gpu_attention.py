@@ -1029,3 +1029,23 @@ def test_attend_with_a_scale_of_keys_that_cannot_be(d, group, rows, bad):
                 assert bool(torch.isnan(c.cache.weights[page, :, :m]).all()), (b, p)
                 assert torch.equal(torch.nan_to_num(c.cache.weights[page, :, m:], nan=7.0),
                                    torch.nan_to_num(start[page, :, m:], nan=7.0))
+
+
+def test_append_of_very_many_tokens():
+    """One head, 15.1 million tokens: the first, some and the last ones, and nothing behind them."""
+    torch = torch_cuda()
+    log("many tokens")
+    n, d = 15_100_001, 64
+    k = _randn(torch, 1, n, 1, d).to(torch.bfloat16)
+    pages = (n + 63) // 64
+    cache = _ops().KV4Cache(pages + 1, 1, d, "mxfp4")
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").unsqueeze(0)
+    cache.append(k, k, table, _ints(torch, [n]))
+    assert not bool(cache.pages[pages].any())
+    whole = cache.read(table, _ints(torch, [n]), n)
+    for at in (0, 1, 4095, 2 ** 23, n // 2, 14_961_000, n - 70):
+        m = min(70, n - at)
+        want = torch.tensor(oa.quantized(_np(k[at:at + m]), "mxfp4")).float().to(torch.bfloat16)
+        for got in whole + cache.read(table, _ints(torch, [at + m]), m):
+            got = got[at:at + m] if got.shape[0] == n else got
+            assert torch.equal(got.cpu(), want), at
