@@ -244,8 +244,8 @@ class KV4Cache(_Fixed):
 
     def attend(self, q, table, lens, scale=None, accumulate=False, out=None, stream=None):
         """Attention of each sequence's last tokens over the cache: q [n, rows, heads, head_dim] (bfloat16 or
-        float16; rows up to 16: a token and its drafts; heads a multiple of kv_heads; any strides but along
-        head_dim).  Row r sees the places below lens - rows + r + 1; a row that sees none gets 0.  With accumulate
+        float16; rows up to 16: a token and its drafts; heads a multiple of kv_heads; n * rows * heads up to 2^23;
+        any strides but along head_dim).  Row r sees the places below lens - rows + r + 1; a row that sees none gets 0.  With accumulate
         every token's weight grows by its probabilities, summed over the rows and the heads that share its keys;
         sequences of such a call must not share pages.
         Sequences with a length that cannot be give NaN, as do rows that see a page the cache does not have, and all
@@ -298,7 +298,7 @@ class KV4Cache(_Fixed):
         others, then those with the largest weights, equal ones by place.  They keep their places below keep, or move
         into those that became free, so a sequence's tokens are not in order afterwards: give append positions from
         then on.  Sequences that are cut must not share pages; one with a length or page that cannot be stays as it
-        is."""
+        is.  A call takes up to 2^17 sequences times kv_heads."""
         _need(self.weights is not None, "the cache keeps no weights")
         seqs = self._seqs(table, lens)
         _need(keep >= 1 and recent >= 0 and sinks >= 0 and recent + sinks <= keep,

@@ -593,8 +593,8 @@ SC_API sc_status kv4_attention_workspace_bytes(const sc_kv4_cache* cache, const 
                                                int32_t q_heads, int32_t accumulate, size_t* bytes);
 
 /* Attention over the cache: row r of sequence b sees the places below d_lens[b]
- * - rows + r + 1 (its own token and those before it).  out = softmax(scale q
- * k^T) v; a row that sees nothing gets 0.  With `accumulate` every token's weight
+ * - rows + r + 1 (its own token and those before it).  n_seqs * rows * q_heads <=
+ * 2^23.  out = softmax(scale q k^T) v; a row that sees nothing gets 0.  With `accumulate` every token's weight
  * grows by the sum of its probabilities over the rows and over the query heads of
  * its head; sequences of such a call must not share pages.  Products are exact;
  * sums and softmax statistics are fp32 in a fixed order; P keeps 11 bits (NVFP4)
@@ -620,7 +620,9 @@ SC_API sc_status kv4_evict_workspace_bytes(const sc_kv4_cache* cache, const sc_k
  * afterwards (attention does not depend on it; later calls to kv4_append should
  * give positions).  d_new_lens[b] = min(d_lens[b], keep); a sequence with a
  * length or page that cannot be stays as it is and keeps its length.  Sequences
- * that are cut must not share pages.  d_new_lens [n_seqs] must not overlap d_lens.
+ * that are cut must not share pages.  n_seqs * kv_heads <= 2^17.  d_new_lens [n_seqs]
+ * must not overlap d_lens.  d_workspace (4-byte aligned) holds nothing from one call
+ * to the next; calls that may run at once need one each.
  * Asynchronous on `stream`, whose device is current; no allocation; can be
  * captured. */
 SC_API sc_status kv4_evict(const sc_kv4_cache* cache, const sc_kv4_seqs* seqs, int32_t keep, int32_t recent,

@@ -252,3 +252,20 @@ def test_the_most_tokens_of_a_call(heads, dim):
         for f, args in ((B.kv4_append, (P, None, None)), (B.kv4_read, (P, None))):
             with pytest.raises(B.SlotCacheError, match=what):
                 f(c, s, r, tokens, *args)
+
+
+def test_the_most_query_rows_of_a_call():
+    c = R(_cache(kv_heads=8))
+    for n, rows, heads in ((65536, 16, 8), (65536, 2, 64), (16384, 1, 512)):
+        assert B.kv4_attention_workspace_bytes(c, R(_seqs(n_seqs=n)), rows, heads, 1) > 0
+    for n, rows, heads in ((65536, 16, 16), (65536, 3, 64), (16385, 1, 512)):
+        _fails(B.kv4_attention_workspace_bytes, c, R(_seqs(n_seqs=n)), rows, heads, 1)
+        _fails(B.kv4_attention, c, R(_seqs(n_seqs=n)), R(_query(rows=rows, q_heads=heads)), 0, P, None)
+
+
+def test_the_most_sequences_of_an_eviction():
+    for n, heads in ((65536, 2), (16384, 8), (128, 1024)):
+        assert B.kv4_evict_workspace_bytes(R(_cache(kv_heads=heads)), R(_seqs(n_seqs=n)), 10) > 0
+    for n, heads in ((65536, 3), (16385, 8), (129, 1024)):
+        _fails(B.kv4_evict_workspace_bytes, R(_cache(kv_heads=heads)), R(_seqs(n_seqs=n)), 10)
+        _fails(B.kv4_evict, R(_cache(kv_heads=heads)), R(_seqs(n_seqs=n)), 10, 0, 0, 16 * P, 2 * P, None)
