@@ -400,4 +400,19 @@ class MoELayer(_Fixed):
         return out
 
 
-from .attention import KV4Cache, prompt_attention  # noqa: E402  (they build on the helpers above)
+# Attention builds on the helpers above, so its names come when they are first asked for: either module may be
+# imported first.
+_ATTENTION = ("KV4Cache", "prompt_attention")
+__all__ = [n for n in globals() if not n.startswith("_")] + list(_ATTENTION)
+
+
+def __getattr__(name):
+    if name in _ATTENTION:
+        from . import attention
+        globals()[name] = getattr(attention, name)
+        return globals()[name]
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))
+
+
+def __dir__():
+    return sorted(set(globals()) | set(_ATTENTION))

@@ -269,3 +269,20 @@ def test_the_most_sequences_of_an_eviction():
     for n, heads in ((65536, 3), (16385, 8), (129, 1024)):
         _fails(B.kv4_evict_workspace_bytes, R(_cache(kv_heads=heads)), R(_seqs(n_seqs=n)), 10)
         _fails(B.kv4_evict, R(_cache(kv_heads=heads)), R(_seqs(n_seqs=n)), 10, 0, 0, 16 * P, 2 * P, None)
+
+
+@pytest.mark.parametrize("first", [
+    "import hbm_expert_slot_amd.attention", "from hbm_expert_slot_amd.attention import KV4Cache, prompt_attention",
+    "from hbm_expert_slot_amd.ops import KV4Cache, prompt_attention", "from hbm_expert_slot_amd.ops import *; KV4Cache; FP4Weight",
+    "import hbm_expert_slot_amd as h; h.ops.prompt_attention; assert 'KV4Cache' in dir(h.ops)",
+])
+def test_either_module_can_be_imported_first(first):
+    pytest.importorskip("torch")
+    import os
+    import subprocess
+    import sys
+    check = "; from hbm_expert_slot_amd import attention, ops; assert ops.KV4Cache is attention.KV4Cache and " \
+            "ops.prompt_attention is attention.prompt_attention and not hasattr(ops, 'prompt')"
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", first + check], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-1000:]
