@@ -125,10 +125,11 @@ class KV4Cache(_Fixed):
 
     Sequences are given to each call: table int32 [n, width] names the pages of
     each sequence, lens int32 [n] its tokens, those that come with the call
-    included.  Handing out pages is the caller's part.  Calls that write the cache
-    (append, evict, attend with accumulate) have to be ordered with all others on
-    it; attend and read may run at once.  The cache may be dropped while calls are
-    under way, but not while a captured graph is to be replayed."""
+    included.  Handing out pages is the caller's part.  The constructor waits until
+    the pages are zeros (not in a capture, where that is part of the graph).  Calls
+    that write the cache (append, evict, attend with accumulate) have to be ordered
+    with all others on it; attend and read may run at once.  The cache may be dropped
+    while calls are under way, but not while a captured graph is to be replayed."""
 
     _fixed = frozenset(("fmt", "head_dim", "kv_heads", "n_pages", "device", "pages", "weights", "positions", "k_scale",
                         "v_scale", "_memory", "_streams", "_sizes", "_c", "_ref"))
@@ -154,6 +155,10 @@ class KV4Cache(_Fixed):
         def ptr(t):
             return None if t is None else t.data_ptr()
 
+        # zeros before any stream uses it (in a capture they are nodes of the graph, in its order)
+        with torch.cuda.device(dev):
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()
         memory = [t.detach() for t in (pages, weights, positions, k_scale, v_scale) if t is not None]
         c = B.sc_kv4_cache(_FORMAT[fmt], head_dim, kv_heads, n_pages, ptr(pages), ptr(weights), ptr(positions),
                            ptr(k_scale), ptr(v_scale))

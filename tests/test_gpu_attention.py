@@ -1049,3 +1049,48 @@ def test_append_of_very_many_tokens():
         for got in whole + cache.read(table, _ints(torch, [at + m]), m):
             got = got[at:at + m] if got.shape[0] == n else got
             assert torch.equal(got.cpu(), want), at
+
+
+def test_a_new_cache_on_another_stream():
+    """A cache is zeros before its constructor returns: what another stream appends right away stays."""
+    torch = torch_cuda()
+    log("new cache, other stream")
+    k = _randn(torch, 1, 200, 2, 64).to(torch.bfloat16)
+    table, lens = _ints(torch, [[3, 1, 0, 2]]), _ints(torch, [200])
+    want = torch.tensor(oa.quantized(_np(k), "mxfp4")).float()
+    busy = torch.zeros(1 << 28, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for _ in range(20):                     # several milliseconds on the current stream, before the zeros
+            busy.add_(1.0)
+        cache = _ops().KV4Cache(4, 2, 64, "mxfp4", track=True)
+        cache.append(k, k, table, lens, stream=side)
+        torch.cuda.synchronize()
+        got = cache.read(table, lens, 200, dtype=torch.float32)
+        assert torch.equal(got[0].cpu(), want) and torch.equal(got[1].cpu(), want)
+        assert cache.positions[1, 0].tolist() == list(range(64, 128))
+
+
+def test_a_new_cache_within_a_captured_graph():
+    """Its zeros belong to the graph then."""
+    torch = torch_cuda()
+    log("new cache, captured")
+    k = _randn(torch, 1, 100, 1, 64).to(torch.bfloat16)
+    q = _randn(torch, 2, 1, 1, 2, 64).to(torch.bfloat16)
+    table, lens = _ints(torch, [[0, 1]]), _ints(torch, [100])
+
+    def step():
+        cache = _ops().KV4Cache(2, 1, 64, track=True)
+        cache.append(k, k, table, lens)
+        return cache, cache.attend(q, table, lens, accumulate=True), cache.weights
+
+    want = step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for _ in range(3):
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
