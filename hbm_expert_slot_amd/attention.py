@@ -40,7 +40,7 @@ def _scale_of(scale, dim):
     if scale is None:
         return 1.0 / math.sqrt(dim)
     scale = float(scale)
-    _need(0.0 < scale < 3e38, "scale must be positive and finite")
+    _need(0.0 < scale <= 2.3e38, "scale must be positive and at most 2.3e38")
     return scale
 
 

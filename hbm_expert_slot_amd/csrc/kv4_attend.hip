@@ -934,7 +934,7 @@ sc_status kv4_attention(const sc_kv4_cache* cache, const sc_kv4_seqs* seqs, cons
   const sc_status s = check_attention(cache, seqs, x->rows, x->q_heads);
   if (s != SC_OK) return s;
   if (x->type != SC_DTYPE_BF16 && x->type != SC_DTYPE_F16) return fail(SC_E_ARG, "type must be bf16 or fp16");
-  if (!(x->scale > 0.0f) || x->scale > 3e38f) return fail(SC_E_ARG, "scale must be positive and finite");
+  if (!(x->scale > 0.0f) || x->scale > SC_ATTENTION_MAX_SCALE) return fail(SC_E_ARG, "scale must be positive and at most 2.3e38");
   if (accumulate && !cache->d_weights) return fail(SC_E_ARG, "the cache keeps no weights");
   if (seqs->n_seqs == 0) return SC_OK;
   if (!x->d_q || !x->d_out || (uintptr_t)x->d_q % 2 || (uintptr_t)x->d_out % 2)

@@ -548,7 +548,7 @@ sc_status prompt_attention_workspace_bytes(const sc_prompt* p, size_t* bytes) {
 sc_status prompt_attention(const sc_prompt* p, void* d_workspace, void* stream) {
   const sc_status s = prompt::check(p);
   if (s != SC_OK) return s;
-  if (!(p->scale > 0.0f) || p->scale > 3e38f) return fail(SC_E_ARG, "scale must be positive and finite");
+  if (!(p->scale > 0.0f) || p->scale > SC_ATTENTION_MAX_SCALE) return fail(SC_E_ARG, "scale must be positive and at most 2.3e38");
   if (p->n_seqs == 0 || p->rows == 0) return SC_OK;
   if (!p->d_q || !p->d_out || (p->keys > 0 && (!p->d_k || !p->d_v))) return fail(SC_E_ARG, "q, k, v or out is NULL");
   if ((uintptr_t)p->d_q % 2 || (uintptr_t)p->d_k % 2 || (uintptr_t)p->d_v % 2 || (uintptr_t)p->d_out % 2 ||

@@ -465,6 +465,7 @@ SC_API sc_status moe_layer_forward(const sc_moe_config* cfg, const sc_moe_weight
 #define SC_PROMPT_MAX_STRIDE (1 << 23)   /* elements from a key or value to the next */
 
 #define SC_PROMPT_PART_KEYS 2048
+#define SC_ATTENTION_MAX_SCALE 2.3e38f   /* times log2 e it is still an fp32 number */
 
 /* Packed sequences: sequence b has the rows d_starts[b] .. d_starts[b+1]-1 of q
  * and the keys d_key_starts[b] .. d_key_starts[b+1]-1 of k and v.  Element d of
@@ -476,7 +477,7 @@ typedef struct {
   int32_t q_heads, kv_heads;      /* q_heads is a multiple of kv_heads; head h reads key head h / (q_heads / kv_heads) */
   int32_t n_seqs;                 /* <= SC_PROMPT_MAX_SEQS */
   int32_t rows, keys;             /* of all sequences; (rows / 128 + n_seqs) * q_heads < 2^24 */
-  float scale;                    /* > 0 */
+  float scale;                    /* > 0, <= SC_ATTENTION_MAX_SCALE */
   const void* d_q;
   const void* d_k;
   const void* d_v;
@@ -582,7 +583,7 @@ typedef struct {
   int32_t type;              /* of q and out: SC_DTYPE_BF16 or SC_DTYPE_F16 */
   int32_t rows;              /* 1 .. SC_KV4_MAX_ROWS: a token and its drafts */
   int32_t q_heads;           /* a multiple of kv_heads, up to SC_KV4_MAX_GROUP times */
-  float scale;               /* > 0 */
+  float scale;               /* > 0, <= SC_ATTENTION_MAX_SCALE */
   const void* d_q;
   void* d_out;
   int64_t q_stride[3], out_stride[3];

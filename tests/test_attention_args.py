@@ -286,3 +286,16 @@ def test_either_module_can_be_imported_first(first):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", first + check], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-1000:]
+
+
+def test_scales_that_exceed_fp32_in_base_2():
+    """Scores are formed in base 2: log2(e) times a scale above 2.358e38 would be infinite, and 0 times that NaN."""
+    torch = pytest.importorskip("torch")
+    from hbm_expert_slot_amd import attention
+    assert torch.tensor(2.3e38) * 1.4426950408889634 < float("inf") and torch.tensor(2.36e38) * 1.4426950408889634 == float("inf")
+    for scale in (2.31e38, 2.9e38):
+        _fails(B.prompt_attention, R(_prompt(scale=scale)), None, None)
+        _fails(B.kv4_attention, R(_cache()), R(_seqs()), R(_query(scale=scale)), 0, P, None)
+        with pytest.raises(ValueError, match="scale"):
+            attention._scale_of(scale, 64)
+    assert attention._scale_of(2.3e38, 64) == 2.3e38

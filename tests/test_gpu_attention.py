@@ -1094,3 +1094,14 @@ def test_a_new_cache_within_a_captured_graph():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+
+
+def test_the_largest_scale():
+    """Scores of zero stay zero under it: every row has the mean of the values that it sees."""
+    torch = torch_cuda()
+    log("largest scale")
+    q = torch.zeros(70, 2, 64, dtype=torch.bfloat16, device="cuda")
+    v = _randn(torch, 1, 70, 1, 64).to(torch.bfloat16)
+    _check_prompt(torch, q, v, v, [70], [70], "bf16", scale=2.3e38)
+    c = Filled(torch, "mxfp4", 64, 1, [70])
+    _check_attend(torch, c, q[:3].unsqueeze(0), "bf16", scale=2.3e38)
