@@ -1105,3 +1105,227 @@ def test_the_largest_scale():
     _check_prompt(torch, q, v, v, [70], [70], "bf16", scale=2.3e38)
     c = Filled(torch, "mxfp4", 64, 1, [70])
     _check_attend(torch, c, q[:3].unsqueeze(0), "bf16", scale=2.3e38)
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1e-38, 1e-42])
+def test_the_smallest_scales(scale):
+    """Scores of nearly zero, and masked ones that stay masked."""
+    torch = torch_cuda()
+    log("smallest scale", scale)
+    q, v = _randn(torch, 1, 70, 2, 64).to(torch.bfloat16), _randn(torch, 2, 70, 1, 64).to(torch.bfloat16)
+    _check_prompt(torch, q, v, v, [70], [70], "bf16", scale=scale)
+    c = Filled(torch, "nvfp4", 64, 1, [70])
+    _check_attend(torch, c, q[:3].unsqueeze(0), "bf16", scale=scale)
+
+
+def _later(torch, stream, dst, src, busy):
+    """dst gets src on the stream, behind work of some milliseconds."""
+    with torch.cuda.stream(stream):
+        for _ in range(60):
+            busy.add_(1.0)
+        dst.copy_(src)
+
+
+def _behind(stream):
+    """Waits for the stream, which has to be busy until now: what came before it on the host was not waited for."""
+    assert not stream.query()
+    stream.synchronize()
+
+
+def test_calls_run_on_the_given_stream():
+    """Every call's input is written late on the stream that is given, while the current stream is idle: a call that
+    ran on the current one would read what was there before.  What the calls leave is read on that stream as well."""
+    torch = torch_cuda()
+    log("given stream")
+    ops = _ops()
+    n, d, hkv = [300, 70], 128, 2
+    T = sum(n)
+    side, busy = torch.cuda.Stream(), torch.zeros(1 << 27, device="cuda")
+    table, lens, starts = _ints(torch, [[0, 1, 2, 3, 4], [5, 6, 7, 8, 9]]), _ints(torch, n), _starts(torch, n)
+    k1, v1 = (_randn(torch, i, T, hkv, d).to(torch.bfloat16) for i in range(2))
+    q1 = _randn(torch, 3, 2, 2, 8, d).to(torch.bfloat16)
+    pq1 = _randn(torch, 4, T, 4, d).to(torch.bfloat16)
+    w1 = torch.rand(10, hkv, 64, device="cuda")
+
+    def fresh():
+        c = ops.KV4Cache(10, hkv, d, track=True)
+        c.append(k1, v1, table, lens, starts)
+        c.weights.copy_(w1)
+        return c
+
+    c = fresh()
+    want = dict(prompt=ops.prompt_attention(pq1, k1, v1, starts), attend=c.attend(q1, table, lens),
+                read=c.read(table, lens, T, starts))
+    c.attend(q1, table, lens, accumulate=True)
+    want["weights"] = c.weights.clone()
+    want["new"] = c.evict(table, lens, 64, recent=8)
+    want["evicted"] = c.read(table, want["new"], 128)
+    nothing = torch.zeros_like
+    torch.cuda.synchronize()
+
+    # a prompt, whose queries come late
+    pq = nothing(pq1)
+    torch.cuda.synchronize()
+    _later(torch, side, pq, pq1, busy)
+    got, lse = ops.prompt_attention(pq, k1, v1, starts, return_lse=True, stream=side)
+    _behind(side)
+    assert torch.equal(got, want["prompt"])
+
+    # attention, whose queries come late
+    c, q = fresh(), nothing(q1)
+    torch.cuda.synchronize()
+    _later(torch, side, q, q1, busy)
+    got = c.attend(q, table, lens, stream=side)
+    _behind(side)
+    assert torch.equal(got, want["attend"])
+
+    # append, whose keys come late, and read behind it
+    c, k = ops.KV4Cache(10, hkv, d, track=True), nothing(k1)
+    torch.cuda.synchronize()
+    _later(torch, side, k, k1, busy)
+    c.append(k, v1, table, lens, starts, stream=side)
+    got = c.read(table, lens, T, starts, stream=side)
+    _behind(side)
+    assert all(torch.equal(a, b) for a, b in zip(got, want["read"]))
+
+    # weights that come late, what attention adds to them, and the eviction that goes by them
+    c = fresh()
+    c.weights.zero_()
+    torch.cuda.synchronize()
+    _later(torch, side, c.weights, w1, busy)
+    c.attend(q1, table, lens, accumulate=True, stream=side)
+    with torch.cuda.stream(side):
+        w = c.weights.clone()
+    new = c.evict(table, lens, 64, recent=8, stream=side)
+    got = c.read(table, new, 128, stream=side)
+    _behind(side)
+    assert torch.equal(w, want["weights"]) and torch.equal(new, want["new"])
+    assert all(torch.equal(a, b) for a, b in zip(got, want["evicted"]))
+
+
+def test_what_calls_on_a_stream_use_may_be_dropped():
+    """Inputs, caches and results that are dropped while a stream has the call still before it: their memory is not
+    given out to the current stream before."""
+    torch = torch_cuda()
+    log("dropped")
+    ops = _ops()
+    side, busy = torch.cuda.Stream(), torch.zeros(1 << 27, device="cuda")
+    n, d, hkv = 640, 128, 2
+    table, lens, starts = torch.arange(10, dtype=torch.int32, device="cuda").unsqueeze(0), _ints(torch, [n]), _ints(torch, [0, n])
+    k1, v1 = (_randn(torch, i, n, hkv, d).to(torch.bfloat16) for i in range(2))
+    q1 = _randn(torch, 3, 1, 1, 8, d).to(torch.bfloat16)
+    scale1 = torch.tensor([0.5], device="cuda")
+    first = ops.KV4Cache(10, hkv, d, k_scale=scale1)
+    first.append(k1, v1, table, lens)
+    want, pwant = first.attend(q1, table, lens), ops.prompt_attention(k1, k1, v1, starts)
+    for _ in range(3):
+        c = ops.KV4Cache(10, hkv, d, k_scale=scale1.clone())
+        c.append(k1, v1, table, lens)
+        q, k, v, t, ln, st = q1.clone(), k1.clone(), v1.clone(), table.clone(), lens.clone(), starts.clone()
+        torch.cuda.synchronize()
+        sizes = [x.numel() * x.element_size() for x in (c.pages, q, k, v, t, ln, st)]
+        with torch.cuda.stream(side):
+            for _ in range(60):
+                busy.add_(1.0)
+        got = c.attend(q, t, ln, stream=side)
+        pgot = ops.prompt_attention(k, k, v, st, stream=side)
+        del c, q, k, v, t, ln, st
+        junk = [torch.full((s,), 255, dtype=torch.uint8, device="cuda") for s in sizes for _ in range(4)]
+        torch.cuda.current_stream().synchronize()
+        _behind(side)
+        assert torch.equal(got, want) and torch.equal(pgot, pwant)
+        del junk
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_attend_on_other_pages_and_in_other_batches(fmt):
+    """On other pages: the same bits.  Alone or in another batch, whose list is cut elsewhere: the same but for the
+    order of the sums, whose bounds hold for each."""
+    torch = torch_cuda()
+    log("other pages, other batches", fmt)
+    lens = [1000, 3, 500, 64, 2500]
+    c = Filled(torch, fmt, 128, 2, lens)
+    q = _randn(torch, 1, 5, 2, 8, 128).to(torch.bfloat16)
+    want, _ = _check_attend(torch, c, q, "bf16")
+    k, v = c.cache.read(c.table, c.d_lens, sum(lens), _starts(torch, lens), dtype=torch.float32)
+    perm = torch.randperm(c.cache.n_pages, device="cuda").to(torch.int32)
+    other = _ops().KV4Cache(c.cache.n_pages, 2, 128, fmt)
+    table = torch.where(c.table >= 0, perm[c.table.clamp(min=0).long()], c.table)
+    assert not torch.equal(table, c.table)
+    other.append(k, v, table, c.d_lens, _starts(torch, lens))          # representable: the same codes
+    assert torch.equal(other.attend(q, table, c.d_lens), want)
+    sc = 1.0 / np.sqrt(128)
+    for some in ([0], [4], [2, 0], [4, 3, 1, 0], [0, 0, 0]):
+        got = c.cache.attend(q[some], c.table[some], c.d_lens[some])
+        for i, b in enumerate(some):
+            o, _, _, eo, _, _ = oa.attend(_np(q)[b], *c.of(b), sc, *P_EPS[fmt])
+            _close(got[i], o, eo, "bf16", (some, b))
+
+
+def test_a_prompt_whose_last_rows_leave_weights_before_eviction():
+    """append leaves weights of 0; the last rows of the prompt, attended to again with accumulate, give the tokens
+    theirs, and eviction goes by them."""
+    torch = torch_cuda()
+    log("weights of a prompt")
+    ops = _ops()
+    hq, hkv, d, n = 8, 2, 128, [300, 150]
+    T, R, keep = sum(n), 16, 100
+    starts, lens = _starts(torch, n), _ints(torch, n)
+    q, k, v = (2 * _randn(torch, i, T, h, d) for i, h in enumerate((hq, hkv, hkv)))
+    q, k, v = q.to(torch.bfloat16), k.to(torch.bfloat16), v.to(torch.bfloat16)
+    ops.prompt_attention(q, k, v, starts)
+    c = Filled(torch, "nvfp4", d, hkv, n, track=True)
+    c.cache.append(k, v, c.table, lens, starts)
+    c.k, c.v = c.held(k, 0), c.held(v, 1)
+    last = torch.cat([torch.arange(int(e) - R, int(e)) for e in np.cumsum(n)]).cuda()
+    c.cache.attend(q[last].view(2, R, hq, d), c.table, lens, accumulate=True)
+    got = c.cache.weights.clone()
+    new = c.cache.evict(c.table, lens, keep, recent=8, sinks=2)
+    assert new.tolist() == [keep, keep]
+    gk, _ = c.cache.read(c.table, new, 2 * keep, dtype=torch.float32)
+    for b in range(2):
+        ck, cv = c.of(b)
+        _, _, w, _, _, ew = oa.attend(_np(q[last].view(2, R, hq, d))[b], ck, cv, 1.0 / np.sqrt(d), *P_EPS["nvfp4"])
+        place = np.arange(n[b])
+        page = _np(c.table[b]).astype(int)[place // 64]
+        for h in range(hkv):
+            wd = _np(got)[page, h, place % 64]
+            assert (np.abs(wd - w[:, h]) <= ew[:, h] + 2.0 ** -23 * w[:, h]).all()
+            src = oa.evict(wd.astype(np.float32), place, keep, 8, 2)
+            assert not np.array_equal(src, np.arange(keep))
+            assert np.array_equal(_np(gk)[b * keep:(b + 1) * keep, h], ck[src, h])
+
+
+def test_as_many_sequences_as_a_call_takes():
+    """65536 of them: lists, searches and grids at their limits."""
+    torch = torch_cuda()
+    log("65536 sequences")
+    ops, n = _ops(), 65536
+    cache = ops.KV4Cache(n, 2, 64, "mxfp4", track=True)
+    lens = torch.arange(n, dtype=torch.int32, device="cuda") % 7            # 0 .. 6 tokens
+    T = int(lens.sum())
+    starts = torch.zeros(n + 1, dtype=torch.int32, device="cuda")
+    starts[1:] = torch.cumsum(lens, 0)
+    k, v = (_randn(torch, i, T, 2, 64).to(torch.bfloat16) for i in range(2))
+    for width in (1, 9):                                                    # without a list of pages, and with one
+        table = torch.full((n, width), -1, dtype=torch.int32, device="cuda")
+        table[:, 0] = torch.randperm(n, device="cuda")
+        cache.append(k, v, table, lens, starts)
+        rk, rv = (_np(x) for x in cache.read(table, lens, T, starts, dtype=torch.float32))
+        assert np.array_equal(rk, oa.quantized(_np(k), "mxfp4"))
+        q = _randn(torch, 5, n, 1, 4, 64).to(torch.bfloat16)
+        out = cache.attend(q, table, lens, accumulate=True)
+        new = cache.evict(table, lens, 4)
+        assert torch.equal(new, lens.clamp(max=4))
+        assert not bool(out[lens == 0].any())
+        for b in (1, 6, 6999, 32768 + 5, 65500, n - 1):
+            s, m = int(starts[b]), int(lens[b])
+            o, _, w, eo, _, ew = oa.attend(_np(q[b]), rk[s:s + m], rv[s:s + m], 0.125, *P_EPS["mxfp4"])
+            _close(out[b], o, eo, "bf16", (width, b))
+    q = _randn(torch, 6, T, 2, 64).to(torch.bfloat16)
+    out, lse = ops.prompt_attention(q, k, v, starts, return_lse=True)
+    for b in (1, 6, 6999, 32768 + 5, 65500, n - 1):
+        s, m = int(starts[b]), int(lens[b])
+        o, l, _, eo, el, _ = oa.attend(_np(q[s:s + m]), _np(k[s:s + m]), _np(v[s:s + m]), 0.125, EPS["bf16"])
+        _close(out[s:s + m], o, eo, "bf16", b)
+        _close(lse[s:s + m], l, el, "fp32", b)
