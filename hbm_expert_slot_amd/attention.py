@@ -211,7 +211,9 @@ class KV4Cache(_Fixed):
         """Quantise tokens into the cache: k and v [tokens, kv_heads, head_dim] (float32, bfloat16 or
         float16).  starts int32 [n + 1] packs the sequences' new tokens (None: tokens / n each); they are each
         sequence's last, so the last one goes to place lens - 1.  positions int32 [tokens] are kept for eviction
-        (default: the places).  Places the table does not have and pages the cache does not have are not written;
+        (default: the places).  Their weights are 0 until attend has accumulated some: an evict right after a
+        prompt keeps its first places, unless attend was given the prompt's last rows (up to 16) with accumulate
+        before.  Places the table does not have and pages the cache does not have are not written;
         two tokens must not have one place.  tokens * kv_heads * head_dim is below 2^32, here and in read."""
         seqs = self._seqs(table, lens)
         rows = self._rows(k, v, _TYPE)
@@ -303,7 +305,7 @@ class KV4Cache(_Fixed):
         others, then those with the largest weights, equal ones by place.  They keep their places below keep, or move
         into those that became free, so a sequence's tokens are not in order afterwards: give append positions from
         then on.  Sequences that are cut must not share pages; one with a length or page that cannot be stays as it
-        is.  A call takes up to 2^17 sequences times kv_heads."""
+        is.  Weights are what attend has accumulated (0 for tokens that were only appended).  A call takes up to 2^17 sequences times kv_heads."""
         _need(self.weights is not None, "the cache keeps no weights")
         seqs = self._seqs(table, lens)
         _need(keep >= 1 and recent >= 0 and sinks >= 0 and recent + sinks <= keep,

@@ -5,8 +5,9 @@
 // One pass over the pages keeps the running maximum m, the sum and o (fp32).
 //
 // A head's rows, all query heads that share it times all new tokens, are the
-// columns of the 16x16x32 matrix products, so the cache is read and widened once
-// for all of them:  S^T = K Q^T,  O^T = V^T P^T.  The tokens of S^T that a lane
+// columns of the 16x16x32 matrix products:  S^T = K Q^T,  O^T = V^T P^T.  The cache
+// is read and widened once for up to 32 of them (16 with heads of 256); more columns
+// are chunks of their own, which read the head's pages again.  The tokens of S^T that a lane
 // gets are those whose P it has to supply to the second product, and the columns
 // stay in their lanes, so neither P, the maxima nor the sums ever change lanes
 // but for the four lanes of a column.
@@ -26,9 +27,11 @@
 // What bounds it: HBM.  64 sequences of 717063 tokens in all, 8 key heads and 48 query
 // heads of 128, NVFP4: 145 us, 5.7 TB/s (a copy of 1 GiB moves 5.14 TB/s), and 10 us to
 // join.  One sequence of 131069 tokens, 64 query heads: 31 us, 4.9 TB/s, and 6 to join.
+// MXFP4, the 64 sequences again: 137 us, with fp16 queries in two parts 156.
 // With few pages per wavefront starting, the queries' widening and the join count:
-// 97680 tokens of 16 sequences, 4 rows each, 8 query heads on each of 4, MXFP4: 35 us and
-// 9 where HBM needs 10.
+// 97680 tokens of 16 sequences, 4 rows each, 8 query heads on each of 4, MXFP4: 32 us and
+// 9 where HBM needs 10.  Sixteen rows each, 8 query heads on each of 8, NVFP4 (128
+// columns, four chunks): 117 us and 36 to join, where the products need 42.
 #include "kv4_device.h"
 
 namespace sc {
@@ -40,7 +43,7 @@ constexpr int kWaves = 4, kThreads = 64 * kWaves;
 // (64 sequences of 717063 tokens: 512 parts 184 us, 768 parts 178, before pieces overlapped.)
 constexpr int kMaxParts = 768;
 // Pages up to which a head's are one block's, without a second kernel: four steps of a
-// wavefront (100 tokens: 10.7 us a call, with a list 13.4).
+// wavefront (one sequence of 100 tokens, the one that was measured: 10.7 us a call, with a list 13.4).
 constexpr int kDirectPages = 8;
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -765,6 +768,8 @@ __global__ __launch_bounds__(kThreads) void k_kv4_join(AttendArgs a) {
 // keys twice costs less than writing and reading the scores.  A step belongs to one
 // wavefront, so the order of every sum is fixed.  97680 tokens, 4 key heads, 32 columns
 // each, MXFP4: 17 us (2 TB/s; six steps per wavefront, whose start they do not hide).
+// With more columns the queries of a chunk are widened again at every step: 8 key heads,
+// 128 columns, NVFP4, 146 us.
 template <int D, int FMT, bool HALF, int NQ>
 __global__ __launch_bounds__(kThreads, 2) void k_kv4_weights(AttendArgs a) {
   typedef Layout<D, FMT> L;

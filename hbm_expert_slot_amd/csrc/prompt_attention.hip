@@ -14,10 +14,10 @@
 //
 // A block has 128 rows, 32 per wavefront, and two blocks share a compute unit, so
 // that one wavefront of a SIMD can be in its softmax while the other multiplies.
-// What bounds it: the matrix units, at the clock that their power allows.  16384
-// rows of 32 heads of 128, fp16: 2.13 to 2.23 ms, 0.99 to 1.03 PFLOP/s (an 8192^3
-// bf16 library product on the same card reaches 1.22); matrix units busy in 52% of
-// the cycles at a mean clock of 1.85 GHz.  9708 packed rows of 8 sequences, 48 heads:
+// What bounds it: not settled.  16384 rows of 32 heads of 128, fp16: 2.13 to 2.23
+// ms, 0.99 to 1.03 PFLOP/s (an 8192^3 bf16 library product on the same card reaches
+// 1.22); matrix units busy in 52% of the cycles, no LDS conflicts, at a mean clock of
+// 1.85 GHz, which speaks for power but does not prove it.  9708 packed rows of 8 sequences, 48 heads:
 // 263 to 276 us, 0.79 to 0.83 PFLOP/s; the rest is starting 3840 blocks and tiles on the diagonal.
 // The first kernel here (one buffer through registers, no late maxima, masks
 // everywhere) took 7.03 ms and 783 us.

@@ -560,7 +560,9 @@ SC_API sc_status kv4_page_bytes(int32_t format, int32_t head_dim, size_t* bytes)
 /* Quantises tokens into the cache: sequence b has the tokens d_starts[b] ..
  * d_starts[b+1]-1 (NULL: tokens / n_seqs each), which are its last: the last one
  * goes to place d_lens[b] - 1.  Codes and scales follow fp4_quantize with a given
- * scale.  A cache with weights gets weight 0 and the position d_positions[token]
+ * scale.  A cache with weights gets weight 0 (kv4_attention with `accumulate` adds
+ * to it; the last rows of a prompt, given to it before an eviction, give all of the
+ * prompt's tokens weights) and the position d_positions[token]
  * (NULL: the place).  tokens * kv_heads * head_dim < 2^32, here and in kv4_read.
  * Tokens outside of the sequences, places that are not in the table and pages
  * outside of the cache are not written.  No two tokens of a call may have one place
