@@ -139,6 +139,19 @@ template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
   return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xF, 0xF, false));
 }
+// Sums over the lanes up to each.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_add(int v) {
+  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ int wave_scan(int v) {
+  v = dpp_add<0x111, 0xF>(v);      // from 1, 2, 4 and 8 lanes before in the row of 16
+  v = dpp_add<0x112, 0xF>(v);
+  v = dpp_add<0x114, 0xF>(v);
+  v = dpp_add<0x118, 0xF>(v);
+  v = dpp_add<0x142, 0xA>(v);      // a row's last lane to the next row, the second row's to both behind
+  return dpp_add<0x143, 0xC>(v);
+}
 template <int V>
 constexpr int kTileOut = V >= 4 ? V / 4 : 1;
 template <int V>

@@ -84,20 +84,6 @@ __device__ __forceinline__ int length_of(const Seqs& s, int b) {
   return n >= 0 && n <= s.width * kPage ? n : -1;
 }
 
-// Sums over the lanes up to each.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ int dpp_add(int v) {
-  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
-}
-__device__ __forceinline__ int wave_scan(int v) {
-  v = dpp_add<0x111, 0xF>(v);      // from 1, 2, 4 and 8 lanes before in the row of 16
-  v = dpp_add<0x112, 0xF>(v);
-  v = dpp_add<0x114, 0xF>(v);
-  v = dpp_add<0x118, 0xF>(v);
-  v = dpp_add<0x142, 0xA>(v);      // a row's last lane to the next row, the second row's to both behind
-  return dpp_add<0x143, 0xC>(v);
-}
-
 sc_status check_cache(const sc_kv4_cache* c);
 sc_status check_seqs(const sc_kv4_seqs* s);
 inline Seqs seqs_of(const sc_kv4_seqs* s) { return Seqs{s->d_table, s->d_lens, s->ld_table, s->n_seqs, s->width}; }

@@ -150,19 +150,6 @@ __device__ __forceinline__ Sequence sequence(const PromptArgs& a, int b) {
   }
   return s;
 }
-// Sums over the lanes up to each.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ int dpp_add(int v) {
-  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
-}
-__device__ __forceinline__ int wave_scan(int v) {
-  v = dpp_add<0x111, 0xF>(v);      // from 1, 2, 4 and 8 lanes before in the row of 16
-  v = dpp_add<0x112, 0xF>(v);
-  v = dpp_add<0x114, 0xF>(v);
-  v = dpp_add<0x118, 0xF>(v);
-  v = dpp_add<0x142, 0xA>(v);      // a row's last lane to the next row, the second row's to both behind
-  return dpp_add<0x143, 0xC>(v);
-}
 // The sequence of tile t of all, and t within it; false behind the last.  The lanes
 // hold 64 sequences at a time, so the one that is found needs no further load.
 __device__ __forceinline__ bool sequence_at(const PromptArgs& a, int& t, int lane, Sequence& s) {
