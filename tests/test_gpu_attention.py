@@ -1119,9 +1119,9 @@ def test_the_smallest_scales(scale):
 
 
 def _later(torch, stream, dst, src, busy):
-    """dst gets src on the stream, behind work of some milliseconds."""
+    """dst gets src on the stream, behind work of tens of milliseconds."""
     with torch.cuda.stream(stream):
-        for _ in range(60):
+        for _ in range(200):
             busy.add_(1.0)
         dst.copy_(src)
 
@@ -1225,7 +1225,7 @@ def test_what_calls_on_a_stream_use_may_be_dropped():
         torch.cuda.synchronize()
         sizes = [x.numel() * x.element_size() for x in (c.pages, q, k, v, t, ln, st)]
         with torch.cuda.stream(side):
-            for _ in range(60):
+            for _ in range(200):
                 busy.add_(1.0)
         got = c.attend(q, t, ln, stream=side)
         pgot = ops.prompt_attention(k, k, v, st, stream=side)
